@@ -200,7 +200,8 @@ def _plain_sample(s):
     u24 = (s["u"] * 2.0**24).to(torch.int64)[:, None].clamp(0, (1 << 24) - 1)
     xs, at = torch.sort(x, dim=-1, descending=True, stable=True)
     top = xs[:, :1]
-    w = torch.round(torch.exp((xs - top) / T) * 2.0**31).to(torch.int64)  # of the sorted row; whole numbers: sums are exact
+    per = torch.full_like(T, math.log2(math.e)) / T
+    w = torch.round(torch.exp2((xs - top) * per) * 2.0**31).to(torch.int64)  # of the sorted row; whole numbers: sums are exact
     rank = torch.arange(V, device=x.device)
     w = torch.where((rank < k) | (k <= 0), w, 0)
     run = torch.cumsum(w, dim=-1)
