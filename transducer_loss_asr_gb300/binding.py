@@ -1,4 +1,4 @@
-"""ctypes binding of libtdt_loss.so (include/tdt_loss.h).
+"""ctypes binding of libtdt_loss.so (include/tdt_loss.h, include/tdt_decoder.h).
 
 Argument marshalling only: sizes, strides, dtype codes, raw pointers and the
 current CUDA stream go to the C ABI; every step of the loss runs in the
@@ -7,6 +7,7 @@ no fallback: if the library is missing, importing this module raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -68,6 +69,17 @@ def _load() -> ctypes.CDLL:
     lib.tdt_loss_timing_enable.argtypes = [I]
     lib.tdt_loss_timing_read.restype = I
     lib.tdt_loss_timing_read.argtypes = [P, P, P, I, I]
+    lib.tdt_cross_attn_workspace_size.restype = ctypes.c_size_t
+    lib.tdt_cross_attn_workspace_size.argtypes = [P, I, I]
+    lib.tdt_cross_attn_fwd.restype = I
+    lib.tdt_cross_attn_fwd.argtypes = [P, P, P, P, P, I, P, P, P, ctypes.c_double, P, P, P,
+                                       ctypes.c_size_t, P]
+    lib.tdt_cross_attn_bwd.restype = I
+    lib.tdt_cross_attn_bwd.argtypes = [P, P, P, P, P, P, P, P, I, P, P, P, ctypes.c_double, P, P,
+                                       P, P, ctypes.c_size_t, P]
+    lib.tdt_sample.restype = I
+    lib.tdt_sample.argtypes = [P, P, ctypes.c_int64, I, P, P, P, P, P, ctypes.c_double,
+                               ctypes.c_int64, ctypes.c_double, ctypes.c_double, P, P, P]
     return lib
 
 
@@ -89,6 +101,10 @@ def _i64(vals):
 
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _stream_handle(device):
@@ -214,6 +230,189 @@ def tdt_loss_fwd_bwd_noalloc(logits, labels, logit_lens, label_lens, durations, 
     with torch.cuda.device(logits.device):
         _check(lib.tdt_loss_fwd_bwd_noalloc(*args, _stream_handle(logits.device)))
     return loss_out, grad_out
+
+
+_NO_SWITCH = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device's context, without the cost of a switch where it is current already."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return _NO_SWITCH
+    return torch.cuda.device(device)
+
+
+_Sizes6 = ctypes.c_int64 * 6
+_Strides12 = ctypes.c_int64 * 12
+_Strides24 = ctypes.c_int64 * 24
+
+
+def tdt_cross_attn_workspace_size(sizes, dtype, backward: bool) -> int:
+    """Bytes of scratch of a cross-attention call; sizes = (B, Lq, Lk, H, Hkv, D), dtype a torch
+    dtype (0 for invalid arguments or when none is needed)."""
+    return int(lib.tdt_cross_attn_workspace_size(_Sizes6(*sizes), DTYPES[dtype], int(backward)))
+
+
+def _attn_sizes(q, k, v, k_lens, q_lens, windows):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q must be [B, Lq, H, D], k and v [B, Lk, Hkv, D]")
+    B, Lq, H, D = q.shape
+    _, Lk, Hkv, _ = k.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("k and v must be [B, Lk, Hkv, D] with q's B and D")
+    if q.dtype not in DTYPES:
+        raise TypeError("q dtype must be float32, float16 or bfloat16")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k and v must have one dtype")
+    dev = q.device
+    if k.device != dev or v.device != dev:
+        raise ValueError("q, k and v must be on one device")
+    for name, t in (("k_lens", k_lens), ("q_lens", q_lens)):
+        if t is not None and (t.dtype != torch.int64 or not t.is_contiguous() or t.device != dev
+                              or t.shape != (B,)):
+            raise ValueError("%s must be a contiguous int64 tensor of %d element(s) on %s"
+                             % (name, B, dev))
+    if windows is not None and (windows.dtype != torch.int32 or not windows.is_contiguous()
+                                or windows.device != dev or windows.shape != (B, Lq, 2)):
+        raise ValueError("windows must be a contiguous int32 tensor [B, Lq, 2] on %s" % dev)
+    return B, Lq, Lk, H, Hkv, D
+
+
+def _rows(x):
+    """x with the elements of each head contiguous (a copy only where they are not)."""
+    return x if x.stride(3) == 1 or x.shape[3] == 1 else x.contiguous()
+
+
+def _like(x, t, name):
+    """t, checked to be an output of x's shape and dtype, or a new contiguous one."""
+    if t is None:
+        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or (
+            t.stride(3) != 1 and t.shape[3] != 1):
+        raise ValueError("%s must have the shape, dtype and device of its input and contiguous "
+                         "heads" % name)
+    return t
+
+
+def _scratch(sizes, q, backward, workspace):
+    need = lib.tdt_cross_attn_workspace_size(sizes, DTYPES[q.dtype], backward)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    return workspace
+
+
+def tdt_cross_attn_fwd(q, k, v, k_lens=None, q_lens=None, windows=None, scale=None,
+                       need_lse=True, out=None, lse=None, workspace=None):
+    """Cross attention of label states q [B, Lq, H, D] to encoder frames k, v [B, Lk, Hkv, D] on
+    the current CUDA stream (include/tdt_decoder.h, tdt_cross_attn_fwd); H a multiple of Hkv.
+
+    k_lens, q_lens: int64 [B] or None (all); windows: int32 [B, Lq, 2], the frames [w0, w1) that
+    each query sees, or None; scale: 1 / sqrt(D) unless given.  Few rows (decoding steps, the
+    hypotheses of a beam) take the same call.  Any strides with contiguous heads, such as slices
+    of a fused projection.  Returns (out, lse): out like q, lse float32 [B, H, Lq] (None without
+    need_lse), which tdt_cross_attn_bwd takes.
+    """
+    B, Lq, Lk, H, Hkv, D = dims = _attn_sizes(q, k, v, k_lens, q_lens, windows)
+    q, k, v = _rows(q), _rows(k), _rows(v)
+    out = _like(q, out, "out")
+    if lse is not None:
+        if lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq]")
+    elif need_lse:
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
+    sizes = _Sizes6(*dims)
+    workspace = _scratch(sizes, q, 0, workspace)
+    with _on(q.device):
+        _check(lib.tdt_cross_attn_fwd(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), sizes,
+            _Strides12(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3]),
+            DTYPES[q.dtype], _addr(k_lens), _addr(q_lens), _addr(windows),
+            D ** -0.5 if scale is None else scale, out.data_ptr(), _addr(lse),
+            _addr(workspace), 0 if workspace is None else workspace.numel(),
+            torch.cuda.current_stream(q.device).cuda_stream))
+    return out, lse
+
+
+def tdt_cross_attn_bwd(grad_out, q, k, v, out, lse, k_lens=None, q_lens=None, windows=None,
+                       scale=None, dq=None, dk=None, dv=None, workspace=None):
+    """Gradients (dq, dk, dv) of sum(grad_out * out); out and lse are tdt_cross_attn_fwd's, the
+    other arguments its own.  dq, dk, dv may be given, e.g. as slices of the gradient of a fused
+    projection."""
+    B, Lq, Lk, H, Hkv, D = dims = _attn_sizes(q, k, v, k_lens, q_lens, windows)
+    for name, t in (("grad_out", grad_out), ("out", out)):
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
+            raise ValueError("%s must have q's shape, dtype and device" % name)
+    if lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq]")
+    q, k, v, out, grad_out = _rows(q), _rows(k), _rows(v), _rows(out), _rows(grad_out)
+    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+    sizes = _Sizes6(*dims)
+    workspace = _scratch(sizes, q, 1, workspace)
+    with _on(q.device):
+        _check(lib.tdt_cross_attn_bwd(
+            grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), sizes,
+            _Strides24(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3],
+                       *grad_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3],
+                       *dv.stride()[:3]),
+            DTYPES[q.dtype], _addr(k_lens), _addr(q_lens), _addr(windows),
+            D ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+            _addr(workspace), 0 if workspace is None else workspace.numel(),
+            torch.cuda.current_stream(q.device).cuda_stream))
+    return dq, dk, dv
+
+
+def _setting(x, dtype, N, dev, name):
+    """(device pointer or None, value) of a setting that is one number or a tensor [N]."""
+    if not isinstance(x, torch.Tensor):
+        return None, x
+    if x.dtype != dtype or x.shape != (N,) or not x.is_contiguous() or x.device != dev:
+        raise ValueError("%s must be a number or a contiguous %s tensor of %d element(s) on %s"
+                         % (name, dtype, N, dev))
+    return x.data_ptr(), None
+
+
+def tdt_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None,
+               logprobs=None):
+    """Draws a token of each row of ``logits`` [N, V] from ``uniforms`` (float32 [N], in [0, 1))
+    on the current CUDA stream (include/tdt_decoder.h, tdt_sample): temperature (0: argmax),
+    top_k (0: off), top_p (1: off), min_p (0: off), each a number or a tensor [N] (float32;
+    top_k int32).  Rows may be a slice of wider ones, e.g. the token logits of joint outputs.
+    Returns (tokens int32 [N], logprobs float32 [N]): the log-probability among the tokens that
+    the filters leave."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, V]")
+    if logits.dtype not in DTYPES:
+        raise TypeError("logits dtype must be float32, float16 or bfloat16")
+    N, V = logits.shape
+    dev = logits.device
+    if logits.stride(1) != 1 and V != 1:
+        logits = logits.contiguous()
+    if (uniforms.dtype != torch.float32 or uniforms.shape != (N,) or uniforms.device != dev
+            or not uniforms.is_contiguous()):
+        raise ValueError("uniforms must be a contiguous float32 tensor of %d element(s) on %s"
+                         % (N, dev))
+    f = torch.float32
+    ts, t = _setting(temperature, f, N, dev, "temperature")
+    ks, k = _setting(top_k, torch.int32, N, dev, "top_k")
+    ps, p = _setting(top_p, f, N, dev, "top_p")
+    ms, m = _setting(min_p, f, N, dev, "min_p")
+    for name, x, dtype in (("tokens", tokens, torch.int32), ("logprobs", logprobs, f)):
+        if x is not None and (x.dtype != dtype or x.shape != (N,) or not x.is_contiguous()
+                              or x.device != dev):
+            raise ValueError("%s must be a contiguous %s tensor of %d element(s) on %s"
+                             % (name, dtype, N, dev))
+    if tokens is None:
+        tokens = torch.empty(N, dtype=torch.int32, device=dev)
+    if logprobs is None:
+        logprobs = torch.empty(N, dtype=f, device=dev)
+    with _on(dev):
+        _check(lib.tdt_sample(
+            logits.data_ptr(), (ctypes.c_int64 * 2)(N, V), logits.stride(0), DTYPES[logits.dtype],
+            uniforms.data_ptr(), ts, ks, ps, ms, 1.0 if t is None else t, 0 if k is None else k,
+            1.0 if p is None else p, 0.0 if m is None else m, tokens.data_ptr(),
+            logprobs.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+    return tokens, logprobs
 
 
 def _new_workspace(logits, n_dur):

@@ -30,7 +30,7 @@
 #include <mutex>
 #include <vector>
 
-#include "../../include/tdt_loss.h"
+#include "../../include/tdt_decoder.h"
 #include "tdt_common.cuh"
 
 namespace tdt {
@@ -519,6 +519,11 @@ const char *tdt_status_string(int status) {
     case TDT_ERR_BAD_ALIGNMENT: return "a pointer is not aligned to its element size";
     case TDT_ERR_BAD_ALIASING:
       return "grad_out overlaps the logits other than as the same contiguous tensor";
+    case TDT_ERR_BAD_HEADS:
+      return "invalid heads (H a positive multiple of Hkv, 1 <= D <= 256)";
+    case TDT_ERR_BAD_SCALE: return "scale must be finite and > 0";
+    case TDT_ERR_BAD_SAMPLING:
+      return "invalid sampling setting (temperature >= 0, 0 <= top_p, min_p <= 1, top_k >= 0)";
     case TDT_ERR_NOALLOC_TOO_LARGE:
       return "problem needs more scratch than the fixed array of tdt_loss_fwd_bwd_noalloc "
              "(TDT_NOALLOC_MAX_WORKSPACE_BYTES); use tdt_loss_fwd_bwd or tdt_loss_fwd_bwd_ws";

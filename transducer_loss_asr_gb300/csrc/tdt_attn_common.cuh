@@ -1,0 +1,61 @@
+// tdt_attn_common.cuh -- what the cross-attention kernels share: the argument
+// block, which frames a query sees, and the launchers.
+#pragma once
+
+#include "tdt_common.cuh"
+
+namespace tdt {
+
+constexpr int kMaxHeadDim = 256;
+constexpr float kLn2 = 0.69314718055994531f;
+
+// Element strides of (batch, position, head); the head's elements are contiguous.
+struct Strides {
+  long long b, l, h;
+};
+
+// One call's arguments, passed to the kernels by value.
+struct AttnArgs {
+  const void *q, *k, *v, *out, *go;  // out: written by the forward kernels
+  void *dq, *dk, *dv;
+  float *lse;                        // [B, H, Lq] or NULL (forward only)
+  float *delta;                      // workspace, [B, H, Lq]: grad_out . out of each query
+  Strides sq, sk, sv, so, sgo, sdq, sdk, sdv;
+  long long B;
+  int Lq, Lk, H, Hkv, G, D;          // G = H / Hkv
+  const long long *k_lens, *q_lens;  // NULL: all
+  const int *windows;                // [B, Lq, 2] or NULL
+  float scale;
+};
+
+// Lengths of utterance b.  Lengths outside the tensors see nothing (bad).
+struct Lens {
+  int nq, nk;
+  bool bad;
+};
+__device__ __forceinline__ Lens utt_lens(const AttnArgs &a, long long b) {
+  const long long nk = a.k_lens ? a.k_lens[b] : a.Lk;
+  const long long nq = a.q_lens ? a.q_lens[b] : a.Lq;
+  Lens n;
+  n.bad = nk < 0 || nk > a.Lk || nq < 0 || nq > a.Lq;
+  n.nk = n.bad ? 0 : (int)nk;
+  n.nq = n.bad ? 0 : (int)nq;
+  return n;
+}
+
+// Frames [x, y) that query i of utterance b sees; x = y = 0 if none.
+__device__ __forceinline__ int2 row_range(const AttnArgs &a, long long b, int i, const Lens &n) {
+  int lo = 0, hi = n.nk;
+  if (i >= n.nq) return make_int2(0, 0);
+  if (a.windows) {
+    const int2 w = *reinterpret_cast<const int2 *>(a.windows + (b * a.Lq + i) * 2);
+    lo = max(lo, w.x);
+    hi = min(hi, w.y);
+  }
+  return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
+cudaError_t launch_attn_general_fwd(const AttnArgs &a, int dtype, cudaStream_t stream);
+cudaError_t launch_attn_general_bwd(const AttnArgs &a, int dtype, cudaStream_t stream);
+
+}  // namespace tdt
