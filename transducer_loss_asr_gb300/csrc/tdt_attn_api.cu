@@ -96,7 +96,11 @@ extern "C" {
 size_t tdt_cross_attn_workspace_size(const int64_t sizes[6], int dtype, int backward) {
   using namespace tdt;
   if (check_sizes(sizes, dtype) != TDT_OK) return 0;
-  if (!backward) return 0;
+  if (!backward)
+    return dtype == TDT_DTYPE_F32 || sizes[5] > 128 || sizes[2] == 0
+               ? 0
+               : attn_fwd_tc_workspace(sizes[0], sizes[1], sizes[2], (int)sizes[3], (int)sizes[4],
+                                       (int)sizes[5]);
   const size_t rows = (size_t)sizes[0] * (size_t)sizes[1] * (size_t)sizes[3];
   return (rows * 4 + 255) / 256 * 256;  // delta
 }
@@ -119,7 +123,9 @@ int tdt_cross_attn_fwd(const void *q, const void *k, const void *v, const int64_
   a.v = v;
   a.out = out;
   a.lse = lse;
-  const cudaError_t e = launch_attn_general_fwd(a, dtype, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = attn_fwd_tc_fits(a, dtype) ? launch_attn_fwd_tc(a, dtype, workspace, s)
+                                                   : launch_attn_general_fwd(a, dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

@@ -7,6 +7,7 @@
 namespace tdt {
 
 constexpr int kMaxHeadDim = 256;
+constexpr int kSMs = 152;  // of a GB300
 constexpr float kLn2 = 0.69314718055994531f;
 
 // Element strides of (batch, position, head); the head's elements are contiguous.
@@ -55,6 +56,11 @@ __device__ __forceinline__ int2 row_range(const AttnArgs &a, long long b, int i,
   return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
+// Tensor-core kernels: which calls they take, their workspace (of the sizes alone), and the launch.
+bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);
+size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
+cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
+// CUDA-core kernels: every other call.
 cudaError_t launch_attn_general_fwd(const AttnArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_general_bwd(const AttnArgs &a, int dtype, cudaStream_t stream);
 

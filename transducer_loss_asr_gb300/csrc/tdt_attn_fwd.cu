@@ -1,0 +1,544 @@
+// tdt_attn_fwd.cu -- the forward pass of cross attention on the 5th-generation tensor cores, for
+// float16 and bfloat16 heads of up to 128 elements.
+//
+// A tile is 128 rows, a row being a (query, head) pair: where the group of a key head holds a
+// power of two P of query heads, P heads of 128 / P queries share a tile and so share the frames
+// that are loaded for it.  Two warpgroups each hold a stream of frame tiles:
+//   wide  (more than 128 rows): two row tiles, one a stream, over the same frames;
+//   thin  (at most 128 rows):   one row tile, the streams take the frame tiles in turn and are
+//                               joined at the end: half the steps one after another.
+// One warp loads tiles with TMA, one issues the products, and each stream's 128 threads (thread =
+// row) do the softmax.  Per frame tile and stream:
+//   S = Q K^T            128 x 128, float32 in TMEM, operands in shared memory
+//   P = 2^(S c - m)      rounded to 16 bits, written over S in TMEM
+//   O += P V             P from TMEM, O in TMEM
+// The products of one stream run while the other one's threads are at their softmax.  The
+// reference m of a row moves only when the running maximum has grown by 8 (in base 2), so O is
+// rescaled rarely; weights are then at most 2^8, exact in effect: the factor cancels in O / l.
+// The sum l adds the unrounded float32 weights; P is rounded to the tensors' type, as the
+// products need (error u per term, at most the rounding of the output itself).
+//
+// Few row tiles: the frames are split over several CTAs, whose results (O, and the logarithm of
+// the sum) a second kernel joins in a fixed order.
+#include <climits>
+
+#include "tdt_attn_common.cuh"
+#include "tdt_tc.cuh"
+
+namespace tdt {
+namespace {
+
+constexpr int kRows = 128;          // rows of a tile, frames of a tile
+constexpr int kThreads = 384;       // two softmax warpgroups; a TMA warp, an MMA warp, two idle
+constexpr float kLazy = 8.0f;
+constexpr int kLaunchRegs = 168;    // 3 warpgroups x 168 = 2 x 208 + 88
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+
+struct FwdPlan {
+  int P;          // heads of a tile
+  int packs;      // H / P
+  int wide;       // 1: two row tiles a CTA
+  int tiles;      // row tiles (CTAs) of a pack
+  int splits;     // CTAs that share the frames of a row tile
+};
+
+struct FwdArgs {
+  AttnArgs a;
+  FwdPlan p;
+  int q_b, q_h, k_b, k_h, v_b, v_h;  // 0 for repeated axes
+  float *part_o, *part_l;            // splits > 1: [split][CTA row][DP], [split][CTA row]
+};
+
+template <int DP, bool WIDE> struct FwdShape {
+  static constexpr int CHUNKS = DP / 64;
+  static constexpr int CHUNK = kRows * 128;          // bytes
+  static constexpr int TILE = CHUNKS * CHUNK;
+  static constexpr int NQ = WIDE ? 2 : 1;
+  static constexpr int SLOTS = DP == 64 ? (WIDE ? 8 : 8) : (WIDE ? 4 : 5);
+  static constexpr int BYTES = (NQ + SLOTS) * TILE;
+};
+
+struct FwdShared {
+  unsigned long long full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2],
+      drained;
+  unsigned tmem;
+  int gave_up, first, last;
+  float join_m[kRows], join_l[kRows];
+};
+
+// 128 scores of a row (float32 bits) to weights 2^(s c - ref c); their sum; pairs packed.
+template <int DT>
+__device__ __forceinline__ float exp_pack(unsigned (&s)[32], float c, float neg, unsigned *out) {
+  float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float p0 = fast_exp2(fmaf(__uint_as_float(s[i]), c, neg));
+    const float p1 = fast_exp2(fmaf(__uint_as_float(s[i + 1]), c, neg));
+    sum0 += p0;
+    sum1 += p1;
+    out[i / 2] = pack2<DT>(p0, p1);
+  }
+  return sum0 + sum1;
+}
+
+template <int DT, int DP, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
+                       const __grid_constant__ CUtensorMap vm, const __grid_constant__ FwdArgs f) {
+  typedef FwdShape<DP, WIDE> S;
+  extern __shared__ unsigned char raw[];
+  __shared__ FwdShared sh;
+  unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  unsigned char *q_tile = tiles, *slots = tiles + S::NQ * S::TILE;
+  const AttnArgs &a = f.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  // this CTA's rows and frames
+  long long id = blockIdx.x;
+  const int split = (int)(id % f.p.splits);
+  id /= f.p.splits;
+  const long long cta = id;
+  const int tile = (int)(id % f.p.tiles);
+  id /= f.p.tiles;
+  const int pack = (int)(id % f.p.packs);
+  const long long b = id / f.p.packs;
+  const int P = f.p.P, per = kRows / P, i0 = tile * (WIDE ? 2 : 1) * per;
+  const int h0 = pack * P, hk = h0 / a.G;
+  const Lens n = utt_lens(a, b);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S::SLOTS; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.drained, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&sh.s_full[w], 1);
+      mbar_init(&sh.p_ready[w], 128);
+      mbar_init(&sh.o_full[w], 1);
+    }
+    fence_mbar_init_cluster();
+    sh.gave_up = 0;
+    sh.first = INT_MAX;
+    sh.last = 0;
+  }
+  if (warp == 9) tmem_alloc<512>(&sh.tmem);
+  __syncthreads();
+  // the row of this thread (softmax warps), and the hull of all rows' frames
+  const int stream = warp >> 2, r = threadIdx.x & 127;
+  int row = 0, head = 0;
+  int2 range = make_int2(0, 0);
+  if (warp < 8) {
+    row = i0 + (WIDE ? stream * per : 0) + r / P;
+    head = h0 + r % P;
+    range = row_range(a, b, row, n);
+    if (WIDE || stream == 0) {
+      const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
+      const int hi = __reduce_max_sync(0xffffffffu, range.y);
+      if (lane == 0 && hi > 0) {
+        atomicMin(&sh.first, lo);
+        atomicMax(&sh.last, hi);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned tmem = sh.tmem;
+  const Waiter wait{&sh.gave_up};
+  // frames [first, last) in tiles of 128 from `first`; this CTA takes tiles [t0, t1)
+  const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
+  const int t0 = (int)((long long)all * split / f.p.splits),
+            t1 = (int)((long long)all * (split + 1) / f.p.splits), T = t1 - t0;
+  // tiles of a stream: wide 0, 1, ...; thin w, w + 2, ...
+  const int steps0 = WIDE ? T : (T + 1) / 2, steps1 = WIDE ? T : T / 2;
+  auto frame = [&](int w, int s) { return first + (t0 + (WIDE ? s : 2 * s + w)) * kRows; };
+  const float c = a.scale * kLog2e;
+
+  if (warp >= 8) {
+    warpgroup_give_registers<kOtherRegs>();  // to the softmax warps, which hold a row of scores
+    if (warp == 8 && lane == 0 && T > 0) {
+      tma_prefetch_map(&qm);
+      tma_prefetch_map(&km);
+      tma_prefetch_map(&vm);
+      arrive_expect_tx(&sh.q_full, S::NQ * S::TILE);
+      for (int t = 0; t < S::NQ; ++t)
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
+                      i0 + t * per, (int)b * f.q_b);
+      int at = 0;
+      auto load = [&](bool values, int j0) {
+        const int slot = at % S::SLOTS;
+        const unsigned turn = (unsigned)(at / S::SLOTS) & 1;
+        if (!wait(&sh.empty[slot], turn ^ 1)) return false;
+        arrive_expect_tx(&sh.full[slot], S::TILE);
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, &sh.full[slot],
+                      ch * 64, hk * (values ? f.v_h : f.k_h), j0, (int)b * (values ? f.v_b : f.k_b));
+        ++at;
+        return true;
+      };
+      bool ok = load(false, frame(0, 0));
+      if (!WIDE && steps1 > 0) ok = ok && load(false, frame(1, 0));
+      for (int s = 0; ok && s < steps0; ++s)
+        for (int w = 0; ok && w < (WIDE ? 1 : 2); ++w) {
+          const int steps = w ? steps1 : steps0;
+          if (s < steps) ok = load(true, frame(w, s));
+          if (s + 1 < steps) ok = ok && load(false, frame(w, s + 1));
+        }
+      if (!ok)  // copies in flight land before the CTA ends
+        for (int i = max(0, at - S::SLOTS); i < at; ++i)
+          Waiter::drain(&sh.full[i % S::SLOTS], (unsigned)(i / S::SLOTS) & 1);
+    }
+    if (warp == 9 && T > 0) {
+      constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
+      const unsigned q_addr = smem_u32(q_tile), s_addr = smem_u32(slots);
+      int at = 0;  // slots used so far, in the loader's order
+      bool ok = __all_sync(0xffffffffu, wait(&sh.q_full, 0));
+      auto scores = [&](int w, int slot_at) {  // S_w = Q_w K^T
+        const int slot = slot_at % S::SLOTS;
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.full[slot], (unsigned)(slot_at / S::SLOTS) & 1));
+        tc_fence_after();
+        if (ok && lane == 0) {
+          mma_rows<DP>(tmem + w * kRows, q_addr + (WIDE ? w : 0) * S::TILE, S::CHUNK,
+                       s_addr + slot * S::TILE, S::CHUNK, i_s, false);
+          mma_commit(&sh.s_full[w]);
+          if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int w, int s, int slot_at) {  // O_w += P_w V
+        const int slot = slot_at % S::SLOTS;
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.full[slot], (unsigned)(slot_at / S::SLOTS) & 1));
+        const int valid = n.nk - frame(w, s);
+        // frames past the utterance's end may hold anything, and 0 times NaN is NaN
+        if (ok && valid < kRows && (!WIDE || w == 0))
+          zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, max(valid, 0), kRows);
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.p_ready[w], s & 1));
+        tc_fence_after();
+        if (ok && lane == 0) {
+          mma_across<kRows>(tmem + 2 * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
+                            S::CHUNK, i_o, s > 0);
+          if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
+          if (s + 1 == (w ? steps1 : steps0)) mma_commit(&sh.o_full[w]);
+        }
+        __syncwarp();
+      };
+      if (WIDE) {
+        scores(0, 0);
+        scores(1, 0);
+        at = 1;
+        for (int s = 0; ok && s < T; ++s) {
+          for (int w = 0; w < 2; ++w) {
+            values(w, s, at);
+            if (s + 1 < T) scores(w, at + 1);
+          }
+          at += 2;
+        }
+      } else {
+        scores(0, at++);
+        if (steps1 > 0) scores(1, at++);
+        for (int s = 0; ok && s < steps0; ++s)
+          for (int w = 0; w < 2; ++w) {
+            const int steps = w ? steps1 : steps0;
+            if (s < steps) values(w, s, at++);
+            if (s + 1 < steps) scores(w, at++);
+          }
+      }
+      if (!ok && lane == 0) {  // products in flight end before TMEM is freed
+        mma_commit(&sh.drained);
+        Waiter::drain(&sh.drained, 0);
+      }
+    }
+  } else {
+    warpgroup_take_registers<kSoftmaxRegs>();
+    const int steps = stream ? steps1 : steps0;
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    const unsigned s_col = tmem + lanes + stream * kRows, o_col = tmem + lanes + 2 * kRows + stream * DP;
+    float ref = -INFINITY, l = 0.0f;  // reference maximum (base 2) and sum
+    bool ok = true;
+    for (int s = 0; s < steps; ++s) {
+      ok = wait(&sh.s_full[stream], s & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      unsigned x[4][32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, x[i]);
+      tmem_wait_ld();
+      const int j0 = frame(stream, s);
+      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + kRows)) {
+        const int lo = range.x - j0;
+        const unsigned len = (unsigned)(range.y - range.x);
+#pragma unroll
+        for (int i = 0; i < 128; ++i)
+          if ((unsigned)(i - lo) >= len) x[i >> 5][i & 31] = 0xff800000u;  // -inf
+      }
+      float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 128; i += 4) {
+        m0 = fmaxf(m0, fmaxf(__uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i + 1) & 31])));
+        m1 = fmaxf(m1, fmaxf(__uint_as_float(x[i >> 5][(i + 2) & 31]), __uint_as_float(x[i >> 5][(i + 3) & 31])));
+      }
+      const float top = fmaxf(m0, m1) * c;
+      const bool grow = top > ref + kLazy;  // from -inf: any score
+      if (__any_sync(0xffffffffu, grow)) {
+        const float now = grow ? top : ref;
+        const float scale = grow ? fast_exp2(ref - now) : 1.0f;
+        if (s > 0) {  // the products up to tile s - 1 are done: S of tile s came after them
+          unsigned o[32];
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) {
+            tmem_ld32(o_col + i * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
+            tmem_st32(o_col + i * 32, o);
+          }
+        }
+        l *= scale;
+        ref = now;
+      }
+      const float neg = ref == -INFINITY ? 0.0f : -ref;
+      unsigned p[32];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        l += exp_pack<DT>(x[2 * i], c, neg, p);
+        l += exp_pack<DT>(x[2 * i + 1], c, neg, p + 16);
+        tmem_st32(s_col + i * 32, p);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.p_ready[stream]);
+    }
+    if (steps > 0 && ok) ok = wait(&sh.o_full[stream], 0);
+    __syncwarp();
+    tc_fence_after();
+    float f_other = 0.0f, f_own = 1.0f;
+    if (!WIDE) {
+      // join the streams: stream 1 hands over its reference, sum and output (in the tiles' memory:
+      // every product is done, so nothing reads or writes them)
+      float *join_o = reinterpret_cast<float *>(tiles);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (stream == 1) {
+        sh.join_m[r] = ref;
+        sh.join_l[r] = l;
+        if (steps > 0) {
+          unsigned o[32];
+#pragma unroll
+          for (int i = 0; i < DP / 32; ++i) {
+            tmem_ld32(o_col + i * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) join_o[(i * 32 + k) * kRows + r] = __uint_as_float(o[k]);
+          }
+        }
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (stream == 0 && steps1 > 0) {
+        const float m1 = sh.join_m[r], top = fmaxf(ref, m1);
+        if (top > -INFINITY) {
+          f_own = fast_exp2(ref - top);
+          f_other = fast_exp2(m1 - top);
+          l = l * f_own + sh.join_l[r] * f_other;
+          ref = top;
+        }
+      }
+    }
+    __syncwarp();
+    const bool mine = WIDE || stream == 0;
+    const bool bad = n.bad || !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
+    if (mine && row < a.Lq) {
+      const float total = bad ? NAN : l == 0.0f ? -INFINITY : ref + log2f(l);
+      if (f.p.splits > 1)
+        f.part_l[((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NQ * kRows) +
+                 (WIDE ? stream * kRows : 0) + r] = total;
+      else if (a.lse)
+        a.lse[(b * a.H + head) * a.Lq + row] = total * kLn2;
+    }
+    if (mine) {
+      const float inv = bad ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+      const float *join_o = reinterpret_cast<const float *>(tiles);
+      const bool both = !WIDE && steps1 > 0;
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        unsigned o[32];
+        if (steps > 0) {
+          tmem_ld32(o_col + i * 32, o);
+          tmem_wait_ld();
+        }
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          float x = steps > 0 ? __uint_as_float(o[k]) * f_own : 0.0f;
+          if (both) x += join_o[(i * 32 + k) * kRows + r] * f_other;
+          v[k] = l == 0.0f && !bad ? 0.0f : x * inv;
+        }
+        if (row >= a.Lq) {
+        } else if (f.p.splits > 1) {
+          float4 *dst = reinterpret_cast<float4 *>(
+              f.part_o + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NQ * kRows) +
+                          (WIDE ? stream * kRows : 0) + r) * DP + i * 32);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        } else {
+          unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
+                                row * a.so.l + head * a.so.h + i * 32;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (i * 32 + k * 8 < a.D)
+              reinterpret_cast<uint4 *>(dst)[k] = make_uint4(
+                  pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
+                  pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
+        }
+        __syncwarp();
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) tmem_free<512>(tmem);
+}
+
+// Joins the splits of a row: o = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).  DP / 4 threads a
+// row, the splits in order.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs f, int rows) {
+  constexpr int W = DP / 4;
+  const AttnArgs &a = f.a;
+  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
+  const int d = (threadIdx.x % W) * 4;
+  const long long ctas = (long long)f.p.tiles * f.p.packs * a.B;
+  if (at >= ctas * rows) return;
+  const long long cta = at / rows;
+  const int r = (int)(at % rows), tile = (int)(cta % f.p.tiles);
+  const long long bp = cta / f.p.tiles, b = bp / f.p.packs;
+  const int row = (int)(((long long)tile * rows + r) / f.p.P);
+  const int head = (int)(bp % f.p.packs) * f.p.P + r % f.p.P;
+  if (row >= a.Lq) return;
+  float top = -INFINITY;
+  bool bad = false;
+  for (int s = 0; s < f.p.splits; ++s) {
+    const float x = f.part_l[(s * ctas + cta) * rows + r];
+    bad |= x != x;
+    top = fmaxf(top, x);
+  }
+  float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (top > -INFINITY)
+    for (int s = 0; s < f.p.splits; ++s) {
+      const float x = f.part_l[(s * ctas + cta) * rows + r];
+      if (x == -INFINITY) continue;
+      const float w = fast_exp2(x - top);
+      const float4 v = *reinterpret_cast<const float4 *>(f.part_o + ((s * ctas + cta) * rows + r) * DP + d);
+      sum += w;
+      o[0] += w * v.x;
+      o[1] += w * v.y;
+      o[2] += w * v.z;
+      o[3] += w * v.w;
+    }
+  const float inv = bad ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
+  if (d < a.D) {
+    unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
+                          row * a.so.l + head * a.so.h + d;
+    *reinterpret_cast<uint2 *>(dst) =
+        make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv));
+  }
+  if (d == 0 && a.lse)
+    a.lse[(b * a.H + head) * a.Lq + row] = bad ? NAN : sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+}
+
+int row_pack(int G) {
+  int P = 1;
+  while (P < 16 && G % (2 * P) == 0) P *= 2;
+  return P;
+}
+
+FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
+  FwdPlan p;
+  p.P = row_pack(G);
+  p.packs = H / p.P;
+  const long long rows = Lq * p.P;
+  p.wide = rows > kRows;
+  const int tile_rows = p.wide ? 2 * kRows : kRows;
+  p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
+  // split the frames while the CTAs leave SMs idle and every split keeps two tiles a stream
+  const long long ctas = B * p.packs * p.tiles, steps = (Lk + kRows - 1) / kRows;
+  long long s = ctas > 0 ? kSMs / ctas : 1;
+  const long long most = steps / (p.wide ? 2 : 4);
+  if (s > most) s = most;
+  if (s > 64) s = 64;
+  p.splits = s < 1 ? 1 : (int)s;
+  return p;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+template <int DT, int DP, bool WIDE>
+cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v,
+                   cudaStream_t stream) {
+  typedef FwdShape<DP, WIDE> S;
+  const size_t smem = S::BYTES + 1024;
+  cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_fwd_tc_kernel<DT, DP, WIDE>),
+                                    smem, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  const long long ctas = f.a.B * f.p.packs * f.p.tiles;
+  attn_fwd_tc_kernel<DT, DP, WIDE>
+      <<<(unsigned)(ctas * f.p.splits), kThreads, smem, stream>>>(q.map, k.map, v.map, f);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || f.p.splits == 1) return e;
+  const int rows = S::NQ * kRows;
+  const long long threads = ctas * rows * (DP / 4);
+  attn_join_kernel<DT, DP><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(f, rows);
+  return cudaGetLastError();
+}
+
+template <int DT>
+cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v,
+                     cudaStream_t s) {
+  if (f.a.D <= 64)
+    return f.p.wide ? launch<DT, 64, true>(f, q, k, v, s) : launch<DT, 64, false>(f, q, k, v, s);
+  return f.p.wide ? launch<DT, 128, true>(f, q, k, v, s) : launch<DT, 128, false>(f, q, k, v, s);
+}
+
+}  // namespace
+
+size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
+  const FwdPlan p = plan(B, Lq, Lk, H, H / Hkv);
+  if (p.splits == 1) return 0;
+  const size_t rows = (size_t)B * p.packs * p.tiles * p.splits * (p.wide ? 2 : 1) * kRows;
+  return align256(rows * (D <= 64 ? 64 : 128) * 4) + align256(rows * 4);
+}
+
+bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
+  auto fits = [&](const void *p, const Strides &s, long long L, int H) {
+    return map_fits(p, a.B, L, H, a.D, s.b, s.l, s.h);
+  };
+  return dtype != kF32 && a.D <= 128 && a.Lk > 0 && fits(a.q, a.sq, a.Lq, a.H) &&
+         fits(a.k, a.sk, a.Lk, a.Hkv) && fits(a.v, a.sv, a.Lk, a.Hkv) &&
+         fits(a.out, a.so, a.Lq, a.H) && (row_pack(a.G) == 1 || a.sq.h != 0);
+}
+
+cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
+  FwdArgs f = {};
+  f.a = a;
+  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.G);
+  const size_t rows = (size_t)a.B * f.p.packs * f.p.tiles * f.p.splits * (f.p.wide ? 2 : 1) * kRows;
+  f.part_o = static_cast<float *>(workspace);
+  f.part_l = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                       align256(rows * (a.D <= 64 ? 64 : 128) * 4));
+  TensorMap q, k, v;
+  if (!encode_map(&q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, kRows / f.p.P) ||
+      !encode_map(&k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
+      !encode_map(&v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows))
+    return cudaErrorInvalidValue;
+  f.q_b = q.b_mul;
+  f.q_h = q.h_mul;
+  f.k_b = k.b_mul;
+  f.k_h = k.h_mul;
+  f.v_b = v.b_mul;
+  f.v_h = v.h_mul;
+  return dtype == kF16 ? by_shape<kF16>(f, q, k, v, stream) : by_shape<kBF16>(f, q, k, v, stream);
+}
+
+}  // namespace tdt

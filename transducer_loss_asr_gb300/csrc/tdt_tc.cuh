@@ -1,0 +1,233 @@
+// tdt_tc.cuh -- tensor-core building blocks of the attention kernels (PTX ISA:
+// tcgen05, cp.async.bulk.tensor, mbarrier): tensor maps, bounded waits, matrix
+// descriptors, TMEM allocation and access.
+//
+// Tiles in shared memory are [rows][64 elements of 16 bits], 128 bytes a row with the
+// 128-byte swizzle that TMA writes; a tile wider than 64 is several such chunks one after
+// another.  The same bytes serve as an operand whose contraction runs along the row (K-major:
+// q and k of q.k) or across the rows (MN-major: v of p.v), by the descriptor.
+#pragma once
+
+#include <cuda.h>
+
+#include "tdt_async.cuh"
+
+namespace tdt {
+
+// ---- waits -------------------------------------------------------------------
+// Every wait gives up after kWaitLimitCycles, or at once when another one of the CTA has, and
+// then the CTA's outputs are NaN.
+struct Waiter {
+  int *gave_up;  // shared
+  __device__ __forceinline__ bool operator()(unsigned long long *bar, unsigned parity) const {
+    if (try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    do {
+      if (try_wait(bar, parity)) return true;
+      if (*reinterpret_cast<volatile int *>(gave_up)) return false;
+    } while (clock64() - t0 < kWaitLimitCycles);
+    *reinterpret_cast<volatile int *>(gave_up) = 1;
+    return false;
+  }
+  // After giving up: waits for work in flight, for a hundredth of the limit at most.
+  static __device__ __forceinline__ void drain(unsigned long long *bar, unsigned parity) {
+    const long long end = clock64() + kWaitLimitCycles / 100;
+    while (!try_wait(bar, parity) && clock64() < end) {
+    }
+  }
+  static __device__ __forceinline__ bool try_wait(unsigned long long *bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+  }
+};
+__device__ __forceinline__ void mbar_arrive(unsigned long long *bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Writes to shared memory by this thread become visible to TMA and the tensor cores.
+__device__ __forceinline__ void fence_async_shared() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Moves registers between the warpgroups of a CTA.  What is taken may not exceed what the launch
+// gave the CTA (registers at launch x threads): prepare_tc_kernel checks the launch's count.
+template <int N> __device__ __forceinline__ void warpgroup_take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void warpgroup_give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---- TMA ----------------------------------------------------------------------
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, void *dst,
+                                            unsigned long long *bar, int x, int y, int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
+// ---- TMEM ---------------------------------------------------------------------
+template <int COLS> __device__ __forceinline__ void tmem_alloc(unsigned *base) {  // one warp
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_u32(base)),
+               "n"(COLS)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+template <int COLS> __device__ __forceinline__ void tmem_free(unsigned base) {  // the same warp
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(base), "n"(COLS));
+}
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of this thread's lane (32 x 32-bit).  Registers are valid after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32(unsigned addr, unsigned (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(unsigned addr, const unsigned (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(addr)
+      : "memory");
+}
+
+// ---- matrix products ---------------------------------------------------------------
+// Shared-memory operand descriptors: start address, leading and stride offsets in 16-byte
+// units, version 1, 128-byte swizzle.
+constexpr unsigned long long kDescBase = (1ull << 46) | (2ull << 61);
+// Contraction along the row: groups of 8 rows are 1,024 bytes apart.
+__device__ __forceinline__ unsigned long long desc_k_major(unsigned addr) {
+  return kDescBase | (unsigned long long)((addr >> 4) & 0x3fff) | (1ull << 16) | (64ull << 32);
+}
+// Contraction across the rows: groups of 8 rows 1,024 bytes apart, chunks of 64 columns
+// `chunk_bytes` apart.
+__device__ __forceinline__ unsigned long long desc_mn_major(unsigned addr, unsigned chunk_bytes) {
+  return kDescBase | (unsigned long long)((addr >> 4) & 0x3fff) |
+         ((unsigned long long)(chunk_bytes >> 4) << 16) | (64ull << 32);
+}
+// Instruction descriptor of kind::f16 with float32 accumulators, M = 128.
+template <int DT> __device__ __forceinline__ constexpr unsigned mma_desc(int N, bool b_mn_major) {
+  return (1u << 4) | ((DT == kBF16 ? 1u : 0u) << 7) | ((DT == kBF16 ? 1u : 0u) << 10) |
+         ((b_mn_major ? 1u : 0u) << 16) | ((unsigned)(N >> 3) << 17) | ((128u >> 4) << 24);
+}
+// d (+)= a b, both operands in shared memory.  One thread issues; K = 16.
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b,
+                                       unsigned idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((unsigned)accumulate)
+      : "memory");
+}
+// The same with a in TMEM (lane = row, two 16-bit elements a column).
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b,
+                                       unsigned idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"((unsigned)accumulate)
+      : "memory");
+}
+// Arrive on the barrier once every product issued so far by this thread is done.
+__device__ __forceinline__ void mma_commit(unsigned long long *bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
+// d (+)= A B^T over DP columns: A [128 rows], B [N rows], both K-major tiles of DP / 64 chunks.
+template <int DP>
+__device__ __forceinline__ void mma_rows(unsigned d, unsigned a, unsigned a_chunk, unsigned b,
+                                         unsigned b_chunk, unsigned idesc, bool accumulate) {
+#pragma unroll
+  for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      mma_ss(d, desc_k_major(a + c * a_chunk + k * 32), desc_k_major(b + c * b_chunk + k * 32),
+             idesc, accumulate || c + k > 0);
+}
+// d (+)= P B over KR rows of B: P in TMEM, B [KR rows] an MN-major tile.
+template <int KR>
+__device__ __forceinline__ void mma_across(unsigned d, unsigned p, unsigned b, unsigned b_chunk,
+                                           unsigned idesc, bool accumulate) {
+#pragma unroll
+  for (int k = 0; k < KR / 16; ++k)
+    mma_ts(d, p + k * 8, desc_mn_major(b + k * 2048, b_chunk), idesc, accumulate || k > 0);
+}
+
+// Two floats as one 32-bit pair of the 16-bit type, the first in the low half.
+template <int DT> __device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  unsigned r;
+  if (DT == kBF16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Zeroes rows [first, rows) of a tile in shared memory (a warp), for the tensor cores to read.
+__device__ __forceinline__ void zero_tail(unsigned char *tile, int chunks, int chunk_bytes,
+                                          int first, int rows) {
+  const int lane = threadIdx.x & 31;
+  for (int c = 0; c < chunks; ++c)
+    for (int x = first * 8 + lane; x < rows * 8; x += 32)
+      *reinterpret_cast<uint4 *>(tile + c * chunk_bytes + x * 16) = make_uint4(0, 0, 0, 0);
+  fence_async_shared();
+  __syncwarp();
+}
+
+// Shared memory of a kernel, and a check that it launches with `regs` registers a thread, which
+// its register moves count on.
+cudaError_t prepare_tc_kernel(const void *kernel, size_t smem, int regs);
+
+// ---- host: tensor maps ----------------------------------------------------------------
+// A [B, L, H, D] tensor of 16-bit elements as the map (D, H, L, B) with boxes of 64 x heads x
+// rows / heads.  A batch or head axis of stride 0 becomes one of size 1 (b_mul, h_mul = 0).
+struct TensorMap {
+  CUtensorMap map;
+  int b_mul, h_mul;
+};
+bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long L, long long H,
+                int D, long long sb, long long sl, long long sh, int box_heads, int box_rows);
+// Whether encode_map can take the tensor (16-byte alignment of base and strides).
+bool map_fits(const void *ptr, long long B, long long L, long long H, int D, long long sb,
+              long long sl, long long sh);
+
+}  // namespace tdt
