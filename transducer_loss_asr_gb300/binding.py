@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -232,46 +233,54 @@ def tdt_loss_fwd_bwd_noalloc(logits, labels, logit_lens, label_lens, durations, 
     return loss_out, grad_out
 
 
+# The calls of an attention decoder's steps are short: what follows keeps the host's part of them
+# short too (packed argument arrays, the raw stream handle, no device switch where none is needed).
 _NO_SWITCH = contextlib.nullcontext()
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else \
+    torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_pack2, _pack6, _pack12, _pack24 = (struct.Struct("=%dq" % n).pack for n in (2, 6, 12, 24))
 
 
 def _on(device):
     """The device's context, without the cost of a switch where it is current already."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _NO_SWITCH
-    return torch.cuda.device(device)
-
-
-_Sizes6 = ctypes.c_int64 * 6
-_Strides12 = ctypes.c_int64 * 12
-_Strides24 = ctypes.c_int64 * 24
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device, not on %s" % device)
+    return _NO_SWITCH if device.index == _current_device() else torch.cuda.device(device)
 
 
 def tdt_cross_attn_workspace_size(sizes, dtype, backward: bool) -> int:
     """Bytes of scratch of a cross-attention call; sizes = (B, Lq, Lk, H, Hkv, D), dtype a torch
     dtype (0 for invalid arguments or when none is needed)."""
-    return int(lib.tdt_cross_attn_workspace_size(_Sizes6(*sizes), DTYPES[dtype], int(backward)))
+    return int(lib.tdt_cross_attn_workspace_size(_pack6(*sizes), DTYPES[dtype], int(backward)))
+
+
+def _check_lens(name, t, B, dev):
+    if t.dtype != torch.int64 or not t.is_contiguous() or t.device != dev or t.shape != (B,):
+        raise ValueError("%s must be a contiguous int64 tensor of %d element(s) on %s"
+                         % (name, B, dev))
 
 
 def _attn_sizes(q, k, v, k_lens, q_lens, windows):
-    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("q must be [B, Lq, H, D], k and v [B, Lk, Hkv, D]")
-    B, Lq, H, D = q.shape
-    _, Lk, Hkv, _ = k.shape
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != D:
+    B, Lq, H, D = qs
+    Bk, Lk, Hkv, Dk = ks
+    if v.shape != ks or Bk != B or Dk != D:
         raise ValueError("k and v must be [B, Lk, Hkv, D] with q's B and D")
-    if q.dtype not in DTYPES:
+    dtype, dev = q.dtype, q.device
+    if dtype not in DTYPES:
         raise TypeError("q dtype must be float32, float16 or bfloat16")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype != dtype or v.dtype != dtype:
         raise TypeError("q, k and v must have one dtype")
-    dev = q.device
     if k.device != dev or v.device != dev:
         raise ValueError("q, k and v must be on one device")
-    for name, t in (("k_lens", k_lens), ("q_lens", q_lens)):
-        if t is not None and (t.dtype != torch.int64 or not t.is_contiguous() or t.device != dev
-                              or t.shape != (B,)):
-            raise ValueError("%s must be a contiguous int64 tensor of %d element(s) on %s"
-                             % (name, B, dev))
+    if k_lens is not None:
+        _check_lens("k_lens", k_lens, B, dev)
+    if q_lens is not None:
+        _check_lens("q_lens", q_lens, B, dev)
     if windows is not None and (windows.dtype != torch.int32 or not windows.is_contiguous()
                                 or windows.device != dev or windows.shape != (B, Lq, 2)):
         raise ValueError("windows must be a contiguous int32 tensor [B, Lq, 2] on %s" % dev)
@@ -279,26 +288,35 @@ def _attn_sizes(q, k, v, k_lens, q_lens, windows):
 
 
 def _rows(x):
-    """x with the elements of each head contiguous (a copy only where they are not)."""
-    return x if x.stride(3) == 1 or x.shape[3] == 1 else x.contiguous()
+    """(x, strides) with the elements of each head contiguous (a copy only where they are not)."""
+    st = x.stride()
+    if st[3] == 1 or x.shape[3] == 1:
+        return x, st
+    x = x.contiguous()
+    return x, x.stride()
 
 
 def _like(x, t, name):
-    """t, checked to be an output of x's shape and dtype, or a new contiguous one."""
+    """(t, strides): checked to be an output of x's shape and dtype, or a new contiguous one."""
     if t is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        t = x.new_empty(x.shape)
+        return t, t.stride()
+    st = t.stride()
     if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or (
-            t.stride(3) != 1 and t.shape[3] != 1):
+            st[3] != 1 and t.shape[3] != 1):
         raise ValueError("%s must have the shape, dtype and device of its input and contiguous "
                          "heads" % name)
-    return t
+    return t, st
 
 
-def _scratch(sizes, q, backward, workspace):
-    need = lib.tdt_cross_attn_workspace_size(sizes, DTYPES[q.dtype], backward)
-    if workspace is None and need > 0:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    return workspace
+def _scratch(sizes, code, dev, backward, workspace):
+    """(workspace, address, bytes): the given one, or a new one if the call needs any."""
+    if workspace is None:
+        need = lib.tdt_cross_attn_workspace_size(sizes, code, backward)
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace, workspace.data_ptr(), workspace.numel()
 
 
 def tdt_cross_attn_fwd(q, k, v, k_lens=None, q_lens=None, windows=None, scale=None,
@@ -313,23 +331,23 @@ def tdt_cross_attn_fwd(q, k, v, k_lens=None, q_lens=None, windows=None, scale=No
     need_lse), which tdt_cross_attn_bwd takes.
     """
     B, Lq, Lk, H, Hkv, D = dims = _attn_sizes(q, k, v, k_lens, q_lens, windows)
-    q, k, v = _rows(q), _rows(k), _rows(v)
-    out = _like(q, out, "out")
+    (q, sq), (k, sk), (v, sv) = _rows(q), _rows(k), _rows(v)
+    out, so = _like(q, out, "out")
+    dev = q.device
     if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
-            raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq]")
+        if (lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous()
+                or lse.device != dev):
+            raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq] on %s" % dev)
     elif need_lse:
-        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
-    sizes = _Sizes6(*dims)
-    workspace = _scratch(sizes, q, 0, workspace)
-    with _on(q.device):
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
+    sizes, code = _pack6(*dims), DTYPES[q.dtype]
+    workspace, ws, nbytes = _scratch(sizes, code, dev, 0, workspace)
+    with _on(dev):
         _check(lib.tdt_cross_attn_fwd(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), sizes,
-            _Strides12(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3]),
-            DTYPES[q.dtype], _addr(k_lens), _addr(q_lens), _addr(windows),
-            D ** -0.5 if scale is None else scale, out.data_ptr(), _addr(lse),
-            _addr(workspace), 0 if workspace is None else workspace.numel(),
-            torch.cuda.current_stream(q.device).cuda_stream))
+            _pack12(*sq[:3], *sk[:3], *sv[:3], *so[:3]), code, _addr(k_lens), _addr(q_lens),
+            _addr(windows), D ** -0.5 if scale is None else scale, out.data_ptr(), _addr(lse), ws,
+            nbytes, _raw_stream(dev.index)))
     return out, lse
 
 
@@ -339,26 +357,26 @@ def tdt_cross_attn_bwd(grad_out, q, k, v, out, lse, k_lens=None, q_lens=None, wi
     other arguments its own.  dq, dk, dv may be given, e.g. as slices of the gradient of a fused
     projection."""
     B, Lq, Lk, H, Hkv, D = dims = _attn_sizes(q, k, v, k_lens, q_lens, windows)
+    dev = q.device
     for name, t in (("grad_out", grad_out), ("out", out)):
-        if t.shape != q.shape or t.dtype != q.dtype or t.device != q.device:
+        if t.shape != q.shape or t.dtype != q.dtype or t.device != dev:
             raise ValueError("%s must have q's shape, dtype and device" % name)
-    if lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq]")
-    q, k, v, out, grad_out = _rows(q), _rows(k), _rows(v), _rows(out), _rows(grad_out)
-    dq, dk, dv = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
-    sizes = _Sizes6(*dims)
-    workspace = _scratch(sizes, q, 1, workspace)
-    with _on(q.device):
+    if (lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous()
+            or lse.device != dev):
+        raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq] on %s" % dev)
+    (q, sq), (k, sk), (v, sv) = _rows(q), _rows(k), _rows(v)
+    (out, so), (grad_out, sg) = _rows(out), _rows(grad_out)
+    (dq, sdq), (dk, sdk), (dv, sdv) = _like(q, dq, "dq"), _like(k, dk, "dk"), _like(v, dv, "dv")
+    sizes, code = _pack6(*dims), DTYPES[q.dtype]
+    workspace, ws, nbytes = _scratch(sizes, code, dev, 1, workspace)
+    with _on(dev):
         _check(lib.tdt_cross_attn_bwd(
             grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
             lse.data_ptr(), sizes,
-            _Strides24(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3],
-                       *grad_out.stride()[:3], *dq.stride()[:3], *dk.stride()[:3],
-                       *dv.stride()[:3]),
-            DTYPES[q.dtype], _addr(k_lens), _addr(q_lens), _addr(windows),
-            D ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-            _addr(workspace), 0 if workspace is None else workspace.numel(),
-            torch.cuda.current_stream(q.device).cuda_stream))
+            _pack24(*sq[:3], *sk[:3], *sv[:3], *so[:3], *sg[:3], *sdq[:3], *sdk[:3], *sdv[:3]),
+            code, _addr(k_lens), _addr(q_lens), _addr(windows),
+            D ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), ws,
+            nbytes, _raw_stream(dev.index)))
     return dq, dk, dv
 
 
@@ -408,10 +426,10 @@ def tdt_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
         logprobs = torch.empty(N, dtype=f, device=dev)
     with _on(dev):
         _check(lib.tdt_sample(
-            logits.data_ptr(), (ctypes.c_int64 * 2)(N, V), logits.stride(0), DTYPES[logits.dtype],
+            logits.data_ptr(), _pack2(N, V), logits.stride(0), DTYPES[logits.dtype],
             uniforms.data_ptr(), ts, ks, ps, ms, 1.0 if t is None else t, 0 if k is None else k,
             1.0 if p is None else p, 0.0 if m is None else m, tokens.data_ptr(),
-            logprobs.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
+            logprobs.data_ptr(), _raw_stream(dev.index)))
     return tokens, logprobs
 
 

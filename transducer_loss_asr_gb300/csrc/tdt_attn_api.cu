@@ -81,6 +81,10 @@ int fill(AttnArgs *a, const int64_t sizes[6], const int64_t *strides, int n_tens
   return TDT_OK;
 }
 
+size_t delta_bytes(const int64_t sizes[6]) {
+  return ((size_t)sizes[0] * (size_t)sizes[1] * (size_t)sizes[3] * 4 + 255) / 256 * 256;
+}
+
 bool aligned(int dtype, std::initializer_list<const void *> ptrs) {
   const uintptr_t es = dtype == TDT_DTYPE_F32 ? 4 : 2;
   for (const void *p : ptrs)
@@ -96,13 +100,15 @@ extern "C" {
 size_t tdt_cross_attn_workspace_size(const int64_t sizes[6], int dtype, int backward) {
   using namespace tdt;
   if (check_sizes(sizes, dtype) != TDT_OK) return 0;
+  const bool tc = dtype != TDT_DTYPE_F32 && sizes[5] <= 128 && sizes[2] > 0;
   if (!backward)
-    return dtype == TDT_DTYPE_F32 || sizes[5] > 128 || sizes[2] == 0
-               ? 0
-               : attn_fwd_tc_workspace(sizes[0], sizes[1], sizes[2], (int)sizes[3], (int)sizes[4],
-                                       (int)sizes[5]);
-  const size_t rows = (size_t)sizes[0] * (size_t)sizes[1] * (size_t)sizes[3];
-  return (rows * 4 + 255) / 256 * 256;  // delta
+    return tc ? attn_fwd_tc_workspace(sizes[0], sizes[1], sizes[2], (int)sizes[3], (int)sizes[4],
+                                      (int)sizes[5])
+              : 0;
+  return delta_bytes(sizes) + (tc ? attn_bwd_tc_workspace(sizes[0], sizes[1], sizes[2],
+                                                          (int)sizes[3], (int)sizes[4],
+                                                          (int)sizes[5])
+                                  : 0);
 }
 
 int tdt_cross_attn_fwd(const void *q, const void *k, const void *v, const int64_t sizes[6],
@@ -162,7 +168,10 @@ int tdt_cross_attn_bwd(const void *grad_out, const void *q, const void *k, const
   a.dk = dk;
   a.dv = dv;
   a.delta = static_cast<float *>(workspace);
-  const cudaError_t e = launch_attn_general_bwd(a, dtype, static_cast<cudaStream_t>(stream));
+  void *rest = static_cast<char *>(workspace) + delta_bytes(sizes);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = attn_bwd_tc_fits(a, dtype) ? launch_attn_bwd_tc(a, dtype, rest, s)
+                                                   : launch_attn_general_bwd(a, dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

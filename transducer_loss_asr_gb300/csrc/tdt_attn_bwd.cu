@@ -1,0 +1,807 @@
+// tdt_attn_bwd.cu -- the backward pass of cross attention on the 5th-generation tensor cores, for
+// float16 and bfloat16 heads of up to 128 elements.
+//
+// Two kernels, so that every sum has one owner and a fixed order (no atomics):
+//   dq    a CTA holds 128 rows ((query, head) pairs, packed as in the forward pass) and walks the
+//         frames:  S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K      3 products a tile
+//   dk/dv a CTA holds 128 frames and walks the rows of the heads of its group, with the scores
+//         transposed:  S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q    4 products a tile
+// P = 2^(S c - lse) is formed again from the forward pass's lse.  Seven products where five would
+// do with one walk; that one would add its dQ tiles to memory in float32 in no fixed order.
+// delta = dO . O of each row is formed by the dq kernel and kept for the other.
+//
+// Two warpgroups share a tile's elementwise work (thread = TMEM lane, each group half of the
+// columns); a warp loads with TMA, a warp issues products, and in the dk/dv kernel a warp fetches
+// the rows' lse and delta.  P and dS are rounded to the tensors' type and written over S and dP in
+// TMEM, each group over columns that it alone has read, and go into the products from there.
+// Scores of the next tile are formed while the threads are at this one's dS.
+//
+// Few CTAs: the walk is split over several, whose float32 sums a third kernel adds in order.
+#include <climits>
+
+#include "tdt_attn_common.cuh"
+#include "tdt_tc.cuh"
+
+namespace tdt {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;  // 3 warpgroups x 168 = 2 x 208 + 88
+constexpr int kWorkRegs = 208, kOtherRegs = 88;
+// float16 weights are held as 2^15 p <= 2^15 for the product with dO: what a frame gets from rows that
+// hardly weigh it stays clear of the type's least numbers.  (dS has no such bound, and is held as it is.)
+template <int DT> constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
+template <int DT> constexpr float kUnshift = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
+constexpr int kTileBits = 4096;   // row tiles whose windows the dk/dv kernel looks at beforehand
+
+struct BwdPlan {
+  int P, packs, tiles;          // heads of a row tile, H / P, row tiles of a pack
+  int f_tiles;                  // frame tiles
+  int dq_splits, dkv_splits;
+};
+
+struct BwdArgs {
+  AttnArgs a;
+  BwdPlan p;
+  int q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h;  // 0 for repeated axes
+  float *part;                  // splits > 1: [split][CTA][128][DP], dk's after dv's
+};
+
+template <int DP> struct BwdShape {
+  static constexpr int CHUNKS = DP / 64;
+  static constexpr int CHUNK = kRows * 128;
+  static constexpr int TILE = CHUNKS * CHUNK;
+  static constexpr int KS = 3, VS = 2;  // dq: slots of k and v
+  static constexpr int RS = 2;          // dk/dv: slots of q and of dO
+  static constexpr int DQ_BYTES = (2 + KS + VS) * TILE;
+  static constexpr int DKV_BYTES = (2 + 2 * RS) * TILE;
+};
+
+struct Pipe {  // a ring of tiles
+  unsigned long long full[3], empty[3];
+};
+
+__device__ __forceinline__ void pipe_init(Pipe &p, int slots) {
+  for (int i = 0; i < slots; ++i) {
+    mbar_init(&p.full[i], 1);
+    mbar_init(&p.empty[i], 1);
+  }
+}
+
+template <int DP>
+__device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *dst,
+                                          unsigned long long *bar, int h, int l, int b) {
+  for (int c = 0; c < DP / 64; ++c)
+    tma_load_4d(m, dst + c * BwdShape<DP>::CHUNK, bar, c * 64, h, l, b);
+}
+
+// Stores 32 columns of a row as 16-bit elements.
+template <int DT>
+__device__ __forceinline__ void store32(void *out, long long at, const float (&v)[32], int d0, int D) {
+  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<unsigned short *>(out) + at + d0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (d0 + k * 8 < D)
+      dst[k] = make_uint4(pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
+                          pack2<DT>(v[8 * k + 4], v[8 * k + 5]),
+                          pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
+}
+__device__ __forceinline__ void store32f(float *dst, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    reinterpret_cast<float4 *>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+}
+
+// dot of two rows' elements [d0, d0 + n), n a multiple of 8
+template <int DT>
+__device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
+  typedef typename Elem<DT>::T E;
+  float s = 0.0f;
+  for (int d = 0; d < n; d += 8) {
+    const uint4 xv = *reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d);
+    const uint4 yv = *reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d);
+    const E *xe = reinterpret_cast<const E *>(&xv), *ye = reinterpret_cast<const E *>(&yv);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
+  }
+  return s;
+}
+
+// ---- dq ---------------------------------------------------------------------------
+struct DqShared {
+  Pipe k, v;
+  unsigned long long rows_full, scores, ds_ready, done, drained;
+  unsigned tmem;
+  int gave_up, first, last;
+  float half[kRows];
+};
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dq_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
+                      const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                      const __grid_constant__ BwdArgs f) {
+  typedef BwdShape<DP> S;
+  typedef typename Elem<DT>::T E;
+  extern __shared__ unsigned char raw[];
+  __shared__ DqShared sh;
+  unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  unsigned char *q_tile = tiles, *g_tile = q_tile + S::TILE, *k_slots = g_tile + S::TILE,
+                *v_slots = k_slots + S::KS * S::TILE;
+  const AttnArgs &a = f.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long id = blockIdx.x;
+  const int split = (int)(id % f.p.dq_splits);
+  id /= f.p.dq_splits;
+  const long long cta = id;
+  const int tile = (int)(id % f.p.tiles);
+  id /= f.p.tiles;
+  const int pack = (int)(id % f.p.packs);
+  const long long b = id / f.p.packs;
+  const int P = f.p.P, per = kRows / P, i0 = tile * per, h0 = pack * P, hk = h0 / a.G;
+  const Lens n = utt_lens(a, b);
+  if (threadIdx.x == 0) {
+    pipe_init(sh.k, S::KS);
+    pipe_init(sh.v, S::VS);
+    mbar_init(&sh.rows_full, 1);
+    mbar_init(&sh.scores, 1);
+    mbar_init(&sh.ds_ready, 256);
+    mbar_init(&sh.done, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init_cluster();
+    sh.gave_up = 0;
+    sh.first = INT_MAX;
+    sh.last = 0;
+  }
+  if (warp == 9) tmem_alloc<512>(&sh.tmem);
+  __syncthreads();
+  const int group = warp >> 2, r = threadIdx.x & 127;
+  const int row = i0 + r / P, head = h0 + r % P;
+  int2 range = make_int2(0, 0);
+  if (warp < 8) {
+    range = row_range(a, b, row, n);
+    if (group == 0) {
+      const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
+      const int hi = __reduce_max_sync(0xffffffffu, range.y);
+      if (lane == 0 && hi > 0) {
+        atomicMin(&sh.first, lo);
+        atomicMax(&sh.last, hi);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned tmem = sh.tmem;
+  const Waiter wait{&sh.gave_up};
+  const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
+  const int t0 = (int)((long long)all * split / f.p.dq_splits),
+            t1 = (int)((long long)all * (split + 1) / f.p.dq_splits), T = t1 - t0;
+  auto frame = [&](int s) { return first + (t0 + s) * kRows; };
+  constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ
+
+  if (warp >= 8) {
+    warpgroup_give_registers<kOtherRegs>();
+    if (warp == 8 && lane == 0 && T > 0) {
+      arrive_expect_tx(&sh.rows_full, 2 * S::TILE);
+      load_rows<DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
+      load_rows<DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
+      bool ok = true;
+      int s = 0;
+      for (; ok && s < T; ++s) {
+        const int ks = s % S::KS, vs = s % S::VS;
+        ok = wait(&sh.k.empty[ks], ((unsigned)(s / S::KS) & 1) ^ 1);
+        if (!ok) break;
+        arrive_expect_tx(&sh.k.full[ks], S::TILE);
+        load_rows<DP>(&km, k_slots + ks * S::TILE, &sh.k.full[ks], hk * f.k_h, frame(s), (int)b * f.k_b);
+        ok = wait(&sh.v.empty[vs], ((unsigned)(s / S::VS) & 1) ^ 1);
+        if (!ok) {
+          ++s;
+          break;
+        }
+        arrive_expect_tx(&sh.v.full[vs], S::TILE);
+        load_rows<DP>(&vm, v_slots + vs * S::TILE, &sh.v.full[vs], hk * f.v_h, frame(s), (int)b * f.v_b);
+      }
+      if (!ok) {  // copies in flight land before the CTA ends
+        Waiter::drain(&sh.rows_full, 0);
+        for (int i = max(0, s - S::KS); i < s; ++i) {
+          Waiter::drain(&sh.k.full[i % S::KS], (unsigned)(i / S::KS) & 1);
+          Waiter::drain(&sh.v.full[i % S::VS], (unsigned)(i / S::VS) & 1);
+        }
+      }
+    }
+    if (warp == 9 && T > 0) {
+      constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
+      const unsigned qa = smem_u32(q_tile), ga = smem_u32(g_tile), ka = smem_u32(k_slots),
+                     va = smem_u32(v_slots);
+      bool ok = __all_sync(0xffffffffu, wait(&sh.rows_full, 0));
+      auto scores = [&](int s) {
+        const int slot = s % S::KS, valid = n.nk - frame(s);
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.k.full[slot], (unsigned)(s / S::KS) & 1));
+        // frames past the utterance's end may hold anything, and 0 times NaN is NaN
+        if (ok && valid < kRows)
+          zero_tail(k_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, max(valid, 0), kRows);
+        tc_fence_after();
+        if (ok && lane == 0)
+          mma_rows<DP>(tmem + (s & 1) * kRows, qa, S::CHUNK, ka + slot * S::TILE, S::CHUNK, i_s, false);
+        __syncwarp();
+      };
+      auto grads = [&](int s) {  // dP of tile s; its scores came before
+        const int slot = s % S::VS;
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.v.full[slot], (unsigned)(s / S::VS) & 1));
+        tc_fence_after();
+        if (ok && lane == 0) {
+          mma_rows<DP>(tmem + kDp, ga, S::CHUNK, va + slot * S::TILE, S::CHUNK, i_s, false);
+          mma_commit(&sh.scores);
+          mma_commit(&sh.v.empty[slot]);
+        }
+        __syncwarp();
+      };
+      scores(0);
+      grads(0);
+      for (int s = 0; ok && s < T; ++s) {
+        if (s + 1 < T) scores(s + 1);
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.ds_ready, s & 1));
+        tc_fence_after();
+        if (s + 1 < T) grads(s + 1);
+        if (ok && lane == 0) {
+          const int slot = s % S::KS;
+          const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
+          mma_across<64>(tmem + kAcc, ds, at, S::CHUNK, i_o, s > 0);
+          mma_across<64>(tmem + kAcc, ds + 64, at + 64 * 128, S::CHUNK, i_o, true);
+          mma_commit(&sh.k.empty[slot]);
+          if (s + 1 == T) mma_commit(&sh.done);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) {
+        mma_commit(&sh.drained);
+        Waiter::drain(&sh.drained, 0);
+      }
+    }
+  } else {
+    warpgroup_take_registers<kWorkRegs>();
+    // delta = dO . O of the row, half of the columns in each group
+    const bool real = row < n.nq;
+    const long long stat = (b * a.H + head) * a.Lq + row;
+    float delta = 0.0f, lse2 = INFINITY;
+    {
+      const int h = (a.D / 8 + 1) / 2 * 8, d0 = group ? h : 0, len = group ? a.D - h : h;
+      float x = 0.0f;
+      if (real)
+        x = dot16<DT>(static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
+                      static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
+      if (group == 1) sh.half[r] = x;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float y = sh.half[r];
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group == 0) {
+        delta = x + y;
+        sh.half[r] = delta;
+        if (row < a.Lq && split == 0) a.delta[stat] = delta;
+      }
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      delta = sh.half[r];
+      if (range.y > range.x) lse2 = a.lse[stat] * kLog2e;  // else +inf: every weight is 0
+    }
+    const float c = a.scale * kLog2e;
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    bool ok = true;
+    for (int s = 0; s < T; ++s) {
+      ok = wait(&sh.scores, s & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const unsigned s_col = tmem + lanes + (s & 1) * kRows + group * 64,
+                     p_col = tmem + lanes + kDp + group * 64;
+      unsigned x[2][32], y[2][32], out[32];
+      tmem_ld32(s_col, x[0]);
+      tmem_ld32(s_col + 32, x[1]);
+      tmem_ld32(p_col, y[0]);
+      tmem_ld32(p_col + 32, y[1]);
+      tmem_wait_ld();
+      const int j0 = frame(s) + group * 64;
+      const bool cut = __any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64);
+      const int lo = range.x - j0;
+      const unsigned len = (unsigned)(range.y - range.x);
+#pragma unroll
+      for (int i = 0; i < 64; i += 2) {
+        float d[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p = fast_exp2(fmaf(__uint_as_float(x[i >> 5][(i + k) & 31]), c, -lse2));
+          d[k] = p * (__uint_as_float(y[i >> 5][(i + k) & 31]) - delta);
+          if (cut && (unsigned)(i + k - lo) >= len) d[k] = 0.0f;
+        }
+        out[i / 2] = pack2<DT>(d[0], d[1]);
+      }
+      tmem_st32(s_col, out);
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(&sh.ds_ready);
+    }
+    if (T > 0 && ok) ok = wait(&sh.done, 0);
+    __syncwarp();
+    tc_fence_after();
+    const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
+#pragma unroll
+    for (int i = 0; i < DP / 64; ++i) {
+      const int d0 = (group * (DP / 64) + i) * 32;
+      unsigned o[32];
+      if (T > 0) {
+        tmem_ld32(tmem + lanes + kAcc + d0, o);
+        tmem_wait_ld();
+      }
+      float v[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
+      if (row < a.Lq) {
+        if (f.p.dq_splits > 1)
+          store32f(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * kRows + r) * DP + d0, v);
+        else
+          store32<DT>(a.dq, b * a.sdq.b + row * a.sdq.l + head * a.sdq.h, v, d0, a.D);
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) tmem_free<512>(tmem);
+}
+
+// ---- dk and dv ----------------------------------------------------------------------
+struct DkvShared {
+  Pipe q, g;
+  unsigned long long frames_full, s_full, p_ready, dp_full, ds_ready, stat_full[2], stat_empty[2],
+      done, drained;
+  unsigned tmem;
+  int gave_up;
+  unsigned char active[kTileBits];  // row tiles with a query that sees these frames
+  int cut[2];                       // whether some row of the tile sees only part of them
+  __align__(16) float lse2[2][kRows], delta[2][kRows];
+  __align__(16) int lo[2][kRows], len[2][kRows];
+};
+
+template <int DT, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
+                       const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                       const __grid_constant__ BwdArgs f) {
+  typedef BwdShape<DP> S;
+  extern __shared__ unsigned char raw[];
+  __shared__ DkvShared sh;
+  unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  unsigned char *k_tile = tiles, *v_tile = k_tile + S::TILE, *q_slots = v_tile + S::TILE,
+                *g_slots = q_slots + S::RS * S::TILE;
+  const AttnArgs &a = f.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long id = blockIdx.x;
+  const int split = (int)(id % f.p.dkv_splits);
+  id /= f.p.dkv_splits;
+  const long long cta = id;
+  const int j0 = (int)(id % f.p.f_tiles) * kRows;
+  id /= f.p.f_tiles;
+  const int hk = (int)(id % a.Hkv);
+  const long long b = id / a.Hkv;
+  const int P = f.p.P, per = kRows / P;
+  const Lens n = utt_lens(a, b);
+  // the walk: packs of the group x row tiles with queries, skipping those that see none of these
+  // frames; this CTA takes the steps [t0, t1) of it
+  const int row_tiles = j0 < n.nk ? (n.nq + per - 1) / per : 0;
+  const int all = (a.G / P) * row_tiles;
+  const int t0 = (int)((long long)all * split / f.p.dkv_splits),
+            t1 = (int)((long long)all * (split + 1) / f.p.dkv_splits);
+  if (threadIdx.x == 0) {
+    pipe_init(sh.q, S::RS);
+    pipe_init(sh.g, S::RS);
+    mbar_init(&sh.frames_full, 1);
+    mbar_init(&sh.s_full, 1);
+    mbar_init(&sh.p_ready, 256);
+    mbar_init(&sh.dp_full, 1);
+    mbar_init(&sh.ds_ready, 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.stat_full[i], 32);
+      mbar_init(&sh.stat_empty[i], 256);
+    }
+    mbar_init(&sh.done, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init_cluster();
+    sh.gave_up = 0;
+  }
+  if (warp == 9) tmem_alloc<512>(&sh.tmem);
+  if (a.windows)
+    for (int t = warp; t < min(row_tiles, kTileBits); t += kThreads / 32) {
+      bool sees = false;
+      for (int i = t * per + lane; i < min((t + 1) * per, n.nq); i += 32) {
+        const int2 w = row_range(a, b, i, n);
+        sees |= w.x < j0 + kRows && w.y > j0;
+      }
+      sees = __any_sync(0xffffffffu, sees);
+      if (lane == 0) sh.active[t] = sees;
+    }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned tmem = sh.tmem;
+  const Waiter wait{&sh.gave_up};
+  auto skip = [&](int t) {
+    const int rt = t % row_tiles;
+    return a.windows && rt < kTileBits && !sh.active[rt];
+  };
+  auto next = [&](int t) {  // the first step at or after t
+    while (t < t1 && skip(t)) ++t;
+    return t;
+  };
+  const int start = next(t0);
+  const bool any = start < t1;
+  constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = 2 * kRows + DP;
+
+  if (warp >= 8) {
+    warpgroup_give_registers<kOtherRegs>();
+    if (warp == 8 && lane == 0 && any) {
+      arrive_expect_tx(&sh.frames_full, 2 * S::TILE);
+      load_rows<DP>(&km, k_tile, &sh.frames_full, hk * f.k_h, j0, (int)b * f.k_b);
+      load_rows<DP>(&vm, v_tile, &sh.frames_full, hk * f.v_h, j0, (int)b * f.v_b);
+      bool ok = true;
+      int s = 0;
+      for (int t = start; ok && t < t1; t = next(t + 1), ++s) {
+        const int slot = s % S::RS, l = t % row_tiles * per, h = hk * a.G + t / row_tiles * P;
+        const unsigned turn = ((unsigned)(s / S::RS) & 1) ^ 1;
+        ok = wait(&sh.q.empty[slot], turn);
+        if (!ok) break;
+        arrive_expect_tx(&sh.q.full[slot], S::TILE);
+        load_rows<DP>(&qm, q_slots + slot * S::TILE, &sh.q.full[slot], h * f.q_h, l, (int)b * f.q_b);
+        ok = wait(&sh.g.empty[slot], turn);
+        if (!ok) {
+          ++s;
+          break;
+        }
+        arrive_expect_tx(&sh.g.full[slot], S::TILE);
+        load_rows<DP>(&gm, g_slots + slot * S::TILE, &sh.g.full[slot], h * f.go_h, l, (int)b * f.go_b);
+      }
+      if (!ok) {
+        Waiter::drain(&sh.frames_full, 0);
+        for (int i = max(0, s - S::RS); i < s; ++i) {
+          Waiter::drain(&sh.q.full[i % S::RS], (unsigned)(i / S::RS) & 1);
+          Waiter::drain(&sh.g.full[i % S::RS], (unsigned)(i / S::RS) & 1);
+        }
+      }
+    }
+    if (warp == 9 && any) {
+      constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
+      const unsigned ka = smem_u32(k_tile), va = smem_u32(v_tile), qa = smem_u32(q_slots),
+                     ga = smem_u32(g_slots);
+      bool ok = __all_sync(0xffffffffu, wait(&sh.frames_full, 0));
+      // rows past the utterance's end may hold anything, and 0 times NaN is NaN
+      auto ready = [&](Pipe &pipe, unsigned char *slots, int s, int t) {
+        const int slot = s % S::RS, valid = (n.nq - t % row_tiles * per) * P;
+        ok = __all_sync(0xffffffffu, ok && wait(&pipe.full[slot], (unsigned)(s / S::RS) & 1));
+        if (ok && valid < kRows) zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, valid, kRows);
+        tc_fence_after();
+      };
+      auto scores = [&](int s, int t) {  // S^T
+        ready(sh.q, q_slots, s, t);
+        if (ok && lane == 0) {
+          mma_rows<DP>(tmem, ka, S::CHUNK, qa + s % S::RS * S::TILE, S::CHUNK, i_s, false);
+          mma_commit(&sh.s_full);
+        }
+        __syncwarp();
+      };
+      auto grads = [&](int s, int t) {  // dP^T
+        ready(sh.g, g_slots, s, t);
+        if (ok && lane == 0) {
+          mma_rows<DP>(tmem + kDp, va, S::CHUNK, ga + s % S::RS * S::TILE, S::CHUNK, i_s, false);
+          mma_commit(&sh.dp_full);
+        }
+        __syncwarp();
+      };
+      int t = start;
+      scores(0, t);
+      grads(0, t);
+      for (int s = 0; ok && t < t1; ++s) {
+        const int after = next(t + 1), slot = s % S::RS;
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.p_ready, s & 1));
+        tc_fence_after();
+        if (ok && lane == 0) {  // dV += P^T dO
+          const unsigned at = ga + slot * S::TILE;
+          mma_across<64>(tmem + kDv, tmem, at, S::CHUNK, i_o, s > 0);
+          mma_across<64>(tmem + kDv, tmem + 64, at + 64 * 128, S::CHUNK, i_o, true);
+          mma_commit(&sh.g.empty[slot]);
+        }
+        __syncwarp();
+        if (after < t1) scores(s + 1, after);
+        ok = __all_sync(0xffffffffu, ok && wait(&sh.ds_ready, s & 1));
+        tc_fence_after();
+        if (ok && lane == 0) {  // dK += dS^T Q
+          const unsigned at = qa + slot * S::TILE;
+          mma_across<64>(tmem + kDk, tmem + kDp, at, S::CHUNK, i_o, s > 0);
+          mma_across<64>(tmem + kDk, tmem + kDp + 64, at + 64 * 128, S::CHUNK, i_o, true);
+          mma_commit(&sh.q.empty[slot]);
+          if (after >= t1) mma_commit(&sh.done);
+        }
+        __syncwarp();
+        if (after < t1) grads(s + 1, after);
+        t = after;
+      }
+      if (!ok && lane == 0) {
+        mma_commit(&sh.drained);
+        Waiter::drain(&sh.drained, 0);
+      }
+    }
+    if (warp == 10 && any) {  // the rows' statistics
+      int s = 0;
+      for (int t = start; t < t1; t = next(t + 1), ++s) {
+        const int buf = s & 1, i0 = t % row_tiles * per, h0 = hk * a.G + t / row_tiles * P;
+        const bool ok = wait(&sh.stat_empty[buf], ((unsigned)(s >> 1) & 1) ^ 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        bool cut = false;
+#pragma unroll
+        for (int x = 0; x < kRows / 32; ++x) {
+          const int r = x * 32 + lane, i = i0 + r / P;
+          const int2 w = row_range(a, b, i, n);
+          float l2 = INFINITY, dl = 0.0f;  // rows that see nothing: every weight is 0
+          if (w.y > w.x) {
+            const long long at = (b * a.H + h0 + r % P) * a.Lq + i;
+            l2 = a.lse[at] * kLog2e - kShift<DT>;
+            dl = a.delta[at] * kUnshift<DT>;
+            cut |= w.x > j0 || w.y < min(j0 + kRows, n.nk);
+          }
+          sh.lse2[buf][r] = l2;
+          sh.delta[buf][r] = dl;
+          sh.lo[buf][r] = w.x;
+          sh.len[buf][r] = w.y - w.x;
+        }
+        cut = __any_sync(0xffffffffu, cut);
+        if (lane == 0) sh.cut[buf] = cut;
+        __syncwarp();
+        mbar_arrive(&sh.stat_full[buf]);
+      }
+    }
+  } else {
+    warpgroup_take_registers<kWorkRegs>();
+    const int group = warp >> 2, j = j0 + (threadIdx.x & 127);
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
+    const float c = a.scale * kLog2e;
+    const bool past = __any_sync(0xffffffffu, j >= n.nk);
+    bool ok = true;
+    int s = 0;
+    if (any)
+      for (int t = start; t < t1; t = next(t + 1), ++s) {
+        const int buf = s & 1;
+        ok = wait(&sh.stat_full[buf], (unsigned)(s >> 1) & 1) && wait(&sh.s_full, s & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        unsigned x[2][32], out[32];
+        tmem_ld32(s_col, x[0]);
+        tmem_ld32(s_col + 32, x[1]);
+        tmem_wait_ld();
+        const float *lse2 = sh.lse2[buf] + group * 64, *delta = sh.delta[buf] + group * 64;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 l = *reinterpret_cast<const float4 *>(lse2 + i);
+          const float ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            x[i >> 5][(i + k) & 31] =
+                __float_as_uint(fast_exp2(fmaf(__uint_as_float(x[i >> 5][(i + k) & 31]), c, -ls[k])));
+        }
+        if (past) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (j >= n.nk) x[i >> 5][i & 31] = 0;
+        }
+        if (sh.cut[buf]) {
+          const int *lo = sh.lo[buf] + group * 64, *len = sh.len[buf] + group * 64;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if ((unsigned)(j - lo[i]) >= (unsigned)len[i]) x[i >> 5][i & 31] = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 2)
+          out[i / 2] = pack2<DT>(__uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i + 1) & 31]));
+        tmem_st32(s_col, out);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.p_ready);
+        ok = wait(&sh.dp_full, s & 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+        unsigned y[2][32];
+        tmem_ld32(d_col, y[0]);
+        tmem_ld32(d_col + 32, y[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          const float4 dl = *reinterpret_cast<const float4 *>(delta + i);
+          const float ds[4] = {dl.x, dl.y, dl.z, dl.w};
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float p = __uint_as_float(x[i >> 5][(i + k) & 31]);
+            v[k] = p * fmaf(__uint_as_float(y[i >> 5][(i + k) & 31]), kUnshift<DT>, -ds[k]);
+          }
+          out[i / 2] = pack2<DT>(v[0], v[1]);
+          out[i / 2 + 1] = pack2<DT>(v[2], v[3]);
+        }
+        tmem_st32(d_col, out);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&sh.ds_ready);
+        mbar_arrive(&sh.stat_empty[buf]);
+      }
+    if (any && ok) ok = wait(&sh.done, 0);
+    __syncwarp();
+    tc_fence_after();
+    const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
+    // group 0 stores dv, group 1 dk
+    void *out = group ? a.dk : a.dv;
+    const Strides &st = group ? a.sdk : a.sdv;
+    const float scale = group ? a.scale : kUnshift<DT>;
+    const bool keep = j < n.nk;  // frames past the end: their lanes hold no sums
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) {
+      unsigned o[32];
+      if (any) {
+        tmem_ld32(tmem + lanes + (group ? kDk : kDv) + i * 32, o);
+        tmem_wait_ld();
+      }
+      float v[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = bad ? NAN : any && keep ? __uint_as_float(o[k]) * scale : 0.0f;
+      if (j < a.Lk) {
+        if (f.p.dkv_splits > 1) {
+          const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
+          store32f(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * kRows +
+                             (threadIdx.x & 127)) * DP + i * 32, v);
+        } else {
+          store32<DT>(out, b * st.b + j * st.l + hk * st.h, v, i * 32, a.D);
+        }
+      }
+      __syncwarp();
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 9) tmem_free<512>(tmem);
+}
+
+// Adds the splits of a sum in order: 4 columns a thread.  `which`: 0 dq, 1 dv, 2 dk.
+template <int DT, int DP>
+__global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ BwdArgs f, int which0) {
+  constexpr int W = DP / 4;
+  const AttnArgs &a = f.a;
+  const int which = which0 + blockIdx.y;
+  const long long ctas = which == 0 ? (long long)f.p.tiles * f.p.packs * a.B
+                                    : (long long)f.p.f_tiles * a.Hkv * a.B;
+  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
+  if (at >= ctas * kRows) return;
+  const int d = (threadIdx.x % W) * 4, r = (int)(at % kRows);
+  const long long cta = at / kRows;
+  long long to;
+  void *out;
+  if (which == 0) {
+    const long long bp = cta / f.p.tiles, b = bp / f.p.packs;
+    const int row = (int)(cta % f.p.tiles) * (kRows / f.p.P) + r / f.p.P;
+    if (row >= a.Lq) return;
+    out = a.dq;
+    to = b * a.sdq.b + row * a.sdq.l + ((int)(bp % f.p.packs) * f.p.P + r % f.p.P) * a.sdq.h;
+  } else {
+    const long long bh = cta / f.p.f_tiles;
+    const int j = (int)(cta % f.p.f_tiles) * kRows + r;
+    if (j >= a.Lk) return;
+    const Strides &s = which == 2 ? a.sdk : a.sdv;
+    out = which == 2 ? a.dk : a.dv;
+    to = bh / a.Hkv * s.b + j * s.l + bh % a.Hkv * s.h;
+  }
+  if (d >= a.D) return;
+  const int splits = which == 0 ? f.p.dq_splits : f.p.dkv_splits;
+  const float *p = f.part + ((which == 2 ? ctas * splits : 0) + cta) * (kRows * DP) + r * DP + d;
+  float4 v = *reinterpret_cast<const float4 *>(p);
+  for (int s = 1; s < splits; ++s) {
+    const float4 w = *reinterpret_cast<const float4 *>(p + s * ctas * (kRows * DP));
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(out) + to + d) =
+      make_uint2(pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w));
+}
+
+BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv) {
+  BwdPlan p;
+  const int G = H / Hkv;
+  p.P = attn_row_pack(G);
+  p.packs = H / p.P;
+  p.tiles = (int)((Lq * p.P + kRows - 1) / kRows);
+  p.f_tiles = (int)((Lk + kRows - 1) / kRows);
+  // split a walk while CTAs leave SMs idle and each keeps two steps
+  auto splits = [](long long ctas, long long steps) {
+    long long s = ctas > 0 ? kSMs / ctas : 1;
+    if (s > steps / 2) s = steps / 2;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+  };
+  p.dq_splits = splits(B * p.packs * p.tiles, p.f_tiles);
+  p.dkv_splits = splits(B * Hkv * p.f_tiles, (long long)(G / p.P) * p.tiles);
+  return p;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+struct Maps {
+  TensorMap q, go, k, v;
+};
+
+template <int DT, int DP>
+cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
+  typedef BwdShape<DP> S;
+  const AttnArgs &a = f.a;
+  const long long rows = a.B * f.p.packs * f.p.tiles, frames = a.B * a.Hkv * f.p.f_tiles;
+  const unsigned per_tile = kRows * (DP / 4) / 256;  // blocks of the adding kernel
+  cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dq_tc_kernel<DT, DP>),
+                                    S::DQ_BYTES + 1024, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  attn_dq_tc_kernel<DT, DP><<<(unsigned)(rows * f.p.dq_splits), kThreads, S::DQ_BYTES + 1024, stream>>>(
+      m.q.map, m.go.map, m.k.map, m.v.map, f);
+  if (f.p.dq_splits > 1)
+    attn_add_kernel<DT, DP><<<dim3((unsigned)rows * per_tile, 1), 256, 0, stream>>>(f, 0);
+  e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dkv_tc_kernel<DT, DP>),
+                        S::DKV_BYTES + 1024, kLaunchRegs);
+  if (e != cudaSuccess) return e;
+  attn_dkv_tc_kernel<DT, DP><<<(unsigned)(frames * f.p.dkv_splits), kThreads, S::DKV_BYTES + 1024, stream>>>(
+      m.q.map, m.go.map, m.k.map, m.v.map, f);
+  if (f.p.dkv_splits > 1)
+    attn_add_kernel<DT, DP><<<dim3((unsigned)frames * per_tile, 2), 256, 0, stream>>>(f, 1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
+  const BwdPlan p = plan(B, Lq, Lk, H, Hkv);
+  const size_t tile = (size_t)kRows * (D <= 64 ? 64 : 128) * 4;
+  size_t dq = p.dq_splits > 1 ? tile * B * p.packs * p.tiles * p.dq_splits : 0;
+  size_t dkv = p.dkv_splits > 1 ? 2 * tile * B * Hkv * p.f_tiles * p.dkv_splits : 0;
+  return align256(dq > dkv ? dq : dkv);
+}
+
+bool attn_bwd_tc_fits(const AttnArgs &a, int dtype) {
+  auto fits = [&](const void *p, const Strides &s, long long L, int H) {
+    return map_fits(p, a.B, L, H, a.D, s.b, s.l, s.h);
+  };
+  const bool heads = attn_row_pack(a.G) == 1 || (a.sq.h != 0 && a.sgo.h != 0);
+  return dtype != kF32 && a.D <= 128 && a.Lk > 0 && a.Lq > 0 && heads &&
+         fits(a.q, a.sq, a.Lq, a.H) && fits(a.k, a.sk, a.Lk, a.Hkv) &&
+         fits(a.v, a.sv, a.Lk, a.Hkv) && fits(a.out, a.so, a.Lq, a.H) &&
+         fits(a.go, a.sgo, a.Lq, a.H) && fits(a.dq, a.sdq, a.Lq, a.H) &&
+         fits(a.dk, a.sdk, a.Lk, a.Hkv) && fits(a.dv, a.sdv, a.Lk, a.Hkv);
+}
+
+cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
+  BwdArgs f = {};
+  f.a = a;
+  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.Hkv);
+  f.part = static_cast<float *>(workspace);
+  Maps m;
+  const int per = kRows / f.p.P;
+  if (!encode_map(&m.q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, per) ||
+      !encode_map(&m.go, a.go, dtype, a.B, a.Lq, a.H, a.D, a.sgo.b, a.sgo.l, a.sgo.h, f.p.P, per) ||
+      !encode_map(&m.k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
+      !encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows))
+    return cudaErrorInvalidValue;
+  f.q_b = m.q.b_mul;
+  f.q_h = m.q.h_mul;
+  f.go_b = m.go.b_mul;
+  f.go_h = m.go.h_mul;
+  f.k_b = m.k.b_mul;
+  f.k_h = m.k.h_mul;
+  f.v_b = m.v.b_mul;
+  f.v_h = m.v.h_mul;
+  if (dtype == kF16)
+    return a.D <= 64 ? launch<kF16, 64>(f, m, stream) : launch<kF16, 128>(f, m, stream);
+  return a.D <= 64 ? launch<kBF16, 64>(f, m, stream) : launch<kBF16, 128>(f, m, stream);
+}
+
+}  // namespace tdt

@@ -60,6 +60,11 @@ __device__ __forceinline__ int2 row_range(const AttnArgs &a, long long b, int i,
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
+bool attn_bwd_tc_fits(const AttnArgs &a, int dtype);
+size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
+cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
+// Heads that share a row tile, of a group of G: the largest power of two that divides G, up to 16.
+int attn_row_pack(int G);
 // CUDA-core kernels: every other call.
 cudaError_t launch_attn_general_fwd(const AttnArgs &a, int dtype, cudaStream_t stream);
 cudaError_t launch_attn_general_bwd(const AttnArgs &a, int dtype, cudaStream_t stream);

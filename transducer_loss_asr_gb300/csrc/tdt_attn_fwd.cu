@@ -31,6 +31,8 @@ namespace {
 constexpr int kRows = 128;          // rows of a tile, frames of a tile
 constexpr int kThreads = 384;       // two softmax warpgroups; a TMA warp, an MMA warp, two idle
 constexpr float kLazy = 8.0f;
+// float16 weights start at 2^7 and so stay clear of the type's least numbers; at most 2^15
+template <int DT> constexpr float kShift = DT == kF16 ? 7.0f : 0.0f;
 constexpr int kLaunchRegs = 168;    // 3 warpgroups x 168 = 2 x 208 + 88
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 
@@ -281,9 +283,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         m1 = fmaxf(m1, fmaxf(__uint_as_float(x[i >> 5][(i + 2) & 31]), __uint_as_float(x[i >> 5][(i + 3) & 31])));
       }
       const float top = fmaxf(m0, m1) * c;
-      const bool grow = top > ref + kLazy;  // from -inf: any score
+      const bool grow = top > ref + (kLazy + kShift<DT>);  // from -inf: any score
       if (__any_sync(0xffffffffu, grow)) {
-        const float now = grow ? top : ref;
+        const float now = grow ? top - kShift<DT> : ref;
         const float scale = grow ? fast_exp2(ref - now) : 1.0f;
         if (s > 0) {  // the products up to tile s - 1 are done: S of tile s came after them
           unsigned o[32];
@@ -448,15 +450,9 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     a.lse[(b * a.H + head) * a.Lq + row] = bad ? NAN : sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-int row_pack(int G) {
-  int P = 1;
-  while (P < 16 && G % (2 * P) == 0) P *= 2;
-  return P;
-}
-
 FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
   FwdPlan p;
-  p.P = row_pack(G);
+  p.P = attn_row_pack(G);
   p.packs = H / p.P;
   const long long rows = Lq * p.P;
   p.wide = rows > kRows;
@@ -503,6 +499,12 @@ cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, c
 
 }  // namespace
 
+int attn_row_pack(int G) {
+  int P = 1;
+  while (P < 16 && G % (2 * P) == 0) P *= 2;
+  return P;
+}
+
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
   const FwdPlan p = plan(B, Lq, Lk, H, H / Hkv);
   if (p.splits == 1) return 0;
@@ -516,7 +518,7 @@ bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
   };
   return dtype != kF32 && a.D <= 128 && a.Lk > 0 && fits(a.q, a.sq, a.Lq, a.H) &&
          fits(a.k, a.sk, a.Lk, a.Hkv) && fits(a.v, a.sv, a.Lk, a.Hkv) &&
-         fits(a.out, a.so, a.Lq, a.H) && (row_pack(a.G) == 1 || a.sq.h != 0);
+         fits(a.out, a.so, a.Lq, a.H) && (attn_row_pack(a.G) == 1 || a.sq.h != 0);
 }
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
