@@ -309,3 +309,13 @@ def test_offsets_past_32_bits(binding):
         _near("dk", dk[:, -200:], *want["dk"])
         _near("dv", dv[:, -200:], *want["dv"])
         assert bool((dk[:, :-200] == 0).all()) and bool((dv[:, :-200] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES[1:], ids=["f16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_tails_of_every_walk_length(binding, dtype, D):
+    """What lies past an utterance's end never shows, however many tiles come before the cut one."""
+    for tiles in range(1, 13):
+        for Lq in (40, 200):
+            _check(binding, (1, Lq, tiles * 128 - 20, 1, 1, D), dtype, seed=tiles, lens=True)
+            _check(binding, (1, tiles * 128 - 20, 150, 2, 1, D), dtype, seed=tiles, lens=True)

@@ -11,8 +11,8 @@
 // delta = dO . O of each row is formed by the dq kernel and kept for the other.
 //
 // Two warpgroups share a tile's elementwise work (thread = TMEM lane, each group half of the
-// columns); a warp loads with TMA, a warp issues products, and in the dk/dv kernel a warp fetches
-// the rows' lse and delta.  P and dS are rounded to the tensors' type and written over S and dP in
+// columns); a warp loads with TMA, a warp issues products, one zeroes tails, and in the dk/dv kernel one
+// fetches the rows' lse and delta.  P and dS are rounded to the tensors' type and written over S and dP in
 // TMEM, each group over columns that it alone has read, and go into the products from there.
 // Scores of the next tile are formed while the threads are at this one's dS.
 //
@@ -111,7 +111,7 @@ __device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
 // ---- dq ---------------------------------------------------------------------------
 struct DqShared {
   Pipe k, v;
-  unsigned long long rows_full, scores, ds_ready, done, drained;
+  unsigned long long rows_full, scores, ds_ready, done, tail_full, drained;
   unsigned tmem;
   int gave_up, first, last;
   float half[kRows];
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *q_tile = tiles, *g_tile = q_tile + S::TILE, *k_slots = g_tile + S::TILE,
                 *v_slots = k_slots + S::KS * S::TILE;
   const AttnArgs &a = f.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   long long id = blockIdx.x;
   const int split = (int)(id % f.p.dq_splits);
   id /= f.p.dq_splits;
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.scores, 1);
     mbar_init(&sh.ds_ready, 256);
     mbar_init(&sh.done, 1);
+    mbar_init(&sh.tail_full, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
@@ -173,13 +174,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const unsigned tmem = sh.tmem;
+  const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
   const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
   const int t0 = (int)((long long)all * split / f.p.dq_splits),
             t1 = (int)((long long)all * (split + 1) / f.p.dq_splits), T = t1 - t0;
   auto frame = [&](int s) { return first + (t0 + s) * kRows; };
   constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ
+  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
+  // k a warp of its own zeroes them (unless TMA did, past the tensor's end): the load then arrives
+  // at tail_full, and that warp hands the tile on.
+  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
@@ -193,8 +198,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ks = s % S::KS, vs = s % S::VS;
         ok = wait(&sh.k.empty[ks], ((unsigned)(s / S::KS) & 1) ^ 1);
         if (!ok) break;
-        arrive_expect_tx(&sh.k.full[ks], S::TILE);
-        load_rows<DP>(&km, k_slots + ks * S::TILE, &sh.k.full[ks], hk * f.k_h, frame(s), (int)b * f.k_b);
+        unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[ks];
+        arrive_expect_tx(bar, S::TILE);
+        load_rows<DP>(&km, k_slots + ks * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
         ok = wait(&sh.v.empty[vs], ((unsigned)(s / S::VS) & 1) ^ 1);
         if (!ok) {
           ++s;
@@ -211,51 +217,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (warp == 9 && T > 0) {
+    if (warp == 10 && cut) {
+      const int slot = (T - 1) % S::KS;
+      if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
+        zero_tail(k_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame(T - 1), kRows);
+      if (lane == 0) mbar_arrive(&sh.k.full[slot]);
+    }
+    if (warp == 9 && T > 0 && elect_one()) {
       constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
       const unsigned qa = smem_u32(q_tile), ga = smem_u32(g_tile), ka = smem_u32(k_slots),
                      va = smem_u32(v_slots);
-      bool ok = __all_sync(0xffffffffu, wait(&sh.rows_full, 0));
+      bool ok = wait(&sh.rows_full, 0);
       auto scores = [&](int s) {
-        const int slot = s % S::KS, valid = n.nk - frame(s);
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.k.full[slot], (unsigned)(s / S::KS) & 1));
-        // frames past the utterance's end may hold anything, and 0 times NaN is NaN
-        if (ok && valid < kRows)
-          zero_tail(k_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, max(valid, 0), kRows);
+        const int slot = s % S::KS;
+        ok = ok && wait(&sh.k.full[slot], (unsigned)(s / S::KS) & 1);
         tc_fence_after();
-        if (ok && lane == 0)
+        if (ok)
           mma_rows<DP>(tmem + (s & 1) * kRows, qa, S::CHUNK, ka + slot * S::TILE, S::CHUNK, i_s, false);
-        __syncwarp();
       };
       auto grads = [&](int s) {  // dP of tile s; its scores came before
         const int slot = s % S::VS;
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.v.full[slot], (unsigned)(s / S::VS) & 1));
+        ok = ok && wait(&sh.v.full[slot], (unsigned)(s / S::VS) & 1);
         tc_fence_after();
-        if (ok && lane == 0) {
-          mma_rows<DP>(tmem + kDp, ga, S::CHUNK, va + slot * S::TILE, S::CHUNK, i_s, false);
-          mma_commit(&sh.scores);
-          mma_commit(&sh.v.empty[slot]);
-        }
-        __syncwarp();
+        if (!ok) return;
+        mma_rows<DP>(tmem + kDp, ga, S::CHUNK, va + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_commit(&sh.scores);
+        mma_commit(&sh.v.empty[slot]);
       };
       scores(0);
       grads(0);
       for (int s = 0; ok && s < T; ++s) {
         if (s + 1 < T) scores(s + 1);
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.ds_ready, s & 1));
+        ok = ok && wait(&sh.ds_ready, s & 1);
         tc_fence_after();
         if (s + 1 < T) grads(s + 1);
-        if (ok && lane == 0) {
-          const int slot = s % S::KS;
-          const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
-          mma_across<64>(tmem + kAcc, ds, at, S::CHUNK, i_o, s > 0);
-          mma_across<64>(tmem + kAcc, ds + 64, at + 64 * 128, S::CHUNK, i_o, true);
-          mma_commit(&sh.k.empty[slot]);
-          if (s + 1 == T) mma_commit(&sh.done);
-        }
-        __syncwarp();
+        if (!ok) break;
+        const int slot = s % S::KS;
+        const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
+        mma_across<64>(tmem + kAcc, ds, at, S::CHUNK, i_o, s > 0);
+        mma_across<64>(tmem + kAcc, ds + 64, at + 64 * 128, S::CHUNK, i_o, true);
+        mma_commit(&sh.k.empty[slot]);
+        if (s + 1 == T) mma_commit(&sh.done);
       }
-      if (!ok && lane == 0) {
+      if (!ok) {
         mma_commit(&sh.drained);
         Waiter::drain(&sh.drained, 0);
       }
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 struct DkvShared {
   Pipe q, g;
   unsigned long long frames_full, s_full, p_ready, dp_full, ds_ready, stat_full[2], stat_empty[2],
-      done, drained;
+      done, q_tail[2], g_tail[2], drained;
   unsigned tmem;
   int gave_up;
   unsigned char active[kTileBits];  // row tiles with a query that sees these frames
@@ -374,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *k_tile = tiles, *v_tile = k_tile + S::TILE, *q_slots = v_tile + S::TILE,
                 *g_slots = q_slots + S::RS * S::TILE;
   const AttnArgs &a = f.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   long long id = blockIdx.x;
   const int split = (int)(id % f.p.dkv_splits);
   id /= f.p.dkv_splits;
@@ -404,6 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.stat_empty[i], 256);
     }
     mbar_init(&sh.done, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.q_tail[i], 1);
+      mbar_init(&sh.g_tail[i], 1);
+    }
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const unsigned tmem = sh.tmem;
+  const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
   auto skip = [&](int t) {
     const int rt = t % row_tiles;
@@ -434,6 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   const int start = next(t0);
   const bool any = start < t1;
+  // Rows past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last row tile of
+  // each walk over the rows a warp of its own zeroes them (unless TMA did, past the tensor's end):
+  // the loads then arrive at q_tail and g_tail, and that warp hands the tiles on.
+  auto cut = [&](int t) { return n.nq < a.Lq && (t % row_tiles + 1) * per > n.nq; };
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = 2 * kRows + DP;
 
   if (warp >= 8) {
@@ -449,15 +461,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const unsigned turn = ((unsigned)(s / S::RS) & 1) ^ 1;
         ok = wait(&sh.q.empty[slot], turn);
         if (!ok) break;
-        arrive_expect_tx(&sh.q.full[slot], S::TILE);
-        load_rows<DP>(&qm, q_slots + slot * S::TILE, &sh.q.full[slot], h * f.q_h, l, (int)b * f.q_b);
+        unsigned long long *bar = cut(t) ? &sh.q_tail[slot] : &sh.q.full[slot];
+        arrive_expect_tx(bar, S::TILE);
+        load_rows<DP>(&qm, q_slots + slot * S::TILE, bar, h * f.q_h, l, (int)b * f.q_b);
         ok = wait(&sh.g.empty[slot], turn);
         if (!ok) {
           ++s;
           break;
         }
-        arrive_expect_tx(&sh.g.full[slot], S::TILE);
-        load_rows<DP>(&gm, g_slots + slot * S::TILE, &sh.g.full[slot], h * f.go_h, l, (int)b * f.go_b);
+        bar = cut(t) ? &sh.g_tail[slot] : &sh.g.full[slot];
+        arrive_expect_tx(bar, S::TILE);
+        load_rows<DP>(&gm, g_slots + slot * S::TILE, bar, h * f.go_h, l, (int)b * f.go_b);
       }
       if (!ok) {
         Waiter::drain(&sh.frames_full, 0);
@@ -467,63 +481,66 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-    if (warp == 9 && any) {
+    if (warp == 11 && any) {
+      int s = 0;
+      unsigned turns = 0;  // bit: parity of the slot's next cut tile
+      for (int t = start; t < t1; t = next(t + 1), ++s) {
+        if (!cut(t)) continue;
+        const int slot = s % S::RS, valid = (n.nq - t % row_tiles * per) * P;
+        if (!__all_sync(0xffffffffu, wait(&sh.q_tail[slot], turns >> slot & 1))) break;
+        zero_tail(q_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, valid, kRows);
+        if (lane == 0) mbar_arrive(&sh.q.full[slot]);
+        if (!__all_sync(0xffffffffu, wait(&sh.g_tail[slot], turns >> slot & 1))) break;
+        zero_tail(g_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, valid, kRows);
+        if (lane == 0) mbar_arrive(&sh.g.full[slot]);
+        turns ^= 1u << slot;
+      }
+    }
+    if (warp == 9 && any && elect_one()) {
       constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
       const unsigned ka = smem_u32(k_tile), va = smem_u32(v_tile), qa = smem_u32(q_slots),
                      ga = smem_u32(g_slots);
-      bool ok = __all_sync(0xffffffffu, wait(&sh.frames_full, 0));
-      // rows past the utterance's end may hold anything, and 0 times NaN is NaN
-      auto ready = [&](Pipe &pipe, unsigned char *slots, int s, int t) {
-        const int slot = s % S::RS, valid = (n.nq - t % row_tiles * per) * P;
-        ok = __all_sync(0xffffffffu, ok && wait(&pipe.full[slot], (unsigned)(s / S::RS) & 1));
-        if (ok && valid < kRows) zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, valid, kRows);
+      bool ok = wait(&sh.frames_full, 0);
+      auto scores = [&](int s) {  // S^T
+        const int slot = s % S::RS;
+        ok = ok && wait(&sh.q.full[slot], (unsigned)(s / S::RS) & 1);
         tc_fence_after();
+        if (!ok) return;
+        mma_rows<DP>(tmem, ka, S::CHUNK, qa + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_commit(&sh.s_full);
       };
-      auto scores = [&](int s, int t) {  // S^T
-        ready(sh.q, q_slots, s, t);
-        if (ok && lane == 0) {
-          mma_rows<DP>(tmem, ka, S::CHUNK, qa + s % S::RS * S::TILE, S::CHUNK, i_s, false);
-          mma_commit(&sh.s_full);
-        }
-        __syncwarp();
-      };
-      auto grads = [&](int s, int t) {  // dP^T
-        ready(sh.g, g_slots, s, t);
-        if (ok && lane == 0) {
-          mma_rows<DP>(tmem + kDp, va, S::CHUNK, ga + s % S::RS * S::TILE, S::CHUNK, i_s, false);
-          mma_commit(&sh.dp_full);
-        }
-        __syncwarp();
+      auto grads = [&](int s) {  // dP^T
+        const int slot = s % S::RS;
+        ok = ok && wait(&sh.g.full[slot], (unsigned)(s / S::RS) & 1);
+        tc_fence_after();
+        if (!ok) return;
+        mma_rows<DP>(tmem + kDp, va, S::CHUNK, ga + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_commit(&sh.dp_full);
       };
       int t = start;
-      scores(0, t);
-      grads(0, t);
+      scores(0);
+      grads(0);
       for (int s = 0; ok && t < t1; ++s) {
         const int after = next(t + 1), slot = s % S::RS;
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.p_ready, s & 1));
+        ok = wait(&sh.p_ready, s & 1);
         tc_fence_after();
-        if (ok && lane == 0) {  // dV += P^T dO
-          const unsigned at = ga + slot * S::TILE;
-          mma_across<64>(tmem + kDv, tmem, at, S::CHUNK, i_o, s > 0);
-          mma_across<64>(tmem + kDv, tmem + 64, at + 64 * 128, S::CHUNK, i_o, true);
-          mma_commit(&sh.g.empty[slot]);
-        }
-        __syncwarp();
-        if (after < t1) scores(s + 1, after);
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.ds_ready, s & 1));
+        if (!ok) break;
+        const unsigned g_at = ga + slot * S::TILE, q_at = qa + slot * S::TILE;
+        mma_across<64>(tmem + kDv, tmem, g_at, S::CHUNK, i_o, s > 0);  // dV += P^T dO
+        mma_across<64>(tmem + kDv, tmem + 64, g_at + 64 * 128, S::CHUNK, i_o, true);
+        mma_commit(&sh.g.empty[slot]);
+        if (after < t1) scores(s + 1);
+        ok = ok && wait(&sh.ds_ready, s & 1);
         tc_fence_after();
-        if (ok && lane == 0) {  // dK += dS^T Q
-          const unsigned at = qa + slot * S::TILE;
-          mma_across<64>(tmem + kDk, tmem + kDp, at, S::CHUNK, i_o, s > 0);
-          mma_across<64>(tmem + kDk, tmem + kDp + 64, at + 64 * 128, S::CHUNK, i_o, true);
-          mma_commit(&sh.q.empty[slot]);
-          if (after >= t1) mma_commit(&sh.done);
-        }
-        __syncwarp();
-        if (after < t1) grads(s + 1, after);
+        if (!ok) break;
+        mma_across<64>(tmem + kDk, tmem + kDp, q_at, S::CHUNK, i_o, s > 0);  // dK += dS^T Q
+        mma_across<64>(tmem + kDk, tmem + kDp + 64, q_at + 64 * 128, S::CHUNK, i_o, true);
+        mma_commit(&sh.q.empty[slot]);
+        if (after >= t1) mma_commit(&sh.done);
+        if (after < t1) grads(s + 1);
         t = after;
       }
-      if (!ok && lane == 0) {
+      if (!ok) {
         mma_commit(&sh.drained);
         Waiter::drain(&sh.drained, 0);
       }

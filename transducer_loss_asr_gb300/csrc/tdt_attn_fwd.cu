@@ -29,7 +29,7 @@ namespace tdt {
 namespace {
 
 constexpr int kRows = 128;          // rows of a tile, frames of a tile
-constexpr int kThreads = 384;       // two softmax warpgroups; a TMA warp, an MMA warp, two idle
+constexpr int kThreads = 384;       // two softmax warpgroups; a TMA warp, an MMA warp, one for tails
 constexpr float kLazy = 8.0f;
 // float16 weights start at 2^7 and so stay clear of the type's least numbers; at most 2^15
 template <int DT> constexpr float kShift = DT == kF16 ? 7.0f : 0.0f;
@@ -62,7 +62,7 @@ template <int DP, bool WIDE> struct FwdShape {
 
 struct FwdShared {
   unsigned long long full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2],
-      drained;
+      tail_full, drained;
   unsigned tmem;
   int gave_up, first, last;
   float join_m[kRows], join_l[kRows];
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   unsigned char *q_tile = tiles, *slots = tiles + S::NQ * S::TILE;
   const AttnArgs &a = f.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   // this CTA's rows and frames
   long long id = blockIdx.x;
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.empty[i], 1);
     }
     mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.tail_full, 1);
     mbar_init(&sh.drained, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sh.s_full[w], 1);
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const unsigned tmem = sh.tmem;
+  const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
   // frames [first, last) in tiles of 128 from `first`; this CTA takes tiles [t0, t1)
   const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
@@ -155,8 +156,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             t1 = (int)((long long)all * (split + 1) / f.p.splits), T = t1 - t0;
   // tiles of a stream: wide 0, 1, ...; thin w, w + 2, ...
   const int steps0 = WIDE ? T : (T + 1) / 2, steps1 = WIDE ? T : T / 2;
-  auto frame = [&](int w, int s) { return first + (t0 + (WIDE ? s : 2 * s + w)) * kRows; };
+  auto frame_of = [&](int t) { return first + t * kRows; };
+  auto frame = [&](int w, int s) { return frame_of(t0 + (WIDE ? s : 2 * s + w)); };
   const float c = a.scale * kLog2e;
+
+  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
+  // v, which is the last tile loaded, a warp of its own zeroes them (unless TMA did, past the
+  // tensor's end): the load then arrives at tail_full, and that warp hands the tile on.
+  const bool cut = T > 0 && n.nk < a.Lk && frame_of(t1 - 1) + kRows > n.nk;
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();  // to the softmax warps, which hold a row of scores
@@ -174,9 +181,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int slot = at % S::SLOTS;
         const unsigned turn = (unsigned)(at / S::SLOTS) & 1;
         if (!wait(&sh.empty[slot], turn ^ 1)) return false;
-        arrive_expect_tx(&sh.full[slot], S::TILE);
+        unsigned long long *bar = cut && at == 2 * T - 1 ? &sh.tail_full : &sh.full[slot];
+        arrive_expect_tx(bar, S::TILE);
         for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, &sh.full[slot],
+          tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, bar,
                       ch * 64, hk * (values ? f.v_h : f.k_h), j0, (int)b * (values ? f.v_b : f.k_b));
         ++at;
         return true;
@@ -193,62 +201,74 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = max(0, at - S::SLOTS); i < at; ++i)
           Waiter::drain(&sh.full[i % S::SLOTS], (unsigned)(i / S::SLOTS) & 1);
     }
-    if (warp == 9 && T > 0) {
+    if (warp == 10 && cut) {
+      const int slot = (2 * T - 1) % S::SLOTS;
+      if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
+        zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame_of(t1 - 1), kRows);
+      if (lane == 0) mbar_arrive(&sh.full[slot]);
+    }
+    if (warp == 9 && T > 0 && elect_one()) {
       constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
       const unsigned q_addr = smem_u32(q_tile), s_addr = smem_u32(slots);
-      int at = 0;  // slots used so far, in the loader's order
-      bool ok = __all_sync(0xffffffffu, wait(&sh.q_full, 0));
-      auto scores = [&](int w, int slot_at) {  // S_w = Q_w K^T
-        const int slot = slot_at % S::SLOTS;
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.full[slot], (unsigned)(slot_at / S::SLOTS) & 1));
-        tc_fence_after();
-        if (ok && lane == 0) {
-          mma_rows<DP>(tmem + w * kRows, q_addr + (WIDE ? w : 0) * S::TILE, S::CHUNK,
-                       s_addr + slot * S::TILE, S::CHUNK, i_s, false);
-          mma_commit(&sh.s_full[w]);
-          if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
-        }
-        __syncwarp();
+      bool ok = wait(&sh.q_full, 0);
+      auto loaded = [&](int at) {  // slots count up in the loader's order
+        ok = ok && wait(&sh.full[at % S::SLOTS], (unsigned)(at / S::SLOTS) & 1);
       };
-      auto values = [&](int w, int s, int slot_at) {  // O_w += P_w V
-        const int slot = slot_at % S::SLOTS;
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.full[slot], (unsigned)(slot_at / S::SLOTS) & 1));
-        const int valid = n.nk - frame(w, s);
-        // frames past the utterance's end may hold anything, and 0 times NaN is NaN
-        if (ok && valid < kRows && (!WIDE || w == 0))
-          zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, max(valid, 0), kRows);
-        ok = __all_sync(0xffffffffu, ok && wait(&sh.p_ready[w], s & 1));
+      auto scores = [&](int w, int at) {  // S_w = Q_w K^T
         tc_fence_after();
-        if (ok && lane == 0) {
-          mma_across<kRows>(tmem + 2 * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
-                            S::CHUNK, i_o, s > 0);
-          if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
-          if (s + 1 == (w ? steps1 : steps0)) mma_commit(&sh.o_full[w]);
-        }
-        __syncwarp();
+        if (!ok) return;
+        const int slot = at % S::SLOTS;
+        mma_rows<DP>(tmem + w * kRows, q_addr + (WIDE ? w : 0) * S::TILE, S::CHUNK,
+                     s_addr + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_commit(&sh.s_full[w]);
+        if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
       };
+      auto values = [&](int w, int s, int at) {  // O_w += P_w V
+        const int slot = at % S::SLOTS;
+        ok = ok && wait(&sh.p_ready[w], s & 1);
+        tc_fence_after();
+        if (!ok) return;
+        mma_across<kRows>(tmem + 2 * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
+                          S::CHUNK, i_o, s > 0);
+        if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
+        if (s + 1 == (w ? steps1 : steps0)) mma_commit(&sh.o_full[w]);
+      };
+      loaded(0);
       if (WIDE) {
         scores(0, 0);
         scores(1, 0);
-        at = 1;
         for (int s = 0; ok && s < T; ++s) {
-          for (int w = 0; w < 2; ++w) {
-            values(w, s, at);
-            if (s + 1 < T) scores(w, at + 1);
+          const int at = 1 + 2 * s;
+          loaded(at);
+          values(0, s, at);
+          if (s + 1 < T) {
+            loaded(at + 1);
+            scores(0, at + 1);
           }
-          at += 2;
+          values(1, s, at);
+          if (s + 1 < T) scores(1, at + 1);
         }
       } else {
+        int at = 0;
         scores(0, at++);
-        if (steps1 > 0) scores(1, at++);
+        if (steps1 > 0) {
+          loaded(at);
+          scores(1, at++);
+        }
         for (int s = 0; ok && s < steps0; ++s)
           for (int w = 0; w < 2; ++w) {
             const int steps = w ? steps1 : steps0;
-            if (s < steps) values(w, s, at++);
-            if (s + 1 < steps) scores(w, at++);
+            if (s < steps) {
+              loaded(at);
+              values(w, s, at++);
+            }
+            if (s + 1 < steps) {
+              loaded(at);
+              scores(w, at++);
+            }
           }
       }
-      if (!ok && lane == 0) {  // products in flight end before TMEM is freed
+      if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(&sh.drained);
         Waiter::drain(&sh.drained, 0);
       }
