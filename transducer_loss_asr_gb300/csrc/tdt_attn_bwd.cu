@@ -29,7 +29,7 @@ constexpr int kRows = 128;
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;  // 3 warpgroups x 168 = 2 x 208 + 88
 constexpr int kWorkRegs = 208, kOtherRegs = 88;
-// float16 weights are held as 2^15 p <= 2^15 for the product with dO: what a frame gets from rows that
+// float16 weights are held as 2^15 p for the product with dO (p <= 1, so below the type's most): what a frame gets from rows that
 // hardly weigh it stays clear of the type's least numbers.  (dS has no such bound, and is held as it is.)
 template <int DT> constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
 template <int DT> constexpr float kUnshift = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
@@ -305,19 +305,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(p_col + 32, y[1]);
       tmem_wait_ld();
       const int j0 = frame(s) + group * 64;
-      const bool cut = __any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64);
-      const int lo = range.x - j0;
-      const unsigned len = (unsigned)(range.y - range.x);
+      const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2),
+                   d2 = make_float2(-delta, -delta);
+      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64)) {
+        // frames that the row does not see: s = -inf weighs 0, and dP may be anything
+        const int lo = range.x - j0;
+        const unsigned len = (unsigned)(range.y - range.x);
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if ((unsigned)(i - lo) >= len) {
+            x[i >> 5][i & 31] = 0xff800000u;
+            y[i >> 5][i & 31] = 0;
+          }
+      }
 #pragma unroll
       for (int i = 0; i < 64; i += 2) {
-        float d[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float p = fast_exp2(fmaf(__uint_as_float(x[i >> 5][(i + k) & 31]), c, -lse2));
-          d[k] = p * (__uint_as_float(y[i >> 5][(i + k) & 31]) - delta);
-          if (cut && (unsigned)(i + k - lo) >= len) d[k] = 0.0f;
-        }
-        out[i / 2] = pack2<DT>(d[0], d[1]);
+        const float2 z = fma2(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), c2, l2);
+        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        const float2 ds = mul2(p, add2(pair(y[i >> 5][i & 31], y[i >> 5][(i + 1) & 31]), d2));
+        out[i / 2] = pack2<DT>(ds.x, ds.y);
       }
       tmem_st32(s_col, out);
       tmem_wait_st();
@@ -362,7 +368,7 @@ struct DkvShared {
   int gave_up;
   unsigned char active[kTileBits];  // row tiles with a query that sees these frames
   int cut[2];                       // whether some row of the tile sees only part of them
-  __align__(16) float lse2[2][kRows], delta[2][kRows];
+  __align__(16) float lse2[2][kRows], delta[2][kRows];  // of the rows, both negated
   __align__(16) int lo[2][kRows], len[2][kRows];
 };
 
@@ -556,11 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < kRows / 32; ++x) {
           const int r = x * 32 + lane, i = i0 + r / P;
           const int2 w = row_range(a, b, i, n);
-          float l2 = INFINITY, dl = 0.0f;  // rows that see nothing: every weight is 0
+          float l2 = -INFINITY, dl = 0.0f;  // rows that see nothing: every weight is 0
           if (w.y > w.x) {
             const long long at = (b * a.H + h0 + r % P) * a.Lq + i;
-            l2 = a.lse[at] * kLog2e - kShift<DT>;
-            dl = a.delta[at] * kUnshift<DT>;
+            l2 = kShift<DT> - a.lse[at] * kLog2e;
+            dl = -a.delta[at] * kUnshift<DT>;
             cut |= w.x > j0 || w.y < min(j0 + kRows, n.nk);
           }
           sh.lse2[buf][r] = l2;
@@ -594,14 +600,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(s_col + 32, x[1]);
         tmem_wait_ld();
         const float *lse2 = sh.lse2[buf] + group * 64, *delta = sh.delta[buf] + group * 64;
+        const float2 c2 = make_float2(c, c);
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
           const float4 l = *reinterpret_cast<const float4 *>(lse2 + i);
-          const float ls[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            x[i >> 5][(i + k) & 31] =
-                __float_as_uint(fast_exp2(fmaf(__uint_as_float(x[i >> 5][(i + k) & 31]), c, -ls[k])));
+          unsigned *v = &x[i >> 5][i & 31];
+          const float2 z0 = fma2(pair(v[0], v[1]), c2, make_float2(l.x, l.y)),
+                       z1 = fma2(pair(v[2], v[3]), c2, make_float2(l.z, l.w));
+          v[0] = __float_as_uint(fast_exp2(z0.x));
+          v[1] = __float_as_uint(fast_exp2(z0.y));
+          v[2] = __float_as_uint(fast_exp2(z1.x));
+          v[3] = __float_as_uint(fast_exp2(z1.y));
         }
         if (past) {
 #pragma unroll
@@ -631,15 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
           const float4 dl = *reinterpret_cast<const float4 *>(delta + i);
-          const float ds[4] = {dl.x, dl.y, dl.z, dl.w};
-          float v[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float p = __uint_as_float(x[i >> 5][(i + k) & 31]);
-            v[k] = p * fmaf(__uint_as_float(y[i >> 5][(i + k) & 31]), kUnshift<DT>, -ds[k]);
-          }
-          out[i / 2] = pack2<DT>(v[0], v[1]);
-          out[i / 2 + 1] = pack2<DT>(v[2], v[3]);
+          const float2 un = make_float2(kUnshift<DT>, kUnshift<DT>);
+          const unsigned *p = &x[i >> 5][i & 31], *g = &y[i >> 5][i & 31];
+          const float2 d0 = make_float2(dl.x, dl.y), d1 = make_float2(dl.z, dl.w);
+          const float2 g0 = pair(g[0], g[1]), g1 = pair(g[2], g[3]);
+          const float2 v0 = mul2(pair(p[0], p[1]), DT == kF16 ? fma2(g0, un, d0) : add2(g0, d0)),
+                       v1 = mul2(pair(p[2], p[3]), DT == kF16 ? fma2(g1, un, d1) : add2(g1, d1));
+          out[i / 2] = pack2<DT>(v0.x, v0.y);
+          out[i / 2 + 1] = pack2<DT>(v1.x, v1.y);
         }
         tmem_st32(d_col, out);
         tmem_wait_st();

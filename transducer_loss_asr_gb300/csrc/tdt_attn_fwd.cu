@@ -68,19 +68,18 @@ struct FwdShared {
   float join_m[kRows], join_l[kRows];
 };
 
-// 128 scores of a row (float32 bits) to weights 2^(s c - ref c); their sum; pairs packed.
+// 32 scores of a row (float32 bits) to weights 2^(s c - ref), packed in pairs and added to sum.
 template <int DT>
-__device__ __forceinline__ float exp_pack(unsigned (&s)[32], float c, float neg, unsigned *out) {
-  float sum0 = 0.0f, sum1 = 0.0f;
+__device__ __forceinline__ void exp_pack(const unsigned (&s)[32], float c, float neg, unsigned *out,
+                                         float2 &sum) {
+  const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    const float p0 = fast_exp2(fmaf(__uint_as_float(s[i]), c, neg));
-    const float p1 = fast_exp2(fmaf(__uint_as_float(s[i + 1]), c, neg));
-    sum0 += p0;
-    sum1 += p1;
-    out[i / 2] = pack2<DT>(p0, p1);
+    const float2 z = fma2(pair(s[i], s[i + 1]), c2, n2);
+    const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+    sum = add2(sum, p);
+    out[i / 2] = pack2<DT>(p.x, p.y);
   }
-  return sum0 + sum1;
 }
 
 template <int DT, int DP, bool WIDE>
@@ -298,9 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 128; i += 4) {
-        m0 = fmaxf(m0, fmaxf(__uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i + 1) & 31])));
-        m1 = fmaxf(m1, fmaxf(__uint_as_float(x[i >> 5][(i + 2) & 31]), __uint_as_float(x[i >> 5][(i + 3) & 31])));
+      for (int i = 0; i < 32; i += 2) {
+        m0 = max3(m0, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
+        m1 = max3(m1, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
+        m0 = max3(m0, __uint_as_float(x[2][i]), __uint_as_float(x[2][i + 1]));
+        m1 = max3(m1, __uint_as_float(x[3][i]), __uint_as_float(x[3][i + 1]));
       }
       const float top = fmaxf(m0, m1) * c;
       const bool grow = top > ref + (kLazy + kShift<DT>);  // from -inf: any score
@@ -323,12 +324,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float neg = ref == -INFINITY ? 0.0f : -ref;
       unsigned p[32];
+      float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        l += exp_pack<DT>(x[2 * i], c, neg, p);
-        l += exp_pack<DT>(x[2 * i + 1], c, neg, p + 16);
+        exp_pack<DT>(x[2 * i], c, neg, p, sum0);
+        exp_pack<DT>(x[2 * i + 1], c, neg, p + 16, sum1);
         tmem_st32(s_col + i * 32, p);
       }
+      sum0 = add2(sum0, sum1);
+      l += sum0.x + sum0.y;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sh.p_ready[stream]);
