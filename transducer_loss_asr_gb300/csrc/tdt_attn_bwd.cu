@@ -1,13 +1,17 @@
 // tdt_attn_bwd.cu -- the backward pass of cross attention on the 5th-generation tensor cores, for
 // float16 and bfloat16 heads of up to 128 elements.
 //
-// Two kernels, so that every sum has one owner and a fixed order (no atomics):
+// Every sum has one owner and a fixed order (no atomics).  Where the rows of a key head fill at most one
+// tile of 128 and heads are at most 64 wide (label states of one utterance), one kernel walks the frames
+// and forms all three gradients with five products a tile; P and dS go through shared memory, since
+// they are contracted along both axes.  Otherwise two kernels:
 //   dq    a CTA holds 128 rows ((query, head) pairs, packed as in the forward pass) and walks the
 //         frames:  S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K      3 products a tile
 //   dk/dv a CTA holds 128 frames and walks the rows of the heads of its group, with the scores
 //         transposed:  S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q    4 products a tile
 // P = 2^(S c - lse) is formed again from the forward pass's lse.  Seven products where five would
-// do with one walk; that one would add its dQ tiles to memory in float32 in no fixed order.
+// do with one walk; over several row tiles that one would add its dQ tiles to memory in float32 in no
+// fixed order.
 // delta = dO . O of each row is formed by the dq kernel and kept for the other.
 //
 // Two warpgroups share a tile's elementwise work (thread = TMEM lane, each group half of the
@@ -39,6 +43,7 @@ struct BwdPlan {
   int P, packs, tiles;          // heads of a row tile, H / P, row tiles of a pack
   int f_tiles;                  // frame tiles
   int dq_splits, dkv_splits;
+  bool one;                     // one row tile a key head and D <= 64: attn_one_tc_kernel
 };
 
 struct BwdArgs {
@@ -692,6 +697,325 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) tmem_free<512>(tmem);
 }
 
+// ---- dq, dk and dv of one row tile -----------------------------------------------------
+// Threads: two warpgroups of elementwise work (thread = row, each group half of the frames), one that
+// stores dk and dv tiles (thread = frame), four warps: TMA, products, tails.
+constexpr int kOneThreads = 512;
+constexpr int kOneLaunchRegs = 128;  // 4 x 128 = 2 x 160 + 112 + 80
+constexpr int kOneWorkRegs = 160, kOneStoreRegs = 112, kOneOtherRegs = 80;
+
+struct OneShape {
+  static constexpr int TILE = kRows * 128;            // 64 columns
+  static constexpr int KV = 2;                        // slots of k and of v
+  static constexpr int PDS = 2 * TILE;                // P or dS: 128 x 128
+  static constexpr int BYTES = (2 + 2 * KV) * TILE + 2 * PDS;
+};
+
+struct OneShared {
+  Pipe k, v;
+  unsigned long long rows_in, rows_full, sp_full, pds_ready, pds_free, dkv_full, dkv_free, done, tail_full,
+      drained;
+  unsigned tmem;
+  int gave_up, first, last;
+  float half[kRows];
+};
+
+template <int DT>
+__global__ void __launch_bounds__(kOneThreads, 1)
+    attn_one_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
+                       const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                       const __grid_constant__ BwdArgs f) {
+  constexpr int DP = 64;
+  typedef OneShape S;
+  typedef typename Elem<DT>::T E;
+  extern __shared__ unsigned char raw[];
+  __shared__ OneShared sh;
+  unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  unsigned char *q_tile = tiles, *g_tile = q_tile + S::TILE, *k_slots = g_tile + S::TILE,
+                *v_slots = k_slots + S::KV * S::TILE, *p_tile = v_slots + S::KV * S::TILE,
+                *ds_tile = p_tile + S::PDS;
+  const AttnArgs &a = f.a;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int split = (int)(blockIdx.x % f.p.dq_splits);
+  const long long cta = blockIdx.x / f.p.dq_splits;  // = b * Hkv + hk
+  const int hk = (int)(cta % a.Hkv), h0 = hk * a.G;
+  const long long b = cta / a.Hkv;
+  const int P = f.p.P, per = kRows / P;
+  const Lens n = utt_lens(a, b);
+  if (threadIdx.x == 0) {
+    pipe_init(sh.k, S::KV);
+    pipe_init(sh.v, S::KV);
+    mbar_init(&sh.rows_in, 1);
+    mbar_init(&sh.rows_full, 1);
+    mbar_init(&sh.sp_full, 1);
+    mbar_init(&sh.pds_ready, 256);
+    mbar_init(&sh.pds_free, 1);
+    mbar_init(&sh.dkv_full, 1);
+    mbar_init(&sh.dkv_free, 128);
+    mbar_init(&sh.done, 1);
+    mbar_init(&sh.tail_full, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init_cluster();
+    sh.gave_up = 0;
+    sh.first = INT_MAX;
+    sh.last = 0;
+  }
+  if (warp == 13) tmem_alloc<512>(&sh.tmem);
+  __syncthreads();
+  const int group = warp >> 2, r = threadIdx.x & 127, row = r / P, head = h0 + r % P;
+  int2 range = make_int2(0, 0);
+  if (group < 2) {
+    range = row_range(a, b, row, n);
+    const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, range.y);
+    if (group == 0 && lane == 0 && hi > 0) {
+      atomicMin(&sh.first, lo);
+      atomicMax(&sh.last, hi);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
+  const Waiter wait{&sh.gave_up};
+  // this CTA's frame tiles [t0, t1); those that a row sees are [ta, tb)
+  const int t0 = (int)((long long)f.p.f_tiles * split / f.p.dq_splits),
+            t1 = (int)((long long)f.p.f_tiles * (split + 1) / f.p.dq_splits);
+  const int ta = sh.last > sh.first ? max(t0, sh.first / kRows) : t1,
+            tb = min(t1, (sh.last + kRows - 1) / kRows), T = max(0, tb - ta);
+  auto frame = [&](int s) { return (ta + s) * kRows; };
+  constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = kDv + DP, kAcc = kDk + DP;
+  // Rows and frames past the utterance's ends may hold anything, and 0 times NaN is NaN: a warp of its own
+  // zeroes them in the tiles of q and dO and in the last tile of k before handing these on (unless TMA
+  // did, past the tensor's ends).
+  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk, cut_rows = n.nq < a.Lq;
+
+  if (group == 3) {
+    warpgroup_give_registers<kOneOtherRegs>();
+    if (warp == 12 && lane == 0 && T > 0) {
+      unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
+      arrive_expect_tx(rows, 2 * S::TILE);
+      tma_load_4d(&qm, q_tile, rows, 0, h0 * f.q_h, 0, (int)b * f.q_b);
+      tma_load_4d(&gm, g_tile, rows, 0, h0 * f.go_h, 0, (int)b * f.go_b);
+      bool ok = true;
+      int s = 0;
+      for (; ok && s < T; ++s) {
+        const int slot = s % S::KV;
+        const unsigned turn = ((unsigned)(s / S::KV) & 1) ^ 1;
+        ok = wait(&sh.k.empty[slot], turn) && wait(&sh.v.empty[slot], turn);
+        if (!ok) break;
+        unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
+        arrive_expect_tx(bar, S::TILE);
+        tma_load_4d(&km, k_slots + slot * S::TILE, bar, 0, hk * f.k_h, frame(s), (int)b * f.k_b);
+        arrive_expect_tx(&sh.v.full[slot], S::TILE);
+        tma_load_4d(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], 0, hk * f.v_h, frame(s), (int)b * f.v_b);
+      }
+      if (!ok) {  // copies in flight land before the CTA ends
+        Waiter::drain(rows, 0);
+        for (int i = max(0, s - S::KV); i < s; ++i) {
+          Waiter::drain(&sh.k.full[i % S::KV], (unsigned)(i / S::KV) & 1);
+          Waiter::drain(&sh.v.full[i % S::KV], (unsigned)(i / S::KV) & 1);
+        }
+      }
+    }
+    if (warp == 14 && T > 0) {
+      if (cut_rows) {
+        if (__all_sync(0xffffffffu, wait(&sh.rows_in, 0))) {
+          zero_tail(q_tile, 1, S::TILE, n.nq * P, kRows);
+          zero_tail(g_tile, 1, S::TILE, n.nq * P, kRows);
+        }
+        if (lane == 0) mbar_arrive(&sh.rows_full);
+      }
+      if (cut) {
+        const int slot = (T - 1) % S::KV;
+        if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
+          zero_tail(k_slots + slot * S::TILE, 1, S::TILE, n.nk - frame(T - 1), kRows);
+        if (lane == 0) mbar_arrive(&sh.k.full[slot]);
+      }
+    }
+    if (warp == 13 && T > 0 && elect_one()) {
+      constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_t = mma_desc<DT>(DP, true, true),
+                         i_o = mma_desc<DT>(DP, true);
+      const unsigned qa = smem_u32(q_tile), ga = smem_u32(g_tile), ka = smem_u32(k_slots),
+                     va = smem_u32(v_slots), pa = smem_u32(p_tile), da = smem_u32(ds_tile);
+      bool ok = wait(&sh.rows_full, 0);
+      auto scores = [&](int s) {  // S and dP
+        const int slot = s % S::KV;
+        const unsigned turn = (unsigned)(s / S::KV) & 1;
+        ok = ok && wait(&sh.k.full[slot], turn) && wait(&sh.v.full[slot], turn);
+        tc_fence_after();
+        if (!ok) return;
+        mma_rows<DP>(tmem, qa, S::TILE, ka + slot * S::TILE, S::TILE, i_s, false);
+        mma_rows<DP>(tmem + kDp, ga, S::TILE, va + slot * S::TILE, S::TILE, i_s, false);
+        mma_commit(&sh.sp_full);
+        mma_commit(&sh.v.empty[slot]);
+      };
+      scores(0);
+      for (int s = 0; ok && s < T; ++s) {
+        const int slot = s % S::KV;
+        ok = wait(&sh.pds_ready, s & 1);
+        if (s + 1 < T) scores(s + 1);
+        ok = ok && wait(&sh.dkv_free, (s & 1) ^ 1);
+        tc_fence_after();
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)  // dV = P^T dO
+          mma_ss(tmem + kDv, desc_mn_major(pa + k * 2048, S::TILE), desc_mn_major(ga + k * 2048, S::TILE),
+                 i_t, k > 0);
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)  // dK = dS^T Q
+          mma_ss(tmem + kDk, desc_mn_major(da + k * 2048, S::TILE), desc_mn_major(qa + k * 2048, S::TILE),
+                 i_t, k > 0);
+        mma_commit(&sh.dkv_full);
+#pragma unroll
+        for (int k = 0; k < kRows / 16; ++k)  // dQ += dS K
+          mma_ss(tmem + kAcc, desc_k_major(da + (k / 4) * S::TILE + (k % 4) * 32),
+                 desc_mn_major(ka + slot * S::TILE + k * 2048, S::TILE), i_o, s > 0 || k > 0);
+        mma_commit(&sh.k.empty[slot]);
+        mma_commit(&sh.pds_free);
+        if (s + 1 == T) mma_commit(&sh.done);
+      }
+      if (!ok) {
+        mma_commit(&sh.drained);
+        Waiter::drain(&sh.drained, 0);
+      }
+    }
+  } else if (group == 2) {
+    warpgroup_give_registers<kOneStoreRegs>();
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    const float zero[32] = {};
+    for (int t = t0; t < t1; ++t) {
+      const int j = t * kRows + r, s = t - ta;
+      const bool sums = t >= ta && t < tb;
+      bool ok = true;
+      if (sums) {
+        ok = wait(&sh.dkv_full, s & 1);
+        ok = __all_sync(0xffffffffu, ok) && !*reinterpret_cast<volatile int *>(&sh.gave_up);
+        __syncwarp();
+        tc_fence_after();
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // 32 columns of dv, dv, dk, dk
+        void *out = i < 2 ? a.dv : a.dk;
+        const Strides &st = i < 2 ? a.sdv : a.sdk;
+        const long long at = b * st.b + j * st.l + hk * st.h;
+        if (!sums) {
+          if (j < a.Lk) store32<DT>(out, at, zero, (i & 1) * 32, a.D);
+          continue;
+        }
+        unsigned o[32];
+        tmem_ld32(tmem + lanes + kDv + i * 32, o);
+        tmem_wait_ld();
+        if (i == 3) {
+          tc_fence_before();
+          mbar_arrive(&sh.dkv_free);
+        }
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          v[k] = ok ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : NAN;
+        if (j < a.Lk) store32<DT>(out, at, v, (i & 1) * 32, a.D);
+        __syncwarp();
+      }
+    }
+    tc_fence_before();
+  } else {
+    warpgroup_take_registers<kOneWorkRegs>();
+    const bool real = row < n.nq;
+    const long long stat = (b * a.H + head) * a.Lq + row;
+    float delta, lse2 = -INFINITY;  // both negated
+    {
+      const int h = (a.D / 8 + 1) / 2 * 8, d0 = group ? h : 0, len = group ? a.D - h : h;
+      float x = 0.0f;
+      if (real)
+        x = dot16<DT>(static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
+                      static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
+      if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
+      if (group == 1) sh.half[r] = x;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      const float y = sh.half[r];
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (group == 0) sh.half[r] = x + y;
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      delta = -sh.half[r] * kUnshift<DT>;
+    }
+    const float c = a.scale * kLog2e;
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
+    unsigned char *p_row = p_tile + group * S::TILE + r * 128, *ds_row = ds_tile + group * S::TILE + r * 128;
+    const float2 c2 = make_float2(c, c), l2 = make_float2(lse2, lse2), d2 = make_float2(delta, delta),
+                 un = make_float2(kUnshift<DT>, kUnshift<DT>);
+    bool ok = true;
+    for (int s = 0; s < T; ++s) {
+      ok = wait(&sh.sp_full, s & 1);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      unsigned x[2][32], y[2][32];
+      tmem_ld32(s_col, x[0]);
+      tmem_ld32(s_col + 32, x[1]);
+      tmem_ld32(d_col, y[0]);
+      tmem_ld32(d_col + 32, y[1]);
+      tmem_wait_ld();
+      const int j0 = frame(s) + group * 64;
+      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64)) {
+        // frames that the row does not see: s = -inf weighs 0, and dP may be anything
+        const int lo = range.x - j0;
+        const unsigned len = (unsigned)(range.y - range.x);
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if ((unsigned)(i - lo) >= len) {
+            x[i >> 5][i & 31] = 0xff800000u;
+            y[i >> 5][i & 31] = 0;
+          }
+      }
+      ok = wait(&sh.pds_free, (s & 1) ^ 1);  // the products have read the last tile's P and dS
+      if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {  // 8 frames: 16 bytes of P and of dS, swizzled as TMA would
+        unsigned pw[4], dw[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int i = q * 8 + k * 2;
+          const float2 z = fma2(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), c2, l2);
+          const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+          const float2 g = pair(y[i >> 5][i & 31], y[i >> 5][(i + 1) & 31]);
+          const float2 ds = mul2(p, DT == kF16 ? fma2(g, un, d2) : add2(g, d2));
+          pw[k] = pack2<DT>(p.x, p.y);
+          dw[k] = pack2<DT>(ds.x, ds.y);
+        }
+        const int at = (q ^ (r & 7)) * 16;
+        *reinterpret_cast<uint4 *>(p_row + at) = make_uint4(pw[0], pw[1], pw[2], pw[3]);
+        *reinterpret_cast<uint4 *>(ds_row + at) = make_uint4(dw[0], dw[1], dw[2], dw[3]);
+      }
+      fence_async_shared();
+      tc_fence_before();
+      mbar_arrive(&sh.pds_ready);
+    }
+    if (T > 0 && ok) ok = wait(&sh.done, 0);
+    __syncwarp();
+    tc_fence_after();
+    const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
+    unsigned o[32];
+    if (T > 0) {
+      tmem_ld32(tmem + lanes + kAcc + group * 32, o);
+      tmem_wait_ld();
+    }
+    float v[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
+    if (row < a.Lq) {
+      if (f.p.dq_splits > 1)
+        store32f(f.part + ((split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
+      else
+        store32<DT>(a.dq, b * a.sdq.b + row * a.sdq.l + head * a.sdq.h, v, group * 32, a.D);
+    }
+    __syncwarp();
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 13) tmem_free<512>(tmem);
+}
+
 // Adds the splits of a sum in order: 4 columns a thread.  `which`: 0 dq, 1 dv, 2 dk.
 template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ BwdArgs f, int which0) {
@@ -735,7 +1059,7 @@ __global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ B
       make_uint2(pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w));
 }
 
-BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv) {
+BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
   BwdPlan p;
   const int G = H / Hkv;
   p.P = attn_row_pack(G);
@@ -749,7 +1073,8 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv) {
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
   p.dq_splits = splits(B * p.packs * p.tiles, p.f_tiles);
-  p.dkv_splits = splits(B * Hkv * p.f_tiles, (long long)(G / p.P) * p.tiles);
+  p.one = D <= 64 && p.P == G && p.tiles == 1;
+  p.dkv_splits = p.one ? 1 : splits(B * Hkv * p.f_tiles, (long long)(G / p.P) * p.tiles);
   return p;
 }
 
@@ -758,6 +1083,18 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 struct Maps {
   TensorMap q, go, k, v;
 };
+
+template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
+  const cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_one_tc_kernel<DT>),
+                                          OneShape::BYTES + 1024, kOneLaunchRegs);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = (unsigned)(f.a.B * f.a.Hkv);
+  attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
+      m.q.map, m.go.map, m.k.map, m.v.map, f);
+  if (f.p.dq_splits > 1)
+    attn_add_kernel<DT, 64><<<dim3(ctas * (kRows * 16 / 256), 1), 256, 0, stream>>>(f, 0);
+  return cudaGetLastError();
+}
 
 template <int DT, int DP>
 cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
@@ -785,7 +1122,7 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
 }  // namespace
 
 size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
-  const BwdPlan p = plan(B, Lq, Lk, H, Hkv);
+  const BwdPlan p = plan(B, Lq, Lk, H, Hkv, D);
   const size_t tile = (size_t)kRows * (D <= 64 ? 64 : 128) * 4;
   size_t dq = p.dq_splits > 1 ? tile * B * p.packs * p.tiles * p.dq_splits : 0;
   size_t dkv = p.dkv_splits > 1 ? 2 * tile * B * Hkv * p.f_tiles * p.dkv_splits : 0;
@@ -807,7 +1144,7 @@ bool attn_bwd_tc_fits(const AttnArgs &a, int dtype) {
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
   BwdArgs f = {};
   f.a = a;
-  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.Hkv);
+  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D);
   f.part = static_cast<float *>(workspace);
   Maps m;
   const int per = kRows / f.p.P;
@@ -824,6 +1161,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.k_h = m.k.h_mul;
   f.v_b = m.v.b_mul;
   f.v_h = m.v.h_mul;
+  if (f.p.one) return dtype == kF16 ? launch_one<kF16>(f, m, stream) : launch_one<kBF16>(f, m, stream);
   if (dtype == kF16)
     return a.D <= 64 ? launch<kF16, 64>(f, m, stream) : launch<kF16, 128>(f, m, stream);
   return a.D <= 64 ? launch<kBF16, 64>(f, m, stream) : launch<kBF16, 128>(f, m, stream);

@@ -3,16 +3,16 @@
 //
 // A tile is 128 rows, a row being a (query, head) pair: where the group of a key head holds a
 // power of two P of query heads, P heads of 128 / P queries share a tile and so share the frames
-// that are loaded for it.  Two warpgroups each hold a stream of frame tiles:
-//   wide  (more than 128 rows): two row tiles, one a stream, over the same frames;
-//   thin  (at most 128 rows):   one row tile, the streams take the frame tiles in turn and are
-//                               joined at the end: half the steps one after another.
-// One warp loads tiles with TMA, one issues the products, and each stream's 128 threads (thread =
-// row) do the softmax.  Per frame tile and stream:
+// that are loaded for it.  A stream is a row tile's walk over the frames, with 128 threads (thread =
+// row) for its softmax:
+//   wide    (more than 128 rows): a CTA walks two row tiles over the same frames;
+//   single  (at most 128 rows):   a CTA walks one, with half of the SM's TMEM, registers and shared
+//                                 memory, so that two CTAs share an SM.
+// One warp loads tiles with TMA, one issues the products.  Per frame tile and stream:
 //   S = Q K^T            128 x 128, float32 in TMEM, operands in shared memory
 //   P = 2^(S c - m)      rounded to 16 bits, written over S in TMEM
 //   O += P V             P from TMEM, O in TMEM
-// The products of one stream run while the other one's threads are at their softmax.  The
+// The products of one stream run while the threads of the SM's other one are at their softmax.  The
 // reference m of a row moves only when the running maximum has grown by 8 (in base 2), so O is
 // rescaled rarely; weights are then at most 2^8, exact in effect: the factor cancels in O / l.
 // The sum l adds the unrounded float32 weights; P is rounded to the tensors' type, as the
@@ -29,17 +29,14 @@ namespace tdt {
 namespace {
 
 constexpr int kRows = 128;          // rows of a tile, frames of a tile
-constexpr int kThreads = 384;       // two softmax warpgroups; a TMA warp, an MMA warp, one for tails
 constexpr float kLazy = 8.0f;
 // float16 weights start at 2^7 and so stay clear of the type's least numbers; at most 2^15
 template <int DT> constexpr float kShift = DT == kF16 ? 7.0f : 0.0f;
-constexpr int kLaunchRegs = 168;    // 3 warpgroups x 168 = 2 x 208 + 88
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 
 struct FwdPlan {
   int P;          // heads of a tile
   int packs;      // H / P
-  int wide;       // 1: two row tiles a CTA
+  int wide;       // 1: two row tiles a CTA, else one
   int tiles;      // row tiles (CTAs) of a pack
   int splits;     // CTAs that share the frames of a row tile
 };
@@ -55,17 +52,23 @@ template <int DP, bool WIDE> struct FwdShape {
   static constexpr int CHUNKS = DP / 64;
   static constexpr int CHUNK = kRows * 128;          // bytes
   static constexpr int TILE = CHUNKS * CHUNK;
-  static constexpr int NQ = WIDE ? 2 : 1;
-  static constexpr int SLOTS = DP == 64 ? (WIDE ? 8 : 8) : (WIDE ? 4 : 5);
-  static constexpr int BYTES = (NQ + SLOTS) * TILE;
+  static constexpr int NS = WIDE ? 2 : 1;            // streams
+  static constexpr int SLOTS = WIDE ? (DP == 64 ? 8 : 4) : (DP == 64 ? 5 : 2);
+  static constexpr int BYTES = (NS + SLOTS) * TILE;
+  static constexpr int THREADS = NS * 128 + 128;     // softmax; TMA, MMA, tails, a spare warp
+  static constexpr int CTAS = WIDE ? 1 : 2;          // of an SM
+  static constexpr int TMEM = WIDE ? 512 : 256;      // columns: S and O of each stream
+  // registers of a thread: at launch, then of the softmax warpgroups and of the other one, which
+  // adds up to the same: 3 x 168 = 2 x 208 + 88, 2 x 128 = 200 + 56
+  static constexpr int REGS = WIDE ? 168 : 128;
+  static constexpr int SOFTMAX_REGS = WIDE ? 208 : 200;
+  static constexpr int OTHER_REGS = WIDE ? 88 : 56;
 };
 
 struct FwdShared {
-  unsigned long long full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2],
-      tail_full, drained;
+  unsigned long long full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2], tail_full, drained;
   unsigned tmem;
   int gave_up, first, last;
-  float join_m[kRows], join_l[kRows];
 };
 
 // 32 scores of a row (float32 bits) to weights 2^(s c - ref), packed in pairs and added to sum.
@@ -83,14 +86,14 @@ __device__ __forceinline__ void exp_pack(const unsigned (&s)[32], float c, float
 }
 
 template <int DT, int DP, bool WIDE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE>::CTAS)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                        const __grid_constant__ CUtensorMap vm, const __grid_constant__ FwdArgs f) {
   typedef FwdShape<DP, WIDE> S;
   extern __shared__ unsigned char raw[];
   __shared__ FwdShared sh;
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  unsigned char *q_tile = tiles, *slots = tiles + S::NQ * S::TILE;
+  unsigned char *q_tile = tiles, *slots = tiles + S::NS * S::TILE;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   id /= f.p.tiles;
   const int pack = (int)(id % f.p.packs);
   const long long b = id / f.p.packs;
-  const int P = f.p.P, per = kRows / P, i0 = tile * (WIDE ? 2 : 1) * per;
+  const int P = f.p.P, per = kRows / P, i0 = tile * S::NS * per;
   const int h0 = pack * P, hk = h0 / a.G;
   const Lens n = utt_lens(a, b);
 
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.tail_full, 1);
     mbar_init(&sh.drained, 1);
-    for (int w = 0; w < 2; ++w) {
+    for (int w = 0; w < S::NS; ++w) {
       mbar_init(&sh.s_full[w], 1);
       mbar_init(&sh.p_ready[w], 128);
       mbar_init(&sh.o_full[w], 1);
@@ -125,23 +128,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.first = INT_MAX;
     sh.last = 0;
   }
-  if (warp == 9) tmem_alloc<512>(&sh.tmem);
+  constexpr int kAux = S::NS * 4;  // the first warp past the softmax's
+  if (warp == kAux + 1) tmem_alloc<S::TMEM>(&sh.tmem);
   __syncthreads();
   // the row of this thread (softmax warps), and the hull of all rows' frames
   const int stream = warp >> 2, r = threadIdx.x & 127;
   int row = 0, head = 0;
   int2 range = make_int2(0, 0);
-  if (warp < 8) {
-    row = i0 + (WIDE ? stream * per : 0) + r / P;
+  if (warp < kAux) {
+    row = i0 + stream * per + r / P;
     head = h0 + r % P;
     range = row_range(a, b, row, n);
-    if (WIDE || stream == 0) {
-      const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
-      const int hi = __reduce_max_sync(0xffffffffu, range.y);
-      if (lane == 0 && hi > 0) {
-        atomicMin(&sh.first, lo);
-        atomicMax(&sh.last, hi);
-      }
+    const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, range.y);
+    if (lane == 0 && hi > 0) {
+      atomicMin(&sh.first, lo);
+      atomicMax(&sh.last, hi);
     }
   }
   tc_fence_before();
@@ -153,25 +155,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
   const int t0 = (int)((long long)all * split / f.p.splits),
             t1 = (int)((long long)all * (split + 1) / f.p.splits), T = t1 - t0;
-  // tiles of a stream: wide 0, 1, ...; thin w, w + 2, ...
-  const int steps0 = WIDE ? T : (T + 1) / 2, steps1 = WIDE ? T : T / 2;
-  auto frame_of = [&](int t) { return first + t * kRows; };
-  auto frame = [&](int w, int s) { return frame_of(t0 + (WIDE ? s : 2 * s + w)); };
+  auto frame = [&](int s) { return first + (t0 + s) * kRows; };
   const float c = a.scale * kLog2e;
 
   // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
   // v, which is the last tile loaded, a warp of its own zeroes them (unless TMA did, past the
   // tensor's end): the load then arrives at tail_full, and that warp hands the tile on.
-  const bool cut = T > 0 && n.nk < a.Lk && frame_of(t1 - 1) + kRows > n.nk;
+  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
-  if (warp >= 8) {
-    warpgroup_give_registers<kOtherRegs>();  // to the softmax warps, which hold a row of scores
-    if (warp == 8 && lane == 0 && T > 0) {
+  if (warp >= kAux) {
+    warpgroup_give_registers<S::OTHER_REGS>();  // to the softmax warps, which hold a row of scores
+    if (warp == kAux && lane == 0 && T > 0) {
       tma_prefetch_map(&qm);
       tma_prefetch_map(&km);
       tma_prefetch_map(&vm);
-      arrive_expect_tx(&sh.q_full, S::NQ * S::TILE);
-      for (int t = 0; t < S::NQ; ++t)
+      arrive_expect_tx(&sh.q_full, S::NS * S::TILE);
+      for (int t = 0; t < S::NS; ++t)
         for (int ch = 0; ch < S::CHUNKS; ++ch)
           tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
                       i0 + t * per, (int)b * f.q_b);
@@ -188,25 +187,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++at;
         return true;
       };
-      bool ok = load(false, frame(0, 0));
-      if (!WIDE && steps1 > 0) ok = ok && load(false, frame(1, 0));
-      for (int s = 0; ok && s < steps0; ++s)
-        for (int w = 0; ok && w < (WIDE ? 1 : 2); ++w) {
-          const int steps = w ? steps1 : steps0;
-          if (s < steps) ok = load(true, frame(w, s));
-          if (s + 1 < steps) ok = ok && load(false, frame(w, s + 1));
-        }
+      bool ok = load(false, frame(0));
+      for (int s = 0; ok && s < T; ++s) {
+        ok = load(true, frame(s));
+        if (s + 1 < T) ok = ok && load(false, frame(s + 1));
+      }
       if (!ok)  // copies in flight land before the CTA ends
         for (int i = max(0, at - S::SLOTS); i < at; ++i)
           Waiter::drain(&sh.full[i % S::SLOTS], (unsigned)(i / S::SLOTS) & 1);
     }
-    if (warp == 10 && cut) {
+    if (warp == kAux + 2 && cut) {
       const int slot = (2 * T - 1) % S::SLOTS;
       if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
-        zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame_of(t1 - 1), kRows);
+        zero_tail(slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame(T - 1), kRows);
       if (lane == 0) mbar_arrive(&sh.full[slot]);
     }
-    if (warp == 9 && T > 0 && elect_one()) {
+    if (warp == kAux + 1 && T > 0 && elect_one()) {
       constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_o = mma_desc<DT>(DP, true);
       const unsigned q_addr = smem_u32(q_tile), s_addr = smem_u32(slots);
       bool ok = wait(&sh.q_full, 0);
@@ -217,55 +213,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (!ok) return;
         const int slot = at % S::SLOTS;
-        mma_rows<DP>(tmem + w * kRows, q_addr + (WIDE ? w : 0) * S::TILE, S::CHUNK,
+        mma_rows<DP>(tmem + w * kRows, q_addr + w * S::TILE, S::CHUNK,
                      s_addr + slot * S::TILE, S::CHUNK, i_s, false);
         mma_commit(&sh.s_full[w]);
-        if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
+        if (w == S::NS - 1) mma_commit(&sh.empty[slot]);
       };
       auto values = [&](int w, int s, int at) {  // O_w += P_w V
         const int slot = at % S::SLOTS;
         ok = ok && wait(&sh.p_ready[w], s & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_across<kRows>(tmem + 2 * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
+        mma_across<kRows>(tmem + S::NS * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
                           S::CHUNK, i_o, s > 0);
-        if (!WIDE || w == 1) mma_commit(&sh.empty[slot]);
-        if (s + 1 == (w ? steps1 : steps0)) mma_commit(&sh.o_full[w]);
+        if (w == S::NS - 1) mma_commit(&sh.empty[slot]);
+        if (s + 1 == T) mma_commit(&sh.o_full[w]);
       };
       loaded(0);
-      if (WIDE) {
-        scores(0, 0);
-        scores(1, 0);
-        for (int s = 0; ok && s < T; ++s) {
-          const int at = 1 + 2 * s;
-          loaded(at);
-          values(0, s, at);
+      for (int w = 0; w < S::NS; ++w) scores(w, 0);
+      for (int s = 0; ok && s < T; ++s) {
+        const int at = 1 + 2 * s;
+        loaded(at);
+#pragma unroll
+        for (int w = 0; w < S::NS; ++w) {
+          values(w, s, at);
           if (s + 1 < T) {
-            loaded(at + 1);
-            scores(0, at + 1);
+            if (w == 0) loaded(at + 1);
+            scores(w, at + 1);
           }
-          values(1, s, at);
-          if (s + 1 < T) scores(1, at + 1);
         }
-      } else {
-        int at = 0;
-        scores(0, at++);
-        if (steps1 > 0) {
-          loaded(at);
-          scores(1, at++);
-        }
-        for (int s = 0; ok && s < steps0; ++s)
-          for (int w = 0; w < 2; ++w) {
-            const int steps = w ? steps1 : steps0;
-            if (s < steps) {
-              loaded(at);
-              values(w, s, at++);
-            }
-            if (s + 1 < steps) {
-              loaded(at);
-              scores(w, at++);
-            }
-          }
       }
       if (!ok) {  // products in flight end before TMEM is freed
         mma_commit(&sh.drained);
@@ -273,13 +248,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    warpgroup_take_registers<kSoftmaxRegs>();
-    const int steps = stream ? steps1 : steps0;
+    warpgroup_take_registers<S::SOFTMAX_REGS>();
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
-    const unsigned s_col = tmem + lanes + stream * kRows, o_col = tmem + lanes + 2 * kRows + stream * DP;
+    const unsigned s_col = tmem + lanes + stream * kRows, o_col = tmem + lanes + S::NS * kRows + stream * DP;
     float ref = -INFINITY, l = 0.0f;  // reference maximum (base 2) and sum
     bool ok = true;
-    for (int s = 0; s < steps; ++s) {
+    for (int s = 0; s < T; ++s) {
       ok = wait(&sh.s_full[stream], s & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -287,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, x[i]);
       tmem_wait_ld();
-      const int j0 = frame(stream, s);
+      const int j0 = frame(s);
       if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + kRows)) {
         const int lo = range.x - j0;
         const unsigned len = (unsigned)(range.y - range.x);
@@ -337,94 +311,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       mbar_arrive(&sh.p_ready[stream]);
     }
-    if (steps > 0 && ok) ok = wait(&sh.o_full[stream], 0);
+    if (T > 0 && ok) ok = wait(&sh.o_full[stream], 0);
     __syncwarp();
     tc_fence_after();
-    float f_other = 0.0f, f_own = 1.0f;
-    if (!WIDE) {
-      // join the streams: stream 1 hands over its reference, sum and output (in the tiles' memory:
-      // every product is done, so nothing reads or writes them)
-      float *join_o = reinterpret_cast<float *>(tiles);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (stream == 1) {
-        sh.join_m[r] = ref;
-        sh.join_l[r] = l;
-        if (steps > 0) {
-          unsigned o[32];
-#pragma unroll
-          for (int i = 0; i < DP / 32; ++i) {
-            tmem_ld32(o_col + i * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) join_o[(i * 32 + k) * kRows + r] = __uint_as_float(o[k]);
-          }
-        }
-      }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (stream == 0 && steps1 > 0) {
-        const float m1 = sh.join_m[r], top = fmaxf(ref, m1);
-        if (top > -INFINITY) {
-          f_own = fast_exp2(ref - top);
-          f_other = fast_exp2(m1 - top);
-          l = l * f_own + sh.join_l[r] * f_other;
-          ref = top;
-        }
-      }
-    }
-    __syncwarp();
-    const bool mine = WIDE || stream == 0;
     const bool bad = n.bad || !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
-    if (mine && row < a.Lq) {
+    const long long part = ((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NS * kRows) +
+                           threadIdx.x;
+    if (row < a.Lq) {
       const float total = bad ? NAN : l == 0.0f ? -INFINITY : ref + log2f(l);
       if (f.p.splits > 1)
-        f.part_l[((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NQ * kRows) +
-                 (WIDE ? stream * kRows : 0) + r] = total;
+        f.part_l[part] = total;
       else if (a.lse)
         a.lse[(b * a.H + head) * a.Lq + row] = total * kLn2;
     }
-    if (mine) {
-      const float inv = bad ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
-      const float *join_o = reinterpret_cast<const float *>(tiles);
-      const bool both = !WIDE && steps1 > 0;
+    const float inv = bad ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-      for (int i = 0; i < DP / 32; ++i) {
-        unsigned o[32];
-        if (steps > 0) {
-          tmem_ld32(o_col + i * 32, o);
-          tmem_wait_ld();
-        }
-        float v[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          float x = steps > 0 ? __uint_as_float(o[k]) * f_own : 0.0f;
-          if (both) x += join_o[(i * 32 + k) * kRows + r] * f_other;
-          v[k] = l == 0.0f && !bad ? 0.0f : x * inv;
-        }
-        if (row >= a.Lq) {
-        } else if (f.p.splits > 1) {
-          float4 *dst = reinterpret_cast<float4 *>(
-              f.part_o + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NQ * kRows) +
-                          (WIDE ? stream * kRows : 0) + r) * DP + i * 32);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-        } else {
-          unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
-                                row * a.so.l + head * a.so.h + i * 32;
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (i * 32 + k * 8 < a.D)
-              reinterpret_cast<uint4 *>(dst)[k] = make_uint4(
-                  pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
-                  pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
-        }
-        __syncwarp();
+    for (int i = 0; i < DP / 32; ++i) {
+      unsigned o[32];
+      if (T > 0) {
+        tmem_ld32(o_col + i * 32, o);
+        tmem_wait_ld();
       }
+      float v[32];
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        v[k] = bad ? NAN : l == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
+      if (row >= a.Lq) {
+      } else if (f.p.splits > 1) {
+        float4 *dst = reinterpret_cast<float4 *>(f.part_o + part * DP + i * 32);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+      } else {
+        unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
+                              row * a.so.l + head * a.so.h + i * 32;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i * 32 + k * 8 < a.D)
+            reinterpret_cast<uint4 *>(dst)[k] = make_uint4(
+                pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
+                pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
+      }
+      __syncwarp();
     }
     tc_fence_before();
   }
   __syncthreads();
-  if (warp == 9) tmem_free<512>(tmem);
+  if (warp == kAux + 1) tmem_free<S::TMEM>(tmem);
 }
 
 // Joins the splits of a row: o = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).  DP / 4 threads a
@@ -482,10 +415,10 @@ FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
   p.wide = rows > kRows;
   const int tile_rows = p.wide ? 2 * kRows : kRows;
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-  // split the frames while the CTAs leave SMs idle and every split keeps two tiles a stream
+  // split the frames while the CTAs leave SMs idle and every split keeps four tiles
   const long long ctas = B * p.packs * p.tiles, steps = (Lk + kRows - 1) / kRows;
-  long long s = ctas > 0 ? kSMs / ctas : 1;
-  const long long most = steps / (p.wide ? 2 : 4);
+  long long s = ctas > 0 ? (p.wide ? 1 : 2) * kSMs / ctas : 1;
+  const long long most = steps / 4;
   if (s > most) s = most;
   if (s > 64) s = 64;
   p.splits = s < 1 ? 1 : (int)s;
@@ -500,14 +433,14 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
   typedef FwdShape<DP, WIDE> S;
   const size_t smem = S::BYTES + 1024;
   cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_fwd_tc_kernel<DT, DP, WIDE>),
-                                    smem, kLaunchRegs);
+                                    smem, S::REGS);
   if (e != cudaSuccess) return e;
   const long long ctas = f.a.B * f.p.packs * f.p.tiles;
   attn_fwd_tc_kernel<DT, DP, WIDE>
-      <<<(unsigned)(ctas * f.p.splits), kThreads, smem, stream>>>(q.map, k.map, v.map, f);
+      <<<(unsigned)(ctas * f.p.splits), S::THREADS, smem, stream>>>(q.map, k.map, v.map, f);
   e = cudaGetLastError();
   if (e != cudaSuccess || f.p.splits == 1) return e;
-  const int rows = S::NQ * kRows;
+  const int rows = S::NS * kRows;
   const long long threads = ctas * rows * (DP / 4);
   attn_join_kernel<DT, DP><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(f, rows);
   return cudaGetLastError();

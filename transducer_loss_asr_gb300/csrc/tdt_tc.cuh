@@ -152,9 +152,10 @@ __device__ __forceinline__ unsigned long long desc_mn_major(unsigned addr, unsig
          ((unsigned long long)(chunk_bytes >> 4) << 16) | (64ull << 32);
 }
 // Instruction descriptor of kind::f16 with float32 accumulators, M = 128.
-template <int DT> __device__ __forceinline__ constexpr unsigned mma_desc(int N, bool b_mn_major) {
+template <int DT>
+__device__ __forceinline__ constexpr unsigned mma_desc(int N, bool b_mn_major, bool a_mn_major = false) {
   return (1u << 4) | ((DT == kBF16 ? 1u : 0u) << 7) | ((DT == kBF16 ? 1u : 0u) << 10) |
-         ((b_mn_major ? 1u : 0u) << 16) | ((unsigned)(N >> 3) << 17) | ((128u >> 4) << 24);
+         ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((unsigned)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 // d (+)= a b, both operands in shared memory.  One thread issues; K = 16.
 __device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b,
