@@ -299,7 +299,7 @@ def _rows(x):
 def _like(x, t, name):
     """(t, strides): checked to be an output of x's shape and dtype, or a new contiguous one."""
     if t is None:
-        t = x.new_empty(x.shape)
+        t = torch.empty(x.shape, dtype=x.dtype, device=x.device)
         return t, t.stride()
     st = t.stride()
     if t.shape != x.shape or t.dtype != x.dtype or t.device != x.device or (

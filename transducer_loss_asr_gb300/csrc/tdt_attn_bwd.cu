@@ -21,8 +21,6 @@
 // Scores of the next tile are formed while the threads are at this one's dS.
 //
 // Few CTAs: the walk is split over several, whose float32 sums a third kernel adds in order.
-#include <climits>
-
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -118,7 +116,8 @@ struct DqShared {
   Pipe k, v;
   unsigned long long rows_full, scores, ds_ready, done, tail_full, drained;
   unsigned tmem;
-  int gave_up, first, last;
+  int gave_up;
+  Hull hull;
   float half[kRows];
 };
 
@@ -136,17 +135,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *v_slots = k_slots + S::KS * S::TILE;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  long long id = blockIdx.x;
-  const int split = (int)(id % f.p.dq_splits);
+  unsigned id = blockIdx.x;
+  const int split = id % f.p.dq_splits;
   id /= f.p.dq_splits;
-  const long long cta = id;
-  const int tile = (int)(id % f.p.tiles);
+  const unsigned cta = id;
+  const int tile = id % f.p.tiles;
   id /= f.p.tiles;
-  const int pack = (int)(id % f.p.packs);
+  const int pack = id % f.p.packs;
   const long long b = id / f.p.packs;
   const int P = f.p.P, per = kRows / P, i0 = tile * per, h0 = pack * P, hk = h0 / a.G;
   const Lens n = utt_lens(a, b);
-  if (threadIdx.x == 0) {
+  const bool some = i0 < n.nq && n.nk > 0;  // else no row sees a frame
+  const int group = warp >> 2, r = threadIdx.x & 127;
+  const int row = i0 + r / P, head = h0 + r % P;
+  int2 range = make_int2(0, 0);
+  if (warp < 8) {
+    range = row_range(a, b, row, n);
+    if (a.windows) hull_note(sh.hull, warp, range);
+  } else if (warp == 8 && lane == 0) {
     pipe_init(sh.k, S::KS);
     pipe_init(sh.v, S::VS);
     mbar_init(&sh.rows_full, 1);
@@ -157,33 +163,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
-    sh.first = INT_MAX;
-    sh.last = 0;
-  }
-  if (warp == 9) tmem_alloc<512>(&sh.tmem);
-  __syncthreads();
-  const int group = warp >> 2, r = threadIdx.x & 127;
-  const int row = i0 + r / P, head = h0 + r % P;
-  int2 range = make_int2(0, 0);
-  if (warp < 8) {
-    range = row_range(a, b, row, n);
-    if (group == 0) {
-      const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
-      const int hi = __reduce_max_sync(0xffffffffu, range.y);
-      if (lane == 0 && hi > 0) {
-        atomicMin(&sh.first, lo);
-        atomicMax(&sh.last, hi);
-      }
+    if (some) {
+      arrive_expect_tx(&sh.rows_full, 2 * S::TILE);
+      load_rows<DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
+      load_rows<DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
     }
+  } else if (warp == 9) {
+    tmem_alloc<512>(&sh.tmem);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
-  const int t0 = (int)((long long)all * split / f.p.dq_splits),
-            t1 = (int)((long long)all * (split + 1) / f.p.dq_splits), T = t1 - t0;
+  const int2 hull = a.windows ? hull_of<8>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
+  const int first = hull.x;
+  const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.dq_splits);
+  const int t0 = steps.x, T = steps.y - steps.x;
   auto frame = [&](int s) { return first + (t0 + s) * kRows; };
   constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ
   // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
@@ -193,10 +189,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
+    if (warp == 8 && lane == 0 && some && T == 0) wait(&sh.rows_full, 0);  // nobody else does
     if (warp == 8 && lane == 0 && T > 0) {
-      arrive_expect_tx(&sh.rows_full, 2 * S::TILE);
-      load_rows<DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
-      load_rows<DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
       bool ok = true;
       int s = 0;
       for (; ok && s < T; ++s) {
@@ -272,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     warpgroup_take_registers<kWorkRegs>();
     // delta = dO . O of the row, half of the columns in each group
-    const bool real = row < n.nq;
+    const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta = 0.0f, lse2 = INFINITY;
     {
@@ -312,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j0 = frame(s) + group * 64;
       const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2),
                    d2 = make_float2(-delta, -delta);
-      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64)) {
+      if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
         // frames that the row does not see: s = -inf weighs 0, and dP may be anything
         const int lo = range.x - j0;
         const unsigned len = (unsigned)(range.y - range.x);
@@ -349,7 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       float v[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
+      for (int k = 0; k < 32; ++k)
+        v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * a.scale : 0.0f;
       if (row < a.Lq) {
         if (f.p.dq_splits > 1)
           store32f(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * kRows + r) * DP + d0, v);
@@ -390,46 +385,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *g_slots = q_slots + S::RS * S::TILE;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  long long id = blockIdx.x;
-  const int split = (int)(id % f.p.dkv_splits);
+  unsigned id = blockIdx.x;
+  const int split = id % f.p.dkv_splits;
   id /= f.p.dkv_splits;
-  const long long cta = id;
+  const unsigned cta = id;
   const int j0 = (int)(id % f.p.f_tiles) * kRows;
   id /= f.p.f_tiles;
-  const int hk = (int)(id % a.Hkv);
+  const int hk = id % a.Hkv;
   const long long b = id / a.Hkv;
   const int P = f.p.P, per = kRows / P;
   const Lens n = utt_lens(a, b);
   // the walk: packs of the group x row tiles with queries, skipping those that see none of these
   // frames; this CTA takes the steps [t0, t1) of it
   const int row_tiles = j0 < n.nk ? (n.nq + per - 1) / per : 0;
-  const int all = (a.G / P) * row_tiles;
-  const int t0 = (int)((long long)all * split / f.p.dkv_splits),
-            t1 = (int)((long long)all * (split + 1) / f.p.dkv_splits);
-  if (threadIdx.x == 0) {
-    pipe_init(sh.q, S::RS);
-    pipe_init(sh.g, S::RS);
-    mbar_init(&sh.frames_full, 1);
-    mbar_init(&sh.s_full, 1);
-    mbar_init(&sh.p_ready, 256);
-    mbar_init(&sh.dp_full, 1);
-    mbar_init(&sh.ds_ready, 256);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.stat_full[i], 32);
-      mbar_init(&sh.stat_empty[i], 256);
+  const int2 steps = share_of((a.G / P) * row_tiles, split, f.p.dkv_splits);
+  const int t0 = steps.x, t1 = steps.y;
+  if (warp == 8) {
+    if (lane == 0) {
+      pipe_init(sh.q, S::RS);
+      pipe_init(sh.g, S::RS);
+      mbar_init(&sh.frames_full, 1);
+      mbar_init(&sh.s_full, 1);
+      mbar_init(&sh.p_ready, 256);
+      mbar_init(&sh.dp_full, 1);
+      mbar_init(&sh.ds_ready, 256);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.stat_full[i], 32);
+        mbar_init(&sh.stat_empty[i], 256);
+        mbar_init(&sh.q_tail[i], 1);
+        mbar_init(&sh.g_tail[i], 1);
+      }
+      mbar_init(&sh.done, 1);
+      mbar_init(&sh.drained, 1);
+      fence_mbar_init_cluster();
+      sh.gave_up = 0;
+      if (t1 > t0) {
+        arrive_expect_tx(&sh.frames_full, 2 * S::TILE);
+        load_rows<DP>(&km, k_tile, &sh.frames_full, hk * f.k_h, j0, (int)b * f.k_b);
+        load_rows<DP>(&vm, v_tile, &sh.frames_full, hk * f.v_h, j0, (int)b * f.v_b);
+      }
     }
-    mbar_init(&sh.done, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_tail[i], 1);
-      mbar_init(&sh.g_tail[i], 1);
-    }
-    mbar_init(&sh.drained, 1);
-    fence_mbar_init_cluster();
-    sh.gave_up = 0;
-  }
-  if (warp == 9) tmem_alloc<512>(&sh.tmem);
-  if (a.windows)
-    for (int t = warp; t < min(row_tiles, kTileBits); t += kThreads / 32) {
+  } else if (warp == 9) {
+    tmem_alloc<512>(&sh.tmem);
+  } else if (a.windows) {  // ten warps
+    for (int t = warp < 8 ? warp : warp - 2; t < min(row_tiles, kTileBits); t += 10) {
       bool sees = false;
       for (int i = t * per + lane; i < min((t + 1) * per, n.nq); i += 32) {
         const int2 w = row_range(a, b, i, n);
@@ -438,6 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       sees = __any_sync(0xffffffffu, sees);
       if (lane == 0) sh.active[t] = sees;
     }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -461,10 +461,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
+    if (warp == 8 && lane == 0 && t1 > t0 && !any) wait(&sh.frames_full, 0);  // nobody else does
     if (warp == 8 && lane == 0 && any) {
-      arrive_expect_tx(&sh.frames_full, 2 * S::TILE);
-      load_rows<DP>(&km, k_tile, &sh.frames_full, hk * f.k_h, j0, (int)b * f.k_b);
-      load_rows<DP>(&vm, v_tile, &sh.frames_full, hk * f.v_h, j0, (int)b * f.v_b);
       bool ok = true;
       int s = 0;
       for (int t = start; ok && t < t1; t = next(t + 1), ++s) {
@@ -716,7 +714,8 @@ struct OneShared {
   unsigned long long rows_in, rows_full, sp_full, pds_ready, pds_free, dkv_full, dkv_free, done, tail_full,
       drained;
   unsigned tmem;
-  int gave_up, first, last;
+  int gave_up;
+  Hull hull;
   float half[kRows];
 };
 
@@ -736,13 +735,22 @@ __global__ void __launch_bounds__(kOneThreads, 1)
                 *ds_tile = p_tile + S::PDS;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int split = (int)(blockIdx.x % f.p.dq_splits);
-  const long long cta = blockIdx.x / f.p.dq_splits;  // = b * Hkv + hk
-  const int hk = (int)(cta % a.Hkv), h0 = hk * a.G;
+  const int split = blockIdx.x % f.p.dq_splits;
+  const unsigned cta = blockIdx.x / f.p.dq_splits;  // = b * Hkv + hk
+  const int hk = cta % a.Hkv, h0 = hk * a.G;
   const long long b = cta / a.Hkv;
   const int P = f.p.P, per = kRows / P;
   const Lens n = utt_lens(a, b);
-  if (threadIdx.x == 0) {
+  const int group = warp >> 2, r = threadIdx.x & 127, row = r / P, head = h0 + r % P;
+  int2 range = make_int2(0, 0);
+  // Rows and frames past the utterance's ends may hold anything, and 0 times NaN is NaN: a warp of its own
+  // zeroes them in the tiles of q and dO and in the last tile of k before handing these on (unless TMA
+  // did, past the tensor's ends).
+  const bool some = n.nq > 0 && n.nk > 0, cut_rows = n.nq < a.Lq;
+  if (group < 2) {
+    range = row_range(a, b, row, n);
+    if (a.windows) hull_note(sh.hull, warp, range);
+  } else if (warp == 12 && lane == 0) {
     pipe_init(sh.k, S::KV);
     pipe_init(sh.v, S::KV);
     mbar_init(&sh.rows_in, 1);
@@ -757,46 +765,35 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
-    sh.first = INT_MAX;
-    sh.last = 0;
-  }
-  if (warp == 13) tmem_alloc<512>(&sh.tmem);
-  __syncthreads();
-  const int group = warp >> 2, r = threadIdx.x & 127, row = r / P, head = h0 + r % P;
-  int2 range = make_int2(0, 0);
-  if (group < 2) {
-    range = row_range(a, b, row, n);
-    const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, range.y);
-    if (group == 0 && lane == 0 && hi > 0) {
-      atomicMin(&sh.first, lo);
-      atomicMax(&sh.last, hi);
+    if (some) {
+      unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
+      arrive_expect_tx(rows, 2 * S::TILE);
+      tma_load_4d(&qm, q_tile, rows, 0, h0 * f.q_h, 0, (int)b * f.q_b);
+      tma_load_4d(&gm, g_tile, rows, 0, h0 * f.go_h, 0, (int)b * f.go_b);
     }
+  } else if (warp == 13) {
+    tmem_alloc<512>(&sh.tmem);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
+  const int2 hull = a.windows ? hull_of<8>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
   // this CTA's frame tiles [t0, t1); those that a row sees are [ta, tb)
-  const int t0 = (int)((long long)f.p.f_tiles * split / f.p.dq_splits),
-            t1 = (int)((long long)f.p.f_tiles * (split + 1) / f.p.dq_splits);
-  const int ta = sh.last > sh.first ? max(t0, sh.first / kRows) : t1,
-            tb = min(t1, (sh.last + kRows - 1) / kRows), T = max(0, tb - ta);
+  const int2 mine = share_of(f.p.f_tiles, split, f.p.dq_splits);
+  const int t0 = mine.x, t1 = mine.y;
+  const int ta = hull.y > hull.x ? max(t0, hull.x / kRows) : t1, tb = min(t1, (hull.y + kRows - 1) / kRows),
+            T = max(0, tb - ta);
   auto frame = [&](int s) { return (ta + s) * kRows; };
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = kDv + DP, kAcc = kDk + DP;
-  // Rows and frames past the utterance's ends may hold anything, and 0 times NaN is NaN: a warp of its own
-  // zeroes them in the tiles of q and dO and in the last tile of k before handing these on (unless TMA
-  // did, past the tensor's ends).
-  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk, cut_rows = n.nq < a.Lq;
+  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
   if (group == 3) {
     warpgroup_give_registers<kOneOtherRegs>();
+    unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
+    if (warp == 12 && lane == 0 && some && T == 0) wait(rows, 0);  // nobody else does
     if (warp == 12 && lane == 0 && T > 0) {
-      unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
-      arrive_expect_tx(rows, 2 * S::TILE);
-      tma_load_4d(&qm, q_tile, rows, 0, h0 * f.q_h, 0, (int)b * f.q_b);
-      tma_load_4d(&gm, g_tile, rows, 0, h0 * f.go_h, 0, (int)b * f.go_b);
       bool ok = true;
       int s = 0;
       for (; ok && s < T; ++s) {
@@ -913,7 +910,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          v[k] = ok ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : NAN;
+          v[k] = !ok ? NAN : j < n.nk ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : 0.0f;
         if (j < a.Lk) store32<DT>(out, at, v, (i & 1) * 32, a.D);
         __syncwarp();
       }
@@ -921,7 +918,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     tc_fence_before();
   } else {
     warpgroup_take_registers<kOneWorkRegs>();
-    const bool real = row < n.nq;
+    const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta, lse2 = -INFINITY;  // both negated
     {
@@ -957,7 +954,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       tmem_ld32(d_col + 32, y[1]);
       tmem_wait_ld();
       const int j0 = frame(s) + group * 64;
-      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + 64)) {
+      if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
         // frames that the row does not see: s = -inf weighs 0, and dP may be anything
         const int lo = range.x - j0;
         const unsigned len = (unsigned)(range.y - range.x);
@@ -1005,7 +1002,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
     if (row < a.Lq) {
       if (f.p.dq_splits > 1)
-        store32f(f.part + ((split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
+        store32f(f.part + (((long long)split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
       else
         store32<DT>(a.dq, b * a.sdq.b + row * a.sdq.l + head * a.sdq.h, v, group * 32, a.D);
     }

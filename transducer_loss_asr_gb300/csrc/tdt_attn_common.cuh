@@ -56,6 +56,37 @@ __device__ __forceinline__ int2 row_range(const AttnArgs &a, long long b, int i,
   return hi > lo ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
+// Steps [first, last) of `all` that part `i` of `parts` takes.
+__device__ __forceinline__ int2 share_of(int all, int i, int parts) {
+  if (parts == 1) return make_int2(0, all);
+  const int q = all / parts, more = all % parts;
+  const int first = q * i + min(i, more);
+  return make_int2(first, first + q + (i < more ? 1 : 0));
+}
+
+// The hull of the frame ranges of a CTA's rows.  Warps with rows note theirs; after a barrier every
+// thread reads the hull of all.  Without windows it is known beforehand.
+struct Hull {
+  int lo[8], hi[8];
+};
+__device__ __forceinline__ void hull_note(Hull &h, int warp, int2 range) {
+  const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : 0x7fffffff);
+  const int hi = __reduce_max_sync(0xffffffffu, range.y);
+  if ((threadIdx.x & 31) == 0) {
+    h.lo[warp] = lo;
+    h.hi[warp] = hi;
+  }
+}
+template <int WARPS> __device__ __forceinline__ int2 hull_of(const Hull &h) {
+  int lo = h.lo[0], hi = h.hi[0];
+#pragma unroll
+  for (int i = 1; i < WARPS; ++i) {
+    lo = min(lo, h.lo[i]);
+    hi = max(hi, h.hi[i]);
+  }
+  return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
+}
+
 // Tensor-core kernels: which calls they take, their workspace (of the sizes alone), and the launch.
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);

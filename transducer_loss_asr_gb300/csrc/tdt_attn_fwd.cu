@@ -20,8 +20,6 @@
 //
 // Few row tiles: the frames are split over several CTAs, whose results (O, and the logarithm of
 // the sum) a second kernel joins in a fixed order.
-#include <climits>
-
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -68,7 +66,8 @@ template <int DP, bool WIDE> struct FwdShape {
 struct FwdShared {
   unsigned long long full[8], empty[8], q_full, s_full[2], p_ready[2], o_full[2], tail_full, drained;
   unsigned tmem;
-  int gave_up, first, last;
+  int gave_up;
+  Hull hull;
 };
 
 // 32 scores of a row (float32 bits) to weights 2^(s c - ref), packed in pairs and added to sum.
@@ -98,19 +97,29 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   // this CTA's rows and frames
-  long long id = blockIdx.x;
-  const int split = (int)(id % f.p.splits);
+  unsigned id = blockIdx.x;
+  const int split = id % f.p.splits;
   id /= f.p.splits;
-  const long long cta = id;
-  const int tile = (int)(id % f.p.tiles);
+  const unsigned cta = id;
+  const int tile = id % f.p.tiles;
   id /= f.p.tiles;
-  const int pack = (int)(id % f.p.packs);
+  const int pack = id % f.p.packs;
   const long long b = id / f.p.packs;
   const int P = f.p.P, per = kRows / P, i0 = tile * S::NS * per;
   const int h0 = pack * P, hk = h0 / a.G;
   const Lens n = utt_lens(a, b);
+  const bool some = i0 < n.nq && n.nk > 0;  // else no row sees a frame
 
-  if (threadIdx.x == 0) {
+  constexpr int kAux = S::NS * 4;  // the first warp past the softmax's: TMA
+  const int stream = warp >> 2, r = threadIdx.x & 127;
+  int row = 0, head = 0;
+  int2 range = make_int2(0, 0);
+  if (warp < kAux) {
+    row = i0 + stream * per + r / P;
+    head = h0 + r % P;
+    range = row_range(a, b, row, n);
+    if (a.windows) hull_note(sh.hull, warp, range);
+  } else if (warp == kAux && lane == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
@@ -125,36 +134,26 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     }
     fence_mbar_init_cluster();
     sh.gave_up = 0;
-    sh.first = INT_MAX;
-    sh.last = 0;
-  }
-  constexpr int kAux = S::NS * 4;  // the first warp past the softmax's
-  if (warp == kAux + 1) tmem_alloc<S::TMEM>(&sh.tmem);
-  __syncthreads();
-  // the row of this thread (softmax warps), and the hull of all rows' frames
-  const int stream = warp >> 2, r = threadIdx.x & 127;
-  int row = 0, head = 0;
-  int2 range = make_int2(0, 0);
-  if (warp < kAux) {
-    row = i0 + stream * per + r / P;
-    head = h0 + r % P;
-    range = row_range(a, b, row, n);
-    const int lo = __reduce_min_sync(0xffffffffu, range.y > range.x ? range.x : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, range.y);
-    if (lane == 0 && hi > 0) {
-      atomicMin(&sh.first, lo);
-      atomicMax(&sh.last, hi);
+    if (some) {
+      arrive_expect_tx(&sh.q_full, S::NS * S::TILE);
+      for (int t = 0; t < S::NS; ++t)
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
+                      i0 + t * per, (int)b * f.q_b);
     }
+  } else if (warp == kAux + 1) {
+    tmem_alloc<S::TMEM>(&sh.tmem);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  // frames [first, last) in tiles of 128 from `first`; this CTA takes tiles [t0, t1)
-  const int first = sh.first, all = sh.last > first ? (sh.last - first + kRows - 1) / kRows : 0;
-  const int t0 = (int)((long long)all * split / f.p.splits),
-            t1 = (int)((long long)all * (split + 1) / f.p.splits), T = t1 - t0;
+  // frames [hull.x, hull.y) in tiles of 128 from hull.x; this CTA takes tiles [t0, t0 + T)
+  const int2 hull = a.windows ? hull_of<kAux>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
+  const int first = hull.x;
+  const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.splits);
+  const int t0 = steps.x, T = steps.y - steps.x;
   auto frame = [&](int s) { return first + (t0 + s) * kRows; };
   const float c = a.scale * kLog2e;
 
@@ -165,15 +164,8 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
 
   if (warp >= kAux) {
     warpgroup_give_registers<S::OTHER_REGS>();  // to the softmax warps, which hold a row of scores
+    if (warp == kAux && lane == 0 && some && T == 0) wait(&sh.q_full, 0);  // nobody else does
     if (warp == kAux && lane == 0 && T > 0) {
-      tma_prefetch_map(&qm);
-      tma_prefetch_map(&km);
-      tma_prefetch_map(&vm);
-      arrive_expect_tx(&sh.q_full, S::NS * S::TILE);
-      for (int t = 0; t < S::NS; ++t)
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
-                      i0 + t * per, (int)b * f.q_b);
       int at = 0;
       auto load = [&](bool values, int j0) {
         const int slot = at % S::SLOTS;
@@ -252,6 +244,8 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
     const unsigned s_col = tmem + lanes + stream * kRows, o_col = tmem + lanes + S::NS * kRows + stream * DP;
     float ref = -INFINITY, l = 0.0f;  // reference maximum (base 2) and sum
+    // a row that sees nothing holds whatever its tile does: its result is set at the end
+    const bool alive = range.y > range.x;
     bool ok = true;
     for (int s = 0; s < T; ++s) {
       ok = wait(&sh.s_full[stream], s & 1);
@@ -262,7 +256,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
       for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, x[i]);
       tmem_wait_ld();
       const int j0 = frame(s);
-      if (__any_sync(0xffffffffu, range.x > j0 || range.y < j0 + kRows)) {
+      if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + kRows))) {
         const int lo = range.x - j0;
         const unsigned len = (unsigned)(range.y - range.x);
 #pragma unroll
@@ -278,7 +272,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
         m1 = max3(m1, __uint_as_float(x[3][i]), __uint_as_float(x[3][i + 1]));
       }
       const float top = fmaxf(m0, m1) * c;
-      const bool grow = top > ref + (kLazy + kShift<DT>);  // from -inf: any score
+      const bool grow = alive && top > ref + (kLazy + kShift<DT>);  // from -inf: any score
       if (__any_sync(0xffffffffu, grow)) {
         const float now = grow ? top - kShift<DT> : ref;
         const float scale = grow ? fast_exp2(ref - now) : 1.0f;
@@ -314,6 +308,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     if (T > 0 && ok) ok = wait(&sh.o_full[stream], 0);
     __syncwarp();
     tc_fence_after();
+    if (!alive) l = 0.0f;
     const bool bad = n.bad || !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
     const long long part = ((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NS * kRows) +
                            threadIdx.x;
