@@ -47,7 +47,7 @@ struct BwdPlan {
 struct BwdArgs {
   AttnArgs a;
   BwdPlan p;
-  int q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h;  // 0 for repeated axes
+  int q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h, dq_b, dq_h, dk_b, dk_h, dv_b, dv_h;  // 0 for repeated axes
   float *part;                  // splits > 1: [split][CTA][128][DP], dk's after dv's
 };
 
@@ -79,17 +79,7 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *d
     tma_load_4d(m, dst + c * BwdShape<DP>::CHUNK, bar, c * 64, h, l, b);
 }
 
-// Stores 32 columns of a row as 16-bit elements.
-template <int DT>
-__device__ __forceinline__ void store32(void *out, long long at, const float (&v)[32], int d0, int D) {
-  uint4 *dst = reinterpret_cast<uint4 *>(static_cast<unsigned short *>(out) + at + d0);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (d0 + k * 8 < D)
-      dst[k] = make_uint4(pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
-                          pack2<DT>(v[8 * k + 4], v[8 * k + 5]),
-                          pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
-}
+// 32 columns of a row as float32.
 __device__ __forceinline__ void store32f(float *dst, const float (&v)[32]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k)
@@ -125,7 +115,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
                       const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
-                      const __grid_constant__ BwdArgs f) {
+                      const __grid_constant__ CUtensorMap dqm, const __grid_constant__ BwdArgs f) {
   typedef BwdShape<DP> S;
   typedef typename Elem<DT>::T E;
   extern __shared__ unsigned char raw[];
@@ -330,6 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(&sh.ds_ready);
     }
     if (T > 0 && ok) ok = wait(&sh.done, 0);
+    if (T == 0 && some) ok = wait(&sh.rows_full, 0);  // the tile's memory is used below
     __syncwarp();
     tc_fence_after();
     const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
@@ -345,11 +336,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * a.scale : 0.0f;
-      if (row < a.Lq) {
-        if (f.p.dq_splits > 1)
-          store32f(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * kRows + r) * DP + d0, v);
-        else
-          store32<DT>(a.dq, b * a.sdq.b + row * a.sdq.l + head * a.sdq.h, v, d0, a.D);
+      if (f.p.dq_splits == 1)
+        stage32<DT>(q_tile, S::CHUNK, r, d0, v);  // every product with q is done
+      else if (row < a.Lq)
+        store32f(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * kRows + r) * DP + d0, v);
+      __syncwarp();
+    }
+    if (f.p.dq_splits == 1) {
+      fence_async_shared();
+      named_barrier<256>(1);
+      if (threadIdx.x == 0) {
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_store_4d(&dqm, q_tile + ch * S::CHUNK, ch * 64, h0 * f.dq_h, i0, (int)b * f.dq_b);
+        tma_store_commit();
+        tma_store_wait_read();
       }
       __syncwarp();
     }
@@ -376,6 +376,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_dkv_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
                        const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                       const __grid_constant__ CUtensorMap dkm, const __grid_constant__ CUtensorMap dvm,
                        const __grid_constant__ BwdArgs f) {
   typedef BwdShape<DP> S;
   extern __shared__ unsigned char raw[];
@@ -659,12 +660,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sh.stat_empty[buf]);
       }
     if (any && ok) ok = wait(&sh.done, 0);
+    if (!any && t1 > t0) ok = wait(&sh.frames_full, 0);  // the tiles' memory is used below
     __syncwarp();
     tc_fence_after();
     const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
     // group 0 stores dv, group 1 dk
-    void *out = group ? a.dk : a.dv;
-    const Strides &st = group ? a.sdk : a.sdv;
+    unsigned char *out = group ? k_tile : v_tile;  // every product with them is done
     const float scale = group ? a.scale : kUnshift<DT>;
     const bool keep = j < n.nk;  // frames past the end: their lanes hold no sums
 #pragma unroll
@@ -678,14 +679,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         v[k] = bad ? NAN : any && keep ? __uint_as_float(o[k]) * scale : 0.0f;
-      if (j < a.Lk) {
-        if (f.p.dkv_splits > 1) {
-          const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
-          store32f(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * kRows +
-                             (threadIdx.x & 127)) * DP + i * 32, v);
-        } else {
-          store32<DT>(out, b * st.b + j * st.l + hk * st.h, v, i * 32, a.D);
-        }
+      if (f.p.dkv_splits == 1) {
+        stage32<DT>(out, S::CHUNK, threadIdx.x & 127, i * 32, v);
+      } else if (j < a.Lk) {
+        const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
+        store32f(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * kRows +
+                           (threadIdx.x & 127)) * DP + i * 32, v);
+      }
+      __syncwarp();
+    }
+    if (f.p.dkv_splits == 1) {
+      fence_async_shared();
+      named_barrier<128>(1 + group);
+      if ((threadIdx.x & 127) == 0) {
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_store_4d(group ? &dkm : &dvm, out + ch * S::CHUNK, ch * 64,
+                       hk * (group ? f.dk_h : f.dv_h), j0, (int)b * (group ? f.dk_b : f.dv_b));
+        tma_store_commit();
+        tma_store_wait_read();
       }
       __syncwarp();
     }
@@ -706,7 +717,7 @@ struct OneShape {
   static constexpr int TILE = kRows * 128;            // 64 columns
   static constexpr int KV = 2;                        // slots of k and of v
   static constexpr int PDS = 2 * TILE;                // P or dS: 128 x 128
-  static constexpr int BYTES = (2 + 2 * KV) * TILE + 2 * PDS;
+  static constexpr int BYTES = (2 + 2 * KV + 2) * TILE + 2 * PDS;
 };
 
 struct OneShared {
@@ -723,7 +734,8 @@ template <int DT>
 __global__ void __launch_bounds__(kOneThreads, 1)
     attn_one_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
                        const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
-                       const __grid_constant__ BwdArgs f) {
+                       const __grid_constant__ CUtensorMap dqm, const __grid_constant__ CUtensorMap dkm,
+                       const __grid_constant__ CUtensorMap dvm, const __grid_constant__ BwdArgs f) {
   constexpr int DP = 64;
   typedef OneShape S;
   typedef typename Elem<DT>::T E;
@@ -732,14 +744,14 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   unsigned char *q_tile = tiles, *g_tile = q_tile + S::TILE, *k_slots = g_tile + S::TILE,
                 *v_slots = k_slots + S::KV * S::TILE, *p_tile = v_slots + S::KV * S::TILE,
-                *ds_tile = p_tile + S::PDS;
+                *ds_tile = p_tile + S::PDS, *out_tiles = ds_tile + S::PDS;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = blockIdx.x % f.p.dq_splits;
   const unsigned cta = blockIdx.x / f.p.dq_splits;  // = b * Hkv + hk
   const int hk = cta % a.Hkv, h0 = hk * a.G;
   const long long b = cta / a.Hkv;
-  const int P = f.p.P, per = kRows / P;
+  const int P = f.p.P;
   const Lens n = utt_lens(a, b);
   const int group = warp >> 2, r = threadIdx.x & 127, row = r / P, head = h0 + r % P;
   int2 range = make_int2(0, 0);
@@ -766,10 +778,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     fence_mbar_init_cluster();
     sh.gave_up = 0;
     if (some) {
-      unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
-      arrive_expect_tx(rows, 2 * S::TILE);
-      tma_load_4d(&qm, q_tile, rows, 0, h0 * f.q_h, 0, (int)b * f.q_b);
-      tma_load_4d(&gm, g_tile, rows, 0, h0 * f.go_h, 0, (int)b * f.go_b);
+      unsigned long long *in = cut_rows ? &sh.rows_in : &sh.rows_full;
+      arrive_expect_tx(in, 2 * S::TILE);
+      tma_load_4d(&qm, q_tile, in, 0, h0 * f.q_h, 0, (int)b * f.q_b);
+      tma_load_4d(&gm, g_tile, in, 0, h0 * f.go_h, 0, (int)b * f.go_b);
     }
   } else if (warp == 13) {
     tmem_alloc<512>(&sh.tmem);
@@ -789,9 +801,9 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = kDv + DP, kAcc = kDk + DP;
   const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
+  unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
   if (group == 3) {
     warpgroup_give_registers<kOneOtherRegs>();
-    unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
     if (warp == 12 && lane == 0 && some && T == 0) wait(rows, 0);  // nobody else does
     if (warp == 12 && lane == 0 && T > 0) {
       bool ok = true;
@@ -880,7 +892,6 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   } else if (group == 2) {
     warpgroup_give_registers<kOneStoreRegs>();
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
-    const float zero[32] = {};
     for (int t = t0; t < t1; ++t) {
       const int j = t * kRows + r, s = t - ta;
       const bool sums = t >= ta && t < tb;
@@ -891,30 +902,37 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         __syncwarp();
         tc_fence_after();
       }
+      if (r == 0) tma_store_wait_read();  // the tiles before these have been read
+      named_barrier<128>(2);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {  // 32 columns of dv, dv, dk, dk
-        void *out = i < 2 ? a.dv : a.dk;
-        const Strides &st = i < 2 ? a.sdv : a.sdk;
-        const long long at = b * st.b + j * st.l + hk * st.h;
-        if (!sums) {
-          if (j < a.Lk) store32<DT>(out, at, zero, (i & 1) * 32, a.D);
-          continue;
-        }
         unsigned o[32];
-        tmem_ld32(tmem + lanes + kDv + i * 32, o);
-        tmem_wait_ld();
-        if (i == 3) {
-          tc_fence_before();
-          mbar_arrive(&sh.dkv_free);
+        if (sums) {
+          tmem_ld32(tmem + lanes + kDv + i * 32, o);
+          tmem_wait_ld();
+          if (i == 3) {
+            tc_fence_before();
+            mbar_arrive(&sh.dkv_free);
+          }
         }
         float v[32];
 #pragma unroll
         for (int k = 0; k < 32; ++k)
-          v[k] = !ok ? NAN : j < n.nk ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : 0.0f;
-        if (j < a.Lk) store32<DT>(out, at, v, (i & 1) * 32, a.D);
+          v[k] = !ok ? NAN
+                     : sums && j < n.nk ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : 0.0f;
+        stage32<DT>(out_tiles + (i / 2) * S::TILE, S::TILE, r, (i & 1) * 32, v);
         __syncwarp();
       }
+      fence_async_shared();
+      named_barrier<128>(2);
+      if (r == 0) {
+        tma_store_4d(&dvm, out_tiles, 0, hk * f.dv_h, t * kRows, (int)b * f.dv_b);
+        tma_store_4d(&dkm, out_tiles + S::TILE, 0, hk * f.dk_h, t * kRows, (int)b * f.dk_b);
+        tma_store_commit();
+      }
     }
+    if (r == 0) tma_store_wait_read();
+    __syncwarp();
     tc_fence_before();
   } else {
     warpgroup_take_registers<kOneWorkRegs>();
@@ -989,6 +1007,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       mbar_arrive(&sh.pds_ready);
     }
     if (T > 0 && ok) ok = wait(&sh.done, 0);
+    if (T == 0 && some) ok = wait(rows, 0);  // the tile's memory is used below
     __syncwarp();
     tc_fence_after();
     const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
@@ -1000,11 +1019,17 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     float v[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
-    if (row < a.Lq) {
-      if (f.p.dq_splits > 1)
-        store32f(f.part + (((long long)split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
-      else
-        store32<DT>(a.dq, b * a.sdq.b + row * a.sdq.l + head * a.sdq.h, v, group * 32, a.D);
+    if (f.p.dq_splits == 1) {
+      stage32<DT>(q_tile, S::TILE, r, group * 32, v);  // every product with q is done
+      fence_async_shared();
+      named_barrier<256>(1);
+      if (threadIdx.x == 0) {
+        tma_store_4d(&dqm, q_tile, 0, h0 * f.dq_h, 0, (int)b * f.dq_b);
+        tma_store_commit();
+        tma_store_wait_read();
+      }
+    } else if (row < a.Lq) {
+      store32f(f.part + (((long long)split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
     }
     __syncwarp();
     tc_fence_before();
@@ -1078,7 +1103,7 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Maps {
-  TensorMap q, go, k, v;
+  TensorMap q, go, k, v, dq, dk, dv;
 };
 
 template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
@@ -1087,7 +1112,7 @@ template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaSt
   if (e != cudaSuccess) return e;
   const unsigned ctas = (unsigned)(f.a.B * f.a.Hkv);
   attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, f);
+      m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, m.dk.map, m.dv.map, f);
   if (f.p.dq_splits > 1)
     attn_add_kernel<DT, 64><<<dim3(ctas * (kRows * 16 / 256), 1), 256, 0, stream>>>(f, 0);
   return cudaGetLastError();
@@ -1103,14 +1128,14 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
                                     S::DQ_BYTES + 1024, kLaunchRegs);
   if (e != cudaSuccess) return e;
   attn_dq_tc_kernel<DT, DP><<<(unsigned)(rows * f.p.dq_splits), kThreads, S::DQ_BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, f);
+      m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, f);
   if (f.p.dq_splits > 1)
     attn_add_kernel<DT, DP><<<dim3((unsigned)rows * per_tile, 1), 256, 0, stream>>>(f, 0);
   e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dkv_tc_kernel<DT, DP>),
                         S::DKV_BYTES + 1024, kLaunchRegs);
   if (e != cudaSuccess) return e;
   attn_dkv_tc_kernel<DT, DP><<<(unsigned)(frames * f.p.dkv_splits), kThreads, S::DKV_BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, f);
+      m.q.map, m.go.map, m.k.map, m.v.map, m.dk.map, m.dv.map, f);
   if (f.p.dkv_splits > 1)
     attn_add_kernel<DT, DP><<<dim3((unsigned)frames * per_tile, 2), 256, 0, stream>>>(f, 1);
   return cudaGetLastError();
@@ -1148,7 +1173,10 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   if (!encode_map(&m.q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, per) ||
       !encode_map(&m.go, a.go, dtype, a.B, a.Lq, a.H, a.D, a.sgo.b, a.sgo.l, a.sgo.h, f.p.P, per) ||
       !encode_map(&m.k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
-      !encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows))
+      !encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows) ||
+      !encode_map(&m.dq, a.dq, dtype, a.B, a.Lq, a.H, a.D, a.sdq.b, a.sdq.l, a.sdq.h, f.p.P, per) ||
+      !encode_map(&m.dk, a.dk, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdk.b, a.sdk.l, a.sdk.h, 1, kRows) ||
+      !encode_map(&m.dv, a.dv, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdv.b, a.sdv.l, a.sdv.h, 1, kRows))
     return cudaErrorInvalidValue;
   f.q_b = m.q.b_mul;
   f.q_h = m.q.h_mul;
@@ -1158,6 +1186,12 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.k_h = m.k.h_mul;
   f.v_b = m.v.b_mul;
   f.v_h = m.v.h_mul;
+  f.dq_b = m.dq.b_mul;
+  f.dq_h = m.dq.h_mul;
+  f.dk_b = m.dk.b_mul;
+  f.dk_h = m.dk.h_mul;
+  f.dv_b = m.dv.b_mul;
+  f.dv_h = m.dv.h_mul;
   if (f.p.one) return dtype == kF16 ? launch_one<kF16>(f, m, stream) : launch_one<kBF16>(f, m, stream);
   if (dtype == kF16)
     return a.D <= 64 ? launch<kF16, 64>(f, m, stream) : launch<kF16, 128>(f, m, stream);

@@ -42,7 +42,7 @@ struct FwdPlan {
 struct FwdArgs {
   AttnArgs a;
   FwdPlan p;
-  int q_b, q_h, k_b, k_h, v_b, v_h;  // 0 for repeated axes
+  int q_b, q_h, k_b, k_h, v_b, v_h, o_b, o_h;  // 0 for repeated axes
   float *part_o, *part_l;            // splits > 1: [split][CTA row][DP], [split][CTA row]
 };
 
@@ -87,7 +87,8 @@ __device__ __forceinline__ void exp_pack(const unsigned (&s)[32], float c, float
 template <int DT, int DP, bool WIDE>
 __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE>::CTAS)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
-                       const __grid_constant__ CUtensorMap vm, const __grid_constant__ FwdArgs f) {
+                       const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om,
+                       const __grid_constant__ FwdArgs f) {
   typedef FwdShape<DP, WIDE> S;
   extern __shared__ unsigned char raw[];
   __shared__ FwdShared sh;
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
       mbar_arrive(&sh.p_ready[stream]);
     }
     if (T > 0 && ok) ok = wait(&sh.o_full[stream], 0);
+    if (T == 0 && some) ok = wait(&sh.q_full, 0);  // the tile's memory is used below
     __syncwarp();
     tc_fence_after();
     if (!alive) l = 0.0f;
@@ -320,6 +322,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
         a.lse[(b * a.H + head) * a.Lq + row] = total * kLn2;
     }
     const float inv = bad ? NAN : l == 0.0f ? 0.0f : 1.0f / l;
+    unsigned char *out_tile = q_tile + stream * S::TILE;  // every product with q is done
 #pragma unroll
     for (int i = 0; i < DP / 32; ++i) {
       unsigned o[32];
@@ -331,21 +334,24 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
 #pragma unroll
       for (int k = 0; k < 32; ++k)
         v[k] = bad ? NAN : l == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
-      if (row >= a.Lq) {
-      } else if (f.p.splits > 1) {
+      if (f.p.splits == 1) {
+        stage32<DT>(out_tile, S::CHUNK, r, i * 32, v);
+      } else if (row < a.Lq) {
         float4 *dst = reinterpret_cast<float4 *>(f.part_o + part * DP + i * 32);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-      } else {
-        unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
-                              row * a.so.l + head * a.so.h + i * 32;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (i * 32 + k * 8 < a.D)
-            reinterpret_cast<uint4 *>(dst)[k] = make_uint4(
-                pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
-                pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
+      }
+      __syncwarp();
+    }
+    if (f.p.splits == 1) {
+      fence_async_shared();
+      named_barrier<128>(1 + stream);
+      if (r == 0 && row < a.Lq) {
+        for (int ch = 0; ch < S::CHUNKS; ++ch)
+          tma_store_4d(&om, out_tile + ch * S::CHUNK, ch * 64, h0 * f.o_h, row, (int)b * f.o_b);
+        tma_store_commit();
+        tma_store_wait_read();
       }
       __syncwarp();
     }
@@ -423,7 +429,7 @@ FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 template <int DT, int DP, bool WIDE>
-cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v,
+cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v, const TensorMap &o,
                    cudaStream_t stream) {
   typedef FwdShape<DP, WIDE> S;
   const size_t smem = S::BYTES + 1024;
@@ -432,7 +438,7 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
   if (e != cudaSuccess) return e;
   const long long ctas = f.a.B * f.p.packs * f.p.tiles;
   attn_fwd_tc_kernel<DT, DP, WIDE>
-      <<<(unsigned)(ctas * f.p.splits), S::THREADS, smem, stream>>>(q.map, k.map, v.map, f);
+      <<<(unsigned)(ctas * f.p.splits), S::THREADS, smem, stream>>>(q.map, k.map, v.map, o.map, f);
   e = cudaGetLastError();
   if (e != cudaSuccess || f.p.splits == 1) return e;
   const int rows = S::NS * kRows;
@@ -442,11 +448,11 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
 }
 
 template <int DT>
-cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v,
+cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v, const TensorMap &o,
                      cudaStream_t s) {
   if (f.a.D <= 64)
-    return f.p.wide ? launch<DT, 64, true>(f, q, k, v, s) : launch<DT, 64, false>(f, q, k, v, s);
-  return f.p.wide ? launch<DT, 128, true>(f, q, k, v, s) : launch<DT, 128, false>(f, q, k, v, s);
+    return f.p.wide ? launch<DT, 64, true>(f, q, k, v, o, s) : launch<DT, 64, false>(f, q, k, v, o, s);
+  return f.p.wide ? launch<DT, 128, true>(f, q, k, v, o, s) : launch<DT, 128, false>(f, q, k, v, o, s);
 }
 
 }  // namespace
@@ -481,18 +487,21 @@ cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.part_o = static_cast<float *>(workspace);
   f.part_l = reinterpret_cast<float *>(static_cast<char *>(workspace) +
                                        align256(rows * (a.D <= 64 ? 64 : 128) * 4));
-  TensorMap q, k, v;
+  TensorMap q, k, v, o;
   if (!encode_map(&q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, kRows / f.p.P) ||
       !encode_map(&k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
-      !encode_map(&v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows))
+      !encode_map(&v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows) ||
+      !encode_map(&o, a.out, dtype, a.B, a.Lq, a.H, a.D, a.so.b, a.so.l, a.so.h, f.p.P, kRows / f.p.P))
     return cudaErrorInvalidValue;
+  f.o_b = o.b_mul;
+  f.o_h = o.h_mul;
   f.q_b = q.b_mul;
   f.q_h = q.h_mul;
   f.k_b = k.b_mul;
   f.k_h = k.h_mul;
   f.v_b = v.b_mul;
   f.v_h = v.h_mul;
-  return dtype == kF16 ? by_shape<kF16>(f, q, k, v, stream) : by_shape<kBF16>(f, q, k, v, stream);
+  return dtype == kF16 ? by_shape<kF16>(f, q, k, v, o, stream) : by_shape<kBF16>(f, q, k, v, o, stream);
 }
 
 }  // namespace tdt

@@ -73,6 +73,25 @@ __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, void *dst,
       "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+// Stores a tile; elements past the tensor's ends are not written.  The thread that issues commits and
+// waits until the tile has been read before its memory is used again or the CTA ends.
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void *src, int x, int y,
+                                             int z, int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          map),
+      "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+}
+template <int THREADS> __device__ __forceinline__ void named_barrier(int id) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
@@ -245,6 +264,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Columns [d0, d0 + 32) of a row as 16-bit elements into a tile, placed as TMA places them.  (A thread
+// that holds a row would otherwise store it straight to memory: 32 lines an instruction, which was
+// measured to take the load/store path away from everybody else.)
+template <int DT>
+__device__ __forceinline__ void stage32(unsigned char *tile, int chunk_bytes, int row, int d0,
+                                        const float (&v)[32]) {
+  unsigned char *at = tile + (d0 / 64) * chunk_bytes + row * 128;
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<uint4 *>(at + (((d0 % 64) / 8 + k) ^ (row & 7)) * 16) =
+        make_uint4(pack2<DT>(v[8 * k], v[8 * k + 1]), pack2<DT>(v[8 * k + 2], v[8 * k + 3]),
+                   pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
 }
 
 // Zeroes rows [first, rows) of a tile in shared memory (a warp), for the tensor cores to read.
