@@ -136,6 +136,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int P = f.p.P, per = kRows / P, i0 = tile * per, h0 = pack * P, hk = h0 / a.G;
   const Lens n = utt_lens(a, b);
   const bool some = i0 < n.nq && n.nk > 0;  // else no row sees a frame
+  // frames [hull.x, hull.y) in tiles of 128 from hull.x; this CTA takes T tiles from `begin`
+  int begin = 0, T = 0;
+  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
+  // k a warp of its own zeroes them (unless TMA did, past the tensor's end): the load then arrives
+  // at tail_full, and that warp hands the tile on.
+  bool cut = false;
+  auto walk = [&](int2 hull) {
+    const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.dq_splits);
+    begin = hull.x + steps.x * kRows;
+    T = steps.y - steps.x;
+    cut = T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;
+  };
+  if (!a.windows && some) walk(make_int2(0, n.nk));
+  auto frame = [&](int s) { return begin + s * kRows; };
+  auto load_k = [&](int s) {
+    const int slot = s % S::KS;
+    unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
+    arrive_expect_tx(bar, S::TILE);
+    load_rows<DP>(&km, k_slots + slot * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
+  };
+  auto load_v = [&](int s) {
+    const int slot = s % S::VS;
+    arrive_expect_tx(&sh.v.full[slot], S::TILE);
+    load_rows<DP>(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], hk * f.v_h, frame(s), (int)b * f.v_b);
+  };
   const int group = warp >> 2, r = threadIdx.x & 127;
   const int row = i0 + r / P, head = h0 + r % P;
   int2 range = make_int2(0, 0);
@@ -158,6 +183,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       load_rows<DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
       load_rows<DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
     }
+    if (T > 0) {  // no windows: the walk is known
+      load_k(0);
+      load_v(0);
+    }
   } else if (warp == 9) {
     tmem_alloc<512>(&sh.tmem);
   }
@@ -166,16 +195,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  const int2 hull = a.windows ? hull_of<8>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
-  const int first = hull.x;
-  const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.dq_splits);
-  const int t0 = steps.x, T = steps.y - steps.x;
-  auto frame = [&](int s) { return first + (t0 + s) * kRows; };
+  if (a.windows) walk(hull_of<8>(sh.hull));
   constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ
-  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
-  // k a warp of its own zeroes them (unless TMA did, past the tensor's end): the load then arrives
-  // at tail_full, and that warp hands the tile on.
-  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
@@ -184,19 +205,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int s = 0;
       for (; ok && s < T; ++s) {
-        const int ks = s % S::KS, vs = s % S::VS;
-        ok = wait(&sh.k.empty[ks], ((unsigned)(s / S::KS) & 1) ^ 1);
+        if (s == 0 && !a.windows) continue;  // loaded above
+        ok = wait(&sh.k.empty[s % S::KS], ((unsigned)(s / S::KS) & 1) ^ 1);
         if (!ok) break;
-        unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[ks];
-        arrive_expect_tx(bar, S::TILE);
-        load_rows<DP>(&km, k_slots + ks * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
-        ok = wait(&sh.v.empty[vs], ((unsigned)(s / S::VS) & 1) ^ 1);
+        load_k(s);
+        ok = wait(&sh.v.empty[s % S::VS], ((unsigned)(s / S::VS) & 1) ^ 1);
         if (!ok) {
           ++s;
           break;
         }
-        arrive_expect_tx(&sh.v.full[vs], S::TILE);
-        load_rows<DP>(&vm, v_slots + vs * S::TILE, &sh.v.full[vs], hk * f.v_h, frame(s), (int)b * f.v_b);
+        load_v(s);
       }
       if (!ok) {  // copies in flight land before the CTA ends
         Waiter::drain(&sh.rows_full, 0);
@@ -708,21 +726,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- dq, dk and dv of one row tile -----------------------------------------------------
 // Threads: two warpgroups of elementwise work (thread = row, each group half of the frames), one that
-// stores dk and dv tiles (thread = frame), four warps: TMA, products, tails.
+// stages dk and dv tiles (thread = frame), four warps: loads, products, tails, stores.
 constexpr int kOneThreads = 512;
 constexpr int kOneLaunchRegs = 128;  // 4 x 128 = 2 x 160 + 112 + 80
 constexpr int kOneWorkRegs = 160, kOneStoreRegs = 112, kOneOtherRegs = 80;
 
 struct OneShape {
   static constexpr int TILE = kRows * 128;            // 64 columns
-  static constexpr int KV = 2;                        // slots of k and of v
-  static constexpr int PDS = 2 * TILE;                // P or dS: 128 x 128
-  static constexpr int BYTES = (2 + 2 * KV + 2) * TILE + 2 * PDS;
+  static constexpr int KS = 3, VS = 2;                // slots of k and of v
+  static constexpr int PDS = 2 * TILE;                // P or dS: 128 x 128; P once, dS twice
+  static constexpr int BYTES = (2 + KS + VS) * TILE + 3 * PDS;
 };
 
 struct OneShared {
   Pipe k, v;
-  unsigned long long rows_in, rows_full, sp_full, pds_ready, pds_free, dkv_full, dkv_free, done, tail_full,
+  unsigned long long rows_in, rows_full, sp_full, pds_ready, p_free, ds_free[2], dkv_full, dkv_free, dq_done[2], staged[2], done, tail_full,
       drained;
   unsigned tmem;
   int gave_up;
@@ -743,8 +761,8 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   __shared__ OneShared sh;
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   unsigned char *q_tile = tiles, *g_tile = q_tile + S::TILE, *k_slots = g_tile + S::TILE,
-                *v_slots = k_slots + S::KV * S::TILE, *p_tile = v_slots + S::KV * S::TILE,
-                *ds_tile = p_tile + S::PDS, *out_tiles = ds_tile + S::PDS;
+                *v_slots = k_slots + S::KS * S::TILE, *p_tile = v_slots + S::VS * S::TILE,
+                *ds_tiles = p_tile + S::PDS;
   const AttnArgs &a = f.a;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = blockIdx.x % f.p.dq_splits;
@@ -759,19 +777,49 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   // zeroes them in the tiles of q and dO and in the last tile of k before handing these on (unless TMA
   // did, past the tensor's ends).
   const bool some = n.nq > 0 && n.nk > 0, cut_rows = n.nq < a.Lq;
+  // this CTA's frame tiles [t0, t1); those that a row sees are [ta, tb)
+  const int2 mine = share_of(f.p.f_tiles, split, f.p.dq_splits);
+  const int t0 = mine.x, t1 = mine.y;
+  int ta = t1, tb = t1, T = 0;
+  bool cut = false;
+  auto walk = [&](int2 hull) {
+    ta = hull.y > hull.x ? max(t0, hull.x / kRows) : t1;
+    tb = min(t1, (hull.y + kRows - 1) / kRows);
+    T = max(0, tb - ta);
+    cut = T > 0 && n.nk < a.Lk && (ta + T) * kRows > n.nk;
+  };
+  if (!a.windows && some) walk(make_int2(0, n.nk));
+  auto frame = [&](int s) { return (ta + s) * kRows; };
+  auto load_k = [&](int s) {
+    const int slot = s % S::KS;
+    unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
+    arrive_expect_tx(bar, S::TILE);
+    tma_load_4d(&km, k_slots + slot * S::TILE, bar, 0, hk * f.k_h, frame(s), (int)b * f.k_b);
+  };
+  auto load_v = [&](int s) {
+    const int slot = s % S::VS;
+    arrive_expect_tx(&sh.v.full[slot], S::TILE);
+    tma_load_4d(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], 0, hk * f.v_h, frame(s), (int)b * f.v_b);
+  };
   if (group < 2) {
     range = row_range(a, b, row, n);
     if (a.windows) hull_note(sh.hull, warp, range);
   } else if (warp == 12 && lane == 0) {
-    pipe_init(sh.k, S::KV);
-    pipe_init(sh.v, S::KV);
+    pipe_init(sh.k, S::KS);
+    pipe_init(sh.v, S::VS);
     mbar_init(&sh.rows_in, 1);
     mbar_init(&sh.rows_full, 1);
     mbar_init(&sh.sp_full, 1);
     mbar_init(&sh.pds_ready, 256);
-    mbar_init(&sh.pds_free, 1);
+    mbar_init(&sh.p_free, 1);
+    mbar_init(&sh.ds_free[0], 1);
+    mbar_init(&sh.ds_free[1], 1);
     mbar_init(&sh.dkv_full, 1);
     mbar_init(&sh.dkv_free, 128);
+    mbar_init(&sh.dq_done[0], 1);
+    mbar_init(&sh.dq_done[1], 1);
+    mbar_init(&sh.staged[0], 128);
+    mbar_init(&sh.staged[1], 128);
     mbar_init(&sh.done, 1);
     mbar_init(&sh.tail_full, 1);
     mbar_init(&sh.drained, 1);
@@ -783,6 +831,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       tma_load_4d(&qm, q_tile, in, 0, h0 * f.q_h, 0, (int)b * f.q_b);
       tma_load_4d(&gm, g_tile, in, 0, h0 * f.go_h, 0, (int)b * f.go_b);
     }
+    if (T > 0) {  // no windows: the walk is known
+      load_k(0);
+      load_v(0);
+    }
   } else if (warp == 13) {
     tmem_alloc<512>(&sh.tmem);
   }
@@ -791,16 +843,8 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  const int2 hull = a.windows ? hull_of<8>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
-  // this CTA's frame tiles [t0, t1); those that a row sees are [ta, tb)
-  const int2 mine = share_of(f.p.f_tiles, split, f.p.dq_splits);
-  const int t0 = mine.x, t1 = mine.y;
-  const int ta = hull.y > hull.x ? max(t0, hull.x / kRows) : t1, tb = min(t1, (hull.y + kRows - 1) / kRows),
-            T = max(0, tb - ta);
-  auto frame = [&](int s) { return (ta + s) * kRows; };
+  if (a.windows) walk(hull_of<8>(sh.hull));
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = kDv + DP, kAcc = kDk + DP;
-  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
-
   unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
   if (group == 3) {
     warpgroup_give_registers<kOneOtherRegs>();
@@ -809,22 +853,34 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       bool ok = true;
       int s = 0;
       for (; ok && s < T; ++s) {
-        const int slot = s % S::KV;
-        const unsigned turn = ((unsigned)(s / S::KV) & 1) ^ 1;
-        ok = wait(&sh.k.empty[slot], turn) && wait(&sh.v.empty[slot], turn);
+        if (s == 0 && !a.windows) continue;  // loaded above
+        ok = wait(&sh.k.empty[s % S::KS], ((unsigned)(s / S::KS) & 1) ^ 1);
         if (!ok) break;
-        unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
-        arrive_expect_tx(bar, S::TILE);
-        tma_load_4d(&km, k_slots + slot * S::TILE, bar, 0, hk * f.k_h, frame(s), (int)b * f.k_b);
-        arrive_expect_tx(&sh.v.full[slot], S::TILE);
-        tma_load_4d(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], 0, hk * f.v_h, frame(s), (int)b * f.v_b);
+        load_k(s);
+        ok = wait(&sh.v.empty[s % S::VS], ((unsigned)(s / S::VS) & 1) ^ 1);
+        if (!ok) {
+          ++s;
+          break;
+        }
+        load_v(s);
       }
       if (!ok) {  // copies in flight land before the CTA ends
         Waiter::drain(rows, 0);
-        for (int i = max(0, s - S::KV); i < s; ++i) {
-          Waiter::drain(&sh.k.full[i % S::KV], (unsigned)(i / S::KV) & 1);
-          Waiter::drain(&sh.v.full[i % S::KV], (unsigned)(i / S::KV) & 1);
+        for (int i = max(0, s - S::KS); i < s; ++i) {
+          Waiter::drain(&sh.k.full[i % S::KS], (unsigned)(i / S::KS) & 1);
+          Waiter::drain(&sh.v.full[i % S::VS], (unsigned)(i / S::VS) & 1);
         }
+      }
+    }
+    if (warp == 15 && lane == 0) {  // stores the staged tiles; they are free once read
+      for (int s = 0; s < T; ++s) {
+        if (!wait(&sh.staged[s & 1], (unsigned)(s >> 1) & 1)) break;
+        const unsigned char *out_tile = ds_tiles + (s & 1) * S::PDS;
+        tma_store_4d(&dvm, out_tile, 0, hk * f.dv_h, frame(s), (int)b * f.dv_b);
+        tma_store_4d(&dkm, out_tile + S::TILE, 0, hk * f.dk_h, frame(s), (int)b * f.dk_b);
+        tma_store_commit();
+        tma_store_wait_read();
+        mbar_arrive(&sh.ds_free[s & 1]);
       }
     }
     if (warp == 14 && T > 0) {
@@ -836,7 +892,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         if (lane == 0) mbar_arrive(&sh.rows_full);
       }
       if (cut) {
-        const int slot = (T - 1) % S::KV;
+        const int slot = (T - 1) % S::KS;
         if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
           zero_tail(k_slots + slot * S::TILE, 1, S::TILE, n.nk - frame(T - 1), kRows);
         if (lane == 0) mbar_arrive(&sh.k.full[slot]);
@@ -846,22 +902,23 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       constexpr unsigned i_s = mma_desc<DT>(kRows, false), i_t = mma_desc<DT>(DP, true, true),
                          i_o = mma_desc<DT>(DP, true);
       const unsigned qa = smem_u32(q_tile), ga = smem_u32(g_tile), ka = smem_u32(k_slots),
-                     va = smem_u32(v_slots), pa = smem_u32(p_tile), da = smem_u32(ds_tile);
+                     va = smem_u32(v_slots), pa = smem_u32(p_tile);
       bool ok = wait(&sh.rows_full, 0);
       auto scores = [&](int s) {  // S and dP
-        const int slot = s % S::KV;
-        const unsigned turn = (unsigned)(s / S::KV) & 1;
-        ok = ok && wait(&sh.k.full[slot], turn) && wait(&sh.v.full[slot], turn);
+        const int ks = s % S::KS, vs = s % S::VS;
+        ok = ok && wait(&sh.k.full[ks], (unsigned)(s / S::KS) & 1) &&
+             wait(&sh.v.full[vs], (unsigned)(s / S::VS) & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_rows<DP>(tmem, qa, S::TILE, ka + slot * S::TILE, S::TILE, i_s, false);
-        mma_rows<DP>(tmem + kDp, ga, S::TILE, va + slot * S::TILE, S::TILE, i_s, false);
+        mma_rows<DP>(tmem, qa, S::TILE, ka + ks * S::TILE, S::TILE, i_s, false);
+        mma_rows<DP>(tmem + kDp, ga, S::TILE, va + vs * S::TILE, S::TILE, i_s, false);
         mma_commit(&sh.sp_full);
-        mma_commit(&sh.v.empty[slot]);
+        mma_commit(&sh.v.empty[vs]);
       };
       scores(0);
       for (int s = 0; ok && s < T; ++s) {
-        const int slot = s % S::KV;
+        const int slot = s % S::KS;
+        const unsigned da = smem_u32(ds_tiles) + (s & 1) * S::PDS;
         ok = wait(&sh.pds_ready, s & 1);
         if (s + 1 < T) scores(s + 1);
         ok = ok && wait(&sh.dkv_free, (s & 1) ^ 1);
@@ -871,6 +928,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         for (int k = 0; k < kRows / 16; ++k)  // dV = P^T dO
           mma_ss(tmem + kDv, desc_mn_major(pa + k * 2048, S::TILE), desc_mn_major(ga + k * 2048, S::TILE),
                  i_t, k > 0);
+        mma_commit(&sh.p_free);
 #pragma unroll
         for (int k = 0; k < kRows / 16; ++k)  // dK = dS^T Q
           mma_ss(tmem + kDk, desc_mn_major(da + k * 2048, S::TILE), desc_mn_major(qa + k * 2048, S::TILE),
@@ -881,7 +939,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
           mma_ss(tmem + kAcc, desc_k_major(da + (k / 4) * S::TILE + (k % 4) * 32),
                  desc_mn_major(ka + slot * S::TILE + k * 2048, S::TILE), i_o, s > 0 || k > 0);
         mma_commit(&sh.k.empty[slot]);
-        mma_commit(&sh.pds_free);
+        mma_commit(&sh.dq_done[s & 1]);
         if (s + 1 == T) mma_commit(&sh.done);
       }
       if (!ok) {
@@ -894,45 +952,56 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
     for (int t = t0; t < t1; ++t) {
       const int j = t * kRows + r, s = t - ta;
-      const bool sums = t >= ta && t < tb;
-      bool ok = true;
-      if (sums) {
-        ok = wait(&sh.dkv_full, s & 1);
-        ok = __all_sync(0xffffffffu, ok) && !*reinterpret_cast<volatile int *>(&sh.gave_up);
-        __syncwarp();
-        tc_fence_after();
-      }
-      if (r == 0) tma_store_wait_read();  // the tiles before these have been read
-      named_barrier<128>(2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // 32 columns of dv, dv, dk, dk
-        unsigned o[32];
-        if (sums) {
-          tmem_ld32(tmem + lanes + kDv + i * 32, o);
-          tmem_wait_ld();
-          if (i == 3) {
-            tc_fence_before();
-            mbar_arrive(&sh.dkv_free);
-          }
+      if (t < ta || t >= tb) {  // no row sees these frames
+        for (int x = r; x < kRows * 8; x += 128) {
+          const int jz = t * kRows + x / 8, d = x % 8 * 8;
+          if (jz >= a.Lk || d >= a.D) continue;
+          typedef unsigned short Raw;
+          *reinterpret_cast<uint4 *>(static_cast<Raw *>(a.dv) + b * a.sdv.b + jz * a.sdv.l + hk * a.sdv.h + d) =
+              make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4 *>(static_cast<Raw *>(a.dk) + b * a.sdk.b + jz * a.sdk.l + hk * a.sdk.h + d) =
+              make_uint4(0, 0, 0, 0);
         }
-        float v[32];
+        continue;
+      }
+      bool ok = wait(&sh.dkv_full, s & 1);
+      ok = __all_sync(0xffffffffu, ok) && !*reinterpret_cast<volatile int *>(&sh.gave_up);
+      __syncwarp();
+      tc_fence_after();
+      unsigned packed[2][32];  // dv and dk of the frame
 #pragma unroll
-        for (int k = 0; k < 32; ++k)
-          v[k] = !ok ? NAN
-                     : sums && j < n.nk ? __uint_as_float(o[k]) * (i < 2 ? kUnshift<DT> : a.scale) : 0.0f;
-        stage32<DT>(out_tiles + (i / 2) * S::TILE, S::TILE, r, (i & 1) * 32, v);
-        __syncwarp();
+      for (int i = 0; i < 4; ++i) {
+        unsigned o[32];
+        tmem_ld32(tmem + lanes + kDv + i * 32, o);
+        tmem_wait_ld();
+        const float f_out = i < 2 ? kUnshift<DT> : a.scale;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          const float2 v = mul2(pair(o[k], o[k + 1]), make_float2(f_out, f_out));
+          packed[i / 2][(i & 1) * 16 + k / 2] = pack2<DT>(v.x, v.y);
+        }
       }
+      if (!ok || j >= n.nk) {
+        const unsigned fill = ok ? 0u : pack2<DT>(NAN, NAN);
+#pragma unroll
+        for (int k = 0; k < 64; ++k) packed[k / 32][k % 32] = fill;
+      }
+      __syncwarp();
+      tc_fence_before();
+      mbar_arrive(&sh.dkv_free);
+      // the tiles go out through the memory of this step's dS, once the products have read it
+      wait(&sh.dq_done[s & 1], (unsigned)(s >> 1) & 1);
+      __syncwarp();
+      unsigned char *out_tile = ds_tiles + (s & 1) * S::PDS;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          *reinterpret_cast<uint4 *>(out_tile + i * S::TILE + r * 128 + (k ^ (r & 7)) * 16) =
+              make_uint4(packed[i][4 * k], packed[i][4 * k + 1], packed[i][4 * k + 2], packed[i][4 * k + 3]);
       fence_async_shared();
-      named_barrier<128>(2);
-      if (r == 0) {
-        tma_store_4d(&dvm, out_tiles, 0, hk * f.dv_h, t * kRows, (int)b * f.dv_b);
-        tma_store_4d(&dkm, out_tiles + S::TILE, 0, hk * f.dk_h, t * kRows, (int)b * f.dk_b);
-        tma_store_commit();
-      }
+      mbar_arrive(&sh.staged[s & 1]);
     }
-    if (r == 0) tma_store_wait_read();
-    __syncwarp();
     tc_fence_before();
   } else {
     warpgroup_take_registers<kOneWorkRegs>();
@@ -957,7 +1026,6 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     const float c = a.scale * kLog2e;
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
     const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
-    unsigned char *p_row = p_tile + group * S::TILE + r * 128, *ds_row = ds_tile + group * S::TILE + r * 128;
     const float2 c2 = make_float2(c, c), l2 = make_float2(lse2, lse2), d2 = make_float2(delta, delta),
                  un = make_float2(kUnshift<DT>, kUnshift<DT>);
     bool ok = true;
@@ -983,7 +1051,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
             y[i >> 5][i & 31] = 0;
           }
       }
-      ok = wait(&sh.pds_free, (s & 1) ^ 1);  // the products have read the last tile's P and dS
+      // what was in this P and dS has been read
+      ok = wait(&sh.p_free, (s & 1) ^ 1) && wait(&sh.ds_free[s & 1], ((unsigned)(s >> 1) & 1) ^ 1);
+      unsigned char *p_row = p_tile + group * S::TILE + r * 128,
+                    *ds_row = ds_tiles + (s & 1) * S::PDS + group * S::TILE + r * 128;
       if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {  // 8 frames: 16 bytes of P and of dS, swizzled as TMA would

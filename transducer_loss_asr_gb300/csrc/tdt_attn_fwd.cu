@@ -110,6 +110,29 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
   const int h0 = pack * P, hk = h0 / a.G;
   const Lens n = utt_lens(a, b);
   const bool some = i0 < n.nq && n.nk > 0;  // else no row sees a frame
+  // frames [hull.x, hull.y) in tiles of 128 from hull.x; this CTA takes T tiles from `begin`
+  int begin = 0, T = 0;
+  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
+  // v, which is the last tile loaded, a warp of its own zeroes them (unless TMA did, past the
+  // tensor's end): the load then arrives at tail_full, and that warp hands the tile on.
+  bool cut = false;
+  auto walk = [&](int2 hull) {
+    const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.splits);
+    begin = hull.x + steps.x * kRows;
+    T = steps.y - steps.x;
+    cut = T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;
+  };
+  if (!a.windows && some) walk(make_int2(0, n.nk));
+  auto frame = [&](int s) { return begin + s * kRows; };
+  auto load = [&](int at) {  // tiles count up: k of step 0, v of step 0, k of step 1, ...
+    const int slot = at % S::SLOTS, s = at / 2;
+    const bool values = at & 1;
+    unsigned long long *bar = cut && at == 2 * T - 1 ? &sh.tail_full : &sh.full[slot];
+    arrive_expect_tx(bar, S::TILE);
+    for (int ch = 0; ch < S::CHUNKS; ++ch)
+      tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, bar, ch * 64,
+                  hk * (values ? f.v_h : f.k_h), frame(s), (int)b * (values ? f.v_b : f.k_b));
+  };
 
   constexpr int kAux = S::NS * 4;  // the first warp past the softmax's: TMA
   const int stream = warp >> 2, r = threadIdx.x & 127;
@@ -142,6 +165,10 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
           tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
                       i0 + t * per, (int)b * f.q_b);
     }
+    if (T > 0) {  // no windows: the walk is known
+      load(0);
+      load(1);
+    }
   } else if (warp == kAux + 1) {
     tmem_alloc<S::TMEM>(&sh.tmem);
   }
@@ -150,40 +177,19 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  // frames [hull.x, hull.y) in tiles of 128 from hull.x; this CTA takes tiles [t0, t0 + T)
-  const int2 hull = a.windows ? hull_of<kAux>(sh.hull) : some ? make_int2(0, n.nk) : make_int2(0, 0);
-  const int first = hull.x;
-  const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.splits);
-  const int t0 = steps.x, T = steps.y - steps.x;
-  auto frame = [&](int s) { return first + (t0 + s) * kRows; };
+  if (a.windows) walk(hull_of<kAux>(sh.hull));
   const float c = a.scale * kLog2e;
-
-  // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
-  // v, which is the last tile loaded, a warp of its own zeroes them (unless TMA did, past the
-  // tensor's end): the load then arrives at tail_full, and that warp hands the tile on.
-  const bool cut = T > 0 && n.nk < a.Lk && frame(T - 1) + kRows > n.nk;
 
   if (warp >= kAux) {
     warpgroup_give_registers<S::OTHER_REGS>();  // to the softmax warps, which hold a row of scores
     if (warp == kAux && lane == 0 && some && T == 0) wait(&sh.q_full, 0);  // nobody else does
     if (warp == kAux && lane == 0 && T > 0) {
-      int at = 0;
-      auto load = [&](bool values, int j0) {
-        const int slot = at % S::SLOTS;
-        const unsigned turn = (unsigned)(at / S::SLOTS) & 1;
-        if (!wait(&sh.empty[slot], turn ^ 1)) return false;
-        unsigned long long *bar = cut && at == 2 * T - 1 ? &sh.tail_full : &sh.full[slot];
-        arrive_expect_tx(bar, S::TILE);
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, bar,
-                      ch * 64, hk * (values ? f.v_h : f.k_h), j0, (int)b * (values ? f.v_b : f.k_b));
-        ++at;
-        return true;
-      };
-      bool ok = load(false, frame(0));
-      for (int s = 0; ok && s < T; ++s) {
-        ok = load(true, frame(s));
-        if (s + 1 < T) ok = ok && load(false, frame(s + 1));
+      bool ok = true;
+      int at = a.windows ? 0 : 2;  // the first two were loaded above
+      for (; at < 2 * T; ++at) {
+        ok = wait(&sh.empty[at % S::SLOTS], ((unsigned)(at / S::SLOTS) & 1) ^ 1);
+        if (!ok) break;
+        load(at);
       }
       if (!ok)  // copies in flight land before the CTA ends
         for (int i = max(0, at - S::SLOTS); i < at; ++i)
