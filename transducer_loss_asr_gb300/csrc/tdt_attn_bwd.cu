@@ -86,15 +86,22 @@ __device__ __forceinline__ void store32f(float *dst, const float (&v)[32]) {
     reinterpret_cast<float4 *>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
 }
 
-// dot of two rows' elements [d0, d0 + n), n a multiple of 8
-template <int DT>
-__device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
+// dot of the first `n` of N elements of two rows, n a multiple of 8; every load is in flight at once
+template <int DT, int N> __device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
   typedef typename Elem<DT>::T E;
+  uint4 xv[N / 8], yv[N / 8];
+#pragma unroll
+  for (int d = 0; d < N; d += 8) {
+    xv[d / 8] = yv[d / 8] = make_uint4(0, 0, 0, 0);
+    if (d < n) {
+      xv[d / 8] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d));
+      yv[d / 8] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
+    }
+  }
   float s = 0.0f;
-  for (int d = 0; d < n; d += 8) {
-    const uint4 xv = *reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d);
-    const uint4 yv = *reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d);
-    const E *xe = reinterpret_cast<const E *>(&xv), *ye = reinterpret_cast<const E *>(&yv);
+#pragma unroll
+  for (int d = 0; d < N / 8; ++d) {
+    const E *xe = reinterpret_cast<const E *>(&xv[d]), *ye = reinterpret_cast<const E *>(&yv[d]);
 #pragma unroll
     for (int k = 0; k < 8; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
   }
@@ -104,7 +111,7 @@ __device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
 // ---- dq ---------------------------------------------------------------------------
 struct DqShared {
   Pipe k, v;
-  unsigned long long rows_full, scores, ds_ready, done, tail_full, drained;
+  unsigned long long rows_full, scores, dp_free, ds_ready, done, tail_full, drained;
   unsigned tmem;
   int gave_up;
   Hull hull;
@@ -172,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pipe_init(sh.v, S::VS);
     mbar_init(&sh.rows_full, 1);
     mbar_init(&sh.scores, 1);
+    mbar_init(&sh.dp_free, 256);
     mbar_init(&sh.ds_ready, 256);
     mbar_init(&sh.done, 1);
     mbar_init(&sh.tail_full, 1);
@@ -254,10 +262,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       scores(0);
       grads(0);
       for (int s = 0; ok && s < T; ++s) {
-        if (s + 1 < T) scores(s + 1);
+        if (s + 1 < T) {
+          scores(s + 1);
+          ok = ok && wait(&sh.dp_free, s & 1);
+          grads(s + 1);
+        }
         ok = ok && wait(&sh.ds_ready, s & 1);
         tc_fence_after();
-        if (s + 1 < T) grads(s + 1);
         if (!ok) break;
         const int slot = s % S::KS;
         const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
@@ -278,11 +289,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta = 0.0f, lse2 = INFINITY;
     {
-      const int h = (a.D / 8 + 1) / 2 * 8, d0 = group ? h : 0, len = group ? a.D - h : h;
+      const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
       float x = 0.0f;
       if (real)
-        x = dot16<DT>(static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
-                      static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
+        x = dot16<DT, DP / 2>(
+            static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
+            static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
       if (group == 1) sh.half[r] = x;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       const float y = sh.half[r];
@@ -311,6 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tmem_ld32(p_col, y[0]);
       tmem_ld32(p_col + 32, y[1]);
       tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&sh.dp_free);
       const int j0 = frame(s) + group * 64;
       const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2),
                    d2 = make_float2(-delta, -delta);
@@ -740,7 +754,7 @@ struct OneShape {
 
 struct OneShared {
   Pipe k, v;
-  unsigned long long rows_in, rows_full, sp_full, pds_ready, p_free, ds_free[2], dkv_full, dkv_free, dq_done[2], staged[2], done, tail_full,
+  unsigned long long rows_in, rows_full, sp_full, sp_free, pds_ready, p_free, ds_free[2], dkv_full, dkv_free, dq_done[2], staged[2], done, tail_full,
       drained;
   unsigned tmem;
   int gave_up;
@@ -810,6 +824,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     mbar_init(&sh.rows_in, 1);
     mbar_init(&sh.rows_full, 1);
     mbar_init(&sh.sp_full, 1);
+    mbar_init(&sh.sp_free, 256);
     mbar_init(&sh.pds_ready, 256);
     mbar_init(&sh.p_free, 1);
     mbar_init(&sh.ds_free[0], 1);
@@ -919,8 +934,11 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       for (int s = 0; ok && s < T; ++s) {
         const int slot = s % S::KS;
         const unsigned da = smem_u32(ds_tiles) + (s & 1) * S::PDS;
-        ok = wait(&sh.pds_ready, s & 1);
-        if (s + 1 < T) scores(s + 1);
+        if (s + 1 < T) {
+          ok = wait(&sh.sp_free, s & 1);
+          scores(s + 1);
+        }
+        ok = ok && wait(&sh.pds_ready, s & 1);
         ok = ok && wait(&sh.dkv_free, (s & 1) ^ 1);
         tc_fence_after();
         if (!ok) break;
@@ -1009,11 +1027,12 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta, lse2 = -INFINITY;  // both negated
     {
-      const int h = (a.D / 8 + 1) / 2 * 8, d0 = group ? h : 0, len = group ? a.D - h : h;
+      const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
       float x = 0.0f;
       if (real)
-        x = dot16<DT>(static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
-                      static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
+        x = dot16<DT, DP / 2>(
+            static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
+            static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
       if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
       if (group == 1) sh.half[r] = x;
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1039,6 +1058,8 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       tmem_ld32(d_col, y[0]);
       tmem_ld32(d_col + 32, y[1]);
       tmem_wait_ld();
+      tc_fence_before();
+      mbar_arrive(&sh.sp_free);
       const int j0 = frame(s) + group * 64;
       if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
         // frames that the row does not see: s = -inf weighs 0, and dP may be anything
