@@ -130,8 +130,10 @@ int tdt_cross_attn_fwd(const void *q, const void *k, const void *v, const int64_
   a.out = out;
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = attn_fwd_tc_fits(a, dtype) ? launch_attn_fwd_tc(a, dtype, workspace, s)
-                                                   : launch_attn_general_fwd(a, dtype, s);
+  const bool tc = attn_fwd_tc_fits(a, dtype);
+  const cudaError_t e = attn_step_fits(a, dtype, tc) ? launch_attn_step(a, dtype, s)
+                        : tc                         ? launch_attn_fwd_tc(a, dtype, workspace, s)
+                                                     : launch_attn_general_fwd(a, dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

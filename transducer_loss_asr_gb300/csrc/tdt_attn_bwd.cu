@@ -56,13 +56,13 @@ template <int DP> struct BwdShape {
   static constexpr int CHUNK = kRows * 128;
   static constexpr int TILE = CHUNKS * CHUNK;
   static constexpr int KS = 3, VS = 2;  // dq: slots of k and v
-  static constexpr int RS = 2;          // dk/dv: slots of q and of dO
+  static constexpr int RS = DP == 64 ? 4 : 2;  // dk/dv: slots of q and of dO
   static constexpr int DQ_BYTES = (2 + KS + VS) * TILE;
   static constexpr int DKV_BYTES = (2 + 2 * RS) * TILE;
 };
 
 struct Pipe {  // a ring of tiles
-  unsigned long long full[3], empty[3];
+  unsigned long long full[4], empty[4];
 };
 
 __device__ __forceinline__ void pipe_init(Pipe &p, int slots) {
@@ -392,16 +392,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---- dk and dv ----------------------------------------------------------------------
+constexpr int kStats = 4;  // row tiles whose statistics are held
+
 struct DkvShared {
   Pipe q, g;
-  unsigned long long frames_full, s_full, p_ready, dp_full, ds_ready, stat_full[2], stat_empty[2],
-      done, q_tail[2], g_tail[2], drained;
+  unsigned long long frames_full, s_full, p_ready, dp_full, ds_ready, stat_full[kStats], stat_empty[kStats],
+      done, q_tail[4], g_tail[4], drained;
   unsigned tmem;
   int gave_up;
   unsigned char active[kTileBits];  // row tiles with a query that sees these frames
-  int cut[2];                       // whether some row of the tile sees only part of them
-  __align__(16) float lse2[2][kRows], delta[2][kRows];  // of the rows, both negated
-  __align__(16) int lo[2][kRows], len[2][kRows];
+  int cut[kStats];                  // whether some row of the tile sees only part of them
+  __align__(16) float lse2[kStats][kRows], delta[kStats][kRows];  // of the rows, both negated
+  __align__(16) int lo[kStats][kRows], len[kStats][kRows];
 };
 
 template <int DT, int DP>
@@ -442,9 +444,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.p_ready, 256);
       mbar_init(&sh.dp_full, 1);
       mbar_init(&sh.ds_ready, 256);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < kStats; ++i) {
         mbar_init(&sh.stat_full[i], 32);
         mbar_init(&sh.stat_empty[i], 256);
+      }
+      for (int i = 0; i < S::RS; ++i) {
         mbar_init(&sh.q_tail[i], 1);
         mbar_init(&sh.g_tail[i], 1);
       }
@@ -587,28 +591,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         Waiter::drain(&sh.drained, 0);
       }
     }
+    if (warp == 10) wait_for_predecessor();  // delta is the dq kernel's; and nobody overtakes it
     if (warp == 10 && any) {  // the rows' statistics
       int s = 0;
       for (int t = start; t < t1; t = next(t + 1), ++s) {
-        const int buf = s & 1, i0 = t % row_tiles * per, h0 = hk * a.G + t / row_tiles * P;
-        const bool ok = wait(&sh.stat_empty[buf], ((unsigned)(s >> 1) & 1) ^ 1);
+        const int buf = s % kStats, i0 = t % row_tiles * per, h0 = hk * a.G + t / row_tiles * P;
+        const bool ok = wait(&sh.stat_empty[buf], ((unsigned)(s / kStats) & 1) ^ 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         bool cut = false;
+        constexpr int X = kRows / 32;
+        int2 w[X];
+        float l2[X], dl[X];
 #pragma unroll
-        for (int x = 0; x < kRows / 32; ++x) {
-          const int r = x * 32 + lane, i = i0 + r / P;
-          const int2 w = row_range(a, b, i, n);
-          float l2 = -INFINITY, dl = 0.0f;  // rows that see nothing: every weight is 0
-          if (w.y > w.x) {
-            const long long at = (b * a.H + h0 + r % P) * a.Lq + i;
-            l2 = kShift<DT> - a.lse[at] * kLog2e;
-            dl = -a.delta[at] * kUnshift<DT>;
-            cut |= w.x > j0 || w.y < min(j0 + kRows, n.nk);
-          }
-          sh.lse2[buf][r] = l2;
-          sh.delta[buf][r] = dl;
-          sh.lo[buf][r] = w.x;
-          sh.len[buf][r] = w.y - w.x;
+        for (int x = 0; x < X; ++x) w[x] = row_range(a, b, i0 + (x * 32 + lane) / P, n);
+#pragma unroll
+        for (int x = 0; x < X; ++x) {  // every load in flight at once
+          const int r = x * 32 + lane, i = min(i0 + r / P, a.Lq - 1);
+          const long long at = (b * a.H + h0 + r % P) * a.Lq + i;
+          l2[x] = __ldg(a.lse + at);
+          dl[x] = a.delta[at];  // not the read-only path: it was written since this kernel was launched
+        }
+#pragma unroll
+        for (int x = 0; x < X; ++x) {
+          const int r = x * 32 + lane;
+          const bool sees = w[x].y > w[x].x;  // else every weight is 0
+          cut |= sees && (w[x].x > j0 || w[x].y < min(j0 + kRows, n.nk));
+          sh.lse2[buf][r] = sees ? kShift<DT> - l2[x] * kLog2e : -INFINITY;
+          sh.delta[buf][r] = sees ? -dl[x] * kUnshift<DT> : 0.0f;
+          sh.lo[buf][r] = w[x].x;
+          sh.len[buf][r] = w[x].y - w[x].x;
         }
         cut = __any_sync(0xffffffffu, cut);
         if (lane == 0) sh.cut[buf] = cut;
@@ -627,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int s = 0;
     if (any)
       for (int t = start; t < t1; t = next(t + 1), ++s) {
-        const int buf = s & 1;
-        ok = wait(&sh.stat_full[buf], (unsigned)(s >> 1) & 1) && wait(&sh.s_full, s & 1);
+        const int buf = s % kStats;
+        ok = wait(&sh.stat_full[buf], (unsigned)(s / kStats) & 1) && wait(&sh.s_full, s & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         unsigned x[2][32], out[32];
@@ -1135,6 +1146,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ BwdArgs f, int which0) {
   constexpr int W = DP / 4;
   const AttnArgs &a = f.a;
+  wait_for_predecessor();
   const int which = which0 + blockIdx.y;
   const long long ctas = which == 0 ? (long long)f.p.tiles * f.p.packs * a.B
                                     : (long long)f.p.f_tiles * a.Hkv * a.B;
@@ -1180,10 +1192,10 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
   p.packs = H / p.P;
   p.tiles = (int)((Lq * p.P + kRows - 1) / kRows);
   p.f_tiles = (int)((Lk + kRows - 1) / kRows);
-  // split a walk while CTAs leave SMs idle and each keeps two steps
+  // split a walk while CTAs leave SMs idle and each keeps three steps
   auto splits = [](long long ctas, long long steps) {
     long long s = ctas > 0 ? kSMs / ctas : 1;
-    if (s > steps / 2) s = steps / 2;
+    if (s > steps / 3) s = steps / 3;
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
   p.dq_splits = splits(B * p.packs * p.tiles, p.f_tiles);
@@ -1206,7 +1218,8 @@ template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaSt
   attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
       m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, m.dk.map, m.dv.map, f);
   if (f.p.dq_splits > 1)
-    attn_add_kernel<DT, 64><<<dim3(ctas * (kRows * 16 / 256), 1), 256, 0, stream>>>(f, 0);
+    return launch_follower(attn_add_kernel<DT, 64>, dim3(ctas * (kRows * 16 / 256), 1), 256, 0, stream,
+                           f, 0);
   return cudaGetLastError();
 }
 
@@ -1221,16 +1234,19 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   attn_dq_tc_kernel<DT, DP><<<(unsigned)(rows * f.p.dq_splits), kThreads, S::DQ_BYTES + 1024, stream>>>(
       m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, f);
-  if (f.p.dq_splits > 1)
-    attn_add_kernel<DT, DP><<<dim3((unsigned)rows * per_tile, 1), 256, 0, stream>>>(f, 0);
-  e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dkv_tc_kernel<DT, DP>),
-                        S::DKV_BYTES + 1024, kLaunchRegs);
-  if (e != cudaSuccess) return e;
-  attn_dkv_tc_kernel<DT, DP><<<(unsigned)(frames * f.p.dkv_splits), kThreads, S::DKV_BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, m.dk.map, m.dv.map, f);
-  if (f.p.dkv_splits > 1)
-    attn_add_kernel<DT, DP><<<dim3((unsigned)frames * per_tile, 2), 256, 0, stream>>>(f, 1);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e == cudaSuccess && f.p.dq_splits > 1)
+    e = launch_follower(attn_add_kernel<DT, DP>, dim3((unsigned)rows * per_tile, 1), 256, 0, stream, f, 0);
+  if (e == cudaSuccess)
+    e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dkv_tc_kernel<DT, DP>),
+                          S::DKV_BYTES + 1024, kLaunchRegs);
+  if (e == cudaSuccess)
+    e = launch_follower(attn_dkv_tc_kernel<DT, DP>, dim3((unsigned)(frames * f.p.dkv_splits)), kThreads,
+                        S::DKV_BYTES + 1024, stream, m.q.map, m.go.map, m.k.map, m.v.map, m.dk.map,
+                        m.dv.map, f);
+  if (e == cudaSuccess && f.p.dkv_splits > 1)
+    e = launch_follower(attn_add_kernel<DT, DP>, dim3((unsigned)frames * per_tile, 2), 256, 0, stream, f, 1);
+  return e;
 }
 
 }  // namespace

@@ -91,6 +91,9 @@ template <int WARPS> __device__ __forceinline__ int2 hull_of(const Hull &h) {
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
+// Few rows: a kernel that reads k and v at memory speed.
+bool attn_step_fits(const AttnArgs &a, int dtype, bool tc_fits);
+cudaError_t launch_attn_step(const AttnArgs &a, int dtype, cudaStream_t stream);
 bool attn_bwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);

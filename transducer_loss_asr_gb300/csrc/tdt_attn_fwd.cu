@@ -373,6 +373,7 @@ template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs f, int rows) {
   constexpr int W = DP / 4;
   const AttnArgs &a = f.a;
+  wait_for_predecessor();
   const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
   const int d = (threadIdx.x % W) * 4;
   const long long ctas = (long long)f.p.tiles * f.p.packs * a.B;
@@ -422,13 +423,14 @@ FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
   p.wide = rows > kRows;
   const int tile_rows = p.wide ? 2 * kRows : kRows;
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-  // split the frames while the CTAs leave SMs idle and every split keeps four tiles
+  // split the frames while the CTAs leave SMs idle and every split keeps four tiles; joining costs about
+  // as much as six tiles
   const long long ctas = B * p.packs * p.tiles, steps = (Lk + kRows - 1) / kRows;
   long long s = ctas > 0 ? (p.wide ? 1 : 2) * kSMs / ctas : 1;
   const long long most = steps / 4;
   if (s > most) s = most;
   if (s > 64) s = 64;
-  p.splits = s < 1 ? 1 : (int)s;
+  p.splits = s < 1 || steps < 10 ? 1 : (int)s;
   return p;
 }
 
@@ -449,8 +451,8 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
   if (e != cudaSuccess || f.p.splits == 1) return e;
   const int rows = S::NS * kRows;
   const long long threads = ctas * rows * (DP / 4);
-  attn_join_kernel<DT, DP><<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(f, rows);
-  return cudaGetLastError();
+  return launch_follower(attn_join_kernel<DT, DP>, dim3((unsigned)((threads + 255) / 256)), 256, 0,
+                         stream, f, rows);
 }
 
 template <int DT>

@@ -291,6 +291,27 @@ __device__ __forceinline__ void zero_tail(unsigned char *tile, int chunks, int c
   __syncwarp();
 }
 
+// A kernel that follows another one of the same call is launched while that one still runs, and waits
+// for it (all of it: no kernel here lets its successor go early) before it reads its results.
+__device__ __forceinline__ void wait_for_predecessor() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_follower(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem,
+                            cudaStream_t stream, const A &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Shared memory of a kernel, and a check that it launches with `regs` registers a thread, which
 // its register moves count on.
 cudaError_t prepare_tc_kernel(const void *kernel, size_t smem, int regs);
