@@ -79,13 +79,6 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *d
     tma_load_4d(m, dst + c * BwdShape<DP>::CHUNK, bar, c * 64, h, l, b);
 }
 
-// 32 columns of a row as float32.
-__device__ __forceinline__ void store32f(float *dst, const float (&v)[32]) {
-#pragma unroll
-  for (int k = 0; k < 8; ++k)
-    reinterpret_cast<float4 *>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-}
-
 // dot of the first `n` of N elements of two rows, n a multiple of 8; every load is in flight at once
 template <int DT, int N> __device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
   typedef typename Elem<DT>::T E;
@@ -371,7 +364,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (f.p.dq_splits == 1)
         stage32<DT>(q_tile, S::CHUNK, r, d0, v);  // every product with q is done
       else if (row < a.Lq)
-        store32f(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * kRows + r) * DP + d0, v);
+        store_columns(f.part + (((long long)split * f.p.tiles * f.p.packs * a.B + cta) * DP + d0) * kRows + r,
+                      kRows, v);
       __syncwarp();
     }
     if (f.p.dq_splits == 1) {
@@ -726,8 +720,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         stage32<DT>(out, S::CHUNK, threadIdx.x & 127, i * 32, v);
       } else if (j < a.Lk) {
         const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
-        store32f(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * kRows +
-                           (threadIdx.x & 127)) * DP + i * 32, v);
+        store_columns(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * DP + i * 32) * kRows +
+                          (threadIdx.x & 127), kRows, v);
       }
       __syncwarp();
     }
@@ -1132,7 +1126,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         tma_store_wait_read();
       }
     } else if (row < a.Lq) {
-      store32f(f.part + (((long long)split * a.Hkv * a.B + cta) * kRows + r) * DP + group * 32, v);
+      store_columns(f.part + (((long long)split * a.Hkv * a.B + cta) * DP + group * 32) * kRows + r, kRows, v);
     }
     __syncwarp();
     tc_fence_before();
@@ -1141,48 +1135,72 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   if (warp == 13) tmem_free<512>(tmem);
 }
 
-// Adds the splits of a sum in order: 4 columns a thread.  `which`: 0 dq, 1 dv, 2 dk.
+// Adds the splits of a sum for 32 rows and 32 columns, in order.  The partial sums lie column by column; the
+// results leave row by row through shared memory.  `which0` + blockIdx.y: 0 dq, 1 dv, 2 dk.
 template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ BwdArgs f, int which0) {
-  constexpr int W = DP / 4;
   const AttnArgs &a = f.a;
-  wait_for_predecessor();
-  const int which = which0 + blockIdx.y;
-  const long long ctas = which == 0 ? (long long)f.p.tiles * f.p.packs * a.B
-                                    : (long long)f.p.f_tiles * a.Hkv * a.B;
-  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
-  if (at >= ctas * kRows) return;
-  const int d = (threadIdx.x % W) * 4, r = (int)(at % kRows);
-  const long long cta = at / kRows;
-  long long to;
-  void *out;
-  if (which == 0) {
-    const long long bp = cta / f.p.tiles, b = bp / f.p.packs;
-    const int row = (int)(cta % f.p.tiles) * (kRows / f.p.P) + r / f.p.P;
-    if (row >= a.Lq) return;
-    out = a.dq;
-    to = b * a.sdq.b + row * a.sdq.l + ((int)(bp % f.p.packs) * f.p.P + r % f.p.P) * a.sdq.h;
-  } else {
-    const long long bh = cta / f.p.f_tiles;
-    const int j = (int)(cta % f.p.f_tiles) * kRows + r;
-    if (j >= a.Lk) return;
-    const Strides &s = which == 2 ? a.sdk : a.sdv;
-    out = which == 2 ? a.dk : a.dv;
-    to = bh / a.Hkv * s.b + j * s.l + bh % a.Hkv * s.h;
-  }
-  if (d >= a.D) return;
+  __shared__ float out[32][33];
+  const int which = which0 + blockIdx.y, r = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const unsigned d0 = blockIdx.x % (DP / 32) * 32, block = blockIdx.x / (DP / 32);
+  const unsigned cta = block / (kRows / 32), r0 = block % (kRows / 32) * 32;
+  const long long ctas = gridDim.x / (DP / 32) / (kRows / 32);
   const int splits = which == 0 ? f.p.dq_splits : f.p.dkv_splits;
-  const float *p = f.part + ((which == 2 ? ctas * splits : 0) + cta) * (kRows * DP) + r * DP + d;
-  float4 v = *reinterpret_cast<const float4 *>(p);
-  for (int s = 1; s < splits; ++s) {
-    const float4 w = *reinterpret_cast<const float4 *>(p + s * ctas * (kRows * DP));
-    v.x += w.x;
-    v.y += w.y;
-    v.z += w.z;
-    v.w += w.w;
+  void *to;
+  long long base;         // of the CTA's first head in the result
+  int first, count, per;  // position of row r0, positions of the tensor, rows of a position
+  long long sl, sh;
+  if (which == 0) {
+    const unsigned bp = cta / f.p.tiles;
+    first = (int)(cta % f.p.tiles) * (kRows / f.p.P) + r0 / f.p.P;
+    per = f.p.P;
+    count = a.Lq;
+    to = a.dq;
+    base = bp / f.p.packs * a.sdq.b + bp % f.p.packs * f.p.P * a.sdq.h;
+    sl = a.sdq.l;
+    sh = a.sdq.h;
+  } else {
+    const Strides &s = which == 2 ? a.sdk : a.sdv;
+    const unsigned bh = cta / f.p.f_tiles;
+    first = (int)(cta % f.p.f_tiles) * kRows + r0;
+    per = 1;
+    count = a.Lk;
+    to = which == 2 ? a.dk : a.dv;
+    base = bh / a.Hkv * s.b + bh % a.Hkv * s.h;
+    sl = s.l;
+    sh = 0;
   }
-  *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(out) + to + d) =
-      make_uint2(pack2<DT>(v.x, v.y), pack2<DT>(v.z, v.w));
+  if (first >= count) return;
+  const bool real = first + r / per < count;
+  wait_for_predecessor();
+  const float *p = f.part + (((which == 2 ? ctas * splits : 0) + cta) * DP + d0 + part) * kRows + r0 + r;
+  const long long next = ctas * (kRows * DP);
+  constexpr int U = 8;  // splits whose loads are in flight
+  float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s0 = 0; s0 < splits; s0 += U) {
+    float v[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[u][i] = real && s0 + u < splits ? p[(s0 + u) * next + i * 8 * kRows] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += v[u][i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[r][part + i * 8] = o[i];
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int rr = threadIdx.x / 4, d = threadIdx.x % 4 * 8, at = first + rr / per;
+    if (at < count && d0 + d < a.D) {
+      unsigned short *dst = static_cast<unsigned short *>(to) + base + at * sl + rr % per * sh + d0 + d;
+      const float *x = &out[rr][d];
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                                                   pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+    }
+  }
 }
 
 BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
@@ -1218,7 +1236,7 @@ template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaSt
   attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
       m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, m.dk.map, m.dv.map, f);
   if (f.p.dq_splits > 1)
-    return launch_follower(attn_add_kernel<DT, 64>, dim3(ctas * (kRows * 16 / 256), 1), 256, 0, stream,
+    return launch_follower(attn_add_kernel<DT, 64>, dim3(ctas * (kRows / 32) * 2, 1), 256, 0, stream,
                            f, 0);
   return cudaGetLastError();
 }
@@ -1228,7 +1246,7 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   typedef BwdShape<DP> S;
   const AttnArgs &a = f.a;
   const long long rows = a.B * f.p.packs * f.p.tiles, frames = a.B * a.Hkv * f.p.f_tiles;
-  const unsigned per_tile = kRows * (DP / 4) / 256;  // blocks of the adding kernel
+  const unsigned per_tile = (kRows / 32) * (DP / 32);  // blocks of the adding kernel
   cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dq_tc_kernel<DT, DP>),
                                     S::DQ_BYTES + 1024, kLaunchRegs);
   if (e != cudaSuccess) return e;

@@ -27,6 +27,7 @@ namespace tdt {
 namespace {
 
 constexpr int kRows = 128;          // rows of a tile, frames of a tile
+constexpr int kMostSplits = 64;
 constexpr float kLazy = 8.0f;
 // float16 weights start at 2^7 and so stay clear of the type's least numbers; at most 2^15
 template <int DT> constexpr float kShift = DT == kF16 ? 7.0f : 0.0f;
@@ -318,12 +319,11 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     tc_fence_after();
     if (!alive) l = 0.0f;
     const bool bad = n.bad || !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
-    const long long part = ((long long)split * f.p.tiles * f.p.packs * a.B + cta) * (S::NS * kRows) +
-                           threadIdx.x;
+    const long long tile_at = (long long)split * f.p.tiles * f.p.packs * a.B + cta;  // of a partial result
     if (row < a.Lq) {
       const float total = bad ? NAN : l == 0.0f ? -INFINITY : ref + log2f(l);
       if (f.p.splits > 1)
-        f.part_l[part] = total;
+        f.part_l[tile_at * (S::NS * kRows) + threadIdx.x] = total;
       else if (a.lse)
         a.lse[(b * a.H + head) * a.Lq + row] = total * kLn2;
     }
@@ -343,10 +343,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
       if (f.p.splits == 1) {
         stage32<DT>(out_tile, S::CHUNK, r, i * 32, v);
       } else if (row < a.Lq) {
-        float4 *dst = reinterpret_cast<float4 *>(f.part_o + part * DP + i * 32);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+        store_columns(f.part_o + (tile_at * DP + i * 32) * (S::NS * kRows) + threadIdx.x, S::NS * kRows, v);
       }
       __syncwarp();
     }
@@ -367,52 +364,76 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
   if (warp == kAux + 1) tmem_free<S::TMEM>(tmem);
 }
 
-// Joins the splits of a row: o = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s).  DP / 4 threads a
-// row, the splits in order.
+// Joins the splits for 32 rows and 32 columns: o = sum_s 2^(l_s - l) o_s, l = log2 sum_s 2^(l_s), the
+// splits in order.  The partial results lie column by column; they leave row by row through shared memory.
+// Blocks are small and every split's loads go out together: the kernel's time is a few memory latencies.
 template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs f, int rows) {
-  constexpr int W = DP / 4;
   const AttnArgs &a = f.a;
+  __shared__ float out[32][33], weight[kMostSplits][32];
+  const unsigned d0 = blockIdx.x % (DP / 32) * 32, block = blockIdx.x / (DP / 32);
+  const int groups = rows / 32, r = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const unsigned cta = block / groups, r0 = block % groups * 32;
+  const unsigned ctas = gridDim.x / (DP / 32) / groups;
+  const int tile = cta % f.p.tiles, pack = cta / f.p.tiles % f.p.packs;
+  const long long b = cta / f.p.tiles / f.p.packs;
+  const int first = tile * (rows / f.p.P) + r0 / f.p.P;  // position of row r0; P divides 32 or 32 divides it
+  auto row_of = [&](int x) { return first + (int)((r0 % f.p.P + x) / f.p.P); };
+  auto head_of = [&](int x) { return pack * f.p.P + (int)((r0 + x) % f.p.P); };
+  if (first >= a.Lq) return;
+  const bool real = row_of(r) < a.Lq;
+  const int splits = f.p.splits;
   wait_for_predecessor();
-  const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / W;
-  const int d = (threadIdx.x % W) * 4;
-  const long long ctas = (long long)f.p.tiles * f.p.packs * a.B;
-  if (at >= ctas * rows) return;
-  const long long cta = at / rows;
-  const int r = (int)(at % rows), tile = (int)(cta % f.p.tiles);
-  const long long bp = cta / f.p.tiles, b = bp / f.p.packs;
-  const int row = (int)(((long long)tile * rows + r) / f.p.P);
-  const int head = (int)(bp % f.p.packs) * f.p.P + r % f.p.P;
-  if (row >= a.Lq) return;
-  float top = -INFINITY;
+  for (int s = part; s < splits; s += 8)
+    weight[s][r] = real ? f.part_l[((long long)s * ctas + cta) * rows + r0 + r] : -INFINITY;
+  const float *po = f.part_o + ((long long)cta * DP + d0 + part) * rows + r0 + r;
+  const long long next = (long long)ctas * DP * rows;
+  constexpr int U = 8;  // splits whose loads are in flight
+  float v[U][4];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[u][i] = real && s0 + u < splits ? po[(s0 + u) * next + i * 8 * rows] : 0.0f;
+  };
+  load(0);
+  __syncthreads();
+  float top = -INFINITY, sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   bool bad = false;
-  for (int s = 0; s < f.p.splits; ++s) {
-    const float x = f.part_l[(s * ctas + cta) * rows + r];
+  for (int s = 0; s < splits; ++s) {
+    const float x = weight[s][r];
     bad |= x != x;
     top = fmaxf(top, x);
   }
-  float sum = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (top > -INFINITY)
-    for (int s = 0; s < f.p.splits; ++s) {
-      const float x = f.part_l[(s * ctas + cta) * rows + r];
-      if (x == -INFINITY) continue;
-      const float w = fast_exp2(x - top);
-      const float4 v = *reinterpret_cast<const float4 *>(f.part_o + ((s * ctas + cta) * rows + r) * DP + d);
-      sum += w;
-      o[0] += w * v.x;
-      o[1] += w * v.y;
-      o[2] += w * v.z;
-      o[3] += w * v.w;
-    }
-  const float inv = bad ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
-  if (d < a.D) {
-    unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
-                          row * a.so.l + head * a.so.h + d;
-    *reinterpret_cast<uint2 *>(dst) =
-        make_uint2(pack2<DT>(o[0] * inv, o[1] * inv), pack2<DT>(o[2] * inv, o[3] * inv));
+  for (int s0 = 0; s0 < splits; s0 += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (s0 + u < splits && top > -INFINITY) {
+        const float w = fast_exp2(weight[s0 + u][r] - top);
+        sum += w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = fmaf(w, v[u][i], o[i]);
+      }
+    if (s0 + U < splits) load(s0 + U);
   }
-  if (d == 0 && a.lse)
-    a.lse[(b * a.H + head) * a.Lq + row] = bad ? NAN : sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  const float inv = bad ? NAN : sum > 0.0f ? 1.0f / sum : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[r][part + i * 8] = bad ? NAN : o[i] * inv;
+  if (part == 0 && d0 == 0 && real && a.lse)
+    a.lse[(b * a.H + head_of(r)) * a.Lq + row_of(r)] =
+        bad ? NAN : sum > 0.0f ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int rr = threadIdx.x / 4, d = threadIdx.x % 4 * 8;
+    if (row_of(rr) < a.Lq && d0 + d < a.D) {
+      unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
+                            row_of(rr) * a.so.l + head_of(rr) * a.so.h + d0 + d;
+      const float *x = &out[rr][d];
+      *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
+                                                   pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
+    }
+  }
 }
 
 FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
@@ -423,14 +444,13 @@ FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
   p.wide = rows > kRows;
   const int tile_rows = p.wide ? 2 * kRows : kRows;
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-  // split the frames while the CTAs leave SMs idle and every split keeps four tiles; joining costs about
-  // as much as six tiles
+  // split the frames while the CTAs leave SMs idle, if that saves a CTA a dozen tiles: joining costs
+  // about as much time as eight
   const long long ctas = B * p.packs * p.tiles, steps = (Lk + kRows - 1) / kRows;
   long long s = ctas > 0 ? (p.wide ? 1 : 2) * kSMs / ctas : 1;
-  const long long most = steps / 4;
-  if (s > most) s = most;
-  if (s > 64) s = 64;
-  p.splits = s < 1 || steps < 10 ? 1 : (int)s;
+  if (s > steps / 4) s = steps / 4;
+  if (s > kMostSplits) s = kMostSplits;
+  p.splits = s < 2 || steps - steps / s < 12 ? 1 : (int)s;
   return p;
 }
 
@@ -450,8 +470,7 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
   e = cudaGetLastError();
   if (e != cudaSuccess || f.p.splits == 1) return e;
   const int rows = S::NS * kRows;
-  const long long threads = ctas * rows * (DP / 4);
-  return launch_follower(attn_join_kernel<DT, DP>, dim3((unsigned)((threads + 255) / 256)), 256, 0,
+  return launch_follower(attn_join_kernel<DT, DP>, dim3((unsigned)(ctas * (rows / 32) * (DP / 32))), 256, 0,
                          stream, f, rows);
 }
 

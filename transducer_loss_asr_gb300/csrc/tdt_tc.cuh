@@ -280,6 +280,13 @@ __device__ __forceinline__ void stage32(unsigned char *tile, int chunk_bytes, in
                    pack2<DT>(v[8 * k + 4], v[8 * k + 5]), pack2<DT>(v[8 * k + 6], v[8 * k + 7]));
 }
 
+// 32 columns of a row as float32 into a partial result that lies column by column: neighbouring threads
+// hold neighbouring rows.
+__device__ __forceinline__ void store_columns(float *part, long long rows, const float (&v)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) part[k * rows] = v[k];
+}
+
 // Zeroes rows [first, rows) of a tile in shared memory (a warp), for the tensor cores to read.
 __device__ __forceinline__ void zero_tail(unsigned char *tile, int chunks, int chunk_bytes,
                                           int first, int rows) {
