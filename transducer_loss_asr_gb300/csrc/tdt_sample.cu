@@ -11,17 +11,20 @@
 // scanned by one warp for the digit at which the count reaches top_k, or the
 // weight reaches the share top_p of what top_k leaves.
 //
-// One CTA a row.  Every warp owns a contiguous range of the row, so sums by
-// warp are running sums of the vocabulary's order.
-//   pass 1  the maximum X;
-//   pass 2  the weights: sums by warp, and the tokens with z >= -12 into a
-//           list in shared memory (each warp its own part, in index order).
-// The cut usually lies among the listed tokens -- top_k of them exist, or
-// their weight reaches top_p's share of all, or min_p is above 2^-12 -- and
-// then selection and draw read the list only.  Otherwise they read the row
-// again (it is in L2 by then).
+// One CTA a row.  Every warp owns a contiguous range of the row, so sums by warp are running sums of the
+// vocabulary's order.
+//   pass 1  the maximum X; rows of up to 16,384 tokens stay in shared memory, as float32;
+//   pass 2  the sum of all weights, if the settings need it, and the tokens with z >= -12 (overflowing:
+//           -6, -3) into a list in shared memory, each warp its own part, in index order.
+// The cut usually lies among the listed tokens -- top_k of them exist, or their weight reaches top_p's
+// share of all, or min_p is above any unlisted weight -- and then selection and draw read the list only.
+// Otherwise they read the row again (from L2, where it does not stay).
+// Pass 2 is what bounds wide rows: its weights are below 2^-9 of the largest, apart from the listed ones,
+// and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no conversion, and
+// 32-bit sums.  Two tokens an instruction where the hardware has it.
 #include "../../include/tdt_decoder.h"
 #include "tdt_rowio.cuh"
+#include "tdt_tc.cuh"
 
 namespace tdt {
 namespace {
@@ -29,7 +32,9 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kListTokens = 4096;      // entries of the list, 8 bytes each
-constexpr float kListZ = 12.0f;        // z >= -kListZ goes into the list
+constexpr int kResident = 16384;       // tokens of a row that stays in shared memory
+constexpr int kListZ = 12;             // z >= -kListZ goes into the list; if that overflows, half of it, ...
+constexpr int kListTries = 3;
 constexpr float kZeroZ = 33.0f;        // z < -32 weighs 0
 
 struct SampleArgs {
@@ -96,8 +101,8 @@ struct Held {
 template <int NW> struct Shared {
   float xs[kListTokens];
   int ids[kListTokens];
-  unsigned cnt[256];
-  u64 mass[256];
+  // of a digit: tokens, and their weight in three parts (over 2^48 + hi 2^16 + lo)
+  unsigned cnt[256], lo[256], hi[256], over[256];
   Held held[NW];
   int listed[NW];
   float red[NW];
@@ -106,6 +111,7 @@ template <int NW> struct Shared {
   u64 above_cnt, above_mass, target;
   int winner, token;
   unsigned ties_left;
+  __align__(16) float row[4];  // the row itself, if it is resident
 };
 
 // The prefix that stays: keys above `key`, and the first `ties` tokens with that key.
@@ -115,7 +121,7 @@ struct Cut {
   u64 mass;  // its weight
 };
 
-template <int DT, int NW> struct Sampler {
+template <int DT, int NW, bool RESIDENT> struct Sampler {
   typedef typename Elem<DT>::T E;
   static constexpr int VEC = Vec<DT>::N;
   static constexpr int CAP = kListTokens / NW;  // list entries of a warp
@@ -135,24 +141,76 @@ template <int DT, int NW> struct Sampler {
     chunk = (vectors + NW - 1) / NW * VEC;
   }
 
-  // f(index, x) for the warp's range, VEC consecutive tokens a lane; 32 * VEC consecutive
-  // ones a step.  Every lane takes every step; tokens outside the row come as -inf.
-  template <typename F> __device__ __forceinline__ void each_vector(F f) const {
+  // f(index, x) for the warp's range, VEC consecutive tokens a lane; 32 * VEC consecutive ones a step.
+  // Every lane takes every step; tokens outside the row and NaN come as -inf.  `from_memory`: not from
+  // the resident copy.  Steps come in pairs, so that two loads are in flight.
+  template <typename F> __device__ __forceinline__ void each_vector(F f, bool from_memory = false) const {
     const int end = min(chunk * (warp + 1), V + head);
-    for (int p = chunk * warp + lane * VEC; p - lane * VEC < end; p += 32 * VEC) {
-      float x[VEC];
-      const int i = p - head;
-      if (i >= 0 && i + VEC <= V && p < end) {
-        const uint4 raw = __ldg(reinterpret_cast<const uint4 *>(row + i));
-        const E *e = reinterpret_cast<const E *>(&raw);
+    const int p0 = chunk * warp + lane * VEC, steps = (end - chunk * warp + 32 * VEC - 1) / (32 * VEC);
+    if (RESIDENT && !from_memory) {
+      for (int t = 0; t < steps; ++t) {
+        const int p = p0 + t * 32 * VEC;
+        float x[VEC];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) x[j] = Elem<DT>::to_float(e[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          x[j] = (i + j >= 0 && i + j < V && p < end) ? Elem<DT>::load(row + i + j) : -INFINITY;
+        for (int j = 0; j < VEC; j += 4) {
+          const float4 v = p < end ? *reinterpret_cast<const float4 *>(s.row + p + j)
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          x[j] = v.x;
+          x[j + 1] = v.y;
+          x[j + 2] = v.z;
+          x[j + 3] = v.w;
+        }
+        f(p - head, x);
       }
-      f(i, x);
+      return;
+    }
+    constexpr int U = 4;
+    for (int t = 0; t < steps; t += U) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = p0 + (t + u) * 32 * VEC, i = p - head;
+        if (i >= 0 && i + VEC <= V && p < end) {
+          raw[u] = __ldg(reinterpret_cast<const uint4 *>(row + i));
+        } else {
+          E *e = reinterpret_cast<E *>(&raw[u]);
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            e[j] = (i + j >= 0 && i + j < V && p < end) ? row[i + j] : Elem<DT>::from_float(-INFINITY);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (t + u >= steps) break;
+        float x[VEC];
+        unpack(raw[u], x);
+        f(p0 + (t + u) * 32 * VEC - head, x);
+      }
+    }
+  }
+  // VEC tokens as float32, NaN as -inf
+  static __device__ __forceinline__ void unpack(uint4 raw, float (&x)[VEC]) {
+    unsigned v[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (DT == kF32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = fmaxf(__uint_as_float(v[j]), -INFINITY);
+    } else if constexpr (DT == kBF16) {
+      const __nv_bfloat162 low = __floats2bfloat162_rn(-INFINITY, -INFINITY);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 c = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&v[j]), low);
+        const unsigned b = *reinterpret_cast<const unsigned *>(&c);
+        x[2 * j] = __uint_as_float(b << 16);
+        x[2 * j + 1] = __uint_as_float(b & 0xffff0000u);
+      }
+    } else {
+      const __half2 low = __floats2half2_rn(-INFINITY, -INFINITY);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 c = __half22float2(__hmax2(*reinterpret_cast<__half2 *>(&v[j]), low));
+        x[2 * j] = c.x;
+        x[2 * j + 1] = c.y;
+      }
     }
   }
   // f(x) for every token of this thread's share of the warp's tokens: the list's or the row's.
@@ -166,13 +224,24 @@ template <int DT, int NW> struct Sampler {
       });
     }
   }
+  // Token i of the row, NaN as -inf.
+  __device__ __forceinline__ float token(int i) const {
+    return RESIDENT ? s.row[i + head] : fmaxf(Elem<DT>::load(row + i), -INFINITY);
+  }
 
-  __device__ float maximum() const {
+  __device__ float maximum() {
     float m = -INFINITY;
-    each_vector([&](int, const float *x) {
+    each_vector(
+        [&](int i, const float *x) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) m = fmaxf(m, x[j]);  // fmaxf passes over NaN
-    });
+          for (int j = 0; j < VEC; ++j) m = fmaxf(m, x[j]);
+          // the resident copy; a thread reads back what it wrote, others only after a barrier
+          if (RESIDENT && i < V && i + head < chunk * (warp + 1))
+#pragma unroll
+            for (int j = 0; j < VEC; j += 4)
+              *reinterpret_cast<float4 *>(s.row + i + head + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        },
+        true);
     m = warp_max(m);
     if (lane == 0) s.red[warp] = m;
     __syncthreads();
@@ -181,45 +250,74 @@ template <int DT, int NW> struct Sampler {
     return m;
   }
 
-  // Pass 2: the sum of all weights, by warp into held[].mass; with `want`, the list of tokens
-  // with keys of at least `from`.  Returns the number of listed tokens, -1 if they do not fit.
-  __device__ int weigh(bool want, unsigned from) {
+  // Pass 2.  MASS: the sum of the weights, by warp into held[].mass: of all tokens, or with LIST of those
+  // below `near`.  LIST: the tokens from `near` up into the list.  Returns the number of listed tokens, -1
+  // if they do not fit.
+  template <bool MASS, bool LIST> __device__ int weigh(float near) {
     u64 mass = 0;
     int n = 0;
     bool fits = true;
+    const float2 x2 = make_float2(-w.X, -w.X), per2 = make_float2(w.per, w.per);
+    // z < -9 for tokens below `near`: reading a weight off the sum is exact (see the head of the file)
+    const bool small = !w.infinite && (near - w.X) * w.per < -9.5f;
+    constexpr float kMagic = 1.5f / 256.0f;
     each_vector([&](int i, const float *x) {
-      unsigned in = 0;
+      if (MASS && small) {
+        unsigned sum = 0;
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        mass += w(x[j]);
-        in |= (order_key(x[j]) >= from ? 1u : 0u) << j;
-      }
-      if (!want || !__any_sync(0xffffffffu, in != 0)) return;
-      // place of this lane's first token: the tokens of lower lanes come before it
-      int before = __popc(in);
+        for (int j = 0; j < VEC; j += 2) {
+          const float2 z = mul2(add2(make_float2(x[j], x[j + 1]), x2), per2);
+          const float2 m = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(kMagic, kMagic));
+          if (!(x[j] >= near)) sum += __float_as_uint(m.x) - __float_as_uint(kMagic);
+          if (!(x[j + 1] >= near)) sum += __float_as_uint(m.y) - __float_as_uint(kMagic);
+        }
+        mass += sum;
+        if (!LIST) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, before, o);
-        if (lane >= o) before += t;
-      }
-      const int all = __shfl_sync(0xffffffffu, before, 31);
-      int at = n + before - __popc(in);
-      if (n + all > CAP) fits = false;
-      if (fits) {
+          for (int j = 0; j < VEC; ++j)
+            if (x[j] >= near) mass += w(x[j]);
+        }
+      } else if (MASS) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-          if (in >> j & 1) {
-            s.xs[warp * CAP + at] = x[j];
-            s.ids[warp * CAP + at] = i + j;
-            ++at;
-          }
-        n += all;
+          if (!LIST || !(x[j] >= near)) mass += w(x[j]);
+      }
+      if (LIST) {
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j < VEC; ++j) top = fmaxf(top, x[j]);
+        if (!__any_sync(0xffffffffu, top >= near)) return;
+        unsigned in = 0;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) in |= (x[j] >= near ? 1u : 0u) << j;
+        // place of this lane's first token: the tokens of lower lanes come before it
+        int before = __popc(in);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int t = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += t;
+        }
+        const int all = __shfl_sync(0xffffffffu, before, 31);
+        int at = n + before - __popc(in);
+        if (n + all > CAP) fits = false;
+        if (fits) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j)
+            if (in >> j & 1) {
+              s.xs[warp * CAP + at] = x[j];
+              s.ids[warp * CAP + at] = i + j;
+              ++at;
+            }
+          n += all;
+        }
       }
     });
-    mass = warp_sum64(mass);
+    if (MASS) mass = warp_sum64(mass);
     if (lane == 0) {
-      s.held[warp].mass = mass;
-      s.held[warp].ties = 0;
+      if (MASS) {
+        s.held[warp].mass = mass;
+        s.held[warp].ties = 0;
+      }
       s.listed[warp] = n;
     }
     const int bad = __syncthreads_or(!fits);
@@ -230,8 +328,21 @@ template <int DT, int NW> struct Sampler {
     return total;
   }
 
+  // Sum over all threads, known to all; a barrier before and after its use of held[].
+  __device__ u64 total_of(u64 v) {
+    v = warp_sum64(v);
+    __syncthreads();
+    if (lane == 0) s.held[warp].mass = v;
+    __syncthreads();
+    return total_mass();
+  }
+
   __device__ u64 total_mass() const {
     return warp_sum64(lane < NW ? s.held[lane].mass : 0ull);
+  }
+
+  __device__ __forceinline__ u64 mass_of(int digit) const {
+    return ((u64)s.over[digit] << 48) + ((u64)s.hi[digit] << 16) + s.lo[digit];
   }
 
   // Radix selection over the keys in [from, top]: the token at which, in falling order, the
@@ -245,15 +356,22 @@ template <int DT, int NW> struct Sampler {
       const unsigned digits = 1u << (bits - shift);  // at most 256
       for (int i = threadIdx.x; i < 256; i += NW * 32) {
         s.cnt[i] = 0;
-        s.mass[i] = 0;
+        s.lo[i] = 0;
+        s.hi[i] = 0;
+        s.over[i] = 0;
       }
       __syncthreads();
       each([&](float x) {
         const unsigned k = order_key(x);
         if (k >= lo && ((k - lo) >> shift) < digits) {
-          const unsigned d = (k - lo) >> shift;
+          // a weight goes in as two halves of 16 bits, with native 32-bit adds; what a part overflows
+          // is carried into the next one
+          const unsigned d = (k - lo) >> shift, v = w(x), half = v & 0xffffu;
           atomicAdd(&s.cnt[d], 1u);
-          atomicAdd(&s.mass[d], (u64)w(x));
+          const unsigned old = atomicAdd(&s.lo[d], half);
+          const unsigned up = (v >> 16) + (old + half < old ? 0x10000u : 0u);
+          const unsigned old_hi = atomicAdd(&s.hi[d], up);
+          if (old_hi + up < old_hi) atomicAdd(&s.over[d], 1u);
         }
       });
       __syncthreads();
@@ -262,16 +380,16 @@ template <int DT, int NW> struct Sampler {
         u64 c = 0, m = 0;
         for (int i = 0; i < 8; ++i) {
           c += s.cnt[255 - lane * 8 - i];
-          m += s.mass[255 - lane * 8 - i];
+          m += mass_of(255 - lane * 8 - i);
         }
         u64 bc = above_cnt + warp_before64(c), bm = above_mass + warp_before64(m);
         const u64 at = by_count ? bc : bm, step = by_count ? c : m;
         if (at < target && at + step >= target) {
           int d = 255 - lane * 8;
           for (; d > 255 - lane * 8 - 7; --d) {
-            if ((by_count ? bc + s.cnt[d] : bm + s.mass[d]) >= target) break;
+            if ((by_count ? bc + s.cnt[d] : bm + mass_of(d)) >= target) break;
             bc += s.cnt[d];
-            bm += s.mass[d];
+            bm += mass_of(d);
           }
           s.digit = d;
           s.above_cnt = bc;
@@ -394,13 +512,13 @@ template <int DT, int NW> struct Sampler {
     }
     // the row: the winner's range is split over the warps again, until it is short
     int a = max(0, chunk * winner - head), b = min(chunk * (winner + 1) - head, V);
-    while (b - a > 32 * NW) {
+    while (b - a > 128) {
       __syncthreads();
       const int piece = (b - a + NW - 1) / NW, p0 = a + piece * warp, p1 = min(b, p0 + piece);
       u64 mass = 0;
       unsigned ties = 0;
       for (int i = p0 + lane; i < p1; i += 32) {
-        const float x = Elem<DT>::load(row + i);
+        const float x = token(i);
         if (above(x, c, m)) mass += w(x);
         ties += order_key(x) == c.key ? 1u : 0u;
       }
@@ -412,7 +530,7 @@ template <int DT, int NW> struct Sampler {
       for (int i0 = a; i0 < b; i0 += 32) {
         const int i = i0 + lane;
         const bool valid = i < b;
-        const float x = valid ? Elem<DT>::load(row + i) : -INFINITY;
+        const float x = valid ? token(i) : -INFINITY;
         const int hit = step(x, valid, c, m, tie_weight, &target, &left);
         if (hit < 32) {
           if (lane == hit) s.token = i;
@@ -425,7 +543,7 @@ template <int DT, int NW> struct Sampler {
   }
 };
 
-template <int DT, int NW>
+template <int DT, int NW, bool RESIDENT>
 __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   typedef typename Elem<DT>::T E;
   extern __shared__ __align__(16) unsigned char raw[];
@@ -436,7 +554,7 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   const float p = a.top_ps ? a.top_ps[n] : a.top_p;
   const float mp = a.min_ps ? a.min_ps[n] : a.min_p;
   int k = a.top_ks ? a.top_ks[n] : a.top_k;
-  Sampler<DT, NW> r(s, row, a.V);
+  Sampler<DT, NW, RESIDENT> r(s, row, a.V);
   const float X = r.maximum();
   const bool usable = T >= 0.0f && T < INFINITY && p >= 0.0f && p <= 1.0f && mp >= 0.0f &&
                       mp <= 1.0f && k >= 0 && X > -INFINITY;
@@ -456,61 +574,82 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   const unsigned m = __float2uint_ru(mp * 2147483648.0f);
   const unsigned u24 = (unsigned)min(max(__float2int_rd(a.u[n] * 16777216.0f), 0), 16777215);
   const bool by_p = p24 < (1u << 24), filters = k > 0 || by_p || m > 0;
-  const float reach = T == 0.0f ? 0.0f : kListZ / r.w.per, far = T == 0.0f ? 0.0f : kZeroZ / r.w.per;
-  const unsigned top = order_key(X), near = order_key(X - (r.w.infinite ? 0.0f : reach));
-  const int listed = r.weigh(filters, near);
-  const u64 all = r.total_mass();
+  const bool need_all = by_p && k == 0;  // top-p's share is of the weight of every token
+  const unsigned top = order_key(X);
+  // the value at -z below the maximum, as a key's value
+  auto below = [&](float z) {
+    return T == 0.0f || r.w.infinite ? X : key_value(order_key(X - z / r.w.per));
+  };
   Cut cut;
   u64 kept;
   bool sums_ready = false;
   if (!filters) {
+    r.template weigh<true, false>(below((float)kListZ));
     cut.key = 0;
     cut.ties = 0;
-    kept = all;
+    kept = r.total_mass();
     sums_ready = true;  // held[] is the sums by warp of every token
   } else {
-    // does the cut lie among the listed tokens?
-    const unsigned low = 0x80000000u >> 11;  // weight that no unlisted token reaches
+    int listed = -1, z = kListZ;
+    u64 all = 0;
+    float near = 0.0f;
+    for (int i = 0; i < kListTries && listed < 0; ++i) {
+      z = kListZ >> i;
+      near = below((float)z);
+      listed = need_all && i == 0 ? r.template weigh<true, true>(near) : r.template weigh<false, true>(near);
+      if (need_all && i == 0) {
+        all = r.total_mass();  // of the tokens below the first `near`
+        if (listed < 0) {      // the rest was not kept: sum it from the row
+          u64 mass = 0;
+          r.each([&](float x) { mass += x >= near ? (u64)r.w(x) : 0ull; });
+          all += r.total_of(mass);
+        }
+      }
+    }
     u64 listed_mass = 0;
     if (listed >= 0) {
       u64 mass = 0;
       r.listed = true;
       r.each([&](float x) { mass += r.w(x); });
-      __syncthreads();
-      mass = warp_sum64(mass);
-      if (r.lane == 0) s.held[r.warp].mass = mass;
-      __syncthreads();
-      listed_mass = r.total_mass();
+      listed_mass = r.total_of(mass);
+      if (need_all && z == kListZ) all += listed_mass;
     }
+    // does the cut lie among the listed tokens?
+    const unsigned low = (0x80000000u >> z) + (0x80000000u >> (z + 8));  // above any unlisted weight
     const bool enough = listed > 0 && (k > 0   ? listed >= k || (!by_p && m >= low)
                                        : by_p ? listed_mass >= share(all, p24)
                                               : m >= low);
     r.listed = enough;
-    const unsigned from = enough ? near : order_key(X - (r.w.infinite ? 0.0f : far));
+    const unsigned from = order_key(enough ? near : below(kZeroZ));
     // top-k, unless fewer tokens than that weigh anything
     cut.key = from;  // everything from `from` up
     cut.ties = 0xffffffffu;
-    cut.mass = enough ? listed_mass : all;
     bool cut_by_k = false;
     if (k > 0) {
-      u64 have = (u64)listed;
+      u64 have = (u64)max(listed, 0);
       if (!enough) {
-        unsigned c = 0;
+        u64 c = 0;
         r.each([&](float x) { c += order_key(x) >= from ? 1u : 0u; });
-        __syncthreads();
-        u64 c64 = warp_sum64(c);
-        if (r.lane == 0) s.held[r.warp].mass = c64;
-        __syncthreads();
-        have = r.total_mass();
+        have = r.total_of(c);
       }
       if (have >= (u64)k) {
         cut = r.select(true, (u64)k, from, top);
         cut_by_k = true;
       }
     }
+    if (!cut_by_k) {  // the weight of everything from `from` up
+      if (enough) {
+        cut.mass = listed_mass;
+      } else if (need_all) {
+        cut.mass = all;
+      } else {
+        u64 mass = 0;
+        r.each([&](float x) { mass += r.w(x); });
+        cut.mass = r.total_of(mass);
+      }
+    }
     if (by_p) {
-      const u64 base = cut_by_k || !enough ? cut.mass : all;
-      const u64 need = share(base, p24);
+      const u64 need = share(need_all ? all : cut.mass, p24);
       cut = r.select(false, need > 0 ? need : 1, from, top);
     }
     kept = cut.mass;
@@ -544,22 +683,28 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   if (threadIdx.x == 0) {
     a.tokens[n] = token;
     if (a.logprobs) {
-      const float x = Elem<DT>::to_float(row[token < 0 ? 0 : token]);
+      const float x = r.token(token < 0 ? 0 : token);
       const float z = r.w.infinite || T == 0.0f ? 0.0f : __fmul_rn(__fsub_rn(x, X), r.w.per);
       a.logprobs[n] = token < 0 ? NAN : (z - log2f((float)kept * (1.0f / 2147483648.0f))) * 0.69314718055994531f;
     }
   }
 }
 
-template <int DT, int NW> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      sample_kernel<DT, NW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Shared<NW>));
+template <int DT, int NW, bool RESIDENT>
+cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
+  // a resident row starts at its first vector's place and is filled up to whole vectors
+  const size_t smem = sizeof(Shared<NW>) + (RESIDENT ? (size_t)(a.V + 16) * 4 : 0);
+  const cudaError_t e = cudaFuncSetAttribute(sample_kernel<DT, NW, RESIDENT>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  sample_kernel<DT, NW><<<(unsigned)N, NW * 32, sizeof(Shared<NW>), s>>>(a);
+  sample_kernel<DT, NW, RESIDENT><<<(unsigned)N, NW * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
 template <int DT> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
-  return a.V <= 2048 ? launch<DT, 4>(a, N, s) : launch<DT, 16>(a, N, s);
+  if (a.V <= 2048) return launch<DT, 4, true>(a, N, s);
+  if (a.V <= kResident)
+    return N > 2 * 152 ? launch<DT, 8, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
+  return N > 2 * 152 ? launch<DT, 8, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
 }
 
 }  // namespace
