@@ -1,27 +1,27 @@
-// tdt_sample.cu -- draws a token of each row of logits (include/tdt_decoder.h,
-// tdt_sample): temperature, top-k, top-p, min-p, then the inverse of the
-// running sum at a given uniform number.
+// tdt_sample.cu -- draws a token of each row of logits (include/tdt_decoder.h, tdt_sample): temperature,
+// top-k, top-p, min-p, then the inverse of the running sum at a given uniform number.
 //
-// Mathematics.  Weights are whole numbers, w = rint(2^31 * 2^z) with
-// z = (x - X) * (log2(e) / T) and X the row's maximum, so sums of weights are
-// exact whatever their order, and every filter keeps a prefix of the order
-// (x falling, index rising): the kept set is "order key above a cut, and the
-// first c tokens equal to it".  The cut is found by radix selection: the keys
-// in 8-bit digits from the top, each digit's histogram of counts and weights
-// scanned by one warp for the digit at which the count reaches top_k, or the
-// weight reaches the share top_p of what top_k leaves.
+// Mathematics.  Weights are whole numbers, w = rint(2^31 * 2^z) with z = (x - X) * (log2(e) / T) and X the
+// row's maximum, so sums of weights are exact whatever their order, and every filter keeps a prefix of the
+// order (x falling, index rising): the kept set is "order key above a cut, and the first c tokens equal to
+// it".  The cut is found by radix selection: a histogram of counts and weights over 256 stretches of the
+// keys in question tells the stretch at which the count reaches top_k, or the weight the share top_p of
+// what top_k leaves; the tokens of that stretch are ranked by one warp (more than 32 of them: further
+// histograms).  Both cuts use the same first histogram.
 //
 // One CTA a row.  Every warp owns a contiguous range of the row, so sums by warp are running sums of the
 // vocabulary's order.
 //   pass 1  the maximum X; rows of up to 16,384 tokens stay in shared memory, as float32;
-//   pass 2  the sum of all weights, if the settings need it, and the tokens with z >= -12 (overflowing:
-//           -6, -3) into a list in shared memory, each warp its own part, in index order.
+//   pass 2  the sum of all weights, if the settings need it, and the places of vectors with a token of
+//           z >= -12 (overflowing: -6, -3); their tokens then go into a list in shared memory, each warp
+//           its own part, in index order.  Rows of up to 1,024 tokens need no list.
 // The cut usually lies among the listed tokens -- top_k of them exist, or their weight reaches top_p's
 // share of all, or min_p is above any unlisted weight -- and then selection and draw read the list only.
 // Otherwise they read the row again (from L2, where it does not stay).
-// Pass 2 is what bounds wide rows: its weights are below 2^-9 of the largest, apart from the listed ones,
-// and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no conversion, and
-// 32-bit sums.  Two tokens an instruction where the hardware has it.
+// Wide rows are bound by pass 2's instructions.  Its weights are below 2^-9 of the largest, apart from the
+// listed ones, and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no
+// conversion, and whole-number sums of those bits; what the listed tokens contribute is taken out when
+// they are listed.  Two tokens an instruction where the hardware has it.
 #include "../../include/tdt_decoder.h"
 #include "tdt_rowio.cuh"
 #include "tdt_tc.cuh"
@@ -31,11 +31,13 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kListTokens = 4096;      // entries of the list, 8 bytes each
+constexpr int kListTokens = 4096;      // entries of the list
 constexpr int kResident = 16384;       // tokens of a row that stays in shared memory
+constexpr int kOwnList = 1024;         // tokens of a row that needs no list
 constexpr int kListZ = 12;             // z >= -kListZ goes into the list; if that overflows, half of it, ...
 constexpr int kListTries = 3;
 constexpr float kZeroZ = 33.0f;        // z < -32 weighs 0
+constexpr float kMagic = 1.5f / 256.0f;
 
 struct SampleArgs {
   const void *logits;
@@ -49,15 +51,20 @@ struct SampleArgs {
   float *logprobs;
 };
 
-// Order of the floats as unsigned numbers; -0 counts as 0, NaN sorts below everything.
-__device__ __forceinline__ unsigned order_key(float x) {
-  const unsigned b = __float_as_uint(x + 0.0f);
-  if (x != x) return 0;
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
-}
-__device__ __forceinline__ float key_value(unsigned k) {
-  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
-}
+// Order of the floats as unsigned numbers; -0 counts as 0, NaN sorts below everything.  Of the 16-bit
+// types the float32 bits that are always zero are left out.
+template <int DT> struct Key {
+  static constexpr int SHIFT = DT == kF32 ? 0 : DT == kF16 ? 13 : 16;
+  static __device__ __forceinline__ unsigned of(float x) {
+    const unsigned b = __float_as_uint(x + 0.0f);
+    if (x != x) return 0;
+    return ((b & 0x80000000u) ? ~b : b | 0x80000000u) >> SHIFT;
+  }
+  static __device__ __forceinline__ float value(unsigned k) {  // of a key of the type
+    k <<= SHIFT;
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~(k | ((1u << SHIFT) - 1)));
+  }
+};
 
 struct Weigher {
   float X, per;   // row maximum, log2(e) / T
@@ -67,6 +74,11 @@ struct Weigher {
     if (infinite) return x == X ? 0x80000000u : 0u;
     const float z = fmaxf(__fmul_rn(__fsub_rn(x, X), per), -64.0f);  // NaN, -inf: weight 0
     return __float2uint_rn(fast_exp2(z) * 2147483648.0f);
+  }
+  // what pass 2 adds for a token
+  __device__ __forceinline__ unsigned bits(float x) const {
+    const float z = __fmul_rn(__fsub_rn(x, X), per);
+    return __float_as_uint(__fadd_rn(fast_exp2(z), kMagic)) - __float_as_uint(kMagic);
   }
 };
 
@@ -80,6 +92,7 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 // Sum of v over the lanes below this one.
 __device__ __forceinline__ u64 warp_before64(u64 v) {
   const int lane = threadIdx.x & 31;
@@ -87,6 +100,16 @@ __device__ __forceinline__ u64 warp_before64(u64 v) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const u64 t = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += t;
+  }
+  return s - v;
+}
+__device__ __forceinline__ int warp_before_int(int v) {
+  const int lane = threadIdx.x & 31;
+  int s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, s, o);
     if (lane >= o) s += t;
   }
   return s - v;
@@ -99,19 +122,17 @@ struct Held {
 };
 
 template <int NW> struct Shared {
-  float xs[kListTokens];
-  int ids[kListTokens];
-  // of a digit: tokens, and their weight in three parts (over 2^48 + hi 2^16 + lo)
+  // of a stretch of keys: tokens, and their weight in three parts (over 2^48 + hi 2^16 + lo)
   unsigned cnt[256], lo[256], hi[256], over[256];
-  Held held[NW];
+  unsigned keys[32], weights[32];  // tokens to be ranked
+  Held held[NW], low[NW];
   int listed[NW];
   float red[NW];
   // one thread's findings for all
-  unsigned digit;
-  u64 above_cnt, above_mass, target;
-  int winner, token;
+  unsigned digit, found_key, found_ties;
+  u64 above_cnt, above_mass, found_mass, target;
+  int winner, token, ranked;
   unsigned ties_left;
-  __align__(16) float row[4];  // the row itself, if it is resident
 };
 
 // The prefix that stays: keys above `key`, and the first `ties` tokens with that key.
@@ -123,72 +144,49 @@ struct Cut {
 
 template <int DT, int NW, bool RESIDENT> struct Sampler {
   typedef typename Elem<DT>::T E;
+  typedef Key<DT> K;
   static constexpr int VEC = Vec<DT>::N;
   static constexpr int CAP = kListTokens / NW;  // list entries of a warp
 
   Shared<NW> &s;
+  float *own;     // the resident row, from its first vector on
+  float *xs;      // the list: tokens' values, their indices, and the vectors they come from
+  int *ids, *vecs;
   const E *row;
-  int V, warp, lane, chunk, head;
+  int V, warp, lane, head, v0, v1;  // vectors [v0, v1) of the row are the warp's
   Weigher w;
-  bool listed;  // the tokens read below are the list's
+  bool listed;    // the tokens read below are the list's
+  bool whole;     // a short resident row: no list is made
 
-  __device__ Sampler(Shared<NW> &sh, const E *r, int v) : s(sh), row(r), V(v), listed(false) {
+  __device__ Sampler(Shared<NW> &sh, unsigned char *mem, const E *r, int v)
+      : s(sh), row(r), V(v), listed(false), whole(false) {
     warp = threadIdx.x >> 5;
     lane = threadIdx.x & 31;
     // Vectors start at multiples of VEC counted from the 16-byte boundary below the row
     head = (int)(((uintptr_t)row % 16) / sizeof(E));
-    const int vectors = (V + head + VEC - 1) / VEC;
-    chunk = (vectors + NW - 1) / NW * VEC;
+    const int vectors = (V + head + VEC - 1) / VEC, each = (vectors + NW - 1) / NW;
+    v0 = min(each * warp, vectors);
+    v1 = min(v0 + each, vectors);
+    own = reinterpret_cast<float *>(mem);
+    xs = own + (RESIDENT ? (V + 16 + 3) / 4 * 4 : 0);
+    ids = reinterpret_cast<int *>(xs + kListTokens);
+    vecs = ids + kListTokens;
   }
 
-  // f(index, x) for the warp's range, VEC consecutive tokens a lane; 32 * VEC consecutive ones a step.
-  // Every lane takes every step; tokens outside the row and NaN come as -inf.  `from_memory`: not from
-  // the resident copy.  Steps come in pairs, so that two loads are in flight.
-  template <typename F> __device__ __forceinline__ void each_vector(F f, bool from_memory = false) const {
-    const int end = min(chunk * (warp + 1), V + head);
-    const int p0 = chunk * warp + lane * VEC, steps = (end - chunk * warp + 32 * VEC - 1) / (32 * VEC);
-    if (RESIDENT && !from_memory) {
-      for (int t = 0; t < steps; ++t) {
-        const int p = p0 + t * 32 * VEC;
-        float x[VEC];
+  // Vector v as float32: tokens outside the row and NaN come as -inf.
+  __device__ __forceinline__ uint4 fetch(int v) const {
+    const int i = v * VEC - head;
+    uint4 raw;
+    if (i >= 0 && i + VEC <= V) {
+      raw = __ldg(reinterpret_cast<const uint4 *>(row + i));
+    } else {
+      E *e = reinterpret_cast<E *>(&raw);
 #pragma unroll
-        for (int j = 0; j < VEC; j += 4) {
-          const float4 v = p < end ? *reinterpret_cast<const float4 *>(s.row + p + j)
-                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-          x[j] = v.x;
-          x[j + 1] = v.y;
-          x[j + 2] = v.z;
-          x[j + 3] = v.w;
-        }
-        f(p - head, x);
-      }
-      return;
+      for (int j = 0; j < VEC; ++j)
+        e[j] = i + j >= 0 && i + j < V ? row[i + j] : Elem<DT>::from_float(-INFINITY);
     }
-    constexpr int U = 4;
-    for (int t = 0; t < steps; t += U) {
-      uint4 raw[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int p = p0 + (t + u) * 32 * VEC, i = p - head;
-        if (i >= 0 && i + VEC <= V && p < end) {
-          raw[u] = __ldg(reinterpret_cast<const uint4 *>(row + i));
-        } else {
-          E *e = reinterpret_cast<E *>(&raw[u]);
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            e[j] = (i + j >= 0 && i + j < V && p < end) ? row[i + j] : Elem<DT>::from_float(-INFINITY);
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (t + u >= steps) break;
-        float x[VEC];
-        unpack(raw[u], x);
-        f(p0 + (t + u) * 32 * VEC - head, x);
-      }
-    }
+    return raw;
   }
-  // VEC tokens as float32, NaN as -inf
   static __device__ __forceinline__ void unpack(uint4 raw, float (&x)[VEC]) {
     unsigned v[4] = {raw.x, raw.y, raw.z, raw.w};
     if constexpr (DT == kF32) {
@@ -213,12 +211,56 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
       }
     }
   }
-  // f(x) for every token of this thread's share of the warp's tokens: the list's or the row's.
+  // The largest token of a vector, NaN apart.
+  static __device__ __forceinline__ float top_of(uint4 raw) {
+    unsigned v[4] = {raw.x, raw.y, raw.z, raw.w};
+    if constexpr (DT == kF32) {
+      return fmaxf(max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2])),
+                   __uint_as_float(v[3]));
+    } else if constexpr (DT == kBF16) {
+      __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(v);
+      const __nv_bfloat162 c = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+      const unsigned b = *reinterpret_cast<const unsigned *>(&c);
+      return fmaxf(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+    } else {
+      __half2 *h = reinterpret_cast<__half2 *>(v);
+      const float2 c = __half22float2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])));
+      return fmaxf(c.x, c.y);
+    }
+  }
+  // f(vector, raw) for the warp's vectors in memory, a vector a lane; every lane takes every step, and
+  // those past the warp's end get vectors of -inf.
+  template <typename F> __device__ __forceinline__ void each_raw(F f) const {
+    constexpr int U = 4;  // loads in flight
+    const int inner0 = head > 0 ? 1 : 0, inner1 = min(v1, (V + head) / VEC);
+    const uint4 *base = reinterpret_cast<const uint4 *>(row - head);
+    int v = v0;
+    while (v < v1) {
+      if (v >= inner0 && v + 32 * U <= inner1) {
+        uint4 raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = __ldg(base + v + u * 32 + lane);
+#pragma unroll
+        for (int u = 0; u < U; ++u) f(v + u * 32 + lane, raw[u]);
+        v += 32 * U;
+      } else {
+        const bool mine = v + lane < v1;
+        f(v + lane, fetch(mine ? v + lane : (V + head) / VEC + 1));
+        v += 32;
+      }
+    }
+  }
+  // f(x) for every token of this thread's share of the warp's: the list's or the row's.
   template <typename F> __device__ __forceinline__ void each(F f) const {
     if (listed) {
-      for (int i = lane; i < s.listed[warp]; i += 32) f(s.xs[warp * CAP + i]);
+      const int n = s.listed[warp], at = warp * CAP;
+      for (int i = lane; i < n; i += 32) f(xs[at + i]);
+    } else if (RESIDENT) {
+      for (int p = max(v0 * VEC, head) + lane; p < min(v1 * VEC, V + head); p += 32) f(own[p]);
     } else {
-      each_vector([&](int, const float *x) {
+      each_raw([&](int, uint4 raw) {
+        float x[VEC];
+        unpack(raw, x);
 #pragma unroll
         for (int j = 0; j < VEC; ++j) f(x[j]);
       });
@@ -226,109 +268,141 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
   }
   // Token i of the row, NaN as -inf.
   __device__ __forceinline__ float token(int i) const {
-    return RESIDENT ? s.row[i + head] : fmaxf(Elem<DT>::load(row + i), -INFINITY);
+    return RESIDENT ? own[i + head] : fmaxf(Elem<DT>::load(row + i), -INFINITY);
   }
 
   __device__ float maximum() {
     float m = -INFINITY;
-    each_vector(
-        [&](int i, const float *x) {
+    each_raw([&](int v, uint4 raw) {
+      m = fmaxf(m, top_of(raw));  // fmaxf passes over NaN
+      if (RESIDENT && v < v1) {
+        float x[VEC];
+        unpack(raw, x);
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) m = fmaxf(m, x[j]);
-          // the resident copy; a thread reads back what it wrote, others only after a barrier
-          if (RESIDENT && i < V && i + head < chunk * (warp + 1))
-#pragma unroll
-            for (int j = 0; j < VEC; j += 4)
-              *reinterpret_cast<float4 *>(s.row + i + head + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-        },
-        true);
+        for (int j = 0; j < VEC; j += 4)
+          *reinterpret_cast<float4 *>(own + v * VEC + j) = make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+      }
+    });
     m = warp_max(m);
     if (lane == 0) s.red[warp] = m;
     __syncthreads();
-    m = warp_max(lane < NW ? s.red[lane] : -INFINITY);
-    __syncthreads();
-    return m;
+    return warp_max(lane < NW ? s.red[lane] : -INFINITY);
   }
 
-  // Pass 2.  MASS: the sum of the weights, by warp into held[].mass: of all tokens, or with LIST of those
-  // below `near`.  LIST: the tokens from `near` up into the list.  Returns the number of listed tokens, -1
-  // if they do not fit.
+  // Pass 2.  MASS: the weight of the tokens that are not listed, by warp into low[].mass.  LIST: the tokens
+  // of at least `near` into the list, their weight by warp into held[].mass.  Returns the number of listed
+  // tokens, -1 if they do not fit (then the sums are of all tokens, in low[]).
   template <bool MASS, bool LIST> __device__ int weigh(float near) {
-    u64 mass = 0;
-    int n = 0;
+    u64 mass = 0, mass_listed = 0;
+    int n = 0, nv = 0;
     bool fits = true;
-    const float2 x2 = make_float2(-w.X, -w.X), per2 = make_float2(w.per, w.per);
-    // z < -9 for tokens below `near`: reading a weight off the sum is exact (see the head of the file)
+    // reading a weight off the sum is exact below 2^-9: see the head of the file
     const bool small = !w.infinite && (near - w.X) * w.per < -9.5f;
-    constexpr float kMagic = 1.5f / 256.0f;
-    each_vector([&](int i, const float *x) {
+    const float2 x2 = make_float2(-w.X, -w.X), per2 = make_float2(w.per, w.per),
+                 magic2 = make_float2(kMagic, kMagic);
+    auto take = [&](int v, const float (&x)[VEC], float top) {
       if (MASS && small) {
         unsigned sum = 0;
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
           const float2 z = mul2(add2(make_float2(x[j], x[j + 1]), x2), per2);
-          const float2 m = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(kMagic, kMagic));
-          if (!(x[j] >= near)) sum += __float_as_uint(m.x) - __float_as_uint(kMagic);
-          if (!(x[j + 1] >= near)) sum += __float_as_uint(m.y) - __float_as_uint(kMagic);
+          const float2 m = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), magic2);
+          sum += __float_as_uint(m.x) + __float_as_uint(m.y);
         }
-        mass += sum;
-        if (!LIST) {
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (x[j] >= near) mass += w(x[j]);
-        }
+        mass += sum - VEC * __float_as_uint(kMagic);  // modulo 2^32; the sum itself is at most VEC 2^26
       } else if (MASS) {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          if (!LIST || !(x[j] >= near)) mass += w(x[j]);
+        for (int j = 0; j < VEC; ++j) mass += w(x[j]);
       }
-      if (LIST) {
-        float top = x[0];
+      if (!LIST && !(MASS && small)) return;
+      const unsigned hit = __ballot_sync(0xffffffffu, top >= near);
+      if (hit) {
+        const int at = nv + __popc(hit & ((1u << lane) - 1));
+        nv += __popc(hit);
+        if (nv > CAP)
+          fits = false;
+        else if (hit >> lane & 1)
+          vecs[warp * CAP + at] = v;
+      }
+    };
+    if (RESIDENT) {
+      for (int v = v0; v < v1; v += 32) {
+        float x[VEC], top = -INFINITY;
 #pragma unroll
-        for (int j = 1; j < VEC; ++j) top = fmaxf(top, x[j]);
-        if (!__any_sync(0xffffffffu, top >= near)) return;
+        for (int j = 0; j < VEC; j += 4) {
+          const float4 q = v + lane < v1 ? *reinterpret_cast<const float4 *>(own + (v + lane) * VEC + j)
+                                         : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+          x[j] = q.x;
+          x[j + 1] = q.y;
+          x[j + 2] = q.z;
+          x[j + 3] = q.w;
+          top = fmaxf(max3(q.x, q.y, top), fmaxf(q.z, q.w));
+        }
+        take(v + lane, x, top);
+      }
+    } else {
+      each_raw([&](int v, uint4 raw) {
+        float x[VEC];
+        if (MASS) unpack(raw, x);
+        take(v, x, top_of(raw));
+      });
+    }
+    // the tokens of the noted vectors, in order
+    __syncwarp();
+    if (fits)
+      for (int e = 0; e < nv; e += 32) {
+        const bool mine = e + lane < nv;
+        const int v = mine ? vecs[warp * CAP + e + lane] : 0;
+        float x[VEC];
+        if (RESIDENT) {
+#pragma unroll
+          for (int j = 0; j < VEC; ++j) x[j] = own[v * VEC + j];
+        } else {
+          unpack(fetch(v), x);
+        }
         unsigned in = 0;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) in |= (x[j] >= near ? 1u : 0u) << j;
-        // place of this lane's first token: the tokens of lower lanes come before it
-        int before = __popc(in);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int t = __shfl_up_sync(0xffffffffu, before, o);
-          if (lane >= o) before += t;
+        for (int j = 0; j < VEC; ++j) in |= (mine && x[j] >= near ? 1u : 0u) << j;
+        const int here = __popc(in);
+        int at = n + warp_before_int(here);
+        n += warp_sum_int(here);
+        if (LIST && n > CAP) {
+          fits = false;
+          break;
         }
-        const int all = __shfl_sync(0xffffffffu, before, 31);
-        int at = n + before - __popc(in);
-        if (n + all > CAP) fits = false;
-        if (fits) {
 #pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (in >> j & 1) {
-              s.xs[warp * CAP + at] = x[j];
-              s.ids[warp * CAP + at] = i + j;
+        for (int j = 0; j < VEC; ++j)
+          if (in >> j & 1) {
+            const unsigned v31 = w(x[j]);
+            mass_listed += v31;
+            if (MASS) mass -= small ? w.bits(x[j]) : v31;
+            if (LIST) {
+              xs[warp * CAP + at] = x[j];
+              ids[warp * CAP + at] = v * VEC - head + j;
               ++at;
             }
-          n += all;
-        }
+          }
       }
-    });
-    if (MASS) mass = warp_sum64(mass);
+    if (!fits && MASS) {  // too many to set right: the plain sum
+      mass = mass_listed = 0;
+      each([&](float x) { mass += w(x); });
+    }
+    mass = warp_sum64(mass);
+    mass_listed = warp_sum64(mass_listed);
     if (lane == 0) {
-      if (MASS) {
-        s.held[warp].mass = mass;
-        s.held[warp].ties = 0;
-      }
+      s.low[warp].mass = mass;
+      s.held[warp].mass = mass_listed;
+      s.held[warp].ties = 0;
       s.listed[warp] = n;
     }
-    const int bad = __syncthreads_or(!fits);
-    if (bad) return -1;
-    int total = lane < NW ? s.listed[lane] : 0;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    return total;
+    if (__syncthreads_or(!fits)) return -1;
+    return warp_sum_int(lane < NW ? s.listed[lane] : 0);
   }
 
-  // Sum over all threads, known to all; a barrier before and after its use of held[].
+  __device__ u64 total_mass() const { return warp_sum64(lane < NW ? s.held[lane].mass : 0ull); }
+  __device__ u64 total_low() const { return warp_sum64(lane < NW ? s.low[lane].mass : 0ull); }
+
+  // Sum over all threads, known to all.
   __device__ u64 total_of(u64 v) {
     v = warp_sum64(v);
     __syncthreads();
@@ -337,44 +411,39 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     return total_mass();
   }
 
-  __device__ u64 total_mass() const {
-    return warp_sum64(lane < NW ? s.held[lane].mass : 0ull);
-  }
-
   __device__ __forceinline__ u64 mass_of(int digit) const {
     return ((u64)s.over[digit] << 48) + ((u64)s.hi[digit] << 16) + s.lo[digit];
   }
 
-  // Radix selection over the keys in [from, top]: the token at which, in falling order, the
-  // count (by_count) or the weight reaches `target` >= 1.  The caller knows that it is reached.
-  __device__ Cut select(bool by_count, u64 target, unsigned from, unsigned top) {
-    unsigned lo = from;                         // keys [lo, lo + 2^bits) are still in question
-    int bits = 32 - __clz(top - from);          // 0: only one key
-    u64 above_cnt = 0, above_mass = 0;          // of the keys above that range
-    while (bits > 0) {
-      const int shift = max(0, bits - 8);
-      const unsigned digits = 1u << (bits - shift);  // at most 256
-      for (int i = threadIdx.x; i < 256; i += NW * 32) {
-        s.cnt[i] = 0;
-        s.lo[i] = 0;
-        s.hi[i] = 0;
-        s.over[i] = 0;
+  // Counts and weights of the keys in [lo, lo + 2^bits), in stretches of 2^shift.
+  __device__ void histogram(unsigned lo, int bits, int shift) {
+    const unsigned digits = 1u << (bits - shift);  // at most 256
+    __syncthreads();
+    for (int i = threadIdx.x; i < 256; i += NW * 32) s.cnt[i] = s.lo[i] = s.hi[i] = s.over[i] = 0;
+    __syncthreads();
+    each([&](float x) {
+      const unsigned k = K::of(x);
+      if (k >= lo && ((k - lo) >> shift) < digits) {
+        // a weight goes in as two halves of 16 bits, with native 32-bit adds; what a part overflows is
+        // carried into the next one
+        const unsigned d = (k - lo) >> shift, v = w(x), half = v & 0xffffu;
+        atomicAdd(&s.cnt[d], 1u);
+        const unsigned old = atomicAdd(&s.lo[d], half);
+        const unsigned up = (v >> 16) + (old + half < old ? 0x10000u : 0u);
+        const unsigned old_hi = atomicAdd(&s.hi[d], up);
+        if (old_hi + up < old_hi) atomicAdd(&s.over[d], 1u);
       }
-      __syncthreads();
-      each([&](float x) {
-        const unsigned k = order_key(x);
-        if (k >= lo && ((k - lo) >> shift) < digits) {
-          // a weight goes in as two halves of 16 bits, with native 32-bit adds; what a part overflows
-          // is carried into the next one
-          const unsigned d = (k - lo) >> shift, v = w(x), half = v & 0xffffu;
-          atomicAdd(&s.cnt[d], 1u);
-          const unsigned old = atomicAdd(&s.lo[d], half);
-          const unsigned up = (v >> 16) + (old + half < old ? 0x10000u : 0u);
-          const unsigned old_hi = atomicAdd(&s.hi[d], up);
-          if (old_hi + up < old_hi) atomicAdd(&s.over[d], 1u);
-        }
-      });
-      __syncthreads();
+    });
+    __syncthreads();
+  }
+
+  // Selection over the keys in [from, top]: the token at which, in falling order, the count (by_count) or
+  // the weight reaches `target` >= 1, which the caller knows to be reached.  `bits`, `shift` are those of
+  // the histogram that stands (bits 0: only one key).
+  __device__ Cut select(bool by_count, u64 target, unsigned from, int bits, int shift, bool *stands) {
+    unsigned lo = from;
+    u64 above_cnt = 0, above_mass = 0;  // of the keys above those in question
+    while (bits > 0) {
       if (warp == 0) {
         // lane 0 has the 8 highest digits
         u64 c = 0, m = 0;
@@ -394,6 +463,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
           s.digit = d;
           s.above_cnt = bc;
           s.above_mass = bm;
+          s.ranked = 0;
         }
       }
       __syncthreads();
@@ -401,30 +471,70 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
       above_cnt = s.above_cnt;
       above_mass = s.above_mass;
       bits = shift;
+      if (bits == 0) break;
+      const unsigned count = s.cnt[s.digit];
+      if (count <= 32) {  // rank them
+        each([&](float x) {
+          const unsigned k = K::of(x);
+          if (k >= lo && ((k - lo) >> bits) == 0) {
+            const int at = atomicAdd(&s.ranked, 1);
+            s.keys[at] = k;
+            s.weights[at] = w(x);
+          }
+        });
+        __syncthreads();
+        if (warp == 0) {
+          const unsigned k = lane < (int)count ? s.keys[lane] : 0, v = lane < (int)count ? s.weights[lane] : 0;
+          unsigned gt = 0, ge = 0;
+          u64 mass_gt = 0, mass_ge = 0;
+          for (int i = 0; i < (int)count; ++i) {
+            const unsigned k2 = __shfl_sync(0xffffffffu, k, i), v2 = __shfl_sync(0xffffffffu, v, i);
+            gt += k2 > k;
+            ge += k2 >= k;
+            mass_gt += k2 > k ? v2 : 0;
+            mass_ge += k2 >= k ? v2 : 0;
+          }
+          const bool here = lane < (int)count &&
+                            (by_count ? above_cnt + gt < target && above_cnt + ge >= target
+                                      : above_mass + mass_gt < target && above_mass + mass_ge >= target);
+          const unsigned who = __ballot_sync(0xffffffffu, here);
+          if (lane == __ffs(who) - 1) {
+            s.found_key = k;
+            s.above_cnt = above_cnt + gt;
+            s.above_mass = above_mass + mass_gt;
+          }
+        }
+        __syncthreads();
+        lo = s.found_key;
+        above_cnt = s.above_cnt;
+        above_mass = s.above_mass;
+        break;
+      }
+      shift = max(0, bits - 8);
+      histogram(lo, bits, shift);
+      *stands = false;
     }
-    __syncthreads();
     Cut c;
     c.key = lo;
-    const u64 weight = w(key_value(lo));
+    const u64 weight = w(K::value(lo));
     if (by_count)
       c.ties = (unsigned)(target - above_cnt);
     else
       c.ties = (unsigned)((target - above_mass + weight - 1) / weight);  // weight > 0: it moved the sum
     c.mass = above_mass + c.ties * weight;
+    __syncthreads();
     return c;
   }
 
   __device__ __forceinline__ bool above(float x, const Cut &c, unsigned m) const {
-    return order_key(x) > c.key && w(x) >= m;
+    return K::of(x) > c.key && w(x) >= m;
   }
 
   // Reduces each warp's Held over its lanes; all threads then know the warp that the running sum
   // passes `target` in, what is left of the target and of the ties before it.
-  __device__ void pick_warp(u64 mass, unsigned ties, unsigned tie_weight, u64 *target,
-                            unsigned *ties_left) {
+  __device__ void pick_warp(u64 mass, int ties, unsigned tie_weight, u64 *target, unsigned *ties_left) {
     mass = warp_sum64(mass);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) ties += __shfl_xor_sync(0xffffffffu, ties, o);
+    ties = warp_sum_int(ties);
     if (lane == 0) {
       s.held[warp].mass = mass;
       s.held[warp].ties = ties;
@@ -433,20 +543,19 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     find_warp(tie_weight, target, ties_left);
   }
   __device__ void find_warp(unsigned tie_weight, u64 *target, unsigned *ties_left) {
-    if (threadIdx.x == 0) {
-      u64 run = 0;
-      unsigned left = *ties_left;
-      int i = 0;
-      for (; i < NW - 1; ++i) {
-        const unsigned t = min(left, s.held[i].ties);
-        const u64 here = s.held[i].mass + (u64)t * tie_weight;
-        if (run + here > *target) break;
-        run += here;
-        left -= t;
+    if (warp == 0) {  // a lane a warp
+      const Held h = lane < NW ? s.held[lane] : Held{0, 0};
+      const unsigned before_t = (unsigned)warp_before_int((int)h.ties);
+      const unsigned left = *ties_left > before_t ? *ties_left - before_t : 0;
+      const u64 here = h.mass + (u64)min(left, h.ties) * tie_weight;
+      const u64 before = warp_before64(here);
+      const unsigned hit = __ballot_sync(0xffffffffu, lane < NW && before + here > *target);
+      const int who = hit ? __ffs(hit) - 1 : NW - 1;
+      if (lane == who) {
+        s.winner = who;
+        s.target = *target - before;
+        s.ties_left = left;
       }
-      s.winner = i;
-      s.target = *target - run;
-      s.ties_left = left;
     }
     __syncthreads();
     *target = s.target;
@@ -457,7 +566,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
   // Returns the lane, or 32 with the target and the ties moved on.
   __device__ int step(float x, bool valid, const Cut &c, unsigned m, unsigned tie_weight,
                       u64 *target, unsigned *ties_left) const {
-    const bool tie = valid && order_key(x) == c.key;
+    const bool tie = valid && K::of(x) == c.key;
     const unsigned ties = __ballot_sync(0xffffffffu, tie);
     const unsigned rank = __popc(ties & ((1u << lane) - 1));
     u64 v = 0;
@@ -471,9 +580,10 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     return 32;
   }
 
-  // The drawn token, valid in every thread.  `target` < the kept weight.
+  // The drawn token, valid in every thread.  `target` < the kept weight.  `sums_ready`: held[] is the sums
+  // by warp of the kept tokens above the cut, and of the ties.
   __device__ int draw(const Cut &c, unsigned m, u64 target, bool sums_ready) {
-    const unsigned wc = w(key_value(c.key)), tie_weight = wc >= m ? wc : 0;
+    const unsigned wc = w(K::value(c.key)), tie_weight = wc >= m ? wc : 0;
     unsigned left = c.ties;
     if (threadIdx.x == 0) s.token = -1;
     if (sums_ready) {
@@ -481,15 +591,16 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
       find_warp(tie_weight, &target, &left);
     } else {
       u64 mass = 0;
-      unsigned ties = 0;
+      int ties = 0;
       each([&](float x) {
-        const unsigned k = order_key(x);
+        const unsigned k = K::of(x);
         if (k > c.key) {
           const unsigned v = w(x);
           if (v >= m) mass += v;
         }
-        ties += k == c.key ? 1u : 0u;
+        ties += k == c.key ? 1 : 0;
       });
+      __syncthreads();
       pick_warp(mass, ties, tie_weight, &target, &left);
     }
     const int winner = s.winner;
@@ -499,10 +610,10 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
         for (int i0 = 0; i0 < n; i0 += 32) {
           const int i = i0 + lane;
           const bool valid = i < n;
-          const float x = valid ? s.xs[warp * CAP + i] : -INFINITY;
+          const float x = valid ? xs[warp * CAP + i] : -INFINITY;
           const int hit = step(x, valid, c, m, tie_weight, &target, &left);
           if (hit < 32) {
-            if (lane == hit) s.token = s.ids[warp * CAP + i];
+            if (lane == hit) s.token = ids[warp * CAP + i];
             break;
           }
         }
@@ -511,16 +622,18 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
       return s.token;
     }
     // the row: the winner's range is split over the warps again, until it is short
-    int a = max(0, chunk * winner - head), b = min(chunk * (winner + 1) - head, V);
-    while (b - a > 128) {
+    const int vectors = (V + head + VEC - 1) / VEC, each_warp = (vectors + NW - 1) / NW;
+    int a = max(0, min(each_warp * winner, vectors) * VEC - head),
+        b = min(min(each_warp * (winner + 1), vectors) * VEC - head, V);
+    while (NW > 1 && b - a > 128) {
       __syncthreads();
       const int piece = (b - a + NW - 1) / NW, p0 = a + piece * warp, p1 = min(b, p0 + piece);
       u64 mass = 0;
-      unsigned ties = 0;
+      int ties = 0;
       for (int i = p0 + lane; i < p1; i += 32) {
         const float x = token(i);
         if (above(x, c, m)) mass += w(x);
-        ties += order_key(x) == c.key ? 1u : 0u;
+        ties += K::of(x) == c.key ? 1 : 0;
       }
       pick_warp(mass, ties, tie_weight, &target, &left);
       a += piece * s.winner;
@@ -546,15 +659,16 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
 template <int DT, int NW, bool RESIDENT>
 __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   typedef typename Elem<DT>::T E;
-  extern __shared__ __align__(16) unsigned char raw[];
-  Shared<NW> &s = *reinterpret_cast<Shared<NW> *>(raw);
+  typedef Key<DT> K;
+  extern __shared__ __align__(16) unsigned char mem[];
+  __shared__ Shared<NW> s;
   const long long n = blockIdx.x;
   const E *row = static_cast<const E *>(a.logits) + n * a.row_stride;
   const float T = a.temperatures ? a.temperatures[n] : a.temperature;
   const float p = a.top_ps ? a.top_ps[n] : a.top_p;
   const float mp = a.min_ps ? a.min_ps[n] : a.min_p;
   int k = a.top_ks ? a.top_ks[n] : a.top_k;
-  Sampler<DT, NW, RESIDENT> r(s, row, a.V);
+  Sampler<DT, NW, RESIDENT> r(s, mem, row, a.V);
   const float X = r.maximum();
   const bool usable = T >= 0.0f && T < INFINITY && p >= 0.0f && p <= 1.0f && mp >= 0.0f &&
                       mp <= 1.0f && k >= 0 && X > -INFINITY;
@@ -575,72 +689,73 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
   const unsigned u24 = (unsigned)min(max(__float2int_rd(a.u[n] * 16777216.0f), 0), 16777215);
   const bool by_p = p24 < (1u << 24), filters = k > 0 || by_p || m > 0;
   const bool need_all = by_p && k == 0;  // top-p's share is of the weight of every token
-  const unsigned top = order_key(X);
-  // the value at -z below the maximum, as a key's value
-  auto below = [&](float z) {
-    return T == 0.0f || r.w.infinite ? X : key_value(order_key(X - z / r.w.per));
+  const unsigned top = K::of(X);
+  auto below = [&](float z) {  // the value at -z below the maximum
+    return T == 0.0f || r.w.infinite ? X : X - z / r.w.per;
   };
+  r.whole = RESIDENT && a.V <= kOwnList;
   Cut cut;
   u64 kept;
   bool sums_ready = false;
-  if (!filters) {
+  if (!filters && !r.whole) {
     r.template weigh<true, false>(below((float)kListZ));
+    // the sums by warp of every token, whatever pass 2 made of them
+    if (threadIdx.x < NW) s.held[threadIdx.x].mass += s.low[threadIdx.x].mass;
+    __syncthreads();
     cut.key = 0;
     cut.ties = 0;
     kept = r.total_mass();
-    sums_ready = true;  // held[] is the sums by warp of every token
+    sums_ready = true;
   } else {
-    int listed = -1, z = kListZ;
-    u64 all = 0;
+    u64 all = 0, listed_mass = 0;
     float near = 0.0f;
-    for (int i = 0; i < kListTries && listed < 0; ++i) {
-      z = kListZ >> i;
-      near = below((float)z);
-      listed = need_all && i == 0 ? r.template weigh<true, true>(near) : r.template weigh<false, true>(near);
-      if (need_all && i == 0) {
-        all = r.total_mass();  // of the tokens below the first `near`
-        if (listed < 0) {      // the rest was not kept: sum it from the row
-          u64 mass = 0;
-          r.each([&](float x) { mass += x >= near ? (u64)r.w(x) : 0ull; });
-          all += r.total_of(mass);
-        }
-      }
-    }
-    u64 listed_mass = 0;
-    if (listed >= 0) {
+    bool enough = false, have_all = need_all;
+    if (r.whole) {
       u64 mass = 0;
-      r.listed = true;
       r.each([&](float x) { mass += r.w(x); });
-      listed_mass = r.total_of(mass);
-      if (need_all && z == kListZ) all += listed_mass;
+      all = r.total_of(mass);
+      have_all = true;
+    } else {
+      int listed = -1, z = kListZ;
+      for (int i = 0; i < kListTries && listed < 0; ++i) {
+        z = kListZ >> i;
+        near = below((float)z);
+        if (need_all && i == 0) {
+          listed = r.template weigh<true, true>(near);
+          all = r.total_low() + r.total_mass();  // also where the list did not fit
+        } else {
+          listed = r.template weigh<false, true>(near);
+        }
+        listed_mass = r.total_mass();
+        if (listed < 0) __syncthreads();  // before the sums are written again
+      }
+      // does the cut lie among the listed tokens?
+      const unsigned low = (0x80000000u >> z) + (0x80000000u >> (z + 8));  // above any unlisted weight
+      enough = listed > 0 && (k > 0   ? listed >= k || (!by_p && m >= low)
+                              : by_p ? listed_mass >= share(all, p24)
+                                     : m >= low);
+      r.listed = enough;
+      if (enough && listed < k) k = 0;  // top-k keeps more than min-p does
     }
-    // does the cut lie among the listed tokens?
-    const unsigned low = (0x80000000u >> z) + (0x80000000u >> (z + 8));  // above any unlisted weight
-    const bool enough = listed > 0 && (k > 0   ? listed >= k || (!by_p && m >= low)
-                                       : by_p ? listed_mass >= share(all, p24)
-                                              : m >= low);
-    r.listed = enough;
-    const unsigned from = order_key(enough ? near : below(kZeroZ));
+    const unsigned from = K::of(enough ? near : below(kZeroZ));
+    // one histogram for both cuts
+    const int bits = 32 - __clz(top - from), shift = max(0, bits - 8);
+    bool stands = false;
     // top-k, unless fewer tokens than that weigh anything
     cut.key = from;  // everything from `from` up
     cut.ties = 0xffffffffu;
-    bool cut_by_k = false;
-    if (k > 0) {
-      u64 have = (u64)max(listed, 0);
-      if (!enough) {
-        u64 c = 0;
-        r.each([&](float x) { c += order_key(x) >= from ? 1u : 0u; });
-        have = r.total_of(c);
-      }
-      if (have >= (u64)k) {
-        cut = r.select(true, (u64)k, from, top);
-        cut_by_k = true;
-      }
+    cut.mass = listed_mass;
+    if (k > 0 && !enough) {
+      u64 c = 0;
+      r.each([&](float x) { c += K::of(x) >= from ? 1u : 0u; });
+      if (r.total_of(c) < (u64)k) k = 0;
     }
-    if (!cut_by_k) {  // the weight of everything from `from` up
-      if (enough) {
-        cut.mass = listed_mass;
-      } else if (need_all) {
+    if (k > 0) {
+      if (bits > 0) r.histogram(from, bits, shift);
+      stands = true;
+      cut = r.select(true, (u64)k, from, bits, shift, &stands);
+    } else if (!enough) {  // the weight of everything from `from` up
+      if (have_all) {
         cut.mass = all;
       } else {
         u64 mass = 0;
@@ -650,30 +765,30 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
     }
     if (by_p) {
       const u64 need = share(need_all ? all : cut.mass, p24);
-      cut = r.select(false, need > 0 ? need : 1, from, top);
+      if (!stands && bits > 0) r.histogram(from, bits, shift);
+      cut = r.select(false, need > 0 ? need : 1, from, bits, shift, &stands);
     }
     kept = cut.mass;
     if (m > 0) {  // the weight that min-p leaves
       u64 mass = 0;
-      unsigned ties = 0;
+      int ties = 0;
       r.each([&](float x) {
-        const unsigned key = order_key(x);
+        const unsigned key = K::of(x);
         if (key > cut.key) {
           const unsigned v = r.w(x);
           if (v >= m) mass += v;
         }
-        ties += key == cut.key ? 1u : 0u;
+        ties += key == cut.key ? 1 : 0;
       });
       mass = warp_sum64(mass);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) ties += __shfl_xor_sync(0xffffffffu, ties, o);
+      ties = warp_sum_int(ties);
       __syncthreads();
       if (r.lane == 0) {
         s.held[r.warp].mass = mass;
         s.held[r.warp].ties = ties;
       }
       __syncthreads();
-      const unsigned wc = r.w(key_value(cut.key));
+      const unsigned wc = r.w(K::value(cut.key));
       const u64 n_ties = warp_sum64(r.lane < NW ? (u64)s.held[r.lane].ties : 0ull);
       kept = r.total_mass() + (wc >= m ? (n_ties < cut.ties ? n_ties : cut.ties) * wc : 0);
       sums_ready = true;
@@ -693,15 +808,18 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
 template <int DT, int NW, bool RESIDENT>
 cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   // a resident row starts at its first vector's place and is filled up to whole vectors
-  const size_t smem = sizeof(Shared<NW>) + (RESIDENT ? (size_t)(a.V + 16) * 4 : 0);
+  const size_t row = RESIDENT ? (size_t)((a.V + 16 + 3) / 4 * 4) * 4 : 0;
+  const size_t smem = row + (RESIDENT && a.V <= kOwnList ? 0 : 3 * kListTokens * 4);
   const cudaError_t e = cudaFuncSetAttribute(sample_kernel<DT, NW, RESIDENT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   sample_kernel<DT, NW, RESIDENT><<<(unsigned)N, NW * 32, smem, s>>>(a);
   return cudaGetLastError();
 }
+// Warps a row: few for many rows, which share the SMs; many for few rows, where only the time of one counts.
 template <int DT> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
-  if (a.V <= 2048) return launch<DT, 4, true>(a, N, s);
+  if (a.V <= 256) return launch<DT, 1, true>(a, N, s);
+  if (a.V <= kOwnList) return launch<DT, 4, true>(a, N, s);
   if (a.V <= kResident)
     return N > 2 * 152 ? launch<DT, 8, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
   return N > 2 * 152 ? launch<DT, 8, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
