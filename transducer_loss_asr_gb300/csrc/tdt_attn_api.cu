@@ -100,14 +100,14 @@ extern "C" {
 size_t tdt_cross_attn_workspace_size(const int64_t sizes[6], int dtype, int backward) {
   using namespace tdt;
   if (check_sizes(sizes, dtype) != TDT_OK) return 0;
-  const bool tc = dtype != TDT_DTYPE_F32 && sizes[5] <= 128 && sizes[2] > 0;
+  const bool tc = attn_tc_takes(dtype, sizes[1], sizes[2], (int)(sizes[3] / sizes[4]), (int)sizes[5]);
   if (!backward)
     return tc ? attn_fwd_tc_workspace(sizes[0], sizes[1], sizes[2], (int)sizes[3], (int)sizes[4],
-                                      (int)sizes[5])
+                                      (int)sizes[5], dtype)
               : 0;
   return delta_bytes(sizes) + (tc ? attn_bwd_tc_workspace(sizes[0], sizes[1], sizes[2],
                                                           (int)sizes[3], (int)sizes[4],
-                                                          (int)sizes[5])
+                                                          (int)sizes[5], dtype)
                                   : 0);
 }
 

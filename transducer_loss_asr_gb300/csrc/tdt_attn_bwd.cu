@@ -51,12 +51,14 @@ struct BwdArgs {
   float *part;                  // splits > 1: [split][CTA][128][DP], dk's after dv's
 };
 
-template <int DP> struct BwdShape {
+template <int DT, int DP> struct BwdShape {
   static constexpr int CHUNKS = DP / 64;
   static constexpr int CHUNK = kRows * 128;
-  static constexpr int TILE = CHUNKS * CHUNK;
-  static constexpr int KS = 3, VS = 2;  // dq: slots of k and v
-  static constexpr int RS = DP == 64 ? 4 : 2;  // dk/dv: slots of q and of dO
+  static constexpr int PLANES = kPlanes<DT>;
+  static constexpr int PLANE = CHUNKS * CHUNK;
+  static constexpr int TILE = PLANES * PLANE;
+  static constexpr int KS = PLANES == 3 ? 1 : 3, VS = PLANES == 3 ? 1 : 2;   // dq: slots of k and v
+  static constexpr int RS = PLANES == 3 ? 1 : DP == 64 ? 4 : 2;              // dk/dv: slots of q and of dO
   static constexpr int DQ_BYTES = (2 + KS + VS) * TILE;
   static constexpr int DKV_BYTES = (2 + 2 * RS) * TILE;
 };
@@ -72,31 +74,33 @@ __device__ __forceinline__ void pipe_init(Pipe &p, int slots) {
   }
 }
 
-template <int DP>
+template <int DT, int DP>
 __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *dst,
                                           unsigned long long *bar, int h, int l, int b) {
-  for (int c = 0; c < DP / 64; ++c)
-    tma_load_4d(m, dst + c * BwdShape<DP>::CHUNK, bar, c * 64, h, l, b);
+  for (int c = 0; c < kPlanes<DT> * DP / 64; ++c)
+    tma_load_4d(m, dst + c * BwdShape<DT, DP>::CHUNK, bar, c * 64, h, l, b);
 }
 
-// dot of the first `n` of N elements of two rows, n a multiple of 8; every load is in flight at once
-template <int DT, int N> __device__ __forceinline__ float dot16(const void *x, const void *y, int n) {
+// dot of the first `n` of N elements of two rows, n a multiple of a 16-byte load's elements; every load is
+// in flight at once
+template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x, const void *y, int n) {
   typedef typename Elem<DT>::T E;
-  uint4 xv[N / 8], yv[N / 8];
+  constexpr int W = 16 / (int)sizeof(E);
+  uint4 xv[N / W], yv[N / W];
 #pragma unroll
-  for (int d = 0; d < N; d += 8) {
-    xv[d / 8] = yv[d / 8] = make_uint4(0, 0, 0, 0);
+  for (int d = 0; d < N; d += W) {
+    xv[d / W] = yv[d / W] = make_uint4(0, 0, 0, 0);
     if (d < n) {
-      xv[d / 8] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d));
-      yv[d / 8] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
+      xv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d));
+      yv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
     }
   }
   float s = 0.0f;
 #pragma unroll
-  for (int d = 0; d < N / 8; ++d) {
+  for (int d = 0; d < N / W; ++d) {
     const E *xe = reinterpret_cast<const E *>(&xv[d]), *ye = reinterpret_cast<const E *>(&yv[d]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
+    for (int k = 0; k < W; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
   }
   return s;
 }
@@ -116,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_dq_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
                       const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                       const __grid_constant__ CUtensorMap dqm, const __grid_constant__ BwdArgs f) {
-  typedef BwdShape<DP> S;
+  typedef BwdShape<DT, DP> S;
   typedef typename Elem<DT>::T E;
   extern __shared__ unsigned char raw[];
   __shared__ DqShared sh;
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.dq_splits);
     begin = hull.x + steps.x * kRows;
     T = steps.y - steps.x;
-    cut = T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;
+    cut = S::PLANES == 1 && T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;  // planes end in zeros
   };
   if (!a.windows && some) walk(make_int2(0, n.nk));
   auto frame = [&](int s) { return begin + s * kRows; };
@@ -154,12 +158,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = s % S::KS;
     unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
     arrive_expect_tx(bar, S::TILE);
-    load_rows<DP>(&km, k_slots + slot * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
+    load_rows<DT, DP>(&km, k_slots + slot * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
   };
   auto load_v = [&](int s) {
     const int slot = s % S::VS;
     arrive_expect_tx(&sh.v.full[slot], S::TILE);
-    load_rows<DP>(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], hk * f.v_h, frame(s), (int)b * f.v_b);
+    load_rows<DT, DP>(&vm, v_slots + slot * S::TILE, &sh.v.full[slot], hk * f.v_h, frame(s), (int)b * f.v_b);
   };
   const int group = warp >> 2, r = threadIdx.x & 127;
   const int row = i0 + r / P, head = h0 + r % P;
@@ -181,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     sh.gave_up = 0;
     if (some) {
       arrive_expect_tx(&sh.rows_full, 2 * S::TILE);
-      load_rows<DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
-      load_rows<DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
+      load_rows<DT, DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
+      load_rows<DT, DP>(&gm, g_tile, &sh.rows_full, h0 * f.go_h, i0, (int)b * f.go_b);
     }
     if (T > 0) {  // no windows: the walk is known
       load_k(0);
@@ -197,7 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
   if (a.windows) walk(hull_of<8>(sh.hull));
-  constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ
+  constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ,
+  constexpr unsigned kThird = kAcc + 64;                 // the third plane of dS (float32)
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
@@ -241,21 +246,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && wait(&sh.k.full[slot], (unsigned)(s / S::KS) & 1);
         tc_fence_after();
         if (ok)
-          mma_rows<DP>(tmem + (s & 1) * kRows, qa, S::CHUNK, ka + slot * S::TILE, S::CHUNK, i_s, false);
+          mma_rows_planes<DT, DP>(tmem + (s & 1) * kRows, qa, ka + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
       };
       auto grads = [&](int s) {  // dP of tile s; its scores came before
         const int slot = s % S::VS;
         ok = ok && wait(&sh.v.full[slot], (unsigned)(s / S::VS) & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_rows<DP>(tmem + kDp, ga, S::CHUNK, va + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_rows_planes<DT, DP>(tmem + kDp, ga, va + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
         mma_commit(&sh.scores);
         mma_commit(&sh.v.empty[slot]);
       };
       scores(0);
       grads(0);
       for (int s = 0; ok && s < T; ++s) {
-        if (s + 1 < T) {
+        if (S::KS > 1 && s + 1 < T) {
           scores(s + 1);
           ok = ok && wait(&sh.dp_free, s & 1);
           grads(s + 1);
@@ -265,10 +270,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const int slot = s % S::KS;
         const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
-        mma_across<64>(tmem + kAcc, ds, at, S::CHUNK, i_o, s > 0);
-        mma_across<64>(tmem + kAcc, ds + 64, at + 64 * 128, S::CHUNK, i_o, true);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)  // the columns of each group
+          mma_across_planes<DT, 64>(tmem + kAcc, ds + g * 64, ds + g * 64 + 32, tmem + kThird + g * 32,
+                                    at + g * 64 * 128, S::CHUNK, S::PLANE, i_o,
+                                    (S::PLANES == 1 && s > 0) || g > 0);
         mma_commit(&sh.k.empty[slot]);
         if (s + 1 == T) mma_commit(&sh.done);
+        if (S::KS == 1 && s + 1 < T) {  // k's slot is free after these products only
+          scores(s + 1);
+          grads(s + 1);
+        }
       }
       if (!ok) {
         mma_commit(&sh.drained);
@@ -285,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
       float x = 0.0f;
       if (real)
-        x = dot16<DT, DP / 2>(
+        x = dot_rows<DT, DP / 2>(
             static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
             static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
       if (group == 1) sh.half[r] = x;
@@ -303,14 +315,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const float c = a.scale * kLog2e;
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    // float32: this thread's 32 columns of dQ, to which each tile's part is added
+    float acc[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) acc[k] = 0.0f;
+    auto add_tile = [&]() {
+      if constexpr (S::PLANES == 3) {
+        unsigned o[32];
+        tmem_ld32(tmem + lanes + kAcc + group * 32, o);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) acc[k] += __uint_as_float(o[k]);
+      }
+    };
     bool ok = true;
     for (int s = 0; s < T; ++s) {
       ok = wait(&sh.scores, s & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
+      if (s > 0) add_tile();  // dQ of the tile before was issued before these scores
       const unsigned s_col = tmem + lanes + (s & 1) * kRows + group * 64,
                      p_col = tmem + lanes + kDp + group * 64;
-      unsigned x[2][32], y[2][32], out[32];
+      unsigned x[2][32], y[2][32], out[S::PLANES][32];
       tmem_ld32(s_col, x[0]);
       tmem_ld32(s_col + 32, x[1]);
       tmem_ld32(p_col, y[0]);
@@ -337,9 +363,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 z = fma2(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), c2, l2);
         const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
         const float2 ds = mul2(p, add2(pair(y[i >> 5][i & 31], y[i >> 5][(i + 1) & 31]), d2));
-        out[i / 2] = pack2<DT>(ds.x, ds.y);
+        unsigned planes[S::PLANES];
+        split2<DT>(ds, planes);
+#pragma unroll
+        for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
       }
-      tmem_st32(s_col, out);
+      tmem_st32(s_col, out[0]);
+      if constexpr (S::PLANES == 3) {
+        tmem_st32(s_col + 32, out[1]);
+        tmem_st32(tmem + lanes + kThird + group * 32, out[2]);
+      }
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sh.ds_ready);
@@ -349,18 +382,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
+    if (T > 0) add_tile();
 #pragma unroll
     for (int i = 0; i < DP / 64; ++i) {
       const int d0 = (group * (DP / 64) + i) * 32;
       unsigned o[32];
-      if (T > 0) {
+      if (S::PLANES == 1 && T > 0) {
         tmem_ld32(tmem + lanes + kAcc + d0, o);
         tmem_wait_ld();
       }
       float v[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * a.scale : 0.0f;
+      for (int k = 0; k < 32; ++k) {
+        const float x = S::PLANES == 3 ? acc[k] : __uint_as_float(o[k]);
+        v[k] = bad ? NAN : T > 0 && alive ? x * a.scale : 0.0f;
+      }
       if (f.p.dq_splits == 1)
         stage32<DT>(q_tile, S::CHUNK, r, d0, v);  // every product with q is done
       else if (row < a.Lq)
@@ -372,8 +408,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_async_shared();
       named_barrier<256>(1);
       if (threadIdx.x == 0) {
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_store_4d(&dqm, q_tile + ch * S::CHUNK, ch * 64, h0 * f.dq_h, i0, (int)b * f.dq_b);
+        constexpr int kColumns = DT == kF32 ? 32 : 64;  // of a chunk
+        for (int ch = 0; ch < DP / kColumns; ++ch)
+          if (ch * kColumns < a.D)
+            tma_store_4d(&dqm, q_tile + ch * S::CHUNK, ch * kColumns, h0 * f.dq_h, i0, (int)b * f.dq_b);
         tma_store_commit();
         tma_store_wait_read();
       }
@@ -406,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
                        const __grid_constant__ CUtensorMap dkm, const __grid_constant__ CUtensorMap dvm,
                        const __grid_constant__ BwdArgs f) {
-  typedef BwdShape<DP> S;
+  typedef BwdShape<DT, DP> S;
   extern __shared__ unsigned char raw[];
   __shared__ DkvShared sh;
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -452,8 +490,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.gave_up = 0;
       if (t1 > t0) {
         arrive_expect_tx(&sh.frames_full, 2 * S::TILE);
-        load_rows<DP>(&km, k_tile, &sh.frames_full, hk * f.k_h, j0, (int)b * f.k_b);
-        load_rows<DP>(&vm, v_tile, &sh.frames_full, hk * f.v_h, j0, (int)b * f.v_b);
+        load_rows<DT, DP>(&km, k_tile, &sh.frames_full, hk * f.k_h, j0, (int)b * f.k_b);
+        load_rows<DT, DP>(&vm, v_tile, &sh.frames_full, hk * f.v_h, j0, (int)b * f.v_b);
       }
     }
   } else if (warp == 9) {
@@ -487,8 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Rows past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last row tile of
   // each walk over the rows a warp of its own zeroes them (unless TMA did, past the tensor's end):
   // the loads then arrive at q_tail and g_tail, and that warp hands the tiles on.
-  auto cut = [&](int t) { return n.nq < a.Lq && (t % row_tiles + 1) * per > n.nq; };
+  auto cut = [&](int t) {
+    return S::PLANES == 1 && n.nq < a.Lq && (t % row_tiles + 1) * per > n.nq;  // planes end in zeros
+  };
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = 2 * kRows + DP;
+  constexpr unsigned kThird = kDk + DP;  // the third planes of P and of dS (float32)
 
   if (warp >= 8) {
     warpgroup_give_registers<kOtherRegs>();
@@ -503,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         unsigned long long *bar = cut(t) ? &sh.q_tail[slot] : &sh.q.full[slot];
         arrive_expect_tx(bar, S::TILE);
-        load_rows<DP>(&qm, q_slots + slot * S::TILE, bar, h * f.q_h, l, (int)b * f.q_b);
+        load_rows<DT, DP>(&qm, q_slots + slot * S::TILE, bar, h * f.q_h, l, (int)b * f.q_b);
         ok = wait(&sh.g.empty[slot], turn);
         if (!ok) {
           ++s;
@@ -511,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         bar = cut(t) ? &sh.g_tail[slot] : &sh.g.full[slot];
         arrive_expect_tx(bar, S::TILE);
-        load_rows<DP>(&gm, g_slots + slot * S::TILE, bar, h * f.go_h, l, (int)b * f.go_b);
+        load_rows<DT, DP>(&gm, g_slots + slot * S::TILE, bar, h * f.go_h, l, (int)b * f.go_b);
       }
       if (!ok) {
         Waiter::drain(&sh.frames_full, 0);
@@ -546,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && wait(&sh.q.full[slot], (unsigned)(s / S::RS) & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_rows<DP>(tmem, ka, S::CHUNK, qa + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_rows_planes<DT, DP>(tmem, ka, qa + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
         mma_commit(&sh.s_full);
       };
       auto grads = [&](int s) {  // dP^T
@@ -554,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = ok && wait(&sh.g.full[slot], (unsigned)(s / S::RS) & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_rows<DP>(tmem + kDp, va, S::CHUNK, ga + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_rows_planes<DT, DP>(tmem + kDp, va, ga + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
         mma_commit(&sh.dp_full);
       };
       int t = start;
@@ -566,17 +607,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         if (!ok) break;
         const unsigned g_at = ga + slot * S::TILE, q_at = qa + slot * S::TILE;
-        mma_across<64>(tmem + kDv, tmem, g_at, S::CHUNK, i_o, s > 0);  // dV += P^T dO
-        mma_across<64>(tmem + kDv, tmem + 64, g_at + 64 * 128, S::CHUNK, i_o, true);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)  // dV += P^T dO, the columns of each group
+          mma_across_planes<DT, 64>(tmem + kDv, tmem + g * 64, tmem + g * 64 + 32, tmem + kThird + g * 32,
+                                    g_at + g * 64 * 128, S::CHUNK, S::PLANE, i_o,
+                                    (S::PLANES == 1 && s > 0) || g > 0);
         mma_commit(&sh.g.empty[slot]);
-        if (after < t1) scores(s + 1);
+        if (S::RS > 1 && after < t1) scores(s + 1);
         ok = ok && wait(&sh.ds_ready, s & 1);
         tc_fence_after();
         if (!ok) break;
-        mma_across<64>(tmem + kDk, tmem + kDp, q_at, S::CHUNK, i_o, s > 0);  // dK += dS^T Q
-        mma_across<64>(tmem + kDk, tmem + kDp + 64, q_at + 64 * 128, S::CHUNK, i_o, true);
+#pragma unroll
+        for (int g = 0; g < 2; ++g)  // dK += dS^T Q
+          mma_across_planes<DT, 64>(tmem + kDk, tmem + kDp + g * 64, tmem + kDp + g * 64 + 32,
+                                    tmem + kThird + 64 + g * 32, q_at + g * 64 * 128, S::CHUNK, S::PLANE, i_o,
+                                    (S::PLANES == 1 && s > 0) || g > 0);
         mma_commit(&sh.q.empty[slot]);
         if (after >= t1) mma_commit(&sh.done);
+        if (S::RS == 1 && after < t1) scores(s + 1);  // q's slot is free after these products only
         if (after < t1) grads(s + 1);
         t = after;
       }
@@ -628,6 +676,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
     const float c = a.scale * kLog2e;
     const bool past = __any_sync(0xffffffffu, j >= n.nk);
+    // float32: this thread's 32 columns of dV and of dK, to which each tile's part is added
+    float acc[2][32];
+#pragma unroll
+    for (int k = 0; k < 64; ++k) acc[k / 32][k % 32] = 0.0f;
+    auto add_tile = [&]() {
+      if constexpr (S::PLANES == 3) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          unsigned o[32];
+          tmem_ld32(tmem + lanes + (i ? kDk : kDv) + group * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) acc[i][k] += __uint_as_float(o[k]);
+        }
+      }
+    };
     bool ok = true;
     int s = 0;
     if (any)
@@ -636,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait(&sh.stat_full[buf], (unsigned)(s / kStats) & 1) && wait(&sh.s_full, s & 1);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
-        unsigned x[2][32], out[32];
+        if (s > 0) add_tile();  // the products of the tile before were issued before these scores
+        unsigned x[2][32], out[S::PLANES][32];
         tmem_ld32(s_col, x[0]);
         tmem_ld32(s_col + 32, x[1]);
         tmem_wait_ld();
@@ -666,8 +731,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int i = 0; i < 64; i += 2)
-          out[i / 2] = pack2<DT>(__uint_as_float(x[i >> 5][i & 31]), __uint_as_float(x[i >> 5][(i + 1) & 31]));
-        tmem_st32(s_col, out);
+        {
+          unsigned planes[S::PLANES];
+          split2<DT>(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), planes);
+#pragma unroll
+          for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
+        }
+        tmem_st32(s_col, out[0]);
+        if constexpr (S::PLANES == 3) {
+          tmem_st32(s_col + 32, out[1]);
+          tmem_st32(tmem + lanes + kThird + group * 32, out[2]);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sh.p_ready);
@@ -687,10 +761,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 g0 = pair(g[0], g[1]), g1 = pair(g[2], g[3]);
           const float2 v0 = mul2(pair(p[0], p[1]), DT == kF16 ? fma2(g0, un, d0) : add2(g0, d0)),
                        v1 = mul2(pair(p[2], p[3]), DT == kF16 ? fma2(g1, un, d1) : add2(g1, d1));
-          out[i / 2] = pack2<DT>(v0.x, v0.y);
-          out[i / 2 + 1] = pack2<DT>(v1.x, v1.y);
+          unsigned p0[S::PLANES], p1[S::PLANES];
+          split2<DT>(v0, p0);
+          split2<DT>(v1, p1);
+#pragma unroll
+          for (int k = 0; k < S::PLANES; ++k) {
+            out[k][i / 2] = p0[k];
+            out[k][i / 2 + 1] = p1[k];
+          }
         }
-        tmem_st32(d_col, out);
+        tmem_st32(d_col, out[0]);
+        if constexpr (S::PLANES == 3) {
+          tmem_st32(d_col + 32, out[1]);
+          tmem_st32(tmem + lanes + kThird + 64 + group * 32, out[2]);
+        }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sh.ds_ready);
@@ -701,37 +785,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_after();
     const bool bad = !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
-    // group 0 stores dv, group 1 dk
-    unsigned char *out = group ? k_tile : v_tile;  // every product with them is done
-    const float scale = group ? a.scale : kUnshift<DT>;
     const bool keep = j < n.nk;  // frames past the end: their lanes hold no sums
-#pragma unroll
-    for (int i = 0; i < DP / 32; ++i) {
-      unsigned o[32];
-      if (any) {
-        tmem_ld32(tmem + lanes + (group ? kDk : kDv) + i * 32, o);
-        tmem_wait_ld();
-      }
-      float v[32];
-#pragma unroll
-      for (int k = 0; k < 32; ++k)
-        v[k] = bad ? NAN : any && keep ? __uint_as_float(o[k]) * scale : 0.0f;
-      if (f.p.dkv_splits == 1) {
-        stage32<DT>(out, S::CHUNK, threadIdx.x & 127, i * 32, v);
-      } else if (j < a.Lk) {
-        const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
-        store_columns(f.part + (((group ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * DP + i * 32) * kRows +
+    const long long ctas = (long long)f.p.f_tiles * a.Hkv * a.B;
+    // 32 columns of dv (which 0) or dk (1), through the tile that no product needs any more
+    auto put = [&](int which, int d0, const float (&v)[32]) {
+      if (f.p.dkv_splits == 1)
+        stage32<DT>(which ? k_tile : v_tile, S::CHUNK, threadIdx.x & 127, d0, v);
+      else if (j < a.Lk)
+        store_columns(f.part + (((which ? ctas * f.p.dkv_splits : 0) + split * ctas + cta) * DP + d0) * kRows +
                           (threadIdx.x & 127), kRows, v);
-      }
       __syncwarp();
+    };
+    if constexpr (S::PLANES == 3) {  // each group has half of the columns of both
+      if (any) add_tile();
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : any && keep ? acc[i][k] * (i ? a.scale : 1.0f) : 0.0f;
+        put(i, group * 32, v);
+      }
+    } else {  // group 0 has dv, group 1 dk
+      const float scale = group ? a.scale : kUnshift<DT>;
+#pragma unroll
+      for (int i = 0; i < DP / 32; ++i) {
+        unsigned o[32];
+        if (any) {
+          tmem_ld32(tmem + lanes + (group ? kDk : kDv) + i * 32, o);
+          tmem_wait_ld();
+        }
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          v[k] = bad ? NAN : any && keep ? __uint_as_float(o[k]) * scale : 0.0f;
+        put(group, i * 32, v);
+      }
     }
     if (f.p.dkv_splits == 1) {
       fence_async_shared();
-      named_barrier<128>(1 + group);
+      named_barrier<256>(1);
       if ((threadIdx.x & 127) == 0) {
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_store_4d(group ? &dkm : &dvm, out + ch * S::CHUNK, ch * 64,
-                       hk * (group ? f.dk_h : f.dv_h), j0, (int)b * (group ? f.dk_b : f.dv_b));
+        constexpr int kColumns = DT == kF32 ? 32 : 64;  // of a chunk
+        for (int ch = 0; ch < DP / kColumns; ++ch)
+          if (ch * kColumns < a.D)
+            tma_store_4d(group ? &dkm : &dvm, (group ? k_tile : v_tile) + ch * S::CHUNK, ch * kColumns,
+                         hk * (group ? f.dk_h : f.dv_h), j0, (int)b * (group ? f.dk_b : f.dv_b));
         tma_store_commit();
         tma_store_wait_read();
       }
@@ -1035,7 +1133,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
       float x = 0.0f;
       if (real)
-        x = dot16<DT, DP / 2>(
+        x = dot_rows<DT, DP / 2>(
             static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
             static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
       if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
@@ -1194,16 +1292,21 @@ __global__ void __launch_bounds__(256) attn_add_kernel(const __grid_constant__ B
   __syncthreads();
   if (threadIdx.x < 128) {
     const int rr = threadIdx.x / 4, d = threadIdx.x % 4 * 8, at = first + rr / per;
-    if (at < count && d0 + d < a.D) {
+    const float *x = &out[rr][d];
+    if (at >= count || d0 + d >= a.D) {
+    } else if constexpr (DT == kF32) {
+      float *dst = static_cast<float *>(to) + base + at * sl + rr % per * sh + d0 + d;
+      *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+      if (d0 + d + 4 < a.D) *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
       unsigned short *dst = static_cast<unsigned short *>(to) + base + at * sl + rr % per * sh + d0 + d;
-      const float *x = &out[rr][d];
       *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
                                                    pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
     }
   }
 }
 
-BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
+BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
   BwdPlan p;
   const int G = H / Hkv;
   p.P = attn_row_pack(G);
@@ -1217,7 +1320,7 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
     return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
   };
   p.dq_splits = splits(B * p.packs * p.tiles, p.f_tiles);
-  p.one = D <= 64 && p.P == G && p.tiles == 1;
+  p.one = dtype != kF32 && D <= 64 && p.P == G && p.tiles == 1;
   p.dkv_splits = p.one ? 1 : splits(B * Hkv * p.f_tiles, (long long)(G / p.P) * p.tiles);
   return p;
 }
@@ -1243,7 +1346,7 @@ template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaSt
 
 template <int DT, int DP>
 cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
-  typedef BwdShape<DP> S;
+  typedef BwdShape<DT, DP> S;
   const AttnArgs &a = f.a;
   const long long rows = a.B * f.p.packs * f.p.tiles, frames = a.B * a.Hkv * f.p.f_tiles;
   const unsigned per_tile = (kRows / 32) * (DP / 32);  // blocks of the adding kernel
@@ -1267,43 +1370,86 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   return e;
 }
 
+// The workspace: planes of q, dO, k, v (float32), then the partial sums of splits.
+struct BwdSpace {
+  size_t q, go, k, v, part, total;
+};
+BwdSpace space(const BwdPlan &p, long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
+  BwdSpace s = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  if (dtype == kF32) {
+    s.q = take(plane_bytes(B, Lq, H));
+    s.go = take(plane_bytes(B, Lq, H));
+    s.k = take(plane_bytes(B, Lk, Hkv));
+    s.v = take(plane_bytes(B, Lk, Hkv));
+  }
+  const size_t tile = (size_t)kRows * (D <= 64 ? 64 : 128) * 4;
+  const size_t dq = p.dq_splits > 1 ? tile * B * p.packs * p.tiles * p.dq_splits : 0;
+  const size_t dkv = p.dkv_splits > 1 ? 2 * tile * B * Hkv * p.f_tiles * p.dkv_splits : 0;
+  s.part = take(dq > dkv ? dq : dkv);
+  s.total = at;
+  return s;
+}
+
 }  // namespace
 
-size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
-  const BwdPlan p = plan(B, Lq, Lk, H, Hkv, D);
-  const size_t tile = (size_t)kRows * (D <= 64 ? 64 : 128) * 4;
-  size_t dq = p.dq_splits > 1 ? tile * B * p.packs * p.tiles * p.dq_splits : 0;
-  size_t dkv = p.dkv_splits > 1 ? 2 * tile * B * Hkv * p.f_tiles * p.dkv_splits : 0;
-  return align256(dq > dkv ? dq : dkv);
+size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
+  return space(plan(B, Lq, Lk, H, Hkv, D, dtype), B, Lq, Lk, H, Hkv, D, dtype).total;
 }
 
 bool attn_bwd_tc_fits(const AttnArgs &a, int dtype) {
   auto fits = [&](const void *p, const Strides &s, long long L, int H) {
-    return map_fits(p, a.B, L, H, a.D, s.b, s.l, s.h);
+    return map_fits(dtype, p, a.B, L, H, a.D, s.b, s.l, s.h);
   };
-  const bool heads = attn_row_pack(a.G) == 1 || (a.sq.h != 0 && a.sgo.h != 0);
-  return dtype != kF32 && a.D <= 128 && a.Lk > 0 && a.Lq > 0 && heads &&
-         fits(a.q, a.sq, a.Lq, a.H) && fits(a.k, a.sk, a.Lk, a.Hkv) &&
-         fits(a.v, a.sv, a.Lk, a.Hkv) && fits(a.out, a.so, a.Lq, a.H) &&
-         fits(a.go, a.sgo, a.Lq, a.H) && fits(a.dq, a.sdq, a.Lq, a.H) &&
-         fits(a.dk, a.sdk, a.Lk, a.Hkv) && fits(a.dv, a.sdv, a.Lk, a.Hkv);
+  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D)) return false;
+  // out and dO are read in vectors of 16 bytes, the results are stored by TMA
+  if (!fits(a.out, a.so, a.Lq, a.H) || !fits(a.go, a.sgo, a.Lq, a.H) || !fits(a.dq, a.sdq, a.Lq, a.H) ||
+      !fits(a.dk, a.sdk, a.Lk, a.Hkv) || !fits(a.dv, a.sdv, a.Lk, a.Hkv))
+    return false;
+  return dtype == kF32 || ((attn_row_pack(a.G) == 1 || (a.sq.h != 0 && a.sgo.h != 0)) &&
+                           fits(a.q, a.sq, a.Lq, a.H) && fits(a.k, a.sk, a.Lk, a.Hkv) &&
+                           fits(a.v, a.sv, a.Lk, a.Hkv));
 }
 
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
   BwdArgs f = {};
   f.a = a;
-  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D);
-  f.part = static_cast<float *>(workspace);
+  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D, dtype);
+  const BwdSpace at = space(f.p, a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D, dtype);
+  char *ws = static_cast<char *>(workspace);
+  f.part = reinterpret_cast<float *>(ws + at.part);
   Maps m;
   const int per = kRows / f.p.P;
-  if (!encode_map(&m.q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, per) ||
-      !encode_map(&m.go, a.go, dtype, a.B, a.Lq, a.H, a.D, a.sgo.b, a.sgo.l, a.sgo.h, f.p.P, per) ||
-      !encode_map(&m.k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
-      !encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows) ||
-      !encode_map(&m.dq, a.dq, dtype, a.B, a.Lq, a.H, a.D, a.sdq.b, a.sdq.l, a.sdq.h, f.p.P, per) ||
-      !encode_map(&m.dk, a.dk, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdk.b, a.sdk.l, a.sdk.h, 1, kRows) ||
-      !encode_map(&m.dv, a.dv, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdv.b, a.sdv.l, a.sdv.h, 1, kRows))
-    return cudaErrorInvalidValue;
+  bool ok = encode_map(&m.dq, a.dq, dtype, a.B, a.Lq, a.H, a.D, a.sdq.b, a.sdq.l, a.sdq.h, f.p.P, per) &&
+            encode_map(&m.dk, a.dk, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdk.b, a.sdk.l, a.sdk.h, 1, kRows) &&
+            encode_map(&m.dv, a.dv, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdv.b, a.sdv.l, a.sdv.h, 1, kRows);
+  if (dtype == kF32) {
+    auto source = [&](const void *p, const Strides &s, const long long *lens, int L, int H, size_t to) {
+      return PlaneSource{static_cast<const float *>(p), s.b, s.l, s.h, lens, L, H,
+                         reinterpret_cast<unsigned short *>(ws + to)};
+    };
+    const PlaneSource t[4] = {source(a.q, a.sq, a.q_lens, a.Lq, a.H, at.q),
+                              source(a.go, a.sgo, a.q_lens, a.Lq, a.H, at.go),
+                              source(a.k, a.sk, a.k_lens, a.Lk, a.Hkv, at.k),
+                              source(a.v, a.sv, a.k_lens, a.Lk, a.Hkv, at.v)};
+    const cudaError_t e = launch_planes(t, 4, a.B, a.D, stream);
+    if (e != cudaSuccess) return e;
+    ok = ok && encode_planes(&m.q, t[0].dst, a.B, a.Lq, a.H, f.p.P, per) &&
+         encode_planes(&m.go, t[1].dst, a.B, a.Lq, a.H, f.p.P, per) &&
+         encode_planes(&m.k, t[2].dst, a.B, a.Lk, a.Hkv, 1, kRows) &&
+         encode_planes(&m.v, t[3].dst, a.B, a.Lk, a.Hkv, 1, kRows);
+  } else {
+    ok = ok && encode_map(&m.q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, per) &&
+         encode_map(&m.go, a.go, dtype, a.B, a.Lq, a.H, a.D, a.sgo.b, a.sgo.l, a.sgo.h, f.p.P, per) &&
+         encode_map(&m.k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) &&
+         encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   f.q_b = m.q.b_mul;
   f.q_h = m.q.h_mul;
   f.go_b = m.go.b_mul;
@@ -1318,6 +1464,7 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.dk_h = m.dk.h_mul;
   f.dv_b = m.dv.b_mul;
   f.dv_h = m.dv.h_mul;
+  if (dtype == kF32) return launch<kF32, 64>(f, m, stream);
   if (f.p.one) return dtype == kF16 ? launch_one<kF16>(f, m, stream) : launch_one<kBF16>(f, m, stream);
   if (dtype == kF16)
     return a.D <= 64 ? launch<kF16, 64>(f, m, stream) : launch<kF16, 128>(f, m, stream);

@@ -88,14 +88,15 @@ template <int WARPS> __device__ __forceinline__ int2 hull_of(const Hull &h) {
 }
 
 // Tensor-core kernels: which calls they take, their workspace (of the sizes alone), and the launch.
-bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);
-size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
+bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D);  // by type and sizes
+bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);                      // and by strides and alignment
+size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
 // Few rows: a kernel that reads k and v at memory speed.
 bool attn_step_fits(const AttnArgs &a, int dtype, bool tc_fits);
 cudaError_t launch_attn_step(const AttnArgs &a, int dtype, cudaStream_t stream);
 bool attn_bwd_tc_fits(const AttnArgs &a, int dtype);
-size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D);
+size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
 // Heads that share a row tile, of a group of G: the largest power of two that divides G, up to 16.
 int attn_row_pack(int G);

@@ -47,16 +47,18 @@ struct FwdArgs {
   float *part_o, *part_l;            // splits > 1: [split][CTA row][DP], [split][CTA row]
 };
 
-template <int DP, bool WIDE> struct FwdShape {
+template <int DT, int DP, bool WIDE> struct FwdShape {
   static constexpr int CHUNKS = DP / 64;
   static constexpr int CHUNK = kRows * 128;          // bytes
-  static constexpr int TILE = CHUNKS * CHUNK;
+  static constexpr int PLANES = kPlanes<DT>;
+  static constexpr int PLANE = CHUNKS * CHUNK;
+  static constexpr int TILE = PLANES * PLANE;
   static constexpr int NS = WIDE ? 2 : 1;            // streams
-  static constexpr int SLOTS = WIDE ? (DP == 64 ? 8 : 4) : (DP == 64 ? 5 : 2);
+  static constexpr int SLOTS = PLANES == 3 ? (WIDE ? 2 : 3) : WIDE ? (DP == 64 ? 8 : 4) : (DP == 64 ? 5 : 2);
   static constexpr int BYTES = (NS + SLOTS) * TILE;
   static constexpr int THREADS = NS * 128 + 128;     // softmax; TMA, MMA, tails, a spare warp
   static constexpr int CTAS = WIDE ? 1 : 2;          // of an SM
-  static constexpr int TMEM = WIDE ? 512 : 256;      // columns: S and O of each stream
+  static constexpr int TMEM = WIDE ? 512 : 256;      // columns: S and O of each stream, a third plane of P
   // registers of a thread: at launch, then of the softmax warpgroups and of the other one, which
   // adds up to the same: 3 x 168 = 2 x 208 + 88, 2 x 128 = 200 + 56
   static constexpr int REGS = WIDE ? 168 : 128;
@@ -71,26 +73,30 @@ struct FwdShared {
   Hull hull;
 };
 
-// 32 scores of a row (float32 bits) to weights 2^(s c - ref), packed in pairs and added to sum.
-template <int DT>
-__device__ __forceinline__ void exp_pack(const unsigned (&s)[32], float c, float neg, unsigned *out,
-                                         float2 &sum) {
+// 32 scores of a row (float32 bits) to weights 2^(s c - ref), packed in pairs of each plane and added to
+// sum.
+template <int DT, int N>
+__device__ __forceinline__ void exp_pack(const unsigned (&s)[32], float c, float neg,
+                                         unsigned (&out)[kPlanes<DT>][N], int at, float2 &sum) {
   const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
     const float2 z = fma2(pair(s[i], s[i + 1]), c2, n2);
     const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
     sum = add2(sum, p);
-    out[i / 2] = pack2<DT>(p.x, p.y);
+    unsigned planes[kPlanes<DT>];
+    split2<DT>(p, planes);
+#pragma unroll
+    for (int k = 0; k < kPlanes<DT>; ++k) out[k][at + i / 2] = planes[k];
   }
 }
 
 template <int DT, int DP, bool WIDE>
-__global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE>::CTAS)
+__global__ void __launch_bounds__(FwdShape<DT, DP, WIDE>::THREADS, FwdShape<DT, DP, WIDE>::CTAS)
     attn_fwd_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap km,
                        const __grid_constant__ CUtensorMap vm, const __grid_constant__ CUtensorMap om,
                        const __grid_constant__ FwdArgs f) {
-  typedef FwdShape<DP, WIDE> S;
+  typedef FwdShape<DT, DP, WIDE> S;
   extern __shared__ unsigned char raw[];
   __shared__ FwdShared sh;
   unsigned char *tiles = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
@@ -121,7 +127,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     const int2 steps = share_of((hull.y - hull.x + kRows - 1) / kRows, split, f.p.splits);
     begin = hull.x + steps.x * kRows;
     T = steps.y - steps.x;
-    cut = T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;
+    cut = S::PLANES == 1 && T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;  // planes end in zeros
   };
   if (!a.windows && some) walk(make_int2(0, n.nk));
   auto frame = [&](int s) { return begin + s * kRows; };
@@ -130,7 +136,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     const bool values = at & 1;
     unsigned long long *bar = cut && at == 2 * T - 1 ? &sh.tail_full : &sh.full[slot];
     arrive_expect_tx(bar, S::TILE);
-    for (int ch = 0; ch < S::CHUNKS; ++ch)
+    for (int ch = 0; ch < S::PLANES * S::CHUNKS; ++ch)
       tma_load_4d(values ? &vm : &km, slots + slot * S::TILE + ch * S::CHUNK, bar, ch * 64,
                   hk * (values ? f.v_h : f.k_h), frame(s), (int)b * (values ? f.v_b : f.k_b));
   };
@@ -162,7 +168,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     if (some) {
       arrive_expect_tx(&sh.q_full, S::NS * S::TILE);
       for (int t = 0; t < S::NS; ++t)
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
+        for (int ch = 0; ch < S::PLANES * S::CHUNKS; ++ch)
           tma_load_4d(&qm, q_tile + t * S::TILE + ch * S::CHUNK, &sh.q_full, ch * 64, h0 * f.q_h,
                       i0 + t * per, (int)b * f.q_b);
     }
@@ -213,8 +219,8 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
         tc_fence_after();
         if (!ok) return;
         const int slot = at % S::SLOTS;
-        mma_rows<DP>(tmem + w * kRows, q_addr + w * S::TILE, S::CHUNK,
-                     s_addr + slot * S::TILE, S::CHUNK, i_s, false);
+        mma_rows_planes<DT, DP>(tmem + w * kRows, q_addr + w * S::TILE, s_addr + slot * S::TILE, S::CHUNK,
+                                S::PLANE, i_s);
         mma_commit(&sh.s_full[w]);
         if (w == S::NS - 1) mma_commit(&sh.empty[slot]);
       };
@@ -223,8 +229,23 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
         ok = ok && wait(&sh.p_ready[w], s & 1);
         tc_fence_after();
         if (!ok) return;
-        mma_across<kRows>(tmem + S::NS * kRows + w * DP, tmem + w * kRows, s_addr + slot * S::TILE,
-                          S::CHUNK, i_o, s > 0);
+        const unsigned o_at = tmem + S::NS * kRows + w * DP, p_at = tmem + w * kRows,
+                       third = tmem + S::NS * (kRows + DP) + w * 64, v_at = s_addr + slot * S::TILE;
+        if constexpr (S::PLANES == 1) {
+          mma_across<kRows>(o_at, p_at, v_at, S::CHUNK, i_o, s > 0);
+        } else {  // this tile's part of O: 32 frames' planes 0 and 1 lie where their scores were
+#pragma unroll
+          for (int i = 0; i < kPlanePairs<DT>; ++i)
+#pragma unroll
+            for (int k = 0; k < kRows / 16; ++k) {
+              const unsigned in = k / 2 * 32 + k % 2 * 8;
+              const unsigned pa = plane_a<DT>(i) == 0   ? p_at + in
+                                  : plane_a<DT>(i) == 1 ? p_at + in + 16
+                                                        : third + k * 8;
+              mma_ts(o_at, pa, desc_mn_major(v_at + plane_b<DT>(i) * S::PLANE + k * 2048, S::CHUNK), i_o,
+                     i + k > 0);
+            }
+        }
         if (w == S::NS - 1) mma_commit(&sh.empty[slot]);
         if (s + 1 == T) mma_commit(&sh.o_full[w]);
       };
@@ -254,61 +275,120 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     float ref = -INFINITY, l = 0.0f;  // reference maximum (base 2) and sum
     // a row that sees nothing holds whatever its tile does: its result is set at the end
     const bool alive = range.y > range.x;
+    float o_row[S::PLANES == 3 ? DP : 1];  // float32: the row of O, to which each tile's part is added
+#pragma unroll
+    for (int k = 0; k < (S::PLANES == 3 ? DP : 1); ++k) o_row[k] = 0.0f;
+    auto add_tile = [&]() {
+      if constexpr (S::PLANES == 3) {
+#pragma unroll
+        for (int i = 0; i < DP / 32; ++i) {
+          unsigned o[32];
+          tmem_ld32(o_col + i * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o_row[i * 32 + k] += __uint_as_float(o[k]);
+        }
+      }
+    };
     bool ok = true;
     for (int s = 0; s < T; ++s) {
       ok = wait(&sh.s_full[stream], s & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      unsigned x[4][32];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, x[i]);
-      tmem_wait_ld();
       const int j0 = frame(s);
-      if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + kRows))) {
-        const int lo = range.x - j0;
-        const unsigned len = (unsigned)(range.y - range.x);
+      const bool masked = __any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + kRows));
+      const int lo = range.x - j0;
+      const unsigned len = (unsigned)(range.y - range.x);
+      if constexpr (S::PLANES == 3) {
+        // the scores are read twice, 32 at a time: registers hold the row of O
+        unsigned x[32];
+        auto scores = [&](int i) {
+          tmem_ld32(s_col + i * 32, x);
+          tmem_wait_ld();
+          if (masked)
 #pragma unroll
-        for (int i = 0; i < 128; ++i)
-          if ((unsigned)(i - lo) >= len) x[i >> 5][i & 31] = 0xff800000u;  // -inf
-      }
-      float m0 = -INFINITY, m1 = -INFINITY;
+            for (int k = 0; k < 32; ++k)
+              if ((unsigned)(i * 32 + k - lo) >= len) x[k] = 0xff800000u;  // -inf
+        };
+        if (s > 0) add_tile();
+        float m0 = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) {
-        m0 = max3(m0, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
-        m1 = max3(m1, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
-        m0 = max3(m0, __uint_as_float(x[2][i]), __uint_as_float(x[2][i + 1]));
-        m1 = max3(m1, __uint_as_float(x[3][i]), __uint_as_float(x[3][i + 1]));
-      }
-      const float top = fmaxf(m0, m1) * c;
-      const bool grow = alive && top > ref + (kLazy + kShift<DT>);  // from -inf: any score
-      if (__any_sync(0xffffffffu, grow)) {
-        const float now = grow ? top - kShift<DT> : ref;
-        const float scale = grow ? fast_exp2(ref - now) : 1.0f;
-        if (s > 0) {  // the products up to tile s - 1 are done: S of tile s came after them
-          unsigned o[32];
+        for (int i = 0; i < 4; ++i) {
+          scores(i);
 #pragma unroll
-          for (int i = 0; i < DP / 32; ++i) {
-            tmem_ld32(o_col + i * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
-            tmem_st32(o_col + i * 32, o);
-          }
+          for (int k = 0; k < 32; k += 2) m0 = max3(m0, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
         }
-        l *= scale;
-        ref = now;
-      }
-      const float neg = ref == -INFINITY ? 0.0f : -ref;
-      unsigned p[32];
-      float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+        const float top = m0 * c;
+        if (alive && top > ref) {
+          const float scale = fast_exp2(ref - top);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        exp_pack<DT>(x[2 * i], c, neg, p, sum0);
-        exp_pack<DT>(x[2 * i + 1], c, neg, p + 16, sum1);
-        tmem_st32(s_col + i * 32, p);
+          for (int k = 0; k < DP; ++k) o_row[k] *= scale;
+          l *= scale;
+          ref = top;
+        }
+        __syncwarp();
+        const float neg = ref == -INFINITY ? 0.0f : -ref;
+        const unsigned third = tmem + lanes + S::NS * (kRows + DP) + stream * 64;
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          unsigned p[S::PLANES][16];
+          scores(i);
+          exp_pack<DT>(x, c, neg, p, 0, sum);
+          tmem_st16(s_col + i * 32, p[0]);
+          tmem_st16(s_col + i * 32 + 16, p[1]);
+          tmem_st16(third + i * 16, p[2]);
+        }
+        l += sum.x + sum.y;
+      } else {
+        unsigned x[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(s_col + i * 32, x[i]);
+        tmem_wait_ld();
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if ((unsigned)(i - lo) >= len) x[i >> 5][i & 31] = 0xff800000u;  // -inf
+        }
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          m0 = max3(m0, __uint_as_float(x[0][i]), __uint_as_float(x[0][i + 1]));
+          m1 = max3(m1, __uint_as_float(x[1][i]), __uint_as_float(x[1][i + 1]));
+          m0 = max3(m0, __uint_as_float(x[2][i]), __uint_as_float(x[2][i + 1]));
+          m1 = max3(m1, __uint_as_float(x[3][i]), __uint_as_float(x[3][i + 1]));
+        }
+        const float top = fmaxf(m0, m1) * c;
+        const bool grow = alive && top > ref + (kLazy + kShift<DT>);  // from -inf: any score
+        if (__any_sync(0xffffffffu, grow)) {
+          const float now = grow ? top - kShift<DT> : ref;
+          const float scale = grow ? fast_exp2(ref - now) : 1.0f;
+          if (s > 0) {  // the products up to tile s - 1 are done: S of tile s came after them
+            unsigned o[32];
+#pragma unroll
+            for (int i = 0; i < DP / 32; ++i) {
+              tmem_ld32(o_col + i * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale);
+              tmem_st32(o_col + i * 32, o);
+            }
+          }
+          l *= scale;
+          ref = now;
+        }
+        const float neg = ref == -INFINITY ? 0.0f : -ref;
+        float2 sum0 = make_float2(0.0f, 0.0f), sum1 = sum0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          unsigned p[S::PLANES][32];
+          exp_pack<DT>(x[2 * i], c, neg, p, 0, sum0);
+          exp_pack<DT>(x[2 * i + 1], c, neg, p, 16, sum1);
+          tmem_st32(s_col + i * 32, p[0]);
+        }
+        sum0 = add2(sum0, sum1);
+        l += sum0.x + sum0.y;
       }
-      sum0 = add2(sum0, sum1);
-      l += sum0.x + sum0.y;
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(&sh.p_ready[stream]);
@@ -317,6 +397,7 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
     if (T == 0 && some) ok = wait(&sh.q_full, 0);  // the tile's memory is used below
     __syncwarp();
     tc_fence_after();
+    if (S::PLANES == 3 && T > 0) add_tile();
     if (!alive) l = 0.0f;
     const bool bad = n.bad || !ok || *reinterpret_cast<volatile int *>(&sh.gave_up);
     const long long tile_at = (long long)split * f.p.tiles * f.p.packs * a.B + cta;  // of a partial result
@@ -332,14 +413,16 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
 #pragma unroll
     for (int i = 0; i < DP / 32; ++i) {
       unsigned o[32];
-      if (T > 0) {
+      if (S::PLANES == 1 && T > 0) {
         tmem_ld32(o_col + i * 32, o);
         tmem_wait_ld();
       }
       float v[32];
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        v[k] = bad ? NAN : l == 0.0f ? 0.0f : __uint_as_float(o[k]) * inv;
+      for (int k = 0; k < 32; ++k) {
+        const float x = S::PLANES == 3 ? o_row[S::PLANES == 3 ? i * 32 + k : 0] : __uint_as_float(o[k]);
+        v[k] = bad ? NAN : l == 0.0f ? 0.0f : x * inv;
+      }
       if (f.p.splits == 1) {
         stage32<DT>(out_tile, S::CHUNK, r, i * 32, v);
       } else if (row < a.Lq) {
@@ -351,8 +434,10 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
       fence_async_shared();
       named_barrier<128>(1 + stream);
       if (r == 0 && row < a.Lq) {
-        for (int ch = 0; ch < S::CHUNKS; ++ch)
-          tma_store_4d(&om, out_tile + ch * S::CHUNK, ch * 64, h0 * f.o_h, row, (int)b * f.o_b);
+        constexpr int kColumns = DT == kF32 ? 32 : 64;  // of a chunk
+        for (int ch = 0; ch < DP / kColumns; ++ch)
+          if (ch * kColumns < a.D)
+            tma_store_4d(&om, out_tile + ch * S::CHUNK, ch * kColumns, h0 * f.o_h, row, (int)b * f.o_b);
         tma_store_commit();
         tma_store_wait_read();
       }
@@ -370,7 +455,8 @@ __global__ void __launch_bounds__(FwdShape<DP, WIDE>::THREADS, FwdShape<DP, WIDE
 template <int DT, int DP>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs f, int rows) {
   const AttnArgs &a = f.a;
-  __shared__ float out[32][33], weight[kMostSplits][32];
+  __shared__ float out[32][33];
+  __shared__ float weight[kMostSplits][32];
   const unsigned d0 = blockIdx.x % (DP / 32) * 32, block = blockIdx.x / (DP / 32);
   const int groups = rows / 32, r = threadIdx.x & 31, part = threadIdx.x >> 5;
   const unsigned cta = block / groups, r0 = block % groups * 32;
@@ -426,10 +512,17 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   __syncthreads();
   if (threadIdx.x < 128) {
     const int rr = threadIdx.x / 4, d = threadIdx.x % 4 * 8;
-    if (row_of(rr) < a.Lq && d0 + d < a.D) {
+    const float *x = &out[rr][d];
+    if (row_of(rr) >= a.Lq || d0 + d >= a.D) {
+    } else if constexpr (DT == kF32) {
+      float *dst = static_cast<float *>(const_cast<void *>(a.out)) + b * a.so.b + row_of(rr) * a.so.l +
+                   head_of(rr) * a.so.h + d0 + d;
+      *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+      if (d0 + d + 4 < a.D)
+        *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
       unsigned short *dst = static_cast<unsigned short *>(const_cast<void *>(a.out)) + b * a.so.b +
                             row_of(rr) * a.so.l + head_of(rr) * a.so.h + d0 + d;
-      const float *x = &out[rr][d];
       *reinterpret_cast<uint4 *>(dst) = make_uint4(pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]),
                                                    pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7]));
     }
@@ -459,7 +552,7 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 template <int DT, int DP, bool WIDE>
 cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v, const TensorMap &o,
                    cudaStream_t stream) {
-  typedef FwdShape<DP, WIDE> S;
+  typedef FwdShape<DT, DP, WIDE> S;
   const size_t smem = S::BYTES + 1024;
   cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_fwd_tc_kernel<DT, DP, WIDE>),
                                     smem, S::REGS);
@@ -475,11 +568,36 @@ cudaError_t launch(const FwdArgs &f, const TensorMap &q, const TensorMap &k, con
 }
 
 template <int DT>
-cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v, const TensorMap &o,
-                     cudaStream_t s) {
-  if (f.a.D <= 64)
-    return f.p.wide ? launch<DT, 64, true>(f, q, k, v, o, s) : launch<DT, 64, false>(f, q, k, v, o, s);
-  return f.p.wide ? launch<DT, 128, true>(f, q, k, v, o, s) : launch<DT, 128, false>(f, q, k, v, o, s);
+cudaError_t by_shape(const FwdArgs &f, const TensorMap &q, const TensorMap &k, const TensorMap &v,
+                     const TensorMap &o, cudaStream_t s) {
+  if constexpr (DT != kF32)
+    if (f.a.D > 64)
+      return f.p.wide ? launch<DT, 128, true>(f, q, k, v, o, s) : launch<DT, 128, false>(f, q, k, v, o, s);
+  return f.p.wide ? launch<DT, 64, true>(f, q, k, v, o, s) : launch<DT, 64, false>(f, q, k, v, o, s);
+}
+
+// The workspace: planes of q, k, v (float32), then the partial results of splits.
+struct FwdSpace {
+  size_t q, k, v, part_o, part_l, total;
+};
+FwdSpace space(const FwdPlan &p, long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
+  FwdSpace s = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  if (dtype == kF32) {
+    s.q = take(plane_bytes(B, Lq, H));
+    s.k = take(plane_bytes(B, Lk, Hkv));
+    s.v = take(plane_bytes(B, Lk, Hkv));
+  }
+  const size_t rows = p.splits == 1 ? 0 : (size_t)B * p.packs * p.tiles * p.splits * (p.wide ? 2 : 1) * kRows;
+  s.part_o = take(rows * (D <= 64 ? 64 : 128) * 4);
+  s.part_l = take(rows * 4);
+  s.total = at;
+  return s;
 }
 
 }  // namespace
@@ -490,36 +608,54 @@ int attn_row_pack(int G) {
   return P;
 }
 
-size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D) {
-  const FwdPlan p = plan(B, Lq, Lk, H, H / Hkv);
-  if (p.splits == 1) return 0;
-  const size_t rows = (size_t)B * p.packs * p.tiles * p.splits * (p.wide ? 2 : 1) * kRows;
-  return align256(rows * (D <= 64 ? 64 : 128) * 4) + align256(rows * 4);
+bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D) {
+  if (Lq == 0 || Lk == 0) return false;
+  return dtype == kF32 ? D <= 64 && Lq * G > 8 : D <= 128;
+}
+
+size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
+  return space(plan(B, Lq, Lk, H, H / Hkv), B, Lq, Lk, H, Hkv, D, dtype).total;
 }
 
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
   auto fits = [&](const void *p, const Strides &s, long long L, int H) {
-    return map_fits(p, a.B, L, H, a.D, s.b, s.l, s.h);
+    return map_fits(dtype, p, a.B, L, H, a.D, s.b, s.l, s.h);
   };
-  return dtype != kF32 && a.D <= 128 && a.Lk > 0 && fits(a.q, a.sq, a.Lq, a.H) &&
-         fits(a.k, a.sk, a.Lk, a.Hkv) && fits(a.v, a.sv, a.Lk, a.Hkv) &&
-         fits(a.out, a.so, a.Lq, a.H) && (attn_row_pack(a.G) == 1 || a.sq.h != 0);
+  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D) || !fits(a.out, a.so, a.Lq, a.H)) return false;
+  return dtype == kF32 || (fits(a.q, a.sq, a.Lq, a.H) && fits(a.k, a.sk, a.Lk, a.Hkv) &&
+                           fits(a.v, a.sv, a.Lk, a.Hkv) && (attn_row_pack(a.G) == 1 || a.sq.h != 0));
 }
 
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
   FwdArgs f = {};
   f.a = a;
   f.p = plan(a.B, a.Lq, a.Lk, a.H, a.G);
-  const size_t rows = (size_t)a.B * f.p.packs * f.p.tiles * f.p.splits * (f.p.wide ? 2 : 1) * kRows;
-  f.part_o = static_cast<float *>(workspace);
-  f.part_l = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                       align256(rows * (a.D <= 64 ? 64 : 128) * 4));
+  const FwdSpace at = space(f.p, a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D, dtype);
+  char *ws = static_cast<char *>(workspace);
+  f.part_o = reinterpret_cast<float *>(ws + at.part_o);
+  f.part_l = reinterpret_cast<float *>(ws + at.part_l);
   TensorMap q, k, v, o;
-  if (!encode_map(&q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, kRows / f.p.P) ||
-      !encode_map(&k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) ||
-      !encode_map(&v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows) ||
-      !encode_map(&o, a.out, dtype, a.B, a.Lq, a.H, a.D, a.so.b, a.so.l, a.so.h, f.p.P, kRows / f.p.P))
-    return cudaErrorInvalidValue;
+  bool ok = encode_map(&o, a.out, dtype, a.B, a.Lq, a.H, a.D, a.so.b, a.so.l, a.so.h, f.p.P, kRows / f.p.P);
+  if (dtype == kF32) {
+    const PlaneSource t[3] = {
+        {static_cast<const float *>(a.q), a.sq.b, a.sq.l, a.sq.h, a.q_lens, a.Lq, a.H,
+         reinterpret_cast<unsigned short *>(ws + at.q)},
+        {static_cast<const float *>(a.k), a.sk.b, a.sk.l, a.sk.h, a.k_lens, a.Lk, a.Hkv,
+         reinterpret_cast<unsigned short *>(ws + at.k)},
+        {static_cast<const float *>(a.v), a.sv.b, a.sv.l, a.sv.h, a.k_lens, a.Lk, a.Hkv,
+         reinterpret_cast<unsigned short *>(ws + at.v)}};
+    const cudaError_t e = launch_planes(t, 3, a.B, a.D, stream);
+    if (e != cudaSuccess) return e;
+    ok = ok && encode_planes(&q, t[0].dst, a.B, a.Lq, a.H, f.p.P, kRows / f.p.P) &&
+         encode_planes(&k, t[1].dst, a.B, a.Lk, a.Hkv, 1, kRows) &&
+         encode_planes(&v, t[2].dst, a.B, a.Lk, a.Hkv, 1, kRows);
+  } else {
+    ok = ok &&
+         encode_map(&q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, kRows / f.p.P) &&
+         encode_map(&k, a.k, dtype, a.B, a.Lk, a.Hkv, a.D, a.sk.b, a.sk.l, a.sk.h, 1, kRows) &&
+         encode_map(&v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows);
+  }
+  if (!ok) return cudaErrorInvalidValue;
   f.o_b = o.b_mul;
   f.o_h = o.h_mul;
   f.q_b = q.b_mul;
@@ -528,7 +664,9 @@ cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.k_h = k.h_mul;
   f.v_b = v.b_mul;
   f.v_h = v.h_mul;
-  return dtype == kF16 ? by_shape<kF16>(f, q, k, v, o, stream) : by_shape<kBF16>(f, q, k, v, o, stream);
+  return dtype == kF32   ? by_shape<kF32>(f, q, k, v, o, stream)
+         : dtype == kF16 ? by_shape<kF16>(f, q, k, v, o, stream)
+                         : by_shape<kBF16>(f, q, k, v, o, stream);
 }
 
 }  // namespace tdt

@@ -64,6 +64,19 @@ template <int N> __device__ __forceinline__ void warpgroup_give_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ---- float32 as planes -----------------------------------------------------------
+// The tensor cores multiply 16-bit numbers.  A float32 operand becomes three bfloat16 planes, x = x0 + x1 +
+// x2 to 24 bits and more (each rounds what the ones before leave), and a product the six products of planes
+// whose orders add up to 2 at the most, small ones first; what is left out is below 2^-25 of |x||y|.
+template <int DT> constexpr int kPlanes = DT == kF32 ? 3 : 1;
+template <int DT> constexpr int kPlanePairs = DT == kF32 ? 6 : 1;
+template <int DT> __device__ __forceinline__ constexpr int plane_a(int i) {
+  return DT != kF32 ? 0 : i == 0 ? 2 : i == 2 || i == 3 ? 1 : 0;  // 2 0 1 1 0 0
+}
+template <int DT> __device__ __forceinline__ constexpr int plane_b(int i) {
+  return DT != kF32 ? 0 : i == 1 ? 2 : i == 2 || i == 4 ? 1 : 0;  // 0 2 1 0 1 0
+}
+
 // ---- TMA ----------------------------------------------------------------------
 __device__ __forceinline__ void tma_load_4d(const CUtensorMap *map, void *dst,
                                             unsigned long long *bar, int x, int y, int z, int w) {
@@ -156,6 +169,16 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// 16 columns.
+__device__ __forceinline__ void tmem_st16(unsigned addr, const unsigned *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+
 // ---- matrix products ---------------------------------------------------------------
 // Shared-memory operand descriptors: start address, leading and stride offsets in 16-byte
 // units, version 1, 128-byte swizzle.
@@ -173,7 +196,7 @@ __device__ __forceinline__ unsigned long long desc_mn_major(unsigned addr, unsig
 // Instruction descriptor of kind::f16 with float32 accumulators, M = 128.
 template <int DT>
 __device__ __forceinline__ constexpr unsigned mma_desc(int N, bool b_mn_major, bool a_mn_major = false) {
-  return (1u << 4) | ((DT == kBF16 ? 1u : 0u) << 7) | ((DT == kBF16 ? 1u : 0u) << 10) |
+  return (1u << 4) | ((DT != kF16 ? 1u : 0u) << 7) | ((DT != kF16 ? 1u : 0u) << 10) |
          ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) | ((unsigned)(N >> 3) << 17) | ((128u >> 4) << 24);
 }
 // d (+)= a b, both operands in shared memory.  One thread issues; K = 16.
@@ -222,10 +245,30 @@ __device__ __forceinline__ void mma_across(unsigned d, unsigned p, unsigned b, u
     mma_ts(d, p + k * 8, desc_mn_major(b + k * 2048, b_chunk), idesc, accumulate || k > 0);
 }
 
-// Two floats as one 32-bit pair of the 16-bit type, the first in the low half.
+// The same over the pairs of planes; planes of A and B lie *_plane bytes apart, those of P in the TMEM
+// columns p0, p1, p2.
+template <int DT, int DP>
+__device__ __forceinline__ void mma_rows_planes(unsigned d, unsigned a, unsigned b, unsigned chunk,
+                                                unsigned plane, unsigned idesc) {
+#pragma unroll
+  for (int i = 0; i < kPlanePairs<DT>; ++i)
+    mma_rows<DP>(d, a + plane_a<DT>(i) * plane, chunk, b + plane_b<DT>(i) * plane, chunk, idesc, i > 0);
+}
+template <int DT, int KR>
+__device__ __forceinline__ void mma_across_planes(unsigned d, unsigned p0, unsigned p1, unsigned p2, unsigned b,
+                                                  unsigned chunk, unsigned plane, unsigned idesc,
+                                                  bool accumulate) {
+#pragma unroll
+  for (int i = 0; i < kPlanePairs<DT>; ++i)
+    mma_across<KR>(d, plane_a<DT>(i) == 0 ? p0 : plane_a<DT>(i) == 1 ? p1 : p2, b + plane_b<DT>(i) * plane,
+                   chunk, idesc, accumulate || i > 0);
+}
+
+// Two floats as one 32-bit pair of the 16-bit type (of bfloat16 planes for float32), the first in the
+// low half.
 template <int DT> __device__ __forceinline__ unsigned pack2(float lo, float hi) {
   unsigned r;
-  if (DT == kBF16)
+  if (DT != kF16)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   else
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -266,12 +309,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Two floats as pairs of their planes.
+template <int DT> __device__ __forceinline__ void split2(float2 v, unsigned (&out)[kPlanes<DT>]) {
+  out[0] = pack2<DT>(v.x, v.y);
+#pragma unroll
+  for (int i = 1; i < kPlanes<DT>; ++i) {
+    const float2 got = make_float2(-__uint_as_float(out[i - 1] << 16),
+                                   -__uint_as_float(out[i - 1] & 0xffff0000u));
+    v = add2(v, got);  // exact
+    out[i] = pack2<DT>(v.x, v.y);
+  }
+}
+
 // Columns [d0, d0 + 32) of a row as 16-bit elements into a tile, placed as TMA places them.  (A thread
 // that holds a row would otherwise store it straight to memory: 32 lines an instruction, which was
 // measured to take the load/store path away from everybody else.)
+// Float32 tiles have chunks of 32 columns.
 template <int DT>
 __device__ __forceinline__ void stage32(unsigned char *tile, int chunk_bytes, int row, int d0,
                                         const float (&v)[32]) {
+  if (DT == kF32) {
+    unsigned char *at = tile + (d0 / 32) * chunk_bytes + row * 128;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float4 *>(at + (k ^ (row & 7)) * 16) =
+          make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    return;
+  }
   unsigned char *at = tile + (d0 / 64) * chunk_bytes + row * 128;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -324,7 +388,7 @@ cudaError_t launch_follower(void (*kernel)(P...), dim3 grid, unsigned threads, s
 cudaError_t prepare_tc_kernel(const void *kernel, size_t smem, int regs);
 
 // ---- host: tensor maps ----------------------------------------------------------------
-// A [B, L, H, D] tensor of 16-bit elements as the map (D, H, L, B) with boxes of 64 x heads x
+// A [B, L, H, D] tensor as the map (D, H, L, B) with boxes of 128 bytes (64 16-bit elements) x heads x
 // rows / heads.  A batch or head axis of stride 0 becomes one of size 1 (b_mul, h_mul = 0).
 struct TensorMap {
   CUtensorMap map;
@@ -333,7 +397,21 @@ struct TensorMap {
 bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long L, long long H,
                 int D, long long sb, long long sl, long long sh, int box_heads, int box_rows);
 // Whether encode_map can take the tensor (16-byte alignment of base and strides).
-bool map_fits(const void *ptr, long long B, long long L, long long H, int D, long long sb,
+bool map_fits(int dtype, const void *ptr, long long B, long long L, long long H, int D, long long sb,
               long long sl, long long sh);
+
+// Float32 tensors as bfloat16 planes [B, H, L, 3, 64], rows at or past the utterance's length as zeros.
+struct PlaneSource {
+  const float *src;
+  long long sb, sl, sh;
+  const long long *lens;  // or NULL
+  int L, H;
+  unsigned short *dst;
+};
+inline size_t plane_bytes(long long B, long long L, long long H) { return (size_t)(B * L * H) * 3 * 64 * 2; }
+cudaError_t launch_planes(const PlaneSource *src, int n, long long B, int D, cudaStream_t stream);
+// The map of such planes, as if of heads of 192 elements.
+bool encode_planes(TensorMap *m, const unsigned short *planes, long long B, long long L, long long H,
+                   int box_heads, int box_rows);
 
 }  // namespace tdt
