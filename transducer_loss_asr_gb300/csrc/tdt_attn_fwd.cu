@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
+FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G, int dtype) {
   FwdPlan p;
   p.P = attn_row_pack(G);
   p.packs = H / p.P;
@@ -537,13 +537,14 @@ FwdPlan plan(long long B, long long Lq, long long Lk, int H, int G) {
   p.wide = rows > kRows;
   const int tile_rows = p.wide ? 2 * kRows : kRows;
   p.tiles = (int)((rows + tile_rows - 1) / tile_rows);
-  // split the frames while the CTAs leave SMs idle, if that saves a CTA a dozen tiles: joining costs
-  // about as much time as eight
+  // split the frames while the CTAs leave SMs idle, if that saves a CTA a dozen tiles' time: joining
+  // costs about as much as eight take; a float32 tile has six times the products and takes three times as
+  // long
   const long long ctas = B * p.packs * p.tiles, steps = (Lk + kRows - 1) / kRows;
   long long s = ctas > 0 ? (p.wide ? 1 : 2) * kSMs / ctas : 1;
   if (s > steps / 4) s = steps / 4;
   if (s > kMostSplits) s = kMostSplits;
-  p.splits = s < 2 || steps - steps / s < 12 ? 1 : (int)s;
+  p.splits = s < 2 || (steps - steps / s) * (dtype == kF32 ? 3 : 1) < 12 ? 1 : (int)s;
   return p;
 }
 
@@ -614,7 +615,7 @@ bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D) {
 }
 
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
-  return space(plan(B, Lq, Lk, H, H / Hkv), B, Lq, Lk, H, Hkv, D, dtype).total;
+  return space(plan(B, Lq, Lk, H, H / Hkv, dtype), B, Lq, Lk, H, Hkv, D, dtype).total;
 }
 
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
@@ -629,7 +630,7 @@ bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream) {
   FwdArgs f = {};
   f.a = a;
-  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.G);
+  f.p = plan(a.B, a.Lq, a.Lk, a.H, a.G, dtype);
   const FwdSpace at = space(f.p, a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D, dtype);
   char *ws = static_cast<char *>(workspace);
   f.part_o = reinterpret_cast<float *>(ws + at.part_o);

@@ -37,7 +37,7 @@ constexpr int kOwnList = 1024;         // tokens of a row that needs no list
 constexpr int kListZ = 12;             // z >= -kListZ goes into the list; if that overflows, half of it, ...
 constexpr int kListTries = 3;
 constexpr float kZeroZ = 33.0f;        // z < -32 weighs 0
-constexpr float kMagic = 1.5f / 256.0f;
+constexpr float kMagic = 1.5f / 256.0f;  // bits 0x3bc00000: bits 26 and 0 to 21 are clear
 
 struct SampleArgs {
   const void *logits;
@@ -231,24 +231,32 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
   // f(vector, raw) for the warp's vectors in memory, a vector a lane; every lane takes every step, and
   // those past the warp's end get vectors of -inf.
   template <typename F> __device__ __forceinline__ void each_raw(F f) const {
-    constexpr int U = 4;  // loads in flight
+    constexpr int U = 4;  // loads of a turn; the next turn's are in flight while this one's are at work
     const int inner0 = head > 0 ? 1 : 0, inner1 = min(v1, (V + head) / VEC);
     const uint4 *base = reinterpret_cast<const uint4 *>(row - head);
     int v = v0;
-    while (v < v1) {
-      if (v >= inner0 && v + 32 * U <= inner1) {
-        uint4 raw[U];
+    auto edge = [&]() {
+      const bool mine = v + lane < v1;
+      f(v + lane, fetch(mine ? v + lane : (V + head) / VEC + 1));
+      v += 32;
+    };
+    if (v < inner0 && v < v1) edge();
+    if (v + 32 * U <= inner1) {
+      uint4 raw[U], next[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) raw[u] = __ldg(base + v + u * 32 + lane);
+      for (int u = 0; u < U; ++u) next[u] = __ldg(base + v + u * 32 + lane);
+      while (v + 32 * U <= inner1) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
+        if (v + 64 * U <= inner1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) next[u] = __ldg(base + v + (U + u) * 32 + lane);
 #pragma unroll
         for (int u = 0; u < U; ++u) f(v + u * 32 + lane, raw[u]);
         v += 32 * U;
-      } else {
-        const bool mine = v + lane < v1;
-        f(v + lane, fetch(mine ? v + lane : (V + head) / VEC + 1));
-        v += 32;
       }
     }
+    while (v < v1) edge();
   }
   // f(x) for every token of this thread's share of the warp's: the list's or the row's.
   template <typename F> __device__ __forceinline__ void each(F f) const {
@@ -301,21 +309,26 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     const float2 x2 = make_float2(-w.X, -w.X), per2 = make_float2(w.per, w.per),
                  magic2 = make_float2(kMagic, kMagic);
     auto take = [&](int v, const float (&x)[VEC], float top) {
+      bool here = top >= near;
       if (MASS && small) {
-        unsigned sum = 0;
+        unsigned sum = 0, any = 0;
 #pragma unroll
         for (int j = 0; j < VEC; j += 2) {
           const float2 z = mul2(add2(make_float2(x[j], x[j + 1]), x2), per2);
           const float2 m = add2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), magic2);
           sum += __float_as_uint(m.x) + __float_as_uint(m.y);
+          any |= __float_as_uint(m.x) | __float_as_uint(m.y);
         }
         mass += sum - VEC * __float_as_uint(kMagic);  // modulo 2^32; the sum itself is at most VEC 2^26
+        // A weight of 2^-12 and more sets one of the bits 19 to 21, or (from 2^-9 on) bit 26, which the
+        // others do not: vectors with a token of z >= -12 are among these.
+        here = any & 0x04380000u;
       } else if (MASS) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) mass += w(x[j]);
       }
       if (!LIST && !(MASS && small)) return;
-      const unsigned hit = __ballot_sync(0xffffffffu, top >= near);
+      const unsigned hit = __ballot_sync(0xffffffffu, here);
       if (hit) {
         const int at = nv + __popc(hit & ((1u << lane) - 1));
         nv += __popc(hit);
@@ -344,7 +357,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
       each_raw([&](int v, uint4 raw) {
         float x[VEC];
         if (MASS) unpack(raw, x);
-        take(v, x, top_of(raw));
+        take(v, x, MASS && small ? 0.0f : top_of(raw));
       });
     }
     // the tokens of the noted vectors, in order
@@ -657,7 +670,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
 };
 
 template <int DT, int NW, bool RESIDENT>
-__global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(NW * 32, NW == 8 && !RESIDENT ? 3 : 1) sample_kernel(SampleArgs a) {
   typedef typename Elem<DT>::T E;
   typedef Key<DT> K;
   extern __shared__ __align__(16) unsigned char mem[];
@@ -719,7 +732,7 @@ __global__ void __launch_bounds__(NW * 32) sample_kernel(SampleArgs a) {
       int listed = -1, z = kListZ;
       for (int i = 0; i < kListTries && listed < 0; ++i) {
         z = kListZ >> i;
-        near = below((float)z);
+        near = below((float)z - 0.002f);  // so that pass 2's bits are sure to show every token from here up
         if (need_all && i == 0) {
           listed = r.template weigh<true, true>(near);
           all = r.total_low() + r.total_mass();  // also where the list did not fit
