@@ -362,16 +362,23 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     }
     // the tokens of the noted vectors, in order
     __syncwarp();
-    if (fits)
+    if (fits) {
+      uint4 raw_next = make_uint4(0, 0, 0, 0);
+      int v_next = lane < nv ? vecs[warp * CAP + lane] : v0;
+      if (!RESIDENT && nv > 0) raw_next = fetch(v_next);
       for (int e = 0; e < nv; e += 32) {
         const bool mine = e + lane < nv;
-        const int v = mine ? vecs[warp * CAP + e + lane] : 0;
+        const int v = v_next;
         float x[VEC];
         if (RESIDENT) {
 #pragma unroll
           for (int j = 0; j < VEC; ++j) x[j] = own[v * VEC + j];
         } else {
-          unpack(fetch(v), x);
+          unpack(raw_next, x);
+        }
+        if (e + 32 < nv) {  // the next ones on their way
+          v_next = e + 32 + lane < nv ? vecs[warp * CAP + e + 32 + lane] : v0;
+          if (!RESIDENT) raw_next = fetch(v_next);
         }
         unsigned in = 0;
 #pragma unroll
@@ -396,6 +403,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
             }
           }
       }
+    }
     if (!fits && MASS) {  // too many to set right: the plain sum
       mass = mass_listed = 0;
       each([&](float x) { mass += w(x); });
@@ -670,7 +678,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
 };
 
 template <int DT, int NW, bool RESIDENT>
-__global__ void __launch_bounds__(NW * 32, NW == 8 && !RESIDENT ? 3 : 1) sample_kernel(SampleArgs a) {
+__global__ void __launch_bounds__(NW * 32, NW == 16 && !RESIDENT ? 2 : 1) sample_kernel(SampleArgs a) {
   typedef typename Elem<DT>::T E;
   typedef Key<DT> K;
   extern __shared__ __align__(16) unsigned char mem[];
@@ -830,12 +838,14 @@ cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   return cudaGetLastError();
 }
 // Warps a row: few for many rows, which share the SMs; many for few rows, where only the time of one counts.
+// Wide rows are read twice, and two a SM at a time are what L2 holds (2,048 x 131,072 bfloat16: 262 us; three
+// of 8 warps 286, one of 32 warps 314).
 template <int DT> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   if (a.V <= 256) return launch<DT, 1, true>(a, N, s);
   if (a.V <= kOwnList) return launch<DT, 4, true>(a, N, s);
   if (a.V <= kResident)
     return N > 2 * 152 ? launch<DT, 8, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
-  return N > 2 * 152 ? launch<DT, 8, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
+  return N > 2 * 152 ? launch<DT, 16, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
 }
 
 }  // namespace
