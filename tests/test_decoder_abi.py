@@ -193,3 +193,17 @@ def test_binding_refuses_bad_sampling_tensors(lib):
 def test_new_status_texts(lib):
     for code in (-14, -15, -16):
         assert lib.tdt_status_string(code) != "unknown status"
+
+
+def test_cross_attention_op_fake_shapes_and_cpu_rejection(lib):
+    from transducer_loss_asr_gb300 import autograd
+
+    q, k = torch.empty(2, 5, 4, 8, device="meta"), torch.empty(2, 7, 2, 8, device="meta")
+    out, lse = torch.ops.tdt_gb300.cross_attention_forward(q, k, k, None, None, None, 0.3)
+    assert out.shape == q.shape and lse.shape == (2, 4, 5) and lse.dtype == torch.float32
+    grads = torch.ops.tdt_gb300.cross_attention_backward(q, q, k, k, out, lse, None, None, None, 0.3)
+    assert [g.shape for g in grads] == [q.shape, k.shape, k.shape]
+    with pytest.raises(NotImplementedError):  # CUDA kernels only: no silent CPU path
+        autograd.cross_attention(torch.zeros(2, 5, 4, 8), torch.zeros(2, 7, 2, 8), torch.zeros(2, 7, 2, 8))
+    with pytest.raises(ValueError):
+        lib.tdt_cross_attn_fwd(torch.zeros(2, 5, 4, 8), torch.zeros(2, 7, 2, 8), torch.zeros(2, 7, 2, 8))

@@ -1,4 +1,4 @@
-"""PyTorch autograd and torch.compile support for the TDT loss.
+"""PyTorch autograd and torch.compile support for the TDT loss and for cross attention.
 
 The loss is registered as two custom ops over the split C ABI
 (``tdt_loss_fwd`` / ``tdt_loss_bwd`` in include/tdt_loss.h):
@@ -19,7 +19,7 @@ kernels only: called with CPU tensors they raise.
 """
 from __future__ import annotations
 
-from typing import List, Tuple
+from typing import List, Optional, Tuple
 
 import torch
 from torch import Tensor
@@ -140,3 +140,78 @@ class TDTLoss(torch.nn.Module):
                 sigma=0.0, reduction="mean_volume"):
         return tdt_loss(logits, labels, logit_lengths, label_lengths, durations, blank, sigma,
                         reduction)
+
+
+# ---- cross attention ------------------------------------------------------------------------------
+
+
+@torch.library.custom_op("tdt_gb300::cross_attention_forward", mutates_args=(), device_types="cuda")
+def cross_attention_forward(q: Tensor, k: Tensor, v: Tensor, k_lens: Optional[Tensor],
+                            q_lens: Optional[Tensor], windows: Optional[Tensor],
+                            scale: float) -> Tuple[Tensor, Tensor]:
+    from . import binding
+
+    return binding.tdt_cross_attn_fwd(q, k, v, k_lens, q_lens, windows, scale)
+
+
+@cross_attention_forward.register_fake
+def _cross_attention_forward_fake(q, k, v, k_lens, q_lens, windows, scale):
+    B, Lq, H, _ = q.shape
+    return (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+            torch.empty((B, H, Lq), dtype=torch.float32, device=q.device))
+
+
+@torch.library.custom_op("tdt_gb300::cross_attention_backward", mutates_args=(), device_types="cuda")
+def cross_attention_backward(grad_out: Tensor, q: Tensor, k: Tensor, v: Tensor, out: Tensor,
+                             lse: Tensor, k_lens: Optional[Tensor], q_lens: Optional[Tensor],
+                             windows: Optional[Tensor],
+                             scale: float) -> Tuple[Tensor, Tensor, Tensor]:
+    from . import binding
+
+    return binding.tdt_cross_attn_bwd(grad_out, q, k, v, out, lse, k_lens, q_lens, windows, scale)
+
+
+@cross_attention_backward.register_fake
+def _cross_attention_backward_fake(grad_out, q, k, v, out, lse, k_lens, q_lens, windows, scale):
+    return tuple(torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
+
+
+def _cross_attention_setup(ctx, inputs, output):
+    q, k, v, k_lens, q_lens, windows, scale = inputs
+    out, lse = output
+    ctx.save_for_backward(q, k, v, out, lse, k_lens, q_lens, windows)
+    ctx.scale = scale
+    ctx.mark_non_differentiable(lse)
+
+
+def _cross_attention_backward(ctx, grad_out, grad_lse):
+    q, k, v, out, lse, k_lens, q_lens, windows = ctx.saved_tensors
+    dq, dk, dv = cross_attention_backward(grad_out, q, k, v, out, lse, k_lens, q_lens, windows,
+                                          ctx.scale)
+    return dq, dk, dv, None, None, None, None
+
+
+cross_attention_forward.register_autograd(_cross_attention_backward,
+                                          setup_context=_cross_attention_setup)
+
+
+def cross_attention(q: Tensor, k: Tensor, v: Tensor, k_lens: Optional[Tensor] = None,
+                    q_lens: Optional[Tensor] = None, windows: Optional[Tensor] = None,
+                    scale: Optional[float] = None) -> Tensor:
+    """Cross attention of label states ``q`` [B, Lq, H, D] to encoder frames ``k``, ``v``
+    [B, Lk, Hkv, D] (CUDA; float32/float16/bfloat16; H a multiple of Hkv), differentiable w.r.t. q,
+    k and v; the result is like q.
+
+    k_lens, q_lens: int64 [B], frames and queries past them take no part; windows: int32 [B, Lq, 2],
+    the frames [w0, w1) that each query sees; scale: 1 / sqrt(D) unless given.  A query that sees no
+    frame gets zeros and no gradient.
+    """
+    scale = float(q.shape[-1]) ** -0.5 if scale is None else float(scale)
+    return cross_attention_forward(q, k, v, k_lens, q_lens, windows, scale)[0]
+
+
+class CrossAttention(torch.nn.Module):
+    """Stateless module form of :func:`cross_attention` (same arguments)."""
+
+    def forward(self, q, k, v, k_lens=None, q_lens=None, windows=None, scale=None):
+        return cross_attention(q, k, v, k_lens, q_lens, windows, scale)

@@ -123,7 +123,7 @@ struct Held {
 
 template <int NW> struct Shared {
   // of a stretch of keys: tokens, and their weight in three parts (over 2^48 + hi 2^16 + lo)
-  unsigned cnt[256], lo[256], hi[256], over[256];
+  __align__(16) unsigned cnt[256], lo[256], hi[256], over[256];
   unsigned keys[32], weights[32];  // tokens to be ranked
   Held held[NW], low[NW];
   int listed[NW];
@@ -146,7 +146,8 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
   typedef typename Elem<DT>::T E;
   typedef Key<DT> K;
   static constexpr int VEC = Vec<DT>::N;
-  static constexpr int CAP = kListTokens / NW;  // list entries of a warp
+  static constexpr int LIST = kListTokens;
+  static constexpr int CAP = LIST / NW;  // list entries of a warp
 
   Shared<NW> &s;
   float *own;     // the resident row, from its first vector on
@@ -169,8 +170,8 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     v1 = min(v0 + each, vectors);
     own = reinterpret_cast<float *>(mem);
     xs = own + (RESIDENT ? (V + 16 + 3) / 4 * 4 : 0);
-    ids = reinterpret_cast<int *>(xs + kListTokens);
-    vecs = ids + kListTokens;
+    ids = reinterpret_cast<int *>(xs + LIST);
+    vecs = ids + LIST;
   }
 
   // Vector v as float32: tokens outside the row and NaN come as -inf.
@@ -432,10 +433,6 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     return total_mass();
   }
 
-  __device__ __forceinline__ u64 mass_of(int digit) const {
-    return ((u64)s.over[digit] << 48) + ((u64)s.hi[digit] << 16) + s.lo[digit];
-  }
-
   // Counts and weights of the keys in [lo, lo + 2^bits), in stretches of 2^shift.
   __device__ void histogram(unsigned lo, int bits, int shift) {
     const unsigned digits = 1u << (bits - shift);  // at most 256
@@ -466,22 +463,43 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     u64 above_cnt = 0, above_mass = 0;  // of the keys above those in question
     while (bits > 0) {
       if (warp == 0) {
-        // lane 0 has the 8 highest digits
-        u64 c = 0, m = 0;
-        for (int i = 0; i < 8; ++i) {
-          c += s.cnt[255 - lane * 8 - i];
-          m += mass_of(255 - lane * 8 - i);
+        // lane 0 has the 8 highest digits, 248 to 255, lane 1 the 8 below them
+        const int d0 = 248 - lane * 8;
+        unsigned cnt[8];
+        u64 mass[8], m = 0;
+        unsigned c = 0;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const uint4 n4 = *reinterpret_cast<const uint4 *>(&s.cnt[d0 + i]),
+                      l4 = *reinterpret_cast<const uint4 *>(&s.lo[d0 + i]),
+                      h4 = *reinterpret_cast<const uint4 *>(&s.hi[d0 + i]),
+                      o4 = *reinterpret_cast<const uint4 *>(&s.over[d0 + i]);
+          cnt[i] = n4.x; cnt[i + 1] = n4.y; cnt[i + 2] = n4.z; cnt[i + 3] = n4.w;
+          mass[i] = ((u64)o4.x << 48) + ((u64)h4.x << 16) + l4.x;
+          mass[i + 1] = ((u64)o4.y << 48) + ((u64)h4.y << 16) + l4.y;
+          mass[i + 2] = ((u64)o4.z << 48) + ((u64)h4.z << 16) + l4.z;
+          mass[i + 3] = ((u64)o4.w << 48) + ((u64)h4.w << 16) + l4.w;
         }
-        u64 bc = above_cnt + warp_before64(c), bm = above_mass + warp_before64(m);
-        const u64 at = by_count ? bc : bm, step = by_count ? c : m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          c += cnt[i];
+          m += mass[i];
+        }
+        u64 bc = above_cnt + (unsigned)warp_before_int((int)c), bm = above_mass + warp_before64(m);
+        const u64 at = by_count ? bc : bm, step = by_count ? (u64)c : m;
         if (at < target && at + step >= target) {
-          int d = 255 - lane * 8;
-          for (; d > 255 - lane * 8 - 7; --d) {
-            if ((by_count ? bc + s.cnt[d] : bm + mass_of(d)) >= target) break;
-            bc += s.cnt[d];
-            bm += mass_of(d);
-          }
-          s.digit = d;
+          bool found = false;
+#pragma unroll
+          for (int i = 7; i >= 0; --i)
+            if (!found) {
+              if ((by_count ? bc + cnt[i] : bm + mass[i]) >= target) {
+                found = true;
+                s.digit = d0 + i;
+              } else {
+                bc += cnt[i];
+                bm += mass[i];
+              }
+            }
           s.above_cnt = bc;
           s.above_mass = bm;
           s.ranked = 0;
@@ -830,7 +848,7 @@ template <int DT, int NW, bool RESIDENT>
 cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   // a resident row starts at its first vector's place and is filled up to whole vectors
   const size_t row = RESIDENT ? (size_t)((a.V + 16 + 3) / 4 * 4) * 4 : 0;
-  const size_t smem = row + (RESIDENT && a.V <= kOwnList ? 0 : 3 * kListTokens * 4);
+  const size_t smem = row + (RESIDENT && a.V <= kOwnList ? 0 : 3 * Sampler<DT, NW, RESIDENT>::LIST * 4);
   const cudaError_t e = cudaFuncSetAttribute(sample_kernel<DT, NW, RESIDENT>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
