@@ -31,8 +31,9 @@ constexpr int kRows = 128;
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;  // 3 warpgroups x 168 = 2 x 208 + 88
 constexpr int kWorkRegs = 208, kOtherRegs = 88;
-// float16 weights are held as 2^15 p for the product with dO (p <= 1, so below the type's most): what a frame gets from rows that
-// hardly weigh it stays clear of the type's least numbers.  (dS has no such bound, and is held as it is.)
+// float16 weights are held as 2^15 p for the product with dO (p <= 1, so below the type's most): what a
+// frame gets from rows that hardly weigh it stays clear of the type's least numbers.  (dS has no such
+// bound, and is held as it is.)
 template <int DT> constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
 template <int DT> constexpr float kUnshift = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
 constexpr int kTileBits = 4096;   // row tiles whose windows the dk/dv kernel looks at beforehand
@@ -47,7 +48,8 @@ struct BwdPlan {
 struct BwdArgs {
   AttnArgs a;
   BwdPlan p;
-  int q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h, dq_b, dq_h, dk_b, dk_h, dv_b, dv_h;  // 0 for repeated axes
+  // 0 for repeated axes
+  int out_b, out_h, q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h, dq_b, dq_h, dk_b, dk_h, dv_b, dv_h;
   float *part;                  // splits > 1: [split][CTA][128][DP], dk's after dv's
 };
 
@@ -843,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---- dq, dk and dv of one row tile -----------------------------------------------------
 // Threads: two warpgroups of elementwise work (thread = row, each group half of the frames), one that
-// stages dk and dv tiles (thread = frame), four warps: loads, products, tails, stores.
+// stores dk and dv tiles (thread = frame), four warps: loads, products, tails, one idle.
 constexpr int kOneThreads = 512;
 constexpr int kOneLaunchRegs = 128;  // 4 x 128 = 2 x 160 + 112 + 80
 constexpr int kOneWorkRegs = 160, kOneStoreRegs = 112, kOneOtherRegs = 80;
@@ -857,8 +859,8 @@ struct OneShape {
 
 struct OneShared {
   Pipe k, v;
-  unsigned long long rows_in, rows_full, sp_full, sp_free, pds_ready, p_free, ds_free[2], dkv_full, dkv_free, dq_done[2], staged[2], done, tail_full,
-      drained;
+  unsigned long long rows_in, rows_full, out_full, sp_full, sp_free, pds_ready, p_free, ds_free[2], dkv_full,
+      dkv_free, dq_done[2], done, tail_full, drained;
   unsigned tmem;
   int gave_up;
   Hull hull;
@@ -869,8 +871,8 @@ template <int DT>
 __global__ void __launch_bounds__(kOneThreads, 1)
     attn_one_tc_kernel(const __grid_constant__ CUtensorMap qm, const __grid_constant__ CUtensorMap gm,
                        const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
-                       const __grid_constant__ CUtensorMap dqm, const __grid_constant__ CUtensorMap dkm,
-                       const __grid_constant__ CUtensorMap dvm, const __grid_constant__ BwdArgs f) {
+                       const __grid_constant__ CUtensorMap om, const __grid_constant__ CUtensorMap dqm,
+                       const __grid_constant__ BwdArgs f) {
   constexpr int DP = 64;
   typedef OneShape S;
   typedef typename Elem<DT>::T E;
@@ -926,18 +928,17 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     pipe_init(sh.v, S::VS);
     mbar_init(&sh.rows_in, 1);
     mbar_init(&sh.rows_full, 1);
+    mbar_init(&sh.out_full, 1);
     mbar_init(&sh.sp_full, 1);
     mbar_init(&sh.sp_free, 256);
     mbar_init(&sh.pds_ready, 256);
     mbar_init(&sh.p_free, 1);
-    mbar_init(&sh.ds_free[0], 1);
-    mbar_init(&sh.ds_free[1], 1);
+    mbar_init(&sh.ds_free[0], 128);
+    mbar_init(&sh.ds_free[1], 128);
     mbar_init(&sh.dkv_full, 1);
     mbar_init(&sh.dkv_free, 128);
     mbar_init(&sh.dq_done[0], 1);
     mbar_init(&sh.dq_done[1], 1);
-    mbar_init(&sh.staged[0], 128);
-    mbar_init(&sh.staged[1], 128);
     mbar_init(&sh.done, 1);
     mbar_init(&sh.tail_full, 1);
     mbar_init(&sh.drained, 1);
@@ -946,6 +947,8 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     if (some) {
       unsigned long long *in = cut_rows ? &sh.rows_in : &sh.rows_full;
       arrive_expect_tx(in, 2 * S::TILE);
+      arrive_expect_tx(&sh.out_full, S::TILE);
+      tma_load_4d(&om, p_tile, &sh.out_full, 0, h0 * f.out_h, 0, (int)b * f.out_b);  // P comes later
       tma_load_4d(&qm, q_tile, in, 0, h0 * f.q_h, 0, (int)b * f.q_b);
       tma_load_4d(&gm, g_tile, in, 0, h0 * f.go_h, 0, (int)b * f.go_b);
     }
@@ -988,17 +991,6 @@ __global__ void __launch_bounds__(kOneThreads, 1)
           Waiter::drain(&sh.k.full[i % S::KS], (unsigned)(i / S::KS) & 1);
           Waiter::drain(&sh.v.full[i % S::VS], (unsigned)(i / S::VS) & 1);
         }
-      }
-    }
-    if (warp == 15 && lane == 0) {  // stores the staged tiles; they are free once read
-      for (int s = 0; s < T; ++s) {
-        if (!wait(&sh.staged[s & 1], (unsigned)(s >> 1) & 1)) break;
-        const unsigned char *out_tile = ds_tiles + (s & 1) * S::PDS;
-        tma_store_4d(&dvm, out_tile, 0, hk * f.dv_h, frame(s), (int)b * f.dv_b);
-        tma_store_4d(&dkm, out_tile + S::TILE, 0, hk * f.dk_h, frame(s), (int)b * f.dk_b);
-        tma_store_commit();
-        tma_store_wait_read();
-        mbar_arrive(&sh.ds_free[s & 1]);
       }
     }
     if (warp == 14 && T > 0) {
@@ -1120,8 +1112,26 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         for (int k = 0; k < 8; ++k)
           *reinterpret_cast<uint4 *>(out_tile + i * S::TILE + r * 128 + (k ^ (r & 7)) * 16) =
               make_uint4(packed[i][4 * k], packed[i][4 * k + 1], packed[i][4 * k + 2], packed[i][4 * k + 3]);
-      fence_async_shared();
-      mbar_arrive(&sh.staged[s & 1]);
+      named_barrier<128>(2);
+      // 8 threads a row: whole lines.  Plain stores free this memory once it is in registers; a TMA store
+      // frees it once it has been read.
+      uint4 piece[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int x = i * 128 + r, jr = x % 1024 / 8, k = x % 8;
+        piece[i] = *reinterpret_cast<const uint4 *>(out_tile + (x / 1024) * S::TILE + jr * 128 +
+                                                    (k ^ (jr & 7)) * 16);
+      }
+      mbar_arrive(&sh.ds_free[s & 1]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int x = i * 128 + r, jr = t * kRows + x % 1024 / 8, d = x % 8 * 8;
+        const bool is_k = x >= 1024;
+        const Strides &st = is_k ? a.sdk : a.sdv;
+        if (jr < a.Lk && d < a.D)
+          *reinterpret_cast<uint4 *>(static_cast<unsigned short *>(is_k ? a.dk : a.dv) + b * st.b + jr * st.l +
+                                     hk * st.h + d) = piece[i];
+      }
     }
     tc_fence_before();
   } else {
@@ -1130,12 +1140,20 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta, lse2 = -INFINITY;  // both negated
     {
-      const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
+      // this group's half of the columns, from the tiles of dO and out
       float x = 0.0f;
-      if (real)
-        x = dot_rows<DT, DP / 2>(
-            static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
-            static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
+      if (some && wait(&sh.out_full, 0) && wait(rows, 0) && real) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = r * 128 + ((group * 4 + k) ^ (r & 7)) * 16;
+          const uint4 gv = *reinterpret_cast<const uint4 *>(g_tile + at),
+                      ov = *reinterpret_cast<const uint4 *>(p_tile + at);
+          const E *ge = reinterpret_cast<const E *>(&gv), *oe = reinterpret_cast<const E *>(&ov);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x = fmaf(Elem<DT>::to_float(ge[i]), Elem<DT>::to_float(oe[i]), x);
+        }
+      }
+      __syncwarp();
       if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
       if (group == 1) sh.half[r] = x;
       asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -1328,7 +1346,7 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Maps {
-  TensorMap q, go, k, v, dq, dk, dv;
+  TensorMap q, go, k, v, out, dq, dk, dv;
 };
 
 template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
@@ -1337,7 +1355,7 @@ template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaSt
   if (e != cudaSuccess) return e;
   const unsigned ctas = (unsigned)(f.a.B * f.a.Hkv);
   attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, m.dk.map, m.dv.map, f);
+      m.q.map, m.go.map, m.k.map, m.v.map, m.out.map, m.dq.map, f);
   if (f.p.dq_splits > 1)
     return launch_follower(attn_add_kernel<DT, 64>, dim3(ctas * (kRows / 32) * 2, 1), 256, 0, stream,
                            f, 0);
@@ -1425,7 +1443,9 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   f.part = reinterpret_cast<float *>(ws + at.part);
   Maps m;
   const int per = kRows / f.p.P;
-  bool ok = encode_map(&m.dq, a.dq, dtype, a.B, a.Lq, a.H, a.D, a.sdq.b, a.sdq.l, a.sdq.h, f.p.P, per) &&
+  bool ok = !f.p.one ||
+            encode_map(&m.out, a.out, dtype, a.B, a.Lq, a.H, a.D, a.so.b, a.so.l, a.so.h, f.p.P, per);
+  ok = ok && encode_map(&m.dq, a.dq, dtype, a.B, a.Lq, a.H, a.D, a.sdq.b, a.sdq.l, a.sdq.h, f.p.P, per) &&
             encode_map(&m.dk, a.dk, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdk.b, a.sdk.l, a.sdk.h, 1, kRows) &&
             encode_map(&m.dv, a.dv, dtype, a.B, a.Lk, a.Hkv, a.D, a.sdv.b, a.sdv.l, a.sdv.h, 1, kRows);
   if (dtype == kF32) {
@@ -1450,6 +1470,8 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
          encode_map(&m.v, a.v, dtype, a.B, a.Lk, a.Hkv, a.D, a.sv.b, a.sv.l, a.sv.h, 1, kRows);
   }
   if (!ok) return cudaErrorInvalidValue;
+  f.out_b = f.p.one ? m.out.b_mul : 0;
+  f.out_h = f.p.one ? m.out.h_mul : 0;
   f.q_b = m.q.b_mul;
   f.q_h = m.q.h_mul;
   f.go_b = m.go.b_mul;
