@@ -319,3 +319,11 @@ def test_tails_of_every_walk_length(binding, dtype, D):
         for Lq in (40, 200):
             _check(binding, (1, Lq, tiles * 128 - 20, 1, 1, D), dtype, seed=tiles, lens=True)
             _check(binding, (1, tiles * 128 - 20, 150, 2, 1, D), dtype, seed=tiles, lens=True)
+
+
+@pytest.mark.parametrize("lens,windows", [(False, False), (True, False), (True, True)])
+@pytest.mark.parametrize("shape", [(1, 9, 1, 1, 1, 65), (1, 20, 130, 1, 1, 128), (2, 129, 500, 2, 2, 80), (1, 50, 5000, 2, 1, 68),
+                                   (2, 100, 260, 8, 2, 96), (1, 700, 300, 6, 2, 128), (3, 300, 1100, 16, 1, 72)], ids=str)
+def test_float32_heads_over_64(binding, record_margin, shape, lens, windows):
+    """One tile and many, walks shared by 1 to 8 blocks, packed heads, widths that fill their last part or not."""
+    _check(binding, shape, torch.float32, record=record_margin, case=f"wide {shape}", lens=lens, windows=windows)

@@ -1,5 +1,6 @@
 // tdt_attn_bwd.cu -- the backward pass of cross attention on the 5th-generation tensor cores, for
-// float16 and bfloat16 heads of up to 128 elements.
+// float16 and bfloat16 heads of up to 128 elements and float32 heads of up to 64 (three bfloat16 planes a
+// tensor, six products for one, each tile's sums added to float32 registers; as in the forward pass).
 //
 // Every sum has one owner and a fixed order (no atomics).  Where the rows of a key head fill at most one
 // tile of 128 and heads are at most 64 wide (label states of one utterance), one kernel walks the frames
@@ -21,6 +22,20 @@
 // Scores of the next tile are formed while the threads are at this one's dS.
 //
 // Few CTAs: the walk is split over several, whose float32 sums a third kernel adds in order.
+//
+// P, dS: rounding them to 16 bits is what the products need.  With delta from the rounded O it is what
+// dq's error consists of (bfloat16: 2.5e-3 of the largest element, 1.7e-3 where only inputs and results are
+// rounded); a delta from the unrounded O would need it kept from the forward pass in float32, and a dS of
+// two planes a product more.
+//
+// Bound by the tensor cores and the shared memory that feeds them: a product of two shared-memory operands
+// of 128 x 128 x 16 takes the 64 clocks of its reads, and S, dP in both kernels are such.  Measured:
+//   16 x 1024 x 4096, 16 heads on 4 of 128, bfloat16   1,307 us (dq 567): 1,050 TFLOP/s on the five products
+//                                                      of the formula, 1,470 on the seven done
+//   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   82 us (dq 40, dk/dv 42)
+//   16 x 121 x 750 ragged, 16 heads of 64, one kernel  33.7 us for 66 MB; the two kernels: 48 us
+//   4 x 41 x 200, 8 heads of 64, one kernel            8.2 us, latency
+//   1201 x 2000, 8 heads of 64, float32                148 us (planes 6, dq 68, dk/dv 74)
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -81,30 +96,6 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *d
                                           unsigned long long *bar, int h, int l, int b) {
   for (int c = 0; c < kPlanes<DT> * DP / 64; ++c)
     tma_load_4d(m, dst + c * BwdShape<DT, DP>::CHUNK, bar, c * 64, h, l, b);
-}
-
-// dot of the first `n` of N elements of two rows, n a multiple of a 16-byte load's elements; every load is
-// in flight at once
-template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x, const void *y, int n) {
-  typedef typename Elem<DT>::T E;
-  constexpr int W = 16 / (int)sizeof(E);
-  uint4 xv[N / W], yv[N / W];
-#pragma unroll
-  for (int d = 0; d < N; d += W) {
-    xv[d / W] = yv[d / W] = make_uint4(0, 0, 0, 0);
-    if (d < n) {
-      xv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d));
-      yv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
-    }
-  }
-  float s = 0.0f;
-#pragma unroll
-  for (int d = 0; d < N / W; ++d) {
-    const E *xe = reinterpret_cast<const E *>(&xv[d]), *ye = reinterpret_cast<const E *>(&yv[d]);
-#pragma unroll
-    for (int k = 0; k < W; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
-  }
-  return s;
 }
 
 // ---- dq ---------------------------------------------------------------------------
@@ -1459,10 +1450,10 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
                               source(a.v, a.sv, a.k_lens, a.Lk, a.Hkv, at.v)};
     const cudaError_t e = launch_planes(t, 4, a.B, a.D, stream);
     if (e != cudaSuccess) return e;
-    ok = ok && encode_planes(&m.q, t[0].dst, a.B, a.Lq, a.H, f.p.P, per) &&
-         encode_planes(&m.go, t[1].dst, a.B, a.Lq, a.H, f.p.P, per) &&
-         encode_planes(&m.k, t[2].dst, a.B, a.Lk, a.Hkv, 1, kRows) &&
-         encode_planes(&m.v, t[3].dst, a.B, a.Lk, a.Hkv, 1, kRows);
+    ok = ok && encode_planes(&m.q, t[0].dst, a.B, a.Lq, a.H, 1, f.p.P, per) &&
+         encode_planes(&m.go, t[1].dst, a.B, a.Lq, a.H, 1, f.p.P, per) &&
+         encode_planes(&m.k, t[2].dst, a.B, a.Lk, a.Hkv, 1, 1, kRows) &&
+         encode_planes(&m.v, t[3].dst, a.B, a.Lk, a.Hkv, 1, 1, kRows);
   } else {
     ok = ok && encode_map(&m.q, a.q, dtype, a.B, a.Lq, a.H, a.D, a.sq.b, a.sq.l, a.sq.h, f.p.P, per) &&
          encode_map(&m.go, a.go, dtype, a.B, a.Lq, a.H, a.D, a.sgo.b, a.sgo.l, a.sgo.h, f.p.P, per) &&

@@ -87,6 +87,30 @@ template <int WARPS> __device__ __forceinline__ int2 hull_of(const Hull &h) {
   return hi > 0 ? make_int2(lo, hi) : make_int2(0, 0);
 }
 
+// dot of the first `n` of N elements of two rows, n a multiple of a 16-byte load's elements; every load is
+// in flight at once
+template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x, const void *y, int n) {
+  typedef typename Elem<DT>::T E;
+  constexpr int W = 16 / (int)sizeof(E);
+  uint4 xv[N / W], yv[N / W];
+#pragma unroll
+  for (int d = 0; d < N; d += W) {
+    xv[d / W] = yv[d / W] = make_uint4(0, 0, 0, 0);
+    if (d < n) {
+      xv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(x) + d));
+      yv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int d = 0; d < N / W; ++d) {
+    const E *xe = reinterpret_cast<const E *>(&xv[d]), *ye = reinterpret_cast<const E *>(&yv[d]);
+#pragma unroll
+    for (int k = 0; k < W; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
+  }
+  return s;
+}
+
 // Tensor-core kernels: which calls they take, their workspace (of the sizes alone), and the launch.
 bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D);  // by type and sizes
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);                      // and by strides and alignment
@@ -98,6 +122,11 @@ cudaError_t launch_attn_step(const AttnArgs &a, int dtype, cudaStream_t stream);
 bool attn_bwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
+// Float32 heads of 65 to 128 elements, as bfloat16 planes.
+bool attn_planes_takes(int dtype, long long Lq, long long Lk, int G, int D);
+bool attn_planes_fits(const AttnArgs &a, int dtype, bool backward);
+size_t attn_planes_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, bool backward);
+cudaError_t launch_attn_planes(const AttnArgs &a, bool backward, void *workspace, cudaStream_t stream);
 // Heads that share a row tile, of a group of G: the largest power of two that divides G, up to 16.
 int attn_row_pack(int G);
 // CUDA-core kernels: every other call.

@@ -90,8 +90,9 @@ bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long
 }
 
 bool encode_planes(TensorMap *m, const unsigned short *planes, long long B, long long L, long long H,
-                   int box_heads, int box_rows) {
-  return encode_map(m, planes, kBF16, B, L, H, 192, H * L * 192, 192, L * 192, box_heads, box_rows);
+                   int chunks, int box_heads, int box_rows) {
+  const int n = chunks * 192;
+  return encode_map(m, planes, kBF16, B, L, H, n, H * L * n, n, L * n, box_heads, box_rows);
 }
 
 namespace {
@@ -99,14 +100,14 @@ namespace {
 struct PlaneArgs {
   PlaneSource t[4];
   long long rows[4];  // B * H * L
-  int D;
+  int D, chunks;
 };
 
 // A thread has 8 columns of a row: 32 bytes in, 16 bytes out of each plane.  Bound by memory.
 __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ PlaneArgs a) {
   const PlaneSource &t = a.t[blockIdx.y];
-  const long long x = (long long)blockIdx.x * 256 + threadIdx.x, row = x / 8;
-  const int d0 = (int)(x % 8) * 8;
+  const long long x = (long long)blockIdx.x * 256 + threadIdx.x, row = x / (8 * a.chunks);
+  const int d0 = (int)(x % (8 * a.chunks)) * 8;
   if (row >= a.rows[blockIdx.y]) return;
   const unsigned l = (unsigned)(row % t.L);
   const long long bh = row / t.L, b = bh / t.H, h = bh % t.H;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Pla
   }
 #pragma unroll
   for (int p = 0; p < 3; ++p)
-    *reinterpret_cast<uint4 *>(t.dst + (row * 3 + p) * 64 + d0) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    *reinterpret_cast<uint4 *>(t.dst + ((row * a.chunks + d0 / 64) * 3 + p) * 64 + d0 % 64) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 }  // namespace
@@ -147,8 +148,9 @@ cudaError_t launch_planes(const PlaneSource *src, int n, long long B, int D, cud
     most = a.rows[i] > most ? a.rows[i] : most;
   }
   a.D = D;
+  a.chunks = (D + 63) / 64;
   if (most == 0) return cudaSuccess;
-  planes_kernel<<<dim3((unsigned)((most * 8 + 255) / 256), n), 256, 0, stream>>>(a);
+  planes_kernel<<<dim3((unsigned)((most * 8 * a.chunks + 255) / 256), n), 256, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -400,7 +400,8 @@ bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long
 bool map_fits(int dtype, const void *ptr, long long B, long long L, long long H, int D, long long sb,
               long long sl, long long sh);
 
-// Float32 tensors as bfloat16 planes [B, H, L, 3, 64], rows at or past the utterance's length as zeros.
+// Float32 tensors as bfloat16 planes [B, H, L, chunk of 64 columns, 3, 64], rows at or past the utterance's
+// length and columns past D as zeros.
 struct PlaneSource {
   const float *src;
   long long sb, sl, sh;
@@ -408,10 +409,11 @@ struct PlaneSource {
   int L, H;
   unsigned short *dst;
 };
+// of one chunk
 inline size_t plane_bytes(long long B, long long L, long long H) { return (size_t)(B * L * H) * 3 * 64 * 2; }
 cudaError_t launch_planes(const PlaneSource *src, int n, long long B, int D, cudaStream_t stream);
-// The map of such planes, as if of heads of 192 elements.
+// The map of such planes, as if of heads of 192 elements a chunk.
 bool encode_planes(TensorMap *m, const unsigned short *planes, long long B, long long L, long long H,
-                   int box_heads, int box_rows);
+                   int chunks, int box_heads, int box_rows);
 
 }  // namespace tdt
