@@ -100,8 +100,9 @@ extern "C" {
 size_t tdt_cross_attn_workspace_size(const int64_t sizes[6], int dtype, int backward) {
   using namespace tdt;
   if (check_sizes(sizes, dtype) != TDT_OK) return 0;
-  const bool tc = attn_tc_takes(dtype, sizes[1], sizes[2], (int)(sizes[3] / sizes[4]), (int)sizes[5]);
-  if (attn_planes_takes(dtype, sizes[1], sizes[2], (int)(sizes[3] / sizes[4]), (int)sizes[5]))
+  const int G = (int)(sizes[3] / sizes[4]), D = (int)sizes[5];
+  const bool tc = attn_tc_takes(dtype, sizes[1], sizes[2], G, D, backward != 0);
+  if (attn_planes_takes(dtype, sizes[1], sizes[2], G, D, backward != 0))
     return (backward ? delta_bytes(sizes) : 0) +
            attn_planes_workspace(sizes[0], sizes[1], sizes[2], (int)sizes[3], (int)sizes[4], backward != 0);
   if (!backward)
@@ -134,10 +135,10 @@ int tdt_cross_attn_fwd(const void *q, const void *k, const void *v, const int64_
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool tc = attn_fwd_tc_fits(a, dtype);
-  const cudaError_t e = attn_step_fits(a, dtype, tc) ? launch_attn_step(a, dtype, s)
-                        : tc                         ? launch_attn_fwd_tc(a, dtype, workspace, s)
+  const cudaError_t e = attn_step_fits(a, dtype, tc)        ? launch_attn_step(a, dtype, s)
+                        : tc                                ? launch_attn_fwd_tc(a, dtype, workspace, s)
                         : attn_planes_fits(a, dtype, false) ? launch_attn_planes(a, false, workspace, s)
-                                                     : launch_attn_general_fwd(a, dtype, s);
+                                                            : launch_attn_general_fwd(a, dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 
@@ -176,9 +177,9 @@ int tdt_cross_attn_bwd(const void *grad_out, const void *q, const void *k, const
   a.delta = static_cast<float *>(workspace);
   void *rest = static_cast<char *>(workspace) + delta_bytes(sizes);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = attn_bwd_tc_fits(a, dtype) ? launch_attn_bwd_tc(a, dtype, rest, s)
+  const cudaError_t e = attn_bwd_tc_fits(a, dtype)         ? launch_attn_bwd_tc(a, dtype, rest, s)
                         : attn_planes_fits(a, dtype, true) ? launch_attn_planes(a, true, rest, s)
-                                                   : launch_attn_general_bwd(a, dtype, s);
+                                                           : launch_attn_general_bwd(a, dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

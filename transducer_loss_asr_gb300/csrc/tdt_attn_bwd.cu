@@ -24,18 +24,18 @@
 // Few CTAs: the walk is split over several, whose float32 sums a third kernel adds in order.
 //
 // P, dS: rounding them to 16 bits is what the products need.  With delta from the rounded O it is what
-// dq's error consists of (bfloat16: 2.5e-3 of the largest element, 1.7e-3 where only inputs and results are
-// rounded); a delta from the unrounded O would need it kept from the forward pass in float32, and a dS of
-// two planes a product more.
+// dq's error consists of (bfloat16: 2.5e-3 of its norm, 1.7e-3 where only the result is rounded; delta's part
+// is 8e-4 at 512 frames and less with more).  A delta from the unrounded O would need it kept from the forward
+// pass in float32, and a dS of two planes two products more.
 //
 // Bound by the tensor cores and the shared memory that feeds them: a product of two shared-memory operands
 // of 128 x 128 x 16 takes the 64 clocks of its reads, and S, dP in both kernels are such.  Measured:
 //   16 x 1024 x 4096, 16 heads on 4 of 128, bfloat16   1,307 us (dq 567): 1,050 TFLOP/s on the five products
 //                                                      of the formula, 1,470 on the seven done
 //   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   82 us (dq 40, dk/dv 42)
-//   16 x 121 x 750 ragged, 16 heads of 64, one kernel  33.7 us for 66 MB; the two kernels: 48 us
-//   4 x 41 x 200, 8 heads of 64, one kernel            8.2 us, latency
-//   1201 x 2000, 8 heads of 64, float32                148 us (planes 6, dq 68, dk/dv 74)
+//   16 x 121 x 750, 16 heads of 64                     36.5 us by one kernel, 82.5 by two (ragged: 33.7)
+//   4 x 41 x 200, 8 heads of 64                        8.0 us by one kernel, 11.9 by two; latency
+//   1201 x 2000, 8 heads of 64, float32                149 us (alone: planes 6, dq 81, dk/dv 74)
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -1415,7 +1415,7 @@ bool attn_bwd_tc_fits(const AttnArgs &a, int dtype) {
   auto fits = [&](const void *p, const Strides &s, long long L, int H) {
     return map_fits(dtype, p, a.B, L, H, a.D, s.b, s.l, s.h);
   };
-  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D)) return false;
+  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D, true)) return false;
   // out and dO are read in vectors of 16 bytes, the results are stored by TMA
   if (!fits(a.out, a.so, a.Lq, a.H) || !fits(a.go, a.sgo, a.Lq, a.H) || !fits(a.dq, a.sdq, a.Lq, a.H) ||
       !fits(a.dk, a.sdk, a.Lk, a.Hkv) || !fits(a.dv, a.sdv, a.Lk, a.Hkv))

@@ -112,18 +112,19 @@ template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x
 }
 
 // Tensor-core kernels: which calls they take, their workspace (of the sizes alone), and the launch.
-bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D);  // by type and sizes
+bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D, bool backward);  // by type and sizes
 bool attn_fwd_tc_fits(const AttnArgs &a, int dtype);                      // and by strides and alignment
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype);
 cudaError_t launch_attn_fwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
 // Few rows: a kernel that reads k and v at memory speed.
+constexpr int kStepRows = 32;  // rows of a key head at most
 bool attn_step_fits(const AttnArgs &a, int dtype, bool tc_fits);
 cudaError_t launch_attn_step(const AttnArgs &a, int dtype, cudaStream_t stream);
 bool attn_bwd_tc_fits(const AttnArgs &a, int dtype);
 size_t attn_bwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype);
 cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cudaStream_t stream);
 // Float32 heads of 65 to 128 elements, as bfloat16 planes.
-bool attn_planes_takes(int dtype, long long Lq, long long Lk, int G, int D);
+bool attn_planes_takes(int dtype, long long Lq, long long Lk, int G, int D, bool backward);
 bool attn_planes_fits(const AttnArgs &a, int dtype, bool backward);
 size_t attn_planes_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, bool backward);
 cudaError_t launch_attn_planes(const AttnArgs &a, bool backward, void *workspace, cudaStream_t stream);

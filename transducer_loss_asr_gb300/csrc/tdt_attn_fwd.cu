@@ -20,7 +20,7 @@
 //
 // float32: q, k and v are split beforehand into three bfloat16 planes (8 + 8 + 8 bits), P in the threads,
 // and six products of planes stand for one; what they leave out is below 2^-24 of a term.  TMEM sums
-// are cut, not rounded, so each tile's sum is added to float32 registers (error 8e-7 of the largest output,
+// are cut, not rounded, so each tile's sum is added to float32 registers (error 8e-7 of the output's norm,
 // 1.2e-5 when the sum stayed in TMEM).
 //
 // Few row tiles: the frames are split over several CTAs, whose results (O, and the logarithm of
@@ -32,8 +32,9 @@
 // 2 of 96, windows of 300 frames: 25.6 us.  8 x 121 x 7501 ragged, bfloat16, 16 heads on 4 of 128: 57 us.
 // By latency at small ones: 4 x 41 x 200, 8 heads of 64: 7 us.  float32, 1201 x 2000, 8 heads of 64: 39 us
 // with the planes.
-// Two row tiles a CTA halve the reads of k and v from L2; one tile a CTA and two CTAs an SM do as well
-// where there is no second tile, and fill the SM when there are few.
+// Two row tiles a CTA halve the reads of k and v from L2 (16 x 1024 x 4096, 8 heads on 2 of 128: 197 us
+// against 210); where there is no second tile, one a CTA and two CTAs an SM (16 x 121 x 750, 16 heads of
+// 64: 15.5 us against 24.1).
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -623,9 +624,10 @@ int attn_row_pack(int G) {
   return P;
 }
 
-bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D) {
+bool attn_tc_takes(int dtype, long long Lq, long long Lk, int G, int D, bool backward) {
   if (Lq == 0 || Lk == 0) return false;
-  return dtype == kF32 ? D <= 64 && Lq * G > 8 : D <= 128;
+  // no workspace for float32 steps
+  return dtype == kF32 ? D <= 64 && (backward || Lq * G > kStepRows || D % 8 != 0) : D <= 128;
 }
 
 size_t attn_fwd_tc_workspace(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
@@ -636,7 +638,7 @@ bool attn_fwd_tc_fits(const AttnArgs &a, int dtype) {
   auto fits = [&](const void *p, const Strides &s, long long L, int H) {
     return map_fits(dtype, p, a.B, L, H, a.D, s.b, s.l, s.h);
   };
-  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D) || !fits(a.out, a.so, a.Lq, a.H)) return false;
+  if (!attn_tc_takes(dtype, a.Lq, a.Lk, a.G, a.D, false) || !fits(a.out, a.so, a.Lq, a.H)) return false;
   return dtype == kF32 || (fits(a.q, a.sq, a.Lq, a.H) && fits(a.k, a.sk, a.Lk, a.Hkv) &&
                            fits(a.v, a.sv, a.Lk, a.Hkv) && (attn_row_pack(a.G) == 1 || a.sq.h != 0));
 }

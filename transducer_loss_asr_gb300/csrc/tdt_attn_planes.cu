@@ -15,7 +15,12 @@
 //
 // Few CTAs: a cluster of up to 8 shares the walk; the sums are added over distributed shared memory, in order.
 //
-// Bound by the loads: a step of dq has 4.6 us of products at the tensor cores' rate and loads 480 KB.
+// Bound by the loads and the waits between products and elementwise work: a step of dq has 4.6 us of products at
+// the tensor cores' rate and loads 480 KB.  4 x 1201 x 2000, 8 heads of 128: forward 343 us, backward
+// 1,166 us (92 TFLOP/s of float32 products).  2 x 801 x 982 ragged, 8 heads of 128, forward: 62 us with the
+// call, 251 on the CUDA cores.  1 x 300 x 2000, 4 heads on 1 of 96, windows of 300: 23 us and 60 us.
+// Products go plane by plane, the small ones of both halves first: TMEM's cut sums are then small while there are
+// many of them (error 4 to 7e-7 of the results; half by half 1 to 2e-6, and a tenth faster).
 #include <cooperative_groups.h>
 
 #include "tdt_attn_common.cuh"
@@ -521,15 +526,16 @@ size_t tensor_bytes(long long B, long long L, long long H) { return (2 * plane_b
 
 }  // namespace
 
-bool attn_planes_takes(int dtype, long long Lq, long long Lk, int G, int D) {
-  return dtype == kF32 && D > 64 && D <= 128 && Lq > 0 && Lk > 0 && Lq * G > 8;
+bool attn_planes_takes(int dtype, long long Lq, long long Lk, int G, int D, bool backward) {
+  return dtype == kF32 && D > 64 && D <= 128 && Lq > 0 && Lk > 0 &&
+         (backward || Lq * G > kStepRows || D % 8 != 0);
 }
 
 bool attn_planes_fits(const AttnArgs &a, int dtype, bool backward) {
   auto fits = [&](const void *p, const Strides &s, long long L, int H) {  // 16-byte vectors
     return map_fits(dtype, p, a.B, L, H, a.D, s.b, s.l, s.h);
   };
-  return attn_planes_takes(dtype, a.Lq, a.Lk, a.G, a.D) &&
+  return attn_planes_takes(dtype, a.Lq, a.Lk, a.G, a.D, backward) &&
          (!backward || (fits(a.out, a.so, a.Lq, a.H) && fits(a.go, a.sgo, a.Lq, a.H)));
 }
 

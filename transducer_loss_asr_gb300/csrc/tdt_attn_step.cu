@@ -1,6 +1,7 @@
 // tdt_attn_step.cu -- cross attention of few query rows (a decoding step, a small beam), every type.
 //
-// With R = Lq * G rows a key head (G query heads share it), the work is to read k and v once: 4 R flops
+// With R = Lq * G rows a key head (G query heads share it; 8 a CTA, more rows: more CTAs, which mostly find
+// k and v in L2), the work is to read k and v once: 4 R flops
 // an element read; bound by memory for one or two rows (6.3 TB/s in float32, 5.4 TB/s in bfloat16 at
 // 64 x 16 heads of 64 and 750 frames, of 6.8 measured), by instructions above.  A cluster of S CTAs has one (utterance, key head); its CTAs take the
 // frames in turns of equal parts, the warps of a CTA again.  In a warp a frame belongs to L lanes (8, 16 or
@@ -21,12 +22,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kStepRows = 8;       // rows of a key head at most
+constexpr int kCtaRows = 8;  // rows of a key head that a CTA has
 constexpr int kWarps = 4;
 
 struct StepArgs {
   AttnArgs a;
   int splits;  // CTAs of a cluster
+  int groups;  // clusters that share the rows of a key head
 };
 
 // 8 elements as float32
@@ -75,11 +77,12 @@ __global__ void __launch_bounds__(kWarps * 32) attn_step_kernel(const __grid_con
   __shared__ float cta_m[R], cta_l[R];
   __shared__ __align__(16) float cta_o[R][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / L, d0 = lane % L * 8;
-  const unsigned unit = blockIdx.x / f.splits;  // = b * Hkv + hk
+  const unsigned cluster_id = blockIdx.x / f.splits, unit = cluster_id / f.groups;  // = b * Hkv + hk
   const int split = blockIdx.x % f.splits, hk = unit % a.Hkv;
   const long long b = unit / a.Hkv;
   const Lens n = utt_lens(a, b);
-  const int rows = a.Lq * a.G;                 // row r: query r / G, head hk * G + r % G
+  const int row0 = cluster_id % f.groups * R;
+  const int rows = a.Lq * a.G - row0;          // row r: query (row0 + r) / G, head hk * G + (row0 + r) % G
   const bool wide = d0 < a.D;                  // D is a multiple of 8
   int2 range[R];
   float q[R][8], o[R][8], m[R], l[R];
@@ -87,7 +90,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_step_kernel(const __grid_con
   const float c = a.scale * kLog2e;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int i = r / a.G;
+    const int i = (row0 + r) / a.G;
     range[r] = r < rows ? row_range(a, b, i, n) : make_int2(0, 0);
     if (range[r].y > range[r].x) {
       first = min(first, range[r].x);
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_step_kernel(const __grid_con
     }
     Load8<DT> x;
     if (wide && range[r].y > range[r].x) {
-      x.load(static_cast<const E *>(a.q) + b * a.sq.b + i * a.sq.l + (hk * a.G + r % a.G) * a.sq.h + d0);
+      x.load(static_cast<const E *>(a.q) + b * a.sq.b + i * a.sq.l + (hk * a.G + (row0 + r) % a.G) * a.sq.h + d0);
       x.get(q[r]);
     } else {
 #pragma unroll
@@ -254,7 +257,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_step_kernel(const __grid_con
         out += g * *cluster.map_shared_rank(&cta_o[r][d], i);
       }
     }
-    const int i = r / a.G, h = hk * a.G + r % a.G;
+    const int i = (row0 + r) / a.G, h = hk * a.G + (row0 + r) % a.G;
     const float v = n.bad ? NAN : sum == 0.0f ? 0.0f : out / sum;
     if (d < a.D)
       static_cast<E *>(const_cast<void *>(a.out))[b * a.so.b + i * a.so.l + h * a.so.h + d] =
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_step_kernel(const __grid_con
 
 template <int DT, int R, int L> cudaError_t launch(const StepArgs &f, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(f.a.B * f.a.Hkv * f.splits));
+  cfg.gridDim = dim3((unsigned)(f.a.B * f.a.Hkv * f.groups * f.splits));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
@@ -301,8 +304,11 @@ bool attn_step_fits(const AttnArgs &a, int dtype, bool tc_fits) {
   };
   // The arithmetic of R rows is on the CUDA cores: where the tensor-core kernel can take the call, it
   // is as fast from 3 rows on (bfloat16, 64 x 16 heads of 64, 750 frames: 1 row 36 us against 50,
-  // 2 rows 40 against 50, 4 rows 74 against 51; the step then is bound by its instructions).
-  const int most = tc_fits ? 2 : kStepRows;
+  // 2 rows 40 against 50, 4 rows 74 against 51; the step then is bound by its instructions).  In float32
+  // the tensor cores take six products and planes of k and v made beforehand, and this kernel is ahead up
+  // to about 32 rows (64 x 8 heads of 64, 750 frames: 16 rows 105 us against 175, 32 rows 194 against 177,
+  // of three query heads a key head 193 against 339; 200 frames, one utterance: 8 against 14).
+  const int most = tc_fits && dtype != kF32 ? 2 : kStepRows;
   return (long long)a.Lq * a.G <= most && a.D % 8 == 0 && fits(a.q, a.sq, a.Lq, a.H) &&
          fits(a.k, a.sk, a.Lk, a.Hkv) && fits(a.v, a.sv, a.Lk, a.Hkv);
 }
@@ -311,7 +317,8 @@ cudaError_t launch_attn_step(const AttnArgs &a, int dtype, cudaStream_t stream) 
   StepArgs f = {};
   f.a = a;
   // a cluster's CTAs, while CTAs leave the GPU idle (8 of 4 warps an SM) and each keeps 64 frames
-  const long long units = a.B * a.Hkv;
+  f.groups = (a.Lq * a.G + kCtaRows - 1) / kCtaRows;
+  const long long units = a.B * a.Hkv * f.groups;
   long long s = units > 0 ? 8 * kSMs / units : 1;
   s = std::min<long long>({s, (a.Lk + 63) / 64, 8});
   f.splits = 1;

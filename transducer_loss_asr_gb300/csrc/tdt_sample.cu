@@ -18,6 +18,9 @@
 // The cut usually lies among the listed tokens -- top_k of them exist, or their weight reaches top_p's
 // share of all, or min_p is above any unlisted weight -- and then selection and draw read the list only.
 // Otherwise they read the row again (from L2, where it does not stay).
+// Bound: few rows by the latency of the phases (1 x 8,193: 10 us); 656 x 8,193 float32 with each row's own
+// settings by the selection's instructions, 70 us for 21 MB; 2,048 x 131,072 bfloat16 by pass 2's
+// instructions and the second read, 263 us for 537 MB (2.0 TB/s of logits).
 // Wide rows are bound by pass 2's instructions.  Its weights are below 2^-9 of the largest, apart from the
 // listed ones, and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no
 // conversion, and whole-number sums of those bits; what the listed tokens contribute is taken out when
@@ -856,14 +859,24 @@ cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   return cudaGetLastError();
 }
 // Warps a row: few for many rows, which share the SMs; many for few rows, where only the time of one counts.
-// Wide rows are read twice, and two a SM at a time are what L2 holds (2,048 x 131,072 bfloat16: 262 us; three
+// Measured, bfloat16, top_k 50 and top_p 0.95, us:
+//     rows x tokens    1 warp   4 warps   8 warps   16 warps   32 warps
+//        656 x 250       20.1      11.8
+//      2,048 x 250       23.7      31.6
+//        100 x 1,000               17.7                 11.5
+//        300 x 1,000               18.5                 22.3
+//        656 x 8,193                         55.4       60.1
+//          1 x 16,384                        11.3        9.7
+//          1 x 131,072                                  26.5       24.4
+// Wide rows are read twice, and two a SM at a time are what L2 holds (2,048 x 131,072, top_p 0.9: 262 us; three
 // of 8 warps 286, one of 32 warps 314).
 template <int DT> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
-  if (a.V <= 256) return launch<DT, 1, true>(a, N, s);
-  if (a.V <= kOwnList) return launch<DT, 4, true>(a, N, s);
+  constexpr int kSMs = 152;
+  if (a.V <= 256) return N > 8 * kSMs ? launch<DT, 1, true>(a, N, s) : launch<DT, 4, true>(a, N, s);
+  if (a.V <= kOwnList) return N > kSMs ? launch<DT, 4, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
   if (a.V <= kResident)
-    return N > 2 * 152 ? launch<DT, 8, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
-  return N > 2 * 152 ? launch<DT, 16, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
+    return N > 2 * kSMs ? launch<DT, 8, true>(a, N, s) : launch<DT, 16, true>(a, N, s);
+  return N > 2 * kSMs ? launch<DT, 16, false>(a, N, s) : launch<DT, 32, false>(a, N, s);
 }
 
 }  // namespace
