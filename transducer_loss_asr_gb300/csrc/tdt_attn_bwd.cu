@@ -205,15 +205,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       for (; ok && s < T; ++s) {
         if (s == 0 && !a.windows) continue;  // loaded above
-        ok = wait(&sh.k.empty[s % S::KS], ((unsigned)(s / S::KS) & 1) ^ 1);
-        if (!ok) break;
-        load_k(s);
-        ok = wait(&sh.v.empty[s % S::VS], ((unsigned)(s / S::VS) & 1) ^ 1);
-        if (!ok) {
-          ++s;
-          break;
-        }
-        load_v(s);
+        for (int x = 0; ok && x < 2; ++x)  // in the order of the products
+          if ((x == 0) == (S::KS > 1)) {
+            ok = wait(&sh.k.empty[s % S::KS], ((unsigned)(s / S::KS) & 1) ^ 1);
+            if (ok) load_k(s);
+          } else {
+            ok = wait(&sh.v.empty[s % S::VS], ((unsigned)(s / S::VS) & 1) ^ 1);
+            if (ok) load_v(s);
+          }
       }
       if (!ok) {  // copies in flight land before the CTA ends
         Waiter::drain(&sh.rows_full, 0);
@@ -241,22 +240,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok)
           mma_rows_planes<DT, DP>(tmem + (s & 1) * kRows, qa, ka + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
       };
-      auto grads = [&](int s) {  // dP of tile s; its scores came before
+      auto grads = [&](int s) {  // dP of tile s
         const int slot = s % S::VS;
         ok = ok && wait(&sh.v.full[slot], (unsigned)(s / S::VS) & 1);
         tc_fence_after();
         if (!ok) return;
         mma_rows_planes<DT, DP>(tmem + kDp, ga, va + slot * S::TILE, S::CHUNK, S::PLANE, i_s);
-        mma_commit(&sh.scores);
         mma_commit(&sh.v.empty[slot]);
       };
       scores(0);
       grads(0);
+      if (ok) mma_commit(&sh.scores);
       for (int s = 0; ok && s < T; ++s) {
-        if (S::KS > 1 && s + 1 < T) {
-          scores(s + 1);
+        if (s + 1 < T) {
+          if (S::KS > 1) scores(s + 1);
           ok = ok && wait(&sh.dp_free, s & 1);
           grads(s + 1);
+          if (S::KS > 1 && ok) mma_commit(&sh.scores);
         }
         ok = ok && wait(&sh.ds_ready, s & 1);
         tc_fence_after();
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (s + 1 == T) mma_commit(&sh.done);
         if (S::KS == 1 && s + 1 < T) {  // k's slot is free after these products only
           scores(s + 1);
-          grads(s + 1);
+          if (ok) mma_commit(&sh.scores);
         }
       }
       if (!ok) {
@@ -533,19 +533,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = start; ok && t < t1; t = next(t + 1), ++s) {
         const int slot = s % S::RS, l = t % row_tiles * per, h = hk * a.G + t / row_tiles * P;
         const unsigned turn = ((unsigned)(s / S::RS) & 1) ^ 1;
-        ok = wait(&sh.q.empty[slot], turn);
-        if (!ok) break;
-        unsigned long long *bar = cut(t) ? &sh.q_tail[slot] : &sh.q.full[slot];
-        arrive_expect_tx(bar, S::TILE);
-        load_rows<DT, DP>(&qm, q_slots + slot * S::TILE, bar, h * f.q_h, l, (int)b * f.q_b);
-        ok = wait(&sh.g.empty[slot], turn);
-        if (!ok) {
-          ++s;
-          break;
-        }
-        bar = cut(t) ? &sh.g_tail[slot] : &sh.g.full[slot];
-        arrive_expect_tx(bar, S::TILE);
-        load_rows<DT, DP>(&gm, g_slots + slot * S::TILE, bar, h * f.go_h, l, (int)b * f.go_b);
+        for (int x = 0; ok && x < 2; ++x)  // in the order of the products
+          if ((x == 0) == (S::RS > 1)) {
+            ok = wait(&sh.q.empty[slot], turn);
+            if (!ok) break;
+            unsigned long long *bar = cut(t) ? &sh.q_tail[slot] : &sh.q.full[slot];
+            arrive_expect_tx(bar, S::TILE);
+            load_rows<DT, DP>(&qm, q_slots + slot * S::TILE, bar, h * f.q_h, l, (int)b * f.q_b);
+          } else {
+            ok = wait(&sh.g.empty[slot], turn);
+            if (!ok) break;
+            unsigned long long *bar = cut(t) ? &sh.g_tail[slot] : &sh.g.full[slot];
+            arrive_expect_tx(bar, S::TILE);
+            load_rows<DT, DP>(&gm, g_slots + slot * S::TILE, bar, h * f.go_h, l, (int)b * f.go_b);
+          }
       }
       if (!ok) {
         Waiter::drain(&sh.frames_full, 0);
@@ -617,8 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     (S::PLANES == 1 && s > 0) || g > 0);
         mma_commit(&sh.q.empty[slot]);
         if (after >= t1) mma_commit(&sh.done);
-        if (S::RS == 1 && after < t1) scores(s + 1);  // q's slot is free after these products only
         if (after < t1) grads(s + 1);
+        if (S::RS == 1 && after < t1) scores(s + 1);  // q's slot is free after dK's products only
         t = after;
       }
       if (!ok) {
