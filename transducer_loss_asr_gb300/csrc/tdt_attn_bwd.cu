@@ -35,7 +35,7 @@
 //   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   82 us (dq 40, dk/dv 42)
 //   16 x 121 x 750, 16 heads of 64                     36.5 us by one kernel, 82.5 by two (ragged: 33.7)
 //   4 x 41 x 200, 8 heads of 64                        8.0 us by one kernel, 11.9 by two; latency
-//   1201 x 2000, 8 heads of 64, float32                149 us (alone: planes 6, dq 81, dk/dv 74)
+//   1201 x 2000, 8 heads of 64, float32                135 us with the planes
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -329,42 +329,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (s > 0) add_tile();  // dQ of the tile before was issued before these scores
       const unsigned s_col = tmem + lanes + (s & 1) * kRows + group * 64,
                      p_col = tmem + lanes + kDp + group * 64;
-      unsigned x[2][32], y[2][32], out[S::PLANES][32];
+      constexpr int H = S::PLANES == 3 ? 2 : 1;  // float32: half of the columns at a time, for the registers' sake
+      unsigned x[2][32], y[2 / H][32];
       tmem_ld32(s_col, x[0]);
       tmem_ld32(s_col + 32, x[1]);
-      tmem_ld32(p_col, y[0]);
-      tmem_ld32(p_col + 32, y[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      mbar_arrive(&sh.dp_free);
-      const int j0 = frame(s) + group * 64;
+      const int j0 = frame(s) + group * 64, lo = range.x - j0;
+      const unsigned len = (unsigned)(range.y - range.x);
       const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2),
                    d2 = make_float2(-delta, -delta);
-      if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
-        // frames that the row does not see: s = -inf weighs 0, and dP may be anything
-        const int lo = range.x - j0;
-        const unsigned len = (unsigned)(range.y - range.x);
+      const bool part = __any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64));
 #pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if ((unsigned)(i - lo) >= len) {
-            x[i >> 5][i & 31] = 0xff800000u;
-            y[i >> 5][i & 31] = 0;
-          }
-      }
+      for (int h = 0; h < H; ++h) {
+        constexpr int N = 64 / H;
 #pragma unroll
-      for (int i = 0; i < 64; i += 2) {
-        const float2 z = fma2(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), c2, l2);
-        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
-        const float2 ds = mul2(p, add2(pair(y[i >> 5][i & 31], y[i >> 5][(i + 1) & 31]), d2));
-        unsigned planes[S::PLANES];
-        split2<DT>(ds, planes);
+        for (int i = 0; i < N / 32; ++i) tmem_ld32(p_col + h * N + i * 32, y[i]);
+        tmem_wait_ld();
+        if (h == H - 1) {
+          tc_fence_before();
+          mbar_arrive(&sh.dp_free);
+        }
+        if (part) {
+          // frames that the row does not see: s = -inf weighs 0, and dP may be anything
 #pragma unroll
-        for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
-      }
-      tmem_st32(s_col, out[0]);
-      if constexpr (S::PLANES == 3) {
-        tmem_st32(s_col + 32, out[1]);
-        tmem_st32(tmem + lanes + kThird + group * 32, out[2]);
+          for (int i = 0; i < N; ++i)
+            if ((unsigned)(h * N + i - lo) >= len) {
+              x[(h * N + i) >> 5][i & 31] = 0xff800000u;
+              y[i >> 5][i & 31] = 0;
+            }
+        }
+        unsigned out[S::PLANES][N / 2];
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const unsigned *xs = &x[(h * N + i) >> 5][i & 31], *ys = &y[i >> 5][i & 31];
+          const float2 z = fma2(pair(xs[0], xs[1]), c2, l2);
+          const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+          const float2 ds = mul2(p, add2(pair(ys[0], ys[1]), d2));
+          unsigned planes[S::PLANES];
+          split2<DT>(ds, planes);
+#pragma unroll
+          for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
+        }
+        if constexpr (S::PLANES == 3) {
+          tmem_st16(s_col + h * 16, out[0]);
+          tmem_st16(s_col + 32 + h * 16, out[1]);
+          tmem_st16(tmem + lanes + kThird + group * 32 + h * 16, out[2]);
+        } else {
+          tmem_st32(s_col, out[0]);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -695,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
         if (s > 0) add_tile();  // the products of the tile before were issued before these scores
-        unsigned x[2][32], out[S::PLANES][32];
+        constexpr int H = S::PLANES == 3 ? 2 : 1, N = 64 / H;  // float32: half of the columns at a time
+        unsigned x[2][32];
         tmem_ld32(s_col, x[0]);
         tmem_ld32(s_col + 32, x[1]);
         tmem_wait_ld();
@@ -724,17 +736,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((unsigned)(j - lo[i]) >= (unsigned)len[i]) x[i >> 5][i & 31] = 0;
         }
 #pragma unroll
-        for (int i = 0; i < 64; i += 2)
-        {
-          unsigned planes[S::PLANES];
-          split2<DT>(pair(x[i >> 5][i & 31], x[i >> 5][(i + 1) & 31]), planes);
+        for (int h = 0; h < H; ++h) {
+          unsigned out[S::PLANES][N / 2];
 #pragma unroll
-          for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
-        }
-        tmem_st32(s_col, out[0]);
-        if constexpr (S::PLANES == 3) {
-          tmem_st32(s_col + 32, out[1]);
-          tmem_st32(tmem + lanes + kThird + group * 32, out[2]);
+          for (int i = 0; i < N; i += 2) {
+            const unsigned *xs = &x[(h * N + i) >> 5][i & 31];
+            unsigned planes[S::PLANES];
+            split2<DT>(pair(xs[0], xs[1]), planes);
+#pragma unroll
+            for (int k = 0; k < S::PLANES; ++k) out[k][i / 2] = planes[k];
+          }
+          if constexpr (S::PLANES == 3) {
+            tmem_st16(s_col + h * 16, out[0]);
+            tmem_st16(s_col + 32 + h * 16, out[1]);
+            tmem_st16(tmem + lanes + kThird + group * 32 + h * 16, out[2]);
+          } else {
+            tmem_st32(s_col, out[0]);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -747,27 +765,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(d_col + 32, y[1]);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          const float4 dl = *reinterpret_cast<const float4 *>(delta + i);
-          const float2 un = make_float2(kUnshift<DT>, kUnshift<DT>);
-          const unsigned *p = &x[i >> 5][i & 31], *g = &y[i >> 5][i & 31];
-          const float2 d0 = make_float2(dl.x, dl.y), d1 = make_float2(dl.z, dl.w);
-          const float2 g0 = pair(g[0], g[1]), g1 = pair(g[2], g[3]);
-          const float2 v0 = mul2(pair(p[0], p[1]), DT == kF16 ? fma2(g0, un, d0) : add2(g0, d0)),
-                       v1 = mul2(pair(p[2], p[3]), DT == kF16 ? fma2(g1, un, d1) : add2(g1, d1));
-          unsigned p0[S::PLANES], p1[S::PLANES];
-          split2<DT>(v0, p0);
-          split2<DT>(v1, p1);
+        for (int h = 0; h < H; ++h) {
+          unsigned out[S::PLANES][N / 2];
 #pragma unroll
-          for (int k = 0; k < S::PLANES; ++k) {
-            out[k][i / 2] = p0[k];
-            out[k][i / 2 + 1] = p1[k];
+          for (int i = h * N; i < h * N + N; i += 4) {
+            const float4 dl = *reinterpret_cast<const float4 *>(delta + i);
+            const float2 un = make_float2(kUnshift<DT>, kUnshift<DT>);
+            const unsigned *p = &x[i >> 5][i & 31], *g = &y[i >> 5][i & 31];
+            const float2 d0 = make_float2(dl.x, dl.y), d1 = make_float2(dl.z, dl.w);
+            const float2 g0 = pair(g[0], g[1]), g1 = pair(g[2], g[3]);
+            const float2 v0 = mul2(pair(p[0], p[1]), DT == kF16 ? fma2(g0, un, d0) : add2(g0, d0)),
+                         v1 = mul2(pair(p[2], p[3]), DT == kF16 ? fma2(g1, un, d1) : add2(g1, d1));
+            unsigned p0[S::PLANES], p1[S::PLANES];
+            split2<DT>(v0, p0);
+            split2<DT>(v1, p1);
+#pragma unroll
+            for (int k = 0; k < S::PLANES; ++k) {
+              out[k][(i - h * N) / 2] = p0[k];
+              out[k][(i - h * N) / 2 + 1] = p1[k];
+            }
           }
-        }
-        tmem_st32(d_col, out[0]);
-        if constexpr (S::PLANES == 3) {
-          tmem_st32(d_col + 32, out[1]);
-          tmem_st32(tmem + lanes + kThird + 64 + group * 32, out[2]);
+          if constexpr (S::PLANES == 3) {
+            tmem_st16(d_col + h * 16, out[0]);
+            tmem_st16(d_col + 32 + h * 16, out[1]);
+            tmem_st16(tmem + lanes + kThird + 64 + group * 32 + h * 16, out[2]);
+          } else {
+            tmem_st32(d_col, out[0]);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
