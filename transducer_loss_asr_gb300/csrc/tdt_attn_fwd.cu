@@ -30,6 +30,7 @@
 // 345 us, 1,590 TFLOP/s of 1,936 measured for a library product; what is lost are the walk's two ends and
 // exponentials that the other stream's products do not cover.  8 x 1201 x 2000 ragged, float16, 8 heads on
 // 2 of 96, windows of 300 frames: 25.6 us.  8 x 121 x 7501 ragged, bfloat16, 16 heads on 4 of 128: 57 us.
+// By memory for steps of shared heads: 128 x 1 x 6000, 32 heads on 8 of 128: 485 us, 6.5 TB/s of 6.8 measured.
 // By latency at small ones: 4 x 41 x 200, 8 heads of 64: 7 us.  float32, 1201 x 2000, 8 heads of 64: 39 us
 // with the planes.
 // Two row tiles a CTA halve the reads of k and v from L2 (16 x 1024 x 4096, 8 heads on 2 of 128: 197 us

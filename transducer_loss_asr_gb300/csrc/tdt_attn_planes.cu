@@ -17,7 +17,7 @@
 //
 // Bound by the loads and the waits between products and elementwise work: a step of dq has 4.6 us of products at
 // the tensor cores' rate and loads 480 KB.  4 x 1201 x 2000, 8 heads of 128: forward 343 us, backward
-// 1,166 us (92 TFLOP/s of float32 products).  2 x 801 x 982 ragged, 8 heads of 128, forward: 62 us with the
+// 1,166 us (91 TFLOP/s of float32 products).  2 x 801 x 982 ragged, 8 heads of 128, forward: 62 us with the
 // call, 251 on the CUDA cores.  1 x 300 x 2000, 4 heads on 1 of 96, windows of 300: 23 us and 60 us.
 // Products go plane by plane, the small ones of both halves first: TMEM's cut sums are then small while there are
 // many of them (error 4 to 7e-7 of the results; half by half 1 to 2e-6, and a tenth faster).

@@ -1,13 +1,16 @@
 // tdt_attn_step.cu -- cross attention of few query rows (a decoding step, a small beam), every type.
 //
 // With R = Lq * G rows a key head (G query heads share it; 8 a CTA, more rows: more CTAs, which mostly find
-// k and v in L2), the work is to read k and v once: 4 R flops
-// an element read; bound by memory for one or two rows (6.3 TB/s in float32, 5.4 TB/s in bfloat16 at
-// 64 x 16 heads of 64 and 750 frames, of 6.8 measured), by instructions above.  A cluster of S CTAs has one (utterance, key head); its CTAs take the
-// frames in turns of equal parts, the warps of a CTA again.  In a warp a frame belongs to L lanes (8, 16 or
-// 32, of 8 elements each), so a 16-byte load a lane (two for float32) reads 32 / L frames, and U = 4 such
-// groups of k and v are in flight, and the next turn's are loaded while this one's are at work.  A lane holds its 8 elements of each row of q and of the running output, and each
-// group of L lanes its own running maximum and sum, so lanes exchange partial scores only:
+// k and v in L2), the work is to read k and v once: 4 R flops an element read; bound by memory for one or two
+// rows (6.3 TB/s in float32, 5.4 TB/s in bfloat16 at 64 x 16 heads of 64 and 750 frames, of 6.8 measured), by
+// instructions above.  64 ragged x 750, 16 heads of 64, float16: 30 us, 4.9 TB/s.  1 x 200, 8 heads of 64: 4.3 us,
+// latency.
+// A cluster of S CTAs has one (utterance, key head); its CTAs take the frames in turns of equal parts, the
+// warps of a CTA again.  In a warp a frame belongs to L lanes (8, 16 or 32, of 8 elements each), so a 16-byte
+// load a lane (two for float32) reads 32 / L frames; U = 4 such groups of k and v are in flight (2 for
+// float32 or more rows), and the next turn's are loaded while this one's are at work.  A lane holds its 8
+// elements of each row of q and of the running output, and each group of L lanes its own running maximum and
+// sum, so lanes exchange partial scores only:
 //   s = q . k (log2 L shuffles), m' = max(m, s), l = l 2^(m - m') + 2^(s - m'), o = o 2^(m - m') + 2^(s - m') v
 // The groups, the warps and then the CTAs of the cluster (over distributed shared memory) are joined in
 // a fixed order.

@@ -20,7 +20,7 @@
 // Otherwise they read the row again (from L2, where it does not stay).
 // Bound: few rows by the latency of the phases (1 x 8,193: 10 us); 656 x 8,193 float32 with each row's own
 // settings by the selection's instructions, 70 us for 21 MB; 2,048 x 131,072 bfloat16 by pass 2's
-// instructions and the second read, 263 us for 537 MB (2.0 TB/s of logits).
+// instructions and the second read, 241 to 319 us for 537 MB, by card.
 // Wide rows are bound by pass 2's instructions.  Its weights are below 2^-9 of the largest, apart from the
 // listed ones, and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no
 // conversion, and whole-number sums of those bits; what the listed tokens contribute is taken out when
@@ -868,8 +868,8 @@ cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
 //        656 x 8,193                         55.4       60.1
 //          1 x 16,384                        11.3        9.7
 //          1 x 131,072                                  26.5       24.4
-// Wide rows are read twice, and two a SM at a time are what L2 holds (2,048 x 131,072, top_p 0.9: 262 us; three
-// of 8 warps 286, one of 32 warps 314).
+// Wide rows are read twice, and two a SM at a time are what L2 holds (2,048 x 131,072, top_p 0.9, on one card: 262 us;
+// three of 8 warps 286, one of 32 warps 314).
 template <int DT> cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   constexpr int kSMs = 152;
   if (a.V <= 256) return N > 8 * kSMs ? launch<DT, 1, true>(a, N, s) : launch<DT, 4, true>(a, N, s);

@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(256) planes_kernel(const __grid_constant__ Pla
   }
 #pragma unroll
   for (int p = 0; p < 3; ++p)
-    *reinterpret_cast<uint4 *>(t.dst + ((row * a.chunks + d0 / 64) * 3 + p) * 64 + d0 % 64) = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+    *reinterpret_cast<uint4 *>(t.dst + ((row * a.chunks + d0 / 64) * 3 + p) * 64 + d0 % 64) =
+        make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
 }
 
 }  // namespace
