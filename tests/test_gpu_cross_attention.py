@@ -327,3 +327,49 @@ def test_tails_of_every_walk_length(binding, dtype, D):
 def test_float32_heads_over_64(binding, record_margin, shape, lens, windows):
     """One tile and many, walks shared by 1 to 8 blocks, packed heads, widths that fill their last part or not."""
     _check(binding, shape, torch.float32, record=record_margin, case=f"wide {shape}", lens=lens, windows=windows)
+
+
+def test_float32_heads_over_64_off_the_usual_ways(binding):
+    """Odd addresses, bad lengths, another stream, a graph, and the same bits each time."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    base = torch.randn(2, 300, 3, 99, generator=g, device="cuda")
+    q, k, v, go = base[:, :70, :2, 1:97], base[:, :, :1, 2:98], base[:, :, 1:2, 3:99], base[:, 80:150, 1:3, 0:96]
+    want = _reference(q, k, v, go, _seen(2, 70, 300, None, None, None, q.device), 96 ** -0.5, torch.float32)
+    out, lse = binding.tdt_cross_attn_fwd(q, k, v)
+    dq, dk, dv = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse)
+    for name, x in dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv).items():
+        _near(name, x, *want[name])
+    q, go = (torch.randn(3, 70, 2, 96, generator=g, device="cuda") for _ in range(2))
+    k, v = (torch.randn(3, 130, 1, 96, generator=g, device="cuda") for _ in range(2))
+    for key, bad in (("k_lens", [131, -1, 130]), ("q_lens", [71, -2, 70])):
+        a = {key: torch.tensor(bad, device="cuda")}
+        out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+        assert bool(out[:2].isnan().all()) and bool(lse[:2].isnan().all()) and bool(out[2].isfinite().all())
+        for x in binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a):
+            assert bool((x[:2] == 0).all()) and bool(x.isfinite().all())
+    q, k, v, go, a = _inputs((3, 140, 1500, 4, 2, 128), torch.float32, 14, lens=True, windows=True)
+    out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+    want = (out, lse) + binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        o2, l2 = binding.tdt_cross_attn_fwd(q, k, v, **a)
+        got = (o2, l2) + binding.tdt_cross_attn_bwd(go, q, k, v, o2, l2, **a)
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o3, l3 = binding.tdt_cross_attn_fwd(q, k, v, **a)
+        replayed = (o3, l3) + binding.tdt_cross_attn_bwd(go, q, k, v, o3, l3, **a)
+    graph.replay()
+    torch.cuda.synchronize()
+    for x, y, z in zip(want, got, replayed):
+        assert torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0)) and torch.equal(x.nan_to_num(7.0), z.nan_to_num(7.0))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 9, 300, 2, 2, 64), (2, 5, 200, 12, 4, 40), (1, 32, 130, 1, 1, 128), (2, 3, 90, 8, 1, 192),
+                                   (1, 33, 130, 1, 1, 72), (2, 11, 500, 6, 2, 256)], ids=str)
+def test_rows_shared_by_blocks(binding, record_margin, shape, dtype):
+    """9 to 33 rows a key head: several blocks share a key head's rows, the last one in part."""
+    for how in (dict(), dict(lens=True), dict(lens=True, windows=True)):
+        _check(binding, shape, dtype, record=record_margin, case=f"rows {shape}", **how)
