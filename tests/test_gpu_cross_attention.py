@@ -373,3 +373,47 @@ def test_rows_shared_by_blocks(binding, record_margin, shape, dtype):
     """9 to 33 rows a key head: several blocks share a key head's rows, the last one in part."""
     for how in (dict(), dict(lens=True), dict(lens=True, windows=True)):
         _check(binding, shape, dtype, record=record_margin, case=f"rows {shape}", **how)
+
+
+def _past_lengths(shape, dtype, q_len, k_len, past, seed=0, empty=None):
+    """Inputs of one head width whose rows and frames past the lengths hold `past`; rows of `empty` have empty windows."""
+    B, Lq, Lk, H, Hkv, D = shape
+    q, k, v, go, a = _inputs(shape, dtype, seed, lens=True, poison=False)
+    a["q_lens"].fill_(q_len)
+    a["k_lens"].fill_(k_len)
+    for t, n in ((q, q_len), (go, q_len), (k, k_len), (v, k_len)):
+        t[:, n:] = past
+    if empty:
+        w = torch.zeros(B, Lq, 2, dtype=torch.int32, device="cuda")
+        w[..., 1] = Lk
+        w[:, slice(*empty)] = 0
+        a["windows"] = w
+    return q, k, v, go, a
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("past", [math.nan, math.inf], ids=["nan", "inf"])
+@pytest.mark.parametrize("Lk,k_len", [(200, 100), (2000, 1900)])  # one block a walk, and several
+@pytest.mark.parametrize("H,Lq,q_lens", [(2, 121, (0, 1, 31, 32, 33, 60, 64, 121)), (4, 31, (0, 8, 15, 31))])
+def test_rows_that_take_no_part_beside_frames_that_hold_anything(binding, dtype, past, Lk, k_len, H, Lq, q_lens):
+    """Whole warps of rows past the queries' length, in tiles whose frames past theirs are no numbers."""
+    for q_len in q_lens:
+        q, k, v, go, a = _past_lengths((1, Lq, Lk, H, 2, 64), dtype, q_len, k_len, past)
+        want = _reference(q, k, v, go, _seen(1, Lq, Lk, **a, dev=q.device), 0.125, dtype)
+        out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+        dq, dk, dv = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a)
+        assert bool((dq[:, q_len:] == 0).all()), q_len
+        for name, x in dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv).items():
+            _near(name, x, *want[name])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("Lq", [121, 300])  # one row tile and three
+def test_empty_windows_beside_frames_that_hold_anything(binding, dtype, Lq):
+    q, k, v, go, a = _past_lengths((2, Lq, 200, 2, 2, 64), dtype, Lq, 100, math.nan, empty=(32, 64))
+    want = _reference(q, k, v, go, _seen(2, Lq, 200, **a, dev=q.device), 0.125, dtype)
+    out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+    dq, dk, dv = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a)
+    assert bool((dq[:, 32:64] == 0).all())
+    for name, x in dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv).items():
+        _near(name, x, *want[name])

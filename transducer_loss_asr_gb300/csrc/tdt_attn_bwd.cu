@@ -1246,8 +1246,11 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       tmem_wait_ld();
     }
     float v[32];
+    // A row that sees nothing weighs 0 everywhere, but its dP meets frames past the utterance's end, whose v may hold
+    // anything, and 0 times that need not be 0.  Its dS then spoils its own dQ, set here, and the dK of those frames, which
+    // the storing warps set.
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 ? __uint_as_float(o[k]) * a.scale : 0.0f;
+    for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * a.scale : 0.0f;
     if (f.p.dq_splits == 1) {
       stage32<DT>(q_tile, S::TILE, r, group * 32, v);  // every product with q is done
       fence_async_shared();
