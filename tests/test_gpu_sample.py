@@ -229,3 +229,39 @@ def test_on_another_stream_and_in_a_graph(binding):
     torch.cuda.synchronize()
     for a, b, c in zip(want, got, again):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("V", [3000, 20000])
+@pytest.mark.parametrize("X,temperatures", [(20.0, [3e-6 * 1.1 ** i for i in range(16)]), (1e8, [8.0 * 1.1 ** i for i in range(12)])])
+def test_logits_on_a_coarse_grid(binding, V, X, temperatures):
+    """Neighbouring floats that are far apart in units of the temperature: three tokens weigh anything, two of them equal
+    and light; top-p takes one of the two, the one of lower index."""
+    rows, ts, ps, want = [], [], [], []
+    for T in temperatures:
+        per = LOG2E / np.float32(T)
+        x = np.float32(X)
+        for _ in range(200):
+            x = np.nextafter(x, np.float32(-np.inf))
+            z = float(np.float32(np.float32(x - np.float32(X)) * per))
+            if z < -15:
+                break
+            if z > -9:
+                continue
+            w = 2.0 ** (31 + z)  # the light ones' weight
+            p24 = math.ceil((2.0 ** 31 + 0.5 * w) / (2.0 ** 31 + 2 * w) * 2.0 ** 24)
+            if not 2.0 ** 31 + 0.2 * w < p24 / 2.0 ** 24 * (2.0 ** 31 + 2 * w) < 2.0 ** 31 + 0.8 * w:
+                continue
+            row = np.full(V, -np.inf, np.float32)
+            row[1], row[1000], row[1001] = x, X, x
+            rows.append(row)
+            ts.append(T)
+            ps.append(p24 / 2.0 ** 24)
+    n = len(rows)
+    assert n >= 20
+    logits = torch.from_numpy(np.stack(rows)).cuda()
+    how = dict(temperature=torch.tensor(ts, dtype=torch.float32, device="cuda"),
+               top_p=torch.tensor(ps, dtype=torch.float32, device="cuda"))
+    # the first of the kept tokens in the vocabulary's order, and the last
+    for u, token in ((0.0, 1), (1.0 - 2.0 ** -24, 1000)):
+        tokens, logp = binding.tdt_sample(logits, torch.full((n,), u, device="cuda"), **how)
+        assert tokens.tolist() == [token] * n

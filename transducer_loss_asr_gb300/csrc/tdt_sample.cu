@@ -763,6 +763,8 @@ __global__ void __launch_bounds__(NW * 32, NW == 16 && !RESIDENT ? 2 : 1) sample
         z = kListZ >> i;
         near = below((float)z - 0.002f);  // so that pass 2's bits are sure to show every token from here up
         if (need_all && i == 0) {
+          // ... also where neighbouring floats are far apart for the temperature, and this one weighs less than 2^-12
+          if (r.w.bits(near) < 1u << 19 && near < X) near = nextafterf(near, X);
           listed = r.template weigh<true, true>(near);
           all = r.total_low() + r.total_mass();  // also where the list did not fit
         } else {
