@@ -4,7 +4,9 @@ Where every weight is a power of two (T = log2(e), logits whole numbers) the dra
 gives the same token.  Elsewhere the exponential is good to 2^-21, so the drawn token's stretch of the running sum has to
 contain the target within 2^-20 of the weight that stays.
 """
+import ctypes
 import math
+import subprocess
 
 import numpy as np
 import pytest
@@ -265,3 +267,61 @@ def test_logits_on_a_coarse_grid(binding, V, X, temperatures):
     for u, token in ((0.0, 1), (1.0 - 2.0 ** -24, 1000)):
         tokens, logp = binding.tdt_sample(logits, torch.full((n,), u, device="cuda"), **how)
         assert tokens.tolist() == [token] * n
+
+
+HAMMER = r"""
+#include <cstdint>
+#include <atomic>
+#include <thread>
+#include <vector>
+typedef int (*Sample)(const void *, const int64_t *, int64_t, int, const float *, const float *, const int32_t *,
+                      const float *, const float *, double, int64_t, double, double, int32_t *, float *, void *);
+// `threads` threads call at once, each with rows of its own length on a stream of its own; returns the calls that failed
+extern "C" int hammer(Sample f, int threads, int times, void **logits, const int64_t *V, int64_t N, const float *u,
+                      int32_t **tokens, float **logprobs, void **streams) {
+  std::atomic<int> failed{0}, ready{0};
+  std::vector<std::thread> all;
+  for (int i = 0; i < threads; ++i)
+    all.emplace_back([&, i] {
+      const int64_t sizes[2] = {N, V[i]};
+      for (++ready; ready < threads;) {
+      }
+      for (int k = 0; k < times; ++k)
+        failed += f(logits[i], sizes, V[i], 0, u, nullptr, nullptr, nullptr, nullptr, 0.8, 50, 0.9, 0.0, tokens[i],
+                    logprobs[i], streams[i]) != 0;
+    });
+  for (auto &t : all) t.join();
+  return failed;
+}
+"""
+
+
+@pytest.mark.parametrize("N,times", [(2, 3000), (400, 300)])
+def test_threads_that_sample_rows_of_other_lengths(binding, tmp_path, N, times):
+    """Host threads whose calls want other amounts of shared memory of one kernel do not make each other's launches fail."""
+    (tmp_path / "hammer.cpp").write_text(HAMMER)
+    so = str(tmp_path / "hammer.so")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-pthread", "-o", so, str(tmp_path / "hammer.cpp")],
+                   check=True)
+    g = torch.Generator(device="cuda").manual_seed(10)
+    lengths = (1100, 16000, 1500, 12000)
+    rows = [torch.randn(N, V, generator=g, device="cuda") for V in lengths]
+    u = torch.rand(N, generator=g, device="cuda")
+    want = [binding.tdt_sample(x, u, 0.8, 50, 0.9) for x in rows]
+    got = [tuple(torch.empty_like(t) for t in pair) for pair in want]
+    streams = [torch.cuda.Stream() for _ in rows]
+    torch.cuda.synchronize()
+    n = len(rows)
+
+    def addresses(x):
+        return (ctypes.c_void_p * n)(*x)
+
+    failed = ctypes.CDLL(so).hammer(
+        ctypes.cast(binding.lib.tdt_sample, ctypes.c_void_p), n, times, addresses(x.data_ptr() for x in rows),
+        (ctypes.c_int64 * n)(*lengths), ctypes.c_int64(N), ctypes.c_void_p(u.data_ptr()),
+        addresses(t.data_ptr() for t, _ in got), addresses(l.data_ptr() for _, l in got),
+        addresses(s.cuda_stream for s in streams))
+    torch.cuda.synchronize()
+    assert failed == 0
+    for (t, l), (t2, l2) in zip(want, got):
+        assert torch.equal(t, t2) and torch.equal(l, l2)

@@ -852,10 +852,13 @@ __global__ void __launch_bounds__(NW * 32, NW == 16 && !RESIDENT ? 2 : 1) sample
 template <int DT, int NW, bool RESIDENT>
 cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   // a resident row starts at its first vector's place and is filled up to whole vectors
-  const size_t row = RESIDENT ? (size_t)((a.V + 16 + 3) / 4 * 4) * 4 : 0;
-  const size_t smem = row + (RESIDENT && a.V <= kOwnList ? 0 : 3 * Sampler<DT, NW, RESIDENT>::LIST * 4);
+  constexpr size_t list = 3 * Sampler<DT, NW, RESIDENT>::LIST * 4;
+  auto row = [](int V) { return RESIDENT ? (size_t)((V + 16 + 3) / 4 * 4) * 4 : 0; };
+  const size_t smem = row(a.V) + (RESIDENT && a.V <= kOwnList ? 0 : list);
+  // The limit is the kernel's, shared by all host threads: the most that any call wants, never this call's own.
   const cudaError_t e = cudaFuncSetAttribute(sample_kernel<DT, NW, RESIDENT>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)(row(kResident) + list));
   if (e != cudaSuccess) return e;
   sample_kernel<DT, NW, RESIDENT><<<(unsigned)N, NW * 32, smem, s>>>(a);
   return cudaGetLastError();
