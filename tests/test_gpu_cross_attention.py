@@ -417,3 +417,58 @@ def test_empty_windows_beside_frames_that_hold_anything(binding, dtype, Lq):
     assert bool((dq[:, 32:64] == 0).all())
     for name, x in dict(out=out, lse=lse, dq=dq, dk=dk, dv=dv).items():
         _near(name, x, *want[name])
+
+
+def _norm_errors(binding, q, k, v, go, a, dtype, units, least=None):
+    """The results' errors in 2-norm, each of its value's norm times `units` plus what the type's least step makes of it."""
+    D = q.shape[3]
+    want = _reference(q, k, v, go, _seen(q.shape[0], q.shape[1], k.shape[1], **a, dev=q.device), D ** -0.5, dtype)
+    out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+    dq, dk, dv = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a)
+    for name, x in dict(out=out, dq=dq, dk=dk, dv=dv).items():
+        value = want[name][0]
+        bound = units * value.norm().item() + (least or 0.0) / 2 * value.numel() ** 0.5
+        error = (x.double() - value).norm().item()
+        assert error <= bound, "%s: %.3g of its norm, %.3g allowed" % (
+            name, error / value.norm().item(), bound / value.norm().item())
+
+
+F16_SHAPES = [(1, 121, 2000, 2, 2, 64), (1, 300, 2000, 2, 2, 64), (2, 300, 700, 4, 2, 96), (3, 30, 500, 8, 2, 40)]
+
+
+@pytest.mark.parametrize("std", [1.0, 1e-3, 3e-4, 1e-4, 1e-5])
+@pytest.mark.parametrize("shape", F16_SHAPES, ids=str)
+def test_float16_small_upstream_gradients(binding, shape, std):
+    """Gradients keep the type's accuracy where grad_out times a weight is below the type's normal range.
+
+    Bound: a unit each for the results' rounding, for that of dS (or P) and for delta's from the rounded out; and half
+    a least step of the type an element."""
+    q, k, v, go, a = _inputs(shape, torch.float16, 21, lens=shape[0] > 1)
+    _norm_errors(binding, q, k, v, go * std, a, torch.float16, 3 * UNIT[torch.float16], 2.0 ** -24)
+
+
+@pytest.mark.parametrize("Lq", [100, 300])
+def test_float16_large_upstream_gradients(binding, Lq):
+    """grad_out . v past the type's range, results within it: nothing overflows on the way."""
+    q, k, v, go, a = _inputs((2, Lq, 8, 2, 2, 64), torch.float16, 22)
+    _norm_errors(binding, q * 0.05, k * 0.25, v * 16.0, go * 4000.0, a, torch.float16, 3 * UNIT[torch.float16], 2.0 ** -24)
+
+
+def test_float16_utterances_of_other_sizes(binding):
+    """Each utterance and key head has its own range: one of grad_out 1e4 beside one of 1e-4, zeros beside both."""
+    for Lq in (60, 200):
+        q, k, v, go, a = _inputs((3, Lq, 900, 4, 2, 64), torch.float16, 23)
+        go[0] *= 1e3
+        go[1] *= 1e-4
+        go[2] = 0.0
+        out, lse = binding.tdt_cross_attn_fwd(q, k, v)
+        for x in binding.tdt_cross_attn_bwd(go, q, k, v, out, lse):
+            assert bool((x[2] == 0).all())
+        for b in (0, 1):
+            _norm_errors(binding, *(t[b:b + 1] for t in (q, k, v, go)), a, torch.float16, 3 * UNIT[torch.float16], 2.0 ** -24)
+        want = [binding.tdt_cross_attn_bwd(*(t[b:b + 1] for t in (go, q, k, v, out)), lse[b:b + 1].contiguous())
+                for b in (0, 1)]
+        got = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse)
+        for b in (0, 1):
+            for x, y in zip(got, want[b]):
+                assert (x[b:b + 1].double() - y.double()).norm() <= 2 * UNIT[torch.float16] * y.double().norm() + 1e-7 * y.numel() ** 0.5

@@ -32,10 +32,12 @@
 // of 128 x 128 x 16 takes the 64 clocks of its reads, and S, dP in both kernels are such.  Measured:
 //   16 x 1024 x 4096, 16 heads on 4 of 128, bfloat16   1,307 us (dq 567): 1,050 TFLOP/s on the five products
 //                                                      of the formula, 1,470 on the seven done
-//   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   82 us (dq 40, dk/dv 42)
+//   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   88 us (max |v| 3, dq 39, dk/dv 46)
 //   16 x 121 x 750, 16 heads of 64                     36.5 us by one kernel, 82.5 by two (ragged: 33.7)
 //   4 x 41 x 200, 8 heads of 64                        8.0 us by one kernel, 11.9 by two; latency
 //   1201 x 2000, 8 heads of 64, float32                135 us with the planes
+#include <algorithm>
+
 #include "tdt_attn_common.cuh"
 #include "tdt_tc.cuh"
 
@@ -47,17 +49,35 @@ constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;  // 3 warpgroups x 168 = 2 x 208 + 88
 constexpr int kWorkRegs = 208, kOtherRegs = 88;
 // float16 weights are held as 2^15 p for the product with dO (p <= 1, so below the type's most): what a
-// frame gets from rows that hardly weigh it stays clear of the type's least numbers.  (dS has no such
-// bound, and is held as it is.)
+// frame gets from rows that hardly weigh it stays clear of the type's least numbers.
 template <int DT> constexpr float kShift = DT == kF16 ? 15.0f : 0.0f;
 template <int DT> constexpr float kUnshift = DT == kF16 ? 1.0f / 32768.0f : 1.0f;
 constexpr int kTileBits = 4096;   // row tiles whose windows the dk/dv kernel looks at beforehand
+
+// float16 dS is held as 2^e dS, since dS is as small as dO / frames and as large as dO . v: in 16 bits one falls
+// below the type's normal range and the other goes past it where the gradients themselves are far from either.
+//   |dS_ij| = p_ij |dO_i . v_j - delta_i| <= |dO_i| |v_j| + |delta_i| =: bound,   2^e bound in [2^14, 2^15),
+// with |v_j| <= sqrt(D) max |v| over the utterance's frames of the key head, from a kernel that reads v beforehand
+// (attn_v_most_kernel).  dq: an e for each row, so a row's accuracy is its own.  dk, dv and the one-tile kernel: one
+// for the CTA, from the largest |dO_i| and |delta_i| of the rows of the key head.  2^e goes in with factors that are
+// there anyway and out with `scale`.  Error of dq, 2,000 frames, dO of size 1, 1e-3, 1e-4: 3.0e-4, 5.1e-4, 4.6e-3 of its
+// norm, where rounding the result alone gives 2.1e-4, 4.6e-4, 4.6e-3.  (bfloat16 has float32's range, and float32's
+// planes too.)
+constexpr int kVParts = 32;  // stretches of the frames whose max |v| is noted apart: a lane each
+
+// 0 where there is nothing to bound, or no finite bound
+__device__ __forceinline__ int ds_shift(float bound) {
+  if (!(bound > 0.0f) || !(bound < INFINITY)) return 0;
+  return min(14 - ((int)(__float_as_uint(bound) >> 23) - 127), 64);
+}
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((unsigned)(127 + e) << 23); }
 
 struct BwdPlan {
   int P, packs, tiles;          // heads of a row tile, H / P, row tiles of a pack
   int f_tiles;                  // frame tiles
   int dq_splits, dkv_splits;
   bool one;                     // one row tile a key head and D <= 64: attn_one_tc_kernel
+  int v_parts;                  // float16: stretches of the frames in v_most, else 0
 };
 
 struct BwdArgs {
@@ -66,6 +86,9 @@ struct BwdArgs {
   // 0 for repeated axes
   int out_b, out_h, q_b, q_h, go_b, go_h, k_b, k_h, v_b, v_h, dq_b, dq_h, dk_b, dk_h, dv_b, dv_h;
   float *part;                  // splits > 1: [split][CTA][128][DP], dk's after dv's
+  // float16: [B][Hkv][v_parts] largest |v|, [B][packs][tiles] largest |dO_i| and |delta_i| of a row tile
+  float *v_most;
+  float2 *row_most;
 };
 
 template <int DT, int DP> struct BwdShape {
@@ -98,6 +121,50 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *d
     tma_load_4d(m, dst + c * BwdShape<DT, DP>::CHUNK, bar, c * 64, h, l, b);
 }
 
+// ---- float16: the largest |v| ---------------------------------------------------------
+// A CTA has a stretch of the frames of one (utterance, key head); 8 or 16 lanes a frame.  Bound by memory.
+template <int L> __global__ void __launch_bounds__(256) attn_v_most_kernel(const __grid_constant__ BwdArgs f) {
+  const AttnArgs &a = f.a;
+  __shared__ float red[8];
+  const int part = blockIdx.x % f.p.v_parts, hk = blockIdx.x / f.p.v_parts % a.Hkv;
+  const long long b = blockIdx.x / f.p.v_parts / a.Hkv;
+  const int2 mine = share_of(utt_lens(a, b).nk, part, f.p.v_parts);
+  const int d0 = threadIdx.x % L * 8;
+  const __half *v = static_cast<const __half *>(a.v) + b * a.sv.b + hk * a.sv.h + d0;
+  constexpr int U = 4, F = 256 / L;  // loads in flight, frames at a time
+  __half2 most = __float2half2_rn(0.0f);
+  if (d0 < a.D)  // D is a multiple of 8
+    for (int j0 = mine.x + threadIdx.x / L; j0 < mine.y; j0 += U * F) {
+      uint4 x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        x[u] = j0 + u * F < mine.y ? __ldg(reinterpret_cast<const uint4 *>(v + (j0 + u * F) * a.sv.l))
+                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const __half2 *h = reinterpret_cast<const __half2 *>(&x[u]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) most = __hmax2(most, __habs2(h[k]));
+      }
+    }
+  const float2 m = __half22float2(most);
+  const float top = warp_max(fmaxf(m.x, m.y));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float all = red[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) all = fmaxf(all, red[i]);
+    f.v_most[blockIdx.x] = all;
+  }
+}
+// sqrt(D) max |v|, by a whole warp; after the kernel above.
+__device__ __forceinline__ float v_bound(const BwdArgs &f, long long b, int hk) {
+  const int lane = threadIdx.x & 31;
+  const float m = lane < f.p.v_parts ? f.v_most[(b * f.a.Hkv + hk) * f.p.v_parts + lane] : 0.0f;
+  return warp_max(m) * sqrtf((float)f.a.D);
+}
+
 // ---- dq ---------------------------------------------------------------------------
 struct DqShared {
   Pipe k, v;
@@ -105,7 +172,8 @@ struct DqShared {
   unsigned tmem;
   int gave_up;
   Hull hull;
-  float half[kRows];
+  float half[kRows], norm2[kRows];
+  unsigned most[2];  // float16: bits of the rows' largest |dO|^2 and |delta|
 };
 
 template <int DT, int DP>
@@ -176,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
+    sh.most[0] = sh.most[1] = 0;
     if (some) {
       arrive_expect_tx(&sh.rows_full, 2 * S::TILE);
       load_rows<DT, DP>(&qm, q_tile, &sh.rows_full, h0 * f.q_h, i0, (int)b * f.q_b);
@@ -285,26 +354,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     // delta = dO . O of the row, half of the columns in each group
     const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
-    float delta = 0.0f, lse2 = INFINITY;
+    float delta = 0.0f, lse2 = INFINITY, out_scale = a.scale;
     {
       const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
-      float x = 0.0f;
+      float x = 0.0f, x2 = 0.0f;
       if (real)
         x = dot_rows<DT, DP / 2>(
             static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
-            static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len);
-      if (group == 1) sh.half[r] = x;
+            static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len,
+            DT == kF16 ? &x2 : nullptr);
+      if (group == 1) {
+        sh.half[r] = x;
+        if (DT == kF16) sh.norm2[r] = x2;
+      }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float y = sh.half[r];
+      const float y = sh.half[r], y2 = DT == kF16 ? sh.norm2[r] : 0.0f;
       asm volatile("bar.sync 1, 256;" ::: "memory");
       if (group == 0) {
         delta = x + y;
         sh.half[r] = delta;
         if (row < a.Lq && split == 0) a.delta[stat] = delta;
+        if (DT == kF16) {
+          sh.norm2[r] = x2 + y2;
+          const unsigned m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(x2 + y2)),
+                         m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(delta)));
+          if (lane == 0) {  // the order does not matter to a maximum
+            atomicMax(&sh.most[0], m0);
+            atomicMax(&sh.most[1], m1);
+          }
+        }
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       delta = sh.half[r];
       if (range.y > range.x) lse2 = a.lse[stat] * kLog2e;  // else +inf: every weight is 0
+      if constexpr (DT == kF16) {
+        if (threadIdx.x == 0 && split == 0)
+          f.row_most[cta] = make_float2(sqrtf(__uint_as_float(sh.most[0])), __uint_as_float(sh.most[1]));
+        wait_for_predecessor();  // v's largest
+        const int e = ds_shift(fmaf(sqrtf(sh.norm2[r]), v_bound(f, b, hk), fabsf(delta)));
+        lse2 -= (float)e;  // 2^e p
+        out_scale *= power_of_2(-e);
+      }
     }
     const float c = a.scale * kLog2e;
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
@@ -399,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const float x = S::PLANES == 3 ? acc[k] : __uint_as_float(o[k]);
-        v[k] = bad ? NAN : T > 0 && alive ? x * a.scale : 0.0f;
+        v[k] = bad ? NAN : T > 0 && alive ? x * out_scale : 0.0f;
       }
       if (f.p.dq_splits == 1)
         stage32<DT>(q_tile, S::CHUNK, r, d0, v);  // every product with q is done
@@ -438,6 +528,7 @@ struct DkvShared {
   int gave_up;
   unsigned char active[kTileBits];  // row tiles with a query that sees these frames
   int cut[kStats];                  // whether some row of the tile sees only part of them
+  float ds_in, ds_out;              // float16: 2^(e - 15), 2^-e
   __align__(16) float lse2[kStats][kRows], delta[kStats][kRows];  // of the rows, both negated
   __align__(16) int lo[kStats][kRows], len[kStats][kRows];
 };
@@ -640,6 +731,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (warp == 10) wait_for_predecessor();  // delta is the dq kernel's; and nobody overtakes it
     if (warp == 10 && any) {  // the rows' statistics
+      float ds_in = kUnshift<DT>;
+      if constexpr (DT == kF16) {
+        const int tiles = a.G / P * f.p.tiles;
+        const float2 *most = f.row_most + (b * a.Hkv + hk) * tiles;
+        float g = 0.0f, d = 0.0f;
+        bool finite = true;  // a maximum passes over NaN
+        for (int t = lane; t < tiles; t += 32) {
+          const float2 m = most[t];
+          g = fmaxf(g, m.x);
+          d = fmaxf(d, m.y);
+          finite = finite && m.x + m.y < INFINITY;
+        }
+        const int e = ds_shift(fmaf(warp_max(g), v_bound(f, b, hk), warp_max(d)));
+        ds_in *= __all_sync(0xffffffffu, finite) ? power_of_2(e) : 1.0f;
+        if (lane == 0) {
+          sh.ds_in = ds_in;
+          sh.ds_out = kUnshift<DT> / ds_in;
+        }
+      }
       int s = 0;
       for (int t = start; t < t1; t = next(t + 1), ++s) {
         const int buf = s % kStats, i0 = t % row_tiles * per, h0 = hk * a.G + t / row_tiles * P;
@@ -664,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool sees = w[x].y > w[x].x;  // else every weight is 0
           cut |= sees && (w[x].x > j0 || w[x].y < min(j0 + kRows, n.nk));
           sh.lse2[buf][r] = sees ? kShift<DT> - l2[x] * kLog2e : -INFINITY;
-          sh.delta[buf][r] = sees ? -dl[x] * kUnshift<DT> : 0.0f;
+          sh.delta[buf][r] = sees ? -dl[x] * ds_in : 0.0f;
           sh.lo[buf][r] = w[x].x;
           sh.len[buf][r] = w[x].y - w[x].x;
         }
@@ -712,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(s_col + 32, x[1]);
         tmem_wait_ld();
         const float *lse2 = sh.lse2[buf] + group * 64, *delta = sh.delta[buf] + group * 64;
+        const float ds_in = DT == kF16 ? sh.ds_in : 1.0f;
         const float2 c2 = make_float2(c, c);
 #pragma unroll
         for (int i = 0; i < 64; i += 4) {
@@ -770,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = h * N; i < h * N + N; i += 4) {
             const float4 dl = *reinterpret_cast<const float4 *>(delta + i);
-            const float2 un = make_float2(kUnshift<DT>, kUnshift<DT>);
+            const float2 un = make_float2(ds_in, ds_in);
             const unsigned *p = &x[i >> 5][i & 31], *g = &y[i >> 5][i & 31];
             const float2 d0 = make_float2(dl.x, dl.y), d1 = make_float2(dl.z, dl.w);
             const float2 g0 = pair(g[0], g[1]), g1 = pair(g[2], g[3]);
@@ -824,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         put(i, group * 32, v);
       }
     } else {  // group 0 has dv, group 1 dk
-      const float scale = group ? a.scale : kUnshift<DT>;
+      const float scale = !group ? kUnshift<DT> : DT == kF16 && any ? a.scale * sh.ds_out : a.scale;
 #pragma unroll
       for (int i = 0; i < DP / 32; ++i) {
         unsigned o[32];
@@ -880,7 +991,9 @@ struct OneShared {
   unsigned tmem;
   int gave_up;
   Hull hull;
-  float half[kRows];
+  float half[kRows], norm2[kRows];
+  unsigned most[2];  // float16: bits of the rows' largest |dO|^2 and |delta|
+  float ds_out;      // float16: 2^-e
 };
 
 template <int DT>
@@ -960,6 +1073,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init_cluster();
     sh.gave_up = 0;
+    sh.most[0] = sh.most[1] = 0;
     if (some) {
       unsigned long long *in = cut_rows ? &sh.rows_in : &sh.rows_full;
       arrive_expect_tx(in, 2 * S::TILE);
@@ -1103,7 +1217,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         unsigned o[32];
         tmem_ld32(tmem + lanes + kDv + i * 32, o);
         tmem_wait_ld();
-        const float f_out = i < 2 ? kUnshift<DT> : a.scale;
+        const float f_out = i < 2 ? kUnshift<DT> : DT == kF16 ? a.scale * sh.ds_out : a.scale;
 #pragma unroll
         for (int k = 0; k < 32; k += 2) {
           const float2 v = mul2(pair(o[k], o[k + 1]), make_float2(f_out, f_out));
@@ -1155,9 +1269,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta, lse2 = -INFINITY;  // both negated
+    float ds_in = kUnshift<DT>, out_scale = a.scale;
     {
       // this group's half of the columns, from the tiles of dO and out
-      float x = 0.0f;
+      float x = 0.0f, x2 = 0.0f;
       if (some && wait(&sh.out_full, 0) && wait(rows, 0) && real) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -1166,24 +1281,49 @@ __global__ void __launch_bounds__(kOneThreads, 1)
                       ov = *reinterpret_cast<const uint4 *>(p_tile + at);
           const E *ge = reinterpret_cast<const E *>(&gv), *oe = reinterpret_cast<const E *>(&ov);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x = fmaf(Elem<DT>::to_float(ge[i]), Elem<DT>::to_float(oe[i]), x);
+          for (int i = 0; i < 8; ++i) {
+            const float g = Elem<DT>::to_float(ge[i]);
+            x = fmaf(g, Elem<DT>::to_float(oe[i]), x);
+            if (DT == kF16) x2 = fmaf(g, g, x2);
+          }
         }
       }
       __syncwarp();
       if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
-      if (group == 1) sh.half[r] = x;
+      if (group == 1) {
+        sh.half[r] = x;
+        if (DT == kF16) sh.norm2[r] = x2;
+      }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      const float y = sh.half[r];
+      const float y = sh.half[r], y2 = DT == kF16 ? sh.norm2[r] : 0.0f;
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (group == 0) sh.half[r] = x + y;
+      if (group == 0) {
+        sh.half[r] = x + y;
+        if (DT == kF16) {
+          const unsigned m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(x2 + y2)),
+                         m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(x + y)));
+          if (lane == 0) {  // the order does not matter to a maximum
+            atomicMax(&sh.most[0], m0);
+            atomicMax(&sh.most[1], m1);
+          }
+        }
+      }
       asm volatile("bar.sync 1, 256;" ::: "memory");
-      delta = -sh.half[r] * kUnshift<DT>;
+      if constexpr (DT == kF16) {
+        wait_for_predecessor();  // v's largest
+        const int e = ds_shift(fmaf(sqrtf(__uint_as_float(sh.most[0])), v_bound(f, b, hk),
+                                    __uint_as_float(sh.most[1])));
+        ds_in *= power_of_2(e);
+        out_scale *= power_of_2(-e);
+        if (threadIdx.x == 0) sh.ds_out = power_of_2(-e);  // read after the first tile's products
+      }
+      delta = -sh.half[r] * ds_in;
     }
     const float c = a.scale * kLog2e;
     const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
     const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
     const float2 c2 = make_float2(c, c), l2 = make_float2(lse2, lse2), d2 = make_float2(delta, delta),
-                 un = make_float2(kUnshift<DT>, kUnshift<DT>);
+                 un = make_float2(ds_in, ds_in);
     bool ok = true;
     for (int s = 0; s < T; ++s) {
       ok = wait(&sh.sp_full, s & 1);
@@ -1250,7 +1390,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     // anything, and 0 times that need not be 0.  Its dS then spoils its own dQ, set here, and the dK of those frames, which
     // the storing warps set.
 #pragma unroll
-    for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * a.scale : 0.0f;
+    for (int k = 0; k < 32; ++k) v[k] = bad ? NAN : T > 0 && alive ? __uint_as_float(o[k]) * out_scale : 0.0f;
     if (f.p.dq_splits == 1) {
       stage32<DT>(q_tile, S::TILE, r, group * 32, v);  // every product with q is done
       fence_async_shared();
@@ -1359,6 +1499,12 @@ BwdPlan plan(long long B, long long Lq, long long Lk, int H, int Hkv, int D, int
   p.dq_splits = splits(B * p.packs * p.tiles, p.f_tiles);
   p.one = dtype != kF32 && D <= 64 && p.P == G && p.tiles == 1;
   p.dkv_splits = p.one ? 1 : splits(B * Hkv * p.f_tiles, (long long)(G / p.P) * p.tiles);
+  // v's reader: eight CTAs an SM, 64 frames each at the least
+  p.v_parts = 0;
+  if (dtype == kF16) {
+    const long long parts = B * Hkv > 0 ? std::min<long long>({8 * kSMs / (B * Hkv), (Lk + 63) / 64, kVParts}) : 1;
+    p.v_parts = (int)std::max<long long>(parts, 1);
+  }
   return p;
 }
 
@@ -1368,17 +1514,36 @@ struct Maps {
   TensorMap q, go, k, v, out, dq, dk, dv;
 };
 
+// The first kernel of a call; float16: after the one that reads v.
+template <int DT, typename... P, typename... A>
+cudaError_t launch_after_v_most(void (*kernel)(P...), const BwdArgs &f, unsigned blocks, unsigned threads, size_t smem,
+                                cudaStream_t stream, const A &...args) {
+  if constexpr (DT == kF16) {
+    const unsigned parts = (unsigned)(f.a.B * f.a.Hkv * f.p.v_parts);
+    if (f.a.D <= 64)
+      attn_v_most_kernel<8><<<parts, 256, 0, stream>>>(f);
+    else
+      attn_v_most_kernel<16><<<parts, 256, 0, stream>>>(f);
+    const cudaError_t e = cudaGetLastError();
+    return e != cudaSuccess ? e : launch_follower(kernel, dim3(blocks), threads, smem, stream, args...);
+  } else {
+    kernel<<<blocks, threads, smem, stream>>>(args...);
+    return cudaGetLastError();
+  }
+}
+
 template <int DT> cudaError_t launch_one(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   const cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_one_tc_kernel<DT>),
                                           OneShape::BYTES + 1024, kOneLaunchRegs);
   if (e != cudaSuccess) return e;
   const unsigned ctas = (unsigned)(f.a.B * f.a.Hkv);
-  attn_one_tc_kernel<DT><<<ctas * f.p.dq_splits, kOneThreads, OneShape::BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, m.out.map, m.dq.map, f);
-  if (f.p.dq_splits > 1)
+  const cudaError_t e1 = launch_after_v_most<DT>(attn_one_tc_kernel<DT>, f, ctas * f.p.dq_splits, kOneThreads,
+                                                 OneShape::BYTES + 1024, stream, m.q.map, m.go.map, m.k.map, m.v.map,
+                                                 m.out.map, m.dq.map, f);
+  if (e1 == cudaSuccess && f.p.dq_splits > 1)
     return launch_follower(attn_add_kernel<DT, 64>, dim3(ctas * (kRows / 32) * 2, 1), 256, 0, stream,
                            f, 0);
-  return cudaGetLastError();
+  return e1;
 }
 
 template <int DT, int DP>
@@ -1390,9 +1555,8 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   cudaError_t e = prepare_tc_kernel(reinterpret_cast<const void *>(attn_dq_tc_kernel<DT, DP>),
                                     S::DQ_BYTES + 1024, kLaunchRegs);
   if (e != cudaSuccess) return e;
-  attn_dq_tc_kernel<DT, DP><<<(unsigned)(rows * f.p.dq_splits), kThreads, S::DQ_BYTES + 1024, stream>>>(
-      m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, f);
-  e = cudaGetLastError();
+  e = launch_after_v_most<DT>(attn_dq_tc_kernel<DT, DP>, f, (unsigned)(rows * f.p.dq_splits), kThreads,
+                              S::DQ_BYTES + 1024, stream, m.q.map, m.go.map, m.k.map, m.v.map, m.dq.map, f);
   if (e == cudaSuccess && f.p.dq_splits > 1)
     e = launch_follower(attn_add_kernel<DT, DP>, dim3((unsigned)rows * per_tile, 1), 256, 0, stream, f, 0);
   if (e == cudaSuccess)
@@ -1407,9 +1571,10 @@ cudaError_t launch(const BwdArgs &f, const Maps &m, cudaStream_t stream) {
   return e;
 }
 
-// The workspace: planes of q, dO, k, v (float32), then the partial sums of splits.
+// The workspace: planes of q, dO, k, v (float32), then the partial sums of splits, then the sizes that dS's shift is
+// chosen by (float16).
 struct BwdSpace {
-  size_t q, go, k, v, part, total;
+  size_t q, go, k, v, part, v_most, row_most, total;
 };
 BwdSpace space(const BwdPlan &p, long long B, long long Lq, long long Lk, int H, int Hkv, int D, int dtype) {
   BwdSpace s = {};
@@ -1429,6 +1594,8 @@ BwdSpace space(const BwdPlan &p, long long B, long long Lq, long long Lk, int H,
   const size_t dq = p.dq_splits > 1 ? tile * B * p.packs * p.tiles * p.dq_splits : 0;
   const size_t dkv = p.dkv_splits > 1 ? 2 * tile * B * Hkv * p.f_tiles * p.dkv_splits : 0;
   s.part = take(dq > dkv ? dq : dkv);
+  s.v_most = take((size_t)B * Hkv * p.v_parts * 4);
+  s.row_most = take(dtype == kF16 ? (size_t)B * p.packs * p.tiles * 8 : 0);
   s.total = at;
   return s;
 }
@@ -1460,6 +1627,8 @@ cudaError_t launch_attn_bwd_tc(const AttnArgs &a, int dtype, void *workspace, cu
   const BwdSpace at = space(f.p, a.B, a.Lq, a.Lk, a.H, a.Hkv, a.D, dtype);
   char *ws = static_cast<char *>(workspace);
   f.part = reinterpret_cast<float *>(ws + at.part);
+  f.v_most = reinterpret_cast<float *>(ws + at.v_most);
+  f.row_most = reinterpret_cast<float2 *>(ws + at.row_most);
   Maps m;
   const int per = kRows / f.p.P;
   bool ok = !f.p.one ||

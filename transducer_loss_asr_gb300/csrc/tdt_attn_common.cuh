@@ -88,8 +88,9 @@ template <int WARPS> __device__ __forceinline__ int2 hull_of(const Hull &h) {
 }
 
 // dot of the first `n` of N elements of two rows, n a multiple of a 16-byte load's elements; every load is
-// in flight at once
-template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x, const void *y, int n) {
+// in flight at once.  `xx`, if given: the square of x's norm.
+template <int DT, int N>
+__device__ __forceinline__ float dot_rows(const void *x, const void *y, int n, float *xx = nullptr) {
   typedef typename Elem<DT>::T E;
   constexpr int W = 16 / (int)sizeof(E);
   uint4 xv[N / W], yv[N / W];
@@ -101,13 +102,18 @@ template <int DT, int N> __device__ __forceinline__ float dot_rows(const void *x
       yv[d / W] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const E *>(y) + d));
     }
   }
-  float s = 0.0f;
+  float s = 0.0f, s2 = 0.0f;
 #pragma unroll
   for (int d = 0; d < N / W; ++d) {
     const E *xe = reinterpret_cast<const E *>(&xv[d]), *ye = reinterpret_cast<const E *>(&yv[d]);
 #pragma unroll
-    for (int k = 0; k < W; ++k) s = fmaf(Elem<DT>::to_float(xe[k]), Elem<DT>::to_float(ye[k]), s);
+    for (int k = 0; k < W; ++k) {
+      const float f = Elem<DT>::to_float(xe[k]);
+      s = fmaf(f, Elem<DT>::to_float(ye[k]), s);
+      if (xx) s2 = fmaf(f, f, s2);
+    }
   }
+  if (xx) *xx = s2;
   return s;
 }
 
