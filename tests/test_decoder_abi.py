@@ -207,3 +207,14 @@ def test_cross_attention_op_fake_shapes_and_cpu_rejection(lib):
         autograd.cross_attention(torch.zeros(2, 5, 4, 8), torch.zeros(2, 7, 2, 8), torch.zeros(2, 7, 2, 8))
     with pytest.raises(ValueError):
         lib.tdt_cross_attn_fwd(torch.zeros(2, 5, 4, 8), torch.zeros(2, 7, 2, 8), torch.zeros(2, 7, 2, 8))
+
+
+@pytest.mark.parametrize("workspace", [torch.zeros(1 << 20, dtype=torch.float32), torch.empty(1 << 20, dtype=torch.uint8, device="meta"),
+                                       torch.zeros(1, dtype=torch.uint8).expand(1 << 20), torch.zeros(1 << 20, dtype=torch.uint8)[::2]],
+                         ids=["dtype", "device", "one byte", "strided"])
+def test_binding_refuses_scratch_that_is_not_the_devices_own(lib, workspace):
+    q, k = torch.zeros(2, 5, 4, 8), torch.zeros(2, 7, 2, 8)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.tdt_cross_attn_fwd(q, k, k, workspace=workspace)
+    with pytest.raises(ValueError, match="workspace"):
+        lib.tdt_cross_attn_bwd(q, q, k, k, q, torch.zeros(2, 4, 5), workspace=workspace)

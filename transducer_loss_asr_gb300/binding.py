@@ -316,6 +316,9 @@ def _scratch(sizes, code, dev, backward, workspace):
         if need == 0:
             return None, None, 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+          or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
     return workspace, workspace.data_ptr(), workspace.numel()
 
 
@@ -327,7 +330,8 @@ def tdt_cross_attn_fwd(q, k, v, k_lens=None, q_lens=None, windows=None, scale=No
     k_lens, q_lens: int64 [B] or None (all); windows: int32 [B, Lq, 2], the frames [w0, w1) that
     each query sees, or None; scale: 1 / sqrt(D) unless given.  Few rows (decoding steps, the
     hypotheses of a beam) take the same call.  Any strides with contiguous heads, such as slices
-    of a fused projection.  Returns (out, lse): out like q, lse float32 [B, H, Lq] (None without
+    of a fused projection.  workspace: a contiguous uint8 tensor of
+    tdt_cross_attn_workspace_size bytes at least, allocated unless given.  Returns (out, lse): out like q, lse float32 [B, H, Lq] (None without
     need_lse), which tdt_cross_attn_bwd takes.
     """
     B, Lq, Lk, H, Hkv, D = dims = _attn_sizes(q, k, v, k_lens, q_lens, windows)
