@@ -260,3 +260,19 @@ def test_binding_import_fails_loudly_without_the_library(tmp_path):
                        cwd=tmp_path, capture_output=True, text=True, timeout=300)
     assert r.returncode != 0
     assert "ImportError" in r.stderr and "libtdt_loss.so is not built" in r.stderr
+
+
+def test_binding_refuses_workspaces_that_are_not_the_devices_own(lib):
+    import torch
+
+    z, lens = torch.zeros(2, 5, 3, 13), torch.full((2,), 3)
+    labels = torch.zeros(2, 2, dtype=torch.long)
+    u8 = torch.uint8
+    for ws in (torch.empty(1 << 20, dtype=u8, device="meta"), torch.zeros(1, dtype=u8).expand(1 << 20),
+               torch.zeros(1 << 20, dtype=u8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            lib.tdt_loss_fwd_bwd_ws(z, labels, lens, lens, [0, 1, 2], 6, ws)
+        with pytest.raises(ValueError, match="workspace"):
+            lib.tdt_loss_fwd(z, labels, lens, lens, [0, 1, 2], 6, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            lib.tdt_loss_bwd(z, labels, lens, lens, [0, 1, 2], 6, ws)

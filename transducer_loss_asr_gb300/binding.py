@@ -198,10 +198,16 @@ def tdt_greedy_decode(logits, logit_lens, durations, blank, max_symbols=10):
     return n, tok, frm, dur
 
 
+def _check_workspace(workspace, dev):
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+
+
 def tdt_loss_fwd_bwd_ws(logits, labels, logit_lens, label_lens, durations, blank, workspace,
                         sigma=0.0, reduction="mean_volume", loss_out=None, grad_out=None,
                         compute_grad=True):
     """As tdt_loss_fwd_bwd with a caller-owned uint8 CUDA workspace tensor."""
+    _check_workspace(workspace, logits.device)
     args, loss_out, grad_out = _marshal(logits, labels, logit_lens, label_lens, durations,
                                         blank, sigma, reduction, loss_out, grad_out,
                                         compute_grad)
@@ -453,6 +459,7 @@ def tdt_loss_fwd(logits, labels, logit_lens, label_lens, durations, blank, sigma
                                  reduction, loss_out, None, False)
     if workspace is None:
         workspace = _new_workspace(logits, len(durations))
+    _check_workspace(workspace, logits.device)
     with torch.cuda.device(logits.device):
         _check(lib.tdt_loss_fwd(*args[:-1], _ptr(workspace), workspace.numel(),
                                 _stream_handle(logits.device)))
@@ -469,6 +476,7 @@ def tdt_loss_bwd(logits, labels, logit_lens, label_lens, durations, blank, works
     may be ``logits`` itself (contiguous logits): the gradient then replaces
     them.
     """
+    _check_workspace(workspace, logits.device)
     B = logits.shape[0]
     if grad_loss is not None:
         want = B if reduction == "none" else 1
