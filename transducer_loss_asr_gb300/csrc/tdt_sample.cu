@@ -149,8 +149,7 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
   typedef typename Elem<DT>::T E;
   typedef Key<DT> K;
   static constexpr int VEC = Vec<DT>::N;
-  static constexpr int LIST = kListTokens;
-  static constexpr int CAP = LIST / NW;  // list entries of a warp
+  static constexpr int CAP = kListTokens / NW;  // list entries of a warp
 
   Shared<NW> &s;
   float *own;     // the resident row, from its first vector on
@@ -173,8 +172,8 @@ template <int DT, int NW, bool RESIDENT> struct Sampler {
     v1 = min(v0 + each, vectors);
     own = reinterpret_cast<float *>(mem);
     xs = own + (RESIDENT ? (V + 16 + 3) / 4 * 4 : 0);
-    ids = reinterpret_cast<int *>(xs + LIST);
-    vecs = ids + LIST;
+    ids = reinterpret_cast<int *>(xs + kListTokens);
+    vecs = ids + kListTokens;
   }
 
   // Vector v as float32: tokens outside the row and NaN come as -inf.
@@ -852,7 +851,7 @@ __global__ void __launch_bounds__(NW * 32, NW == 16 && !RESIDENT ? 2 : 1) sample
 template <int DT, int NW, bool RESIDENT>
 cudaError_t launch(const SampleArgs &a, long long N, cudaStream_t s) {
   // a resident row starts at its first vector's place and is filled up to whole vectors
-  constexpr size_t list = 3 * Sampler<DT, NW, RESIDENT>::LIST * 4;
+  constexpr size_t list = 3 * kListTokens * 4;
   auto row = [](int V) { return RESIDENT ? (size_t)((V + 16 + 3) / 4 * 4) * 4 : 0; };
   const size_t smem = row(a.V) + (RESIDENT && a.V <= kOwnList ? 0 : list);
   // The limit is the kernel's, shared by all host threads: the most that any call wants, never this call's own.

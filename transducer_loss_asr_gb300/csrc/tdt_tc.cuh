@@ -105,9 +105,6 @@ __device__ __forceinline__ void tma_store_wait_read() {
 template <int THREADS> __device__ __forceinline__ void named_barrier(int id) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "n"(THREADS) : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap *map) {
-  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
-}
 
 // ---- TMEM ---------------------------------------------------------------------
 template <int COLS> __device__ __forceinline__ void tmem_alloc(unsigned *base) {  // one warp
