@@ -472,3 +472,29 @@ def test_float16_utterances_of_other_sizes(binding):
         for b in (0, 1):
             for x, y in zip(got, want[b]):
                 assert (x[b:b + 1].double() - y.double()).norm() <= 2 * UNIT[torch.float16] * y.double().norm() + 1e-7 * y.numel() ** 0.5
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("shape", [(2, 121, 2500, 2, 2, 64), (2, 300, 1000, 4, 2, 64), (1, 130, 2500, 2, 1, 128),
+                                   (2, 3, 1500, 4, 2, 96), (4, 1, 2000, 4, 4, 64), (1, 40, 1000, 2, 1, 200)], ids=str)
+def test_errors_in_norm(binding, shape, dtype):
+    """Three units of the type (results, P or dS, delta) in 2-norm; float32: exponentials good to 2^-20, four times
+    that.  One average frame of 2,500 that is missing or doubled changes the results by 2 %."""
+    units = 3 * UNIT[dtype] if dtype != torch.float32 else 2.0 ** -18
+    q, k, v, go, a = _inputs(shape, dtype, 24, lens=shape[0] > 1)
+    _norm_errors(binding, q, k, v, go, a, dtype, units, 2.0 ** -24 if dtype == torch.float16 else None)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+def test_given_workspace(binding, dtype):
+    for shape in ((2, 70, 900, 4, 2, 64), (1, 300, 700, 2, 1, 96), (1, 10, 300, 2, 1, 200)):
+        q, k, v, go, a = _inputs(shape, dtype, 25, lens=True)
+        ws = [torch.full((binding.tdt_cross_attn_workspace_size(shape, dtype, back) + 1,), 255, dtype=torch.uint8, device="cuda")
+              for back in (False, True)]
+        out, lse = binding.tdt_cross_attn_fwd(q, k, v, **a)
+        o2, l2 = binding.tdt_cross_attn_fwd(q, k, v, workspace=ws[0], **a)
+        grads = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, **a)
+        g2 = binding.tdt_cross_attn_bwd(go, q, k, v, out, lse, workspace=ws[1], **a)
+        for x, y in zip((out, lse) + grads, (o2, l2) + g2):
+            assert torch.equal(x.nan_to_num(7.0), y.nan_to_num(7.0))
+        assert ws[0][-1] == 255 and ws[1][-1] == 255

@@ -325,3 +325,31 @@ def test_threads_that_sample_rows_of_other_lengths(binding, tmp_path, N, times):
     assert failed == 0
     for (t, l), (t2, l2) in zip(want, got):
         assert torch.equal(t, t2) and torch.equal(l, l2)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,V,std", [(50, 130, 3.0), (30, 2048, 0.3), (20, 8193, 3.0), (4, 131072, 3.0)])
+def test_log_probabilities(binding, dtype, N, V, std):
+    """log-probability of the drawn token among those that stay, in 64 bits from the definition's weights.
+
+    Bound: weights good to 2^-20 and one unit each (the exponential's error may move the last rounding), float32
+    arithmetic on numbers of the size of z and of the logarithm; top-p's cut may fall one token to either side."""
+    g = torch.Generator(device="cuda").manual_seed(V)
+    x = (torch.randn(N, V, generator=g, device="cuda") * std).to(dtype)
+    u = torch.rand(N, generator=g, device="cuda")
+    xs = x.float().cpu().numpy()
+    for k, p, m in FILTERS:
+        for T in (0.7, 1.3):
+            tokens, logp = (t.cpu().numpy() for t in binding.tdt_sample(x, u, T, k, p, m))
+            for i in range(N):
+                order, w, sure, most = _kept(xs[i], T, k, p, m)
+                z = float(np.float32(np.float32(xs[i][tokens[i]] - xs[i].max()) * (LOG2E / np.float32(T))))
+                off = math.inf
+                for n in range(sure, len(order) + 1):
+                    total = int(w[order[:n]].sum())
+                    lg = math.log2(total / 2.0 ** 31)
+                    bound = (2.0 ** -20 + n / total + 2.0 ** -22 * (1 + abs(z) + abs(lg))) * math.log(2.0) * 2
+                    off = min(off, abs(logp[i] - (z - lg) * math.log(2.0)) / bound)
+                    if off <= 1:
+                        break
+                assert off <= 1, (T, k, p, m, i, off)
