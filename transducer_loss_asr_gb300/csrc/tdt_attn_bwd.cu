@@ -13,7 +13,7 @@
 // P = 2^(S c - lse) is formed again from the forward pass's lse.  Seven products where five would
 // do with one walk; over several row tiles that one would add its dQ tiles to memory in float32 in no
 // fixed order.
-// delta = dO . O of each row is formed by the dq kernel and kept for the other.
+// delta = dO . O of each row is formed by the dq kernel and kept for the other (short walks: see kDeltaFrames).
 //
 // Two warpgroups share a tile's elementwise work (thread = TMEM lane, each group half of the
 // columns); a warp loads with TMA, a warp issues products, one zeroes tails, and in the dk/dv kernel one
@@ -23,10 +23,9 @@
 //
 // Few CTAs: the walk is split over several, whose float32 sums a third kernel adds in order.
 //
-// P, dS: rounding them to 16 bits is what the products need.  With delta from the rounded O it is what
-// dq's error consists of (bfloat16: 2.5e-3 of its norm, 1.7e-3 where only the result is rounded; delta's part
-// is 8e-4 at 512 frames and less with more).  A delta from the unrounded O would need it kept from the forward
-// pass in float32, and a dS of two planes two products more.
+// P, dS: rounding them to 16 bits is what the products need.  With delta from the rounded O (long walks only, see
+// kDeltaFrames) it is what dq's error consists of (bfloat16: 2.4e-3 to 2.5e-3 of its norm, 1.7e-3 where only the result is
+// rounded).  A dS of two planes would take two products more.
 //
 // Bound by the tensor cores and the shared memory that feeds them: a product of two shared-memory operands
 // of 128 x 128 x 16 takes the 64 clocks of its reads, and S, dP in both kernels are such.  Measured:
@@ -34,7 +33,7 @@
 //                                                      of the formula, 1,470 on the seven done
 //   8 x 1201 x 2000 ragged, 8 heads on 2 of 96, float16, windows of 300   88 us (max |v| 3, dq 39, dk/dv 46)
 //   16 x 121 x 750, 16 heads of 64                     36.5 us by one kernel, 82.5 by two (ragged: 33.7)
-//   4 x 41 x 200, 8 heads of 64                        8.0 us by one kernel, 11.9 by two; latency
+//   4 x 41 x 200, 8 heads of 64                        9.8 us by one kernel; latency
 //   1201 x 2000, 8 heads of 64, float32                135 us with the planes
 #include <algorithm>
 
@@ -121,6 +120,49 @@ __device__ __forceinline__ void load_rows(const CUtensorMap *m, unsigned char *d
     tma_load_4d(m, dst + c * BwdShape<DT, DP>::CHUNK, bar, c * 64, h, l, b);
 }
 
+// 16-bit types: delta is dO . O of the rounded O where rows see more frames than this (or a walk is split), and sum_j p_ij
+// dP_ij, from a walk of its own over the same frames, where none of a CTA's rows does.  Error of dq over that of rounding
+// the result alone, 41 and 150 rows: at 20 frames 1.6 from the rounded O and 1.4 from the sum, at 60 1.55 and 1.44, at 200
+// 1.52 and 1.44, at 1,000 1.5 from the rounded O.  Time of the backward pass: 4 x 41 x 200, 8 heads of 64, 8.2 and 9.8 us;
+// 16 x 1024 x 250, 16 heads on 4 of 128, 218 and 230; 8 x 1201 x 2000, 8 heads on 2 of 96, windows of 200, 77 and 83.
+constexpr int kDeltaFrames = 256;
+
+// The most frames that a row sees, as Hull does.
+__device__ __forceinline__ void seen_note(int *seen, int warp, int2 range) {
+  const int most = __reduce_max_sync(0xffffffffu, range.y - range.x);
+  if ((threadIdx.x & 31) == 0) seen[warp] = most;
+}
+template <int WARPS> __device__ __forceinline__ int seen_of(const int *seen) {
+  int most = seen[0];
+#pragma unroll
+  for (int i = 1; i < WARPS; ++i) most = max(most, seen[i]);
+  return most;
+}
+// sum += p dP over the 64 frames from j0, of a row that sees those of `range`; neg: of p, -lse in base 2.  What a row that
+// sees nothing gets may be anything.
+__device__ __forceinline__ float2 sum_p_dp(unsigned (&x)[2][32], unsigned (&y)[2][32], int2 range, int j0, float c,
+                                           float neg, float2 sum) {
+  const bool alive = range.y > range.x;
+  if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
+    const int lo = range.x - j0;
+    const unsigned len = (unsigned)(range.y - range.x);
+#pragma unroll
+    for (int i = 0; i < 64; ++i)
+      if ((unsigned)(i - lo) >= len) {
+        x[i >> 5][i & 31] = 0xff800000u;
+        y[i >> 5][i & 31] = 0;
+      }
+  }
+  const float2 c2 = make_float2(c, c), n2 = make_float2(neg, neg);
+#pragma unroll
+  for (int i = 0; i < 64; i += 2) {
+    const unsigned *xs = &x[i >> 5][i & 31], *ys = &y[i >> 5][i & 31];
+    const float2 z = fma2(pair(xs[0], xs[1]), c2, n2);
+    sum = fma2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), pair(ys[0], ys[1]), sum);
+  }
+  return sum;
+}
+
 // ---- float16: the largest |v| ---------------------------------------------------------
 // A CTA has a stretch of the frames of one (utterance, key head); 8 or 16 lanes a frame.  Bound by memory.
 template <int L> __global__ void __launch_bounds__(256) attn_v_most_kernel(const __grid_constant__ BwdArgs f) {
@@ -172,6 +214,7 @@ struct DqShared {
   unsigned tmem;
   int gave_up;
   Hull hull;
+  int seen[8];
   float half[kRows], norm2[kRows];
   unsigned most[2];  // float16: bits of the rows' largest |dO|^2 and |delta|
 };
@@ -203,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool some = i0 < n.nq && n.nk > 0;  // else no row sees a frame
   // frames [hull.x, hull.y) in tiles of 128 from hull.x; this CTA takes T tiles from `begin`
   int begin = 0, T = 0;
+  int pre = 0, N = 0;  // steps that form delta (kDeltaFrames) before those that form dq: the same tiles; all steps
   // Frames past the utterance's end may hold anything, and 0 times NaN is NaN.  In the last tile of
   // k a warp of its own zeroes them (unless TMA did, past the tensor's end): the load then arrives
   // at tail_full, and that warp hands the tile on.
@@ -213,11 +257,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     T = steps.y - steps.x;
     cut = S::PLANES == 1 && T > 0 && n.nk < a.Lk && begin + T * kRows > n.nk;  // planes end in zeros
   };
-  if (!a.windows && some) walk(make_int2(0, n.nk));
-  auto frame = [&](int s) { return begin + s * kRows; };
+  auto count = [&](int seen) {  // `seen`: frames that a row sees at the most
+    pre = S::PLANES == 1 && f.p.dq_splits == 1 && seen <= kDeltaFrames ? T : 0;
+    N = pre + T;
+  };
+  if (!a.windows && some) {
+    walk(make_int2(0, n.nk));
+    count(n.nk);
+  }
+  auto frame = [&](int s) { return begin + (s < pre ? s : s - pre) * kRows; };
   auto load_k = [&](int s) {
     const int slot = s % S::KS;
-    unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
+    unsigned long long *bar = cut && s == N - 1 ? &sh.tail_full : &sh.k.full[slot];
     arrive_expect_tx(bar, S::TILE);
     load_rows<DT, DP>(&km, k_slots + slot * S::TILE, bar, hk * f.k_h, frame(s), (int)b * f.k_b);
   };
@@ -231,7 +282,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int2 range = make_int2(0, 0);
   if (warp < 8) {
     range = row_range(a, b, row, n);
-    if (a.windows) hull_note(sh.hull, warp, range);
+    if (a.windows) {
+      hull_note(sh.hull, warp, range);
+      seen_note(sh.seen, warp, range);
+    }
   } else if (warp == 8 && lane == 0) {
     pipe_init(sh.k, S::KS);
     pipe_init(sh.v, S::VS);
@@ -262,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  if (a.windows) walk(hull_of<8>(sh.hull));
+  if (a.windows) {
+    walk(hull_of<8>(sh.hull));
+    count(seen_of<8>(sh.seen));
+  }
   constexpr unsigned kDp = 2 * kRows, kAcc = 3 * kRows;  // TMEM columns: S twice, dP, dQ,
   constexpr unsigned kThird = kAcc + 64;                 // the third plane of dS (float32)
 
@@ -272,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 8 && lane == 0 && T > 0) {
       bool ok = true;
       int s = 0;
-      for (; ok && s < T; ++s) {
+      for (; ok && s < N; ++s) {
         if (s == 0 && !a.windows) continue;  // loaded above
         for (int x = 0; ok && x < 2; ++x)  // in the order of the products
           if ((x == 0) == (S::KS > 1)) {
@@ -292,9 +349,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (warp == 10 && cut) {
-      const int slot = (T - 1) % S::KS;
+      const int slot = (N - 1) % S::KS;
       if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
-        zero_tail(k_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame(T - 1), kRows);
+        zero_tail(k_slots + slot * S::TILE, S::CHUNKS, S::CHUNK, n.nk - frame(N - 1), kRows);
       if (lane == 0) mbar_arrive(&sh.k.full[slot]);
     }
     if (warp == 9 && T > 0 && elect_one()) {
@@ -320,26 +377,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       scores(0);
       grads(0);
       if (ok) mma_commit(&sh.scores);
-      for (int s = 0; ok && s < T; ++s) {
-        if (s + 1 < T) {
+      for (int s = 0; ok && s < N; ++s) {
+        const int slot = s % S::KS;
+        if (s + 1 < N) {
           if (S::KS > 1) scores(s + 1);
           ok = ok && wait(&sh.dp_free, s & 1);
           grads(s + 1);
           if (S::KS > 1 && ok) mma_commit(&sh.scores);
         }
-        ok = ok && wait(&sh.ds_ready, s & 1);
+        if (s < pre) {
+          if (ok) mma_commit(&sh.k.empty[slot]);
+          continue;
+        }
+        ok = ok && wait(&sh.ds_ready, (s - pre) & 1);
         tc_fence_after();
         if (!ok) break;
-        const int slot = s % S::KS;
         const unsigned ds = tmem + (s & 1) * kRows, at = ka + slot * S::TILE;
 #pragma unroll
         for (int g = 0; g < 2; ++g)  // the columns of each group
           mma_across_planes<DT, 64>(tmem + kAcc, ds + g * 64, ds + g * 64 + 32, tmem + kThird + g * 32,
                                     at + g * 64 * 128, S::CHUNK, S::PLANE, i_o,
-                                    (S::PLANES == 1 && s > 0) || g > 0);
+                                    (S::PLANES == 1 && s > pre) || g > 0);
         mma_commit(&sh.k.empty[slot]);
-        if (s + 1 == T) mma_commit(&sh.done);
-        if (S::KS == 1 && s + 1 < T) {  // k's slot is free after these products only
+        if (s + 1 == N) mma_commit(&sh.done);
+        if (S::KS == 1 && s + 1 < N) {  // k's slot is free after these products only
           scores(s + 1);
           if (ok) mma_commit(&sh.scores);
         }
@@ -351,10 +412,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     warpgroup_take_registers<kWorkRegs>();
-    // delta = dO . O of the row, half of the columns in each group
+    // delta = dO . O of the row, half of the columns in each group; or sum p dP, half of the frames
     const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
     float delta = 0.0f, lse2 = INFINITY, out_scale = a.scale;
+    if (alive) lse2 = a.lse[stat] * kLog2e;  // else +inf: every weight is 0
+    const float c = a.scale * kLog2e;
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    bool ok = true;
     {
       const int d0 = group * (DP / 2), len = min(DP / 2, a.D - d0);
       float x = 0.0f, x2 = 0.0f;
@@ -363,6 +428,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             static_cast<const E *>(a.go) + b * a.sgo.b + row * a.sgo.l + head * a.sgo.h + d0,
             static_cast<const E *>(a.out) + b * a.so.b + row * a.so.l + head * a.so.h + d0, len,
             DT == kF16 ? &x2 : nullptr);
+      if constexpr (S::PLANES == 1)
+        if (pre > 0) {
+          float2 sum = make_float2(0.0f, 0.0f);
+          for (int s = 0; s < pre; ++s) {
+            ok = wait(&sh.scores, s & 1);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            unsigned x[2][32], y[2][32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              tmem_ld32(tmem + lanes + (s & 1) * kRows + group * 64 + i * 32, x[i]);
+              tmem_ld32(tmem + lanes + kDp + group * 64 + i * 32, y[i]);
+            }
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(&sh.dp_free);
+            sum = sum_p_dp(x, y, range, frame(s) + group * 64, c, -lse2, sum);
+          }
+          __syncwarp();
+          x = alive ? sum.x + sum.y : 0.0f;
+        }
       if (group == 1) {
         sh.half[r] = x;
         if (DT == kF16) sh.norm2[r] = x2;
@@ -386,7 +472,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
       delta = sh.half[r];
-      if (range.y > range.x) lse2 = a.lse[stat] * kLog2e;  // else +inf: every weight is 0
       if constexpr (DT == kF16) {
         if (threadIdx.x == 0 && split == 0)
           f.row_most[cta] = make_float2(sqrtf(__uint_as_float(sh.most[0])), __uint_as_float(sh.most[1]));
@@ -396,8 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         out_scale *= power_of_2(-e);
       }
     }
-    const float c = a.scale * kLog2e;
-    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
     // float32: this thread's 32 columns of dQ, to which each tile's part is added
     float acc[32];
 #pragma unroll
@@ -411,9 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < 32; ++k) acc[k] += __uint_as_float(o[k]);
       }
     };
-    bool ok = true;
-    for (int s = 0; s < T; ++s) {
-      ok = wait(&sh.scores, s & 1);
+    for (int s = pre; s < N; ++s) {
+      ok = ok && wait(&sh.scores, s & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       if (s > 0) add_tile();  // dQ of the tile before was issued before these scores
@@ -991,6 +1073,7 @@ struct OneShared {
   unsigned tmem;
   int gave_up;
   Hull hull;
+  int seen[8];
   float half[kRows], norm2[kRows];
   unsigned most[2];  // float16: bits of the rows' largest |dO|^2 and |delta|
   float ds_out;      // float16: 2^-e
@@ -1029,6 +1112,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   const int2 mine = share_of(f.p.f_tiles, split, f.p.dq_splits);
   const int t0 = mine.x, t1 = mine.y;
   int ta = t1, tb = t1, T = 0;
+  int pre = 0, N = 0;  // steps that form delta (kDeltaFrames) before those that form the gradients: the same tiles; all steps
   bool cut = false;
   auto walk = [&](int2 hull) {
     ta = hull.y > hull.x ? max(t0, hull.x / kRows) : t1;
@@ -1036,11 +1120,18 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     T = max(0, tb - ta);
     cut = T > 0 && n.nk < a.Lk && (ta + T) * kRows > n.nk;
   };
-  if (!a.windows && some) walk(make_int2(0, n.nk));
-  auto frame = [&](int s) { return (ta + s) * kRows; };
+  auto count = [&](int seen) {  // `seen`: frames that a row sees at the most
+    pre = f.p.dq_splits == 1 && seen <= kDeltaFrames ? T : 0;
+    N = pre + T;
+  };
+  if (!a.windows && some) {
+    walk(make_int2(0, n.nk));
+    count(n.nk);
+  }
+  auto frame = [&](int s) { return (ta + (s < pre ? s : s - pre)) * kRows; };
   auto load_k = [&](int s) {
     const int slot = s % S::KS;
-    unsigned long long *bar = cut && s == T - 1 ? &sh.tail_full : &sh.k.full[slot];
+    unsigned long long *bar = cut && s == N - 1 ? &sh.tail_full : &sh.k.full[slot];
     arrive_expect_tx(bar, S::TILE);
     tma_load_4d(&km, k_slots + slot * S::TILE, bar, 0, hk * f.k_h, frame(s), (int)b * f.k_b);
   };
@@ -1051,7 +1142,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   };
   if (group < 2) {
     range = row_range(a, b, row, n);
-    if (a.windows) hull_note(sh.hull, warp, range);
+    if (a.windows) {
+      hull_note(sh.hull, warp, range);
+      seen_note(sh.seen, warp, range);
+    }
   } else if (warp == 12 && lane == 0) {
     pipe_init(sh.k, S::KS);
     pipe_init(sh.v, S::VS);
@@ -1094,7 +1188,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
   tc_fence_after();
   const unsigned tmem = __shfl_sync(0xffffffffu, sh.tmem, 0);
   const Waiter wait{&sh.gave_up};
-  if (a.windows) walk(hull_of<8>(sh.hull));
+  if (a.windows) {
+    walk(hull_of<8>(sh.hull));
+    count(seen_of<8>(sh.seen));
+  }
   constexpr unsigned kDp = kRows, kDv = 2 * kRows, kDk = kDv + DP, kAcc = kDk + DP;
   unsigned long long *rows = cut_rows ? &sh.rows_in : &sh.rows_full;
   if (group == 3) {
@@ -1103,7 +1200,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     if (warp == 12 && lane == 0 && T > 0) {
       bool ok = true;
       int s = 0;
-      for (; ok && s < T; ++s) {
+      for (; ok && s < N; ++s) {
         if (s == 0 && !a.windows) continue;  // loaded above
         ok = wait(&sh.k.empty[s % S::KS], ((unsigned)(s / S::KS) & 1) ^ 1);
         if (!ok) break;
@@ -1132,9 +1229,9 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         if (lane == 0) mbar_arrive(&sh.rows_full);
       }
       if (cut) {
-        const int slot = (T - 1) % S::KS;
+        const int slot = (N - 1) % S::KS;
         if (__all_sync(0xffffffffu, wait(&sh.tail_full, 0)))
-          zero_tail(k_slots + slot * S::TILE, 1, S::TILE, n.nk - frame(T - 1), kRows);
+          zero_tail(k_slots + slot * S::TILE, 1, S::TILE, n.nk - frame(N - 1), kRows);
         if (lane == 0) mbar_arrive(&sh.k.full[slot]);
       }
     }
@@ -1156,12 +1253,16 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         mma_commit(&sh.v.empty[vs]);
       };
       scores(0);
-      for (int s = 0; ok && s < T; ++s) {
-        const int slot = s % S::KS;
+      for (int x = 0; ok && x < N; ++x) {
+        const int slot = x % S::KS, s = x - pre;
         const unsigned da = smem_u32(ds_tiles) + (s & 1) * S::PDS;
-        if (s + 1 < T) {
-          ok = wait(&sh.sp_free, s & 1);
-          scores(s + 1);
+        if (x + 1 < N) {
+          ok = wait(&sh.sp_free, x & 1);
+          scores(x + 1);
+        }
+        if (s < 0) {
+          if (ok) mma_commit(&sh.k.empty[slot]);
+          continue;
         }
         ok = ok && wait(&sh.pds_ready, s & 1);
         ok = ok && wait(&sh.dkv_free, (s & 1) ^ 1);
@@ -1268,10 +1369,14 @@ __global__ void __launch_bounds__(kOneThreads, 1)
     warpgroup_take_registers<kOneWorkRegs>();
     const bool real = row < n.nq, alive = range.y > range.x;
     const long long stat = (b * a.H + head) * a.Lq + row;
+    const float c = a.scale * kLog2e;
+    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
+    const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
+    bool ok = true;
     float delta, lse2 = -INFINITY;  // both negated
     float ds_in = kUnshift<DT>, out_scale = a.scale;
     {
-      // this group's half of the columns, from the tiles of dO and out
+      // dO . O: this group's half of the columns, from the tiles of dO and out; or sum p dP, half of the frames
       float x = 0.0f, x2 = 0.0f;
       if (some && wait(&sh.out_full, 0) && wait(rows, 0) && real) {
 #pragma unroll
@@ -1289,7 +1394,26 @@ __global__ void __launch_bounds__(kOneThreads, 1)
         }
       }
       __syncwarp();
-      if (range.y > range.x) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
+      if (alive) lse2 = kShift<DT> - a.lse[stat] * kLog2e;
+      if (pre > 0) {
+        float2 sum = make_float2(0.0f, 0.0f);
+        for (int s = 0; s < pre; ++s) {
+          ok = wait(&sh.sp_full, s & 1);
+          if (!__all_sync(0xffffffffu, ok)) break;
+          tc_fence_after();
+          unsigned x[2][32], y[2][32];
+          tmem_ld32(s_col, x[0]);
+          tmem_ld32(s_col + 32, x[1]);
+          tmem_ld32(d_col, y[0]);
+          tmem_ld32(d_col + 32, y[1]);
+          tmem_wait_ld();
+          tc_fence_before();
+          mbar_arrive(&sh.sp_free);
+          sum = sum_p_dp(x, y, range, frame(s) + group * 64, c, lse2 - kShift<DT>, sum);
+        }
+        __syncwarp();
+        x = alive ? sum.x + sum.y : 0.0f;
+      }
       if (group == 1) {
         sh.half[r] = x;
         if (DT == kF16) sh.norm2[r] = x2;
@@ -1319,14 +1443,10 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       }
       delta = -sh.half[r] * ds_in;
     }
-    const float c = a.scale * kLog2e;
-    const unsigned lanes = (unsigned)((warp & 3) * 32) << 16;
-    const unsigned s_col = tmem + lanes + group * 64, d_col = s_col + kDp;
     const float2 c2 = make_float2(c, c), l2 = make_float2(lse2, lse2), d2 = make_float2(delta, delta),
                  un = make_float2(ds_in, ds_in);
-    bool ok = true;
     for (int s = 0; s < T; ++s) {
-      ok = wait(&sh.sp_full, s & 1);
+      ok = ok && wait(&sh.sp_full, (pre + s) & 1);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       unsigned x[2][32], y[2][32];
@@ -1337,7 +1457,7 @@ __global__ void __launch_bounds__(kOneThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       mbar_arrive(&sh.sp_free);
-      const int j0 = frame(s) + group * 64;
+      const int j0 = frame(pre + s) + group * 64;
       if (__any_sync(0xffffffffu, alive && (range.x > j0 || range.y < j0 + 64))) {
         // frames that the row does not see: s = -inf weighs 0, and dP may be anything
         const int lo = range.x - j0;
