@@ -56,8 +56,8 @@ extern "C" {
  *            (all Lq), e.g. label_lens + 1.  Frames at or past k_lens[b] and
  *            queries at or past q_lens[b] may hold anything, NaN included;
  *            frames before k_lens[b] that a query's window leaves out, and
- *            queries before q_lens[b] whose window is empty, are to be finite
- *            (their weight is 0, and is multiplied).  A length outside [0, Lk] or [0, Lq] gives that
+ *            queries before q_lens[b] whose window is empty, are to be finite,
+ *            and so their products (their weight is 0, and is multiplied).  A length outside [0, Lk] or [0, Lq] gives that
  *            utterance NaN outputs and zero gradients.
  *   windows  device int32 [B, Lq, 2] contiguous or NULL, e.g. around the
  *            frames that tdt_greedy_decode emits tokens at.

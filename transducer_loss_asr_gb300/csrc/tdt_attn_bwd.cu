@@ -2,7 +2,7 @@
 // float16 and bfloat16 heads of up to 128 elements and float32 heads of up to 64 (three bfloat16 planes a
 // tensor, six products for one, each tile's sums added to float32 registers; as in the forward pass).
 //
-// Every sum has one owner and a fixed order (no atomics).  Where the rows of a key head fill at most one
+// Every sum has one owner and a fixed order (no atomic sums).  Where the rows of a key head fill at most one
 // tile of 128 and heads are at most 64 wide (label states of one utterance), one kernel walks the frames
 // and forms all three gradients with five products a tile; P and dS go through shared memory, since
 // they are contracted along both axes.  Otherwise two kernels:
@@ -11,8 +11,8 @@
 //   dk/dv a CTA holds 128 frames and walks the rows of the heads of its group, with the scores
 //         transposed:  S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q    4 products a tile
 // P = 2^(S c - lse) is formed again from the forward pass's lse.  Seven products where five would
-// do with one walk; over several row tiles that one would add its dQ tiles to memory in float32 in no
-// fixed order.
+// do with one walk; over several row tiles that one would add its dQ tiles to memory in float32, each
+// frame tile in its turn for a fixed order.  Which is faster was not measured.
 // delta = dO . O of each row is formed by the dq kernel and kept for the other (short walks: see kDeltaFrames).
 //
 // Two warpgroups share a tile's elementwise work (thread = TMEM lane, each group half of the
@@ -35,6 +35,7 @@
 //   16 x 121 x 750, 16 heads of 64                     36.5 us by one kernel, 82.5 by two (ragged: 33.7)
 //   4 x 41 x 200, 8 heads of 64                        9.8 us by one kernel; latency
 //   1201 x 2000, 8 heads of 64, float32                135 us with the planes
+// The float32 walks spill: 504 bytes of stores a thread in dq, 244 in dk/dv (scores, dP and sums of a row at once).
 #include <algorithm>
 
 #include "tdt_attn_common.cuh"

@@ -21,7 +21,8 @@
 // float32: q, k and v are split beforehand into three bfloat16 planes (8 + 8 + 8 bits), P in the threads,
 // and six products of planes stand for one; what they leave out is below 2^-24 of a term.  TMEM sums
 // are cut, not rounded, so each tile's sum is added to float32 registers (error 8e-7 of the output's norm,
-// 1.2e-5 when the sum stayed in TMEM).
+// 1.2e-5 when the sum stayed in TMEM).  Row of sums and scores together spill 660 bytes a thread where a CTA has two row
+// tiles.
 //
 // Few row tiles: the frames are split over several CTAs, whose results (O, and the logarithm of
 // the sum) a second kernel joins in a fixed order.

@@ -19,8 +19,9 @@
 // share of all, or min_p is above any unlisted weight -- and then selection and draw read the list only.
 // Otherwise they read the row again (from L2, where it does not stay).
 // Bound: few rows by the latency of the phases (1 x 8,193: 10 us); 656 x 8,193 float32 with each row's own
-// settings by the selection's instructions, 70 us for 21 MB; 2,048 x 131,072 bfloat16 by pass 2's
-// instructions and the second read, 241 to 319 us for 537 MB, by card.
+// settings by the latency and barriers of the selection, at two CTAs an SM (96 registers of 256 threads, 86 KB), 70 us
+// for 21 MB; 2,048 x 131,072 bfloat16 by pass 2's instructions (71 % of the issue slots over the kernel; its read comes
+// from L2), 241 to 321 us for 537 MB, by card.
 // Wide rows are bound by pass 2's instructions.  Its weights are below 2^-9 of the largest, apart from the
 // listed ones, and adding 1.5 * 2^-8 to such a weight leaves rint(2^31 w) in the low bits of the sum: no
 // conversion, and whole-number sums of those bits; what the listed tokens contribute is taken out when
