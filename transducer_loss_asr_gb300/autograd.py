@@ -1,4 +1,4 @@
-"""PyTorch autograd and torch.compile support for the TDT loss and for cross attention.
+"""PyTorch autograd and torch.compile support for the TDT loss, cross attention and token log-probabilities.
 
 The loss is registered as two custom ops over the split C ABI
 (``tdt_loss_fwd`` / ``tdt_loss_bwd`` in include/tdt_loss.h):
@@ -215,3 +215,86 @@ class CrossAttention(torch.nn.Module):
 
     def forward(self, q, k, v, k_lens=None, q_lens=None, windows=None, scale=None):
         return cross_attention(q, k, v, k_lens, q_lens, windows, scale)
+
+
+# ---- log-probabilities of given tokens ------------------------------------------------------------
+
+
+@torch.library.custom_op("tdt_gb300::token_logprobs_forward", mutates_args=(), device_types="cuda")
+def token_logprobs_forward(logits: Tensor, tokens: Tensor,
+                           n_top: int) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    from . import binding
+
+    r = binding.tdt_token_logprobs_fwd(logits, tokens, n_top)
+    if n_top:
+        return tuple(r)
+    N = logits.shape[0]
+    return (*r[:3], logits.new_empty((N, 0), dtype=torch.int32),
+            logits.new_empty((N, 0), dtype=torch.float32))
+
+
+@token_logprobs_forward.register_fake
+def _token_logprobs_forward_fake(logits, tokens, n_top):
+    N, f = logits.shape[0], torch.float32
+    return (logits.new_empty((N,), dtype=f), logits.new_empty((N,), dtype=f),
+            logits.new_empty((N, 2), dtype=f), logits.new_empty((N, n_top), dtype=torch.int32),
+            logits.new_empty((N, n_top), dtype=f))
+
+
+@torch.library.custom_op("tdt_gb300::token_logprobs_backward", mutates_args=(), device_types="cuda")
+def token_logprobs_backward(grad_logprobs: Optional[Tensor], grad_entropy: Optional[Tensor],
+                            grad_top: Optional[Tensor], logits: Tensor, tokens: Tensor, entropy: Tensor,
+                            stats: Tensor, top_tokens: Tensor) -> Tensor:
+    from . import binding
+
+    a, b, c = (None if g is None else g.contiguous() for g in (grad_logprobs, grad_entropy, grad_top))
+    r = binding.TokenLogprobs(entropy, entropy, stats, top_tokens)
+    return binding.tdt_token_logprobs_bwd(logits, tokens, r, a, b, c)
+
+
+@token_logprobs_backward.register_fake
+def _token_logprobs_backward_fake(grad_logprobs, grad_entropy, grad_top, logits, tokens, entropy, stats,
+                                  top_tokens):
+    return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+
+
+def _token_logprobs_setup(ctx, inputs, output):
+    logits, tokens, n_top = inputs
+    _, entropy, stats, top_tokens, _ = output
+    ctx.save_for_backward(logits, tokens, entropy, stats, top_tokens)
+    ctx.n_top = n_top
+    ctx.mark_non_differentiable(stats, top_tokens)
+    ctx.set_materialize_grads(False)
+
+
+def _token_logprobs_backward(ctx, grad_logprobs, grad_entropy, grad_stats, grad_tokens, grad_top):
+    if grad_logprobs is None and grad_entropy is None and grad_top is None:
+        return None, None, None
+    grad = token_logprobs_backward(grad_logprobs, grad_entropy, grad_top if ctx.n_top else None,
+                                   *ctx.saved_tensors)
+    return grad, None, None
+
+
+token_logprobs_forward.register_autograd(_token_logprobs_backward, setup_context=_token_logprobs_setup)
+
+
+def token_logprobs(logits: Tensor, tokens: Tensor,
+                   n_top: int = 0) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    """(logprobs, entropy, top_tokens, top_logprobs) of ``tokens`` [...] under ``logits`` [..., V] (CUDA;
+    float32/float16/bfloat16; may be a slice ``base[..., :V]``): the log-probability of each token, the
+    entropy of its row, and the n_top most probable tokens ([..., n_top], int32) with theirs.
+    Differentiable w.r.t. logits through logprobs, entropy and top_logprobs.
+
+    tokens: int64; a negative one is padding (-100): its row takes no part, and its results are 0
+    (alternatives -1 and -inf).  -sum(logprobs) is the cross entropy of the labels.
+    """
+    V, shape = logits.shape[-1], tokens.shape
+    lp, entropy, _, top, top_lp = token_logprobs_forward(logits.reshape(-1, V), tokens.reshape(-1), int(n_top))
+    return lp.view(shape), entropy.view(shape), top.view(*shape, n_top), top_lp.view(*shape, n_top)
+
+
+class TokenLogprobs(torch.nn.Module):
+    """Stateless module form of :func:`token_logprobs` (same arguments)."""
+
+    def forward(self, logits, tokens, n_top=0):
+        return token_logprobs(logits, tokens, n_top)

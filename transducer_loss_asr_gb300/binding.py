@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import os
 import struct
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -81,6 +82,22 @@ def _load() -> ctypes.CDLL:
     lib.tdt_sample.restype = I
     lib.tdt_sample.argtypes = [P, P, ctypes.c_int64, I, P, P, P, P, P, ctypes.c_double,
                                ctypes.c_int64, ctypes.c_double, ctypes.c_double, P, P, P]
+    I64 = ctypes.c_int64
+    lib.tdt_cache_write.restype = I
+    lib.tdt_cache_write.argtypes = [P, P, P, P, I, P, P, I64, P, P, P]
+    lib.tdt_cache_read.restype = I
+    lib.tdt_cache_read.argtypes = [P, P, I64, P, P, P, P, I, P, P, P]
+    lib.tdt_paged_attn_workspace_size.restype = ctypes.c_size_t
+    lib.tdt_paged_attn_workspace_size.argtypes = [P, I, P]
+    lib.tdt_paged_attn.restype = I
+    lib.tdt_paged_attn.argtypes = [P, P, P, I, P, P, I64, P, P, ctypes.c_double, P, P, P,
+                                   ctypes.c_size_t, P]
+    lib.tdt_token_logprobs_fwd.restype = I
+    lib.tdt_token_logprobs_fwd.argtypes = [P, P, I64, I, P, P, P, P, P, P, P]
+    lib.tdt_token_logprobs_bwd.restype = I
+    lib.tdt_token_logprobs_bwd.argtypes = [P, P, P, I, P, P, P, P, P, P, P, P, P]
+    lib.tdt_token_logprobs_fwd_bwd.restype = I
+    lib.tdt_token_logprobs_fwd_bwd.argtypes = [P, P, P, I, P, P, P, P, P, P, P, P, P, P]
     return lib
 
 
@@ -246,7 +263,8 @@ _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice
     torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
-_pack2, _pack6, _pack12, _pack24 = (struct.Struct("=%dq" % n).pack for n in (2, 6, 12, 24))
+_pack2, _pack3, _pack4, _pack6, _pack12, _pack24 = (
+    struct.Struct("=%dq" % n).pack for n in (2, 3, 4, 6, 12, 24))
 
 
 def _on(device):
@@ -441,6 +459,309 @@ def tdt_sample(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0,
             1.0 if p is None else p, 0.0 if m is None else m, tokens.data_ptr(),
             logprobs.data_ptr(), _raw_stream(dev.index)))
     return tokens, logprobs
+
+
+# ---- the paged cache of label states --------------------------------------------------------------
+E4M3 = torch.float8_e4m3fn
+_CACHE_DTYPES = {**DTYPES, E4M3: 3}
+_pack_cache = struct.Struct("=4Q4q12qi4x").pack  # tdt_paged_cache
+
+
+class PagedCache:
+    """Keys and values of label states in pages (include/tdt_decoder.h, tdt_paged_cache).
+
+    k, v: [n_pages, page_size, heads, head_dim] of float32, float16, bfloat16 or float8_e4m3fn, any
+    strides with contiguous rows (slices of one tensor, heads before places); page_size a power of
+    two.  k_scales, v_scales: uint8 [n_pages, page_size, heads], with float8_e4m3fn only: a row
+    stands for e4m3 * 2^(byte - 127).  ``PagedCache.empty`` allocates them.  Which pages an utterance
+    has says its row of the page table that the calls take.
+    """
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "device", "page_size", "heads",
+                 "head_dim", "_packed")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None):
+        shape, dtype, dev = k.shape, k.dtype, k.device
+        if len(shape) != 4 or v.shape != shape:
+            raise ValueError("k and v must be [n_pages, page_size, heads, head_dim]")
+        if dtype not in _CACHE_DTYPES:
+            raise TypeError("pages must be float32, float16, bfloat16 or float8_e4m3fn")
+        if v.dtype != dtype or v.device != dev:
+            raise ValueError("k and v must have one dtype and device")
+        sk, sv = k.stride(), v.stride()
+        if (sk[3] != 1 or sv[3] != 1) and shape[3] != 1:
+            raise ValueError("the elements of a row of pages must be contiguous")
+        if dtype == E4M3:
+            for t in (k_scales, v_scales):
+                if t is None or t.dtype != torch.uint8 or t.shape != shape[:3] or t.device != dev:
+                    raise ValueError("k_scales and v_scales must be uint8 [n_pages, page_size, heads] "
+                                     "on %s" % dev)
+            ks, vs = k_scales.data_ptr(), v_scales.data_ptr()
+            strides = sk[:3] + sv[:3] + k_scales.stride() + v_scales.stride()
+        elif k_scales is not None or v_scales is not None:
+            raise ValueError("only pages of float8_e4m3fn have scales")
+        else:
+            ks = vs = 0
+            strides = sk[:3] + sv[:3] + (0,) * 6
+        self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
+        self.dtype, self.device = dtype, dev
+        self.page_size, self.heads, self.head_dim = shape[1:]
+        self._packed = _pack_cache(k.data_ptr(), v.data_ptr(), ks, vs, *shape, *strides,
+                                   _CACHE_DTYPES[dtype])
+
+    @classmethod
+    def empty(cls, n_pages, page_size, heads, head_dim, dtype=torch.bfloat16, device="cuda"):
+        """A cache of new pages, whose contents are not set."""
+        k, v = (torch.empty((n_pages, page_size, heads, head_dim), dtype=dtype, device=device)
+                for _ in range(2))
+        if dtype != E4M3:
+            return cls(k, v)
+        return cls(k, v, *(torch.empty((n_pages, page_size, heads), dtype=torch.uint8, device=device)
+                           for _ in range(2)))
+
+
+def _check_pages(cache, page_table, kv_lens, q_lens, B, dev):
+    """(address, row stride) of the page table."""
+    if cache.device != dev:
+        raise ValueError("the cache must be on %s" % dev)
+    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B
+            or page_table.device != dev or (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
+        raise ValueError("page_table must be an int32 tensor [%d, max_pages] with contiguous rows on %s"
+                         % (B, dev))
+    _check_lens("kv_lens", kv_lens, B, dev)
+    if q_lens is not None:
+        _check_lens("q_lens", q_lens, B, dev)
+    return page_table.data_ptr(), page_table.stride(0)
+
+
+def tdt_cache_write(k, v, cache, page_table, kv_lens, q_lens=None):
+    """Writes new label states' k, v [B, L, heads, head_dim] into the pages of ``cache`` on the current
+    CUDA stream (include/tdt_decoder.h, tdt_cache_write); float8_e4m3fn pages are quantised as they
+    are written.
+
+    Row i < q_lens[b] of utterance b is position kv_lens[b] - q_lens[b] + i: kv_lens (int64 [B]) counts
+    the new rows; q_lens: int64 [B] or None (all L).  page_table: int32 [B, max_pages].  k and v may
+    be slices of a fused projection.
+    """
+    ks = k.shape
+    if len(ks) != 4 or v.shape != ks or ks[2] != cache.heads or ks[3] != cache.head_dim:
+        raise ValueError("k and v must be [B, L, %d, %d]" % (cache.heads, cache.head_dim))
+    dtype, dev = k.dtype, k.device
+    if dtype not in DTYPES or v.dtype != dtype:
+        raise TypeError("k and v must be float32, float16 or bfloat16, of one dtype")
+    if cache.dtype != dtype and cache.dtype != E4M3:
+        raise TypeError("pages of %s cannot hold rows of %s" % (cache.dtype, dtype))
+    if v.device != dev:
+        raise ValueError("k and v must be on one device")
+    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, ks[0], dev)
+    (k, sk), (v, sv) = _rows(k), _rows(v)
+    with _on(dev):
+        _check(lib.tdt_cache_write(
+            k.data_ptr(), v.data_ptr(), _pack3(ks[0], ks[1], page_table.shape[1]),
+            _pack6(*sk[:3], *sv[:3]), DTYPES[dtype], cache._packed, table, stride,
+            kv_lens.data_ptr(), _addr(q_lens), _raw_stream(dev.index)))
+
+
+def tdt_cache_read(cache, page_table, kv_lens, q_lens, length, dtype, k=None, v=None):
+    """Rows of ``cache`` as (k, v), each [B, length, heads, head_dim] of ``dtype``: row i < q_lens[b] of
+    utterance b is position kv_lens[b] - q_lens[b] + i, as in tdt_cache_write (q_lens = kv_lens: whole
+    utterances; None: all ``length``); later rows are 0.  k and v may be given."""
+    B, dev = kv_lens.shape[0], cache.device
+    if dtype not in DTYPES:
+        raise TypeError("dtype must be float32, float16 or bfloat16")
+    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
+    shape, out = (B, length, cache.heads, cache.head_dim), []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        elif (t.shape != shape or t.dtype != dtype or t.device != dev
+              or (t.stride(3) != 1 and shape[3] != 1)):
+            raise ValueError("%s must be %s of %s on %s with contiguous rows" % (name, shape, dtype, dev))
+        out.append(t)
+    k, v = out
+    with _on(dev):
+        _check(lib.tdt_cache_read(
+            cache._packed, table, stride, kv_lens.data_ptr(), _addr(q_lens),
+            _pack3(B, length, page_table.shape[1]), _pack6(*k.stride()[:3], *v.stride()[:3]),
+            DTYPES[dtype], k.data_ptr(), v.data_ptr(), _raw_stream(dev.index)))
+    return k, v
+
+
+def tdt_paged_attn_workspace_size(sizes, dtype, cache) -> int:
+    """Bytes of scratch of tdt_paged_attn; sizes = (B, Lq, H, max_pages), dtype q's (0 for invalid
+    arguments or when none is needed)."""
+    return int(lib.tdt_paged_attn_workspace_size(_pack4(*sizes), DTYPES[dtype], cache._packed))
+
+
+def tdt_paged_attn(q, cache, page_table, kv_lens, q_lens=None, scale=None, need_lse=False, out=None,
+                   lse=None, workspace=None):
+    """Causal attention of new label states q [B, Lq, H, D] over the pages of ``cache``, which hold their
+    own keys and values already (tdt_cache_write of the same lengths), on the current CUDA stream
+    (include/tdt_decoder.h, tdt_paged_attn); H a multiple of the cache's heads.
+
+    Query i < q_lens[b] of utterance b is at position kv_lens[b] - q_lens[b] + i and sees the positions
+    up to its own; queries past q_lens[b] (None: all Lq) get 0.  Pages are of q's dtype or
+    float8_e4m3fn.  scale: 1 / sqrt(D) unless given.  workspace: a contiguous uint8 tensor of
+    tdt_paged_attn_workspace_size bytes at least, allocated unless given.  Returns (out, lse): out like
+    q, lse float32 [B, H, Lq], or None without need_lse.
+    """
+    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+        raise ValueError("q must be [B, Lq, H, %d]" % cache.head_dim)
+    B, Lq, H, D = q.shape
+    dtype, dev = q.dtype, q.device
+    if dtype not in DTYPES:
+        raise TypeError("q dtype must be float32, float16 or bfloat16")
+    if cache.dtype != dtype and cache.dtype != E4M3:
+        raise TypeError("queries of %s cannot read pages of %s" % (dtype, cache.dtype))
+    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
+    q, sq = _rows(q)
+    out, so = _like(q, out, "out")
+    if lse is not None:
+        if (lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous()
+                or lse.device != dev):
+            raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq] on %s" % dev)
+    elif need_lse:
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
+    sizes, code, ws, nbytes = _pack4(B, Lq, H, page_table.shape[1]), DTYPES[dtype], None, 0
+    if workspace is None:
+        nbytes = lib.tdt_paged_attn_workspace_size(sizes, code, cache._packed)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            ws = workspace.data_ptr()
+    elif (workspace.dtype != torch.uint8 or workspace.device != dev
+          or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on %s" % dev)
+    else:
+        ws, nbytes = workspace.data_ptr(), workspace.numel()
+    with _on(dev):
+        _check(lib.tdt_paged_attn(
+            q.data_ptr(), sizes, _pack6(*sq[:3], *so[:3]), code, cache._packed, table, stride,
+            kv_lens.data_ptr(), _addr(q_lens), D ** -0.5 if scale is None else scale, out.data_ptr(),
+            _addr(lse), ws, nbytes, _raw_stream(dev.index)))
+    return out, lse
+
+
+# ---- log-probabilities of given tokens --------------------------------------------------------------
+class TokenLogprobs(NamedTuple):
+    """logprobs, entropy float32 [N]; stats float32 [N, 2]: each row's maximum m and
+    ln sum exp(x - m); top_tokens int32, top_logprobs float32 [N, n_top] (None without)."""
+
+    logprobs: torch.Tensor
+    entropy: torch.Tensor
+    stats: torch.Tensor
+    top_tokens: Optional[torch.Tensor] = None
+    top_logprobs: Optional[torch.Tensor] = None
+
+
+def _check_scored(logits, tokens):
+    """(logits with contiguous rows, N, V)"""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [N, V]")
+    if logits.dtype not in DTYPES:
+        raise TypeError("logits dtype must be float32, float16 or bfloat16")
+    N, V = logits.shape
+    if (tokens.dtype != torch.int64 or tokens.shape != (N,) or not tokens.is_contiguous()
+            or tokens.device != logits.device):
+        raise ValueError("tokens must be a contiguous int64 tensor of %d element(s) on %s"
+                         % (N, logits.device))
+    if logits.stride(1) != 1 and V != 1:
+        logits = logits.contiguous()
+    return logits, N, V
+
+
+def _new_logprobs(N, n_top, dev):
+    f = torch.float32
+    three = (torch.empty(N, dtype=f, device=dev), torch.empty(N, dtype=f, device=dev),
+             torch.empty((N, 2), dtype=f, device=dev))
+    if not n_top:
+        return TokenLogprobs(*three)
+    n_top = max(0, n_top)  # a negative one is refused with the other arguments
+    return TokenLogprobs(*three, torch.empty((N, n_top), dtype=torch.int32, device=dev),
+                         torch.empty((N, n_top), dtype=f, device=dev))
+
+
+def _check_weights(N, dev, **weights):
+    for name, t in weights.items():
+        if t is not None and (t.dtype != torch.float32 or t.shape != (N,) or not t.is_contiguous()
+                              or t.device != dev):
+            raise ValueError("%s must be a contiguous float32 tensor of %d element(s) on %s"
+                             % (name, N, dev))
+
+
+def _grad_rows(logits, grad_out):
+    if grad_out is None:
+        return torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    if (grad_out.shape != logits.shape or grad_out.dtype != logits.dtype
+            or grad_out.device != logits.device or (grad_out.stride(1) != 1 and logits.shape[1] != 1)):
+        raise ValueError("grad_out must have the logits' shape, dtype and device and contiguous rows")
+    return grad_out
+
+
+def tdt_token_logprobs_fwd(logits, tokens, n_top=0):
+    """Log-probability of ``tokens`` (int64 [N]; negative: padding, the row takes no part) under each row
+    of ``logits`` [N, V], the row's entropy, and its ``n_top`` most probable tokens, on the current
+    CUDA stream (include/tdt_decoder.h, tdt_token_logprobs_fwd).  Rows may be a slice of wider ones.
+    Returns TokenLogprobs."""
+    logits, N, V = _check_scored(logits, tokens)
+    dev = logits.device
+    r = _new_logprobs(N, n_top, dev)
+    with _on(dev):
+        _check(lib.tdt_token_logprobs_fwd(
+            logits.data_ptr(), _pack3(N, V, n_top), logits.stride(0), DTYPES[logits.dtype],
+            tokens.data_ptr(), r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(),
+            _addr(r.top_tokens), _addr(r.top_logprobs), _raw_stream(dev.index)))
+    return r
+
+
+def tdt_token_logprobs_bwd(logits, tokens, result, grad_logprobs=None, grad_entropy=None, grad_top=None,
+                           grad_out=None):
+    """The logits' gradient, [N, V] of their dtype, for weights grad_logprobs, grad_entropy (float32 [N])
+    and grad_top (float32 [N, n_top]) of ``result``, which tdt_token_logprobs_fwd returned for the same
+    logits and tokens.  grad_out may be ``logits``: the gradient then replaces them."""
+    rows = logits
+    logits, N, V = _check_scored(logits, tokens)
+    dev = logits.device
+    _check_weights(N, dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, entropy=result.entropy)
+    stats, top, n_top = result.stats, result.top_tokens, 0
+    if (stats.dtype != torch.float32 or stats.shape != (N, 2) or not stats.is_contiguous()
+            or stats.device != dev):
+        raise ValueError("stats must be a contiguous float32 tensor [%d, 2] on %s" % (N, dev))
+    if grad_top is not None:
+        if top is None:
+            raise ValueError("grad_top is of alternatives that the result does not hold")
+        for name, t, dtype in (("grad_top", grad_top, torch.float32), ("top_tokens", top, torch.int32)):
+            if (t.dtype != dtype or t.shape != top.shape or t.dim() != 2 or t.shape[0] != N
+                    or not t.is_contiguous() or t.device != dev):
+                raise ValueError("%s must be a contiguous %s tensor [%d, n_top] on %s"
+                                 % (name, dtype, N, dev))
+        n_top = top.shape[1]
+    grad_out = _grad_rows(rows, grad_out)
+    with _on(dev):
+        _check(lib.tdt_token_logprobs_bwd(
+            logits.data_ptr(), _pack3(N, V, n_top), _pack2(logits.stride(0), grad_out.stride(0)),
+            DTYPES[logits.dtype], tokens.data_ptr(), result.entropy.data_ptr(), stats.data_ptr(),
+            _addr(top), _addr(grad_logprobs), _addr(grad_entropy), _addr(grad_top),
+            grad_out.data_ptr(), _raw_stream(dev.index)))
+    return grad_out
+
+
+def tdt_token_logprobs_fwd_bwd(logits, tokens, grad_logprobs=None, grad_entropy=None, n_top=0,
+                               grad_out=None):
+    """Both in one call, for weights that are known beforehand: (TokenLogprobs, gradient of the logits).
+    Arguments as of tdt_token_logprobs_fwd and tdt_token_logprobs_bwd."""
+    rows = logits
+    logits, N, V = _check_scored(logits, tokens)
+    dev = logits.device
+    _check_weights(N, dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy)
+    grad_out = _grad_rows(rows, grad_out)
+    r = _new_logprobs(N, n_top, dev)
+    with _on(dev):
+        _check(lib.tdt_token_logprobs_fwd_bwd(
+            logits.data_ptr(), _pack3(N, V, n_top), _pack2(logits.stride(0), grad_out.stride(0)),
+            DTYPES[logits.dtype], tokens.data_ptr(), _addr(grad_logprobs), _addr(grad_entropy),
+            r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(), _addr(r.top_tokens),
+            _addr(r.top_logprobs), grad_out.data_ptr(), _raw_stream(dev.index)))
+    return r, grad_out
 
 
 def _new_workspace(logits, n_dur):

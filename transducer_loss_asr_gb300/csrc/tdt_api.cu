@@ -524,6 +524,9 @@ const char *tdt_status_string(int status) {
     case TDT_ERR_BAD_SCALE: return "scale must be finite and > 0";
     case TDT_ERR_BAD_SAMPLING:
       return "invalid sampling setting (temperature >= 0, 0 <= top_p, min_p <= 1, top_k >= 0)";
+    case TDT_ERR_BAD_PAGES:
+      return "invalid pages (n_pages >= 1, page_size a power of two up to 65536, max_pages * page_size < 2^30)";
+    case TDT_ERR_BAD_TOP: return "n_top outside [0, min(V, 64)]";
     case TDT_ERR_NOALLOC_TOO_LARGE:
       return "problem needs more scratch than the fixed array of tdt_loss_fwd_bwd_noalloc "
              "(TDT_NOALLOC_MAX_WORKSPACE_BYTES); use tdt_loss_fwd_bwd or tdt_loss_fwd_bwd_ws";
