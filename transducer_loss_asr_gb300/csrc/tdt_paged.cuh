@@ -94,7 +94,11 @@ struct CacheArgs {
 };
 cudaError_t launch_cache_write(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
-// Attention on the CUDA cores: every call.
+// Few query rows: a kernel that reads k and v at memory speed.
+constexpr int kPagedStepRows = 32;  // rows of a key head at most
+bool paged_step_fits(const PagedArgs &a, int dtype, int cache_dtype);
+cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
+// Attention on the CUDA cores: every other call.
 cudaError_t launch_paged_general(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 
 }  // namespace tdt

@@ -212,7 +212,9 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
   a.q = q;
   a.out = out;
   a.lse = lse;
-  const cudaError_t e = launch_paged_general(a, dtype, cache->dtype, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = paged_step_fits(a, dtype, cache->dtype) ? launch_paged_step(a, dtype, cache->dtype, s)
+                                                                : launch_paged_general(a, dtype, cache->dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

@@ -1,0 +1,507 @@
+// tdt_paged_step.cu -- causal attention of few query rows over a paged cache (a decoding step, a small beam, a few drafted
+// tokens): float16 and bfloat16 queries over pages of their own type or of e4m3, heads up to 128.
+//
+// With R = Lq * G rows a key head (G query heads share it), the work is to read k and v once.  A warp multiplies tiles of
+// 16 keys straight from the registers that its loads fill, by mma.sync m16n8k16, which adds over the lanes by itself: about
+// 1.5 instructions a lane and element of 8 bits, where products on the CUDA cores take 4 R / 2 and the exchange of partial
+// scores.  (A tcgen05 product has 128 rows; its operands would have to go through shared memory first.)
+//   S = Q K^T     A = q, in registers for the whole walk; B = k: lane (g, t) holds key g of 8 and a quarter of its elements.
+//                 A contraction may take its elements in any order, so a lane's quarter is what its 16-byte loads bring.
+//   O^T = V^T P^T A = v: lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9 and an eighth of their elements, two keys to a register by a
+//                 byte permutation; B = p: exactly what S leaves in the lane (query g, keys 2t, 2t+1).
+// Rows 8 to 15 of A and a second B take up to 16 query rows; more rows: more CTAs, which mostly find k and v in L2.
+//
+// e4m3 pages: values become float16 exactly, q is put into float16 by a power of two a row, a key's power of two
+// multiplies its scores and a value row's its weight, relative to the largest so far (E); sums stay in float32.
+// The reference m of a row moves only when its maximum has grown by 8 (in base 2), so O is rescaled rarely.
+//
+// A cluster of S CTAs has one (utterance, key head, group of rows); its warps take the keys in turns.  Loads of the next turn
+// are in flight while one is at work.  Warps and then CTAs (over distributed shared memory) are joined in a fixed order.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "tdt_paged.cuh"
+#include "tdt_tc.cuh"
+
+namespace tdt {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kWarps = 4;
+constexpr float kLazy = 8.0f;
+
+struct StepArgs {
+  PagedArgs a;
+  int splits;  // CTAs of a cluster
+  int groups;  // clusters that share the rows of a key head
+};
+
+// d += a b, 16 x 8 x 16, float32 sums; F16: float16 operands, else bfloat16
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// BYTES contiguous bytes of global memory that is read once, in accesses of at most ALIGN.
+template <int BYTES, int ALIGN> __device__ __forceinline__ void load_words(unsigned (&w)[BYTES / 4], const unsigned char *p) {
+  if (ALIGN >= 16 && BYTES == 16) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[BYTES / 4 - 2]), "=r"(w[BYTES / 4 - 1])
+                 : "l"(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < BYTES / 8; ++i)
+      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[2 * i]), "=r"(w[2 * i + 1]) : "l"(p + 8 * i));
+  }
+}
+
+template <int QT, int PT, int DP, int RT> struct Shape {
+  static constexpr bool E8 = PT == kE4M3;
+  static constexpr bool F16 = E8 || PT == kF16;      // the products' type
+  static constexpr int ES = E8 ? 1 : 2;
+  static constexpr int KT = E8 || DP == 64 ? 32 : 16;  // keys of a turn
+  static constexpr int NT = KT / 8;                  // tiles of 8 keys
+  static constexpr int KL = DP * ES / 64;            // 16-byte loads of a key's quarter (64 bytes an instruction and key)
+  static constexpr int VB = DP * ES / 8 >= 16 ? 16 : DP * ES / 8;  // bytes of a load of a value row's eighth
+  static constexpr int VL = DP * ES / 8 / VB;
+  static constexpr int KSTEPS = DP / 16;
+  static constexpr int MTILES = DP / 16;
+  static constexpr int CTAS = RT == 1 ? 3 : 2;       // of an SM: 168 or 255 registers a thread
+};
+
+// The first of the four elements that lane t of a group contributes to step i of the contraction over a head.
+template <int ES> __device__ __forceinline__ constexpr int step_element(int i, int t) {
+  return ES == 1 ? i / 4 * 64 + t * 16 + i % 4 * 4 : i / 2 * 32 + t * 8 + i % 2 * 4;
+}
+// The first of the two elements that lane group g contributes to tile i of 16 elements of a value row.
+template <int ES, int VB> __device__ __forceinline__ constexpr int tile_element(int i, int g) {
+  constexpr int per = VB / ES / 2;  // tiles of a load
+  return i / per * (8 * VB / ES) + g * (VB / ES) + i % per * 2;
+}
+
+template <int QT, int PT, int DP, int RT, int ALIGN>
+__global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
+    paged_step_kernel(const __grid_constant__ StepArgs f) {
+  typedef Shape<QT, PT, DP, RT> S;
+  typedef typename Elem<QT>::T E;
+  constexpr int R = 8 * RT;
+  constexpr float kShift = S::F16 ? 7.0f : 0.0f;  // float16 weights start at 2^7, at most 2^15
+  const PagedArgs &a = f.a;
+  __shared__ __align__(16) float part_o[kWarps][R][DP + 4];
+  __shared__ float part_m[kWarps][R], part_l[kWarps][R];
+  __shared__ float cta_m[R], cta_l[R];
+  __shared__ int cta_bad;
+  __shared__ __align__(16) float cta_o[R][DP];
+  __shared__ __align__(8) float key_f[kWarps][S::KT], value_f[kWarps][S::KT];  // e4m3: of a turn's rows
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const unsigned cluster_id = blockIdx.x / f.splits, unit = cluster_id / f.groups;  // = b * Hkv + hk
+  const int split = blockIdx.x % f.splits, hk = unit % a.Hkv;
+  const long long b = unit / a.Hkv;
+  const NewRows n = new_rows(a.t, b, a.Lq);
+  const int row0 = cluster_id % f.groups * R;
+  const int rows = min(R, a.Lq * a.G - row0);  // row r: query (row0 + r) / G, head hk * G + (row0 + r) % G
+  const int used = min(n.n, (row0 + rows - 1) / a.G + 1);  // queries that take part, of those up to this group's last
+  const int end = used > row0 / a.G ? n.first + used : 0;  // positions that some row sees
+  if (threadIdx.x == 0) cta_bad = 0;
+  if (S::E8) __syncthreads();  // else the first use is behind the walk's own barrier
+
+  // q: rows g and g + 8, in the order of the contraction's steps
+  unsigned q[S::KSTEPS][RT][2];
+  float c[RT];
+  int last[RT];  // the last position that the row sees
+#pragma unroll
+  for (int h = 0; h < RT; ++h) {
+    const int r = g + 8 * h, i = (row0 + r) / a.G;
+    const bool live = r < rows && i < n.n;
+    last[h] = live ? n.first + i : -1;
+    c[h] = a.scale * kLog2e;
+    const E *src = static_cast<const E *>(a.q) + b * a.sq.b + i * a.sq.l + (hk * a.G + (row0 + r) % a.G) * a.sq.h;
+#pragma unroll
+    for (int x = 0; x < S::KSTEPS; ++x) {
+      const int d = step_element<S::ES>(x, t);
+      uint2 w = make_uint2(0, 0);
+      if (live && d < a.D) w = __ldg(reinterpret_cast<const uint2 *>(src + d));
+      q[x][h][0] = w.x;
+      q[x][h][1] = w.y;
+    }
+    if (QT == kBF16 && S::F16) {  // into float16 by a power of two: the row's largest becomes at most 2^15
+      unsigned top = 0;
+#pragma unroll
+      for (int x = 0; x < S::KSTEPS; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) top = max(top, max(q[x][h][y] << 16 & 0x7fff0000u, q[x][h][y] & 0x7fff0000u));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int e = min(max((int)(top >> 23) - 127 - 14, -110), 113);
+      const float down = __uint_as_float((unsigned)(127 - e) << 23);
+      c[h] *= __uint_as_float((unsigned)(127 + e) << 23);
+#pragma unroll
+      for (int x = 0; x < S::KSTEPS; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          q[x][h][y] = pack2<kF16>(__uint_as_float(q[x][h][y] << 16) * down, __uint_as_float(q[x][h][y] & 0xffff0000u) * down);
+    }
+  }
+  const int least = __reduce_min_sync(0xffffffffu, min(last[0] < 0 ? 0x7fffffff : last[0], last[RT - 1] < 0 ? 0x7fffffff : last[RT - 1]));
+
+  float o[S::MTILES][RT][4], m[RT], l[RT];
+#pragma unroll
+  for (int h = 0; h < RT; ++h) {
+    m[h] = -INFINITY;
+    l[h] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < S::MTILES; ++x)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) o[x][h][y] = 0.0f;
+  }
+  int top_e = 0;  // e4m3: the largest byte of the value rows so far; o is in units of 2^(top_e - 127)
+  bool bad = false;
+
+  const unsigned char *kp = static_cast<const unsigned char *>(a.k.data) + hk * a.k.s.h * S::ES;
+  const unsigned char *vp = static_cast<const unsigned char *>(a.v.data) + hk * a.v.s.h * S::ES;
+  unsigned kx[S::NT][S::KL][4], vx[S::KT / 16][4][S::VL][S::VB / 4];
+  unsigned bytes = 0;  // e4m3: this lane's position's bytes of k and v
+  int id = 0;          // page of this lane's position (of KT)
+  const int place_mask = (1 << a.t.page_bits) - 1;
+  auto lookup = [&](int base) {
+    const int pos = base + lane % S::KT;
+    id = pos < end ? page_of(a.t, b, pos) : -1;
+    bad |= pos < end && id < 0;
+  };
+  auto load_keys = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) {
+      const int pos = base + 8 * j + g, page = __shfl_sync(0xffffffffu, id, 8 * j + g);
+      const unsigned char *row = kp + (page * a.k.s.b + (pos & place_mask) * a.k.s.l) * S::ES;
+#pragma unroll
+      for (int i = 0; i < S::KL; ++i) {
+        kx[j][i][0] = kx[j][i][1] = kx[j][i][2] = kx[j][i][3] = 0;
+        if (page >= 0) {
+          if (64 * i + 16 * t + 16 <= a.D * S::ES)
+            load_words<16, ALIGN>(kx[j][i], row + 64 * i + 16 * t);
+          else if (64 * i + 16 * t < a.D * S::ES)  // 8 bytes are left
+            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i + 16 * t);
+        }
+      }
+    }
+  };
+  auto load_values = [&](int base) {
+#pragma unroll
+    for (int j = 0; j < S::KT / 16; ++j)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int key = 16 * j + 2 * t + (y & 1) + (y >> 1) * 8;
+        const int pos = base + key, page = __shfl_sync(0xffffffffu, id, key);
+        const unsigned char *row = vp + (page * a.v.s.b + (pos & place_mask) * a.v.s.l) * S::ES;
+#pragma unroll
+        for (int i = 0; i < S::VL; ++i) {
+#pragma unroll
+          for (int z = 0; z < S::VB / 4; ++z) vx[j][y][i][z] = 0;
+          const int at = i * 8 * S::VB + g * S::VB;
+          if (page >= 0) {
+            if (at + S::VB <= a.D * S::ES)
+              load_words<S::VB, ALIGN>(vx[j][y][i], row + at);
+            else if (S::VB == 16 && at < a.D * S::ES)
+              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), row + at);
+          }
+        }
+      }
+  };
+  auto load_bytes = [&](int base) {
+    if (!S::E8) return;
+    const int place = (base + lane) & place_mask;
+    bytes = 0;
+    if (id >= 0)
+      bytes = __ldg(a.k.scales + row_at(a.k.ss, id, place, hk)) | (unsigned)__ldg(a.v.scales + row_at(a.v.ss, id, place, hk)) << 8;
+  };
+
+  const int turns = (end + S::KT - 1) / S::KT, step = f.splits * kWarps;
+  int turn = split * kWarps + warp;
+  if (turn < turns) {
+    lookup(turn * S::KT);
+    load_keys(turn * S::KT);
+    load_bytes(turn * S::KT);
+    load_values(turn * S::KT);
+  }
+  for (; turn < turns; turn += step) {
+    const int base = turn * S::KT, next = (turn + step) * S::KT;
+    const bool more = turn + step < turns;
+    // scores: rows g, g + 8; keys 8 j + 2 t, + 1
+    float s[S::NT][4];
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) {
+      s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < S::KSTEPS; ++x) {
+        const unsigned qa[4] = {q[x][0][0], RT == 2 ? q[x][RT - 1][0] : 0, q[x][0][1], RT == 2 ? q[x][RT - 1][1] : 0};
+        if constexpr (S::E8) {
+          const unsigned w = kx[j][x / 4][x % 4];
+          mma16<true>(s[j], qa, e4m3x2_to_half2(w & 0xffffu), e4m3x2_to_half2(w >> 16));
+        } else {
+          mma16<S::F16>(s[j], qa, kx[j][x / 2][x % 2 * 2], kx[j][x / 2][x % 2 * 2 + 1]);
+        }
+      }
+    }
+    if constexpr (S::E8) {
+      const unsigned kb = bytes & 0xffu, vb = bytes >> 8;
+      const int most = (int)__reduce_max_sync(0xffffffffu, vb == kByteNaN ? 0u : vb);
+      if (most > top_e) {
+        if (top_e > 0) {
+          const float down = pow2_nonpos(top_e - most);
+#pragma unroll
+          for (int x = 0; x < S::MTILES; ++x)
+#pragma unroll
+            for (int h = 0; h < RT; ++h)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) o[x][h][y] *= down;
+        }
+        top_e = most;
+      }
+      __syncwarp();
+      key_f[warp][lane] = scale_of(kb);
+      value_f[warp][lane] = vb == kByteNaN ? NAN : pow2_nonpos((int)vb - top_e);
+      __syncwarp();
+    }
+    if (more) {
+      lookup(next);
+      load_keys(next);
+      load_bytes(next);
+    }
+    // weights
+    float top[RT];
+#pragma unroll
+    for (int h = 0; h < RT; ++h) {
+      top[h] = -INFINITY;
+      const bool masked = base + S::KT - 1 > least;
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        float2 kf = make_float2(c[h], c[h]);
+        if constexpr (S::E8) {
+          const float2 two = *reinterpret_cast<const float2 *>(&key_f[warp][8 * j + 2 * t]);
+          kf = make_float2(two.x * c[h], two.y * c[h]);
+        }
+        s[j][2 * h] *= kf.x;
+        s[j][2 * h + 1] *= kf.y;
+        if (masked) {
+          const int key = base + 8 * j + 2 * t;
+          if (key > last[h]) s[j][2 * h] = -INFINITY;
+          if (key + 1 > last[h]) s[j][2 * h + 1] = -INFINITY;
+        }
+        top[h] = fmaxf(top[h], fmaxf(s[j][2 * h], s[j][2 * h + 1]));
+      }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int h = 0; h < RT; ++h) grow |= top[h] > m[h] + (kLazy + kShift);  // from -inf: any score
+    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+      for (int h = 0; h < RT; ++h) {
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 1));
+        top[h] = fmaxf(top[h], __shfl_xor_sync(0xffffffffu, top[h], 2));
+        const bool up = top[h] > m[h] + (kLazy + kShift);
+        const float now = up ? top[h] - kShift : m[h], down = up ? fast_exp2(m[h] - now) : 1.0f;
+        m[h] = now;
+        l[h] *= down;
+        // a lane's columns of o are the queries 2t, 2t + 1
+        const float f0 = __shfl_sync(0xffffffffu, down, 8 * t), f1 = __shfl_sync(0xffffffffu, down, 8 * t + 4);
+#pragma unroll
+        for (int x = 0; x < S::MTILES; ++x) {
+          o[x][h][0] *= f0;
+          o[x][h][1] *= f1;
+          o[x][h][2] *= f0;
+          o[x][h][3] *= f1;
+        }
+      }
+    }
+    unsigned p[S::NT][RT];
+#pragma unroll
+    for (int h = 0; h < RT; ++h) {
+      const float ref = m[h] == -INFINITY ? 0.0f : m[h];
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        float p0 = fast_exp2(s[j][2 * h] - ref), p1 = fast_exp2(s[j][2 * h + 1] - ref);
+        l[h] += p0 + p1;
+        if constexpr (S::E8) {
+          const float2 two = *reinterpret_cast<const float2 *>(&value_f[warp][8 * j + 2 * t]);
+          p0 *= two.x;
+          p1 *= two.y;
+        }
+        p[j][h] = pack2<S::F16 ? (int)kF16 : (int)kBF16>(p0, p1);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < S::KT / 16; ++j)
+#pragma unroll
+      for (int x = 0; x < S::MTILES; ++x) {
+        unsigned va[4];
+        if constexpr (S::E8) {
+          constexpr int per = S::VB / 2;  // tiles of a load
+          const int i = x / per, w = x % per / 2, sel = x % 2 ? 0x7362 : 0x5140;
+          const unsigned lo = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], sel), hi = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], sel);
+          va[0] = e4m3x2_to_half2(lo & 0xffffu);
+          va[1] = e4m3x2_to_half2(lo >> 16);
+          va[2] = e4m3x2_to_half2(hi & 0xffffu);
+          va[3] = e4m3x2_to_half2(hi >> 16);
+        } else {
+          constexpr int per = S::VB / 4;
+          const int i = x / per, w = x % per;
+          va[0] = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], 0x5410);
+          va[1] = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], 0x7632);
+          va[2] = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], 0x5410);
+          va[3] = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], 0x7632);
+        }
+#pragma unroll
+        for (int h = 0; h < RT; ++h) mma16<S::F16>(o[x][h], va, p[2 * j][h], p[2 * j + 1][h]);
+      }
+    if (more) load_values(next);
+  }
+
+  // the warps of a CTA
+  const float unit_f = S::E8 ? scale_of(top_e) : 1.0f;
+#pragma unroll
+  for (int h = 0; h < RT; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if (t == 0) {
+      part_m[warp][g + 8 * h] = m[h];
+      part_l[warp][g + 8 * h] = l[h];
+    }
+#pragma unroll
+    for (int x = 0; x < S::MTILES; ++x) {
+      const int d = tile_element<S::ES, S::VB>(x, g);
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        *reinterpret_cast<float2 *>(&part_o[warp][8 * h + 2 * t + y][d]) = make_float2(o[x][h][y] * unit_f, o[x][h][y + 2] * unit_f);
+    }
+  }
+  if (!S::E8) __syncthreads();  // cta_bad is set to 0
+  if (bad) cta_bad = 1;
+  __syncthreads();
+  for (int x = threadIdx.x; x < R * DP; x += kWarps * 32) {
+    const int r = x / DP, d = x % DP;
+    float top = -INFINITY, sum = 0.0f, out = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, part_m[w][r]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float e = fast_exp2(part_m[w][r] - ref);
+      sum += e * part_l[w][r];
+      out += e * part_o[w][r][d];
+    }
+    cta_o[r][d] = out;
+    if (d == 0) {
+      cta_m[r] = cta_bad ? NAN : top;
+      cta_l[r] = sum;
+    }
+  }
+  cg::cluster_group cluster = cg::this_cluster();
+  if (f.splits > 1)
+    cluster.sync();
+  else
+    __syncthreads();
+  // the CTAs of the cluster: each writes its part of the elements
+  for (int x = split * (kWarps * 32) + threadIdx.x; x < rows * DP; x += f.splits * kWarps * 32) {
+    const int r = x / DP, d = x % DP;
+    float top = -INFINITY, sum = 0.0f, out = 0.0f;
+    bool lost = n.bad;
+    if (f.splits == 1) {
+      top = cta_m[r];
+      sum = cta_l[r];
+      out = cta_o[r][d];
+      lost |= top != top;
+    } else {
+      for (int i = 0; i < f.splits; ++i) {
+        const float x2 = *cluster.map_shared_rank(&cta_m[r], i);
+        lost |= x2 != x2;
+        top = fmaxf(top, x2);
+      }
+      const float ref = top == -INFINITY ? 0.0f : top;
+      for (int i = 0; i < f.splits; ++i) {
+        const float e = fast_exp2(*cluster.map_shared_rank(&cta_m[r], i) - ref);
+        sum += e * *cluster.map_shared_rank(&cta_l[r], i);
+        out += e * *cluster.map_shared_rank(&cta_o[r][d], i);
+      }
+    }
+    const int i = (row0 + r) / a.G, h = hk * a.G + (row0 + r) % a.G;
+    const bool live = i < n.n;
+    if (d < a.D)
+      static_cast<E *>(a.out)[b * a.so.b + i * a.so.l + h * a.so.h + d] =
+          Elem<QT>::from_float(lost ? NAN : live ? out / sum : 0.0f);
+    if (d == 0 && a.lse)
+      a.lse[(b * a.H + h) * a.Lq + i] = lost ? NAN : live ? (top + log2f(sum)) * kLn2 : -INFINITY;
+  }
+  if (f.splits > 1) cluster.sync();  // nobody leaves while its memory may be read
+}
+
+template <int QT, int PT, int DP, int RT, int ALIGN> cudaError_t launch(const StepArgs &f, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(f.a.B * f.a.Hkv * f.groups * f.splits));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = f.splits;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = f.splits > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, paged_step_kernel<QT, PT, DP, RT, ALIGN>, f);
+}
+template <int QT, int PT, int RT, int ALIGN> cudaError_t by_width(const StepArgs &f, cudaStream_t s) {
+  return f.a.D <= 64 ? launch<QT, PT, 64, RT, ALIGN>(f, s) : launch<QT, PT, 128, RT, ALIGN>(f, s);
+}
+template <int QT, int PT, int ALIGN> cudaError_t by_rows(const StepArgs &f, cudaStream_t s) {
+  return f.a.Lq * f.a.G <= 8 ? by_width<QT, PT, 1, ALIGN>(f, s) : by_width<QT, PT, 2, ALIGN>(f, s);
+}
+
+// Bytes that every row of pages is aligned to: 16, 8 or less.
+int alignment(const PagedArgs &a, int es) {
+  uintptr_t x = 0;
+  for (const Pages *p : {&a.k, &a.v})
+    x |= (uintptr_t)p->data | (uintptr_t)(p->s.b * es) | (uintptr_t)(p->s.l * es) | (uintptr_t)(p->s.h * es);
+  return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : 1;
+}
+
+}  // namespace
+
+bool paged_step_fits(const PagedArgs &a, int dtype, int cache_dtype) {
+  const bool e8 = cache_dtype == kE4M3;
+  auto rows_fit = [&](const void *p, const Strides &s) {
+    return (uintptr_t)p % 8 == 0 && (a.B == 1 || s.b % 4 == 0) && (a.Lq == 1 || s.l % 4 == 0) && (a.H == 1 || s.h % 4 == 0);
+  };
+  return dtype != kF32 && a.D <= 128 && a.D % 8 == 0 && (long long)a.Lq * a.G <= kPagedStepRows && rows_fit(a.q, a.sq) &&
+         alignment(a, e8 ? 1 : 2) >= (e8 ? 8 : 16);
+}
+
+cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream) {
+  StepArgs f = {};
+  f.a = a;
+  const int R = a.Lq * a.G <= 8 ? 8 : 16;
+  f.groups = (a.Lq * a.G + R - 1) / R;
+  // a cluster's CTAs, while CTAs leave the GPU idle and each keeps 64 keys
+  const long long units = a.B * a.Hkv * f.groups, most = (long long)a.t.max_pages << a.t.page_bits;
+  long long s = units > 0 ? 3 * kSMs / units : 1;
+  s = std::min<long long>({s, (most + 63) / 64, 8});
+  f.splits = 1;
+  while (f.splits * 2 <= s) f.splits *= 2;
+  if (cache_dtype == kE4M3) {
+    if (alignment(a, 1) == 16)
+      return dtype == kF16 ? by_rows<kF16, kE4M3, 16>(f, stream) : by_rows<kBF16, kE4M3, 16>(f, stream);
+    return dtype == kF16 ? by_rows<kF16, kE4M3, 8>(f, stream) : by_rows<kBF16, kE4M3, 8>(f, stream);
+  }
+  return dtype == kF16 ? by_rows<kF16, kF16, 16>(f, stream) : by_rows<kBF16, kBF16, 16>(f, stream);
+}
+
+}  // namespace tdt
