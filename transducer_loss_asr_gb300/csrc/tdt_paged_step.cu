@@ -171,6 +171,16 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   const unsigned char *kp = static_cast<const unsigned char *>(a.k.data) + hk * a.k.s.h * S::ES;
   const unsigned char *vp = static_cast<const unsigned char *>(a.v.data) + hk * a.v.s.h * S::ES;
   unsigned kx[S::NT][S::KL][4], vx[S::KT / 16][4][S::VL][S::VB / 4];
+#pragma unroll
+  for (int j = 0; j < S::NT; ++j)
+#pragma unroll
+    for (int i = 0; i < S::KL; ++i) kx[j][i][0] = kx[j][i][1] = kx[j][i][2] = kx[j][i][3] = 0;
+#pragma unroll
+  for (int j = 0; j < S::KT / 4; ++j)
+#pragma unroll
+    for (int i = 0; i < S::VL; ++i)
+#pragma unroll
+      for (int z = 0; z < S::VB / 4; ++z) vx[j / 4][j % 4][i][z] = 0;
   unsigned bytes = 0;  // e4m3: this lane's position's bytes of k and v
   int id = 0;          // page of this lane's position (of KT)
   const int place_mask = (1 << a.t.page_bits) - 1;
@@ -179,41 +189,83 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
     id = pos < end ? page_of(a.t, b, pos) : -1;
     bad |= pos < end && id < 0;
   };
+  // Most turns lie within a page and before the end: their rows are a lane's own offset and whole strides apart, and
+  // nothing is left out.  (Loads that D leaves out, in either way, leave their registers 0.)
+  constexpr int kTurnBits = S::KT == 32 ? 5 : 4;
+  const bool turns_in_pages = a.t.page_bits >= kTurnBits;
+  const long long k_row = a.k.s.l * S::ES, v_row = a.v.s.l * S::ES;
+  const int width = a.D * S::ES;
+  auto whole = [&](int base) { return turns_in_pages && base + S::KT <= end && id >= 0; };
   auto load_keys = [&](int base) {
+    if (whole(base)) {
+      const unsigned char *row = kp + id * (a.k.s.b * S::ES) + ((base & place_mask) + g) * k_row + 16 * t;
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < S::KL; ++i) {
+          if (64 * i + 16 * t + 16 <= width)
+            load_words<16, ALIGN>(kx[j][i], row + 64 * i);
+          else if (ALIGN < 16 && 64 * i + 16 * t < width)  // 8 bytes are left
+            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i);
+        }
+        row += 8 * k_row;
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) {
       const int pos = base + 8 * j + g, page = __shfl_sync(0xffffffffu, id, 8 * j + g);
-      const unsigned char *row = kp + (page * a.k.s.b + (pos & place_mask) * a.k.s.l) * S::ES;
+      const unsigned char *row = kp + page * (a.k.s.b * S::ES) + (pos & place_mask) * k_row + 16 * t;
 #pragma unroll
       for (int i = 0; i < S::KL; ++i) {
         kx[j][i][0] = kx[j][i][1] = kx[j][i][2] = kx[j][i][3] = 0;
         if (page >= 0) {
-          if (64 * i + 16 * t + 16 <= a.D * S::ES)
-            load_words<16, ALIGN>(kx[j][i], row + 64 * i + 16 * t);
-          else if (64 * i + 16 * t < a.D * S::ES)  // 8 bytes are left
-            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i + 16 * t);
+          if (64 * i + 16 * t + 16 <= width)
+            load_words<16, ALIGN>(kx[j][i], row + 64 * i);
+          else if (ALIGN < 16 && 64 * i + 16 * t < width)
+            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i);
         }
       }
     }
   };
   auto load_values = [&](int base) {
+    if (whole(base)) {
+      const unsigned char *row = vp + id * (a.v.s.b * S::ES) + ((base & place_mask) + 2 * t) * v_row + g * S::VB;
+#pragma unroll
+      for (int j = 0; j < S::KT / 16; ++j) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const unsigned char *p = row + ((y & 1) + (y >> 1) * 8) * v_row;
+#pragma unroll
+          for (int i = 0; i < S::VL; ++i) {
+            const int at = i * 8 * S::VB + g * S::VB;
+            if (at + S::VB <= width)
+              load_words<S::VB, ALIGN>(vx[j][y][i], p + i * 8 * S::VB);
+            else if (ALIGN < 16 && S::VB == 16 && at < width)
+              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), p + i * 8 * S::VB);
+          }
+        }
+        row += 16 * v_row;
+      }
+      return;
+    }
 #pragma unroll
     for (int j = 0; j < S::KT / 16; ++j)
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int key = 16 * j + 2 * t + (y & 1) + (y >> 1) * 8;
         const int pos = base + key, page = __shfl_sync(0xffffffffu, id, key);
-        const unsigned char *row = vp + (page * a.v.s.b + (pos & place_mask) * a.v.s.l) * S::ES;
+        const unsigned char *row = vp + page * (a.v.s.b * S::ES) + (pos & place_mask) * v_row + g * S::VB;
 #pragma unroll
         for (int i = 0; i < S::VL; ++i) {
 #pragma unroll
           for (int z = 0; z < S::VB / 4; ++z) vx[j][y][i][z] = 0;
           const int at = i * 8 * S::VB + g * S::VB;
           if (page >= 0) {
-            if (at + S::VB <= a.D * S::ES)
-              load_words<S::VB, ALIGN>(vx[j][y][i], row + at);
-            else if (S::VB == 16 && at < a.D * S::ES)
-              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), row + at);
+            if (at + S::VB <= width)
+              load_words<S::VB, ALIGN>(vx[j][y][i], row + i * 8 * S::VB);
+            else if (ALIGN < 16 && S::VB == 16 && at < width)
+              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), row + i * 8 * S::VB);
           }
         }
       }
@@ -490,12 +542,18 @@ cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cu
   f.a = a;
   const int R = a.Lq * a.G <= 8 ? 8 : 16;
   f.groups = (a.Lq * a.G + R - 1) / R;
-  // a cluster's CTAs, while CTAs leave the GPU idle and each keeps 64 keys
-  const long long units = a.B * a.Hkv * f.groups, most = (long long)a.t.max_pages << a.t.page_bits;
-  long long s = units > 0 ? 3 * kSMs / units : 1;
-  s = std::min<long long>({s, (most + 63) / 64, 8});
-  f.splits = 1;
-  while (f.splits * 2 <= s) f.splits *= 2;
+  // a cluster's CTAs: the split whose waves of CTAs take least, in turns of a warp (one CTA's start and end cost about
+  // as much as three)
+  const long long units = a.B * a.Hkv * f.groups, slots = (R == 8 ? 3 : 2) * kSMs;
+  const long long turns = (((long long)a.t.max_pages << a.t.page_bits) + 31) / 32;
+  long long least = -1;
+  for (int s = 1; s <= 8 && (s == 1 || turns >= 2 * s); s *= 2) {
+    const long long waves = (units * s + slots - 1) / slots, cost = waves * ((turns + s * kWarps - 1) / (s * kWarps) + 3);
+    if (least < 0 || cost < least) {
+      least = cost;
+      f.splits = s;
+    }
+  }
   if (cache_dtype == kE4M3) {
     if (alignment(a, 1) == 16)
       return dtype == kF16 ? by_rows<kF16, kE4M3, 16>(f, stream) : by_rows<kBF16, kE4M3, 16>(f, stream);
