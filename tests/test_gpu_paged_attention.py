@@ -52,7 +52,8 @@ def _reference(q, k, v, kv_lens, q_lens, scale):
 
 def _near(name, x, value, bound, record=None, case=""):
     x = x.double()
-    assert torch.equal(x.isinf(), value.isinf()) and torch.equal(x.isnan(), value.isnan()), name
+    same = torch.equal(x.isinf(), value.isinf()) and torch.equal(x.isnan(), value.isnan())
+    assert same, name
     fine = value.isfinite()
     if not fine.any():
         return

@@ -77,7 +77,8 @@ def _near(name, x, want, record=None, case=""):
         return
     value, bound = want
     x = x.double()
-    assert torch.equal(x.isinf(), value.isinf()) and torch.equal(x.isnan(), value.isnan()), name
+    same = torch.equal(x.isinf(), value.isinf()) and torch.equal(x.isnan(), value.isnan())
+    assert same, name
     fine = value.isfinite()
     ratio = ((x - value).abs()[fine] / bound[fine]).max().item()
     if record:

@@ -98,6 +98,12 @@ cudaError_t launch_cache_read(const CacheArgs &a, int dtype, int cache_dtype, cu
 constexpr int kPagedStepRows = 32;  // rows of a key head at most
 bool paged_step_fits(const PagedArgs &a, int dtype, int cache_dtype);
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
+// Many query rows on the tensor cores: which calls (by type and width, then by strides and alignment), and the workspace for
+// up to `most` positions an utterance.
+bool paged_tc_takes(int dtype, int D);
+bool paged_tc_fits(const PagedArgs &a, int dtype, int cache_dtype);
+size_t paged_tc_workspace(long long B, long long Lq, long long most, int H, int Hkv, int D, int cache_dtype);
+cudaError_t launch_paged_tc(const PagedArgs &a, int dtype, int cache_dtype, void *workspace, cudaStream_t stream);
 // Attention on the CUDA cores: every other call.
 cudaError_t launch_paged_general(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 

@@ -167,8 +167,9 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
 
 size_t tdt_paged_attn_workspace_size(const int64_t sizes[4], int dtype, const tdt_paged_cache *cache) {
   using namespace tdt;
-  if (check_attn(sizes, dtype, cache) != TDT_OK) return 0;
-  return 0;
+  if (check_attn(sizes, dtype, cache) != TDT_OK || !paged_tc_takes(dtype, (int)cache->head_dim)) return 0;
+  return paged_tc_workspace(sizes[0], sizes[1], sizes[3] * cache->page_size, (int)sizes[2], (int)cache->n_heads,
+                            (int)cache->head_dim, cache->dtype);
 }
 
 int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[6], int dtype,
@@ -214,6 +215,7 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = paged_step_fits(a, dtype, cache->dtype) ? launch_paged_step(a, dtype, cache->dtype, s)
+                        : paged_tc_fits(a, dtype, cache->dtype) ? launch_paged_tc(a, dtype, cache->dtype, workspace, s)
                                                                 : launch_paged_general(a, dtype, cache->dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
