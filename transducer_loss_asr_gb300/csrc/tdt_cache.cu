@@ -7,6 +7,8 @@
 // it comes from the bits of a, and x 2^-e is exact, so the only rounding is e4m3's own (half a step, 2^-4 of
 // the value, or 2^-10 2^e below 2^-6 2^e).
 // Bound by memory, or by latency for a decoding step.
+//
+// The rows of whole utterances can also be laid out densely, for attention that reads no pages (launch_gather).
 #include "tdt_paged.cuh"
 #include "tdt_rowio.cuh"
 
@@ -109,6 +111,39 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     p.scales[row_at(p.ss, page, place, at.h)] = (unsigned char)(finite ? e + kByteBias : kByteNaN);
 }
 
+// Elements [d0, d0 + 8) of a row of pages as float32, NaN if there is no such page.
+template <int PT, bool VEC>
+__device__ __forceinline__ void read8(const Pages &p, int page, int place, int h, int d0, int D, float (&v)[8]) {
+  if (page < 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = NAN;
+    return;
+  }
+  if constexpr (PT == kE4M3) {
+    const unsigned char *src = static_cast<const unsigned char *>(p.data) + row_at(p.s, page, place, h) + d0;
+    const float up = scale_of(__ldg(p.scales + row_at(p.ss, page, place, h)));
+    unsigned w[2] = {0, 0};
+    if (VEC) {
+      const uint2 two = __ldg(reinterpret_cast<const uint2 *>(src));
+      w[0] = two.x;
+      w[1] = two.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (d0 + i < D) w[i / 4] |= (unsigned)__ldg(src + i) << (i % 4 * 8);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = e4m3x2_to_float2(w[i / 2] >> (i % 2 * 16) & 0xffffu);
+      v[2 * i] = f.x * up;
+      v[2 * i + 1] = f.y * up;
+    }
+  } else {
+    typedef typename Elem<PT>::T P;
+    load8<PT, VEC>(static_cast<const P *>(p.data) + row_at(p.s, page, place, h) + d0, D - d0, v);
+  }
+}
+
 template <int DT, int PT, bool VEC>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, int lane_bits) {
   typedef typename Elem<DT>::T E;
@@ -123,40 +158,53 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   float v[8];
   int page = -1;
   if (at.i < n.n) {
-    const int pos = n.first + at.i, place = pos & ((1 << a.t.page_bits) - 1);
+    const int pos = n.first + at.i;
     page = page_of(a.t, at.b, pos);
-    if (page >= 0) {
-      if constexpr (PT == kE4M3) {
-        const unsigned char *src = static_cast<const unsigned char *>(p.data) + row_at(p.s, page, place, at.h) + d0;
-        const float up = scale_of(__ldg(p.scales + row_at(p.ss, page, place, at.h)));
-        unsigned w[2] = {0, 0};
-        if (VEC) {
-          const uint2 two = __ldg(reinterpret_cast<const uint2 *>(src));
-          w[0] = two.x;
-          w[1] = two.y;
-        } else {
+    read8<PT, VEC>(p, page, pos & ((1 << a.t.page_bits) - 1), at.h, d0, a.D, v);
+  } else {  // nothing to read: 0 past the new rows, NaN where the lengths are bad
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (d0 + i < a.D) w[i / 4] |= (unsigned)__ldg(src + i) << (i % 4 * 8);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = e4m3x2_to_float2(w[i / 2] >> (i % 2 * 16) & 0xffffu);
-          v[2 * i] = f.x * up;
-          v[2 * i + 1] = f.y * up;
-        }
-      } else {
-        typedef typename Elem<PT>::T P;
-        load8<PT, VEC>(static_cast<const P *>(p.data) + row_at(p.s, page, place, at.h) + d0, a.D - d0, v);
-      }
-    }
-  }
-  if (page < 0) {  // nothing to read: 0 past the new rows, NaN where lengths or the page are bad
-    const float none = n.bad || at.i < n.n ? NAN : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = none;
+    for (int i = 0; i < 8; ++i) v[i] = n.bad ? NAN : 0.0f;
   }
   store8<DT, VEC>(static_cast<E *>(blockIdx.y ? a.v : a.k) + at.b * s.b + at.i * s.l + at.h * s.h + d0, a.D - d0, v);
+}
+
+// The rows of whole utterances as dense [B, L, Hkv, D] tensors k and v of type DT, those past an utterance's end left as they are;
+// float16 ends at 65504.  The pages' rows of a chunk of positions go to a block; blocks take chunks in turn.  Beside them the
+// positions that each query sees, and lengths that cross attention refuses where this call's are out of range.
+constexpr int kChunk = 32;  // positions
+template <int DT, int PT, bool VEC>
+__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs f, int lane_bits) {
+  typedef typename Elem<DT>::T E;
+  const CacheArgs &a = f.c;
+  for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < f.B * f.Lq && blockIdx.y == 0;
+       x += (long long)gridDim.x * kThreads) {
+    const long long b = x / f.Lq;
+    const int i = (int)(x % f.Lq);
+    const NewRows n = new_rows(a.t, b, f.Lq);
+    f.windows[x] = make_int2(0, i < n.n ? n.first + i + 1 : 0);
+    if (i == 0) f.lens[b] = n.bad ? -1 : n.first + n.n;
+  }
+  const Pages &p = blockIdx.y ? a.pv : a.pk;
+  const Strides &s = blockIdx.y ? a.sv : a.sk;
+  const int chunks = (a.L + kChunk - 1) / kChunk, units = kChunk * a.Hkv << lane_bits;
+  for (long long c = blockIdx.x; c < f.B * chunks; c += gridDim.x) {
+    const long long b = c / chunks;
+    const int first = (int)(c % chunks) * kChunk;
+    const NewRows n = new_rows(a.t, b, f.Lq);
+    const int end = n.first + n.n;
+    if (first >= end) continue;
+    for (int x = threadIdx.x; x < units; x += kThreads) {
+      const int d0 = (x & ((1 << lane_bits) - 1)) * 8, r = x >> lane_bits, pos = first + r / a.Hkv, h = r % a.Hkv;
+      if (pos >= end || d0 >= a.D) continue;
+      const int page = page_of(a.t, b, pos), place = pos & ((1 << a.t.page_bits) - 1);
+      float v[8];
+      read8<PT, VEC>(p, page, place, h, d0, a.D, v);
+      if (DT == kF16 && PT == kE4M3)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = v[i] != v[i] ? v[i] : fminf(fmaxf(v[i], -65504.0f), 65504.0f);
+      store8<DT, VEC>(static_cast<E *>(blockIdx.y ? a.v : a.k) + b * s.b + pos * s.l + h * s.h + d0, a.D - d0, v);
+    }
+  }
 }
 
 // Whether 8 elements a lane can go as whole vectors.
@@ -190,6 +238,19 @@ template <int DT, int PT, bool READ> cudaError_t launch(const CacheArgs &a, cuda
   return cudaGetLastError();
 }
 
+template <int DT, int PT> cudaError_t gather(const GatherArgs &f, cudaStream_t stream) {
+  int lane_bits = 0;
+  while (8 << lane_bits < f.c.D) ++lane_bits;
+  const long long chunks = f.B * ((f.c.L + kChunk - 1) / kChunk), rows = (f.B * f.Lq + kThreads - 1) / kThreads;
+  const long long most = chunks > rows ? chunks : rows;
+  const dim3 grid((unsigned)(most < 8 * kSMs ? most : 8 * kSMs), 2);
+  if (vectors(f.c, DT, PT))
+    gather_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(f, lane_bits);
+  else
+    gather_kernel<DT, PT, false><<<grid, kThreads, 0, stream>>>(f, lane_bits);
+  return cudaGetLastError();
+}
+
 template <int DT> cudaError_t read_from(const CacheArgs &a, int cache_dtype, cudaStream_t s) {
   return cache_dtype == kE4M3  ? launch<DT, kE4M3, true>(a, s)
          : cache_dtype == kF32 ? launch<DT, kF32, true>(a, s)
@@ -200,8 +261,17 @@ template <int DT> cudaError_t write_to(const CacheArgs &a, int cache_dtype, cuda
   return cache_dtype == kE4M3 ? launch<DT, kE4M3, false>(a, s) : launch<DT, DT, false>(a, s);
 }
 
+template <int DT> cudaError_t gather_from(const GatherArgs &f, int cache_dtype, cudaStream_t s) {
+  return cache_dtype == kE4M3 ? gather<DT, kE4M3>(f, s) : gather<DT, DT>(f, s);
+}
+
 }  // namespace
 
+cudaError_t launch_gather(const GatherArgs &f, int dtype, int cache_dtype, cudaStream_t stream) {
+  return dtype == kF32   ? gather_from<kF32>(f, cache_dtype, stream)
+         : dtype == kF16 ? gather_from<kF16>(f, cache_dtype, stream)
+                         : gather_from<kBF16>(f, cache_dtype, stream);
+}
 cudaError_t launch_cache_write(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream) {
   return dtype == kF32   ? write_to<kF32>(a, cache_dtype, stream)
          : dtype == kF16 ? write_to<kF16>(a, cache_dtype, stream)

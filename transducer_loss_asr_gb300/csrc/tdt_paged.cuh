@@ -94,17 +94,25 @@ struct CacheArgs {
 };
 cudaError_t launch_cache_write(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
-// Few query rows: a kernel that reads k and v at memory speed.
-constexpr int kPagedStepRows = 32;  // rows of a key head at most
-bool paged_step_fits(const PagedArgs &a, int dtype, int cache_dtype);
+// Few query rows: a kernel that reads k and v at memory speed.  (It takes any number of rows; *_takes go by sizes and pages.)
+constexpr int kPagedStepRows = 32;  // rows of a key head up to which it is used
+bool paged_step_takes(const PagedArgs &a, int dtype, int cache_dtype);
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
-// Many query rows on the tensor cores: which calls (by type and width, then by strides and alignment), and the workspace for
-// up to `most` positions an utterance.
-bool paged_tc_takes(int dtype, int D);
-bool paged_tc_fits(const PagedArgs &a, int dtype, int cache_dtype);
-size_t paged_tc_workspace(long long B, long long Lq, long long most, int H, int Hkv, int D, int cache_dtype);
-cudaError_t launch_paged_tc(const PagedArgs &a, int dtype, int cache_dtype, void *workspace, cudaStream_t stream);
-// Attention on the CUDA cores: every other call.
-cudaError_t launch_paged_general(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
+// Many query rows on the tensor cores: which calls (paged_tc_fits: by q and out, too), and the workspace for up to `most`
+// positions an utterance.
+bool paged_tc_takes(const PagedArgs &a, int dtype);
+bool paged_tc_fits(const PagedArgs &a, int dtype);
+size_t paged_tc_workspace(long long B, long long Lq, long long most, int H, int Hkv, int D);
+cudaError_t launch_paged_tc(const PagedArgs &a, int dtype, void *workspace, cudaStream_t stream);
+
+// Every other call: the rows of whole utterances become dense tensors, for cross attention to read.
+struct GatherArgs {
+  CacheArgs c;        // k, v: [B, L, Hkv, D], L: the table's positions; rows and i are not used
+  long long B;
+  int Lq;
+  int2 *windows;      // [B, Lq]: the positions that each query sees
+  long long *lens;    // [B]: positions of an utterance, -1 where lengths are out of range
+};
+cudaError_t launch_gather(const GatherArgs &f, int dtype, int cache_dtype, cudaStream_t stream);
 
 }  // namespace tdt

@@ -117,6 +117,87 @@ int cache_call(CacheArgs *a, const int64_t sizes[3], const int64_t strides[6], i
   return fill_table(&a->t, c, table, table_stride, kv_lens, q_lens, sizes[2]);
 }
 
+// What the choice of kernels goes by: sizes and the cache.
+PagedArgs attn_args(const int64_t sizes[4], const tdt_paged_cache *c) {
+  PagedArgs a = {};
+  a.B = sizes[0];
+  a.Lq = (int)sizes[1];
+  a.H = (int)sizes[2];
+  a.Hkv = (int)c->n_heads;
+  a.G = a.H / a.Hkv;
+  a.D = (int)c->head_dim;
+  a.k = pages_of(c, false);
+  a.v = pages_of(c, true);
+  a.t.n_pages = (int)c->n_pages;
+  a.t.page_bits = page_bits_of(c->page_size);
+  a.t.max_pages = (int)sizes[3];
+  return a;
+}
+enum Way { kStep, kTensor, kGather };
+Way way_of(const PagedArgs &a, int dtype, int cache_dtype) {
+  const bool step = paged_step_takes(a, dtype, cache_dtype);
+  if (step && (long long)a.Lq * a.G <= kPagedStepRows) return kStep;
+  // the step kernel stands in where q or out does not suit TMA
+  return step && dtype == cache_dtype && paged_tc_takes(a, dtype) ? kTensor : kGather;
+}
+
+// Scratch of a call that gathers: dense k and v, windows, lengths, then cross attention's own.
+struct GatherSpace {
+  size_t k, v, windows, lens, rest, total;
+  int64_t sizes[6];  // of cross attention
+};
+GatherSpace gather_space(const int64_t sizes[4], int dtype, const tdt_paged_cache *c) {
+  GatherSpace s = {};
+  const int64_t L = sizes[3] * c->page_size;
+  const int64_t all[6] = {sizes[0], sizes[1], L, sizes[2], c->n_heads, c->head_dim};
+  std::copy(all, all + 6, s.sizes);
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  const size_t dense = (size_t)(sizes[0] * L) * (size_t)(c->n_heads * c->head_dim) * size_of(dtype);
+  s.k = take(dense);
+  s.v = take(dense);
+  s.windows = take((size_t)(sizes[0] * sizes[1]) * 8);
+  s.lens = take((size_t)sizes[0] * 8);
+  s.rest = at;
+  s.total = at + tdt_cross_attn_workspace_size(s.sizes, dtype, 0);
+  return s;
+}
+
+int attend_gathered(const PagedArgs &a, const int64_t sizes[4], const int64_t strides[6], int dtype,
+                    const tdt_paged_cache *c, void *workspace, size_t bytes, cudaStream_t stream) {
+  const GatherSpace at = gather_space(sizes, dtype, c);
+  char *ws = static_cast<char *>(workspace);
+  GatherArgs f = {};
+  const int64_t L = at.sizes[2], Hkv = c->n_heads, D = c->head_dim;
+  f.c.k = ws + at.k;
+  f.c.v = ws + at.v;
+  f.c.sk = f.c.sv = Strides{L * Hkv * D, Hkv * D, D};
+  f.c.pk = a.k;
+  f.c.pv = a.v;
+  f.c.t = a.t;
+  f.c.L = (int)L;
+  f.c.Hkv = (int)Hkv;
+  f.c.D = (int)D;
+  f.B = a.B;
+  f.Lq = a.Lq;
+  f.windows = reinterpret_cast<int2 *>(ws + at.windows);
+  f.lens = reinterpret_cast<long long *>(ws + at.lens);
+  if (launch_gather(f, dtype, c->dtype, stream) != cudaSuccess) return TDT_ERR_CUDA;
+  const int64_t dense[3] = {L * Hkv * D, Hkv * D, D};
+  int64_t all[12];
+  std::copy(strides, strides + 3, all);
+  std::copy(dense, dense + 3, all + 3);
+  std::copy(dense, dense + 3, all + 6);
+  std::copy(strides + 3, strides + 6, all + 9);
+  return tdt_cross_attn_fwd(a.q, f.c.k, f.c.v, at.sizes, all, dtype, reinterpret_cast<const int64_t *>(f.lens),
+                            reinterpret_cast<const int64_t *>(a.t.q_lens), reinterpret_cast<const int32_t *>(f.windows), a.scale, a.out, a.lse, ws + at.rest,
+                            bytes - at.rest, stream);
+}
+
 int check_attn(const int64_t sizes[4], int dtype, const tdt_paged_cache *c) {
   if (!sizes) return TDT_ERR_NULL_POINTER;
   int rc = check_cache(c, dtype, false);
@@ -167,9 +248,13 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
 
 size_t tdt_paged_attn_workspace_size(const int64_t sizes[4], int dtype, const tdt_paged_cache *cache) {
   using namespace tdt;
-  if (check_attn(sizes, dtype, cache) != TDT_OK || !paged_tc_takes(dtype, (int)cache->head_dim)) return 0;
-  return paged_tc_workspace(sizes[0], sizes[1], sizes[3] * cache->page_size, (int)sizes[2], (int)cache->n_heads,
-                            (int)cache->head_dim, cache->dtype);
+  if (check_attn(sizes, dtype, cache) != TDT_OK || sizes[0] == 0 || sizes[1] == 0) return 0;
+  const PagedArgs a = attn_args(sizes, cache);
+  const Way way = way_of(a, dtype, cache->dtype);
+  if (way == kStep) return 0;
+  if (way == kTensor)
+    return paged_tc_workspace(a.B, a.Lq, sizes[3] * cache->page_size, a.H, a.Hkv, a.D);
+  return gather_space(sizes, dtype, cache).total;
 }
 
 int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[6], int dtype,
@@ -184,18 +269,15 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
   if (!(f > 0.0f) || !isfinite(f)) return TDT_ERR_BAD_SCALE;
   for (int i = 0; i < 6; ++i)
     if (strides[i] < 0) return TDT_ERR_BAD_STRIDES;
-  PagedArgs a = {};
-  a.B = sizes[0];
-  a.Lq = (int)sizes[1];
-  a.H = (int)sizes[2];
-  a.Hkv = (int)cache->n_heads;
-  a.G = a.H / a.Hkv;
-  a.D = (int)cache->head_dim;
+  PagedArgs a = attn_args(sizes, cache);
   a.sq = strides_of(strides);
   a.so = strides_of(strides + 3);
-  a.k = pages_of(cache, false);
-  a.v = pages_of(cache, true);
   a.scale = f;
+  const Way way = way_of(a, dtype, cache->dtype);
+  if (way == kGather) {  // as cross attention asks of its sizes
+    const int64_t longest = std::max<int64_t>(a.Lq, sizes[3] * cache->page_size);
+    if (a.B * a.H >= ((int64_t)1 << 31) / std::max<int64_t>(1, (longest + 31) / 32)) return TDT_ERR_BAD_SIZES;
+  }
   const size_t need = tdt_paged_attn_workspace_size(sizes, dtype, cache);
   if (need > 0) {
     if (!workspace) return TDT_ERR_NULL_POINTER;
@@ -214,9 +296,9 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
   a.out = out;
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = paged_step_fits(a, dtype, cache->dtype) ? launch_paged_step(a, dtype, cache->dtype, s)
-                        : paged_tc_fits(a, dtype, cache->dtype) ? launch_paged_tc(a, dtype, cache->dtype, workspace, s)
-                                                                : launch_paged_general(a, dtype, cache->dtype, s);
+  if (way == kGather) return attend_gathered(a, sizes, strides, dtype, cache, workspace, workspace_bytes, s);
+  const cudaError_t e = way == kTensor && paged_tc_fits(a, dtype) ? launch_paged_tc(a, dtype, workspace, s)
+                                                                  : launch_paged_step(a, dtype, cache->dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 

@@ -36,6 +36,7 @@ struct StepArgs {
   PagedArgs a;
   int splits;  // CTAs of a cluster
   int groups;  // clusters that share the rows of a key head
+  int q_whole; // q's rows suit 8-byte loads
 };
 
 // d += a b, 16 x 8 x 16, float32 sums; F16: float16 operands, else bfloat16
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   const int split = blockIdx.x % f.splits, hk = unit % a.Hkv;
   const long long b = unit / a.Hkv;
   const NewRows n = new_rows(a.t, b, a.Lq);
-  const int row0 = cluster_id % f.groups * R;
+  const int row0 = cluster_id % f.groups * R;  // Lq * G < 2^31
   const int rows = min(R, a.Lq * a.G - row0);  // row r: query (row0 + r) / G, head hk * G + (row0 + r) % G
   const int used = min(n.n, (row0 + rows - 1) / a.G + 1);  // queries that take part, of those up to this group's last
   const int end = used > row0 / a.G ? n.first + used : 0;  // positions that some row sees
@@ -131,7 +132,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
     for (int x = 0; x < S::KSTEPS; ++x) {
       const int d = step_element<S::ES>(x, t);
       uint2 w = make_uint2(0, 0);
-      if (live && d < a.D) w = __ldg(reinterpret_cast<const uint2 *>(src + d));
+      if (live && d < a.D) {
+        if (f.q_whole) {
+          w = __ldg(reinterpret_cast<const uint2 *>(src + d));
+        } else {
+          const unsigned short *e = reinterpret_cast<const unsigned short *>(src + d);
+          w = make_uint2(e[0] | (unsigned)e[1] << 16, e[2] | (unsigned)e[3] << 16);
+        }
+      }
       q[x][h][0] = w.x;
       q[x][h][1] = w.y;
     }
@@ -515,33 +523,31 @@ template <int QT, int PT, int RT, int ALIGN> cudaError_t by_width(const StepArgs
   return f.a.D <= 64 ? launch<QT, PT, 64, RT, ALIGN>(f, s) : launch<QT, PT, 128, RT, ALIGN>(f, s);
 }
 template <int QT, int PT, int ALIGN> cudaError_t by_rows(const StepArgs &f, cudaStream_t s) {
-  return f.a.Lq * f.a.G <= 8 ? by_width<QT, PT, 1, ALIGN>(f, s) : by_width<QT, PT, 2, ALIGN>(f, s);
+  return (long long)f.a.Lq * f.a.G <= 8 ? by_width<QT, PT, 1, ALIGN>(f, s) : by_width<QT, PT, 2, ALIGN>(f, s);
 }
 
 // Bytes that every row of pages is aligned to: 16, 8 or less.
 int alignment(const PagedArgs &a, int es) {
   uintptr_t x = 0;
+  auto step = [&](long long n, long long stride) { return n > 1 ? (uintptr_t)(stride * es) : 0; };
   for (const Pages *p : {&a.k, &a.v})
-    x |= (uintptr_t)p->data | (uintptr_t)(p->s.b * es) | (uintptr_t)(p->s.l * es) | (uintptr_t)(p->s.h * es);
+    x |= (uintptr_t)p->data | step(a.t.n_pages, p->s.b) | step(1LL << a.t.page_bits, p->s.l) | step(a.Hkv, p->s.h);
   return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : 1;
 }
 
 }  // namespace
 
-bool paged_step_fits(const PagedArgs &a, int dtype, int cache_dtype) {
+bool paged_step_takes(const PagedArgs &a, int dtype, int cache_dtype) {
   const bool e8 = cache_dtype == kE4M3;
-  auto rows_fit = [&](const void *p, const Strides &s) {
-    return (uintptr_t)p % 8 == 0 && (a.B == 1 || s.b % 4 == 0) && (a.Lq == 1 || s.l % 4 == 0) && (a.H == 1 || s.h % 4 == 0);
-  };
-  return dtype != kF32 && a.D <= 128 && a.D % 8 == 0 && (long long)a.Lq * a.G <= kPagedStepRows && rows_fit(a.q, a.sq) &&
-         alignment(a, e8 ? 1 : 2) >= (e8 ? 8 : 16);
+  return dtype != kF32 && a.D <= 128 && a.D % 8 == 0 && alignment(a, e8 ? 1 : 2) >= (e8 ? 8 : 16);
 }
 
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream) {
   StepArgs f = {};
   f.a = a;
-  const int R = a.Lq * a.G <= 8 ? 8 : 16;
-  f.groups = (a.Lq * a.G + R - 1) / R;
+  f.q_whole = (uintptr_t)a.q % 8 == 0 && (a.B == 1 || a.sq.b % 4 == 0) && (a.Lq == 1 || a.sq.l % 4 == 0) && (a.H == 1 || a.sq.h % 4 == 0);
+  const int R = (long long)a.Lq * a.G <= 8 ? 8 : 16;
+  f.groups = (int)(((long long)a.Lq * a.G + R - 1) / R);
   // a cluster's CTAs: the split whose waves of CTAs take least, in turns of a warp (one CTA's start and end cost about
   // as much as three)
   const long long units = a.B * a.Hkv * f.groups, slots = (R == 8 ? 3 : 2) * kSMs;
