@@ -89,7 +89,7 @@ struct CacheArgs {
   Strides sk, sv;
   Pages pk, pv;
   PageTable t;
-  unsigned rows;  // B * L * Hkv
+  long long B;
   int L, Hkv, D;
 };
 cudaError_t launch_cache_write(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
@@ -107,8 +107,7 @@ cudaError_t launch_paged_tc(const PagedArgs &a, int dtype, void *workspace, cuda
 
 // Every other call: the rows of whole utterances become dense tensors, for cross attention to read.
 struct GatherArgs {
-  CacheArgs c;        // k, v: [B, L, Hkv, D], L: the table's positions; rows and i are not used
-  long long B;
+  CacheArgs c;        // k, v: [B, L, Hkv, D], L: the table's positions
   int Lq;
   int2 *windows;      // [B, Lq]: the positions that each query sees
   long long *lens;    // [B]: positions of an utterance, -1 where lengths are out of range

@@ -91,7 +91,7 @@ int check_rows(const int64_t *sizes, const tdt_paged_cache *c, int64_t heads, in
   const int64_t limit = (int64_t)1 << 30, B = sizes[0], L = sizes[1];
   if (B < 0 || L < 0 || B >= limit || L >= limit) return TDT_ERR_BAD_SIZES;
   if (max_pages < 0 || max_pages >= limit || max_pages * c->page_size >= limit) return TDT_ERR_BAD_PAGES;
-  // a row of 256 elements takes 32 threads of 256 at the most, a tile of 32 rows a block: grids have fewer than 2^31
+  // one block a row and head at the most: grids have fewer than 2^31
   if (L > 0 && B * L >= ((int64_t)1 << 31) / heads) return TDT_ERR_BAD_SIZES;
   return TDT_OK;
 }
@@ -112,8 +112,8 @@ int cache_call(CacheArgs *a, const int64_t sizes[3], const int64_t strides[6], i
   a->L = (int)sizes[1];
   a->Hkv = (int)c->n_heads;
   a->D = (int)c->head_dim;
-  a->rows = (unsigned)(sizes[0] * sizes[1] * c->n_heads);
-  if (a->rows == 0) return TDT_OK;
+  a->B = sizes[0];
+  if (a->B == 0 || a->L == 0) return TDT_OK;
   return fill_table(&a->t, c, table, table_stride, kv_lens, q_lens, sizes[2]);
 }
 
@@ -182,7 +182,7 @@ int attend_gathered(const PagedArgs &a, const int64_t sizes[4], const int64_t st
   f.c.L = (int)L;
   f.c.Hkv = (int)Hkv;
   f.c.D = (int)D;
-  f.B = a.B;
+  f.c.B = a.B;
   f.Lq = a.Lq;
   f.windows = reinterpret_cast<int2 *>(ws + at.windows);
   f.lens = reinterpret_cast<long long *>(ws + at.lens);
@@ -217,7 +217,7 @@ int tdt_cache_write(const void *k, const void *v, const int64_t sizes[3], const 
   using namespace tdt;
   CacheArgs a = {};
   int rc = cache_call(&a, sizes, strides, dtype, false, cache, page_table, table_stride, kv_lens, q_lens);
-  if (rc != TDT_OK || a.rows == 0) return rc;
+  if (rc != TDT_OK || a.B == 0 || a.L == 0) return rc;
   if (!k || !v) return TDT_ERR_NULL_POINTER;
   if (((uintptr_t)k | (uintptr_t)v) % size_of(dtype)) return TDT_ERR_BAD_ALIGNMENT;
   rc = check_cache_memory(cache, true);
@@ -234,7 +234,7 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
   using namespace tdt;
   CacheArgs a = {};
   int rc = cache_call(&a, sizes, strides, dtype, true, cache, page_table, table_stride, kv_lens, q_lens);
-  if (rc != TDT_OK || a.rows == 0) return rc;
+  if (rc != TDT_OK || a.B == 0 || a.L == 0) return rc;
   if (!k || !v) return TDT_ERR_NULL_POINTER;
   if (((uintptr_t)k | (uintptr_t)v) % size_of(dtype)) return TDT_ERR_BAD_ALIGNMENT;
   if (!apart(a.sk, sizes[0], a.L, a.Hkv, a.D) || !apart(a.sv, sizes[0], a.L, a.Hkv, a.D)) return TDT_ERR_BAD_STRIDES;
