@@ -8,20 +8,18 @@
 // the value, or 2^-10 2^e below 2^-6 2^e).
 // Bound by memory, or by latency for a decoding step; by instructions where a thread found its own row by divisions and had
 // 8 elements (16 ragged x 1024 rows of 4 heads of 128, bfloat16 to e4m3: 21 us).  So a block has whole positions of one
-// utterance, and a thread two pieces of 16 elements, whose page lookups, and then loads, are in flight together.
+// utterance, and a thread several pieces of 16 elements, whose page lookups, and then loads, are in flight together.
 //
 // The rows of whole utterances can also be laid out densely, for attention that reads no pages (launch_gather).
 #include <algorithm>
 
 #include "tdt_paged.cuh"
-#include "tdt_rowio.cuh"
 
 namespace tdt {
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPiece = 16;  // elements of a thread
-constexpr int U = 2;        // pieces of a thread in flight
 
 // A call's pieces.  The launch fills it in.
 struct Pieces {
@@ -32,71 +30,119 @@ struct Pieces {
   int div_s;
 };
 
-// 16 elements from `p`, those from `n` on as 0.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_piece(const typename Elem<DT>::T *p, int n, float (&x)[kPiece]) {
+// 16 elements of a type as they lie in memory, and how many pieces a thread holds.
+template <int T> struct Raw {
+  static constexpr int ES = T == kE4M3 ? 1 : T == kF32 ? 4 : 2;
+  static constexpr int W = kPiece * ES / 4;
+  static constexpr int U = ES == 1 ? 4 : ES == 2 ? 2 : 1;  // pieces of a thread in flight
+  unsigned w[W];
+  float up;  // e4m3: the row's power of two
+};
+// The first `n` elements from `p`, the others as 0.  VEC: n is a multiple of 8, p suits accesses of 16 bytes (8 for e4m3).
+template <int T, bool VEC> __device__ __forceinline__ void load_raw(const unsigned char *p, int n, Raw<T> &r) {
+  constexpr int ES = Raw<T>::ES;
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i) x[i] = 0.0f;
-  if (VEC) {  // D is a multiple of 8
-    constexpr int N = Vec<DT>::N;
+  for (int i = 0; i < Raw<T>::W; ++i) r.w[i] = 0;
+  if constexpr (VEC) {
+    constexpr int B = ES == 1 ? 8 : 16;  // bytes of an access
 #pragma unroll
-    for (int i = 0; i < kPiece; i += N)
-      if (i < n) unpack<DT>(ld_vec(p + i), x + i);
-    return;
+    for (int i = 0; i < kPiece * ES; i += B)
+      if (i < n * ES) {
+        if constexpr (B == 16) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p + i));
+          r.w[i / 4] = x.x;
+          r.w[i / 4 + 1] = x.y;
+          r.w[i / 4 + 2] = x.z;
+          r.w[i / 4 + 3] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p + i));
+          r.w[i / 4] = x.x;
+          r.w[i / 4 + 1] = x.y;
+        }
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+      if (i < n) {
+        if constexpr (ES == 1) r.w[i / 4] |= (unsigned)__ldg(p + i) << (i % 4 * 8);
+        if constexpr (ES == 2) r.w[i / 2] |= (unsigned)__ldg(reinterpret_cast<const unsigned short *>(p) + i) << (i % 2 * 16);
+        if constexpr (ES == 4) r.w[i] = __ldg(reinterpret_cast<const unsigned *>(p) + i);
+      }
   }
-#pragma unroll
-  for (int i = 0; i < kPiece; ++i)
-    if (i < n) x[i] = Elem<DT>::load(p + i);
 }
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_piece(typename Elem<DT>::T *p, int n, const float (&x)[kPiece]) {
-  if (VEC) {
-    constexpr int N = Vec<DT>::N;
+template <int T, bool VEC> __device__ __forceinline__ void store_raw(unsigned char *p, int n, const Raw<T> &r) {
+  constexpr int ES = Raw<T>::ES;
+  if constexpr (VEC) {
+    constexpr int B = ES == 1 ? 8 : 16;
 #pragma unroll
-    for (int i = 0; i < kPiece; i += N)
-      if (i < n) *reinterpret_cast<uint4 *>(p + i) = pack<DT>(x + i);
-    return;
+    for (int i = 0; i < kPiece * ES; i += B)
+      if (i < n * ES) {
+        if constexpr (B == 16)
+          *reinterpret_cast<uint4 *>(p + i) = make_uint4(r.w[i / 4], r.w[i / 4 + 1], r.w[i / 4 + 2], r.w[i / 4 + 3]);
+        else
+          *reinterpret_cast<uint2 *>(p + i) = make_uint2(r.w[i / 4], r.w[i / 4 + 1]);
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kPiece; ++i)
+      if (i < n) {
+        if constexpr (ES == 1) p[i] = (unsigned char)(r.w[i / 4] >> (i % 4 * 8));
+        if constexpr (ES == 2) reinterpret_cast<unsigned short *>(p)[i] = (unsigned short)(r.w[i / 2] >> (i % 2 * 16));
+        if constexpr (ES == 4) reinterpret_cast<unsigned *>(p)[i] = r.w[i];
+      }
   }
+}
+// Elements 2i and 2i + 1 as float32.
+template <int T> __device__ __forceinline__ float2 pair_of(const Raw<T> &r, int i) {
+  if constexpr (T == kE4M3) {
+    const float2 f = e4m3x2_to_float2(r.w[i / 2] >> (i % 2 * 16) & 0xffffu);
+    return make_float2(f.x * r.up, f.y * r.up);
+  }
+  if constexpr (T == kF32) return make_float2(__uint_as_float(r.w[2 * i]), __uint_as_float(r.w[2 * i + 1]));
+  if constexpr (T == kF16) return __half22float2(*reinterpret_cast<const __half2 *>(&r.w[i]));
+  return make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+}
+template <int T> __device__ __forceinline__ void set_pair(Raw<T> &r, int i, float2 v) {
+  if constexpr (T == kF32) {
+    r.w[2 * i] = __float_as_uint(v.x);
+    r.w[2 * i + 1] = __float_as_uint(v.y);
+  } else if constexpr (T == kF16) {
+    const __half2 h = __floats2half2_rn(v.x, v.y);
+    r.w[i] = *reinterpret_cast<const unsigned *>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
+    r.w[i] = *reinterpret_cast<const unsigned *>(&h);
+  }
+}
+// A piece of a page as a piece of type DT.  SATURATE: float16 ends at 65504.
+template <int DT, int PT, bool SATURATE> __device__ __forceinline__ void convert(const Raw<PT> &x, Raw<DT> &y) {
 #pragma unroll
-  for (int i = 0; i < kPiece; ++i)
-    if (i < n) p[i] = Elem<DT>::from_float(x[i]);
+  for (int i = 0; i < kPiece / 2; ++i) {
+    if constexpr (DT == PT && DT != kE4M3) {
+#pragma unroll
+      for (int k = 0; k < Raw<DT>::W / (kPiece / 2); ++k)
+        y.w[i * (Raw<DT>::W / (kPiece / 2)) + k] = x.w[i * (Raw<DT>::W / (kPiece / 2)) + k];
+    } else {
+      float2 v = pair_of<PT>(x, i);
+      if (SATURATE && DT == kF16) {  // NaN stays
+        v.x = v.x != v.x ? v.x : fminf(fmaxf(v.x, -65504.0f), 65504.0f);
+        v.y = v.y != v.y ? v.y : fminf(fmaxf(v.y, -65504.0f), 65504.0f);
+      }
+      set_pair<DT>(y, i, v);
+    }
+  }
+}
+template <int DT> __device__ __forceinline__ void fill(Raw<DT> &y, float v) {
+#pragma unroll
+  for (int i = 0; i < kPiece / 2; ++i) set_pair<DT>(y, i, make_float2(v, v));
 }
 
-// Elements [d0, d0 + 16) of a row of pages as float32, NaN if there is no such page.
+// Elements [d0, d0 + 16) of a row of pages; nothing is read if there is no such page.
 template <int PT, bool VEC>
-__device__ __forceinline__ void read_piece(const Pages &p, int page, int place, int h, int d0, int D, float (&v)[kPiece]) {
-  if (page < 0) {
-#pragma unroll
-    for (int i = 0; i < kPiece; ++i) v[i] = NAN;
-    return;
-  }
-  if constexpr (PT == kE4M3) {
-    const unsigned char *src = static_cast<const unsigned char *>(p.data) + row_at(p.s, page, place, h) + d0;
-    const float up = scale_of(__ldg(p.scales + row_at(p.ss, page, place, h)));
-    unsigned w[4] = {0, 0, 0, 0};
-    if (VEC) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (d0 + 8 * i < D) {
-          const uint2 two = __ldg(reinterpret_cast<const uint2 *>(src + 8 * i));
-          w[2 * i] = two.x;
-          w[2 * i + 1] = two.y;
-        }
-    } else {
-#pragma unroll
-      for (int i = 0; i < kPiece; ++i)
-        if (d0 + i < D) w[i / 4] |= (unsigned)__ldg(src + i) << (i % 4 * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kPiece / 2; ++i) {
-      const float2 f = e4m3x2_to_float2(w[i / 2] >> (i % 2 * 16) & 0xffffu);
-      v[2 * i] = f.x * up;
-      v[2 * i + 1] = f.y * up;
-    }
-  } else {
-    typedef typename Elem<PT>::T P;
-    load_piece<PT, VEC>(static_cast<const P *>(p.data) + row_at(p.s, page, place, h) + d0, D - d0, v);
-  }
+__device__ __forceinline__ void load_page(const Pages &p, int page, int place, int h, int d0, int D, Raw<PT> &r) {
+  const unsigned char *src = static_cast<const unsigned char *>(p.data) + (row_at(p.s, page, place, h) + d0) * Raw<PT>::ES;
+  load_raw<PT, VEC>(src, page < 0 ? 0 : D - d0, r);
+  if (PT == kE4M3) r.up = page < 0 ? 0.0f : scale_of(__ldg(p.scales + row_at(p.ss, page, place, h)));
 }
 
 // Piece x of a chunk: row i of it, head h, elements from d0.
@@ -115,7 +161,7 @@ __device__ __forceinline__ At piece_at(const Pieces &q, int x) {
 // blockIdx.y: keys or values.  PT: the pages' type, DT or kE4M3.
 template <int DT, int PT, bool VEC>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
-  typedef typename Elem<DT>::T E;
+  constexpr int U = Raw<DT>::U, ES = Raw<DT>::ES;
   const Pages &p = blockIdx.y ? a.pv : a.pk;
   const Strides &s = blockIdx.y ? a.sv : a.sk;
   const int chunks = (a.L + q.chunk - 1) / q.chunk, units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
@@ -124,50 +170,45 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     const int i0 = (int)(c - b * chunks) * q.chunk;
     const NewRows n = new_rows(a.t, b, a.L);
     if (i0 >= n.n) continue;
-    const E *src = static_cast<const E *>(blockIdx.y ? a.v : a.k) + b * s.b;
+    const unsigned char *src = static_cast<const unsigned char *>(blockIdx.y ? a.v : a.k);
     for (int x0 = 0; x0 < units; x0 += U * kThreads) {  // the whole block goes round: lanes share rows
       At at[U];
       int page[U];
-      float v[U][kPiece];
+      Raw<DT> v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int x = x0 + u * kThreads + threadIdx.x;
         at[u] = piece_at(q, x);
         at[u].i += i0;
-        page[u] = x < units && at[u].i < n.n ? page_of(a.t, b, n.first + at[u].i) : -1;
+        const bool in = x < units && at[u].i < n.n;
+        page[u] = in ? page_of(a.t, b, n.first + at[u].i) : -1;
+        load_raw<DT, VEC>(src + (b * s.b + at[u].i * s.l + at[u].h * s.h + at[u].d0) * ES, in ? a.D - at[u].d0 : 0, v[u]);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        load_piece<DT, VEC>(src + at[u].i * s.l + at[u].h * s.h + at[u].d0, page[u] < 0 ? 0 : a.D - at[u].d0, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int place = (n.first + at[u].i) & place_mask;
+        unsigned char *dst = static_cast<unsigned char *>(p.data) + (row_at(p.s, page[u], place, at[u].h) + at[u].d0) * Raw<PT>::ES;
         if constexpr (PT != kE4M3) {
-          if (page[u] >= 0)
-            store_piece<DT, VEC>(static_cast<E *>(p.data) + row_at(p.s, page[u], place, at[u].h) + at[u].d0, a.D - at[u].d0, v[u]);
+          if (page[u] >= 0) store_raw<PT, VEC>(dst, a.D - at[u].d0, v[u]);
         } else {
           unsigned top = 0;  // bits of the largest magnitude: a NaN's are above infinity's
 #pragma unroll
-          for (int i = 0; i < kPiece; ++i) top = max(top, __float_as_uint(v[u][i]) & 0x7fffffffu);
+          for (int i = 0; i < kPiece / 2; ++i) {
+            const float2 x = pair_of<DT>(v[u], i);
+            top = max(top, max(__float_as_uint(x.x) & 0x7fffffffu, __float_as_uint(x.y) & 0x7fffffffu));
+          }
           for (int o = 1; o < 1 << q.lane_bits; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
           if (page[u] < 0) continue;
           int e = (int)(top >> 23) - 127 - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
           e = min(max(e, kLeastExponent), kMostExponent);
           const float down = __uint_as_float((unsigned)(127 - e) << 23);
-          unsigned w[4] = {0, 0, 0, 0};
+          Raw<kE4M3> y;
 #pragma unroll
-          for (int i = 0; i < kPiece / 2; ++i)
-            w[i / 2] |= float2_to_e4m3x2(v[u][2 * i] * down, v[u][2 * i + 1] * down) << (i % 2 * 16);
-          unsigned char *dst = static_cast<unsigned char *>(p.data) + row_at(p.s, page[u], place, at[u].h) + at[u].d0;
-          if (VEC) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              if (at[u].d0 + 8 * i < a.D) *reinterpret_cast<uint2 *>(dst + 8 * i) = make_uint2(w[2 * i], w[2 * i + 1]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < kPiece; ++i)
-              if (at[u].d0 + i < a.D) dst[i] = (unsigned char)(w[i / 4] >> (i % 4 * 8));
+          for (int i = 0; i < 4; ++i) {
+            const float2 x0 = pair_of<DT>(v[u], 2 * i), x1 = pair_of<DT>(v[u], 2 * i + 1);
+            y.w[i] = float2_to_e4m3x2(x0.x * down, x0.y * down) | float2_to_e4m3x2(x1.x * down, x1.y * down) << 16;
           }
+          store_raw<kE4M3, VEC>(dst, a.D - at[u].d0, y);
           if (at[u].d0 == 0)
             p.scales[row_at(p.ss, page[u], place, at[u].h)] = (unsigned char)(top < 0x7f800000u ? e + kByteBias : kByteNaN);
         }
@@ -178,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 
 template <int DT, int PT, bool VEC>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
-  typedef typename Elem<DT>::T E;
+  constexpr int U = Raw<PT>::U;
   const Pages &p = blockIdx.y ? a.pv : a.pk;
   const Strides &s = blockIdx.y ? a.sv : a.sk;
   const int chunks = (a.L + q.chunk - 1) / q.chunk, units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
@@ -186,30 +227,31 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     const long long b = c / chunks;
     const int i0 = (int)(c - b * chunks) * q.chunk;
     const NewRows n = new_rows(a.t, b, a.L);
-    E *dst = static_cast<E *>(blockIdx.y ? a.v : a.k) + b * s.b;
+    unsigned char *dst = static_cast<unsigned char *>(blockIdx.y ? a.v : a.k);
     for (int x0 = threadIdx.x; x0 < units; x0 += U * kThreads) {
       At at[U];
       int page[U];
-      bool in[U];
-      float v[U][kPiece];
+      Raw<PT> v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int x = x0 + u * kThreads;
         at[u] = piece_at(q, x);
         at[u].i += i0;
-        in[u] = x < units && at[u].i < a.L && at[u].d0 < a.D;
-        page[u] = in[u] && at[u].i < n.n ? page_of(a.t, b, n.first + at[u].i) : -1;
+        if (x >= units || at[u].d0 >= a.D) at[u].i = a.L;
+        page[u] = at[u].i < n.n ? page_of(a.t, b, n.first + at[u].i) : -1;
       }
 #pragma unroll
       for (int u = 0; u < U; ++u)
-        read_piece<PT, VEC>(p, page[u], (n.first + at[u].i) & place_mask, at[u].h, at[u].d0, a.D, v[u]);
+        load_page<PT, VEC>(p, page[u], (n.first + at[u].i) & place_mask, at[u].h, at[u].d0, a.D, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!in[u]) continue;
-        if (at[u].i >= n.n && !n.bad)  // past the new rows
-#pragma unroll
-          for (int i = 0; i < kPiece; ++i) v[u][i] = 0.0f;
-        store_piece<DT, VEC>(dst + at[u].i * s.l + at[u].h * s.h + at[u].d0, a.D - at[u].d0, v[u]);
+        if (at[u].i >= a.L) continue;
+        Raw<DT> y;
+        if (page[u] >= 0)
+          convert<DT, PT, false>(v[u], y);
+        else  // past the new rows 0; NaN where there is no page, or lengths are bad
+          fill<DT>(y, n.bad || at[u].i < n.n ? NAN : 0.0f);
+        store_raw<DT, VEC>(dst + (b * s.b + at[u].i * s.l + at[u].h * s.h + at[u].d0) * Raw<DT>::ES, a.D - at[u].d0, y);
       }
     }
   }
@@ -220,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 // this call's are out of range.
 template <int DT, int PT, bool VEC>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs f, const __grid_constant__ Pieces q) {
-  typedef typename Elem<DT>::T E;
+  constexpr int U = Raw<PT>::U;
   const CacheArgs &a = f.c;
   for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < a.B * f.Lq && blockIdx.y == 0;
        x += (long long)gridDim.x * kThreads) {
@@ -239,29 +281,30 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
     const NewRows n = new_rows(a.t, b, f.Lq);
     const int end = n.first + n.n;
     if (i0 >= end) continue;
-    E *dst = static_cast<E *>(blockIdx.y ? a.v : a.k) + b * s.b;
+    unsigned char *dst = static_cast<unsigned char *>(blockIdx.y ? a.v : a.k);
     for (int x0 = threadIdx.x; x0 < units; x0 += U * kThreads) {
       At at[U];
       int page[U];
-      bool in[U];
-      float v[U][kPiece];
+      Raw<PT> v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int x = x0 + u * kThreads;
         at[u] = piece_at(q, x);
         at[u].i += i0;
-        in[u] = x < units && at[u].i < end && at[u].d0 < a.D;
-        page[u] = in[u] ? page_of(a.t, b, at[u].i) : -1;
+        if (x >= units || at[u].d0 >= a.D) at[u].i = end;
+        page[u] = at[u].i < end ? page_of(a.t, b, at[u].i) : -1;
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) read_piece<PT, VEC>(p, page[u], at[u].i & place_mask, at[u].h, at[u].d0, a.D, v[u]);
+      for (int u = 0; u < U; ++u) load_page<PT, VEC>(p, page[u], at[u].i & place_mask, at[u].h, at[u].d0, a.D, v[u]);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        if (!in[u]) continue;
-        if (DT == kF16 && PT == kE4M3)
-#pragma unroll
-          for (int i = 0; i < kPiece; ++i) v[u][i] = v[u][i] != v[u][i] ? v[u][i] : fminf(fmaxf(v[u][i], -65504.0f), 65504.0f);
-        store_piece<DT, VEC>(dst + at[u].i * s.l + at[u].h * s.h + at[u].d0, a.D - at[u].d0, v[u]);
+        if (at[u].i >= end) continue;
+        Raw<DT> y;
+        if (page[u] >= 0)
+          convert<DT, PT, PT == kE4M3>(v[u], y);
+        else
+          fill<DT>(y, NAN);
+        store_raw<DT, VEC>(dst + (b * s.b + at[u].i * s.l + at[u].h * s.h + at[u].d0) * Raw<DT>::ES, a.D - at[u].d0, y);
       }
     }
   }
@@ -278,11 +321,11 @@ bool vectors(const CacheArgs &a, int dtype, int cache_dtype) {
          fits(a.pv.data, a.pv.s, cache_dtype);
 }
 
-Pieces pieces_of(const CacheArgs &a) {
+Pieces pieces_of(const CacheArgs &a, int in_flight) {
   Pieces q = {};
   while (kPiece << q.lane_bits < a.D) ++q.lane_bits;
   q.unit = a.Hkv << q.lane_bits;
-  q.chunk = std::max(1, U * kThreads / q.unit);
+  q.chunk = std::max(1, in_flight * kThreads / q.unit);
   fast_div_setup(q.unit, &q.div_m, &q.div_s);
   return q;
 }
@@ -291,7 +334,7 @@ dim3 grid_of(long long rounds) { return dim3((unsigned)std::max<long long>(1, st
 long long rounds_of(const CacheArgs &a, const Pieces &q) { return a.B * ((a.L + q.chunk - 1) / q.chunk); }
 
 template <int DT, int PT> cudaError_t write(const CacheArgs &a, cudaStream_t stream) {
-  const Pieces q = pieces_of(a);
+  const Pieces q = pieces_of(a, Raw<DT>::U);
   const dim3 grid = grid_of(rounds_of(a, q));
   if (vectors(a, DT, PT))
     cache_write_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(a, q);
@@ -300,7 +343,7 @@ template <int DT, int PT> cudaError_t write(const CacheArgs &a, cudaStream_t str
   return cudaGetLastError();
 }
 template <int DT, int PT> cudaError_t read(const CacheArgs &a, cudaStream_t stream) {
-  const Pieces q = pieces_of(a);
+  const Pieces q = pieces_of(a, Raw<PT>::U);
   const dim3 grid = grid_of(rounds_of(a, q));
   if (vectors(a, DT, PT))
     cache_read_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(a, q);
@@ -309,7 +352,7 @@ template <int DT, int PT> cudaError_t read(const CacheArgs &a, cudaStream_t stre
   return cudaGetLastError();
 }
 template <int DT, int PT> cudaError_t gather(const GatherArgs &f, cudaStream_t stream) {
-  const Pieces q = pieces_of(f.c);
+  const Pieces q = pieces_of(f.c, Raw<PT>::U);
   const dim3 grid = grid_of(std::max(rounds_of(f.c, q), (f.c.B * f.Lq + kThreads - 1) / kThreads));
   if (vectors(f.c, DT, PT))
     gather_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(f, q);
