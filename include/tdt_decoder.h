@@ -256,7 +256,8 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
  *
  *   logits   device [N, V] of `dtype`, row n at logits + n * row stride,
  *            elements contiguous; rows need no alignment beyond the element's.
- *   sizes    {N, V, n_top}; N >= 0, 1 <= V <= 2^24, 0 <= n_top <= min(V, 64).
+ *   sizes    {N, V, n_top}; 0 <= N < 2^27, 1 <= V <= 2^24,
+ *            0 <= n_top <= min(V, 64).
  *   tokens   device int64 [N].  A negative one (the labels' padding of -100)
  *            leaves its row out: the row is not read and may hold anything;
  *            logprob, entropy and stats are 0, the alternatives -1 and -inf,

@@ -31,7 +31,7 @@ def _reference(x, tokens, n_top, a=None, b=None, c=None):
     x = x.double()
     m = x.amax(1, keepdim=True)
     z = x - m
-    zs = torch.where(z.isinf(), 0.0, z)
+    zs = torch.where(z < -1e4, 0.0, z)  # weight 0
     ez = e32 * zs.abs() * 3 + 2.0 ** -20                 # relative error of a weight
     w = torch.exp(z)
     s = w.sum(1, keepdim=True)
@@ -40,9 +40,9 @@ def _reference(x, tokens, n_top, a=None, b=None, c=None):
     ln_s = torch.log(s)
     e_ln = es + 2.0 ** -20 + 2 * e32 * ln_s.abs()        # log2's own error, and ln 2
     lp = z - ln_s
-    e_lp = e32 * 2 * (zs.abs() + ln_s) + e_ln
+    e_lp = e32 * 2 * (torch.where(z.isinf(), 0.0, z).abs() + ln_s) + e_ln
     p = w / s
-    plp = torch.where(p > 0, p * torch.where(lp.isinf(), 0.0, lp), 0.0)
+    plp = torch.where(p > 0, p * torch.where(lp < -1e4, 0.0, lp), 0.0)
     ent = -plp.sum(1)
     e_ent = (p * zs.abs() * (ez + es + sums)).sum(1) + e_ln[:, 0] + 4 * e32 * (ent + ln_s[:, 0])
     at = tokens[:, None]
@@ -55,7 +55,7 @@ def _reference(x, tokens, n_top, a=None, b=None, c=None):
         zero = torch.zeros(N, dtype=torch.float64, device=x.device)
         a, b = (zero if t is None else t.double() for t in (a, b))
         total = a if c is None else a + c.double().sum(1)
-        lpf = torch.where(lp.isinf(), 0.0, lp)
+        lpf = torch.where(lp < -1e4, 0.0, lp)
         d = -p * total[:, None] - b[:, None] * (plp + p * ent[:, None])
         d.scatter_add_(1, at, a[:, None])
         own = torch.zeros_like(d).scatter_add_(1, at, a.abs()[:, None])
@@ -220,6 +220,26 @@ def test_padding_tokens_out_of_range_and_masked_entries(binding, dtype, V):
         assert float(q.logprobs[6]) == -math.inf
 
 
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("V", [30, 700, 8193, 50257])
+def test_masks_of_the_types_lowest_value_and_few_allowed_tokens(binding, V, dtype):
+    """Most entries are -inf or the type's lowest number; fewer tokens than alternatives are allowed."""
+    N, K = 6, 20
+    x, tokens, a, b, g = _inputs(N, V, dtype, 11)
+    low = torch.finfo(dtype).min
+    few = torch.randint(0, V, (N, 7), generator=g, device="cuda")
+    mask = torch.ones(N, V, dtype=torch.bool, device="cuda").scatter_(1, few, False)
+    x[0] = torch.where(mask[0], -math.inf, x[0])
+    x[1] = torch.where(mask[1], low, x[1])
+    x[2] = torch.where(mask[2], torch.where(torch.arange(V, device="cuda") % 2 == 0, low, -math.inf).to(dtype), x[2])
+    x[3, :V // 2] = low            # what a thread sees first
+    x[4, :V // 2] = -math.inf
+    x[5] = torch.where(torch.arange(V, device="cuda") % 3 == 0, low, -math.inf).to(dtype)  # uniform over a third
+    tokens[:3], tokens[3:] = few[:3, 0], V - V % 3 - 3
+    x[3:5, V - V % 3 - 3] = 1.0
+    _check(binding, x, tokens, K, a, b, g)
+
+
 def test_missing_weights(binding):
     x, tokens, a, b, g = _inputs(5, 700, torch.float32, 3)
     r = binding.tdt_token_logprobs_fwd(x, tokens, 4)
@@ -258,8 +278,8 @@ def test_rows_past_32_bits(binding):
     y = base[:, -V:]
     y.copy_(x)
     r = binding.tdt_token_logprobs_fwd(y, tokens, 3)
-    want = binding.tdt_token_logprobs_fwd(x.contiguous(), tokens, 3)
-    assert all(torch.equal(p, q) for p, q in zip(r, want))
+    for name, w in _reference(x, tokens, 3).items():
+        _near(name, getattr(r, name), w)
     grad = binding.tdt_token_logprobs_bwd(x, tokens, r, a, b)
     binding.tdt_token_logprobs_bwd(y, tokens, r, a, b, grad_out=y)
     assert torch.equal(y, grad) and bool((base[:, :-V] == 0).all())

@@ -5,19 +5,36 @@
 //   logprob = z_t - ln s,   entropy = ln s - t / s,
 //   dx_i = -p_i (a + sum c + b (ln p_i + entropy)) + the given token's and the alternatives' own a and c_j,
 //   ln p_i = z_i - ln s.
-// An entry of -inf has p = 0; ln p is held above -1e4 in products with p, which is 0 there.
+// An entry of -inf has p = 0; its z is held above -200 (in base 2) in products with p, which is 0 there.
+//
+// Forward: one read of the row in 16-byte vectors (whatever the row's alignment: elements before the first and after the last
+// whole vector go one by one).  A thread holds its own maximum, s and t, rescaled where the maximum grows; they are joined in a
+// fixed order.  A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a
+// stretch of it each and exchange their results through distributed shared memory.
+// Alternatives, in the same read: once every thread has seen its first vectors, a threshold that at least n_top
+// elements reach comes from the threads' maxima (the ceil(n_top / warps)-th largest of each warp, the least of the warps); later
+// vectors whose maximum (which the sum needs anyway) is below it cost one comparison.  What reaches it is listed in shared memory, and
+// ranked by (value, index) at the end: the order in which the list fills does not matter.  A list that overflows (many
+// equal elements) is given up for n_top passes over the row.
+// Backward: a read and a write of the row; in one call with the forward pass, the second read finds the row in L2.
+#include <cooperative_groups.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "../../include/tdt_decoder.h"
-#include "tdt_common.cuh"
+#include "tdt_rowio.cuh"
 
 namespace tdt {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
+namespace cg = cooperative_groups;
+
+constexpr int kBlock = 256;
 constexpr int kMostTop = 64;
+constexpr int kMostCtas = 8;   // of a cluster
 constexpr float kLn2f = 0.69314718055994531f;
+constexpr float kLeastZ = -200.0f;  // in base 2: 2^-200 is 0
 
 struct RowArgs {
   const void *x;
@@ -33,6 +50,7 @@ struct RowArgs {
   const float *ga, *gb, *gc;
   unsigned N;
   int V, K;
+  int ctas;           // CTAs of a row
 };
 
 // max that keeps NaN
@@ -42,151 +60,442 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-template <typename F> __device__ float block_reduce(float v, float *part, F f) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = f(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
-#pragma unroll
-  for (int i = 1; i < kWarps; ++i) v = f(v, part[i]);
-  return v;
+// A stretch's maximum, sum of 2^((x - m) log2 e) and sum of those times (x - m) log2 e.
+struct Sums {
+  float m, s, t;
+};
+__device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
+  Sums r;
+  r.m = fmaxf(a.m, b.m);
+  const float ref = r.m == -INFINITY ? 0.0f : r.m;
+  // what holds nothing (m = -inf) has s = t = 0
+  const float da = a.m == -INFINITY ? 0.0f : (a.m - ref) * kLog2e, db = b.m == -INFINITY ? 0.0f : (b.m - ref) * kLog2e;
+  const float fa = fast_exp2(da), fb = fast_exp2(db);
+  r.s = a.s * fa + b.s * fb;
+  r.t = (a.t + max_nan(da, kLeastZ) * a.s) * fa + (b.t + max_nan(db, kLeastZ) * b.s) * fb;
+  return r;
 }
 
-template <int DT, bool FWD, bool BWD>
-__global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a) {
+// A group's (a warp's or a block's) shared memory.
+template <int T> struct GroupShared {
+  static constexpr int LIST = T == 32 ? 160 : 1024;
+  Sums sums[T / 32];
+  float least[T / 32];
+  float best[T / 32];      // of the passes that stand in for a list that overflows
+  int best_at[T / 32];
+  int count;
+  float value[LIST];
+  int index[LIST];
+  float top_value[kMostTop];  // the stretch's own alternatives, ranked
+  int top_index[kMostTop];
+  int top_n;
+  Sums row;                // of the stretch, for the cluster
+  float own_x[kMostTop + 1], own_add[kMostTop + 1];
+  int own_at[kMostTop + 1];
+};
+
+template <int T> __device__ __forceinline__ void group_sync() {
+  if (T == 32)
+    __syncwarp();
+  else
+    __syncthreads();
+}
+
+// The vectors [first, last) of 16 bytes that CTA `i` of `n` has of a row at p, and the elements before the first vector.
+struct Stretch {
+  int head, first, last, vectors;
+};
+template <int DT> __device__ __forceinline__ Stretch stretch_of(const void *p, int V, int i, int n) {
+  Stretch s;
+  s.head = min(head_elems<DT>(p), V);
+  s.vectors = (V - s.head) / Vec<DT>::N;
+  s.first = (int)((long long)s.vectors * i / n);
+  s.last = (int)((long long)s.vectors * (i + 1) / n);
+  return s;
+}
+
+template <int DT, bool FWD, bool BWD, int T>
+__global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ RowArgs a) {
   typedef typename Elem<DT>::T E;
-  __shared__ float part[kWarps];
-  __shared__ int best_at[kWarps];
-  const unsigned n = blockIdx.x;
+  constexpr int N = Vec<DT>::N, U = 4, WARPS = T / 32;
+  constexpr bool IN_PLACE = BWD;  // the logits may be written in this kernel
+  __shared__ GroupShared<T> shared[kBlock / T];
+  GroupShared<T> &sh = shared[threadIdx.x / T];
+  const int tid = threadIdx.x % T, lane = tid & 31, warp = tid >> 5;
+  const int ctas = T == 32 ? 1 : a.ctas, part = T == 32 ? 0 : blockIdx.x % ctas;
+  const unsigned n = T == 32 ? blockIdx.x * (kBlock / 32) + threadIdx.x / 32 : blockIdx.x / ctas;
+  if (n >= a.N) return;  // a whole warp (T = 32)
   const E *x = static_cast<const E *>(a.x) + n * a.sx;
   const long long token = a.tokens[n];
   const bool real = token >= 0 && token < a.V;
-  auto at = [&](int i) { return Elem<DT>::to_float(x[i]); };
+  auto at = [&](int i) { return ld_elem<DT, IN_PLACE>(x + i); };
   const int K = a.K;
   float m = 0.0f, ln_s = 0.0f, ent = 0.0f;
-  if (FWD) {
-    if (!real) {
-      const float none = token < 0 ? 0.0f : NAN;
-      if (threadIdx.x == 0) {
-        a.logprobs[n] = none;
-        if (a.entropy) a.entropy[n] = none;
-        if (a.stats) a.stats[n] = make_float2(none, none);
+  if (FWD && !real && part == 0) {
+    const float none = token < 0 ? 0.0f : NAN;
+    if (tid == 0) {
+      a.logprobs[n] = none;
+      if (a.entropy) a.entropy[n] = none;
+      if (a.stats) a.stats[n] = make_float2(none, none);
+    }
+    for (int k = tid; k < K; k += T) {
+      a.top_tokens[n * (long long)K + k] = -1;
+      a.top_logprobs[n * (long long)K + k] = token < 0 ? -INFINITY : NAN;
+    }
+  }
+  if (FWD && real) {
+    const Stretch w = stretch_of<DT>(x, a.V, part, ctas);
+    const E *body = x + w.head;
+    Sums r = {-INFINITY, 0.0f, 0.0f};
+    float neg = 0.0f;         // -m, of a finite m
+    float threshold = INFINITY;
+    auto note = [&](float v, int i) {
+      if (v >= threshold && v > -INFINITY) {
+        const int k = atomicAdd(&sh.count, 1);
+        if (k < GroupShared<T>::LIST) {
+          sh.value[k] = v;
+          sh.index[k] = i;
+        }
       }
-      for (int k = threadIdx.x; k < K; k += kThreads) {
-        a.top_tokens[n * (long long)K + k] = -1;
-        a.top_logprobs[n * (long long)K + k] = token < 0 ? -INFINITY : NAN;
+    };
+    auto grow = [&](float top) {
+      if (top > r.m) {
+        const float down = r.m == -INFINITY ? 0.0f : fmaxf((r.m - top) * kLog2e, kLeastZ), f = fast_exp2(down);
+        r.t = (r.t + down * r.s) * f;
+        r.s *= f;
+        r.m = top;
+        neg = -top;
       }
+    };
+    auto add = [&](float v) {
+      const float z = max_nan((v + neg) * kLog2e, kLeastZ), p = fast_exp2(z);
+      r.s += p;
+      r.t = fmaf(p, z, r.t);
+    };
+    auto vector_max = [&](const float (&v)[N]) {
+      float top = v[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+      return top;
+    };
+    uint4 raw[U];
+    auto load = [&](int v0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+    };
+    auto take = [&](int v0, bool listing) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * T < w.last) {
+          float v[N];
+          unpack<DT>(raw[u], v);
+          const float top = vector_max(v);
+          grow(top);
+#pragma unroll
+          for (int i = 0; i < N; ++i) add(v[i]);
+          if (listing && top >= threshold)
+#pragma unroll
+            for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
+        }
+    };
+    // the elements outside whole vectors belong to the first CTA, one a thread
+    const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
+    const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
+    int v0 = w.first + tid;
+    load(v0);
+    const float loose_x = loose_at >= 0 ? at(loose_at) : -INFINITY;
+    take(v0, false);
+    if (loose_at >= 0) {
+      grow(loose_x);
+      add(loose_x);
+    }
+    if (K > 0) {
+      // at least K elements reach the threshold: each warp has ceil(K / WARPS) maxima of its lanes that do
+      const int want = (K + WARPS - 1) / WARPS;
+      int ahead = 0;  // lanes with a larger maximum (equal ones: in order)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const float other = __shfl_sync(0xffffffffu, r.m, i);
+        ahead += other > r.m || (other == r.m && i < lane);
+      }
+      if (tid == 0) sh.count = 0;
+      if (ahead == want - 1) sh.least[warp] = r.m;  // want <= 32
+      group_sync<T>();
+      threshold = sh.least[0];
+#pragma unroll
+      for (int i = 1; i < WARPS; ++i) threshold = fminf(threshold, sh.least[i]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * T < w.last) {
+          float v[N];
+          unpack<DT>(raw[u], v);
+          if (vector_max(v) >= threshold)
+#pragma unroll
+            for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
+        }
+      if (loose_at >= 0) note(loose_x, loose_at);
+    }
+    for (v0 += U * T; v0 < w.last; v0 += U * T) {
+      load(v0);
+      take(v0, K > 0);
+    }
+    // threads, then warps, then CTAs
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      Sums other;
+      other.m = __shfl_xor_sync(0xffffffffu, r.m, o);
+      other.s = __shfl_xor_sync(0xffffffffu, r.s, o);
+      other.t = __shfl_xor_sync(0xffffffffu, r.t, o);
+      r = lane & o ? join(other, r) : join(r, other);
+    }
+    if (WARPS > 1) {
+      if (lane == 0) sh.sums[warp] = r;
+      __syncthreads();
+      r = sh.sums[0];
+#pragma unroll
+      for (int i = 1; i < WARPS; ++i) r = join(r, sh.sums[i]);
     } else {
-      m = -INFINITY;
-      for (int i = threadIdx.x; i < a.V; i += kThreads) m = max_nan(m, at(i));
-      m = block_reduce(m, part, max_nan);
-      float s = 0.0f, t = 0.0f;
-      for (int i = threadIdx.x; i < a.V; i += kThreads) {
-        const float z = at(i) - m, w = fast_exp2(z * kLog2e);
-        s += w;
-        t += w * max_nan(z, -1e4f);
+      __syncwarp();
+    }
+    if (K > 0) {
+      const int count = sh.count;
+      if (count <= GroupShared<T>::LIST) {
+        for (int i = tid; i < count; i += T) {
+          const float v = sh.value[i];
+          const int ix = sh.index[i];
+          int rank = 0;
+          for (int j = 0; j < count; ++j) rank += sh.value[j] > v || (sh.value[j] == v && sh.index[j] < ix);
+          if (rank < K) {
+            sh.top_value[rank] = v;
+            sh.top_index[rank] = ix;
+          }
+        }
+        if (tid == 0) sh.top_n = min(count, K);
+      } else {  // the stretch again, once an alternative
+        float last = INFINITY;
+        int last_at = -1, found = 0;
+        for (; found < K; ++found) {
+          float v = -INFINITY;
+          int v_at = a.V;
+          auto offer = [&](float y, int i) {
+            if ((y < last || (y == last && i > last_at)) && (y > v || (y == v && i < v_at && y > -INFINITY))) {
+              v = y;
+              v_at = i;
+            }
+          };
+          for (int q = w.first * N + tid; q < w.last * N; q += T) offer(at(w.head + q), w.head + q);
+          if (loose_at >= 0) offer(loose_x, loose_at);
+          for (int o = 16; o > 0; o >>= 1) {
+            const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
+            const int at2 = __shfl_xor_sync(0xffffffffu, v_at, o);
+            if (v2 > v || (v2 == v && at2 < v_at)) {
+              v = v2;
+              v_at = at2;
+            }
+          }
+          if (WARPS > 1) {
+            __syncthreads();
+            if (lane == 0) {
+              sh.best[warp] = v;
+              sh.best_at[warp] = v_at;
+            }
+            __syncthreads();
+            for (int i = 0; i < WARPS; ++i)
+              if (sh.best[i] > v || (sh.best[i] == v && sh.best_at[i] < v_at)) {
+                v = sh.best[i];
+                v_at = sh.best_at[i];
+              }
+          }
+          if (v_at == a.V) break;  // the same for all threads
+          if (tid == 0) {
+            sh.top_value[found] = v;
+            sh.top_index[found] = v_at;
+          }
+          last = v;
+          last_at = v_at;
+        }
+        if (tid == 0) sh.top_n = found;
       }
-      auto add = [](float p, float q) { return p + q; };
-      s = block_reduce(s, part, add);
-      t = block_reduce(t, part, add);
-      ln_s = log2f(s) * kLn2f;
-      ent = ln_s - t / s;
-      if (threadIdx.x == 0) {
+    }
+    if constexpr (T > 32) {
+      if (ctas > 1) {
+        if (tid == 0) sh.row = r;
+        cg::cluster_group cluster = cg::this_cluster();
+        cluster.sync();
+        r = *cluster.map_shared_rank(&sh.row, 0);
+        for (int i = 1; i < ctas; ++i) r = join(r, *cluster.map_shared_rank(&sh.row, i));
+      }
+    }
+    group_sync<T>();
+    const bool lost = !(r.s > 0.0f) || !(fabsf(r.m) < INFINITY);  // NaN, +inf, or nothing but -inf
+    m = lost ? NAN : r.m;
+    const float log2_s = log2f(r.s);
+    ln_s = lost ? NAN : log2_s * kLn2f;
+    ent = lost ? NAN : (log2_s - r.t / r.s) * kLn2f;
+    if (part == 0) {
+      if (tid == 0) {
         a.logprobs[n] = at((int)token) - m - ln_s;
         if (a.entropy) a.entropy[n] = ent;
         if (a.stats) a.stats[n] = make_float2(m, ln_s);
       }
-      float last = INFINITY;
-      int last_at = -1;
-      const bool lost = s != s;
-      for (int k = 0; k < K; ++k) {
-        float v = -INFINITY;
-        int v_at = a.V;
-        for (int i = threadIdx.x; i < a.V && !lost; i += kThreads) {
-          const float y = at(i);
-          const bool after = y < last || (y == last && i > last_at);
-          if (after && (y > v || v_at == a.V)) {
-            v = y;
-            v_at = i;
+      if (K > 0) {
+        int *to = a.top_tokens + n * (long long)K;
+        float *lp = a.top_logprobs + n * (long long)K;
+        int total = 0;
+        if (lost) {
+          for (int k = tid; k < K; k += T) {
+            to[k] = -1;
+            lp[k] = NAN;
+          }
+          total = K;
+        } else if (ctas == 1) {
+          total = sh.top_n;
+          for (int k = tid; k < total; k += T) {
+            to[k] = sh.top_index[k];
+            lp[k] = sh.top_value[k] - m - ln_s;
+          }
+        } else if constexpr (T > 32) {
+          // each CTA's list is ranked: an entry's rank is its own plus those of the others' before it
+          cg::cluster_group cluster = cg::this_cluster();
+          for (int i = 0; i < ctas; ++i) total += *cluster.map_shared_rank(&sh.top_n, i);
+          total = min(total, K);
+          for (int q = tid; q < ctas * K; q += T) {
+            const int i = q / K, k = q % K;
+            if (k >= *cluster.map_shared_rank(&sh.top_n, i)) continue;
+            const float v = *cluster.map_shared_rank(&sh.top_value[k], i);
+            const int ix = *cluster.map_shared_rank(&sh.top_index[k], i);
+            int rank = k;
+            for (int j = 0; j < ctas && rank < K; ++j) {
+              if (j == i) continue;
+              int lo = 0, hi = *cluster.map_shared_rank(&sh.top_n, j);
+              while (lo < hi) {  // entries of j before this one
+                const int mid = (lo + hi) / 2;
+                const float y = *cluster.map_shared_rank(&sh.top_value[mid], j);
+                const bool before = y > v || (y == v && *cluster.map_shared_rank(&sh.top_index[mid], j) < ix);
+                lo = before ? mid + 1 : lo;
+                hi = before ? hi : mid;
+              }
+              rank += lo;
+            }
+            if (rank < K) {
+              to[rank] = ix;
+              lp[rank] = v - m - ln_s;
+            }
           }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
-          const int at2 = __shfl_xor_sync(0xffffffffu, v_at, o);
-          if (at2 < a.V && (v_at == a.V || v2 > v || (v2 == v && at2 < v_at))) {
-            v = v2;
-            v_at = at2;
+        if (total < K && warp == 0) {  // tokens that are not allowed fill up, the lowest first
+          int k = total;
+          for (int base = 0; base < a.V && k < K; base += 32) {
+            const int i = base + lane;
+            const bool none = i < a.V && at(i) == -INFINITY;
+            const unsigned all = __ballot_sync(0xffffffffu, none);
+            const int mine = k + __popc(all & ((1u << lane) - 1));
+            if (none && mine < K) {
+              to[mine] = i;
+              lp[mine] = -INFINITY;
+            }
+            k += __popc(all);
           }
-        }
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-          part[threadIdx.x >> 5] = v;
-          best_at[threadIdx.x >> 5] = v_at;
-        }
-        __syncthreads();
-        v_at = a.V;
-        for (int w = 0; w < kWarps; ++w)
-          if (best_at[w] < a.V && (v_at == a.V || part[w] > v || (part[w] == v && best_at[w] < v_at))) {
-            v = part[w];
-            v_at = best_at[w];
-          }
-        last = v;
-        last_at = v_at;
-        if (threadIdx.x == 0) {
-          a.top_tokens[n * (long long)K + k] = lost ? -1 : v_at;
-          a.top_logprobs[n * (long long)K + k] = lost ? NAN : v - m - ln_s;
         }
       }
     }
   }
   if (BWD) {
     E *dx = static_cast<E *>(a.dx) + n * a.sdx;
+    const Stretch w = stretch_of<DT>(dx, a.V, part, ctas);
+    const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
+    const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
     if (!real) {
-      for (int i = threadIdx.x; i < a.V; i += kThreads) dx[i] = Elem<DT>::from_float(0.0f);
-      return;
-    }
-    __shared__ int own_at[kMostTop + 1];
-    __shared__ float own_add[kMostTop + 1], own_x[kMostTop + 1];
-    const float ga = a.ga ? a.ga[n] : 0.0f, gb = a.gb ? a.gb[n] : 0.0f;
-    const int kept = a.gc ? K : 0;
-    if (!FWD) {
-      const float2 st = a.in_stats[n];
-      m = st.x;
-      ln_s = st.y;
-      ent = a.gb ? a.in_entropy[n] : 0.0f;
-    }
-    for (int j = threadIdx.x; j <= kept; j += kThreads) {
-      const int i = j == kept ? (int)token : a.in_top[n * (long long)K + j];
-      const bool in = i >= 0 && i < a.V;
-      own_at[j] = in ? i : -1;
-      own_add[j] = j == kept ? ga : a.gc[n * (long long)K + j];
-      own_x[j] = in ? at(i) : 0.0f;
-    }
-    __syncthreads();
-    float all = 0.0f;
-    for (int j = 0; j <= kept; ++j) all += own_add[j];
-    auto slope = [&](float y) {
-      const float z = y - m, lp = z - ln_s;
-      const float p = fast_exp2(lp * kLog2e);
-      return -p * fmaf(gb, max_nan(lp, -1e4f) + ent, all);
-    };
-    for (int i = threadIdx.x; i < a.V; i += kThreads) dx[i] = Elem<DT>::from_float(slope(at(i)));
-    __syncthreads();
-    // tokens with a part of their own: each is written again by the first that names it
-    for (int j = threadIdx.x; j <= kept; j += kThreads) {
-      const int i = own_at[j];
-      bool first = i >= 0;
-      float add = 0.0f;
-      for (int q = 0; q <= kept; ++q)
-        if (own_at[q] == i) {
-          if (q < j) first = false;
-          add += own_add[q];
+      for (int v = w.first + tid; v < w.last; v += T)
+        *reinterpret_cast<uint4 *>(dx + w.head + (long long)v * N) = make_uint4(0, 0, 0, 0);
+      if (loose_at >= 0) dx[loose_at] = Elem<DT>::from_float(0.0f);
+    } else {
+      const float ga = a.ga ? a.ga[n] : 0.0f, gb = a.gb ? a.gb[n] : 0.0f;
+      const int kept = a.gc ? K : 0;
+      if (!FWD) {
+        const float2 st = a.in_stats[n];
+        m = st.x;
+        ln_s = st.y;
+        ent = a.gb ? a.in_entropy[n] : 0.0f;
+      }
+      // tokens with a part of their own that this CTA writes
+      auto mine = [&](int i) {
+        return i < w.head || i >= tail ? part == 0 : i >= w.head + w.first * N && i < w.head + w.last * N;
+      };
+      for (int j = tid; j <= kept; j += T) {
+        const int i = j == kept ? (int)token : a.in_top[n * (long long)K + j];
+        const bool in = i >= 0 && i < a.V;
+        sh.own_at[j] = in ? i : -1;
+        sh.own_add[j] = j == kept ? ga : a.gc[n * (long long)K + j];
+        sh.own_x[j] = in && mine(i) ? at(i) : 0.0f;
+      }
+      const float loose_x = loose_at >= 0 ? at(loose_at) : 0.0f;
+      if constexpr (FWD && T > 32) {
+        if (ctas > 1) cg::this_cluster().sync();  // every read of the row, and of other CTAs' results, is done
+      }
+      group_sync<T>();
+      float all = 0.0f;
+      for (int j = 0; j <= kept; ++j) all += sh.own_add[j];
+      // -p (all + gb (ln p + ent)), from log2 p
+      const float c0 = fmaf(gb, ent, all), c1 = gb * kLn2f, neg = -m, shift = -ln_s * kLog2e;
+      auto slope = [&](float y) {
+        const float lp = fmaf(y + neg, kLog2e, shift), p = fast_exp2(lp);
+        return -p * fmaf(c1, max_nan(lp, kLeastZ), c0);
+      };
+      const int mis = (int)((uintptr_t)(x + w.head) & 15);
+      auto finish = [&](uint4 raw, int v) {
+        float y[N];
+        unpack<DT>(raw, y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[i] = slope(y[i]);
+        *reinterpret_cast<uint4 *>(dx + w.head + (long long)v * N) = pack<DT>(y);
+      };
+      const E *body = x + w.head;
+      if (mis == 0) {
+        for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
+          uint4 raw[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * T < w.last) finish(raw[u], v0 + u * T);
         }
-      if (first) dx[i] = Elem<DT>::from_float(slope(own_x[j]) + add);
+      } else {
+        // The rows of logits and gradient lie differently to 16 bytes: a vector comes from two loads, each of
+        // which holds some of its bytes.
+        const unsigned char *low = reinterpret_cast<const unsigned char *>(body) - mis;
+        for (int v0 = w.first + tid; v0 < w.last; v0 += 2 * T) {
+          uint4 lo[2], hi[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (v0 + u * T < w.last) {
+              lo[u] = ld_row16_l1<IN_PLACE>(low + (long long)(v0 + u * T) * 16);
+              hi[u] = ld_row16_l1<IN_PLACE>(low + (long long)(v0 + u * T) * 16 + 16);
+            }
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            if (v0 + u * T < w.last) finish(funnel16(lo[u], hi[u], mis >> 2, (mis & 3) * 8), v0 + u * T);
+        }
+      }
+      if (loose_at >= 0) dx[loose_at] = Elem<DT>::from_float(slope(loose_x));
+      group_sync<T>();
+      // each token with a part of its own is written again by the first that names it
+      for (int j = tid; j <= kept; j += T) {
+        const int i = sh.own_at[j];
+        bool first = i >= 0 && mine(i);
+        float add = 0.0f;
+        for (int q = 0; q <= kept && first; ++q)
+          if (sh.own_at[q] == i) {
+            if (q < j) first = false;
+            add += sh.own_add[q];
+          }
+        if (first) dx[i] = Elem<DT>::from_float(slope(sh.own_x[j]) + add);
+      }
     }
+  } else if constexpr (FWD && T > 32) {
+    if (real && ctas > 1) cg::this_cluster().sync();  // nobody leaves while its results may be read
   }
 }
 
@@ -197,7 +506,7 @@ int check(const void *logits, const int64_t sizes[3], const int64_t *strides, bo
   if (!sizes || !strides) return TDT_ERR_NULL_POINTER;
   if (!known(dtype)) return TDT_ERR_BAD_DTYPE;
   const int64_t N = sizes[0], V = sizes[1], K = sizes[2];
-  if (N < 0 || N >= (int64_t)1 << 31 || V < 1 || V > 1 << 24) return TDT_ERR_BAD_SIZES;
+  if (N < 0 || N >= (int64_t)1 << 27 || V < 1 || V > 1 << 24) return TDT_ERR_BAD_SIZES;
   if (K < 0 || K > V || K > kMostTop) return TDT_ERR_BAD_TOP;
   if (strides[0] < 0 || (grad && strides[1] < V && N > 1)) return TDT_ERR_BAD_STRIDES;
   if (N == 0) return TDT_OK;
@@ -230,15 +539,34 @@ bool off4(std::initializer_list<const void *> ptrs) {
   return false;
 }
 
+template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
+  const long long bytes = (long long)a.V * (DT == kF32 ? 4 : 2);
+  if (bytes <= 2048 && a.K <= 32 && a.N >= 8) {  // a warp a row
+    rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  // CTAs of a row: while each has 64 KB or CTAs are too few for the SMs, and keeps 8 KB
+  a.ctas = 1;
+  while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > 65536 || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.N * (unsigned)a.ctas);
+  cfg.blockDim = dim3(kBlock);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = a.ctas;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = FWD && a.ctas > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<DT, FWD, BWD, kBlock>, a);
+}
 template <bool FWD, bool BWD> int launch(const RowArgs &a, int dtype, void *stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (dtype == kF32)
-    rows_kernel<kF32, FWD, BWD><<<a.N, kThreads, 0, s>>>(a);
-  else if (dtype == kF16)
-    rows_kernel<kF16, FWD, BWD><<<a.N, kThreads, 0, s>>>(a);
-  else
-    rows_kernel<kBF16, FWD, BWD><<<a.N, kThreads, 0, s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
+  const cudaError_t e = dtype == kF32   ? launch_rows<kF32, FWD, BWD>(a, s)
+                        : dtype == kF16 ? launch_rows<kF16, FWD, BWD>(a, s)
+                                        : launch_rows<kBF16, FWD, BWD>(a, s);
+  return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 
 int fill_outputs(RowArgs *a, float *logprobs, float *entropy, float *stats, int32_t *top_tokens,
