@@ -5,18 +5,21 @@
 //   logprob = z_t - ln s,   entropy = ln s - t / s,
 //   dx_i = -p_i (a + sum c + b (ln p_i + entropy)) + the given token's and the alternatives' own a and c_j,
 //   ln p_i = z_i - ln s.
-// An entry of -inf has p = 0; its z is held above -200 (in base 2) in products with p, which is 0 there.
+// An entry of -inf has p = 0; its logarithm is held above -200 (in base 2) in products with p, which is 0 there.
 //
 // Forward: one read of the row in 16-byte vectors (whatever the row's alignment: elements before the first and after the last
-// whole vector go one by one).  A thread holds its own maximum, s and t, rescaled where the maximum grows; they are joined in a
-// fixed order.  A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a
-// stretch of it each and exchange their results through distributed shared memory.
-// Alternatives, in the same read: once every thread has seen its first vectors, a threshold that at least n_top
-// elements reach comes from the threads' maxima (the ceil(n_top / warps)-th largest of each warp, the least of the warps); later
-// vectors whose maximum (which the sum needs anyway) is below it cost one comparison.  What reaches it is listed in shared memory, and
-// ranked by (value, index) at the end: the order in which the list fills does not matter.  A list that overflows (many
-// equal elements) is given up for n_top passes over the row.
-// Backward: a read and a write of the row; in one call with the forward pass, the second read finds the row in L2.
+// whole vector go one by one).  Arithmetic is in base 2 against a whole number R near the maximum,
+//   z_i = x_i L - R (one fma; L = log2 e in float32),   s = sum 2^z_i,   t = sum 2^z_i z_i,
+// so z is rounded once, at its own size, and what L is off by stays in differences to the maximum: m L - R is the same
+// product.  A thread holds its own R, s and t; R moves only where the maximum has grown by 8.  They are joined in a
+// fixed order.  Where that leaves no sum (a row of numbers at the ends of float32's range), x_i - m is formed instead.
+// A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
+// exchange their results through distributed shared memory.
+// Alternatives: at least n_top elements reach a threshold that comes from the threads' maxima (the ceil(n_top / warps)-th largest
+// of each warp, the least of the warps); only threads whose maximum reaches it, hardly more than n_top, look through their
+// elements again.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
+// fills does not matter.  A list that overflows (many equal elements) is given up for n_top passes over the row.
+// Backward: a read and a write of the row; in one call with the forward pass, the row waits in shared memory.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -24,6 +27,7 @@
 
 #include "../../include/tdt_decoder.h"
 #include "tdt_rowio.cuh"
+#include "tdt_tc.cuh"
 
 namespace tdt {
 namespace {
@@ -34,7 +38,8 @@ constexpr int kBlock = 256;
 constexpr int kMostTop = 64;
 constexpr int kMostCtas = 8;   // of a cluster
 constexpr float kLn2f = 0.69314718055994531f;
-constexpr float kLeastZ = -200.0f;  // in base 2: 2^-200 is 0
+constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
+constexpr float kLazy = 8.0f;
 
 struct RowArgs {
   const void *x;
@@ -51,6 +56,7 @@ struct RowArgs {
   unsigned N;
   int V, K;
   int ctas;           // CTAs of a row
+  int keep;           // the vectors of a stretch stay in dynamic shared memory for the backward pass
 };
 
 // max that keeps NaN
@@ -60,25 +66,24 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// A stretch's maximum, sum of 2^((x - m) log2 e) and sum of those times (x - m) log2 e.
+// A stretch's maximum m, reference R (a whole number), sum of 2^z and sum of 2^z z, z = x log2 e - R.  s = 0: nothing, whatever R.
 struct Sums {
-  float m, s, t;
+  float m, R, s, t;
 };
 __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
   Sums r;
   r.m = fmaxf(a.m, b.m);
-  const float ref = r.m == -INFINITY ? 0.0f : r.m;
-  // what holds nothing (m = -inf) has s = t = 0
-  const float da = a.m == -INFINITY ? 0.0f : (a.m - ref) * kLog2e, db = b.m == -INFINITY ? 0.0f : (b.m - ref) * kLog2e;
+  r.R = fmaxf(a.R, b.R);
+  const float da = fmaxf(a.R - r.R, kLeastZ), db = fmaxf(b.R - r.R, kLeastZ);
   const float fa = fast_exp2(da), fb = fast_exp2(db);
   r.s = a.s * fa + b.s * fb;
-  r.t = (a.t + max_nan(da, kLeastZ) * a.s) * fa + (b.t + max_nan(db, kLeastZ) * b.s) * fb;
+  r.t = fmaf(da, a.s, a.t) * fa + fmaf(db, b.s, b.t) * fb;
   return r;
 }
 
 // A group's (a warp's or a block's) shared memory.
 template <int T> struct GroupShared {
-  static constexpr int LIST = T == 32 ? 160 : 1024;
+  static constexpr int LIST = T == 32 ? 288 : 1024;
   Sums sums[T / 32];
   float least[T / 32];
   float best[T / 32];      // of the passes that stand in for a list that overflows
@@ -130,7 +135,10 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
   const bool real = token >= 0 && token < a.V;
   auto at = [&](int i) { return ld_elem<DT, IN_PLACE>(x + i); };
   const int K = a.K;
-  float m = 0.0f, ln_s = 0.0f, ent = 0.0f;
+  // of the whole row: log2 p_i = x_i L - R - log2_s; R infinite: (x_i - m) L - log2_s
+  float R = 0.0f, m = 0.0f, log2_s = 0.0f, ent = 0.0f;
+  auto log2_of = [&](float v) { return (R < INFINITY ? fmaf(v, kLog2e, -R) : (v - m) * kLog2e) - log2_s; };
+  extern __shared__ uint4 kept_row[];
   if (FWD && !real && part == 0) {
     const float none = token < 0 ? 0.0f : NAN;
     if (tid == 0) {
@@ -146,73 +154,69 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
   if (FWD && real) {
     const Stretch w = stretch_of<DT>(x, a.V, part, ctas);
     const E *body = x + w.head;
-    Sums r = {-INFINITY, 0.0f, 0.0f};
-    float neg = 0.0f;         // -m, of a finite m
-    float threshold = INFINITY;
-    auto note = [&](float v, int i) {
-      if (v >= threshold && v > -INFINITY) {
-        const int k = atomicAdd(&sh.count, 1);
-        if (k < GroupShared<T>::LIST) {
-          sh.value[k] = v;
-          sh.index[k] = i;
-        }
-      }
-    };
+    Sums r = {-INFINITY, -3e38f, 0.0f, 0.0f};
     auto grow = [&](float top) {
-      if (top > r.m) {
-        const float down = r.m == -INFINITY ? 0.0f : fmaxf((r.m - top) * kLog2e, kLeastZ), f = fast_exp2(down);
-        r.t = (r.t + down * r.s) * f;
+      r.m = fmaxf(r.m, top);
+      const float y = top * kLog2e;
+      if (y > r.R + kLazy) {
+        const float now = rintf(y), down = fmaxf(r.R - now, kLeastZ), f = fast_exp2(down);
+        r.t = fmaf(down, r.s, r.t) * f;
         r.s *= f;
-        r.m = top;
-        neg = -top;
+        r.R = now;
       }
     };
-    auto add = [&](float v) {
-      const float z = max_nan((v + neg) * kLog2e, kLeastZ), p = fast_exp2(z);
-      r.s += p;
-      r.t = fmaf(p, z, r.t);
+    const float2 L2 = make_float2(kLog2e, kLog2e);
+    auto add_vector = [&](const float (&v)[N]) {
+      const float2 neg = make_float2(-r.R, -r.R);
+      float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        float2 z = fma2(make_float2(v[i], v[i + 1]), L2, neg);
+        z.x = max_nan(z.x, kLeastZ);
+        z.y = max_nan(z.y, kLeastZ);
+        const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
+        s2 = add2(s2, p);
+        t2 = fma2(p, z, t2);
+      }
+      r.s += s2.x + s2.y;
+      r.t += t2.x + t2.y;
     };
     auto vector_max = [&](const float (&v)[N]) {
-      float top = v[0];
+      float top = fmaxf(v[0], v[1]);
 #pragma unroll
-      for (int i = 1; i < N; ++i) top = fmaxf(top, v[i]);
+      for (int i = 2; i < N; i += 2) top = max3(top, v[i], v[i + 1]);
       return top;
-    };
-    uint4 raw[U];
-    auto load = [&](int v0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
-    };
-    auto take = [&](int v0, bool listing) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + u * T < w.last) {
-          float v[N];
-          unpack<DT>(raw[u], v);
-          const float top = vector_max(v);
-          grow(top);
-#pragma unroll
-          for (int i = 0; i < N; ++i) add(v[i]);
-          if (listing && top >= threshold)
-#pragma unroll
-            for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
-        }
     };
     // the elements outside whole vectors belong to the first CTA, one a thread
     const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
     const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
-    int v0 = w.first + tid;
-    load(v0);
     const float loose_x = loose_at >= 0 ? at(loose_at) : -INFINITY;
-    take(v0, false);
+    const bool keep = BWD && T > 32 && a.keep;
+    for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
+      uint4 raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (v0 + u * T < w.last) {
+          if (keep) kept_row[v0 + u * T - w.first] = raw[u];
+          float v[N];
+          unpack<DT>(raw[u], v);
+          grow(vector_max(v));
+          add_vector(v);
+        }
+    }
     if (loose_at >= 0) {
       grow(loose_x);
-      add(loose_x);
+      const float z = max_nan(fmaf(loose_x, kLog2e, -r.R), kLeastZ), p = fast_exp2(z);
+      r.s += p;
+      r.t = fmaf(p, z, r.t);
     }
     if (K > 0) {
-      // at least K elements reach the threshold: each warp has ceil(K / WARPS) maxima of its lanes that do
-      const int want = (K + WARPS - 1) / WARPS;
+      // At least K elements reach the threshold: each warp all of whose lanes have vectors has ceil(K / such warps) lanes that
+      // do.  (Without such warps, or where they have too few lanes, a stretch is short, and everything is listed.)
+      const int full = min(WARPS, (w.last - w.first) / 32), want = full > 0 ? (K + full - 1) / full : 33;
       int ahead = 0;  // lanes with a larger maximum (equal ones: in order)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -220,31 +224,51 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
         ahead += other > r.m || (other == r.m && i < lane);
       }
       if (tid == 0) sh.count = 0;
-      if (ahead == want - 1) sh.least[warp] = r.m;  // want <= 32
+      if (warp >= full || want > 32) {
+        if (lane == 0) sh.least[warp] = want > 32 ? -INFINITY : INFINITY;
+      } else if (ahead == want - 1) {
+        sh.least[warp] = r.m;
+      }
       group_sync<T>();
-      threshold = sh.least[0];
+      float threshold = sh.least[0];
 #pragma unroll
       for (int i = 1; i < WARPS; ++i) threshold = fminf(threshold, sh.least[i]);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (v0 + u * T < w.last) {
-          float v[N];
-          unpack<DT>(raw[u], v);
-          if (vector_max(v) >= threshold)
-#pragma unroll
-            for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
+      auto note = [&](float v, int i) {
+        if (v >= threshold && v > -INFINITY) {
+          const int k = atomicAdd(&sh.count, 1);
+          if (k < GroupShared<T>::LIST) {
+            sh.value[k] = v;
+            sh.index[k] = i;
+          }
         }
-      if (loose_at >= 0) note(loose_x, loose_at);
-    }
-    for (v0 += U * T; v0 < w.last; v0 += U * T) {
-      load(v0);
-      take(v0, K > 0);
+      };
+      if (r.m >= threshold) {
+        for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
+          uint4 raw[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * T < w.last)
+              raw[u] = keep ? kept_row[v0 + u * T - w.first]
+                            : ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * T < w.last) {
+              float v[N];
+              unpack<DT>(raw[u], v);
+              if (vector_max(v) >= threshold)
+#pragma unroll
+                for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
+            }
+        }
+        if (loose_at >= 0) note(loose_x, loose_at);
+      }
     }
     // threads, then warps, then CTAs
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       Sums other;
       other.m = __shfl_xor_sync(0xffffffffu, r.m, o);
+      other.R = __shfl_xor_sync(0xffffffffu, r.R, o);
       other.s = __shfl_xor_sync(0xffffffffu, r.s, o);
       other.t = __shfl_xor_sync(0xffffffffu, r.t, o);
       r = lane & o ? join(other, r) : join(r, other);
@@ -328,16 +352,42 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       }
     }
     group_sync<T>();
-    const bool lost = !(r.s > 0.0f) || !(fabsf(r.m) < INFINITY);  // NaN, +inf, or nothing but -inf
-    m = lost ? NAN : r.m;
-    const float log2_s = log2f(r.s);
-    ln_s = lost ? NAN : log2_s * kLn2f;
+    if (!(r.s > 0.0f && r.s < INFINITY) && fabsf(r.m) < INFINITY) {
+      // NaN in the row, or numbers that a product with L takes out of range: against the maximum itself, by every CTA
+      r.s = r.t = 0.0f;
+      for (int i = tid; i < a.V; i += T) {
+        const float z = max_nan((at(i) - r.m) * kLog2e, kLeastZ), p = fast_exp2(z);
+        r.s += p;
+        r.t = fmaf(p, z, r.t);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        r.s += __shfl_xor_sync(0xffffffffu, r.s, o);
+        r.t += __shfl_xor_sync(0xffffffffu, r.t, o);
+      }
+      if (WARPS > 1) {
+        if (lane == 0) sh.sums[warp] = r;
+        __syncthreads();
+        r.s = r.t = 0.0f;
+        for (int i = 0; i < WARPS; ++i) {
+          r.s += sh.sums[i].s;
+          r.t += sh.sums[i].t;
+        }
+      }
+      r.R = INFINITY;  // what log2_of knows it by
+    }
+    const bool lost = !(r.s > 0.0f && r.s < INFINITY) || !(fabsf(r.m) < INFINITY);  // NaN, +inf, or nothing but -inf
+    log2_s = lost ? NAN : log2f(r.s);
     ent = lost ? NAN : (log2_s - r.t / r.s) * kLn2f;
+    R = r.R;
+    m = r.m;
+    const float ln_s = lost ? NAN : -log2_of(m) * kLn2f;
+    auto ln_of = [&](float v) { return v - m - ln_s; };  // finite wherever v is
     if (part == 0) {
       if (tid == 0) {
-        a.logprobs[n] = at((int)token) - m - ln_s;
+        a.logprobs[n] = ln_of(at((int)token));
         if (a.entropy) a.entropy[n] = ent;
-        if (a.stats) a.stats[n] = make_float2(m, ln_s);
+        if (a.stats) a.stats[n] = make_float2(lost ? NAN : m, ln_s);
       }
       if (K > 0) {
         int *to = a.top_tokens + n * (long long)K;
@@ -353,7 +403,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
           total = sh.top_n;
           for (int k = tid; k < total; k += T) {
             to[k] = sh.top_index[k];
-            lp[k] = sh.top_value[k] - m - ln_s;
+            lp[k] = ln_of(sh.top_value[k]);
           }
         } else if constexpr (T > 32) {
           // each CTA's list is ranked: an entry's rank is its own plus those of the others' before it
@@ -380,7 +430,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
             }
             if (rank < K) {
               to[rank] = ix;
-              lp[rank] = v - m - ln_s;
+              lp[rank] = ln_of(v);
             }
           }
         }
@@ -416,7 +466,9 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       if (!FWD) {
         const float2 st = a.in_stats[n];
         m = st.x;
-        ln_s = st.y;
+        R = rintf(m * kLog2e);
+        if (!(fabsf(R) < 3e38f)) R = INFINITY;
+        log2_s = st.y * kLog2e + (R < INFINITY ? fmaf(m, kLog2e, -R) : 0.0f);
         ent = a.gb ? a.in_entropy[n] : 0.0f;
       }
       // tokens with a part of their own that this CTA writes
@@ -438,21 +490,38 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       float all = 0.0f;
       for (int j = 0; j <= kept; ++j) all += sh.own_add[j];
       // -p (all + gb (ln p + ent)), from log2 p
-      const float c0 = fmaf(gb, ent, all), c1 = gb * kLn2f, neg = -m, shift = -ln_s * kLog2e;
+      const float c0 = -fmaf(gb, ent, all), c1 = -gb * kLn2f;
       auto slope = [&](float y) {
-        const float lp = fmaf(y + neg, kLog2e, shift), p = fast_exp2(lp);
-        return -p * fmaf(c1, max_nan(lp, kLeastZ), c0);
+        const float lp = log2_of(y);
+        return fast_exp2(lp) * fmaf(c1, max_nan(lp, kLeastZ), c0);
       };
       const int mis = (int)((uintptr_t)(x + w.head) & 15);
       auto finish = [&](uint4 raw, int v) {
         float y[N];
         unpack<DT>(raw, y);
+        if (R < INFINITY) {
+          const float2 L2 = make_float2(kLog2e, kLog2e), neg = make_float2(-R, -R), sum = make_float2(-log2_s, -log2_s);
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[i] = slope(y[i]);
+          for (int i = 0; i < N; i += 2) {
+            const float2 lp = add2(fma2(make_float2(y[i], y[i + 1]), L2, neg), sum);
+            const float2 p = make_float2(fast_exp2(lp.x), fast_exp2(lp.y));
+            float2 f = make_float2(c0, c0);
+            if (c1 != 0.0f)
+              f = fma2(make_float2(c1, c1), make_float2(max_nan(lp.x, kLeastZ), max_nan(lp.y, kLeastZ)), f);
+            f = mul2(p, f);
+            y[i] = f.x;
+            y[i + 1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i) y[i] = slope(y[i]);
+        }
         *reinterpret_cast<uint4 *>(dx + w.head + (long long)v * N) = pack<DT>(y);
       };
       const E *body = x + w.head;
-      if (mis == 0) {
+      if (FWD && T > 32 && a.keep && mis == 0) {  // the thread's own vectors: the stretches are the same
+        for (int v = w.first + tid; v < w.last; v += T) finish(kept_row[v - w.first], v);
+      } else if (mis == 0) {
         for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
           uint4 raw[U];
 #pragma unroll
@@ -545,12 +614,21 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
     rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, 0, s>>>(a);
     return cudaGetLastError();
   }
-  // CTAs of a row: while each has 64 KB or CTAs are too few for the SMs, and keeps 8 KB
+  // CTAs of a row: while each has over 64 KB (32 KB that wait in shared memory) or CTAs are too few for the SMs, and
+  // keeps 8 KB
+  const long long most = FWD && BWD ? 32768 : 65536;
   a.ctas = 1;
-  while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > 65536 || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
+  while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > most || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
+  const long long kept = (bytes / 16 / a.ctas + 1) * 16;
+  a.keep = FWD && BWD && kept <= 65536;
+  if (a.keep) {
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.N * (unsigned)a.ctas);
   cfg.blockDim = dim3(kBlock);
+  cfg.dynamicSmemBytes = a.keep ? (size_t)kept : 0;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
