@@ -16,8 +16,8 @@
 // A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
 // exchange their results through distributed shared memory.
 // Alternatives: at least n_top elements reach a threshold that comes from the threads' maxima (the ceil(n_top / warps)-th largest
-// of each warp, the least of the warps); only threads whose maximum reaches it, hardly more than n_top, look through their
-// elements again.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
+// of each warp, the least of the warps); only threads whose maximum reaches it, hardly more than n_top, look again, at the
+// batches of vectors whose maximum does.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
 // fills does not matter.  A list that overflows (many equal elements) is given up for n_top passes over the row.
 // Backward: a read and a write of the row; in one call with the forward pass, the row waits in shared memory.
 #include <cooperative_groups.h>
@@ -84,6 +84,8 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
 // A group's (a warp's or a block's) shared memory.
 template <int T> struct GroupShared {
   static constexpr int LIST = T == 32 ? 288 : 1024;
+  static constexpr int GROUPS = T == 32 ? 1 : 16;  // of a thread's batches of vectors
+  float group_max[GROUPS][T];
   Sums sums[T / 32];
   float least[T / 32];
   float best[T / 32];      // of the passes that stand in for a list that overflows
@@ -192,21 +194,44 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
     const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
     const float loose_x = loose_at >= 0 ? at(loose_at) : -INFINITY;
     const bool keep = BWD && T > 32 && a.keep;
-    for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
-      uint4 raw[U];
+    // U vectors at a time, the next ones in flight.  Of each group of these batches a thread notes its maximum.
+    constexpr int GROUPS = GroupShared<T>::GROUPS;
+    const int batches = (w.last - w.first + U * T - 1) / (U * T), per = (batches + GROUPS - 1) / GROUPS;  // batches of a group
+    float best = -INFINITY;
+    int group = 0, left = per;
+    auto load = [&](int v0, uint4 (&raw)[U]) {
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+    };
+    uint4 raw[U], next[U];
+    load(w.first + tid, raw);
+    for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
+      load(v0 + U * T, next);
+      float most = -INFINITY;
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * T < w.last) {
           if (keep) kept_row[v0 + u * T - w.first] = raw[u];
           float v[N];
           unpack<DT>(raw[u], v);
-          grow(vector_max(v));
+          const float top = vector_max(v);
+          grow(top);
           add_vector(v);
+          most = fmaxf(most, top);
         }
+      if (K > 0) {
+        best = fmaxf(best, most);
+        if (--left == 0) {
+          sh.group_max[group++][tid] = best;
+          best = -INFINITY;
+          left = per;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = next[u];
     }
+    if (K > 0 && group < GROUPS) sh.group_max[group++][tid] = best;  // each thread reads its own
     if (loose_at >= 0) {
       grow(loose_x);
       const float z = max_nan(fmaf(loose_x, kLog2e, -r.R), kLeastZ), p = fast_exp2(z);
@@ -243,13 +268,8 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
         }
       };
       if (r.m >= threshold) {
-        for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
-          uint4 raw[U];
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (v0 + u * T < w.last)
-              raw[u] = keep ? kept_row[v0 + u * T - w.first]
-                            : ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
+        auto look = [&](int v0) {
+          load(v0, raw);
 #pragma unroll
           for (int u = 0; u < U; ++u)
             if (v0 + u * T < w.last) {
@@ -259,7 +279,10 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
 #pragma unroll
                 for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
             }
-        }
+        };
+        for (int i = 0; i < group; ++i)
+          if (sh.group_max[i][tid] >= threshold)
+            for (int k = i * per; k < min((i + 1) * per, batches); ++k) look(w.first + tid + k * U * T);
         if (loose_at >= 0) note(loose_x, loose_at);
       }
     }
@@ -406,23 +429,29 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
             lp[k] = ln_of(sh.top_value[k]);
           }
         } else if constexpr (T > 32) {
-          // each CTA's list is ranked: an entry's rank is its own plus those of the others' before it
+          // each CTA's list is ranked; they come over together, and an entry's rank is its own plus those of the
+          // others' entries before it
           cg::cluster_group cluster = cg::this_cluster();
-          for (int i = 0; i < ctas; ++i) total += *cluster.map_shared_rank(&sh.top_n, i);
-          total = min(total, K);
+          __syncthreads();  // the list's memory is free
           for (int q = tid; q < ctas * K; q += T) {
             const int i = q / K, k = q % K;
-            if (k >= *cluster.map_shared_rank(&sh.top_n, i)) continue;
-            const float v = *cluster.map_shared_rank(&sh.top_value[k], i);
-            const int ix = *cluster.map_shared_rank(&sh.top_index[k], i);
-            int rank = k;
+            const bool in = k < *cluster.map_shared_rank(&sh.top_n, i);
+            sh.value[q] = in ? *cluster.map_shared_rank(&sh.top_value[k], i) : -INFINITY;
+            sh.index[q] = in ? *cluster.map_shared_rank(&sh.top_index[k], i) : -1;
+          }
+          __syncthreads();
+          for (int q = tid; q < ctas * K; q += T) {
+            const int i = q / K, ix = sh.index[q];
+            const float v = sh.value[q];
+            if (ix < 0) continue;
+            int rank = q % K;
             for (int j = 0; j < ctas && rank < K; ++j) {
               if (j == i) continue;
-              int lo = 0, hi = *cluster.map_shared_rank(&sh.top_n, j);
+              int lo = 0, hi = K;
               while (lo < hi) {  // entries of j before this one
-                const int mid = (lo + hi) / 2;
-                const float y = *cluster.map_shared_rank(&sh.top_value[mid], j);
-                const bool before = y > v || (y == v && *cluster.map_shared_rank(&sh.top_index[mid], j) < ix);
+                const int mid = (lo + hi) / 2, at2 = sh.index[j * K + mid];
+                const float y = sh.value[j * K + mid];
+                const bool before = at2 >= 0 && (y > v || (y == v && at2 < ix));
                 lo = before ? mid + 1 : lo;
                 hi = before ? hi : mid;
               }
@@ -433,6 +462,9 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
               lp[rank] = ln_of(v);
             }
           }
+          total = 0;
+          for (int base = 0; base < ctas * K; base += T) total += __syncthreads_count(base + tid < ctas * K && sh.index[base + tid] >= 0);
+          total = min(total, K);
         }
         if (total < K && warp == 0) {  // tokens that are not allowed fill up, the lowest first
           int k = total;
@@ -614,15 +646,15 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
     rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, 0, s>>>(a);
     return cudaGetLastError();
   }
-  // CTAs of a row: while each has over 64 KB (32 KB that wait in shared memory) or CTAs are too few for the SMs, and
+  // CTAs of a row: while each has over 256 KB (64 KB that wait in shared memory) or CTAs are too few for the SMs, and
   // keeps 8 KB
-  const long long most = FWD && BWD ? 32768 : 65536;
+  const long long most = FWD && BWD ? 65536 : 262144;
   a.ctas = 1;
   while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > most || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
   const long long kept = (bytes / 16 / a.ctas + 1) * 16;
-  a.keep = FWD && BWD && kept <= 65536;
+  a.keep = FWD && BWD && kept <= 65536 + 16;
   if (a.keep) {
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536 + 16);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
