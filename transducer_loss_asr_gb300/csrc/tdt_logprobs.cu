@@ -81,6 +81,17 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b) {
   return r;
 }
 
+// An element in the order of alternatives, the first the largest: by value (-0 equals 0), then by falling index.
+__device__ __forceinline__ unsigned long long key_of(float v, int i) {
+  const unsigned b = __float_as_uint(v + 0.0f);
+  return (unsigned long long)(b & 0x80000000u ? ~b : b | 0x80000000u) << 32 | (0xffffffffu - (unsigned)i);
+}
+__device__ __forceinline__ float value_of(unsigned long long key) {
+  const unsigned b = (unsigned)(key >> 32);
+  return __uint_as_float(b & 0x80000000u ? b & 0x7fffffffu : ~b);
+}
+__device__ __forceinline__ int index_of(unsigned long long key) { return (int)(0xffffffffu - (unsigned)key); }
+
 // A group's (a warp's or a block's) shared memory.
 template <int T> struct GroupShared {
   static constexpr int LIST = T == 32 ? 288 : 1024;
@@ -88,13 +99,10 @@ template <int T> struct GroupShared {
   float group_max[GROUPS][T];
   Sums sums[T / 32];
   float least[T / 32];
-  float best[T / 32];      // of the passes that stand in for a list that overflows
-  int best_at[T / 32];
+  unsigned long long best[T / 32];  // of the passes that stand in for a list that overflows
   int count;
-  float value[LIST];
-  int index[LIST];
-  float top_value[kMostTop];  // the stretch's own alternatives, ranked
-  int top_index[kMostTop];
+  unsigned long long list[LIST];
+  unsigned long long top[kMostTop];  // the stretch's own alternatives, ranked
   int top_n;
   Sums row;                // of the stretch, for the cluster
   float own_x[kMostTop + 1], own_add[kMostTop + 1];
@@ -261,10 +269,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       auto note = [&](float v, int i) {
         if (v >= threshold && v > -INFINITY) {
           const int k = atomicAdd(&sh.count, 1);
-          if (k < GroupShared<T>::LIST) {
-            sh.value[k] = v;
-            sh.index[k] = i;
-          }
+          if (k < GroupShared<T>::LIST) sh.list[k] = key_of(v, i);
         }
       };
       if (r.m >= threshold) {
@@ -309,58 +314,38 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       const int count = sh.count;
       if (count <= GroupShared<T>::LIST) {
         for (int i = tid; i < count; i += T) {
-          const float v = sh.value[i];
-          const int ix = sh.index[i];
+          const unsigned long long mine = sh.list[i];
           int rank = 0;
-          for (int j = 0; j < count; ++j) rank += sh.value[j] > v || (sh.value[j] == v && sh.index[j] < ix);
-          if (rank < K) {
-            sh.top_value[rank] = v;
-            sh.top_index[rank] = ix;
-          }
+#pragma unroll 4
+          for (int j = 0; j < count; ++j) rank += sh.list[j] > mine;
+          if (rank < K) sh.top[rank] = mine;
         }
         if (tid == 0) sh.top_n = min(count, K);
       } else {  // the stretch again, once an alternative
-        float last = INFINITY;
-        int last_at = -1, found = 0;
+        unsigned long long last = ~0ull;
+        int found = 0;
         for (; found < K; ++found) {
-          float v = -INFINITY;
-          int v_at = a.V;
-          auto offer = [&](float y, int i) {
-            if ((y < last || (y == last && i > last_at)) && (y > v || (y == v && i < v_at && y > -INFINITY))) {
-              v = y;
-              v_at = i;
-            }
+          unsigned long long most = 0;  // of what comes after the last one
+          auto offer = [&](float v, int i) {
+            const unsigned long long key = key_of(v, i);
+            if (v > -INFINITY && key < last && key > most) most = key;
           };
           for (int q = w.first * N + tid; q < w.last * N; q += T) offer(at(w.head + q), w.head + q);
           if (loose_at >= 0) offer(loose_x, loose_at);
+#pragma unroll
           for (int o = 16; o > 0; o >>= 1) {
-            const float v2 = __shfl_xor_sync(0xffffffffu, v, o);
-            const int at2 = __shfl_xor_sync(0xffffffffu, v_at, o);
-            if (v2 > v || (v2 == v && at2 < v_at)) {
-              v = v2;
-              v_at = at2;
-            }
+            const unsigned long long other = __shfl_xor_sync(0xffffffffu, most, o);
+            most = other > most ? other : most;
           }
           if (WARPS > 1) {
             __syncthreads();
-            if (lane == 0) {
-              sh.best[warp] = v;
-              sh.best_at[warp] = v_at;
-            }
+            if (lane == 0) sh.best[warp] = most;
             __syncthreads();
-            for (int i = 0; i < WARPS; ++i)
-              if (sh.best[i] > v || (sh.best[i] == v && sh.best_at[i] < v_at)) {
-                v = sh.best[i];
-                v_at = sh.best_at[i];
-              }
+            for (int i = 0; i < WARPS; ++i) most = sh.best[i] > most ? sh.best[i] : most;
           }
-          if (v_at == a.V) break;  // the same for all threads
-          if (tid == 0) {
-            sh.top_value[found] = v;
-            sh.top_index[found] = v_at;
-          }
-          last = v;
-          last_at = v_at;
+          if (most == 0) break;  // the same for all threads
+          if (tid == 0) sh.top[found] = most;
+          last = most;
         }
         if (tid == 0) sh.top_n = found;
       }
@@ -425,8 +410,8 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
         } else if (ctas == 1) {
           total = sh.top_n;
           for (int k = tid; k < total; k += T) {
-            to[k] = sh.top_index[k];
-            lp[k] = ln_of(sh.top_value[k]);
+            to[k] = index_of(sh.top[k]);
+            lp[k] = ln_of(value_of(sh.top[k]));
           }
         } else if constexpr (T > 32) {
           // each CTA's list is ranked; they come over together, and an entry's rank is its own plus those of the
@@ -435,35 +420,30 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
           __syncthreads();  // the list's memory is free
           for (int q = tid; q < ctas * K; q += T) {
             const int i = q / K, k = q % K;
-            const bool in = k < *cluster.map_shared_rank(&sh.top_n, i);
-            sh.value[q] = in ? *cluster.map_shared_rank(&sh.top_value[k], i) : -INFINITY;
-            sh.index[q] = in ? *cluster.map_shared_rank(&sh.top_index[k], i) : -1;
+            sh.list[q] = k < *cluster.map_shared_rank(&sh.top_n, i) ? *cluster.map_shared_rank(&sh.top[k], i) : 0;
           }
           __syncthreads();
-          for (int q = tid; q < ctas * K; q += T) {
-            const int i = q / K, ix = sh.index[q];
-            const float v = sh.value[q];
-            if (ix < 0) continue;
+          for (int base = 0; base < ctas * K; base += T) {
+            const int q = base + tid;
+            const unsigned long long mine = q < ctas * K ? sh.list[q] : 0;
+            total += __syncthreads_count(mine != 0);
             int rank = q % K;
-            for (int j = 0; j < ctas && rank < K; ++j) {
-              if (j == i) continue;
+            for (int j = 0; j < ctas && mine != 0 && rank < K; ++j) {
+              if (j == q / K) continue;
               int lo = 0, hi = K;
               while (lo < hi) {  // entries of j before this one
-                const int mid = (lo + hi) / 2, at2 = sh.index[j * K + mid];
-                const float y = sh.value[j * K + mid];
-                const bool before = at2 >= 0 && (y > v || (y == v && at2 < ix));
+                const int mid = (lo + hi) / 2;
+                const bool before = sh.list[j * K + mid] > mine;
                 lo = before ? mid + 1 : lo;
                 hi = before ? hi : mid;
               }
               rank += lo;
             }
-            if (rank < K) {
-              to[rank] = ix;
-              lp[rank] = ln_of(v);
+            if (mine != 0 && rank < K) {
+              to[rank] = index_of(mine);
+              lp[rank] = ln_of(value_of(mine));
             }
           }
-          total = 0;
-          for (int base = 0; base < ctas * K; base += T) total += __syncthreads_count(base + tid < ctas * K && sh.index[base + tid] >= 0);
           total = min(total, K);
         }
         if (total < K && warp == 0) {  // tokens that are not allowed fill up, the lowest first
@@ -642,7 +622,7 @@ bool off4(std::initializer_list<const void *> ptrs) {
 
 template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
   const long long bytes = (long long)a.V * (DT == kF32 ? 4 : 2);
-  if (bytes <= 2048 && a.K <= 32 && a.N >= 8) {  // a warp a row
+  if (bytes <= 2048 && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 51)
     rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, 0, s>>>(a);
     return cudaGetLastError();
   }
