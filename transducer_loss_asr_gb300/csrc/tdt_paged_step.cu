@@ -190,12 +190,14 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
 #pragma unroll
       for (int z = 0; z < S::VB / 4; ++z) vx[j / 4][j % 4][i][z] = 0;
   unsigned bytes = 0;  // e4m3: this lane's position's bytes of k and v
-  int id = 0;          // page of this lane's position (of KT)
+  int id = -1;         // page of this lane's position (of KT) in the turn that is loaded next
   const int place_mask = (1 << a.t.page_bits) - 1;
-  auto lookup = [&](int base) {
-    const int pos = base + lane % S::KT;
-    id = pos < end ? page_of(a.t, b, pos) : -1;
-    bad |= pos < end && id < 0;
+  auto lookup = [&](int x) {  // of turn x
+    const int pos = x * S::KT + lane % S::KT;
+    if (pos >= end) return -1;
+    const int page = page_of(a.t, b, pos);
+    bad |= page < 0;
+    return page;
   };
   // Most turns lie within a page and before the end: their rows are a lane's own offset and whole strides apart, and
   // nothing is left out.  (Loads that D leaves out, in either way, leave their registers 0.)
@@ -288,8 +290,9 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
 
   const int turns = (end + S::KT - 1) / S::KT, step = f.splits * kWarps;
   int turn = split * kWarps + warp;
+  id = lookup(turn);
+  int ahead = lookup(turn + step);  // pages are looked up two turns ahead, rows loaded one ahead
   if (turn < turns) {
-    lookup(turn * S::KT);
     load_keys(turn * S::KT);
     load_bytes(turn * S::KT);
     load_values(turn * S::KT);
@@ -297,6 +300,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   for (; turn < turns; turn += step) {
     const int base = turn * S::KT, next = (turn + step) * S::KT;
     const bool more = turn + step < turns;
+    id = ahead;
+    ahead = lookup(turn + 2 * step);
     // scores: rows g, g + 8; keys 8 j + 2 t, + 1
     float s[S::NT][4];
 #pragma unroll
@@ -334,7 +339,6 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
       __syncwarp();
     }
     if (more) {
-      lookup(next);
       load_keys(next);
       load_bytes(next);
     }
