@@ -2,11 +2,11 @@
 // tokens): float16 and bfloat16 queries over pages of their own type or of e4m3, heads up to 128.
 //
 // With R = Lq * G rows a key head (G query heads share it), the work is to read k and v once.  A warp multiplies tiles of
-// 16 keys straight from the registers that its loads fill, by mma.sync m16n8k16, which adds over the lanes by itself: about
+// 16 keys in the pieces that its lanes load, by mma.sync m16n8k16, which adds over the lanes by itself: about
 // 1.5 instructions a lane and element of 8 bits, where products on the CUDA cores take 4 R / 2 and the exchange of partial
 // scores.  (A tcgen05 product has 128 rows; its operands would have to go through shared memory first.)
-//   S = Q K^T     A = q, in registers for the whole walk; B = k: lane (g, t) holds key g of 8 and a quarter of its elements.
-//                 A contraction may take its elements in any order, so a lane's quarter is what its 16-byte loads bring.
+//   S = Q K^T     A = q, in registers for the whole walk; B = k: lane (g, t) has key g of 8 and a quarter of its elements.
+//                 A contraction may take its elements in any order, so a lane's quarter is what its 16-byte copies bring.
 //   O^T = V^T P^T A = v: lane (g, t) holds keys 2t, 2t+1, 2t+8, 2t+9 and an eighth of their elements, two keys to a register by a
 //                 byte permutation; B = p: exactly what S leaves in the lane (query g, keys 2t, 2t+1).
 // Rows 8 to 15 of A and a second B take up to 16 query rows; more rows: more CTAs, which mostly find k and v in L2.
@@ -15,8 +15,9 @@
 // multiplies its scores and a value row's its weight, relative to the largest so far (E); sums stay in float32.
 // The reference m of a row moves only when its maximum has grown by 8 (in base 2), so O is rescaled rarely.
 //
-// A cluster of S CTAs has one (utterance, key head, group of rows); its warps take the keys in turns.  Loads of the next turn
-// are in flight while one is at work.  Warps and then CTAs (over distributed shared memory) are joined in a fixed order.
+// A cluster of S CTAs has one (utterance, key head, group of rows); its warps take the keys in turns.  Each warp has 16 KB of
+// shared memory for turns in flight, which TMA fills, a box a page, swizzled so that the lanes' pieces lie in different banks.
+// Warps and then CTAs (over distributed shared memory) are joined in a fixed order.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -37,6 +38,7 @@ struct StepArgs {
   int splits;  // CTAs of a cluster
   int groups;  // clusters that share the rows of a key head
   int q_whole; // q's rows suit 8-byte loads
+  int k_p, k_h, v_p, v_h;  // 0 for repeated axes
 };
 
 // d += a b, 16 x 8 x 16, float32 sums; F16: float16 operands, else bfloat16
@@ -54,19 +56,6 @@ __device__ __forceinline__ void mma16(float (&d)[4], const unsigned (&a)[4], uns
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// BYTES contiguous bytes of global memory that is read once, in accesses of at most ALIGN.
-template <int BYTES, int ALIGN> __device__ __forceinline__ void load_words(unsigned (&w)[BYTES / 4], const unsigned char *p) {
-  if (ALIGN >= 16 && BYTES == 16) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[BYTES / 4 - 2]), "=r"(w[BYTES / 4 - 1])
-                 : "l"(p));
-  } else {
-#pragma unroll
-    for (int i = 0; i < BYTES / 8; ++i)
-      asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w[2 * i]), "=r"(w[2 * i + 1]) : "l"(p + 8 * i));
-  }
-}
-
 template <int QT, int PT, int DP, int RT> struct Shape {
   static constexpr bool E8 = PT == kE4M3;
   static constexpr bool F16 = E8 || PT == kF16;      // the products' type
@@ -78,7 +67,13 @@ template <int QT, int PT, int DP, int RT> struct Shape {
   static constexpr int VL = DP * ES / 8 / VB;
   static constexpr int KSTEPS = DP / 16;
   static constexpr int MTILES = DP / 16;
-  static constexpr int CTAS = RT == 1 ? 3 : 2;       // of an SM: 168 or 255 registers a thread
+  static constexpr int ROW = DP * ES < 128 ? DP * ES : 128;  // bytes of a row in a box
+  static constexpr int CHUNKS = DP * ES / ROW;       // boxes across a head
+  static constexpr int CHUNK = KT * ROW;
+  static constexpr int SIDE = CHUNKS * CHUNK;        // k or v of a turn
+  static constexpr int TURN = 2 * SIDE;
+  static constexpr int STAGES = 16384 / TURN;        // turns in flight
+  static constexpr int CTAS = RT == 1 ? 3 : 2;       // of an SM, by shared memory
 };
 
 // The first of the four elements that lane t of a group contributes to step i of the contraction over a head.
@@ -91,20 +86,25 @@ template <int ES, int VB> __device__ __forceinline__ constexpr int tile_element(
   return i / per * (8 * VB / ES) + g * (VB / ES) + i % per * 2;
 }
 
-template <int QT, int PT, int DP, int RT, int ALIGN>
+template <int QT, int PT, int DP, int RT>
 __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
-    paged_step_kernel(const __grid_constant__ StepArgs f) {
+    paged_step_kernel(const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm,
+                      const __grid_constant__ StepArgs f) {
   typedef Shape<QT, PT, DP, RT> S;
   typedef typename Elem<QT>::T E;
   constexpr int R = 8 * RT;
   constexpr float kShift = S::F16 ? 7.0f : 0.0f;  // float16 weights start at 2^7, at most 2^15
   const PagedArgs &a = f.a;
-  __shared__ __align__(16) float part_o[kWarps][R][DP + 4];
+  // turns in flight of each warp; after the walk, the warps' partial results
+  extern __shared__ unsigned char raw[];
+  unsigned char *fifo = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  float(*part_o)[R][DP + 4] = reinterpret_cast<float(*)[R][DP + 4]>(fifo);
   __shared__ float part_m[kWarps][R], part_l[kWarps][R];
   __shared__ float cta_m[R], cta_l[R];
   __shared__ int cta_bad;
   __shared__ __align__(16) float cta_o[R][DP];
-  __shared__ __align__(8) float key_f[kWarps][S::KT], value_f[kWarps][S::KT];  // e4m3: of a turn's rows
+  __shared__ __align__(8) float key_f[kWarps][32], value_f[kWarps][32];  // e4m3: of a turn's rows
+  __shared__ unsigned long long full[kWarps][S::STAGES][2];  // k, v of a turn have landed
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const unsigned cluster_id = blockIdx.x / f.splits, unit = cluster_id / f.groups;  // = b * Hkv + hk
   const int split = blockIdx.x % f.splits, hk = unit % a.Hkv;
@@ -114,8 +114,17 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   const int rows = min(R, a.Lq * a.G - row0);  // row r: query (row0 + r) / G, head hk * G + (row0 + r) % G
   const int used = min(n.n, (row0 + rows - 1) / a.G + 1);  // queries that take part, of those up to this group's last
   const int end = used > row0 / a.G ? n.first + used : 0;  // positions that some row sees
-  if (threadIdx.x == 0) cta_bad = 0;
-  if (S::E8) __syncthreads();  // else the first use is behind the walk's own barrier
+  __shared__ int gave_up;
+  if (threadIdx.x == 0) cta_bad = gave_up = 0;
+  if (lane == 0) {
+    for (int i = 0; i < S::STAGES; ++i) {
+      mbar_init(&full[warp][i][0], 1);
+      mbar_init(&full[warp][i][1], 1);
+    }
+    fence_mbar_init_cluster();
+  }
+  __syncthreads();
+  const Waiter wait{&gave_up};
 
   // q: rows g and g + 8, in the order of the contraction's steps
   unsigned q[S::KSTEPS][RT][2];
@@ -176,145 +185,80 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   int top_e = 0;  // e4m3: the largest byte of the value rows so far; o is in units of 2^(top_e - 127)
   bool bad = false;
 
-  const unsigned char *kp = static_cast<const unsigned char *>(a.k.data) + hk * a.k.s.h * S::ES;
-  const unsigned char *vp = static_cast<const unsigned char *>(a.v.data) + hk * a.v.s.h * S::ES;
-  unsigned kx[S::NT][S::KL][4], vx[S::KT / 16][4][S::VL][S::VB / 4];
-#pragma unroll
-  for (int j = 0; j < S::NT; ++j)
-#pragma unroll
-    for (int i = 0; i < S::KL; ++i) kx[j][i][0] = kx[j][i][1] = kx[j][i][2] = kx[j][i][3] = 0;
-#pragma unroll
-  for (int j = 0; j < S::KT / 4; ++j)
-#pragma unroll
-    for (int i = 0; i < S::VL; ++i)
-#pragma unroll
-      for (int z = 0; z < S::VB / 4; ++z) vx[j / 4][j % 4][i][z] = 0;
-  unsigned bytes = 0;  // e4m3: this lane's position's bytes of k and v
-  int id = -1;         // page of this lane's position (of KT) in the turn that is loaded next
-  const int place_mask = (1 << a.t.page_bits) - 1;
-  auto lookup = [&](int x) {  // of turn x
+  const int place_mask = (1 << a.t.page_bits) - 1, box_rows = min(1 << a.t.page_bits, S::KT);
+  auto lookup = [&](int x) {  // the page of this lane's position (of KT) of turn x
     const int pos = x * S::KT + lane % S::KT;
     if (pos >= end) return -1;
     const int page = page_of(a.t, b, pos);
     bad |= page < 0;
     return page;
   };
-  // Most turns lie within a page and before the end: their rows are a lane's own offset and whole strides apart, and
-  // nothing is left out.  (Loads that D leaves out, in either way, leave their registers 0.)
-  constexpr int kTurnBits = S::KT == 32 ? 5 : 4;
-  const bool turns_in_pages = a.t.page_bits >= kTurnBits;
-  const long long k_row = a.k.s.l * S::ES, v_row = a.v.s.l * S::ES;
-  const int width = a.D * S::ES;
-  auto whole = [&](int base) { return turns_in_pages && base + S::KT <= end && id >= 0; };
-  auto load_keys = [&](int base) {
-    if (whole(base)) {
-      const unsigned char *row = kp + id * (a.k.s.b * S::ES) + ((base & place_mask) + g) * k_row + 16 * t;
+  // k (or v) of turn x, whose page is `id`: a box for each page, by the lane of its first row.  A box without a page is one
+  // past the tensor's end, which TMA fills with zeros; what lies past the utterance's end in its last page comes along.
+  unsigned char *mine = fifo + warp * (S::STAGES * S::TURN);
+  auto copy = [&](int x, int stage, int id, bool values) {
+    unsigned long long *bar = &full[warp][stage][values];
+    if (lane == 0) arrive_expect_tx(bar, S::SIDE);
+    __syncwarp();
+    if (lane < S::KT && lane % box_rows == 0) {
+      const int page = id < 0 ? a.t.n_pages : id * (values ? f.v_p : f.k_p);
+      const int place = (x * S::KT + lane) & place_mask;
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j) {
-#pragma unroll
-        for (int i = 0; i < S::KL; ++i) {
-          if (64 * i + 16 * t + 16 <= width)
-            load_words<16, ALIGN>(kx[j][i], row + 64 * i);
-          else if (ALIGN < 16 && 64 * i + 16 * t < width)  // 8 bytes are left
-            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i);
-        }
-        row += 8 * k_row;
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < S::NT; ++j) {
-      const int pos = base + 8 * j + g, page = __shfl_sync(0xffffffffu, id, 8 * j + g);
-      const unsigned char *row = kp + page * (a.k.s.b * S::ES) + (pos & place_mask) * k_row + 16 * t;
-#pragma unroll
-      for (int i = 0; i < S::KL; ++i) {
-        kx[j][i][0] = kx[j][i][1] = kx[j][i][2] = kx[j][i][3] = 0;
-        if (page >= 0) {
-          if (64 * i + 16 * t + 16 <= width)
-            load_words<16, ALIGN>(kx[j][i], row + 64 * i);
-          else if (ALIGN < 16 && 64 * i + 16 * t < width)
-            load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(kx[j][i]), row + 64 * i);
-        }
-      }
+      for (int i = 0; i < S::CHUNKS; ++i)
+        tma_load_4d(values ? &vm : &km, mine + stage * S::TURN + (values ? S::SIDE : 0) + i * S::CHUNK + lane * S::ROW, bar,
+                    i * (S::ROW / S::ES), hk * (values ? f.v_h : f.k_h), place, page);
     }
   };
-  auto load_values = [&](int base) {
-    if (whole(base)) {
-      const unsigned char *row = vp + id * (a.v.s.b * S::ES) + ((base & place_mask) + 2 * t) * v_row + g * S::VB;
-#pragma unroll
-      for (int j = 0; j < S::KT / 16; ++j) {
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const unsigned char *p = row + ((y & 1) + (y >> 1) * 8) * v_row;
-#pragma unroll
-          for (int i = 0; i < S::VL; ++i) {
-            const int at = i * 8 * S::VB + g * S::VB;
-            if (at + S::VB <= width)
-              load_words<S::VB, ALIGN>(vx[j][y][i], p + i * 8 * S::VB);
-            else if (ALIGN < 16 && S::VB == 16 && at < width)
-              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), p + i * 8 * S::VB);
-          }
-        }
-        row += 16 * v_row;
-      }
-      return;
-    }
-#pragma unroll
-    for (int j = 0; j < S::KT / 16; ++j)
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const int key = 16 * j + 2 * t + (y & 1) + (y >> 1) * 8;
-        const int pos = base + key, page = __shfl_sync(0xffffffffu, id, key);
-        const unsigned char *row = vp + page * (a.v.s.b * S::ES) + (pos & place_mask) * v_row + g * S::VB;
-#pragma unroll
-        for (int i = 0; i < S::VL; ++i) {
-#pragma unroll
-          for (int z = 0; z < S::VB / 4; ++z) vx[j][y][i][z] = 0;
-          const int at = i * 8 * S::VB + g * S::VB;
-          if (page >= 0) {
-            if (at + S::VB <= width)
-              load_words<S::VB, ALIGN>(vx[j][y][i], row + i * 8 * S::VB);
-            else if (ALIGN < 16 && S::VB == 16 && at < width)
-              load_words<8, ALIGN>(reinterpret_cast<unsigned(&)[2]>(vx[j][y][i]), row + i * 8 * S::VB);
-          }
-        }
-      }
-  };
-  auto load_bytes = [&](int base) {
-    if (!S::E8) return;
-    const int place = (base + lane) & place_mask;
-    bytes = 0;
-    if (id >= 0)
-      bytes = __ldg(a.k.scales + row_at(a.k.ss, id, place, hk)) | (unsigned)__ldg(a.v.scales + row_at(a.v.ss, id, place, hk)) << 8;
+  // where 16-byte unit u of a row lies
+  auto unit_at = [](int row, int u) { return row * S::ROW + (S::ROW == 128 ? u ^ (row & 7) : u ^ (row >> 1 & 3)) * 16; };
+  unsigned bytes = 0;  // e4m3: this lane's position's bytes of k and v
+  auto load_bytes = [&](int x, int id) {
+    if (!S::E8) return 0u;
+    const int place = (x * S::KT + lane) & place_mask;
+    return id < 0 ? 0u
+                  : __ldg(a.k.scales + row_at(a.k.ss, id, place, hk)) |
+                        (unsigned)__ldg(a.v.scales + row_at(a.v.ss, id, place, hk)) << 8;
   };
 
   const int turns = (end + S::KT - 1) / S::KT, step = f.splits * kWarps;
   int turn = split * kWarps + warp;
-  id = lookup(turn);
-  int ahead = lookup(turn + step);  // pages are looked up two turns ahead, rows loaded one ahead
-  if (turn < turns) {
-    load_keys(turn * S::KT);
-    load_bytes(turn * S::KT);
-    load_values(turn * S::KT);
-  }
+  // copies go STAGES turns ahead, and pages are looked up a turn before that
+  int ids[S::STAGES + 1];
+#pragma unroll
+  for (int x = 0; x <= S::STAGES; ++x) ids[x] = lookup(turn + x * step);
+#pragma unroll
+  for (int x = 0; x < S::STAGES; ++x)
+    if (turn + x * step < turns) {
+      copy(turn + x * step, x, ids[x], false);
+      copy(turn + x * step, x, ids[x], true);
+    }
+  bytes = load_bytes(turn, ids[0]);
+  int stage = 0, parity = 0;
+  bool ok = true;
   for (; turn < turns; turn += step) {
-    const int base = turn * S::KT, next = (turn + step) * S::KT;
-    const bool more = turn + step < turns;
-    id = ahead;
-    ahead = lookup(turn + 2 * step);
+    const int base = turn * S::KT, ahead = turn + S::STAGES * step;
+    const bool more = ahead < turns;
+    const int after = lookup(ahead + step);
+    const unsigned next_bytes = load_bytes(turn + step, ids[1]);
+    const unsigned char *k_at = mine + stage * S::TURN, *v_at = k_at + S::SIDE;
+    ok = __all_sync(0xffffffffu, wait(&full[warp][stage][0], parity)) && ok;
     // scores: rows g, g + 8; keys 8 j + 2 t, + 1
     float s[S::NT][4];
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) {
       s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
 #pragma unroll
-      for (int x = 0; x < S::KSTEPS; ++x) {
-        const unsigned qa[4] = {q[x][0][0], RT == 2 ? q[x][RT - 1][0] : 0, q[x][0][1], RT == 2 ? q[x][RT - 1][1] : 0};
-        if constexpr (S::E8) {
-          const unsigned w = kx[j][x / 4][x % 4];
-          mma16<true>(s[j], qa, e4m3x2_to_half2(w & 0xffffu), e4m3x2_to_half2(w >> 16));
-        } else {
-          mma16<S::F16>(s[j], qa, kx[j][x / 2][x % 2 * 2], kx[j][x / 2][x % 2 * 2 + 1]);
+      for (int i = 0; i < S::KL; ++i) {
+        const uint4 piece = *reinterpret_cast<const uint4 *>(k_at + i * 64 / S::ROW * S::CHUNK + unit_at(8 * j + g, i * 4 % (S::ROW / 16) + t));
+        const unsigned w[4] = {piece.x, piece.y, piece.z, piece.w};
+#pragma unroll
+        for (int y = 0; y < (S::E8 ? 4 : 2); ++y) {
+          const int x = i * (S::E8 ? 4 : 2) + y;
+          const unsigned qa[4] = {q[x][0][0], RT == 2 ? q[x][RT - 1][0] : 0, q[x][0][1], RT == 2 ? q[x][RT - 1][1] : 0};
+          if constexpr (S::E8)
+            mma16<true>(s[j], qa, e4m3x2_to_half2(w[y] & 0xffffu), e4m3x2_to_half2(w[y] >> 16));
+          else
+            mma16<S::F16>(s[j], qa, w[2 * y], w[2 * y + 1]);
         }
       }
     }
@@ -338,10 +282,8 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
       value_f[warp][lane] = vb == kByteNaN ? NAN : pow2_nonpos((int)vb - top_e);
       __syncwarp();
     }
-    if (more) {
-      load_keys(next);
-      load_bytes(next);
-    }
+    __syncwarp();  // every lane has read the keys
+    if (more) copy(ahead, stage, ids[S::STAGES], false);
     // weights
     float top[RT];
 #pragma unroll
@@ -404,34 +346,76 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
         p[j][h] = pack2<S::F16 ? (int)kF16 : (int)kBF16>(p0, p1);
       }
     }
+    ok = __all_sync(0xffffffffu, wait(&full[warp][stage][1], parity)) && ok;
+    const bool cut = base + S::KT > end;  // rows past the end may hold anything: 0 times NaN is NaN
 #pragma unroll
     for (int j = 0; j < S::KT / 16; ++j)
 #pragma unroll
-      for (int x = 0; x < S::MTILES; ++x) {
-        unsigned va[4];
-        if constexpr (S::E8) {
-          constexpr int per = S::VB / 2;  // tiles of a load
-          const int i = x / per, w = x % per / 2, sel = x % 2 ? 0x7362 : 0x5140;
-          const unsigned lo = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], sel), hi = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], sel);
-          va[0] = e4m3x2_to_half2(lo & 0xffffu);
-          va[1] = e4m3x2_to_half2(lo >> 16);
-          va[2] = e4m3x2_to_half2(hi & 0xffffu);
-          va[3] = e4m3x2_to_half2(hi >> 16);
-        } else {
-          constexpr int per = S::VB / 4;
-          const int i = x / per, w = x % per;
-          va[0] = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], 0x5410);
-          va[1] = __byte_perm(vx[j][0][i][w], vx[j][1][i][w], 0x7632);
-          va[2] = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], 0x5410);
-          va[3] = __byte_perm(vx[j][2][i][w], vx[j][3][i][w], 0x7632);
+      for (int i = 0; i < S::VL; ++i) {
+        constexpr int W = S::VB / 4;
+        unsigned w[4][W];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int key = 16 * j + 2 * t + (y & 1) + (y >> 1) * 8;
+          if constexpr (S::VB == 16) {
+            const uint4 piece = *reinterpret_cast<const uint4 *>(v_at + i * S::CHUNK + unit_at(key, g));
+            w[y][0] = piece.x;
+            w[y][1] = piece.y;
+            w[y][2] = piece.z;
+            w[y][W - 1] = piece.w;
+          } else {
+            const uint2 piece = *reinterpret_cast<const uint2 *>(v_at + unit_at(key, g / 2) + g % 2 * 8);
+            w[y][0] = piece.x;
+            w[y][W - 1] = piece.y;
+          }
+          if (cut && base + key >= end)
+#pragma unroll
+            for (int z = 0; z < W; ++z) w[y][z] = 0;
         }
 #pragma unroll
-        for (int h = 0; h < RT; ++h) mma16<S::F16>(o[x][h], va, p[2 * j][h], p[2 * j + 1][h]);
+        for (int z = 0; z < W; ++z) {
+#pragma unroll
+          for (int half = 0; half < (S::E8 ? 2 : 1); ++half) {
+            unsigned va[4];
+            if constexpr (S::E8) {
+              const int sel = half ? 0x7362 : 0x5140;
+              const unsigned lo = __byte_perm(w[0][z], w[1][z], sel), hi = __byte_perm(w[2][z], w[3][z], sel);
+              va[0] = e4m3x2_to_half2(lo & 0xffffu);
+              va[1] = e4m3x2_to_half2(lo >> 16);
+              va[2] = e4m3x2_to_half2(hi & 0xffffu);
+              va[3] = e4m3x2_to_half2(hi >> 16);
+            } else {
+              va[0] = __byte_perm(w[0][z], w[1][z], 0x5410);
+              va[1] = __byte_perm(w[0][z], w[1][z], 0x7632);
+              va[2] = __byte_perm(w[2][z], w[3][z], 0x5410);
+              va[3] = __byte_perm(w[2][z], w[3][z], 0x7632);
+            }
+            const int x = i * (S::MTILES / S::VL) + z * (S::E8 ? 2 : 1) + half;
+#pragma unroll
+            for (int h = 0; h < RT; ++h) mma16<S::F16>(o[x][h], va, p[2 * j][h], p[2 * j + 1][h]);
+          }
+        }
       }
-    if (more) load_values(next);
+    __syncwarp();
+    if (more) copy(ahead, stage, ids[S::STAGES], true);
+    bytes = next_bytes;
+#pragma unroll
+    for (int x = 0; x < S::STAGES; ++x) ids[x] = ids[x + 1];
+    ids[S::STAGES] = after;
+    if (++stage == S::STAGES) {
+      stage = 0;
+      parity ^= 1;
+    }
   }
 
+  if (!ok)  // copies in flight land before their memory is used for something else
+    for (int i = 0; i < S::STAGES; ++i) {
+      Waiter::drain(&full[warp][i][0], parity ^ (i < stage));
+      Waiter::drain(&full[warp][i][1], parity ^ (i < stage));
+    }
+
   // the warps of a CTA
+  __syncthreads();  // the memory of turns in flight is free
   const float unit_f = S::E8 ? scale_of(top_e) : 1.0f;
 #pragma unroll
   for (int h = 0; h < RT; ++h) {
@@ -449,8 +433,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
         *reinterpret_cast<float2 *>(&part_o[warp][8 * h + 2 * t + y][d]) = make_float2(o[x][h][y] * unit_f, o[x][h][y + 2] * unit_f);
     }
   }
-  if (!S::E8) __syncthreads();  // cta_bad is set to 0
-  if (bad) cta_bad = 1;
+  if (bad || !ok) cta_bad = 1;
   __syncthreads();
   for (int x = threadIdx.x; x < R * DP; x += kWarps * 32) {
     const int r = x / DP, d = x % DP;
@@ -509,10 +492,26 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
   if (f.splits > 1) cluster.sync();  // nobody leaves while its memory may be read
 }
 
-template <int QT, int PT, int DP, int RT, int ALIGN> cudaError_t launch(const StepArgs &f, cudaStream_t stream) {
+template <int QT, int PT, int DP, int RT> cudaError_t launch(StepArgs f, cudaStream_t stream) {
+  typedef Shape<QT, PT, DP, RT> S;
+  const PagedArgs &a = f.a;
+  TensorMap k, v;
+  const int box = (int)std::min<long long>(1LL << a.t.page_bits, S::KT);
+  auto encode = [&](TensorMap *m, const Pages &p) {
+    return encode_rows(m, p.data, PT == kE4M3 ? 1 : 2, a.t.n_pages, 1LL << a.t.page_bits, a.Hkv, a.D, p.s.b, p.s.l, p.s.h, S::ROW, box);
+  };
+  if (!encode(&k, a.k) || !encode(&v, a.v)) return cudaErrorInvalidValue;
+  f.k_p = k.b_mul;
+  f.k_h = k.h_mul;
+  f.v_p = v.b_mul;
+  f.v_h = v.h_mul;
+  constexpr int smem = 1024 + std::max(kWarps * S::STAGES * S::TURN, kWarps * 8 * RT * (DP + 4) * 4);
+  const cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<QT, PT, DP, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(f.a.B * f.a.Hkv * f.groups * f.splits));
+  cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * f.groups * f.splits));
   cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -521,29 +520,23 @@ template <int QT, int PT, int DP, int RT, int ALIGN> cudaError_t launch(const St
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = f.splits > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, paged_step_kernel<QT, PT, DP, RT, ALIGN>, f);
+  return cudaLaunchKernelEx(&cfg, paged_step_kernel<QT, PT, DP, RT>, k.map, v.map, f);
 }
-template <int QT, int PT, int RT, int ALIGN> cudaError_t by_width(const StepArgs &f, cudaStream_t s) {
-  return f.a.D <= 64 ? launch<QT, PT, 64, RT, ALIGN>(f, s) : launch<QT, PT, 128, RT, ALIGN>(f, s);
+template <int QT, int PT, int RT> cudaError_t by_width(const StepArgs &f, cudaStream_t s) {
+  return f.a.D <= 64 ? launch<QT, PT, 64, RT>(f, s) : launch<QT, PT, 128, RT>(f, s);
 }
-template <int QT, int PT, int ALIGN> cudaError_t by_rows(const StepArgs &f, cudaStream_t s) {
-  return (long long)f.a.Lq * f.a.G <= 8 ? by_width<QT, PT, 1, ALIGN>(f, s) : by_width<QT, PT, 2, ALIGN>(f, s);
-}
-
-// Bytes that every row of pages is aligned to: 16, 8 or less.
-int alignment(const PagedArgs &a, int es) {
-  uintptr_t x = 0;
-  auto step = [&](long long n, long long stride) { return n > 1 ? (uintptr_t)(stride * es) : 0; };
-  for (const Pages *p : {&a.k, &a.v})
-    x |= (uintptr_t)p->data | step(a.t.n_pages, p->s.b) | step(1LL << a.t.page_bits, p->s.l) | step(a.Hkv, p->s.h);
-  return x % 16 == 0 ? 16 : x % 8 == 0 ? 8 : 1;
+template <int QT, int PT> cudaError_t by_rows(const StepArgs &f, cudaStream_t s) {
+  return (long long)f.a.Lq * f.a.G <= 8 ? by_width<QT, PT, 1>(f, s) : by_width<QT, PT, 2>(f, s);
 }
 
 }  // namespace
 
 bool paged_step_takes(const PagedArgs &a, int dtype, int cache_dtype) {
-  const bool e8 = cache_dtype == kE4M3;
-  return dtype != kF32 && a.D <= 128 && a.D % 8 == 0 && alignment(a, e8 ? 1 : 2) >= (e8 ? 8 : 16);
+  const int es = cache_dtype == kE4M3 ? 1 : 2;
+  auto fits = [&](const Pages &p) {
+    return rows_fit(p.data, es, a.t.n_pages, 1LL << a.t.page_bits, a.Hkv, a.D, p.s.b, p.s.l, p.s.h);
+  };
+  return dtype != kF32 && a.D <= 128 && a.D % 8 == 0 && a.t.page_bits >= 3 && fits(a.k) && fits(a.v);
 }
 
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream) {
@@ -564,12 +557,8 @@ cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cu
       f.splits = s;
     }
   }
-  if (cache_dtype == kE4M3) {
-    if (alignment(a, 1) == 16)
-      return dtype == kF16 ? by_rows<kF16, kE4M3, 16>(f, stream) : by_rows<kBF16, kE4M3, 16>(f, stream);
-    return dtype == kF16 ? by_rows<kF16, kE4M3, 8>(f, stream) : by_rows<kBF16, kE4M3, 8>(f, stream);
-  }
-  return dtype == kF16 ? by_rows<kF16, kF16, 16>(f, stream) : by_rows<kBF16, kBF16, 16>(f, stream);
+  if (cache_dtype == kE4M3) return dtype == kF16 ? by_rows<kF16, kE4M3>(f, stream) : by_rows<kBF16, kE4M3>(f, stream);
+  return dtype == kF16 ? by_rows<kF16, kF16>(f, stream) : by_rows<kBF16, kBF16>(f, stream);
 }
 
 }  // namespace tdt

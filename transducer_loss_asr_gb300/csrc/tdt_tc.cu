@@ -89,6 +89,30 @@ bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool rows_fit(const void *ptr, int es, long long B, long long L, long long H, int D, long long sb, long long sl,
+              long long sh) {
+  return (uintptr_t)ptr % 16 == 0 && D * es % 8 == 0 && axis_fits(B, sb, es) && axis_fits(H, sh, es) &&
+         axis_fits(L, sl, es) && (L <= 1 || sl != 0);
+}
+
+bool encode_rows(TensorMap *m, const void *ptr, int es, long long B, long long L, long long H, int D, long long sb,
+                 long long sl, long long sh, int row_bytes, int box_rows) {
+  EncodeTiled fn = encoder();
+  if (!fn) return false;
+  m->b_mul = sb == 0 || B <= 1 ? 0 : 1;
+  m->h_mul = sh == 0 || H <= 1 ? 0 : 1;
+  const cuuint64_t unit = (cuuint64_t)((D * es + 15) / 16 * 16);
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)(m->h_mul ? H : 1), (cuuint64_t)L, (cuuint64_t)(m->b_mul ? B : 1)};
+  const cuuint64_t strides[3] = {m->h_mul ? (cuuint64_t)sh * es : unit, L > 1 ? (cuuint64_t)sl * es : unit,
+                                 m->b_mul ? (cuuint64_t)sb * es : unit};
+  const cuuint32_t box[4] = {(cuuint32_t)(row_bytes / es), 1, (cuuint32_t)box_rows, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  return fn(&m->map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void *>(ptr), dims,
+            strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            row_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_planes(TensorMap *m, const unsigned short *planes, long long B, long long L, long long H,
                    int chunks, int box_heads, int box_rows) {
   const int n = chunks * 192;

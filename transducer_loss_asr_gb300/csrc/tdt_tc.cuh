@@ -397,6 +397,13 @@ bool encode_map(TensorMap *m, const void *ptr, int dtype, long long B, long long
 bool map_fits(int dtype, const void *ptr, long long B, long long L, long long H, int D, long long sb,
               long long sl, long long sh);
 
+// The same of elements of `es` bytes (1 or 2) with boxes of `row_bytes` (64 or 128) x rows of one head, swizzled by their
+// width, and whether it can take the tensor.
+bool encode_rows(TensorMap *m, const void *ptr, int es, long long B, long long L, long long H, int D, long long sb,
+                 long long sl, long long sh, int row_bytes, int box_rows);
+bool rows_fit(const void *ptr, int es, long long B, long long L, long long H, int D, long long sb, long long sl,
+              long long sh);
+
 // Float32 tensors as bfloat16 planes [B, H, L, chunk of 64 columns, 3, 64], rows at or past the utterance's
 // length and columns past D as zeros.
 struct PlaneSource {
