@@ -477,7 +477,7 @@ class PagedCache:
     has says its row of the page table that the calls take.
     """
 
-    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "device", "page_size", "heads",
+    __slots__ = ("k", "v", "k_scales", "v_scales", "dtype", "device", "at", "page_size", "heads",
                  "head_dim", "_packed")
 
     def __init__(self, k, v, k_scales=None, v_scales=None):
@@ -504,7 +504,7 @@ class PagedCache:
             ks = vs = 0
             strides = sk[:3] + sv[:3] + (0,) * 6
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
-        self.dtype, self.device = dtype, dev
+        self.dtype, self.device, self.at = dtype, dev, k.get_device()
         self.page_size, self.heads, self.head_dim = shape[1:]
         self._packed = _pack_cache(k.data_ptr(), v.data_ptr(), ks, vs, *shape, *strides,
                                    _CACHE_DTYPES[dtype])
@@ -521,17 +521,29 @@ class PagedCache:
 
 
 def _check_pages(cache, page_table, kv_lens, q_lens, B, dev):
-    """(address, row stride) of the page table."""
+    """(address, row stride, columns) of the page table."""
     if cache.device != dev:
         raise ValueError("the cache must be on %s" % dev)
-    if (page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != B
-            or page_table.device != dev or (page_table.stride(1) != 1 and page_table.shape[1] > 1)):
+    shape, stride = page_table.shape, page_table.stride()
+    if (len(shape) != 2 or shape[0] != B or page_table.dtype != torch.int32
+            or page_table.get_device() != cache.at or (stride[1] != 1 and shape[1] > 1)):
         raise ValueError("page_table must be an int32 tensor [%d, max_pages] with contiguous rows on %s"
                          % (B, dev))
-    _check_lens("kv_lens", kv_lens, B, dev)
-    if q_lens is not None:
-        _check_lens("q_lens", q_lens, B, dev)
-    return page_table.data_ptr(), page_table.stride(0)
+    for name, t in (("kv_lens", kv_lens), ("q_lens", q_lens)):
+        if t is not None and (t.dtype != torch.int64 or t.shape != (B,) or t.get_device() != cache.at
+                              or not t.is_contiguous()):
+            raise ValueError("%s must be a contiguous int64 tensor of %d element(s) on %s"
+                             % (name, B, dev))
+    return page_table.data_ptr(), stride[0], shape[1]
+
+
+def _out_rows(t, shape, dtype, dev, name):
+    """(t, strides): checked to be an output with contiguous rows, or a new contiguous one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    elif t.shape != shape or t.dtype != dtype or t.device != dev or (t.stride(-1) != 1 and shape[-1] != 1):
+        raise ValueError("%s must be %s of %s on %s with contiguous rows" % (name, tuple(shape), dtype, dev))
+    return t, t.stride()
 
 
 def tdt_cache_write(k, v, cache, page_table, kv_lens, q_lens=None):
@@ -543,23 +555,22 @@ def tdt_cache_write(k, v, cache, page_table, kv_lens, q_lens=None):
     the new rows; q_lens: int64 [B] or None (all L).  page_table: int32 [B, max_pages].  k and v may
     be slices of a fused projection.
     """
-    ks = k.shape
+    ks, dtype, dev = k.shape, k.dtype, cache.device
     if len(ks) != 4 or v.shape != ks or ks[2] != cache.heads or ks[3] != cache.head_dim:
         raise ValueError("k and v must be [B, L, %d, %d]" % (cache.heads, cache.head_dim))
-    dtype, dev = k.dtype, k.device
     if dtype not in DTYPES or v.dtype != dtype:
         raise TypeError("k and v must be float32, float16 or bfloat16, of one dtype")
     if cache.dtype != dtype and cache.dtype != E4M3:
         raise TypeError("pages of %s cannot hold rows of %s" % (cache.dtype, dtype))
-    if v.device != dev:
-        raise ValueError("k and v must be on one device")
-    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, ks[0], dev)
+    if k.get_device() != cache.at or v.get_device() != cache.at:
+        raise ValueError("k, v and the cache must be on one device")
+    table, stride, columns = _check_pages(cache, page_table, kv_lens, q_lens, ks[0], dev)
     (k, sk), (v, sv) = _rows(k), _rows(v)
     with _on(dev):
         _check(lib.tdt_cache_write(
-            k.data_ptr(), v.data_ptr(), _pack3(ks[0], ks[1], page_table.shape[1]),
-            _pack6(*sk[:3], *sv[:3]), DTYPES[dtype], cache._packed, table, stride,
-            kv_lens.data_ptr(), _addr(q_lens), _raw_stream(dev.index)))
+            k.data_ptr(), v.data_ptr(), _pack3(ks[0], ks[1], columns), _pack6(*sk[:3], *sv[:3]),
+            DTYPES[dtype], cache._packed, table, stride, kv_lens.data_ptr(), _addr(q_lens),
+            _raw_stream(dev.index)))
 
 
 def tdt_cache_read(cache, page_table, kv_lens, q_lens, length, dtype, k=None, v=None):
@@ -569,21 +580,14 @@ def tdt_cache_read(cache, page_table, kv_lens, q_lens, length, dtype, k=None, v=
     B, dev = kv_lens.shape[0], cache.device
     if dtype not in DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
-    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
-    shape, out = (B, length, cache.heads, cache.head_dim), []
-    for name, t in (("k", k), ("v", v)):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
-        elif (t.shape != shape or t.dtype != dtype or t.device != dev
-              or (t.stride(3) != 1 and shape[3] != 1)):
-            raise ValueError("%s must be %s of %s on %s with contiguous rows" % (name, shape, dtype, dev))
-        out.append(t)
-    k, v = out
+    table, stride, columns = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
+    shape = (B, length, cache.heads, cache.head_dim)
+    k, sk = _out_rows(k, shape, dtype, dev, "k")
+    v, sv = _out_rows(v, shape, dtype, dev, "v")
     with _on(dev):
         _check(lib.tdt_cache_read(
-            cache._packed, table, stride, kv_lens.data_ptr(), _addr(q_lens),
-            _pack3(B, length, page_table.shape[1]), _pack6(*k.stride()[:3], *v.stride()[:3]),
-            DTYPES[dtype], k.data_ptr(), v.data_ptr(), _raw_stream(dev.index)))
+            cache._packed, table, stride, kv_lens.data_ptr(), _addr(q_lens), _pack3(B, length, columns),
+            _pack6(*sk[:3], *sv[:3]), DTYPES[dtype], k.data_ptr(), v.data_ptr(), _raw_stream(dev.index)))
     return k, v
 
 
@@ -605,24 +609,26 @@ def tdt_paged_attn(q, cache, page_table, kv_lens, q_lens=None, scale=None, need_
     tdt_paged_attn_workspace_size bytes at least, allocated unless given.  Returns (out, lse): out like
     q, lse float32 [B, H, Lq], or None without need_lse.
     """
-    if q.dim() != 4 or q.shape[3] != cache.head_dim:
+    shape, dtype, dev = q.shape, q.dtype, cache.device
+    if len(shape) != 4 or shape[3] != cache.head_dim:
         raise ValueError("q must be [B, Lq, H, %d]" % cache.head_dim)
-    B, Lq, H, D = q.shape
-    dtype, dev = q.dtype, q.device
     if dtype not in DTYPES:
         raise TypeError("q dtype must be float32, float16 or bfloat16")
     if cache.dtype != dtype and cache.dtype != E4M3:
         raise TypeError("queries of %s cannot read pages of %s" % (dtype, cache.dtype))
-    table, stride = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
+    if q.get_device() != cache.at:
+        raise ValueError("q and the cache must be on one device")
+    B, Lq, H, D = shape
+    table, stride, columns = _check_pages(cache, page_table, kv_lens, q_lens, B, dev)
     q, sq = _rows(q)
-    out, so = _like(q, out, "out")
+    out, so = _out_rows(out, shape, dtype, dev, "out")
     if lse is not None:
         if (lse.dtype != torch.float32 or lse.shape != (B, H, Lq) or not lse.is_contiguous()
                 or lse.device != dev):
             raise ValueError("lse must be a contiguous float32 tensor [B, H, Lq] on %s" % dev)
     elif need_lse:
         lse = torch.empty((B, H, Lq), dtype=torch.float32, device=dev)
-    sizes, code, ws, nbytes = _pack4(B, Lq, H, page_table.shape[1]), DTYPES[dtype], None, 0
+    sizes, code, ws, nbytes = _pack4(B, Lq, H, columns), DTYPES[dtype], None, 0
     if workspace is None:
         nbytes = lib.tdt_paged_attn_workspace_size(sizes, code, cache._packed)
         if nbytes:
@@ -654,19 +660,21 @@ class TokenLogprobs(NamedTuple):
 
 
 def _check_scored(logits, tokens):
-    """(logits with contiguous rows, N, V)"""
-    if logits.dim() != 2:
+    """(logits with contiguous rows, N, V, row stride)"""
+    shape, stride = logits.shape, logits.stride()
+    if len(shape) != 2:
         raise ValueError("logits must be [N, V]")
     if logits.dtype not in DTYPES:
         raise TypeError("logits dtype must be float32, float16 or bfloat16")
-    N, V = logits.shape
+    N, V = shape
     if (tokens.dtype != torch.int64 or tokens.shape != (N,) or not tokens.is_contiguous()
-            or tokens.device != logits.device):
+            or tokens.get_device() != logits.get_device()):
         raise ValueError("tokens must be a contiguous int64 tensor of %d element(s) on %s"
                          % (N, logits.device))
-    if logits.stride(1) != 1 and V != 1:
+    if stride[1] != 1 and V != 1:
         logits = logits.contiguous()
-    return logits, N, V
+        stride = logits.stride()
+    return logits, N, V, stride[0]
 
 
 def _new_logprobs(N, n_top, dev):
@@ -680,12 +688,14 @@ def _new_logprobs(N, n_top, dev):
                          torch.empty((N, n_top), dtype=f, device=dev))
 
 
-def _check_weights(N, dev, **weights):
-    for name, t in weights.items():
-        if t is not None and (t.dtype != torch.float32 or t.shape != (N,) or not t.is_contiguous()
-                              or t.device != dev):
-            raise ValueError("%s must be a contiguous float32 tensor of %d element(s) on %s"
-                             % (name, N, dev))
+def _weights(t, N, at, name):
+    """Address of weights (None: none); at: the logits' device index."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.shape != (N,) or t.get_device() != at or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous float32 tensor of %d element(s) on the logits' device"
+                         % (name, N))
+    return t.data_ptr()
 
 
 def _grad_rows(logits, grad_out):
@@ -702,12 +712,12 @@ def tdt_token_logprobs_fwd(logits, tokens, n_top=0):
     of ``logits`` [N, V], the row's entropy, and its ``n_top`` most probable tokens, on the current
     CUDA stream (include/tdt_decoder.h, tdt_token_logprobs_fwd).  Rows may be a slice of wider ones.
     Returns TokenLogprobs."""
-    logits, N, V = _check_scored(logits, tokens)
+    logits, N, V, stride = _check_scored(logits, tokens)
     dev = logits.device
     r = _new_logprobs(N, n_top, dev)
     with _on(dev):
         _check(lib.tdt_token_logprobs_fwd(
-            logits.data_ptr(), _pack3(N, V, n_top), logits.stride(0), DTYPES[logits.dtype],
+            logits.data_ptr(), _pack3(N, V, n_top), stride, DTYPES[logits.dtype],
             tokens.data_ptr(), r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(),
             _addr(r.top_tokens), _addr(r.top_logprobs), _raw_stream(dev.index)))
     return r
@@ -719,9 +729,11 @@ def tdt_token_logprobs_bwd(logits, tokens, result, grad_logprobs=None, grad_entr
     and grad_top (float32 [N, n_top]) of ``result``, which tdt_token_logprobs_fwd returned for the same
     logits and tokens.  grad_out may be ``logits``: the gradient then replaces them."""
     rows = logits
-    logits, N, V = _check_scored(logits, tokens)
+    logits, N, V, stride = _check_scored(logits, tokens)
     dev = logits.device
-    _check_weights(N, dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy, entropy=result.entropy)
+    at = logits.get_device()
+    a, b = _weights(grad_logprobs, N, at, "grad_logprobs"), _weights(grad_entropy, N, at, "grad_entropy")
+    entropy = _weights(result.entropy, N, at, "entropy")
     stats, top, n_top = result.stats, result.top_tokens, 0
     if (stats.dtype != torch.float32 or stats.shape != (N, 2) or not stats.is_contiguous()
             or stats.device != dev):
@@ -738,10 +750,9 @@ def tdt_token_logprobs_bwd(logits, tokens, result, grad_logprobs=None, grad_entr
     grad_out = _grad_rows(rows, grad_out)
     with _on(dev):
         _check(lib.tdt_token_logprobs_bwd(
-            logits.data_ptr(), _pack3(N, V, n_top), _pack2(logits.stride(0), grad_out.stride(0)),
-            DTYPES[logits.dtype], tokens.data_ptr(), result.entropy.data_ptr(), stats.data_ptr(),
-            _addr(top), _addr(grad_logprobs), _addr(grad_entropy), _addr(grad_top),
-            grad_out.data_ptr(), _raw_stream(dev.index)))
+            logits.data_ptr(), _pack3(N, V, n_top), _pack2(stride, grad_out.stride(0)),
+            DTYPES[logits.dtype], tokens.data_ptr(), entropy, stats.data_ptr(), _addr(top), a, b,
+            _addr(grad_top), grad_out.data_ptr(), _raw_stream(dev.index)))
     return grad_out
 
 
@@ -750,16 +761,16 @@ def tdt_token_logprobs_fwd_bwd(logits, tokens, grad_logprobs=None, grad_entropy=
     """Both in one call, for weights that are known beforehand: (TokenLogprobs, gradient of the logits).
     Arguments as of tdt_token_logprobs_fwd and tdt_token_logprobs_bwd."""
     rows = logits
-    logits, N, V = _check_scored(logits, tokens)
+    logits, N, V, stride = _check_scored(logits, tokens)
     dev = logits.device
-    _check_weights(N, dev, grad_logprobs=grad_logprobs, grad_entropy=grad_entropy)
+    at = logits.get_device()
+    a, b = _weights(grad_logprobs, N, at, "grad_logprobs"), _weights(grad_entropy, N, at, "grad_entropy")
     grad_out = _grad_rows(rows, grad_out)
     r = _new_logprobs(N, n_top, dev)
     with _on(dev):
         _check(lib.tdt_token_logprobs_fwd_bwd(
-            logits.data_ptr(), _pack3(N, V, n_top), _pack2(logits.stride(0), grad_out.stride(0)),
-            DTYPES[logits.dtype], tokens.data_ptr(), _addr(grad_logprobs), _addr(grad_entropy),
-            r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(), _addr(r.top_tokens),
+            logits.data_ptr(), _pack3(N, V, n_top), _pack2(stride, grad_out.stride(0)),
+            DTYPES[logits.dtype], tokens.data_ptr(), a, b, r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(), _addr(r.top_tokens),
             _addr(r.top_logprobs), grad_out.data_ptr(), _raw_stream(dev.index)))
     return r, grad_out
 
