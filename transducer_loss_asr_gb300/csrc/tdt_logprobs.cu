@@ -56,7 +56,7 @@ struct RowArgs {
   unsigned N;
   int V, K;
   int ctas;           // CTAs of a row
-  int keep;           // the vectors of a stretch stay in dynamic shared memory for the backward pass
+  int keep;           // vectors of a stretch that stay in dynamic shared memory for the backward pass (0: none do)
 };
 
 // max that keeps NaN
@@ -92,16 +92,20 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
 }
 __device__ __forceinline__ int index_of(unsigned long long key) { return (int)(0xffffffffu - (unsigned)key); }
 
-// A group's (a warp's or a block's) shared memory.
-template <int T> struct GroupShared {
+// Dynamic shared memory of a group (a warp or a block) where there are alternatives.
+template <int T> struct TopShared {
   static constexpr int LIST = T == 32 ? 288 : 1024;
   static constexpr int GROUPS = T == 32 ? 1 : 16;  // of a thread's batches of vectors
+  unsigned long long list[LIST];
   float group_max[GROUPS][T];
+};
+
+// A group's shared memory.
+template <int T> struct GroupShared {
   Sums sums[T / 32];
   float least[T / 32];
   unsigned long long best[T / 32];  // of the passes that stand in for a list that overflows
   int count;
-  unsigned long long list[LIST];
   unsigned long long top[kMostTop];  // the stretch's own alternatives, ranked
   int top_n;
   Sums row;                // of the stretch, for the cluster
@@ -130,7 +134,7 @@ template <int DT> __device__ __forceinline__ Stretch stretch_of(const void *p, i
 }
 
 template <int DT, bool FWD, bool BWD, int T>
-__global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__ RowArgs a) {
   typedef typename Elem<DT>::T E;
   constexpr int N = Vec<DT>::N, U = 4, WARPS = T / 32;
   constexpr bool IN_PLACE = BWD;  // the logits may be written in this kernel
@@ -148,7 +152,8 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
   // of the whole row: log2 p_i = x_i L - R - log2_s; R infinite: (x_i - m) L - log2_s
   float R = 0.0f, m = 0.0f, log2_s = 0.0f, ent = 0.0f;
   auto log2_of = [&](float v) { return (R < INFINITY ? fmaf(v, kLog2e, -R) : (v - m) * kLog2e) - log2_s; };
-  extern __shared__ uint4 kept_row[];
+  extern __shared__ __align__(16) uint4 kept_row[];
+  TopShared<T> &lists = reinterpret_cast<TopShared<T> *>(kept_row + a.keep)[threadIdx.x / T];
   if (FWD && !real && part == 0) {
     const float none = token < 0 ? 0.0f : NAN;
     if (tid == 0) {
@@ -201,9 +206,9 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
     const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
     const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
     const float loose_x = loose_at >= 0 ? at(loose_at) : -INFINITY;
-    const bool keep = BWD && T > 32 && a.keep;
+    const bool keep = BWD && T > 32 && a.keep > 0;
     // U vectors at a time, the next ones in flight.  Of each group of these batches a thread notes its maximum.
-    constexpr int GROUPS = GroupShared<T>::GROUPS;
+    constexpr int GROUPS = TopShared<T>::GROUPS;
     const int batches = (w.last - w.first + U * T - 1) / (U * T), per = (batches + GROUPS - 1) / GROUPS;  // batches of a group
     float best = -INFINITY;
     int group = 0, left = per;
@@ -231,7 +236,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       if (K > 0) {
         best = fmaxf(best, most);
         if (--left == 0) {
-          sh.group_max[group++][tid] = best;
+          lists.group_max[group++][tid] = best;
           best = -INFINITY;
           left = per;
         }
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
 #pragma unroll
       for (int u = 0; u < U; ++u) raw[u] = next[u];
     }
-    if (K > 0 && group < GROUPS) sh.group_max[group++][tid] = best;  // each thread reads its own
+    if (K > 0 && group < GROUPS) lists.group_max[group++][tid] = best;  // each thread reads its own
     if (loose_at >= 0) {
       grow(loose_x);
       const float z = max_nan(fmaf(loose_x, kLog2e, -r.R), kLeastZ), p = fast_exp2(z);
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
       auto note = [&](float v, int i) {
         if (v >= threshold && v > -INFINITY) {
           const int k = atomicAdd(&sh.count, 1);
-          if (k < GroupShared<T>::LIST) sh.list[k] = key_of(v, i);
+          if (k < TopShared<T>::LIST) lists.list[k] = key_of(v, i);
         }
       };
       if (r.m >= threshold) {
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
             }
         };
         for (int i = 0; i < group; ++i)
-          if (sh.group_max[i][tid] >= threshold)
+          if (lists.group_max[i][tid] >= threshold)
             for (int k = i * per; k < min((i + 1) * per, batches); ++k) look(w.first + tid + k * U * T);
         if (loose_at >= 0) note(loose_x, loose_at);
       }
@@ -312,12 +317,12 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
     }
     if (K > 0) {
       const int count = sh.count;
-      if (count <= GroupShared<T>::LIST) {
+      if (count <= TopShared<T>::LIST) {
         for (int i = tid; i < count; i += T) {
-          const unsigned long long mine = sh.list[i];
+          const unsigned long long mine = lists.list[i];
           int rank = 0;
 #pragma unroll 4
-          for (int j = 0; j < count; ++j) rank += sh.list[j] > mine;
+          for (int j = 0; j < count; ++j) rank += lists.list[j] > mine;
           if (rank < K) sh.top[rank] = mine;
         }
         if (tid == 0) sh.top_n = min(count, K);
@@ -420,12 +425,12 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
           __syncthreads();  // the list's memory is free
           for (int q = tid; q < ctas * K; q += T) {
             const int i = q / K, k = q % K;
-            sh.list[q] = k < *cluster.map_shared_rank(&sh.top_n, i) ? *cluster.map_shared_rank(&sh.top[k], i) : 0;
+            lists.list[q] = k < *cluster.map_shared_rank(&sh.top_n, i) ? *cluster.map_shared_rank(&sh.top[k], i) : 0;
           }
           __syncthreads();
           for (int base = 0; base < ctas * K; base += T) {
             const int q = base + tid;
-            const unsigned long long mine = q < ctas * K ? sh.list[q] : 0;
+            const unsigned long long mine = q < ctas * K ? lists.list[q] : 0;
             total += __syncthreads_count(mine != 0);
             int rank = q % K;
             for (int j = 0; j < ctas && mine != 0 && rank < K; ++j) {
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
               int lo = 0, hi = K;
               while (lo < hi) {  // entries of j before this one
                 const int mid = (lo + hi) / 2;
-                const bool before = sh.list[j * K + mid] > mine;
+                const bool before = lists.list[j * K + mid] > mine;
                 lo = before ? mid + 1 : lo;
                 hi = before ? hi : mid;
               }
@@ -531,7 +536,7 @@ __global__ void __launch_bounds__(kBlock) rows_kernel(const __grid_constant__ Ro
         *reinterpret_cast<uint4 *>(dx + w.head + (long long)v * N) = pack<DT>(y);
       };
       const E *body = x + w.head;
-      if (FWD && T > 32 && a.keep && mis == 0) {  // the thread's own vectors: the stretches are the same
+      if (FWD && T > 32 && a.keep > 0 && mis == 0) {  // the thread's own vectors: the stretches are the same
         for (int v = w.first + tid; v < w.last; v += T) finish(kept_row[v - w.first], v);
       } else if (mis == 0) {
         for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
@@ -622,8 +627,9 @@ bool off4(std::initializer_list<const void *> ptrs) {
 
 template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
   const long long bytes = (long long)a.V * (DT == kF32 ? 4 : 2);
-  if (bytes <= 2048 && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 51)
-    rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, 0, s>>>(a);
+  if (bytes <= 2048 && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 37)
+    const size_t smem = FWD && a.K > 0 ? sizeof(TopShared<32>) * (kBlock / 32) : 0;
+    rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, smem, s>>>(a);
     return cudaGetLastError();
   }
   // CTAs of a row: while each has over 256 KB (64 KB that wait in shared memory) or CTAs are too few for the SMs, and
@@ -631,16 +637,18 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
   const long long most = FWD && BWD ? 65536 : 262144;
   a.ctas = 1;
   while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > most || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
-  const long long kept = (bytes / 16 / a.ctas + 1) * 16;
-  a.keep = FWD && BWD && kept <= 65536 + 16;
-  if (a.keep) {
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536 + 16);
+  const long long kept = bytes / 16 / a.ctas + 1;
+  a.keep = FWD && BWD && kept * 16 <= 65536 + 16 ? (int)kept : 0;
+  const size_t smem = (size_t)a.keep * 16 + (FWD && a.K > 0 ? sizeof(TopShared<kBlock>) : 0);
+  if (FWD && smem > 0) {
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               65536 + 16 + (int)sizeof(TopShared<kBlock>));
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.N * (unsigned)a.ctas);
   cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = a.keep ? (size_t)kept : 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
