@@ -66,6 +66,41 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
+// A vector's elements as float32.  What lies below -2e38 (or is -inf) becomes -2e38, so that products with its weight, which
+// is 0, are 0: two elements an instruction in bfloat16.  (The other types' z is held above kLeastZ instead.)
+template <int DT> __device__ __forceinline__ void unpack_held(uint4 raw, float *v) {
+  if constexpr (DT == kBF16) {
+    unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0xff16ff16u));
+    raw = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  unpack<DT>(raw, v);
+}
+template <int DT> __device__ __forceinline__ float2 held(float2 z) {
+  return DT == kBF16 ? z : make_float2(max_nan(z.x, kLeastZ), max_nan(z.y, kLeastZ));
+}
+// A vector's maximum, NaN left out.
+template <int DT> __device__ __forceinline__ float vector_max(uint4 raw) {
+  if constexpr (DT == kF32) {
+    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+  } else {
+    unsigned a, b;
+    if constexpr (DT == kBF16) {
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(raw.x), "r"(raw.y));
+      asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(raw.z), "r"(raw.w));
+      asm("max.bf16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    } else {
+      asm("max.f16x2 %0, %1, %2;" : "=r"(a) : "r"(raw.x), "r"(raw.y));
+      asm("max.f16x2 %0, %1, %2;" : "=r"(b) : "r"(raw.z), "r"(raw.w));
+      asm("max.f16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&a));
+      return fmaxf(f.x, f.y);
+    }
+  }
+}
+
 // A stretch's maximum m, reference R (a whole number), sum of 2^z and sum of 2^z z, z = x log2 e - R.  s = 0: nothing, whatever R.
 struct Sums {
   float m, R, s, t;
@@ -186,21 +221,13 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
-        float2 z = fma2(make_float2(v[i], v[i + 1]), L2, neg);
-        z.x = max_nan(z.x, kLeastZ);
-        z.y = max_nan(z.y, kLeastZ);
+        const float2 z = held<DT>(fma2(make_float2(v[i], v[i + 1]), L2, neg));
         const float2 p = make_float2(fast_exp2(z.x), fast_exp2(z.y));
         s2 = add2(s2, p);
         t2 = fma2(p, z, t2);
       }
       r.s += s2.x + s2.y;
       r.t += t2.x + t2.y;
-    };
-    auto vector_max = [&](const float (&v)[N]) {
-      float top = fmaxf(v[0], v[1]);
-#pragma unroll
-      for (int i = 2; i < N; i += 2) top = max3(top, v[i], v[i + 1]);
-      return top;
     };
     // the elements outside whole vectors belong to the first CTA, one a thread
     const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
@@ -221,17 +248,18 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     load(w.first + tid, raw);
     for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
       load(v0 + U * T, next);
-      float most = -INFINITY;
+      float most = vector_max<DT>(raw[0]);
+#pragma unroll
+      for (int u = 1; u < U; ++u)
+        if (v0 + u * T < w.last) most = fmaxf(most, vector_max<DT>(raw[u]));
+      grow(most);
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * T < w.last) {
           if (keep) kept_row[v0 + u * T - w.first] = raw[u];
           float v[N];
-          unpack<DT>(raw[u], v);
-          const float top = vector_max(v);
-          grow(top);
+          unpack_held<DT>(raw[u], v);
           add_vector(v);
-          most = fmaxf(most, top);
         }
       if (K > 0) {
         best = fmaxf(best, most);
@@ -285,7 +313,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
             if (v0 + u * T < w.last) {
               float v[N];
               unpack<DT>(raw[u], v);
-              if (vector_max(v) >= threshold)
+              if (vector_max<DT>(raw[u]) >= threshold)
 #pragma unroll
                 for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
             }
@@ -515,7 +543,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       const int mis = (int)((uintptr_t)(x + w.head) & 15);
       auto finish = [&](uint4 raw, int v) {
         float y[N];
-        unpack<DT>(raw, y);
+        unpack_held<DT>(raw, y);
         if (R < INFINITY) {
           const float2 L2 = make_float2(kLog2e, kLog2e), neg = make_float2(-R, -R), sum = make_float2(-log2_s, -log2_s);
 #pragma unroll
@@ -524,12 +552,13 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
             const float2 p = make_float2(fast_exp2(lp.x), fast_exp2(lp.y));
             float2 f = make_float2(c0, c0);
             if (c1 != 0.0f)
-              f = fma2(make_float2(c1, c1), make_float2(max_nan(lp.x, kLeastZ), max_nan(lp.y, kLeastZ)), f);
+              f = fma2(make_float2(c1, c1), held<DT>(lp), f);
             f = mul2(p, f);
             y[i] = f.x;
             y[i + 1] = f.y;
           }
         } else {
+          unpack<DT>(raw, y);
 #pragma unroll
           for (int i = 0; i < N; ++i) y[i] = slope(y[i]);
         }
