@@ -281,8 +281,10 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     }
     if (K > 0) {
       // At least K elements reach the threshold: each warp all of whose lanes have vectors has ceil(K / such warps) lanes that
-      // do.  (Without such warps, or where they have too few lanes, a stretch is short, and everything is listed.)
-      const int full = min(WARPS, (w.last - w.first) / 32), want = full > 0 ? (K + full - 1) / full : 33;
+      // do; in a stretch too short for one, the first warp's lanes that have some.  (Where these are fewer than K, everything
+      // is listed.)
+      const int held_vectors = w.last - w.first, full = max(1, min(WARPS, held_vectors / 32));
+      const int want = (K + full - 1) / full <= min(32, held_vectors) ? (K + full - 1) / full : 33;
       int ahead = 0;  // lanes with a larger maximum (equal ones: in order)
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -656,7 +658,7 @@ bool off4(std::initializer_list<const void *> ptrs) {
 
 template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
   const long long bytes = (long long)a.V * (DT == kF32 ? 4 : 2);
-  if (bytes <= 2048 && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 37)
+  if ((bytes <= 2048 || (bytes <= 8192 && a.N >= 1024)) && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 37)
     const size_t smem = FWD && a.K > 0 ? sizeof(TopShared<32>) * (kBlock / 32) : 0;
     rows_kernel<DT, FWD, BWD, 32><<<(a.N + 7) / 8, kBlock, smem, s>>>(a);
     return cudaGetLastError();

@@ -95,7 +95,6 @@ struct CacheArgs {
 cudaError_t launch_cache_write(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 // Few query rows: a kernel that reads k and v at memory speed.  (It takes any number of rows; *_takes go by sizes and pages.)
-constexpr int kPagedStepRows = 32;  // rows of a key head up to which it is used
 bool paged_step_takes(const PagedArgs &a, int dtype, int cache_dtype);
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
 // Many query rows on the tensor cores: which calls (paged_tc_fits: by q and out, too), and the workspace for up to `most`

@@ -134,10 +134,17 @@ PagedArgs attn_args(const int64_t sizes[4], const tdt_paged_cache *c) {
   return a;
 }
 enum Way { kStep, kTensor, kGather };
+// The few-rows kernel reads k and v once for each 16 rows of a key head, the tensor-core kernel once for each row tile of each
+// group of P heads; e4m3 pages are laid out densely for the latter first.  Costs of a read in microseconds at 16 x 2,000
+// positions of 4 heads of 128, bfloat16 and e4m3: 18 (12) of the first kernel, 29 of the second, 24 of the layout (20 rows of 4
+// heads in a group 37 us against 30, 12 rows 19 against 29; e4m3 64 rows 49 against 53, 96 rows 88 against 55; float16, 24 rows of 3
+// heads, which do not share a tile, 84 against 184 at 58 x 6,800).
 Way way_of(const PagedArgs &a, int dtype, int cache_dtype) {
-  const bool step = paged_step_takes(a, dtype, cache_dtype);
-  if (step && (long long)a.Lq * a.G <= kPagedStepRows) return kStep;
-  // the step kernel stands in where q or out does not suit TMA
+  const bool step = paged_step_takes(a, dtype, cache_dtype), e8 = cache_dtype == kE4M3;
+  const int P = attn_row_pack(a.G);
+  const long long few = ((long long)a.Lq * a.G + 15) / 16, many = a.G / P * (((long long)a.Lq * P + 127) / 128);
+  if (step && (e8 ? 12 * few <= 24 + 29 * many : 18 * few <= 29 * many)) return kStep;
+  // the few-rows kernel stands in where q or out does not suit TMA
   return step && dtype == cache_dtype && paged_tc_takes(a, dtype) ? kTensor : kGather;
 }
 
