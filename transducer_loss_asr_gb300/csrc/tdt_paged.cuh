@@ -97,6 +97,9 @@ cudaError_t launch_cache_read(const CacheArgs &a, int dtype, int cache_dtype, cu
 // Few query rows: a kernel that reads k and v at memory speed.  (It takes any number of rows; *_takes go by sizes and pages.)
 bool paged_step_takes(const PagedArgs &a, int dtype, int cache_dtype);
 cudaError_t launch_paged_step(const PagedArgs &a, int dtype, int cache_dtype, cudaStream_t stream);
+// The same of up to kStepRows float32 rows, on the CUDA cores.
+bool paged_step32_takes(const PagedArgs &a, int dtype, int cache_dtype);
+cudaError_t launch_paged_step32(const PagedArgs &a, int cache_dtype, cudaStream_t stream);
 // Many query rows on the tensor cores: which calls (paged_tc_fits: by q and out, too), and the workspace for up to `most`
 // positions an utterance.
 bool paged_tc_takes(const PagedArgs &a, int dtype);

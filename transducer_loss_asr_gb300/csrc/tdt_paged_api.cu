@@ -133,7 +133,7 @@ PagedArgs attn_args(const int64_t sizes[4], const tdt_paged_cache *c) {
   a.t.max_pages = (int)sizes[3];
   return a;
 }
-enum Way { kStep, kTensor, kGather };
+enum Way { kStep, kStep32, kTensor, kGather };
 // The few-rows kernel reads k and v once for each 16 rows of a key head, the tensor-core kernel once for each row tile of each
 // group of P heads; e4m3 pages are laid out densely for the latter first.  Costs of a read in microseconds at 16 x 2,000
 // positions of 4 heads of 128, bfloat16 and e4m3: 18 (12) of the first kernel, 29 of the second, 24 of the layout (20 rows of 4
@@ -144,6 +144,7 @@ Way way_of(const PagedArgs &a, int dtype, int cache_dtype) {
   const int P = attn_row_pack(a.G);
   const long long few = ((long long)a.Lq * a.G + 15) / 16, many = a.G / P * (((long long)a.Lq * P + 127) / 128);
   if (step && (e8 ? 12 * few <= 24 + 29 * many : 18 * few <= 29 * many)) return kStep;
+  if (paged_step32_takes(a, dtype, cache_dtype)) return kStep32;
   // the few-rows kernel stands in where q or out does not suit TMA
   return step && dtype == cache_dtype && paged_tc_takes(a, dtype) ? kTensor : kGather;
 }
@@ -258,7 +259,7 @@ size_t tdt_paged_attn_workspace_size(const int64_t sizes[4], int dtype, const td
   if (check_attn(sizes, dtype, cache) != TDT_OK || sizes[0] == 0 || sizes[1] == 0) return 0;
   const PagedArgs a = attn_args(sizes, cache);
   const Way way = way_of(a, dtype, cache->dtype);
-  if (way == kStep) return 0;
+  if (way == kStep || way == kStep32) return 0;
   if (way == kTensor)
     return paged_tc_workspace(a.B, a.Lq, sizes[3] * cache->page_size, a.H, a.Hkv, a.D);
   return gather_space(sizes, dtype, cache).total;
@@ -304,8 +305,9 @@ int tdt_paged_attn(const void *q, const int64_t sizes[4], const int64_t strides[
   a.lse = lse;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (way == kGather) return attend_gathered(a, sizes, strides, dtype, cache, workspace, workspace_bytes, s);
-  const cudaError_t e = way == kTensor && paged_tc_fits(a, dtype) ? launch_paged_tc(a, dtype, workspace, s)
-                                                                  : launch_paged_step(a, dtype, cache->dtype, s);
+  const cudaError_t e = way == kStep32                              ? launch_paged_step32(a, cache->dtype, s)
+                        : way == kTensor && paged_tc_fits(a, dtype) ? launch_paged_tc(a, dtype, workspace, s)
+                                                                    : launch_paged_step(a, dtype, cache->dtype, s);
   return e == cudaSuccess ? TDT_OK : TDT_ERR_CUDA;
 }
 
