@@ -226,7 +226,8 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
  *            then out; inputs >= 0; no two elements of out may share an address.
  *   dtype    of q and out; pages that are not TDT_DTYPE_E4M3 have the same.
  *            Scores, the softmax, sums and lse are held in float32; values
- *            of e4m3 pages enter as they are, without a rounding in between.
+ *            of e4m3 pages enter as they are, without a rounding in between
+ *            (but with float16 queries they may end at 65504).
  *   kv_lens, q_lens, page_table  as in tdt_cache_write.  Lengths out of range
  *            give that utterance NaN; a page outside [0, n_pages) gives NaN to
  *            the queries that see it, and may to the utterance's others.
@@ -236,7 +237,11 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
  *   workspace  device, 256-byte aligned, at least
  *            tdt_paged_attn_workspace_size(sizes, dtype, cache) bytes; may be
  *            NULL when that is 0.  Not used by anything else until the stream
- *            has passed the call.
+ *            has passed the call.  Many queries over e4m3 pages, and what the
+ *            paged kernels do not take (float32 with many queries, heads over
+ *            128, rows that no 16-byte access fits, pages of under 8 places), need
+ *            room for B * max_pages * page_size dense rows of k and v of `dtype`:
+ *            a table that is no wider than needed keeps it small.
  */
 size_t tdt_paged_attn_workspace_size(const int64_t sizes[4], int dtype, const tdt_paged_cache *cache);
 

@@ -606,8 +606,9 @@ def tdt_paged_attn(q, cache, page_table, kv_lens, q_lens=None, scale=None, need_
     Query i < q_lens[b] of utterance b is at position kv_lens[b] - q_lens[b] + i and sees the positions
     up to its own; queries past q_lens[b] (None: all Lq) get 0.  Pages are of q's dtype or
     float8_e4m3fn.  scale: 1 / sqrt(D) unless given.  workspace: a contiguous uint8 tensor of
-    tdt_paged_attn_workspace_size bytes at least, allocated unless given.  Returns (out, lse): out like
-    q, lse float32 [B, H, Lq], or None without need_lse.
+    tdt_paged_attn_workspace_size bytes at least, allocated unless given; where calls need one it may go
+    with the page table's width, so pass a table no wider than needed.  Returns (out, lse): out like q,
+    lse float32 [B, H, Lq], or None without need_lse.
     """
     shape, dtype, dev = q.shape, q.dtype, cache.device
     if len(shape) != 4 or shape[3] != cache.head_dim:
@@ -770,8 +771,9 @@ def tdt_token_logprobs_fwd_bwd(logits, tokens, grad_logprobs=None, grad_entropy=
     with _on(dev):
         _check(lib.tdt_token_logprobs_fwd_bwd(
             logits.data_ptr(), _pack3(N, V, n_top), _pack2(stride, grad_out.stride(0)),
-            DTYPES[logits.dtype], tokens.data_ptr(), a, b, r.logprobs.data_ptr(), r.entropy.data_ptr(), r.stats.data_ptr(), _addr(r.top_tokens),
-            _addr(r.top_logprobs), grad_out.data_ptr(), _raw_stream(dev.index)))
+            DTYPES[logits.dtype], tokens.data_ptr(), a, b, r.logprobs.data_ptr(), r.entropy.data_ptr(),
+            r.stats.data_ptr(), _addr(r.top_tokens), _addr(r.top_logprobs), grad_out.data_ptr(),
+            _raw_stream(dev.index)))
     return r, grad_out
 
 

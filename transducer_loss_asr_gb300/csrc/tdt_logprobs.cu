@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     }
     const bool lost = !(r.s > 0.0f && r.s < INFINITY) || !(fabsf(r.m) < INFINITY);  // NaN, +inf, or nothing but -inf
     log2_s = lost ? NAN : log2f(r.s);
-    ent = lost ? NAN : (log2_s - r.t / r.s) * kLn2f;
+    ent = lost ? NAN : fmaxf((log2_s - r.t / r.s) * kLn2f, 0.0f);
     R = r.R;
     m = r.m;
     const float ln_s = lost ? NAN : -log2_of(m) * kLn2f;
