@@ -26,8 +26,9 @@ struct Pieces {
   int lane_bits;       // of the lanes that share a row
   int unit;            // pieces of a position: Hkv << lane_bits
   int chunk;           // positions of a block's round
-  unsigned div_m;      // division by `unit`
-  int div_s;
+  unsigned rounds, chunks;  // of the call, of an utterance
+  unsigned div_m, by_m;     // division by `unit`, by `chunks` (64-bit divisions took more instructions than all else)
+  int div_s, by_s;
 };
 
 // 16 elements of a type as they lie in memory, and how many pieces a thread holds.
@@ -160,14 +161,15 @@ __device__ __forceinline__ At piece_at(const Pieces &q, int x) {
 
 // blockIdx.y: keys or values.  PT: the pages' type, DT or kE4M3.
 template <int DT, int PT, bool VEC>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
+__global__ void __launch_bounds__(kThreads, 5) cache_write_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
   constexpr int U = Raw<DT>::U, ES = Raw<DT>::ES;
   const Pages &p = blockIdx.y ? a.pv : a.pk;
   const Strides &s = blockIdx.y ? a.sv : a.sk;
-  const int chunks = (a.L + q.chunk - 1) / q.chunk, units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
-  for (long long c = blockIdx.x; c < a.B * chunks; c += gridDim.x) {
-    const long long b = c / chunks;
-    const int i0 = (int)(c - b * chunks) * q.chunk;
+  const int units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
+  for (unsigned c = blockIdx.x; c < q.rounds; c += gridDim.x) {
+    const unsigned utt = fast_div(c, q.by_m, q.by_s);
+    const long long b = utt;
+    const int i0 = (int)(c - utt * q.chunks) * q.chunk;
     const NewRows n = new_rows(a.t, b, a.L);
     if (i0 >= n.n) continue;
     const unsigned char *src = static_cast<const unsigned char *>(blockIdx.y ? a.v : a.k);
@@ -218,14 +220,15 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
 }
 
 template <int DT, int PT, bool VEC>
-__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
+__global__ void __launch_bounds__(kThreads, 5) cache_read_kernel(const __grid_constant__ CacheArgs a, const __grid_constant__ Pieces q) {
   constexpr int U = Raw<PT>::U;
   const Pages &p = blockIdx.y ? a.pv : a.pk;
   const Strides &s = blockIdx.y ? a.sv : a.sk;
-  const int chunks = (a.L + q.chunk - 1) / q.chunk, units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
-  for (long long c = blockIdx.x; c < a.B * chunks; c += gridDim.x) {
-    const long long b = c / chunks;
-    const int i0 = (int)(c - b * chunks) * q.chunk;
+  const int units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
+  for (unsigned c = blockIdx.x; c < q.rounds; c += gridDim.x) {
+    const unsigned utt = fast_div(c, q.by_m, q.by_s);
+    const long long b = utt;
+    const int i0 = (int)(c - utt * q.chunks) * q.chunk;
     const NewRows n = new_rows(a.t, b, a.L);
     unsigned char *dst = static_cast<unsigned char *>(blockIdx.y ? a.v : a.k);
     for (int x0 = threadIdx.x; x0 < units; x0 += U * kThreads) {
@@ -261,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 // are; float16 ends at 65504.  Beside them the positions that each query sees, and lengths that cross attention refuses where
 // this call's are out of range.
 template <int DT, int PT, bool VEC>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant__ GatherArgs f, const __grid_constant__ Pieces q) {
+__global__ void __launch_bounds__(kThreads, 5) gather_kernel(const __grid_constant__ GatherArgs f, const __grid_constant__ Pieces q) {
   constexpr int U = Raw<PT>::U;
   const CacheArgs &a = f.c;
   for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < a.B * f.Lq && blockIdx.y == 0;
@@ -274,10 +277,11 @@ __global__ void __launch_bounds__(kThreads) gather_kernel(const __grid_constant_
   }
   const Pages &p = blockIdx.y ? a.pv : a.pk;
   const Strides &s = blockIdx.y ? a.sv : a.sk;
-  const int chunks = (a.L + q.chunk - 1) / q.chunk, units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
-  for (long long c = blockIdx.x; c < a.B * chunks; c += gridDim.x) {
-    const long long b = c / chunks;
-    const int i0 = (int)(c - b * chunks) * q.chunk;
+  const int units = q.chunk * q.unit, place_mask = (1 << a.t.page_bits) - 1;
+  for (unsigned c = blockIdx.x; c < q.rounds; c += gridDim.x) {
+    const unsigned utt = fast_div(c, q.by_m, q.by_s);
+    const long long b = utt;
+    const int i0 = (int)(c - utt * q.chunks) * q.chunk;
     const NewRows n = new_rows(a.t, b, f.Lq);
     const int end = n.first + n.n;
     if (i0 >= end) continue;
@@ -326,16 +330,20 @@ Pieces pieces_of(const CacheArgs &a, int in_flight) {
   while (kPiece << q.lane_bits < a.D) ++q.lane_bits;
   q.unit = a.Hkv << q.lane_bits;
   q.chunk = std::max(1, in_flight * kThreads / q.unit);
+  auto chunks = [&] { return (a.L + (long long)q.chunk - 1) / q.chunk; };
+  while (a.B * chunks() > 0x7fffffffLL / 2 && q.chunk < a.L) q.chunk *= 2;  // rounds count in 32 bits; B < 2^30
+  q.chunks = (unsigned)std::max<long long>(1, chunks());
+  q.rounds = (unsigned)(a.B * chunks());
   fast_div_setup(q.unit, &q.div_m, &q.div_s);
+  fast_div_setup(q.chunks, &q.by_m, &q.by_s);
   return q;
 }
 // Blocks for `rounds` rounds: all of them, up to two waves of eight blocks an SM (of keys, and of values).
 dim3 grid_of(long long rounds) { return dim3((unsigned)std::max<long long>(1, std::min<long long>(rounds, 8 * kSMs)), 2); }
-long long rounds_of(const CacheArgs &a, const Pieces &q) { return a.B * ((a.L + q.chunk - 1) / q.chunk); }
 
 template <int DT, int PT> cudaError_t write(const CacheArgs &a, cudaStream_t stream) {
   const Pieces q = pieces_of(a, Raw<DT>::U);
-  const dim3 grid = grid_of(rounds_of(a, q));
+  const dim3 grid = grid_of(q.rounds);
   if (vectors(a, DT, PT))
     cache_write_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(a, q);
   else
@@ -344,7 +352,7 @@ template <int DT, int PT> cudaError_t write(const CacheArgs &a, cudaStream_t str
 }
 template <int DT, int PT> cudaError_t read(const CacheArgs &a, cudaStream_t stream) {
   const Pieces q = pieces_of(a, Raw<PT>::U);
-  const dim3 grid = grid_of(rounds_of(a, q));
+  const dim3 grid = grid_of(q.rounds);
   if (vectors(a, DT, PT))
     cache_read_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(a, q);
   else
@@ -353,7 +361,7 @@ template <int DT, int PT> cudaError_t read(const CacheArgs &a, cudaStream_t stre
 }
 template <int DT, int PT> cudaError_t gather(const GatherArgs &f, cudaStream_t stream) {
   const Pieces q = pieces_of(f.c, Raw<PT>::U);
-  const dim3 grid = grid_of(std::max(rounds_of(f.c, q), (f.c.B * f.Lq + kThreads - 1) / kThreads));
+  const dim3 grid = grid_of(std::max<long long>(q.rounds, (f.c.B * f.Lq + kThreads - 1) / kThreads));
   if (vectors(f.c, DT, PT))
     gather_kernel<DT, PT, true><<<grid, kThreads, 0, stream>>>(f, q);
   else
