@@ -23,7 +23,7 @@
 //
 // 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 70 us, backward 125 us (5.8 TB/s), both in one call 172 us
 // (4.2 TB/s: reading and writing a row take turns, four CTAs an SM).  2,048 x 131,072 bfloat16: 96 us (5.6 TB/s), with twenty
-// alternatives 141 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
+// alternatives 118 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
 // float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072: two CTAs 111 us, four 143).
 #include <cooperative_groups.h>
 #include <math.h>
@@ -136,8 +136,10 @@ __device__ __forceinline__ int index_of(unsigned long long key) { return (int)(0
 template <int T> struct TopShared {
   static constexpr int LIST = T == 32 ? 288 : 1024;
   static constexpr int GROUPS = T == 32 ? 1 : 16;  // of a thread's batches of vectors
+  static constexpr int PAIRS = T == 32 ? 32 : 1024;
   unsigned long long list[LIST];
   float group_max[GROUPS][T];
+  int pairs[PAIRS];  // groups of batches that reach the threshold: group * T + thread
 };
 
 // A group's shared memory.
@@ -145,7 +147,7 @@ template <int T> struct GroupShared {
   Sums sums[T / 32];
   float least[T / 32];
   unsigned long long best[T / 32];  // of the passes that stand in for a list that overflows
-  int count;
+  int count, pairs;
   unsigned long long top[kMostTop];  // the stretch's own alternatives, ranked
   int top_n;
   Sums row;                // of the stretch, for the cluster
@@ -296,7 +298,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
         const float other = __shfl_sync(0xffffffffu, r.m, i);
         ahead += other > r.m || (other == r.m && i < lane);
       }
-      if (tid == 0) sh.count = 0;
+      if (tid == 0) sh.count = sh.pairs = 0;
       if (warp >= full || want > 32) {
         if (lane == 0) sh.least[warp] = want > 32 ? -INFINITY : INFINITY;
       } else if (ahead == want - 1) {
@@ -312,23 +314,33 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
           if (k < TopShared<T>::LIST) lists.list[k] = key_of(v, i);
         }
       };
+      auto look = [&](int v) {  // at a vector
+        const uint4 x4 = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)v * N));
+        if (vector_max<DT>(x4) >= threshold) {
+          float y[N];
+          unpack<DT>(x4, y);
+#pragma unroll
+          for (int i = 0; i < N; ++i) note(y[i], w.head + v * N + i);
+        }
+      };
+      // Groups of batches that reach it are shared out, a vector a thread (a thread that looked through its own would wait
+      // for memory once for each, and its warp for all of its lanes': 141 us against 118 of 2,048 x 131,072, n_top 20).
       if (r.m >= threshold) {
-        auto look = [&](int v0) {
-          load(v0, raw);
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-            if (v0 + u * T < w.last) {
-              float v[N];
-              unpack<DT>(raw[u], v);
-              if (vector_max<DT>(raw[u]) >= threshold)
-#pragma unroll
-                for (int i = 0; i < N; ++i) note(v[i], w.head + (v0 + u * T) * N + i);
-            }
-        };
         for (int i = 0; i < group; ++i)
-          if (lists.group_max[i][tid] >= threshold)
-            for (int k = i * per; k < min((i + 1) * per, batches); ++k) look(w.first + tid + k * U * T);
+          if (lists.group_max[i][tid] >= threshold) {
+            const int k = atomicAdd(&sh.pairs, 1);
+            if (k < TopShared<T>::PAIRS)
+              lists.pairs[k] = i * T + tid;
+            else  // many equal elements
+              for (int v = w.first + tid + i * per * U * T; v < min(w.last, w.first + (i + 1) * per * U * T); v += T) look(v);
+          }
         if (loose_at >= 0) note(loose_x, loose_at);
+      }
+      group_sync<T>();
+      const int found = min(sh.pairs, TopShared<T>::PAIRS), each = per * U;  // vectors of a pair
+      for (int k = tid; k < found * each; k += T) {
+        const int p = lists.pairs[k / each], v = w.first + p % T + (p / T * each + k % each) * T;
+        if (v < w.last) look(v);
       }
     }
     // threads, then warps, then CTAs
