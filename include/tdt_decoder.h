@@ -227,7 +227,11 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
  *   dtype    of q and out; pages that are not TDT_DTYPE_E4M3 have the same.
  *            Scores, the softmax, sums and lse are held in float32; values
  *            of e4m3 pages enter as they are, without a rounding in between
- *            (but with float16 queries they may end at 65504).
+ *            (but with float16 queries they may end at 65504).  Weights of
+ *            16-bit calls are rounded to 16 bits; with few queries over e4m3
+ *            pages to float16, times the value row's power of two relative to
+ *            the utterance's largest: weights of rows more than 2^20 smaller
+ *            than that one lose bits.
  *   kv_lens, q_lens, page_table  as in tdt_cache_write.  Lengths out of range
  *            give that utterance NaN; a page outside [0, n_pages) gives NaN to
  *            the queries that see it, and may to the utterance's others.

@@ -296,3 +296,49 @@ def test_nothing_to_do(binding):
     q = torch.full((1, 3, 4, 64), math.nan, dtype=torch.bfloat16, device="cuda")
     out, lse = binding.tdt_paged_attn(q, cache, table[:, :0], i64([0]), i64([0]), need_lse=True)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", CACHES, ids=IDS)
+@pytest.mark.parametrize("Lq", [1, 5, 20, 60, 130])
+def test_queries_and_outputs_on_odd_addresses(binding, dtype, cache_dtype, Lq):
+    """Pages that suit every kernel, queries and outputs that do not."""
+    cache, table, k, v = make(binding, [300, Lq], 2, 64, 32, cache_dtype, 11)
+    g = torch.Generator(device="cuda").manual_seed(Lq)
+    q = torch.randn(2, Lq, 4, 67, generator=g, device="cuda").to(dtype)[..., 1:65]
+    wide = torch.full((2, Lq, 4, 71), 7.0, dtype=dtype, device="cuda")
+    lens = i64([300, Lq])
+    out, tol, lse, t_lse = _reference(q, k, v, lens, i64([Lq, Lq]), 0.125)
+    got, got_lse = binding.tdt_paged_attn(q, cache, table, lens, out=wide[..., 5:69], need_lse=True)
+    _near("out", got, out, tol)
+    _near("lse", got_lse, lse, t_lse)
+    assert bool((wide[..., :5] == 7.0).all()) and bool((wide[..., 69:] == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", CACHES, ids=IDS)
+@pytest.mark.parametrize("Lq", [1, 40])
+def test_one_page_heads_of_stride_zero_and_shared_queries(binding, dtype, cache_dtype, Lq):
+    cache, table, k, v = make(binding, [77, 50], 1, 64, 128, cache_dtype, 12)
+    heads = [None if t is None else t.expand(-1, -1, 3, *([-1] * (t.dim() - 3))) for t in (cache.k, cache.v, cache.k_scales, cache.v_scales)]
+    shared = binding.PagedCache(*heads)
+    one = binding.PagedCache(*(None if t is None else t[int(table[0, 0]):int(table[0, 0]) + 1] for t in heads))
+    g = torch.Generator(device="cuda").manual_seed(Lq)
+    q = torch.randn(1, Lq, 6, 64, generator=g, device="cuda").to(dtype).expand(2, -1, -1, -1)
+    k, v = (t.expand(-1, -1, 3, -1) for t in (k, v))
+    lens = i64([77, 50])
+    out, tol, _, _ = _reference(q, k, v, lens, i64([Lq, Lq]), 0.125)
+    _near("out", binding.tdt_paged_attn(q, shared, table, lens)[0], out, tol)
+    zero = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    _near("out", binding.tdt_paged_attn(q[:1], one, zero, lens[:1])[0], out[:1], tol[:1])
+
+
+@pytest.mark.parametrize("dtype,cache_dtype", CACHES, ids=IDS)
+@pytest.mark.parametrize("Lq", [3, 200])
+def test_no_pages_and_no_new_rows(binding, dtype, cache_dtype, Lq):
+    cache, table, _, _ = make(binding, [20], 2, 64, 16, cache_dtype)
+    q = torch.full((2, Lq, 4, 64), math.nan, dtype=dtype, device="cuda")
+    table = table.expand(2, -1)
+    for t, lens in ((table[:, :0], [0, 0]), (table, [20, 0])):
+        out, lse = binding.tdt_paged_attn(q, cache, t, i64(lens), i64([0, 0]), need_lse=True)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    out, _ = binding.tdt_paged_attn(q, cache, table[:, :0], i64([1, 0]), i64([1, 0]))
+    assert bool(out[0].isnan().all()) and bool((out[1] == 0).all())

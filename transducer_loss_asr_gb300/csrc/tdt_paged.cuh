@@ -68,7 +68,6 @@ __device__ __forceinline__ unsigned float2_to_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ float e4m3_to_float(unsigned char x) { return e4m3x2_to_float2(x).x; }
 
 // One call of attention over pages, passed by value.
 struct PagedArgs {
