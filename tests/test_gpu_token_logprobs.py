@@ -240,6 +240,25 @@ def test_masks_of_the_types_lowest_value_and_few_allowed_tokens(binding, V, dtyp
     _check(binding, x, tokens, K, a, b, g)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("V", [30, 700, 8193, 50257])
+def test_logits_at_the_ends_of_the_range(binding, V, dtype):
+    """Products with log2 e of such logits, or their differences, leave float32's range; p and the entropy do not."""
+    N = 10
+    x, tokens, a, b, g = _inputs(N, V, dtype, 13)
+    low = torch.finfo(dtype).min
+    x[0], x[1], x[2] = -math.inf, low, -(2.0 ** 126)
+    x[3] = x[3].float() * 1e37
+    x[4] = torch.where(torch.arange(V, device="cuda") % 2 == 0, low, -math.inf).to(dtype)
+    x[5], x[6], x[7] = low, -math.inf, low
+    x[8], x[9] = -1.5e38, -math.inf
+    for i, top in enumerate((2.0 ** 126, 2.0 ** 126, 2.0 ** 126, 1.75 * 2.0 ** 126, 2.0 ** 100, 2.0 ** 127, -(2.0 ** 126), -(2.0 ** 126), 1e38, -1.5e38)):
+        x[i, V // 3] = x[i, V // 2 + 1] = x[i, V - 1] = top  # an entropy of ln 3
+    tokens[:] = V // 2 + 1
+    _check(binding, x, tokens, 3, a, b, g)
+    assert torch.allclose(binding.tdt_token_logprobs_fwd(x, tokens).entropy.cpu(), torch.full((N,), math.log(3.0)), atol=1e-5, rtol=0)
+
+
 def test_missing_weights(binding):
     x, tokens, a, b, g = _inputs(5, 700, torch.float32, 3)
     r = binding.tdt_token_logprobs_fwd(x, tokens, 4)

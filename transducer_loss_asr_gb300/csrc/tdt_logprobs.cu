@@ -12,7 +12,7 @@
 //   z_i = x_i L - R (one fma; L = log2 e in float32),   s = sum 2^z_i,   t = sum 2^z_i z_i,
 // so z is rounded once, at its own size, and what L is off by stays in differences to the maximum: m L - R is the same
 // product.  A thread holds its own R, s and t; R moves only where the maximum has grown by 8.  They are joined in a
-// fixed order.  Where that leaves no sum (a row of numbers at the ends of float32's range), x_i - m is formed instead.
+// fixed order.  Where R is past 2^24, whole numbers that float32 does not hold, x_i - m is formed instead.
 // A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
 // exchange their results through distributed shared memory.
 // Alternatives: at least n_top elements reach a threshold that comes from the threads' maxima (the ceil(n_top / warps)-th largest
@@ -23,7 +23,7 @@
 //
 // 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 70 us, backward 125 us (5.8 TB/s), both in one call 172 us
 // (4.2 TB/s: reading and writing a row take turns, four CTAs an SM).  2,048 x 131,072 bfloat16: 96 us (5.6 TB/s), with twenty
-// alternatives 118 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
+// alternatives 110 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
 // float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072: two CTAs 111 us, four 143).
 #include <cooperative_groups.h>
 #include <math.h>
@@ -45,6 +45,7 @@ constexpr int kMostCtas = 8;   // of a cluster
 constexpr float kLn2f = 0.69314718055994531f;
 constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
 constexpr float kLazy = 8.0f;
+constexpr float kMostR = 16777216.0f;  // whole numbers to here are exact, and x L - R is held to half a unit where x is the maximum
 
 struct RowArgs {
   const void *x;
@@ -308,8 +309,9 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       float threshold = sh.least[0];
 #pragma unroll
       for (int i = 1; i < WARPS; ++i) threshold = fminf(threshold, sh.least[i]);
+      threshold = fmaxf(threshold, -3.402823466e38f);  // not -inf entries
       auto note = [&](float v, int i) {
-        if (v >= threshold && v > -INFINITY) {
+        if (v >= threshold) {
           const int k = atomicAdd(&sh.count, 1);
           if (k < TopShared<T>::LIST) lists.list[k] = key_of(v, i);
         }
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
         }
       };
       // Groups of batches that reach it are shared out, a vector a thread (a thread that looked through its own would wait
-      // for memory once for each, and its warp for all of its lanes': 141 us against 118 of 2,048 x 131,072, n_top 20).
+      // for memory once for each, and its warp for all of its lanes': 141 us against 110 of 2,048 x 131,072, n_top 20).
       if (r.m >= threshold) {
         for (int i = 0; i < group; ++i)
           if (lists.group_max[i][tid] >= threshold) {
@@ -412,8 +414,8 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       }
     }
     group_sync<T>();
-    if (!(r.s > 0.0f && r.s < INFINITY) && fabsf(r.m) < INFINITY) {
-      // NaN in the row, or numbers that a product with L takes out of range: against the maximum itself, by every CTA
+    if (!(r.s > 0.0f && r.s < INFINITY && fabsf(r.R) <= kMostR) && fabsf(r.m) < INFINITY) {
+      // NaN in the row, or numbers so large that a product with L loses whole units: against the maximum itself, by every CTA
       r.s = r.t = 0.0f;
       for (int i = tid; i < a.V; i += T) {
         const float z = max_nan((at(i) - r.m) * kLog2e, kLeastZ), p = fast_exp2(z);
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
         const float2 st = a.in_stats[n];
         m = st.x;
         R = rintf(m * kLog2e);
-        if (!(fabsf(R) < 3e38f)) R = INFINITY;
+        if (!(fabsf(R) <= kMostR)) R = INFINITY;
         log2_s = st.y * kLog2e + (R < INFINITY ? fmaf(m, kLog2e, -R) : 0.0f);
         ent = a.gb ? a.in_entropy[n] : 0.0f;
       }
