@@ -159,6 +159,7 @@ int tdt_sample(const void *logits, const int64_t sizes[2], int64_t row_stride, i
  *   k_scales, v_scales  device uint8 [n_pages, page_size, n_heads], with
  *               TDT_DTYPE_E4M3 only (else NULL): a row of head_dim elements
  *               stands for e4m3 * 2^(byte - 127); byte 255: for NaN.
+ *               (Rounding may take what is past 1.9375 * 2^127 to infinity.)
  *   n_pages     in [1, 2^31).   page_size  a power of two, at most 2^16.
  *   n_heads >= 1, 1 <= head_dim <= 256.
  *   strides     elements, of (page, place, head) of k_pages, v_pages,

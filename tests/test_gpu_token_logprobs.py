@@ -340,6 +340,17 @@ def test_autograd_against_the_formula_and_differences(binding):
         assert abs(float(mine - slope)) <= 2e-5 * float((x.grad.double() * d).abs().sum()) + 1e-6
 
 
+def test_tokens_that_are_slices(binding):
+    from transducer_loss_asr_gb300.autograd import token_logprobs
+
+    x, tokens, *_ = _inputs(12, 50, torch.float32, 3)
+    want = token_logprobs(x, tokens)[0]
+    wide = torch.stack((tokens, tokens + 1), 1)
+    assert torch.equal(token_logprobs(x, wide[:, 0])[0], want)
+    assert torch.equal(token_logprobs(x.view(3, 4, 50), wide.view(3, 4, 2)[..., 0])[0], want.view(3, 4))
+    assert torch.equal(token_logprobs(x.view(3, 4, 50).transpose(0, 1), tokens.view(3, 4).t())[0], want.view(3, 4).t())
+
+
 def test_compiled_opcheck_and_a_captured_backward(binding):
     from transducer_loss_asr_gb300 import autograd
 

@@ -303,3 +303,6 @@ def test_token_logprobs_op_fake_shapes_and_cpu_rejection(lib):
     assert torch.ops.tdt_gb300.token_logprobs_backward(lp, ent, None, x, t, ent, stats, top).shape == x.shape
     with pytest.raises(NotImplementedError):  # CUDA kernels only: no silent CPU path
         autograd.token_logprobs(torch.zeros(6, 50), torch.zeros(6, dtype=torch.int64))
+    for shape in ((3, 2), (6,), (2, 3, 1)):  # as many tokens, of other rows
+        with pytest.raises(ValueError):
+            autograd.token_logprobs(torch.zeros(2, 3, 50), torch.zeros(shape, dtype=torch.int64))

@@ -289,7 +289,10 @@ def token_logprobs(logits: Tensor, tokens: Tensor,
     (alternatives -1 and -inf).  -sum(logprobs) is the cross entropy of the labels.
     """
     V, shape = logits.shape[-1], tokens.shape
-    lp, entropy, _, top, top_lp = token_logprobs_forward(logits.reshape(-1, V), tokens.reshape(-1), int(n_top))
+    if logits.shape[:-1] != shape:
+        raise ValueError("tokens must be of shape %s" % (tuple(logits.shape[:-1]),))
+    lp, entropy, _, top, top_lp = token_logprobs_forward(
+        logits.reshape(-1, V), tokens.reshape(-1).contiguous(), int(n_top))
     return lp.view(shape), entropy.view(shape), top.view(*shape, n_top), top_lp.view(*shape, n_top)
 
 
