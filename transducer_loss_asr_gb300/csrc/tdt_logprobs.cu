@@ -42,6 +42,7 @@ namespace cg = cooperative_groups;
 constexpr int kBlock = 256;
 constexpr int kMostTop = 64;
 constexpr int kMostCtas = 8;   // of a cluster
+constexpr int kMostBatches = 5;  // of a stretch that is kept: 64 KB and a vector in 16 KB each
 constexpr float kLn2f = 0.69314718055994531f;
 constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
 constexpr float kLazy = 8.0f;
@@ -156,6 +157,13 @@ template <int T> struct GroupShared {
   int own_at[kMostTop + 1];
 };
 
+// `bytes` (a multiple of 16) to shared memory, both addresses on 16 bytes; they arrive at `bar`.
+__device__ __forceinline__ void bulk_load(void *to, const void *from, unsigned bytes, unsigned long long *bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(to)), "l"(from),
+               "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 template <int T> __device__ __forceinline__ void group_sync() {
   if (T == 32)
     __syncwarp();
@@ -196,6 +204,8 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
   float R = 0.0f, m = 0.0f, log2_s = 0.0f, ent = 0.0f;
   auto log2_of = [&](float v) { return (R < INFINITY ? fmaf(v, kLog2e, -R) : (v - m) * kLog2e) - log2_s; };
   extern __shared__ __align__(16) uint4 kept_row[];
+  __shared__ unsigned long long full[kMostBatches];
+  __shared__ int gave_up;
   TopShared<T> &lists = reinterpret_cast<TopShared<T> *>(kept_row + a.keep)[threadIdx.x / T];
   if (FWD && !real && part == 0) {
     const float none = token < 0 ? 0.0f : NAN;
@@ -252,10 +262,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       for (int u = 0; u < U; ++u)
         if (v0 + u * T < w.last) raw[u] = ld_row16<IN_PLACE>(reinterpret_cast<const uint4 *>(body + (long long)(v0 + u * T) * N));
     };
-    uint4 raw[U], next[U];
-    load(w.first + tid, raw);
-    for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
-      load(v0 + U * T, next);
+    auto take = [&](int v0, const uint4 (&raw)[U]) {
       float most = vector_max<DT>(raw[0]);
 #pragma unroll
       for (int u = 1; u < U; ++u)
@@ -264,7 +271,6 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (v0 + u * T < w.last) {
-          if (keep) kept_row[v0 + u * T - w.first] = raw[u];
           float v[N];
           unpack_held<DT>(raw[u], v);
           add_vector(v);
@@ -277,8 +283,48 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
           left = per;
         }
       }
+    };
+    uint4 raw[U];
+    if (keep) {  // asked for at once, and waited for a batch at a time
+      if constexpr (BWD && T > 32) {
+        const int first = w.first, vectors = w.last - w.first;
+        if (tid == 0) {
+          gave_up = 0;
+          for (int i = 0; i < batches; ++i) mbar_init(&full[i], 1);
+          fence_mbar_init_cluster();
+          for (int i = 0; i < batches; ++i) {
+            const int here = min(U * T, vectors - i * U * T);
+            arrive_expect_tx(&full[i], here * 16);
+            bulk_load(kept_row + i * U * T, body + (long long)(first + i * U * T) * N, here * 16, &full[i]);
+          }
+        }
+        __syncthreads();
+        const Waiter wait{&gave_up};
+        bool ok = true;
+        for (int i = 0; i < batches; ++i) {
+          ok = ok && wait(&full[i], 0);
+          const int v0 = first + tid + i * U * T;
+          if (!ok || v0 >= w.last) break;
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = next[u];
+          for (int u = 0; u < U; ++u)
+            if (v0 + u * T < w.last) raw[u] = kept_row[v0 + u * T - first];
+          take(v0, raw);
+        }
+        if (!ok) {
+          r.m = INFINITY;  // outputs become NaN
+          if (tid == 0)    // copies in flight land before the CTA ends
+            for (int i = 0; i < batches; ++i) Waiter::drain(&full[i], 0);
+        }
+      }
+    } else {
+      uint4 next[U];
+      load(w.first + tid, raw);
+      for (int v0 = w.first + tid; v0 < w.last; v0 += U * T) {
+        load(v0 + U * T, next);
+        take(v0, raw);
+#pragma unroll
+        for (int u = 0; u < U; ++u) raw[u] = next[u];
+      }
     }
     if (K > 0 && group < GROUPS) lists.group_max[group++][tid] = best;  // each thread reads its own
     if (loose_at >= 0) {
