@@ -62,7 +62,7 @@ struct RowArgs {
   const float *ga, *gb, *gc;
   unsigned N;
   int V, K;
-  int ctas;           // CTAs of a row
+  int cta_bits;       // log2 of the CTAs of a row
   int keep;           // vectors of a stretch that stay in dynamic shared memory for the backward pass (0: none do)
 };
 
@@ -171,16 +171,17 @@ template <int T> __device__ __forceinline__ void group_sync() {
     __syncthreads();
 }
 
-// The vectors [first, last) of 16 bytes that CTA `i` of `n` has of a row at p, and the elements before the first vector.
+// The vectors [first, last) of 16 bytes that CTA `i` of 2^bits has of a row at p, and the elements before the first vector.
+// (Divisions here took as many instructions as the exponentials of 50 elements a thread.)
 struct Stretch {
   int head, first, last, vectors;
 };
-template <int DT> __device__ __forceinline__ Stretch stretch_of(const void *p, int V, int i, int n) {
+template <int DT> __device__ __forceinline__ Stretch stretch_of(const void *p, int V, int i, int bits) {
   Stretch s;
   s.head = min(head_elems<DT>(p), V);
   s.vectors = (V - s.head) / Vec<DT>::N;
-  s.first = (int)((long long)s.vectors * i / n);
-  s.last = (int)((long long)s.vectors * (i + 1) / n);
+  s.first = s.vectors * i >> bits;  // vectors <= 2^22, i < 8
+  s.last = s.vectors * (i + 1) >> bits;
   return s;
 }
 
@@ -192,8 +193,8 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
   __shared__ GroupShared<T> shared[kBlock / T];
   GroupShared<T> &sh = shared[threadIdx.x / T];
   const int tid = threadIdx.x % T, lane = tid & 31, warp = tid >> 5;
-  const int ctas = T == 32 ? 1 : a.ctas, part = T == 32 ? 0 : blockIdx.x % ctas;
-  const unsigned n = T == 32 ? blockIdx.x * (kBlock / 32) + threadIdx.x / 32 : blockIdx.x / ctas;
+  const int bits = T == 32 ? 0 : a.cta_bits, ctas = 1 << bits, part = T == 32 ? 0 : blockIdx.x & (ctas - 1);
+  const unsigned n = T == 32 ? blockIdx.x * (kBlock / 32) + threadIdx.x / 32 : blockIdx.x >> bits;
   if (n >= a.N) return;  // a whole warp (T = 32)
   const E *x = static_cast<const E *>(a.x) + n * a.sx;
   const long long token = a.tokens[n];
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     }
   }
   if (FWD && real) {
-    const Stretch w = stretch_of<DT>(x, a.V, part, ctas);
+    const Stretch w = stretch_of<DT>(x, a.V, part, bits);
     const E *body = x + w.head;
     Sums r = {-INFINITY, -3e38f, 0.0f, 0.0f};
     auto grow = [&](float top) {
@@ -565,7 +566,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
   }
   if (BWD) {
     E *dx = static_cast<E *>(a.dx) + n * a.sdx;
-    const Stretch w = stretch_of<DT>(dx, a.V, part, ctas);
+    const Stretch w = stretch_of<DT>(dx, a.V, part, bits);
     const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
     const int loose_at = part == 0 && tid < loose ? (tid < w.head ? tid : tail + tid - w.head) : -1;
     if (!real) {
@@ -731,9 +732,10 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
   // CTAs of a row: while each has over 256 KB (64 KB that wait in shared memory) or CTAs are too few for the SMs, and
   // keeps 8 KB
   const long long most = FWD && BWD ? 65536 : 262144;
-  a.ctas = 1;
-  while (a.ctas < kMostCtas && bytes / a.ctas > 16384 && (bytes / a.ctas > most || (long long)a.N * a.ctas < 4 * 152)) a.ctas *= 2;
-  const long long kept = bytes / 16 / a.ctas + 1;
+  a.cta_bits = 0;
+  auto share = [&] { return bytes >> a.cta_bits; };
+  while (1 << a.cta_bits < kMostCtas && share() > 16384 && (share() > most || ((long long)a.N << a.cta_bits) < 4 * 152)) ++a.cta_bits;
+  const long long kept = share() / 16 + 1;
   a.keep = FWD && BWD && kept * 16 <= 65536 + 16 ? (int)kept : 0;
   const size_t smem = (size_t)a.keep * 16 + (FWD && a.K > 0 ? sizeof(TopShared<kBlock>) : 0);
   if (FWD && smem > 0) {
@@ -742,17 +744,17 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.N * (unsigned)a.ctas);
+  cfg.gridDim = dim3(a.N << a.cta_bits);
   cfg.blockDim = dim3(kBlock);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = a.ctas;
+  at[0].val.clusterDim.x = 1 << a.cta_bits;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = FWD && a.ctas > 1 ? 1 : 0;
+  cfg.numAttrs = FWD && a.cta_bits > 0 ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, rows_kernel<DT, FWD, BWD, kBlock>, a);
 }
 template <bool FWD, bool BWD> int launch(const RowArgs &a, int dtype, void *stream) {
