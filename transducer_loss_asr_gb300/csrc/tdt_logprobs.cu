@@ -19,12 +19,13 @@
 // of each warp, the least of the warps); only threads whose maximum reaches it, hardly more than n_top, look again, at the
 // batches of vectors whose maximum does.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
 // fills does not matter.  A list that overflows (many equal elements) is given up for n_top passes over the row.
-// Backward: a read and a write of the row; in one call with the forward pass, the row waits in shared memory.
+// Backward: a read and a write of the row; in one call with the forward pass, the row comes in bulk copies that are all asked for
+// at once, and waits in shared memory (loaded by the threads a batch ahead and put there: 173 us for what is 162 with copies).
 //
-// 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 70 us, backward 125 us (5.8 TB/s), both in one call 172 us
-// (4.2 TB/s: reading and writing a row take turns, four CTAs an SM).  2,048 x 131,072 bfloat16: 96 us (5.6 TB/s), with twenty
-// alternatives 110 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in part.  656 x 8,193
-// float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072: two CTAs 111 us, four 143).
+// 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 68 us, backward 125 us (5.8 TB/s), both in one call 147 us
+// (4.9 TB/s: reading and writing a row take turns, four CTAs an SM, 60 % of the issue slots).  2,048 x 131,072 bfloat16: 96 us (5.6
+// TB/s), with twenty alternatives 111 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in
+// part.  656 x 8,193 float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072 scored: two CTAs 104 us, four 143).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -240,20 +241,20 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     const Stretch w = stretch_of<DT>(x, a.V, part, bits);
     const E *body = x + w.head;
     Sums r = {-INFINITY, -3e38f, 0.0f, 0.0f};
+    float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;  // running sums of even and odd elements
     auto grow = [&](float top) {
       r.m = fmaxf(r.m, top);
       const float y = top * kLog2e;
       if (y > r.R + kLazy) {
         const float now = rintf(y), down = fmaxf(r.R - now, kLeastZ), f = fast_exp2(down);
-        r.t = fmaf(down, r.s, r.t) * f;
-        r.s *= f;
+        t2 = make_float2(fmaf(down, s2.x, t2.x) * f, fmaf(down, s2.y, t2.y) * f);
+        s2 = make_float2(s2.x * f, s2.y * f);
         r.R = now;
       }
     };
     const float2 L2 = make_float2(kLog2e, kLog2e);
     auto add_vector = [&](const float (&v)[N]) {
       const float2 neg = make_float2(-r.R, -r.R);
-      float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const float2 z = held<DT>(fma2(make_float2(v[i], v[i + 1]), L2, neg));
@@ -261,8 +262,6 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
         s2 = add2(s2, p);
         t2 = fma2(p, z, t2);
       }
-      r.s += s2.x + s2.y;
-      r.t += t2.x + t2.y;
     };
     // the elements outside whole vectors belong to the first CTA, one a thread
     const int tail = w.head + w.vectors * N, loose = w.head + a.V - tail;
@@ -347,9 +346,11 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
     if (loose_at >= 0) {
       grow(loose_x);
       const float z = max_nan(fmaf(loose_x, kLog2e, -r.R), kLeastZ), p = fast_exp2(z);
-      r.s += p;
-      r.t = fmaf(p, z, r.t);
+      s2.x += p;
+      t2.x = fmaf(p, z, t2.x);
     }
+    r.s = s2.x + s2.y;
+    r.t = t2.x + t2.y;
     if (K > 0) {
       // At least K elements reach the threshold: each warp all of whose lanes have vectors has ceil(K / such warps) lanes that
       // do; in a stretch too short for one, the first warp's lanes that have some.  (Where these are fewer than K, everything
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
         }
       };
       // Groups of batches that reach it are shared out, a vector a thread (a thread that looked through its own would wait
-      // for memory once for each, and its warp for all of its lanes': 141 us against 110 of 2,048 x 131,072, n_top 20).
+      // for memory once for each, and its warp for all of its lanes': 141 us against 111 of 2,048 x 131,072, n_top 20).
       if (r.m >= threshold) {
         for (int i = 0; i < group; ++i)
           if (lists.group_max[i][tid] >= threshold) {
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       };
       const E *body = x + w.head;
       if (FWD && T > 32 && a.keep > 0 && mis == 0) {  // the thread's own vectors: the stretches are the same
-        // (with the choices outside the loop: 154 us against 150 of 4,096 x 50,257)
+        // (the choices outside the loop: 150 us for 154 of 4,096 x 50,257)
         auto finish_kept = [&](auto with_entropy) {
           const uint4 *from = kept_row + tid;
           uint4 *to = reinterpret_cast<uint4 *>(dx + w.head) + w.first + tid;
