@@ -357,17 +357,25 @@ __global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__
       // is listed.)
       const int held_vectors = w.last - w.first, full = max(1, min(WARPS, held_vectors / 32));
       const int want = (K + full - 1) / full <= min(32, held_vectors) ? (K + full - 1) / full : 33;
-      int ahead = 0;  // lanes with a larger maximum (equal ones: in order)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float other = __shfl_sync(0xffffffffu, r.m, i);
-        ahead += other > r.m || (other == r.m && i < lane);
-      }
       if (tid == 0) sh.count = sh.pairs = 0;
       if (warp >= full || want > 32) {
         if (lane == 0) sh.least[warp] = want > 32 ? -INFINITY : INFINITY;
-      } else if (ahead == want - 1) {
-        sh.least[warp] = r.m;
+      } else if (want <= 8) {  // the largest, one lane after the other
+        const int bits = __float_as_int(r.m);
+        int key = bits ^ (bits >> 31 & 0x7fffffff), top = 0;
+        for (int i = 0; i < want; ++i) {
+          top = __reduce_max_sync(0xffffffffu, key);
+          if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = (int)0x80000000;
+        }
+        if (lane == 0) sh.least[warp] = __int_as_float(top ^ (top >> 31 & 0x7fffffff));
+      } else {
+        int ahead = 0;  // lanes with a larger maximum (equal ones: in order)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const float other = __shfl_sync(0xffffffffu, r.m, i);
+          ahead += other > r.m || (other == r.m && i < lane);
+        }
+        if (ahead == want - 1) sh.least[warp] = r.m;
       }
       group_sync<T>();
       float threshold = sh.least[0];
