@@ -127,6 +127,16 @@ def test_whole(binding, record_margin, N, V, n_top, dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,V,n_top", [(609, 10239, 20), (608, 10239, 5), (610, 10241, 64), (609, 20479, 3), (609, 20481, 0), (700, 2000, 64), (613, 4695, 32)])
+def test_many_rows(binding, N, V, n_top, dtype):
+    """Rows that are more than fit at once, on both sides of 40 KB; equal logits, and rows that hold one value."""
+    x, tokens, a, b, g = _inputs(N, V, dtype, N + V, off=1)
+    x[1::7] = torch.round(x[1::7])
+    x[2::31] = 1.5
+    _check(binding, x, tokens, n_top, a, b, g)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
 @pytest.mark.parametrize("N,V,n_top", [(4, 5, 3), (6, 1000, 64), (5, 8193, 33), (3, 50257, 20)])
 def test_ties(binding, N, V, n_top, dtype):
     """Whole numbers: equal logits are everywhere, and alternatives come by rising token."""

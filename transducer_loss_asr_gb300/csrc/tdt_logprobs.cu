@@ -13,7 +13,7 @@
 // so z is rounded once, at its own size, and what L is off by stays in differences to the maximum: m L - R is the same
 // product.  A thread holds its own R, s and t; R moves only where the maximum has grown by 8.  They are joined in a
 // fixed order.  Where R is past 2^24, whole numbers that float32 does not hold, x_i - m is formed instead.
-// A row belongs to a warp (short rows), a CTA, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
+// A row belongs to a warp (short rows), a CTA of 128 or 256 threads, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
 // exchange their results through distributed shared memory.
 // Alternatives: at least n_top elements reach a threshold that comes from the threads' maxima (the ceil(n_top / warps)-th largest
 // of each warp, the least of the warps); only threads whose maximum reaches it, hardly more than n_top, look again, at the
@@ -42,9 +42,10 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kBlock = 256;
+constexpr int kNarrow = 128;   // threads of a CTA where rows are many and not long
 constexpr int kMostTop = 64;
 constexpr int kMostCtas = 8;   // of a cluster
-constexpr int kMostBatches = 5;  // of a stretch that is kept: 64 KB and a vector in 16 KB each
+constexpr int kMostBatches = 5;  // of a stretch that is kept: 64 KB and a vector in 16 KB each (kNarrow: 40 KB in 8 KB)
 constexpr float kLn2f = 0.69314718055994531f;
 constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
 constexpr float kLazy = 8.0f;
@@ -203,11 +204,11 @@ template <int DT> __device__ __forceinline__ Stretch stretch_of(const void *p, i
 }
 
 template <int DT, bool FWD, bool BWD, int T>
-__global__ void __launch_bounds__(kBlock, 4) rows_kernel(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow ? 8 : 4) rows_kernel(const __grid_constant__ RowArgs a) {
   typedef typename Elem<DT>::T E;
   constexpr int N = Vec<DT>::N, U = 4, WARPS = T / 32;
   constexpr bool IN_PLACE = BWD;  // the logits may be written in this kernel
-  __shared__ GroupShared<T> shared[kBlock / T];
+  __shared__ GroupShared<T> shared[T == 32 ? kBlock / 32 : 1];
   GroupShared<T> &sh = shared[threadIdx.x / T];
   const int tid = threadIdx.x % T, lane = tid & 31, warp = tid >> 5;
   const int bits = T == 32 ? 0 : a.cta_bits, ctas = 1 << bits, part = T == 32 ? 0 : blockIdx.x & (ctas - 1);
@@ -757,6 +758,27 @@ bool off4(std::initializer_list<const void *> ptrs) {
   return false;
 }
 
+template <int DT, bool FWD, bool BWD, int T> cudaError_t launch_ctas(const RowArgs &a, cudaStream_t s) {
+  const size_t smem = (size_t)a.keep * 16 + (FWD && a.K > 0 ? sizeof(TopShared<T>) : 0);
+  if (FWD && smem > 0) {
+    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               65536 + 16 + (int)sizeof(TopShared<T>));
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.N << a.cta_bits);
+  cfg.blockDim = dim3(T);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = 1 << a.cta_bits;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = FWD && a.cta_bits > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<DT, FWD, BWD, T>, a);
+}
 template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStream_t s) {
   const long long bytes = (long long)a.V * (DT == kF32 ? 4 : 2);
   if ((bytes <= 2048 || (bytes <= 8192 && a.N >= 1024)) && a.K <= 16 && a.N >= 8) {  // a warp a row (more alternatives take a warp long: 2,500 x 664: 137 us of 32, a CTA 37)
@@ -772,25 +794,13 @@ template <int DT, bool FWD, bool BWD> cudaError_t launch_rows(RowArgs a, cudaStr
   while (1 << a.cta_bits < kMostCtas && share() > 16384 && (share() > most || ((long long)a.N << a.cta_bits) < 4 * 152)) ++a.cta_bits;
   const long long kept = share() / 16 + 1;
   a.keep = FWD && BWD && kept * 16 <= 65536 + 16 ? (int)kept : 0;
-  const size_t smem = (size_t)a.keep * 16 + (FWD && a.K > 0 ? sizeof(TopShared<kBlock>) : 0);
-  if (FWD && smem > 0) {
-    const cudaError_t e = cudaFuncSetAttribute(rows_kernel<DT, FWD, BWD, kBlock>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               65536 + 16 + (int)sizeof(TopShared<kBlock>));
-    if (e != cudaSuccess) return e;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(a.N << a.cta_bits);
-  cfg.blockDim = dim3(kBlock);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = 1 << a.cta_bits;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = FWD && a.cta_bits > 0 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, rows_kernel<DT, FWD, BWD, kBlock>, a);
+  // Rows to 40 KB (whose batches the barriers cover), more of them than CTAs of 256 threads fit: a row's chain of latencies wants
+  // more rows an SM (4,041 x 4,695 float32 scores 27 us against 35, with ten alternatives 39 against 57; 2,000 x 8,192 bfloat16 in
+  // one call 20 against 26; 8,000 x 8,193 float32 78 against 88; 656 x 8,193 scores 12.3 against 14.3, but the gradient
+  // alone takes longer: both calls 26.6 against 24.6)
+  if constexpr (FWD)
+    if (a.cta_bits == 0 && bytes / 16 < kMostBatches * 4 * kNarrow && a.N > 4 * 152) return launch_ctas<DT, FWD, BWD, kNarrow>(a, s);
+  return launch_ctas<DT, FWD, BWD, kBlock>(a, s);
 }
 template <bool FWD, bool BWD> int launch(const RowArgs &a, int dtype, void *stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
