@@ -381,3 +381,33 @@ def test_compiled_opcheck_and_a_captured_backward(binding):
                           test_utils=("test_schema", "test_faketensor"))
     torch.library.opcheck(torch.ops.tdt_gb300.token_logprobs_forward.default, (x.detach(), tokens, 0),
                           test_utils=("test_schema", "test_faketensor"))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,V", [(12, 60), (6, 700), (7, 8193), (5, 50257), (700, 4000), (1, 300000)])
+def test_entropy_weights_of_any_size_over_masked_tokens(binding, N, V, dtype):
+    """-inf or the type's lowest number here and there: such an entry's gradient is 0, however large the entropy's weight.  Both
+    calls, over the logits, and into rows on another address."""
+    x, tokens, a, b, g = _inputs(N, V, dtype, 17)
+    mask = torch.randint(0, 16, (N, V), generator=g, device="cuda") == 0
+    mask.scatter_(1, tokens[:, None], False)
+    x = torch.where(mask, -math.inf, x)
+    x[1::2] = x[1::2].clamp_min(torch.finfo(dtype).min)
+    # float16 results end at 65504; entropies here are under 12, so that products with them stay in float32
+    sizes = [2.0, -2.0, 100.0, -50.0, 1.75] if dtype == torch.float16 else [2.0, -2.0, 65536.0, -1e20, 1e37]
+    for turn in range(len(sizes) if N < len(sizes) else 1):
+        b = torch.tensor(sizes[turn:] + sizes[:turn], device="cuda").repeat(N // len(sizes) + 1)[:N].contiguous()
+        _check(binding, x, tokens, 0, a, b, g)
+        r = binding.tdt_token_logprobs_fwd(x, tokens)
+        split = binding.tdt_token_logprobs_bwd(x, tokens, r, a, b)
+        one = binding.tdt_token_logprobs_fwd_bwd(x, tokens, a, b)[1]
+        assert bool((split[mask] == 0).all()) and bool((one[mask] == 0).all())
+        for off in (0, 3):
+            wide = torch.empty(N, V + 8, dtype=dtype, device="cuda")[:, off:off + V]
+            assert torch.equal(binding.tdt_token_logprobs_bwd(x, tokens, r, a, b, grad_out=wide), split)
+            base = torch.zeros(N, V + 8, dtype=dtype, device="cuda")
+            y = base[:, off:off + V].copy_(x)
+            assert torch.equal(binding.tdt_token_logprobs_bwd(y, tokens, r, a, b, grad_out=y), split)
+            y.copy_(x)
+            got = binding.tdt_token_logprobs_fwd_bwd(y, tokens, a, b, grad_out=y)[1]
+            assert bool((got[mask] == 0).all()) and bool(got.isfinite().all())

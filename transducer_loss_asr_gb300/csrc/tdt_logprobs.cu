@@ -5,7 +5,8 @@
 //   logprob = z_t - ln s,   entropy = ln s - t / s,
 //   dx_i = -p_i (a + sum c + b (ln p_i + entropy)) + the given token's and the alternatives' own a and c_j,
 //   ln p_i = z_i - ln s.
-// An entry of -inf has p = 0; its logarithm is held above -200 (in base 2) in products with p, which is 0 there.
+// An entry of -inf has p = 0; its logarithm (in base 2) is held above -200, in bfloat16 above about -2^31, in products with p, which is
+// 0 there.  A weight b whose product with that would leave float32's range is formed 2^-k times, and p 2^k times.
 //
 // Forward: one read of the row in 16-byte vectors (whatever the row's alignment: elements before the first and after the last
 // whole vector go one by one).  Arithmetic is in base 2 against a whole number R near the maximum,
@@ -48,6 +49,8 @@ constexpr int kMostCtas = 8;   // of a cluster
 constexpr int kMostBatches = 5;  // of a stretch that is kept: 64 KB and a vector in 16 KB each (kNarrow: 40 KB in 8 KB)
 constexpr float kLn2f = 0.69314718055994531f;
 constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
+// log2 of a bound of c1 that keeps its products with held logarithms in float32: of under 2^8, in bfloat16 of under 2^31
+template <int DT> constexpr int kMostSlope = DT == kBF16 ? 96 : 119;
 constexpr float kLazy = 8.0f;
 constexpr float kMostR = 16777216.0f;  // whole numbers to here are exact, and x L - R is held to half a unit where x is the maximum
 
@@ -69,7 +72,7 @@ struct RowArgs {
   int keep;           // vectors of a stretch that stay in dynamic shared memory for the backward pass (0: none do)
 };
 
-// What a row's gradient is formed with, each twice: p (c0 + c1 log2 p), log2 p = y L + neg + sum.
+// What a row's gradient is formed with, each twice: 2^l (c0 + c1 l), l = k + log2 p = y L + neg + sum.
 struct Slopes {
   float2 neg, sum, c0, c1;
 };
@@ -81,13 +84,14 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-// A vector's elements as float32.  What lies below -2e38 (or is -inf) becomes -2e38, so that products with its weight, which
-// is 0, are 0: two elements an instruction in bfloat16.  (The other types' z is held above kLeastZ instead.)
+// A vector's elements as float32.  In bfloat16 what lies below -2^30 (or is -inf) becomes -2^30, two elements an instruction, so that
+// products with its weight, which is 0, are 0 wherever the reference is not below -2^24.  (The other types' z is held above kLeastZ
+// instead.)
 template <int DT> __device__ __forceinline__ void unpack_held(uint4 raw, float *v) {
   if constexpr (DT == kBF16) {
     unsigned w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0xff16ff16u));
+    for (int i = 0; i < 4; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w[i]) : "r"(0xce80ce80u));
     raw = make_uint4(w[0], w[1], w[2], w[3]);
   }
   unpack<DT>(raw, v);
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow 
   const int K = a.K;
   // of the whole row: log2 p_i = x_i L - R - log2_s; R infinite: (x_i - m) L - log2_s
   float R = 0.0f, m = 0.0f, log2_s = 0.0f, ent = 0.0f;
-  auto log2_of = [&](float v) { return (R < INFINITY ? fmaf(v, kLog2e, -R) : (v - m) * kLog2e) - log2_s; };
+  auto z_of = [&](float v) { return R < INFINITY ? fmaf(v, kLog2e, -R) : (v - m) * kLog2e; };
   extern __shared__ __align__(16) uint4 kept_row[];
   __shared__ unsigned long long full[kMostBatches];
   __shared__ int gave_up;
@@ -509,14 +513,14 @@ __global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow 
           r.t += sh.sums[i].t;
         }
       }
-      r.R = INFINITY;  // what log2_of knows it by
+      r.R = INFINITY;  // what z_of knows it by
     }
     const bool lost = !(r.s > 0.0f && r.s < INFINITY) || !(fabsf(r.m) < INFINITY);  // NaN, +inf, or nothing but -inf
     log2_s = lost ? NAN : log2f(r.s);
     ent = lost ? NAN : fmaxf((log2_s - r.t / r.s) * kLn2f, 0.0f);
     R = r.R;
     m = r.m;
-    const float ln_s = lost ? NAN : -log2_of(m) * kLn2f;
+    const float ln_s = lost ? NAN : (log2_s - z_of(m)) * kLn2f;
     auto ln_of = [&](float v) { return v - m - ln_s; };  // finite wherever v is
     if (part == 0) {
       if (tid == 0) {
@@ -628,14 +632,21 @@ __global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow 
       group_sync<T>();
       float all = 0.0f;
       for (int j = 0; j <= kept; ++j) all += sh.own_add[j];
-      // -p (all + gb (ln p + ent)), from log2 p
-      const float c0 = -fmaf(gb, ent, all), c1 = -gb * kLn2f;
+      // -p (all + gb (ln p + ent)), from l = k + log2 p; k = 0 but for weights of 2^96 and more
+      float c0 = -fmaf(gb, ent, all), c1 = -gb * kLn2f, sum = -log2_s;
+      const int k = (int)(__float_as_uint(c1) >> 23 & 255) - 126 - kMostSlope<DT>;  // |c1| < 2^(k + kMostSlope)
+      if (k > 0) {
+        const float down = __uint_as_float((unsigned)(127 - k) << 23);
+        c1 *= down;
+        c0 = -fmaf(gb * down, ent, all * down) - c1 * k;
+        sum += k;
+      }
       auto slope = [&](float y) {
-        const float lp = log2_of(y);
-        return fast_exp2(lp) * fmaf(c1, max_nan(lp, kLeastZ), c0);
+        const float l = z_of(y) + sum;
+        return fast_exp2(l) * fmaf(c1, max_nan(l, kLeastZ), c0);
       };
       const int mis = (int)((uintptr_t)(x + w.head) & 15);
-      const Slopes pairs = {make_float2(-R, -R), make_float2(-log2_s, -log2_s), make_float2(c0, c0), make_float2(c1, c1)};
+      const Slopes pairs = {make_float2(-R, -R), make_float2(sum, sum), make_float2(c0, c0), make_float2(c1, c1)};
       auto finish = [&](uint4 raw, int v) {
         float y[N];
         unpack_held<DT>(raw, y);
