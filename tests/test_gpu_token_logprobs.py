@@ -411,3 +411,26 @@ def test_entropy_weights_of_any_size_over_masked_tokens(binding, N, V, dtype):
             y.copy_(x)
             got = binding.tdt_token_logprobs_fwd_bwd(y, tokens, a, b, grad_out=y)[1]
             assert bool((got[mask] == 0).all()) and bool(got.isfinite().all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("N,V", [(40, 700), (12, 8193), (9, 60000), (1, 131072), (700, 4000)])
+def test_stretches_of_masked_tokens_weigh_nothing(binding, N, V, dtype):
+    """What a thread, a warp or a CTA sees first, or all that it sees, is masked: its sums are nothing, and results are, bit for
+    bit, those over logits so far below the others that their weight is 0."""
+    x, _, a, b, g = _inputs(N, V, dtype, 19)
+    at = torch.arange(V, device="cuda")
+    few = torch.zeros(V, dtype=torch.bool, device="cuda")
+    few[torch.randperm(V, generator=g, device="cuda")[:7]] = True
+    lowest = [-math.inf, torch.finfo(dtype).min] + ([] if dtype == torch.float16 else [-1e30])
+    for allowed in (at >= V // 2, at < V // 10, (at >= V // 3) & (at < V // 2), few):
+        ids = allowed.nonzero()[:, 0]
+        tokens = ids[torch.randint(0, len(ids), (N,), generator=g, device="cuda")]
+        far = torch.where(allowed, x, -1e4)
+        want, want_grad = binding.tdt_token_logprobs_fwd_bwd(far, tokens, a, b, 5)
+        scores = binding.tdt_token_logprobs_fwd(far, tokens, 5)
+        for low in lowest:
+            y = torch.where(allowed, x, low)
+            got, grad = binding.tdt_token_logprobs_fwd_bwd(y, tokens, a, b, 5)
+            for p, q in zip((*want, want_grad, *scores), (*got, grad, *binding.tdt_token_logprobs_fwd(y, tokens, 5))):
+                assert torch.equal(p, q), low

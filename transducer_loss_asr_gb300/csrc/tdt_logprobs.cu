@@ -13,7 +13,9 @@
 //   z_i = x_i L - R (one fma; L = log2 e in float32),   s = sum 2^z_i,   t = sum 2^z_i z_i,
 // so z is rounded once, at its own size, and what L is off by stays in differences to the maximum: m L - R is the same
 // product.  A thread holds its own R, s and t; R moves only where the maximum has grown by 8.  They are joined in a
-// fixed order.  Where R is past 2^24, whole numbers that float32 does not hold, x_i - m is formed instead.
+// fixed order.  R starts at -2^24: what lies far below, masked tokens (-inf, the type's lowest number), has weight 0 wherever it
+// stands, so a thread that sees nothing else has sums of 0.  Where m L is past 2^24 on either side, and whole numbers are more than
+// float32 holds, x_i - m is formed instead.
 // A row belongs to a warp (short rows), a CTA of 128 or 256 threads, or a cluster of CTAs (few or long rows), whose CTAs have a stretch of it each and
 // exchange their results through distributed shared memory.
 // Alternatives: at least n_top elements reach a threshold that comes from the threads' maxima (the ceil(n_top / warps)-th largest
@@ -52,7 +54,7 @@ constexpr float kLeastZ = -200.0f;  // 2^-200 is 0
 // log2 of a bound of c1 that keeps its products with held logarithms in float32: of under 2^8, in bfloat16 of under 2^31
 template <int DT> constexpr int kMostSlope = DT == kBF16 ? 96 : 119;
 constexpr float kLazy = 8.0f;
-constexpr float kMostR = 16777216.0f;  // whole numbers to here are exact, and x L - R is held to half a unit where x is the maximum
+constexpr float kMostR = 16777216.0f;  // whole numbers to +-2^24 are exact, and x L - R is held to half a unit where x is the maximum
 
 struct RowArgs {
   const void *x;
@@ -130,7 +132,8 @@ template <int DT> __device__ __forceinline__ float vector_max(uint4 raw) {
   }
 }
 
-// A stretch's maximum m, reference R (a whole number), sum of 2^z and sum of 2^z z, z = x log2 e - R.  s = 0: nothing, whatever R.
+// A stretch's maximum m, reference R (a whole number, -2^24 at least), sum of 2^z and sum of 2^z z, z = x log2 e - R.  s = 0: nothing
+// that counts, whatever R.
 struct Sums {
   float m, R, s, t;
 };
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow 
   if (FWD && real) {
     const Stretch w = stretch_of<DT>(x, a.V, part, bits);
     const E *body = x + w.head;
-    Sums r = {-INFINITY, -3e38f, 0.0f, 0.0f};
+    Sums r = {-INFINITY, -kMostR, 0.0f, 0.0f};
     float2 s2 = make_float2(0.0f, 0.0f), t2 = s2;  // running sums of even and odd elements
     auto grow = [&](float top) {
       r.m = fmaxf(r.m, top);
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(T == kNarrow ? kNarrow : kBlock, T == kNarrow 
       }
     }
     group_sync<T>();
-    if (!(r.s > 0.0f && r.s < INFINITY && fabsf(r.R) <= kMostR) && fabsf(r.m) < INFINITY) {
+    if (!(r.s > 0.0f && r.s < INFINITY && fabsf(r.m) * kLog2e <= kMostR) && fabsf(r.m) < INFINITY) {
       // NaN in the row, or numbers so large that a product with L loses whole units: against the maximum itself, by every CTA
       r.s = r.t = 0.0f;
       for (int i = tid; i < a.V; i += T) {
