@@ -342,3 +342,18 @@ def test_no_pages_and_no_new_rows(binding, dtype, cache_dtype, Lq):
         assert bool((out == 0).all()) and bool((lse == -math.inf).all())
     out, _ = binding.tdt_paged_attn(q, cache, table[:, :0], i64([1, 0]), i64([1, 0]))
     assert bool(out[0].isnan().all()) and bool((out[1] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=["f32", "f16", "bf16"])
+@pytest.mark.parametrize("Lq", [1, 4, 40])
+def test_value_rows_of_the_least_byte_come_first(binding, dtype, Lq):
+    """Bytes that the caller set: value rows of byte 0 (2^-127) and, after every warp has had some, ordinary ones."""
+    n, tiny = 2400, 1200
+    cache, table, k, v = make(binding, [n, n - 300], 2, 64, 16, E4M3, 13)
+    pages = table[:, :tiny // 16].long()
+    cache.v_scales[pages] = 0
+    v[:, :tiny] = cache.v[pages].double().flatten(1, 2) * 2.0 ** -127
+    q = _queries(2, Lq, 4, 64, dtype, 13, [Lq] * 2)
+    lens = i64([n, n - 300])
+    out, tol, _, _ = _reference(q, k, v, lens, i64([Lq] * 2), 0.125)
+    _near("out", binding.tdt_paged_attn(q, cache, table, lens)[0], out, tol)

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
 #pragma unroll
       for (int y = 0; y < 4; ++y) o[x][h][y] = 0.0f;
   }
-  int top_e = 0;  // e4m3: the largest byte of the value rows so far; o is in units of 2^(top_e - 127)
+  int top_e = -1;  // e4m3: the largest byte of the value rows so far, -1: none; o is in units of 2^(top_e - 127)
   bool bad = false;
 
   const int place_mask = (1 << a.t.page_bits) - 1, box_rows = min(1 << a.t.page_bits, S::KT);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
       const unsigned kb = bytes & 0xffu, vb = bytes >> 8;
       const int most = (int)__reduce_max_sync(0xffffffffu, vb == kByteNaN ? 0u : vb);
       if (most > top_e) {
-        if (top_e > 0) {
+        if (top_e >= 0) {
           const float down = pow2_nonpos(top_e - most);
 #pragma unroll
           for (int x = 0; x < S::MTILES; ++x)
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<QT, PT, DP, RT>::CTAS)
 
   // the warps of a CTA
   __syncthreads();  // the memory of turns in flight is free
-  const float unit_f = S::E8 ? scale_of(top_e) : 1.0f;
+  const float unit_f = S::E8 ? scale_of(max(top_e, 0)) : 1.0f;
 #pragma unroll
   for (int h = 0; h < RT; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
