@@ -434,3 +434,15 @@ def test_stretches_of_masked_tokens_weigh_nothing(binding, N, V, dtype):
             got, grad = binding.tdt_token_logprobs_fwd_bwd(y, tokens, a, b, 5)
             for p, q in zip((*want, want_grad, *scores), (*got, grad, *binding.tdt_token_logprobs_fwd(y, tokens, 5))):
                 assert torch.equal(p, q), low
+
+
+@pytest.mark.parametrize("V", [40, 700, 8193, 60000])
+def test_maxima_on_both_sides_of_the_largest_reference(binding, V):
+    """float32 logits near +-2^24 / log2(e), where the reference of a row gives way to its maximum; masked tokens beside them."""
+    edge = 2.0 ** 24 / math.log2(math.e)
+    x, tokens, a, b, g = _inputs(12, V, torch.float32, 23)
+    base = torch.tensor([s * (edge + d) for s in (1.0, -1.0) for d in (-200.0, -12.0, -3.0, 0.0, 7.0, 300.0)], device="cuda")
+    x = torch.round(x * 2) + base[:, None]
+    x[1::2, :V // 2] = -math.inf
+    tokens = torch.randint(V // 2, V, (12,), generator=g, device="cuda")
+    _check(binding, x, tokens, 5, a, b, g)
