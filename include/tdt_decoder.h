@@ -231,13 +231,15 @@ int tdt_cache_read(const tdt_paged_cache *cache, const int32_t *page_table, int6
  *            (but with float16 queries they may end at 65504).  Weights of
  *            16-bit calls are rounded to 16 bits; with few queries over e4m3
  *            pages to float16, times the value row's power of two relative to
- *            the utterance's largest: weights of rows more than 2^20 smaller
- *            than that one lose bits.
+ *            the utterance's largest: rows more than 2^21 smaller than that
+ *            one lose bits of their weights, and more than 2^31 smaller all.
  *   kv_lens, q_lens, page_table  as in tdt_cache_write.  Lengths out of range
  *            give that utterance NaN; a page outside [0, n_pages) gives NaN to
  *            the queries that see it, and may to the utterance's others.
  *            Places past kv_lens[b] may hold anything, NaN included; positions
- *            before it are to be finite.
+ *            before it are to be finite, and so are scores and 2^15 times the
+ *            sums of values (weights are divided by their sum at the end, and
+ *            may be that large until then).
  *   lse      device float32 [B, H, Lq] contiguous, or NULL.
  *   workspace  device, 256-byte aligned, at least
  *            tdt_paged_attn_workspace_size(sizes, dtype, cache) bytes; may be

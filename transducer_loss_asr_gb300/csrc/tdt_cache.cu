@@ -6,10 +6,11 @@
 // a = m 2^x, 1 <= m < 2, the least e with a <= 448 2^e = 1.75 2^(e + 8) is x - 8, or x - 7 where m > 1.75:
 // it comes from the bits of a, and x 2^-e is exact, so the only rounding is e4m3's own (half a step, 2^-4 of
 // the value, or 2^-10 2^e below 2^-6 2^e).
-// Bound by latency: lengths, page table, row, each a trip to memory after the other (16 ragged x 1024 rows of 4 heads of 128,
-// bfloat16 to e4m3: 12.7 us, and back 14.8 us, for 38 and 46 MB; a decoding step of 64 x 16 heads: 4 us); by instructions, too,
-// where a thread found its own row by divisions and had 8 elements (21 us).  So a block has whole positions of one utterance, and
-// a thread several pieces of 16 elements, whose page lookups, and then loads, are in flight together.
+// A decoding step is bound by latency: lengths, page table, row, each a trip to memory after the other (64 x 16 heads: 4 us).
+// Prompts are bound by that and by instructions (16 ragged x 1024 rows of 4 heads of 128, bfloat16 to e4m3: 12.7 us, 70 % of the issue
+// slots, and back 14.8 us, 60 %, for 38 and 46 MB; 21 us where a thread found its own row by divisions and had 8 elements).  So a
+// block has whole positions of one utterance, and a thread several pieces of 16 elements, whose page lookups, and then loads, are in
+// flight together.
 //
 // The rows of whole utterances can also be laid out densely, for attention that reads no pages (launch_gather).
 #include <algorithm>

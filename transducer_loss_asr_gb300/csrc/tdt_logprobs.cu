@@ -23,10 +23,11 @@
 // batches of vectors whose maximum does.  What reaches it is listed in shared memory and ranked by (value, index): the order in which the list
 // fills does not matter.  A list that overflows (many equal elements) is given up for n_top passes over the row.
 // Backward: a read and a write of the row; in one call with the forward pass, the row comes in bulk copies that are all asked for
-// at once, and waits in shared memory (loaded by the threads a batch ahead and put there: 173 us for what is 162 with copies).
+// at once, and waits in shared memory (put there by the threads, which loaded a batch ahead, it took 11 us more of 173).
 //
 // 4,096 x 50,257 bfloat16, a quarter of the rows padding: forward 68 us, backward 125 us (5.8 TB/s), both in one call 147 us
-// (4.9 TB/s: reading and writing a row take turns, four CTAs an SM, 60 % of the issue slots).  2,048 x 131,072 bfloat16: 96 us (5.6
+// (4.9 TB/s: reading and writing a row take turns, four CTAs an SM, 60 % of the issue slots).  Masked tokens cost no more than others,
+// in stretches, too (1,024 x 131,072 bfloat16, a tenth or seven of the tokens allowed: 45 us, all: 46).  2,048 x 131,072 bfloat16: 96 us (5.6
 // TB/s), with twenty alternatives 111 us: what follows the read, threshold, list, ranks, is latency that four CTAs an SM cover in
 // part.  656 x 8,193 float32: 10 us and 11 us, latency.  A whole row a CTA beats clusters of smaller stretches (131,072 scored: two CTAs 104 us, four 143).
 #include <cooperative_groups.h>
